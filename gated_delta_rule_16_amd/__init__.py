@@ -20,6 +20,17 @@ Functions mirror the C calls:
     gdr2_chunk_bwd(q, k, v, alpha, erase, write, s0, dout, ds_final=None)
         -> (dq, dk, dv, dalpha, derase, dwrite, ds0)
 
+    gdr_short_conv_fwd(x, w, bias=None, s0=None, ...)           -> (y, s_final)
+    gdr_short_conv_step(x, w, bias, state, ...)                 -> y
+    gdr_short_conv_bwd(x, w, bias, s0, dy, ds_final=None, ...)  -> (dx, dw, dbias, ds0)
+    gdr_ssm_scan_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, h0=None, ...)
+        -> (y, h_final)
+    gdr_ssm_step(x, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, ...) -> y
+    gdr_ssm_scan_bwd(x, dt, A, Bm, Cm, D, z, dt_bias, h0, dout, dh_final=None, ...)
+        -> (dx, ddt, dA, dB, dC, dD, dz, ddt_bias, dh0)
+    gdr_layer_norm_fwd(x, w=None, b=None, eps=1e-5, residual=None, ...) -> y or (y, h)
+    gdr_layer_norm_bwd(x, w, dy, eps=1e-5, dres=None, ...)      -> (dx, dw, db)
+
 ``l2norm_qk=True`` calls the ``_ex`` variant of the same C function with
 GDR_L2NORM_QK: q and k are L2-normalised on load inside the kernels.
 """
@@ -39,8 +50,14 @@ __all__ = ["gdr_chunk_fwd", "gdr_recurrent_step", "gdr2_chunk_fwd", "gdr_output_
            "gdr_chunk_fwd_gate_workspace_size",
            "gdr_chunk_bwd_split", "gdr_chunk_bwd_split_workspace_size",
            "gdr2_chunk_fwd_split", "gdr2_chunk_bwd_split", "gdr2_chunk_bwd_split_workspace_size",
+           "gdr_short_conv_fwd", "gdr_short_conv_step", "gdr_short_conv_bwd",
+           "gdr_short_conv_bwd_workspace_size", "gdr_ssm_scan_fwd",
+           "gdr_ssm_scan_fwd_workspace_size", "gdr_ssm_step", "gdr_ssm_scan_bwd",
+           "gdr_ssm_scan_bwd_workspace_size", "gdr_layer_norm_fwd", "gdr_layer_norm_bwd",
+           "gdr_layer_norm_bwd_workspace_size",
            "GdrError", "status_string", "lib", "LIB_PATH", "GDR_F32",
-           "GDR_BF16", "GDR_L2NORM_QK", "GDR_SPLIT_FP32_STATES"]
+           "GDR_BF16", "GDR_L2NORM_QK", "GDR_SPLIT_FP32_STATES", "GDR_CONV_SILU",
+           "GDR_SSM_SOFTPLUS", "GDR_SSM_MAX_N", "GDR_NORM_MAX_C"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)),
                         "libgdr.so")
@@ -55,6 +72,10 @@ lib = ctypes.CDLL(LIB_PATH)
 GDR_F32, GDR_BF16 = 0, 1
 GDR_L2NORM_QK = 1
 GDR_SPLIT_FP32_STATES = 2
+GDR_CONV_SILU = 1
+GDR_SSM_SOFTPLUS = 1
+GDR_SSM_MAX_N = 64
+GDR_NORM_MAX_C = 1048576
 _I64, _P, _E, _U = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_uint32
 
 lib.gdr_chunk_fwd.argtypes = [_I64] * 5 + [_E] + [_P] * 6 + [_E, _P, _P, _P]
@@ -118,6 +139,35 @@ lib.gdr2_chunk_bwd_split_workspace_size.restype = ctypes.c_size_t
 lib.gdr2_chunk_bwd_split.argtypes = ([_I64] * 5 + [_E] + [_P] * 7 + [_E, _P, _P] + [_P] * 7 +
                                      [_I64, _U, _P, ctypes.c_size_t, _P])
 lib.gdr2_chunk_bwd_split.restype = ctypes.c_int
+_F, _Z = ctypes.c_float, ctypes.c_size_t
+lib.gdr_short_conv_fwd.argtypes = [_I64] * 4 + [_E] + [_P] * 5 + [_U, _E, _P, _P, _P]
+lib.gdr_short_conv_fwd.restype = ctypes.c_int
+lib.gdr_short_conv_step.argtypes = [_I64] * 3 + [_E, _P, _I64, _P, _P, _P, _U, _E, _P, _P]
+lib.gdr_short_conv_step.restype = ctypes.c_int
+lib.gdr_short_conv_bwd_workspace_size.argtypes = [_I64] * 4
+lib.gdr_short_conv_bwd_workspace_size.restype = ctypes.c_size_t
+lib.gdr_short_conv_bwd.argtypes = ([_I64] * 4 + [_E] + [_P] * 4 + [_E] + [_P] * 3 + [_U, _E] +
+                                   [_P] * 5 + [_Z, _P])
+lib.gdr_short_conv_bwd.restype = ctypes.c_int
+lib.gdr_ssm_scan_fwd_workspace_size.argtypes = [_I64] * 5
+lib.gdr_ssm_scan_fwd_workspace_size.restype = ctypes.c_size_t
+lib.gdr_ssm_scan_fwd.argtypes = ([_I64] * 5 + [_E] + [_P] * 10 + [_U, _E] + [_P] * 3 + [_Z, _P])
+lib.gdr_ssm_scan_fwd.restype = ctypes.c_int
+lib.gdr_ssm_step.argtypes = [_I64] * 4 + [_E] + [_P] * 10 + [_U, _E, _P, _P]
+lib.gdr_ssm_step.restype = ctypes.c_int
+lib.gdr_ssm_scan_bwd_workspace_size.argtypes = [_I64] * 5
+lib.gdr_ssm_scan_bwd_workspace_size.restype = ctypes.c_size_t
+lib.gdr_ssm_scan_bwd.argtypes = ([_I64] * 5 + [_E] + [_P] * 9 + [_E] + [_P] * 3 + [_U, _E] +
+                                 [_P] * 10 + [_Z, _P])
+lib.gdr_ssm_scan_bwd.restype = ctypes.c_int
+lib.gdr_layer_norm_fwd.argtypes = [_I64, _I64, _E, _P, _I64, _E, _P, _I64, _P, _P, _F, _E, _P, _P,
+                                   _P]
+lib.gdr_layer_norm_fwd.restype = ctypes.c_int
+lib.gdr_layer_norm_bwd_workspace_size.argtypes = [_I64, _I64]
+lib.gdr_layer_norm_bwd_workspace_size.restype = ctypes.c_size_t
+lib.gdr_layer_norm_bwd.argtypes = [_I64, _I64, _E, _P, _I64, _P, _E, _P, _I64, _F, _E, _P, _I64,
+                                   _P, _P, _P, _P, _Z, _P]
+lib.gdr_layer_norm_bwd.restype = ctypes.c_int
 lib.gdr_status_string.argtypes = [ctypes.c_int]
 lib.gdr_status_string.restype = ctypes.c_char_p
 lib.gdr_version.restype = ctypes.c_int
@@ -666,3 +716,421 @@ def gdr2_chunk_bwd_split(q, k, v, alpha, erase, write, s0, dout, ds_final=None, 
         (GDR_L2NORM_QK if l2norm_qk else 0) | (GDR_SPLIT_FP32_STATES if fp32_states else 0),
         _ptr(workspace), workspace.numel(), _stream(stream)))
     return tuple(out) + (ds0,)
+
+
+# ---- operators around the mixer ------------------------------------------------
+#
+# Their inputs may be slices of wider tensors (any batch and token strides,
+# channels contiguous), and they may live on another device than the current
+# one: the call, and everything allocated for it, goes to the tensors' device
+# and to ``stream`` (default: that device's current stream).
+
+
+def _like(name, t, dtype, shape, device):
+    """A tensor of this type and shape on ``device`` whose channels are contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _row_strides(name, t, lead):
+    """Element strides of the ``lead`` leading dimensions; the others must be
+    contiguous."""
+    shape, st = t.shape, t.stride()
+    want = 1
+    for i in range(len(shape) - 1, lead - 1, -1):
+        if shape[i] != 1 and st[i] != want and t.numel():
+            raise ValueError(f"{name} must have contiguous channels")
+        want *= shape[i]
+    return st[:lead]
+
+
+def _whole(name, t, dtype, shape, device):
+    _like(name, t, dtype, shape, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+class _On:
+    """The tensors' device and the call's stream while a call allocates and launches."""
+
+    def __init__(self, device, stream):
+        self.ptr = stream.cuda_stream if stream is not None else None
+        self.device = device
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream must be on {device}, got {stream.device}")
+        self.ctx = None
+        if stream is not None:
+            self.ctx = torch.cuda.stream(stream)       # also makes its device current
+        elif device.index != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        if self.ptr is None:
+            self.ptr = torch.cuda.current_stream(self.device).cuda_stream
+        return self
+
+    def __exit__(self, *exc):
+        return self.ctx.__exit__(*exc) if self.ctx is not None else None
+
+
+def _first(name, t, dims):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got {t.dim()}")
+    if t.dtype not in _DT:
+        raise TypeError(f"unsupported {name} dtype {t.dtype}")
+    return t.device
+
+
+def _dt_of(name, dtype):
+    if dtype not in _DT:
+        raise TypeError(f"unsupported {name} {dtype}")
+    return _DT[dtype]
+
+
+def _buffer(name, t, dtype, shape, device):
+    """A given output buffer, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _whole(name, t, dtype, shape, device)
+    return t
+
+
+def _scratch(workspace, need, device):
+    if workspace is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    _like("workspace", workspace, torch.uint8, workspace.shape, device)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace
+
+
+def _p(t):
+    return None if t is None else t.data_ptr()
+
+
+def _i64s(*v):
+    return (ctypes.c_int64 * len(v))(*v)
+
+
+def gdr_short_conv_fwd(x, w, bias=None, s0=None, *, silu=True, out_dtype=None, y=None,
+                       s_final=None, want_state=True, stream=None):
+    """Short causal depthwise convolution (with SiLU) over whole sequences.
+
+    x [B,T,C] fp32 or bf16 (batch and token strides free); w [C,K] fp32, K = 2,
+    3 or 4; bias [C] fp32 or None; s0 [B,K-1,C] in x's dtype or None: the inputs
+    before x.  Returns (y [B,T,C], s_final [B,K-1,C] or None); ``s_final`` may
+    be passed in (it may be ``s0`` itself)."""
+    dev = _first("x", x, 3)
+    B, T, C = x.shape
+    if not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise ValueError("w must be a [C, K] tensor")
+    K = w.shape[1]
+    xs = _row_strides("x", x, 2)
+    _whole("w", w, torch.float32, (C, K), dev)
+    if bias is not None:
+        _whole("bias", bias, torch.float32, (C,), dev)
+    if s0 is not None:
+        _whole("s0", s0, x.dtype, (B, K - 1, C), dev)
+    odt = out_dtype or (x.dtype if y is None else y.dtype)
+    code = _dt_of("output dtype", odt)
+    with _On(dev, stream) as on:
+        y = _buffer("y", y, odt, (B, T, C), dev)
+        if s_final is not None or want_state:
+            s_final = _buffer("s_final", s_final, x.dtype, (B, max(K - 1, 0), C), dev)
+        _run("gdr_short_conv_fwd", lib.gdr_short_conv_fwd(
+            B, T, C, K, _DT[x.dtype], _p(x), _i64s(*xs), _p(w), _p(bias), _p(s0),
+            GDR_CONV_SILU if silu else 0, code, _p(y), _p(s_final), on.ptr))
+    return y, s_final
+
+
+def gdr_short_conv_step(x, w, bias, state, *, silu=True, out_dtype=None, y=None, stream=None):
+    """One decode token of gdr_short_conv_fwd: x [N,C], state [N,K-1,C] in x's
+    dtype, moved on in place.  Returns y [N,C]."""
+    dev = _first("x", x, 2)
+    N, C = x.shape
+    if not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise ValueError("w must be a [C, K] tensor")
+    K = w.shape[1]
+    xs = _row_strides("x", x, 1)
+    _whole("w", w, torch.float32, (C, K), dev)
+    if bias is not None:
+        _whole("bias", bias, torch.float32, (C,), dev)
+    _whole("state", state, x.dtype, (N, K - 1, C), dev)
+    odt = out_dtype or (x.dtype if y is None else y.dtype)
+    code = _dt_of("output dtype", odt)
+    with _On(dev, stream) as on:
+        y = _buffer("y", y, odt, (N, C), dev)
+        _run("gdr_short_conv_step", lib.gdr_short_conv_step(
+            N, C, K, _DT[x.dtype], _p(x), xs[0], _p(w), _p(bias), _p(state),
+            GDR_CONV_SILU if silu else 0, code, _p(y), on.ptr))
+    return y
+
+
+def gdr_short_conv_bwd_workspace_size(B, T, C, K) -> int:
+    """Bytes of device workspace gdr_short_conv_bwd needs for dw and dbias."""
+    return int(lib.gdr_short_conv_bwd_workspace_size(B, T, C, K))
+
+
+def gdr_short_conv_bwd(x, w, bias, s0, dy, ds_final=None, *, silu=True,
+                       grad_dtype=torch.float32, want_dw=True, want_ds0=True, workspace=None,
+                       stream=None):
+    """Reverse mode of gdr_short_conv_fwd for dL/dy = ``dy`` [B,T,C] (fp32 or
+    bf16, strides free) and dL/ds_final = ``ds_final`` [B,K-1,C] fp32 or None.
+    Returns (dx [B,T,C] in ``grad_dtype``, dw [C,K], dbias [C], ds0 [B,K-1,C]),
+    the last three fp32; dw and dbias are None without ``want_dw``, dbias also
+    without bias, ds0 without ``want_ds0``."""
+    dev = _first("x", x, 3)
+    B, T, C = x.shape
+    if not isinstance(w, torch.Tensor) or w.dim() != 2:
+        raise ValueError("w must be a [C, K] tensor")
+    K = w.shape[1]
+    xs = _row_strides("x", x, 2)
+    _whole("w", w, torch.float32, (C, K), dev)
+    if bias is not None:
+        _whole("bias", bias, torch.float32, (C,), dev)
+    if s0 is not None:
+        _whole("s0", s0, x.dtype, (B, K - 1, C), dev)
+    _first("dy", dy, 3)
+    _like("dy", dy, dy.dtype, (B, T, C), dev)
+    ys = _row_strides("dy", dy, 2)
+    if ds_final is not None:
+        _whole("ds_final", ds_final, torch.float32, (B, K - 1, C), dev)
+    code = _dt_of("grad_dtype", grad_dtype)
+    with _On(dev, stream) as on:
+        f32 = dict(dtype=torch.float32, device=dev)
+        dx = torch.empty((B, T, C), dtype=grad_dtype, device=dev)
+        dw = torch.empty((C, K), **f32) if want_dw else None
+        db = torch.empty((C,), **f32) if want_dw and bias is not None else None
+        ds0 = torch.empty((B, max(K - 1, 0), C), **f32) if want_ds0 else None
+        if want_dw or workspace is not None:
+            workspace = _scratch(workspace, gdr_short_conv_bwd_workspace_size(B, T, C, K), dev)
+        _run("gdr_short_conv_bwd", lib.gdr_short_conv_bwd(
+            B, T, C, K, _DT[x.dtype], _p(x), _p(w), _p(bias), _p(s0), _DT[dy.dtype], _p(dy),
+            _i64s(*xs, *ys), _p(ds_final), GDR_CONV_SILU if silu else 0, code, _p(dx), _p(dw),
+            _p(db), _p(ds0), _p(workspace), 0 if workspace is None else workspace.numel(),
+            on.ptr))
+    return dx, dw, db, ds0
+
+
+def _ssm_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, lead):
+    """Checks shared by the scan's calls; returns (device, sizes, strides)."""
+    dev = _first("x", x, lead + 1)
+    if not isinstance(A, torch.Tensor) or A.dim() != 2:
+        raise ValueError("A must be a [D, N] tensor")
+    if not isinstance(Bm, torch.Tensor) or Bm.dim() != lead + 2:
+        raise ValueError("Bm must be [..., G, N]")
+    Dn, N = A.shape
+    G = Bm.shape[-2]
+    rows = x.shape[:lead]
+    dtype = x.dtype
+    st = []
+    for name, t, tail in (("x", x, (Dn,)), ("dt", dt, (Dn,)), ("Bm", Bm, (G, N)),
+                          ("Cm", Cm, (G, N)), ("z", z, (Dn,))):
+        if t is None and name == "z":
+            st += [0] * lead
+            continue
+        _like(name, t, dtype, rows + tail, dev)
+        st += _row_strides(name, t, lead)
+    _whole("A", A, torch.float32, (Dn, N), dev)
+    if D is not None:
+        _whole("D", D, torch.float32, (Dn,), dev)
+    if dt_bias is not None:
+        _whole("dt_bias", dt_bias, torch.float32, (Dn,), dev)
+    return dev, (*rows, Dn, G, N), st
+
+
+def gdr_ssm_scan_fwd_workspace_size(B, T, D, G, N) -> int:
+    """Bytes of device workspace gdr_ssm_scan_fwd needs (0: none)."""
+    return int(lib.gdr_ssm_scan_fwd_workspace_size(B, T, D, G, N))
+
+
+def gdr_ssm_scan_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, h0=None, *, softplus=True,
+                     out_dtype=None, y=None, h_final=None, want_state=True, workspace=None,
+                     stream=None):
+    """Selective state space scan over whole sequences: with Delta =
+    softplus(dt + dt_bias), h_t = exp(Delta_t A) h_{t-1} + Delta_t x_t B_t,
+    y_t = C_t . h_t + D x_t, times SiLU(z_t) when z is given.
+
+    x, dt, z [B,T,D] and Bm, Cm [B,T,G,N], all one dtype (fp32 or bf16; batch
+    and token strides free); A [D,N], D [D], dt_bias [D] fp32; h0 [B,D,N] fp32
+    or None.  Returns (y [B,T,D], h_final [B,D,N] or None); ``h_final`` may be
+    passed in (it may be ``h0`` itself)."""
+    dev, (B, T, Dn, G, N), st = _ssm_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, 2)
+    if h0 is not None:
+        _whole("h0", h0, torch.float32, (B, Dn, N), dev)
+    odt = out_dtype or (x.dtype if y is None else y.dtype)
+    code = _dt_of("output dtype", odt)
+    need = gdr_ssm_scan_fwd_workspace_size(B, T, Dn, G, N)
+    with _On(dev, stream) as on:
+        y = _buffer("y", y, odt, (B, T, Dn), dev)
+        if h_final is not None or want_state:
+            h_final = _buffer("h_final", h_final, torch.float32, (B, Dn, N), dev)
+        if need or workspace is not None:
+            workspace = _scratch(workspace, need, dev)
+        _run("gdr_ssm_scan_fwd", lib.gdr_ssm_scan_fwd(
+            B, T, Dn, G, N, _DT[x.dtype], _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(z),
+            _p(dt_bias), _p(h0), _i64s(*st), GDR_SSM_SOFTPLUS if softplus else 0, code, _p(y),
+            _p(h_final), _p(workspace), 0 if workspace is None else workspace.numel(), on.ptr))
+    return y, h_final
+
+
+def gdr_ssm_step(x, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, *, softplus=True,
+                 out_dtype=None, y=None, stream=None):
+    """One decode token of gdr_ssm_scan_fwd: x, dt, z [N,D], Bm, Cm [N,G,S] for
+    N sequences and S states; state [N,D,S] fp32, updated in place.  Returns
+    y [N,D]."""
+    dev, (Nq, Dn, G, N), st = _ssm_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, 1)
+    _whole("state", state, torch.float32, (Nq, Dn, N), dev)
+    odt = out_dtype or (x.dtype if y is None else y.dtype)
+    code = _dt_of("output dtype", odt)
+    with _On(dev, stream) as on:
+        y = _buffer("y", y, odt, (Nq, Dn), dev)
+        _run("gdr_ssm_step", lib.gdr_ssm_step(
+            Nq, Dn, G, N, _DT[x.dtype], _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(z),
+            _p(dt_bias), _p(state), _i64s(*st), GDR_SSM_SOFTPLUS if softplus else 0, code, _p(y),
+            on.ptr))
+    return y
+
+
+def gdr_ssm_scan_bwd_workspace_size(B, T, D, G, N) -> int:
+    """Bytes of device workspace gdr_ssm_scan_bwd needs."""
+    return int(lib.gdr_ssm_scan_bwd_workspace_size(B, T, D, G, N))
+
+
+def gdr_ssm_scan_bwd(x, dt, A, Bm, Cm, D, z, dt_bias, h0, dout, dh_final=None, *, softplus=True,
+                     grad_dtype=torch.float32, want_dh0=True, workspace=None, stream=None):
+    """Reverse mode of gdr_ssm_scan_fwd for dL/dy = ``dout`` [B,T,D] (fp32 or
+    bf16, strides free) and dL/dh_final = ``dh_final`` [B,D,N] fp32 or None.
+    Returns (dx, ddt, dA, dB, dC, dD, dz, ddt_bias, dh0): dx, ddt, dB, dC, dz
+    in ``grad_dtype``, the others fp32; None for D, z, dt_bias that were None
+    and for dh0 without ``want_dh0``."""
+    dev, (B, T, Dn, G, N), st = _ssm_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, 2)
+    if h0 is not None:
+        _whole("h0", h0, torch.float32, (B, Dn, N), dev)
+    _first("dout", dout, 3)
+    _like("dout", dout, dout.dtype, (B, T, Dn), dev)
+    st += _row_strides("dout", dout, 2)
+    if dh_final is not None:
+        _whole("dh_final", dh_final, torch.float32, (B, Dn, N), dev)
+    code = _dt_of("grad_dtype", grad_dtype)
+    with _On(dev, stream) as on:
+        f32 = dict(dtype=torch.float32, device=dev)
+        act = dict(dtype=grad_dtype, device=dev)
+        dx, ddt = torch.empty((B, T, Dn), **act), torch.empty((B, T, Dn), **act)
+        dB, dC = torch.empty((B, T, G, N), **act), torch.empty((B, T, G, N), **act)
+        dz = None if z is None else torch.empty((B, T, Dn), **act)
+        dA = torch.empty((Dn, N), **f32)
+        dD = None if D is None else torch.empty((Dn,), **f32)
+        db = None if dt_bias is None else torch.empty((Dn,), **f32)
+        dh0 = torch.empty((B, Dn, N), **f32) if want_dh0 else None
+        workspace = _scratch(workspace, gdr_ssm_scan_bwd_workspace_size(B, T, Dn, G, N), dev)
+        _run("gdr_ssm_scan_bwd", lib.gdr_ssm_scan_bwd(
+            B, T, Dn, G, N, _DT[x.dtype], _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(z),
+            _p(dt_bias), _p(h0), _DT[dout.dtype], _p(dout), _p(dh_final), _i64s(*st),
+            GDR_SSM_SOFTPLUS if softplus else 0, code, _p(dx), _p(ddt), _p(dA), _p(dB), _p(dC),
+            _p(dD), _p(dz), _p(db), _p(dh0), _p(workspace), workspace.numel(), on.ptr))
+    return dx, ddt, dA, dB, dC, dD, dz, db, dh0
+
+
+def _as_rows(name, t):
+    """[..., C] as rows of C channels one stride apart: (rows, C, stride)."""
+    if t.dim() < 1:
+        raise ValueError(f"{name} must be [..., C]")
+    C = t.shape[-1]
+    if t.dim() == 2:
+        _row_strides(name, t, 1)
+        return t.shape[0], C, t.stride(0)
+    if t.is_contiguous():
+        return (t.numel() // C if C else 0), C, C
+    try:
+        v = t.view(-1, C)
+    except RuntimeError:
+        raise ValueError(f"{name} must be rows one stride apart") from None
+    _row_strides(name, v, 1)
+    return v.shape[0], C, v.stride(0)
+
+
+def gdr_layer_norm_fwd(x, w=None, b=None, eps=1e-5, *, residual=None, out_dtype=None, y=None,
+                       h=None, stream=None):
+    """Layer norm over the last axis of x [..., C] (fp32 or bf16), after adding
+    ``residual`` (its own dtype) when given.  w, b [C] fp32 or None (ones,
+    zeros).  Returns y, or (y, h) with the sum h in the residual's dtype.  x and
+    residual may be row slices (one stride from row to row); ``y`` may be x and
+    ``h`` may be residual itself."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    dev = _first("x", x, x.dim())
+    R, C, xr = _as_rows("x", x)
+    rdt, rr = x.dtype, 0
+    if residual is not None:
+        _first("residual", residual, x.dim())
+        _like("residual", residual, residual.dtype, x.shape, dev)
+        rdt, rr = residual.dtype, _as_rows("residual", residual)[2]
+    elif h is not None:
+        raise ValueError("h needs a residual")
+    if w is not None:
+        _whole("w", w, torch.float32, (C,), dev)
+    if b is not None:
+        _whole("b", b, torch.float32, (C,), dev)
+    odt = out_dtype or (x.dtype if y is None else y.dtype)
+    code = _dt_of("output dtype", odt)
+    with _On(dev, stream) as on:
+        y = _buffer("y", y, odt, x.shape, dev)
+        if residual is not None:
+            h = _buffer("h", h, rdt, x.shape, dev)
+        _run("gdr_layer_norm_fwd", lib.gdr_layer_norm_fwd(
+            R, C, _DT[x.dtype], _p(x), xr, _DT[rdt], _p(residual), rr, _p(w), _p(b), float(eps),
+            code, _p(y), _p(h), on.ptr))
+    return y if residual is None else (y, h)
+
+
+def gdr_layer_norm_bwd_workspace_size(R, C) -> int:
+    """Bytes of device workspace gdr_layer_norm_bwd needs for dw and db."""
+    return int(lib.gdr_layer_norm_bwd_workspace_size(R, C))
+
+
+def gdr_layer_norm_bwd(x, w, dy, eps=1e-5, *, dres=None, grad_dtype=torch.float32, want_dw=True,
+                       workspace=None, stream=None):
+    """Reverse mode of gdr_layer_norm_fwd: x [..., C] is the normalised tensor
+    (h where a residual was added), dy [..., C] the gradient of y (fp32 or
+    bf16), ``dres`` [..., C] in ``grad_dtype`` or None the gradient that reaches
+    x past the norm.  Returns (dx in ``grad_dtype``, dw, db [C] fp32), dw and db
+    None without ``want_dw``."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    dev = _first("x", x, x.dim())
+    R, C, xr = _as_rows("x", x)
+    _first("dy", dy, x.dim())
+    _like("dy", dy, dy.dtype, x.shape, dev)
+    yr = _as_rows("dy", dy)[2]
+    code, rr = _dt_of("grad_dtype", grad_dtype), 0
+    if dres is not None:
+        _like("dres", dres, grad_dtype, x.shape, dev)
+        rr = _as_rows("dres", dres)[2]
+    if w is not None:
+        _whole("w", w, torch.float32, (C,), dev)
+    with _On(dev, stream) as on:
+        dx = torch.empty(x.shape, dtype=grad_dtype, device=dev)
+        f32 = dict(dtype=torch.float32, device=dev)
+        dw, db = (torch.empty((C,), **f32), torch.empty((C,), **f32)) if want_dw else (None, None)
+        if want_dw or workspace is not None:
+            workspace = _scratch(workspace, gdr_layer_norm_bwd_workspace_size(R, C), dev)
+        _run("gdr_layer_norm_bwd", lib.gdr_layer_norm_bwd(
+            R, C, _DT[x.dtype], _p(x), xr, _p(w), _DT[dy.dtype], _p(dy), yr, float(eps), code,
+            _p(dres), rr, _p(dx), _p(dw), _p(db), _p(workspace),
+            0 if workspace is None else workspace.numel(), on.ptr))
+    return dx, dw, db

@@ -3,6 +3,7 @@
 // Every check runs on the host before anything is enqueued, so an error
 // status means nothing was written.  No exception leaves this file.
 #include "../../include/gdr.h"
+#include "api_checks.h"
 #include "gdr_device.h"
 #include "launch.h"
 
@@ -17,38 +18,11 @@ __global__ void state_copy_kernel(const float* __restrict__ s0, float* __restric
         s[i] = s0 ? s0[i] : 0.f;
 }
 
-bool aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 bool dims_ok(int64_t dk, int64_t dv) {
     return (dk == 64 || dk == 128) && (dv == 64 || dv == 128);
 }
 
-bool dtype_ok(gdr_dtype_t d) { return d == GDR_F32 || d == GDR_BF16; }
-
 bool flags_ok(uint32_t f) { return (f & ~GDR_L2NORM_QK) == 0; }
-
-gdr_status_t from_hip(hipError_t e) { return e == hipSuccess ? GDR_OK : GDR_ERR_DEVICE; }
-
-// Every listed pointer must be non-NULL and 16-byte aligned.
-bool ptrs_ok(std::initializer_list<const void*> ps) {
-    for (const void* p : ps)
-        if (!p || !aligned(p)) return false;
-    return true;
-}
-
-bool opt_ok(const void* p) { return !p || aligned(p); }
-
-// Element-aligned pointer (scalar gates and outputs are accessed per element).
-bool elem_ok(const void* p, size_t bytes) {
-    return p && (reinterpret_cast<uintptr_t>(p) % bytes) == 0;
-}
-
-// Largest element count of any tensor must fit the kernels' 64-bit offsets.
-bool sizes_ok(int64_t a, int64_t b, int64_t c) {
-    if (a < 0 || b < 0 || c < 0) return false;
-    const double n = (double)a * (double)b * (double)c;
-    return n < 4.0e18;
-}
 
 // One work-item per element over n elements, 256 per workgroup, fits a
 // dispatch (the backward's reductions).
@@ -993,4 +967,4 @@ extern "C" const char* gdr_status_string(gdr_status_t s) {
     return "unknown status";
 }
 
-extern "C" int gdr_version(void) { return 400; }
+extern "C" int gdr_version(void) { return 500; }

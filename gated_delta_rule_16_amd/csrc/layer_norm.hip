@@ -1,0 +1,465 @@
+// gdr_layer_norm_fwd / _bwd: the block's pre-norm over rows of C channels,
+//
+//   h = x (+ r, stored), mu = mean h, v = mean (h - mu)^2,
+//   y = (h - mu) / sqrt(v + eps) * w + b,
+//
+// and its reverse mode, with n = (h - mu) rstd and dn = dy w:
+//
+//   dh = rstd (dn - mean dn - n mean(dn n)) (+ dr),  dw = sum_rows dy n,  db = sum_rows dy.
+//
+// Bound by HBM: one pass over each tensor.  A row is held in registers
+// between its two reductions (mean, then the centred squares, so there is no
+// cancellation of mean squares): one wave per row up to 2048 channels, with no
+// barrier; one workgroup of four waves per row up to 8192; beyond that the
+// workgroup walks the row again (from L2) for each reduction.
+#include "launch.h"
+#include "rows.h"
+
+namespace gdr {
+
+namespace {
+
+constexpr int E = 8;              // channels per lane and access
+
+__device__ __forceinline__ float wave_sum(float x) {
+    x += dpp_mov<0xB1>(x);
+    x += dpp_mov<0x4E>(x);
+    x += dpp_mov<0x141>(x);
+    x += dpp_mov<0x140>(x);
+    x += __shfl_xor(x, 16, 64);
+    x += __shfl_xor(x, 32, 64);
+    return x;
+}
+
+// Sum over the row's threads: its wave (WG false), or the workgroup.  `red`
+// is one of alternating slots, so one barrier per sum suffices: a slot is
+// written again only after the barrier of the sum in between.
+template <bool WG>
+__device__ __forceinline__ float row_total(float x, float* red) {
+    x = wave_sum(x);
+    if constexpr (WG) {
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
+        __syncthreads();
+        x = (red[0] + red[1]) + (red[2] + red[3]);
+    }
+    return x;
+}
+
+__device__ __forceinline__ int left(int64_t C, int64_t c) {
+    const int64_t v = C - c;
+    return v < 0 ? 0 : v > E ? E : (int)v;
+}
+
+// x (+ r, rounded to the stored type) of one group of channels; h is stored.
+__device__ __forceinline__ void sum_in(float (&h)[E], const NormArgs& a, int64_t xo, int64_t ro,
+                                       int64_t ho, int valid) {
+    RawRow<E> rx, rr;
+    row_load<E>(rx, a.x, xo, a.in_bf16, valid);
+    if (a.res) row_load<E>(rr, a.res, ro, a.res_bf16, valid);
+    row_unpack<E>(h, rx, a.in_bf16);
+    if (a.res) {
+        float q[E];
+        row_unpack<E>(q, rr, a.res_bf16);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            h[e] += q[e];
+            if (a.res_bf16) h[e] = bf2f(f2bf(h[e]));
+        }
+        row_store<E>(a.h, ho, a.res_bf16, h, valid);
+    }
+}
+
+// NV groups of 8 channels per thread; WG: a workgroup per row, else a wave.
+template <int NV, bool WG>
+__global__ __launch_bounds__(256) void norm_fwd_kernel(NormArgs a) {
+    __shared__ float red[2][4];
+    constexpr int NT = WG ? 256 : 64;
+    const int id = WG ? threadIdx.x : (threadIdx.x & 63);
+    const int64_t row = WG ? blockIdx.x : (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (row >= a.R) return;           // a whole wave (WG: never)
+    float h[NV][E];
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int64_t c = (int64_t)(k * NT + id) * E;
+        sum_in(h[k], a, row * a.xr + c, row * a.rr + c, row * a.C + c, left(a.C, c));
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int e = 0; e < E; ++e) s += h[k][e];
+    const float inv = 1.f / (float)a.C;
+    const float mu = row_total<WG>(s, red[0]) * inv;
+    s = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int v = left(a.C, (int64_t)(k * NT + id) * E);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            h[k][e] -= mu;
+            if (e < v) s = __builtin_fmaf(h[k][e], h[k][e], s);
+        }
+    }
+    const float rstd = 1.f / sqrtf(row_total<WG>(s, red[1]) * inv + a.eps);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int64_t c = (int64_t)(k * NT + id) * E;
+        const int v = left(a.C, c);
+        float w[E], b[E];
+        if (a.w) param_load<E>(w, a.w + c, v);
+        if (a.b) param_load<E>(b, a.b + c, v);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            float y = h[k][e] * rstd;
+            if (a.w) y *= w[e];
+            if (a.b) y += b[e];
+            h[k][e] = y;
+        }
+        row_store<E>(a.y, row * a.C + c, a.out_bf16, h[k], v);
+    }
+}
+
+// Rows too long for registers: the row is read once per reduction.  With a
+// residual the stored sum is what the later walks read (each thread its own
+// channels, so no barrier is needed between its store and its loads).
+__global__ __launch_bounds__(256) void norm_fwd_long_kernel(NormArgs a) {
+    __shared__ float red[2][4];
+    const int64_t row = blockIdx.x;
+    const int64_t step = 256 * E;
+    float s = 0.f;
+    for (int64_t c = (int64_t)threadIdx.x * E; c < a.C; c += step) {
+        float h[E];
+        sum_in(h, a, row * a.xr + c, row * a.rr + c, row * a.C + c, left(a.C, c));
+#pragma unroll
+        for (int e = 0; e < E; ++e) s += h[e];
+    }
+    const void* src = a.res ? a.h : a.x;
+    const bool sbf = a.res ? a.res_bf16 : a.in_bf16;
+    const int64_t so = row * (a.res ? a.C : a.xr);
+    const float inv = 1.f / (float)a.C;
+    const float mu = row_total<true>(s, red[0]) * inv;
+    s = 0.f;
+    for (int64_t c = (int64_t)threadIdx.x * E; c < a.C; c += step) {
+        RawRow<E> r;
+        float h[E];
+        const int v = left(a.C, c);
+        row_load<E>(r, src, so + c, sbf, v);
+        row_unpack<E>(h, r, sbf);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (e < v) s = __builtin_fmaf(h[e] - mu, h[e] - mu, s);
+    }
+    const float rstd = 1.f / sqrtf(row_total<true>(s, red[1]) * inv + a.eps);
+    for (int64_t c = (int64_t)threadIdx.x * E; c < a.C; c += step) {
+        RawRow<E> r;
+        float h[E], w[E], b[E];
+        const int v = left(a.C, c);
+        row_load<E>(r, src, so + c, sbf, v);
+        row_unpack<E>(h, r, sbf);
+        if (a.w) param_load<E>(w, a.w + c, v);
+        if (a.b) param_load<E>(b, a.b + c, v);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            float y = (h[e] - mu) * rstd;
+            if (a.w) y *= w[e];
+            if (a.b) y += b[e];
+            h[e] = y;
+        }
+        row_store<E>(a.y, row * a.C + c, a.out_bf16, h, v);
+    }
+}
+
+// Backward: a persistent grid walks the rows; dw and db stay in registers
+// over all rows of a wave (WG: of the workgroup) and leave as one partial row
+// [2 C] per workgroup.
+template <int NV, bool WG>
+__global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwdArgs a) {
+    __shared__ float red[4][4];
+    __shared__ float join[WG ? 1 : 3 * 64 * (2 * E + 1)];
+    constexpr int NT = WG ? 256 : 64;
+    const int id = WG ? threadIdx.x : (threadIdx.x & 63);
+    const int wv = threadIdx.x >> 6;
+    float dw[NV][E], db[NV][E];
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int e = 0; e < E; ++e) dw[k][e] = db[k][e] = 0.f;
+    const float inv = 1.f / (float)a.C;
+    const int64_t stride = (int64_t)gridDim.x * (WG ? 1 : 4);
+    for (int64_t row = WG ? blockIdx.x : (int64_t)blockIdx.x * 4 + wv; row < a.R; row += stride) {
+        float h[NV][E], d[NV][E];
+        RawRow<E> rh[NV], rd[NV], rr[NV];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int64_t c = (int64_t)(k * NT + id) * E;
+            const int v = left(a.C, c);
+            row_load<E>(rh[k], a.x, row * a.xr + c, a.in_bf16, v);
+            row_load<E>(rd[k], a.dy, row * a.yr + c, a.dy_bf16, v);
+            if (a.dres) row_load<E>(rr[k], a.dres, row * a.rr + c, a.grad_bf16, v);
+        }
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            row_unpack<E>(h[k], rh[k], a.in_bf16);
+#pragma unroll
+            for (int e = 0; e < E; ++e) s += h[k][e];
+        }
+        const float mu = row_total<WG>(s, red[0]) * inv;
+        s = 0.f;
+        float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int64_t c = (int64_t)(k * NT + id) * E;
+            const int v = left(a.C, c);
+            float w[E];
+            row_unpack<E>(d[k], rd[k], a.dy_bf16);
+            if (a.w) param_load<E>(w, a.w + c, v);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                h[k][e] = e < v ? h[k][e] - mu : 0.f;
+                s = __builtin_fmaf(h[k][e], h[k][e], s);
+                const float dn = a.w ? d[k][e] * w[e] : d[k][e];
+                s1 += dn;
+                s2 = __builtin_fmaf(dn, h[k][e], s2);
+            }
+        }
+        const float rstd = 1.f / sqrtf(row_total<WG>(s, red[1]) * inv + a.eps);
+        const float m1 = row_total<WG>(s1, red[2]) * inv;
+        const float m2 = row_total<WG>(s2, red[3]) * inv * rstd;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int64_t c = (int64_t)(k * NT + id) * E;
+            const int v = left(a.C, c);
+            float w[E], out[E], q[E];
+            if (a.w) param_load<E>(w, a.w + c, v);
+            if (a.dres) row_unpack<E>(q, rr[k], a.grad_bf16);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const float n = h[k][e] * rstd;
+                const float dn = a.w ? d[k][e] * w[e] : d[k][e];
+                dw[k][e] = __builtin_fmaf(d[k][e], n, dw[k][e]);
+                db[k][e] += d[k][e];
+                out[e] = rstd * (dn - m1 - n * m2);
+                if (a.dres) out[e] += q[e];
+            }
+            row_store<E>(a.dx, row * a.C + c, a.grad_bf16, out, v);
+        }
+    }
+    if (!a.part) return;
+    float* part = a.part + (int64_t)blockIdx.x * 2 * a.C;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int64_t c = (int64_t)(k * NT + id) * E;
+        if constexpr (!WG) {
+            // the four waves hold the same channels: join them, group by group
+            if (k > 0) __syncthreads();
+            if (wv > 0) {
+                float* p = join + ((wv - 1) * 64 + id) * (2 * E + 1);
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    p[e] = dw[k][e];
+                    p[E + e] = db[k][e];
+                }
+            }
+            __syncthreads();
+            if (wv > 0) continue;
+#pragma unroll
+            for (int q = 0; q < 3; ++q) {
+                const float* p = join + (q * 64 + id) * (2 * E + 1);
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    dw[k][e] += p[e];
+                    db[k][e] += p[E + e];
+                }
+            }
+        }
+        const int v = left(a.C, c);
+        row_store<E>(part, c, false, dw[k], v);
+        row_store<E>(part, a.C + c, false, db[k], v);
+    }
+}
+
+// Rows too long for registers: dx first, a workgroup per row; the column sums
+// by a second kernel that walks the rows with each row's mean and rstd.
+__global__ __launch_bounds__(256) void norm_bwd_long_kernel(NormBwdArgs a, float* stats) {
+    __shared__ float red[4][4];
+    const int64_t row = blockIdx.x;
+    const int64_t step = 256 * E;
+    const float inv = 1.f / (float)a.C;
+    float s = 0.f;
+    for (int64_t c = (int64_t)threadIdx.x * E; c < a.C; c += step) {
+        RawRow<E> r;
+        float h[E];
+        row_load<E>(r, a.x, row * a.xr + c, a.in_bf16, left(a.C, c));
+        row_unpack<E>(h, r, a.in_bf16);
+#pragma unroll
+        for (int e = 0; e < E; ++e) s += h[e];
+    }
+    const float mu = row_total<true>(s, red[0]) * inv;
+    s = 0.f;
+    float s1 = 0.f, s2 = 0.f;
+    for (int64_t c = (int64_t)threadIdx.x * E; c < a.C; c += step) {
+        RawRow<E> rh, rd;
+        float h[E], d[E], w[E];
+        const int v = left(a.C, c);
+        row_load<E>(rh, a.x, row * a.xr + c, a.in_bf16, v);
+        row_load<E>(rd, a.dy, row * a.yr + c, a.dy_bf16, v);
+        if (a.w) param_load<E>(w, a.w + c, v);
+        row_unpack<E>(h, rh, a.in_bf16);
+        row_unpack<E>(d, rd, a.dy_bf16);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float x = e < v ? h[e] - mu : 0.f;
+            const float dn = a.w ? d[e] * w[e] : d[e];
+            s = __builtin_fmaf(x, x, s);
+            s1 += dn;
+            s2 = __builtin_fmaf(dn, x, s2);
+        }
+    }
+    const float rstd = 1.f / sqrtf(row_total<true>(s, red[1]) * inv + a.eps);
+    const float m1 = row_total<true>(s1, red[2]) * inv;
+    const float m2 = row_total<true>(s2, red[3]) * inv * rstd;
+    if (stats && threadIdx.x == 0) {
+        stats[2 * row] = mu;
+        stats[2 * row + 1] = rstd;
+    }
+    for (int64_t c = (int64_t)threadIdx.x * E; c < a.C; c += step) {
+        RawRow<E> rh, rd, rr;
+        float h[E], d[E], w[E], q[E];
+        const int v = left(a.C, c);
+        row_load<E>(rh, a.x, row * a.xr + c, a.in_bf16, v);
+        row_load<E>(rd, a.dy, row * a.yr + c, a.dy_bf16, v);
+        if (a.dres) row_load<E>(rr, a.dres, row * a.rr + c, a.grad_bf16, v);
+        if (a.w) param_load<E>(w, a.w + c, v);
+        row_unpack<E>(h, rh, a.in_bf16);
+        row_unpack<E>(d, rd, a.dy_bf16);
+        if (a.dres) row_unpack<E>(q, rr, a.grad_bf16);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const float dn = a.w ? d[e] * w[e] : d[e];
+            h[e] = rstd * (dn - m1 - (h[e] - mu) * rstd * m2);
+            if (a.dres) h[e] += q[e];
+        }
+        row_store<E>(a.dx, row * a.C + c, a.grad_bf16, h, v);
+    }
+}
+
+// Column sums of the long rows: a wave owns 64 groups of 8 channels, a
+// workgroup's four waves take every fourth of its rows.
+__global__ __launch_bounds__(256) void norm_dw_long_kernel(NormBwdArgs a, const float* stats,
+                                                           int64_t ncb, int64_t nrow) {
+    __shared__ float join[3 * 64 * (2 * E + 1)];
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    const int64_t cb = blockIdx.x % ncb, slot = blockIdx.x / ncb;
+    const int64_t c = (cb * 64 + lane) * E;
+    const int v = left(a.C, c);
+    float dw[E], db[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) dw[e] = db[e] = 0.f;
+    if (v > 0)
+        for (int64_t row = slot * 4 + wv; row < a.R; row += nrow * 4) {
+            RawRow<E> rh, rd;
+            float h[E], d[E];
+            row_load<E>(rh, a.x, row * a.xr + c, a.in_bf16, v);
+            row_load<E>(rd, a.dy, row * a.yr + c, a.dy_bf16, v);
+            row_unpack<E>(h, rh, a.in_bf16);
+            row_unpack<E>(d, rd, a.dy_bf16);
+            const float mu = stats[2 * row], rstd = stats[2 * row + 1];
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                dw[e] = __builtin_fmaf(d[e], (h[e] - mu) * rstd, dw[e]);
+                db[e] += d[e];
+            }
+        }
+    if (wv > 0) {
+        float* p = join + ((wv - 1) * 64 + lane) * (2 * E + 1);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            p[e] = dw[e];
+            p[E + e] = db[e];
+        }
+    }
+    __syncthreads();
+    if (wv > 0 || v == 0) return;
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+        const float* p = join + (q * 64 + lane) * (2 * E + 1);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            dw[e] += p[e];
+            db[e] += p[E + e];
+        }
+    }
+    float* part = a.part + slot * 2 * a.C;
+    row_store<E>(part, c, false, dw, v);
+    row_store<E>(part, a.C + c, false, db, v);
+}
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+constexpr int64_t WAVE_MAX = 2048, WG_MAX = 8192;
+
+// Workgroups of the backward (= partial rows).
+int64_t bwd_rows(int64_t R, int64_t C) {
+    if (C > WG_MAX) {
+        const int64_t cap = cdiv(2048, cdiv(C, 64 * E));
+        const int64_t n = cdiv(R, 16);
+        return n < cap ? n : cap;
+    }
+    const int64_t n = C <= WAVE_MAX ? cdiv(R, 4) : R;
+    return n < 512 ? n : 512;
+}
+
+size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+}  // namespace
+
+// Workspace: the partials of dw and db [bwd_rows][2 C]; beyond WG_MAX also
+// each row's mean and rstd.
+size_t norm_bwd_workspace_bytes(int64_t R, int64_t C) {
+    size_t n = up256(sizeof(float) * (size_t)(bwd_rows(R, C) * 2 * C));
+    if (C > WG_MAX) n += sizeof(float) * (size_t)(2 * R);
+    return n;
+}
+
+hipError_t launch_norm_fwd(const NormArgs& a) {
+    const int64_t C = a.C;
+    const dim3 wave((unsigned)cdiv(a.R, 4)), wg((unsigned)a.R);
+#define FWD(NV, WG, GRID) \
+    hipLaunchKernelGGL((norm_fwd_kernel<NV, WG>), GRID, dim3(256), 0, a.stream, a)
+    if (C <= 512) FWD(1, false, wave);
+    else if (C <= 1024) FWD(2, false, wave);
+    else if (C <= WAVE_MAX) FWD(4, false, wave);
+    else if (C <= 4096) FWD(2, true, wg);
+    else if (C <= WG_MAX) FWD(4, true, wg);
+    else hipLaunchKernelGGL(norm_fwd_long_kernel, wg, dim3(256), 0, a.stream, a);
+#undef FWD
+    return hipGetLastError();
+}
+
+hipError_t launch_norm_bwd(const NormBwdArgs& a) {
+    const int64_t C = a.C, nrow = bwd_rows(a.R, C);
+    const dim3 grid((unsigned)nrow);
+#define BWD(NV, WG) hipLaunchKernelGGL((norm_bwd_kernel<NV, WG>), grid, dim3(256), 0, a.stream, a)
+    if (C <= 512) BWD(1, false);
+    else if (C <= 1024) BWD(2, false);
+    else if (C <= WAVE_MAX) BWD(4, false);
+    else if (C <= 4096) BWD(2, true);
+    else if (C <= WG_MAX) BWD(4, true);
+    else {
+        const int64_t ncb = cdiv(C, 64 * E);
+        float* stats = a.part ? reinterpret_cast<float*>(reinterpret_cast<char*>(a.part) +
+                                up256(sizeof(float) * (size_t)(nrow * 2 * C))) : nullptr;
+        hipLaunchKernelGGL(norm_bwd_long_kernel, dim3((unsigned)a.R), dim3(256), 0, a.stream, a,
+                           stats);
+        if (a.part)
+            hipLaunchKernelGGL(norm_dw_long_kernel, dim3((unsigned)(ncb * nrow)), dim3(256), 0,
+                               a.stream, a, stats, ncb, nrow);
+    }
+#undef BWD
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !a.part) return e;
+    return launch_sum_partials(a.part, nrow, 2 * C, a.dw, C, a.db, C, nullptr, a.stream);
+}
+
+}  // namespace gdr

@@ -1,0 +1,355 @@
+// gdr_short_conv_*: the short causal depthwise convolution of the block's q,
+// k and v paths (and of a state space layer's input), with an optional SiLU:
+//
+//   u_t[c] = bias[c] + sum_{j<K} w[c][j] x_{t-K+1+j}[c],  y = u or u sigmoid(u),
+//
+// K = 2, 3 or 4; x before the sequence is the state (its last K - 1 inputs).
+// Reverse mode, with du = dy, or dy sigmoid(u)(1 + u (1 - sigmoid(u))):
+//
+//   dx_i = sum_j w[j] du_{i+K-1-j},  dw[j] = sum_t x_{t-K+1+j} du_t,  dbias = sum_t du_t.
+//
+// All of it is bound by HBM: a channel costs 2 (3 backward) accesses against
+// ~2K + 4 (6K + 8) operations.  A lane owns E neighbouring channels and walks
+// along the tokens of its stretch with the last K - 1 inputs in registers, so
+// every input is read once but for the K - 1 rows where stretches meet.
+#include "launch.h"
+#include "rows.h"
+
+namespace gdr {
+
+namespace {
+
+constexpr int E = 8;              // channels per lane: one 16-byte access in bf16
+constexpr int FWD_TOKENS = 4;     // loads in flight per lane
+
+__device__ __forceinline__ int clampi(int64_t v, int hi) {
+    return v < 0 ? 0 : v > hi ? hi : (int)v;
+}
+
+// Row t of [state; x] for one lane's channels: t >= 0 from x, else the state
+// (or zeros without one).
+template <int EE>
+__device__ __forceinline__ void load_in(RawRow<EE>& r, const ConvArgs& a, int64_t b, int64_t t,
+                                        int64_t c, int valid) {
+    if (t >= 0)
+        row_load<EE>(r, a.x, b * a.xb + t * a.xt + c, a.in_bf16, valid);
+    else if (a.s0)
+        row_load<EE>(r, a.s0, (b * (a.K - 1) + t + a.K - 1) * a.C + c, a.in_bf16, valid);
+    else
+        row_load<EE>(r, a.x, 0, a.in_bf16, 0);
+}
+
+template <int K>
+__global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int64_t ncb, int64_t nstretch,
+                                                       int TL) {
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    int64_t id = blockIdx.x;
+    const int64_t cb = id % ncb;
+    id /= ncb;
+    const int64_t st = (id % nstretch) * 4 + wv, b = id / nstretch;
+    const int64_t c = (cb * 64 + lane) * E;
+    const int valid = clampi(a.C - c, E);
+    const int64_t t0 = st * TL;
+    if (valid == 0 || t0 >= a.T) return;
+    const int64_t t1 = t0 + TL < a.T ? t0 + TL : a.T;
+    float w[E * K], bias[E];
+    param_load<E * K>(w, a.w + c * K, valid * K);
+    param_load<E>(bias, a.bias + c, a.bias ? valid : 0);
+    float win[K - 1][E];
+    {
+        RawRow<E> r[K - 1];
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) load_in<E>(r[j], a, b, t0 - (K - 1) + j, c, valid);
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) row_unpack<E>(win[j], r[j], a.in_bf16);
+        if (t0 == 0 && a.s_final) {
+            // the lane that reads the state also writes the next one, so the
+            // two may be the same buffer: all K - 1 rows are read (the state
+            // rows above, or x) before the first is written
+            RawRow<E> f[K - 1];
+#pragma unroll
+            for (int m = 0; m < K - 1; ++m) load_in<E>(f[m], a, b, a.T - (K - 1) + m, c, valid);
+#pragma unroll
+            for (int m = 0; m < K - 1; ++m) {
+                float v[E];
+                row_unpack<E>(v, f[m], a.in_bf16);
+                row_store<E>(a.s_final, (b * (K - 1) + m) * a.C + c, a.in_bf16, v, valid);
+            }
+        }
+    }
+    for (int64_t t = t0; t < t1; t += FWD_TOKENS) {
+        RawRow<E> r[FWD_TOKENS];
+#pragma unroll
+        for (int u = 0; u < FWD_TOKENS; ++u)
+            row_load<E>(r[u], a.x, b * a.xb + (t + u < t1 ? t + u : t1 - 1) * a.xt + c, a.in_bf16,
+                        valid);
+#pragma unroll
+        for (int u = 0; u < FWD_TOKENS; ++u) {
+            float x[E], y[E];
+            row_unpack<E>(x, r[u], a.in_bf16);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                float s = bias[e];
+#pragma unroll
+                for (int j = 0; j < K - 1; ++j) s = __builtin_fmaf(w[e * K + j], win[j][e], s);
+                s = __builtin_fmaf(w[e * K + K - 1], x[e], s);
+                y[e] = a.silu ? s * sigmoid(s) : s;
+#pragma unroll
+                for (int j = 0; j + 1 < K - 1; ++j) win[j][e] = win[j + 1][e];
+                win[K - 2][e] = x[e];
+            }
+            if (t + u < t1) row_store<E>(a.y, (b * a.T + t + u) * a.C + c, a.out_bf16, y, valid);
+        }
+    }
+}
+
+// One decode token: the lane shifts its own channels' state.
+template <int K>
+__global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a, int64_t ncg) {
+    constexpr int SE = 4;
+    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t b = id / ncg, c = (id % ncg) * SE;
+    if (b >= a.B) return;
+    const int valid = clampi(a.C - c, SE);
+    RawRow<SE> r[K];
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j)
+        row_load<SE>(r[j], a.s0, (b * (K - 1) + j) * a.C + c, a.in_bf16, valid);
+    row_load<SE>(r[K - 1], a.x, b * a.xb + c, a.in_bf16, valid);
+    float y[SE], x[K][SE], w[SE * K];
+    param_load<SE * K>(w, a.w + c * K, valid * K);
+    param_load<SE>(y, a.bias + c, a.bias ? valid : 0);
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+        row_unpack<SE>(x[j], r[j], a.in_bf16);
+#pragma unroll
+        for (int e = 0; e < SE; ++e)
+            y[e] = __builtin_fmaf(w[e * K + j], x[j][e], y[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < SE; ++e) y[e] = a.silu ? y[e] * sigmoid(y[e]) : y[e];
+    row_store<SE>(a.y, b * a.C + c, a.out_bf16, y, valid);
+#pragma unroll
+    for (int j = 0; j < K - 1; ++j)
+        row_store<SE>(a.s_final, (b * (K - 1) + j) * a.C + c, a.in_bf16, x[j + 1], valid);
+}
+
+constexpr int BE = 4;             // backward: channels per lane
+
+// Backward.  Wave wv of a workgroup walks stretch 4 i + wv; dw and dbias stay
+// in registers over all of a workgroup's stretches, are joined over its waves
+// through LDS and go out as one partial row [C (K + 1)] per workgroup row.
+// The walk runs K - 1 tokens past the stretch to complete its last dx, and a
+// stretch leaves the dx of the K - 1 rows before it to its neighbour -- but
+// the first, whose earlier rows are the state's gradient.
+template <int K>
+__global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int64_t ncb, int64_t nrow,
+                                                       int64_t nstretch, int TL) {
+    __shared__ float red[3][64][BE * (K + 1) + 1];
+    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    const int64_t cb = blockIdx.x % ncb, row = blockIdx.x / ncb;
+    const int64_t c = (cb * 64 + lane) * BE;
+    const int valid = clampi(a.C - c, BE);
+    float w[BE * K], bias[BE], dw[BE][K], db[BE];
+    param_load<BE * K>(w, a.w + c * K, valid * K);
+    param_load<BE>(bias, a.bias + c, a.bias ? valid : 0);
+#pragma unroll
+    for (int e = 0; e < BE; ++e) {
+        db[e] = 0.f;
+#pragma unroll
+        for (int j = 0; j < K; ++j) dw[e][j] = 0.f;
+    }
+    const int64_t units = a.B * nstretch;
+    if (valid > 0)
+        for (int64_t un = row; un < units; un += nrow) {
+            const int64_t b = un / nstretch, t0 = ((un % nstretch) * 4 + wv) * TL;
+            if (t0 >= a.T) continue;
+            const int64_t t1 = t0 + TL < a.T ? t0 + TL : a.T;
+            // x window: rows t - K + 1 .. t; du window: du_{t-K+1} .. du_t
+            float win[K][BE], du[K][BE];
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) {
+                RawRow<BE> r;
+                load_in<BE>(r, a, b, t0 - (K - 1) + j, c, valid);
+                row_unpack<BE>(win[j + 1], r, a.in_bf16);
+            }
+#pragma unroll
+            for (int j = 0; j < K; ++j)
+#pragma unroll
+                for (int e = 0; e < BE; ++e) du[j][e] = 0.f;
+            const int64_t tend = t1 + K - 1;
+            constexpr int U = 4;
+            for (int64_t tb = t0; tb < tend; tb += U) {
+                RawRow<BE> rx[U], rd[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int64_t t = tb + u;
+                    const int v = t < a.T && t < tend ? valid : 0;
+                    row_load<BE>(rx[u], a.x, v ? b * a.xb + t * a.xt + c : 0, a.in_bf16, v);
+                    row_load<BE>(rd[u], a.dy, v ? b * a.yb + t * a.yt + c : 0, a.dy_bf16, v);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int64_t t = tb + u;
+                    float x[BE], d[BE];
+                    row_unpack<BE>(x, rx[u], a.in_bf16);
+                    row_unpack<BE>(d, rd[u], a.dy_bf16);
+                    const bool mine = t < t1;     // du_t counts for dw here
+                    float out[BE];
+#pragma unroll
+                    for (int e = 0; e < BE; ++e) {
+#pragma unroll
+                        for (int j = 0; j + 1 < K; ++j) {
+                            win[j][e] = win[j + 1][e];
+                            du[j][e] = du[j + 1][e];
+                        }
+                        win[K - 1][e] = x[e];
+                        float g = d[e];
+                        if (a.silu) {
+                            float s = bias[e];
+#pragma unroll
+                            for (int j = 0; j < K; ++j) s = __builtin_fmaf(w[e * K + j], win[j][e], s);
+                            const float sg = sigmoid(s);
+                            g *= sg * __builtin_fmaf(s, 1.f - sg, 1.f);
+                        }
+                        // rows past the sequence loaded zeros, but an infinite
+                        // bias would still make their g NaN
+                        g = t < a.T ? g : 0.f;
+                        du[K - 1][e] = g;
+                        if (mine) {
+                            db[e] += g;
+#pragma unroll
+                            for (int j = 0; j < K; ++j)
+                                dw[e][j] = __builtin_fmaf(win[j][e], g, dw[e][j]);
+                        }
+                        // dx_{t-K+1} = sum_j w[j] du_{t-j}
+                        float o = 0.f;
+#pragma unroll
+                        for (int j = 0; j < K; ++j)
+                            o = __builtin_fmaf(w[e * K + j], du[K - 1 - j][e], o);
+                        out[e] = o;
+                    }
+                    const int64_t i = t - (K - 1);
+                    if (t >= tend || (i < t0 && t0 > 0)) continue;
+                    if (a.ds_final && i >= a.T - (K - 1)) {
+                        const float* p = a.ds_final +
+                                         (b * (K - 1) + i - (a.T - (K - 1))) * a.C + c;
+#pragma unroll
+                        for (int e = 0; e < BE; ++e)
+                            if (e < valid) out[e] += p[e];
+                    }
+                    if (i >= 0)
+                        row_store<BE>(a.dx, (b * a.T + i) * a.C + c, a.grad_bf16, out, valid);
+                    else if (a.ds0)
+                        row_store<BE>(a.ds0, (b * (K - 1) + i + K - 1) * a.C + c, false, out,
+                                      valid);
+                }
+            }
+        }
+    if (!a.part) return;
+    if (wv > 0) {
+#pragma unroll
+        for (int e = 0; e < BE; ++e) {
+#pragma unroll
+            for (int j = 0; j < K; ++j) red[wv - 1][lane][e * K + j] = dw[e][j];
+            red[wv - 1][lane][BE * K + e] = db[e];
+        }
+    }
+    __syncthreads();
+    if (wv == 0 && valid > 0) {
+        float* p = a.part + row * a.C * (K + 1);
+#pragma unroll
+        for (int e = 0; e < BE; ++e) {
+            if (e >= valid) break;
+#pragma unroll
+            for (int j = 0; j < K; ++j)
+                p[(c + e) * K + j] = (dw[e][j] + red[0][lane][e * K + j]) +
+                                     (red[1][lane][e * K + j] + red[2][lane][e * K + j]);
+            p[a.C * K + c + e] = (db[e] + red[0][lane][BE * K + e]) +
+                                 (red[1][lane][BE * K + e] + red[2][lane][BE * K + e]);
+        }
+    }
+}
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Tokens per wave's stretch: long enough that the K - 1 rows read twice are
+// few, short enough that the launch fills the chip.
+int stretch_tokens(int64_t B, int64_t T, int64_t ncb, int lo, int hi) {
+    int TL = hi;
+    while (TL > lo && B * ncb * cdiv(T, TL) < 8192) TL /= 2;
+    return TL;
+}
+
+// Backward: workgroup rows (partials of dw) for the launch.
+void bwd_shape(int64_t B, int64_t T, int64_t C, int64_t& ncb, int64_t& nstretch, int64_t& nrow,
+               int& TL) {
+    ncb = cdiv(C, 64 * BE);
+    TL = stretch_tokens(B, T, ncb, 8, 64);
+    nstretch = cdiv(T, 4 * (int64_t)TL);
+    const int64_t units = B * nstretch;
+    const int64_t cap = cdiv(4096, ncb);
+    nrow = units < cap ? units : cap;
+}
+
+}  // namespace
+
+size_t conv_bwd_workspace_bytes(int64_t B, int64_t T, int64_t C, int64_t K) {
+    int64_t ncb, nstretch, nrow;
+    int TL;
+    bwd_shape(B, T, C, ncb, nstretch, nrow, TL);
+    return sizeof(float) * (size_t)(nrow * C * (K + 1));
+}
+
+int64_t conv_workgroups(int64_t B, int64_t T, int64_t C) {
+    const int64_t ncb = cdiv(C, 64 * E);
+    return ncb * B * cdiv(T, 4 * (int64_t)stretch_tokens(B, T, ncb, 4, 64));
+}
+
+hipError_t launch_conv_fwd(const ConvArgs& a) {
+    const int64_t ncb = cdiv(a.C, 64 * E);
+    const int TL = stretch_tokens(a.B, a.T, ncb, 4, 64);
+    const int64_t nst = cdiv(a.T, 4 * (int64_t)TL);
+    const dim3 grid((unsigned)(ncb * nst * a.B));
+    if (a.K == 4)
+        hipLaunchKernelGGL((conv_fwd_kernel<4>), grid, dim3(256), 0, a.stream, a, ncb, nst, TL);
+    else if (a.K == 3)
+        hipLaunchKernelGGL((conv_fwd_kernel<3>), grid, dim3(256), 0, a.stream, a, ncb, nst, TL);
+    else
+        hipLaunchKernelGGL((conv_fwd_kernel<2>), grid, dim3(256), 0, a.stream, a, ncb, nst, TL);
+    return hipGetLastError();
+}
+
+hipError_t launch_conv_step(const ConvArgs& a) {
+    const int64_t ncg = cdiv(a.C, 4);
+    const dim3 grid((unsigned)cdiv(a.B * ncg, 256));
+    if (a.K == 4)
+        hipLaunchKernelGGL((conv_step_kernel<4>), grid, dim3(256), 0, a.stream, a, ncg);
+    else if (a.K == 3)
+        hipLaunchKernelGGL((conv_step_kernel<3>), grid, dim3(256), 0, a.stream, a, ncg);
+    else
+        hipLaunchKernelGGL((conv_step_kernel<2>), grid, dim3(256), 0, a.stream, a, ncg);
+    return hipGetLastError();
+}
+
+hipError_t launch_conv_bwd(const ConvArgs& a) {
+    int64_t ncb, nstretch, nrow;
+    int TL;
+    bwd_shape(a.B, a.T, a.C, ncb, nstretch, nrow, TL);
+    const dim3 grid((unsigned)(ncb * nrow));
+    if (a.K == 4)
+        hipLaunchKernelGGL((conv_bwd_kernel<4>), grid, dim3(256), 0, a.stream, a, ncb, nrow,
+                           nstretch, TL);
+    else if (a.K == 3)
+        hipLaunchKernelGGL((conv_bwd_kernel<3>), grid, dim3(256), 0, a.stream, a, ncb, nrow,
+                           nstretch, TL);
+    else
+        hipLaunchKernelGGL((conv_bwd_kernel<2>), grid, dim3(256), 0, a.stream, a, ncb, nrow,
+                           nstretch, TL);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !a.part) return e;
+    return launch_sum_partials(a.part, nrow, a.C * (a.K + 1), a.dw, a.C * a.K, a.dbias, a.C,
+                               nullptr, a.stream);
+}
+
+}  // namespace gdr
