@@ -181,10 +181,9 @@ struct SsmBwdArgs {
     hipStream_t stream;
 };
 
-// Launch shape of a scan: lanes per channel, channel blocks per group,
+// Launch shape of a scan: channel blocks per group,
 // segments per sequence and their length.
 struct SsmPlan {
-    int lpc;
     int64_t nblk, nseg, L;
 };
 
@@ -235,6 +234,7 @@ hipError_t launch_norm_fwd(const NormArgs& a);
 hipError_t launch_norm_bwd(const NormBwdArgs& a);
 size_t norm_bwd_workspace_bytes(int64_t R, int64_t C);
 int ssm_lanes(int64_t N);
+int64_t ssm_wg_channels(int64_t N);
 SsmPlan ssm_fwd_plan(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N);
 size_t ssm_fwd_workspace_bytes(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N);
 hipError_t launch_ssm_fwd(SsmArgs a, float* ws);

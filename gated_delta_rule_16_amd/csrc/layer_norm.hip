@@ -50,27 +50,32 @@ __device__ __forceinline__ int left(int64_t C, int64_t c) {
     return v < 0 ? 0 : v > E ? E : (int)v;
 }
 
-// x (+ r, rounded to the stored type) of one group of channels; h is stored.
-__device__ __forceinline__ void sum_in(float (&h)[E], const NormArgs& a, int64_t xo, int64_t ro,
-                                       int64_t ho, int valid) {
-    RawRow<E> rx, rr;
-    row_load<E>(rx, a.x, xo, a.in_bf16, valid);
-    if (a.res) row_load<E>(rr, a.res, ro, a.res_bf16, valid);
-    row_unpack<E>(h, rx, a.in_bf16);
-    if (a.res) {
-        float q[E];
-        row_unpack<E>(q, rr, a.res_bf16);
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            h[e] += q[e];
-            if (a.res_bf16) h[e] = bf2f(f2bf(h[e]));
-        }
-        row_store<E>(a.h, ho, a.res_bf16, h, valid);
+// One group of channels of x (and r), and their sum h: rounded to the stored
+// type, stored.  RES: 0 none, 1 bf16, 2 fp32.
+template <bool BF16, int RES, bool RAG> struct SumIn {
+    Row<E, BF16, RAG> x;
+    Row<RES ? E : 1, RES == 1, RES ? RAG : false> r;
+    __device__ __forceinline__ void load(const NormArgs& a, int64_t row, int64_t c, int valid) {
+        x.load(a.x, row * a.xr + c, valid);
+        if constexpr (RES != 0) r.load(a.res, row * a.rr + c, valid);
     }
-}
+    __device__ __forceinline__ void sum(float (&h)[E], const NormArgs& a, int64_t ho, int valid) {
+        x.unpack(h);
+        if constexpr (RES != 0) {
+            float q[E];
+            r.unpack(q);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                h[e] += q[e];
+                if constexpr (RES == 1) h[e] = bf2f(f2bf(h[e]));
+            }
+            row_store<E>(a.h, ho, RES == 1, h, valid);
+        }
+    }
+};
 
 // NV groups of 8 channels per thread; WG: a workgroup per row, else a wave.
-template <int NV, bool WG>
+template <int NV, bool WG, bool BF16, int RES, bool RAG>
 __global__ __launch_bounds__(256) void norm_fwd_kernel(NormArgs a) {
     __shared__ float red[2][4];
     constexpr int NT = WG ? 256 : 64;
@@ -79,10 +84,16 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormArgs a) {
     if (row >= a.R) return;           // a whole wave (WG: never)
     float h[NV][E];
     float s = 0.f;
+    SumIn<BF16, RES, RAG> in[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int64_t c = (int64_t)(k * NT + id) * E;
-        sum_in(h[k], a, row * a.xr + c, row * a.rr + c, row * a.C + c, left(a.C, c));
+        in[k].load(a, row, c, left(a.C, c));
+    }
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int64_t c = (int64_t)(k * NT + id) * E;
+        in[k].sum(h[k], a, row * a.C + c, left(a.C, c));
     }
 #pragma unroll
     for (int k = 0; k < NV; ++k)
@@ -122,40 +133,43 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormArgs a) {
 // Rows too long for registers: the row is read once per reduction.  With a
 // residual the stored sum is what the later walks read (each thread its own
 // channels, so no barrier is needed between its store and its loads).
+template <bool BF16, int RES>
 __global__ __launch_bounds__(256) void norm_fwd_long_kernel(NormArgs a) {
     __shared__ float red[2][4];
     const int64_t row = blockIdx.x;
     const int64_t step = 256 * E;
     float s = 0.f;
     for (int64_t c = (int64_t)threadIdx.x * E; c < a.C; c += step) {
+        SumIn<BF16, RES, true> in;
         float h[E];
-        sum_in(h, a, row * a.xr + c, row * a.rr + c, row * a.C + c, left(a.C, c));
+        in.load(a, row, c, left(a.C, c));
+        in.sum(h, a, row * a.C + c, left(a.C, c));
 #pragma unroll
         for (int e = 0; e < E; ++e) s += h[e];
     }
-    const void* src = a.res ? a.h : a.x;
-    const bool sbf = a.res ? a.res_bf16 : a.in_bf16;
-    const int64_t so = row * (a.res ? a.C : a.xr);
+    const void* src = RES ? a.h : a.x;
+    constexpr bool sbf = RES ? RES == 1 : BF16;
+    const int64_t so = row * (RES ? a.C : a.xr);
     const float inv = 1.f / (float)a.C;
     const float mu = row_total<true>(s, red[0]) * inv;
     s = 0.f;
     for (int64_t c = (int64_t)threadIdx.x * E; c < a.C; c += step) {
-        RawRow<E> r;
+        Row<E, sbf, true> r;
         float h[E];
         const int v = left(a.C, c);
-        row_load<E>(r, src, so + c, sbf, v);
-        row_unpack<E>(h, r, sbf);
+        r.load(src, so + c, v);
+        r.unpack(h);
 #pragma unroll
         for (int e = 0; e < E; ++e)
             if (e < v) s = __builtin_fmaf(h[e] - mu, h[e] - mu, s);
     }
     const float rstd = 1.f / sqrtf(row_total<true>(s, red[1]) * inv + a.eps);
     for (int64_t c = (int64_t)threadIdx.x * E; c < a.C; c += step) {
-        RawRow<E> r;
+        Row<E, sbf, true> r;
         float h[E], w[E], b[E];
         const int v = left(a.C, c);
-        row_load<E>(r, src, so + c, sbf, v);
-        row_unpack<E>(h, r, sbf);
+        r.load(src, so + c, v);
+        r.unpack(h);
         if (a.w) param_load<E>(w, a.w + c, v);
         if (a.b) param_load<E>(b, a.b + c, v);
 #pragma unroll
@@ -172,7 +186,7 @@ __global__ __launch_bounds__(256) void norm_fwd_long_kernel(NormArgs a) {
 // Backward: a persistent grid walks the rows; dw and db stay in registers
 // over all rows of a wave (WG: of the workgroup) and leave as one partial row
 // [2 C] per workgroup.
-template <int NV, bool WG>
+template <int NV, bool WG, bool BF16, bool DY16, bool G16, bool RAG>
 __global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwdArgs a) {
     __shared__ float red[4][4];
     __shared__ float join[WG ? 1 : 3 * 64 * (2 * E + 1)];
@@ -188,19 +202,21 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwdArgs a) {
     const int64_t stride = (int64_t)gridDim.x * (WG ? 1 : 4);
     for (int64_t row = WG ? blockIdx.x : (int64_t)blockIdx.x * 4 + wv; row < a.R; row += stride) {
         float h[NV][E], d[NV][E];
-        RawRow<E> rh[NV], rd[NV], rr[NV];
+        Row<E, BF16, RAG> rh[NV];
+        Row<E, DY16, RAG> rd[NV];
+        Row<E, G16, RAG> rr[NV];
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int64_t c = (int64_t)(k * NT + id) * E;
             const int v = left(a.C, c);
-            row_load<E>(rh[k], a.x, row * a.xr + c, a.in_bf16, v);
-            row_load<E>(rd[k], a.dy, row * a.yr + c, a.dy_bf16, v);
-            if (a.dres) row_load<E>(rr[k], a.dres, row * a.rr + c, a.grad_bf16, v);
+            rh[k].load(a.x, row * a.xr + c, v);
+            rd[k].load(a.dy, row * a.yr + c, v);
+            rr[k].load(a.dres, row * a.rr + c, a.dres ? v : 0);
         }
         float s = 0.f;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            row_unpack<E>(h[k], rh[k], a.in_bf16);
+            rh[k].unpack(h[k]);
 #pragma unroll
             for (int e = 0; e < E; ++e) s += h[k][e];
         }
@@ -212,7 +228,7 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwdArgs a) {
             const int64_t c = (int64_t)(k * NT + id) * E;
             const int v = left(a.C, c);
             float w[E];
-            row_unpack<E>(d[k], rd[k], a.dy_bf16);
+            rd[k].unpack(d[k]);
             if (a.w) param_load<E>(w, a.w + c, v);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
@@ -232,7 +248,7 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwdArgs a) {
             const int v = left(a.C, c);
             float w[E], out[E], q[E];
             if (a.w) param_load<E>(w, a.w + c, v);
-            if (a.dres) row_unpack<E>(q, rr[k], a.grad_bf16);
+            rr[k].unpack(q);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 const float n = h[k][e] * rstd;
@@ -240,9 +256,9 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwdArgs a) {
                 dw[k][e] = __builtin_fmaf(d[k][e], n, dw[k][e]);
                 db[k][e] += d[k][e];
                 out[e] = rstd * (dn - m1 - n * m2);
-                if (a.dres) out[e] += q[e];
+                out[e] += q[e];
             }
-            row_store<E>(a.dx, row * a.C + c, a.grad_bf16, out, v);
+            row_store<E>(a.dx, row * a.C + c, G16, out, v);
         }
     }
     if (!a.part) return;
@@ -281,6 +297,7 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwdArgs a) {
 
 // Rows too long for registers: dx first, a workgroup per row; the column sums
 // by a second kernel that walks the rows with each row's mean and rstd.
+template <bool BF16, bool DY16, bool G16>
 __global__ __launch_bounds__(256) void norm_bwd_long_kernel(NormBwdArgs a, float* stats) {
     __shared__ float red[4][4];
     const int64_t row = blockIdx.x;
@@ -288,10 +305,10 @@ __global__ __launch_bounds__(256) void norm_bwd_long_kernel(NormBwdArgs a, float
     const float inv = 1.f / (float)a.C;
     float s = 0.f;
     for (int64_t c = (int64_t)threadIdx.x * E; c < a.C; c += step) {
-        RawRow<E> r;
+        Row<E, BF16, true> r;
         float h[E];
-        row_load<E>(r, a.x, row * a.xr + c, a.in_bf16, left(a.C, c));
-        row_unpack<E>(h, r, a.in_bf16);
+        r.load(a.x, row * a.xr + c, left(a.C, c));
+        r.unpack(h);
 #pragma unroll
         for (int e = 0; e < E; ++e) s += h[e];
     }
@@ -299,14 +316,15 @@ __global__ __launch_bounds__(256) void norm_bwd_long_kernel(NormBwdArgs a, float
     s = 0.f;
     float s1 = 0.f, s2 = 0.f;
     for (int64_t c = (int64_t)threadIdx.x * E; c < a.C; c += step) {
-        RawRow<E> rh, rd;
+        Row<E, BF16, true> rh;
+        Row<E, DY16, true> rd;
         float h[E], d[E], w[E];
         const int v = left(a.C, c);
-        row_load<E>(rh, a.x, row * a.xr + c, a.in_bf16, v);
-        row_load<E>(rd, a.dy, row * a.yr + c, a.dy_bf16, v);
+        rh.load(a.x, row * a.xr + c, v);
+        rd.load(a.dy, row * a.yr + c, v);
         if (a.w) param_load<E>(w, a.w + c, v);
-        row_unpack<E>(h, rh, a.in_bf16);
-        row_unpack<E>(d, rd, a.dy_bf16);
+        rh.unpack(h);
+        rd.unpack(d);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             const float x = e < v ? h[e] - mu : 0.f;
@@ -324,28 +342,31 @@ __global__ __launch_bounds__(256) void norm_bwd_long_kernel(NormBwdArgs a, float
         stats[2 * row + 1] = rstd;
     }
     for (int64_t c = (int64_t)threadIdx.x * E; c < a.C; c += step) {
-        RawRow<E> rh, rd, rr;
+        Row<E, BF16, true> rh;
+        Row<E, DY16, true> rd;
+        Row<E, G16, true> rr;
         float h[E], d[E], w[E], q[E];
         const int v = left(a.C, c);
-        row_load<E>(rh, a.x, row * a.xr + c, a.in_bf16, v);
-        row_load<E>(rd, a.dy, row * a.yr + c, a.dy_bf16, v);
-        if (a.dres) row_load<E>(rr, a.dres, row * a.rr + c, a.grad_bf16, v);
+        rh.load(a.x, row * a.xr + c, v);
+        rd.load(a.dy, row * a.yr + c, v);
+        rr.load(a.dres, row * a.rr + c, a.dres ? v : 0);
         if (a.w) param_load<E>(w, a.w + c, v);
-        row_unpack<E>(h, rh, a.in_bf16);
-        row_unpack<E>(d, rd, a.dy_bf16);
-        if (a.dres) row_unpack<E>(q, rr, a.grad_bf16);
+        rh.unpack(h);
+        rd.unpack(d);
+        rr.unpack(q);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             const float dn = a.w ? d[e] * w[e] : d[e];
             h[e] = rstd * (dn - m1 - (h[e] - mu) * rstd * m2);
-            if (a.dres) h[e] += q[e];
+            h[e] += q[e];
         }
-        row_store<E>(a.dx, row * a.C + c, a.grad_bf16, h, v);
+        row_store<E>(a.dx, row * a.C + c, G16, h, v);
     }
 }
 
 // Column sums of the long rows: a wave owns 64 groups of 8 channels, a
 // workgroup's four waves take every fourth of its rows.
+template <bool BF16, bool DY16>
 __global__ __launch_bounds__(256) void norm_dw_long_kernel(NormBwdArgs a, const float* stats,
                                                            int64_t ncb, int64_t nrow) {
     __shared__ float join[3 * 64 * (2 * E + 1)];
@@ -358,12 +379,13 @@ __global__ __launch_bounds__(256) void norm_dw_long_kernel(NormBwdArgs a, const 
     for (int e = 0; e < E; ++e) dw[e] = db[e] = 0.f;
     if (v > 0)
         for (int64_t row = slot * 4 + wv; row < a.R; row += nrow * 4) {
-            RawRow<E> rh, rd;
+            Row<E, BF16, true> rh;
+        Row<E, DY16, true> rd;
             float h[E], d[E];
-            row_load<E>(rh, a.x, row * a.xr + c, a.in_bf16, v);
-            row_load<E>(rd, a.dy, row * a.yr + c, a.dy_bf16, v);
-            row_unpack<E>(h, rh, a.in_bf16);
-            row_unpack<E>(d, rd, a.dy_bf16);
+            rh.load(a.x, row * a.xr + c, v);
+            rd.load(a.dy, row * a.yr + c, v);
+            rh.unpack(h);
+            rd.unpack(d);
             const float mu = stats[2 * row], rstd = stats[2 * row + 1];
 #pragma unroll
             for (int e = 0; e < E; ++e) {
@@ -412,6 +434,78 @@ int64_t bwd_rows(int64_t R, int64_t C) {
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+template <int NV, bool WG, bool BF16, int RES>
+void fwd_r(const NormArgs& a, dim3 grid) {
+    if (a.C % E)
+        hipLaunchKernelGGL((norm_fwd_kernel<NV, WG, BF16, RES, true>), grid, dim3(256), 0, a.stream,
+                           a);
+    else
+        hipLaunchKernelGGL((norm_fwd_kernel<NV, WG, BF16, RES, false>), grid, dim3(256), 0,
+                           a.stream, a);
+}
+
+template <bool BF16, int RES>
+void fwd_t(const NormArgs& a) {
+    const int64_t C = a.C;
+    const dim3 wave((unsigned)cdiv(a.R, 4)), wg((unsigned)a.R);
+    if (C <= 512) fwd_r<1, false, BF16, RES>(a, wave);
+    else if (C <= 1024) fwd_r<2, false, BF16, RES>(a, wave);
+    else if (C <= WAVE_MAX) fwd_r<4, false, BF16, RES>(a, wave);
+    else if (C <= 4096) fwd_r<2, true, BF16, RES>(a, wg);
+    else if (C <= WG_MAX) fwd_r<4, true, BF16, RES>(a, wg);
+    else
+        hipLaunchKernelGGL((norm_fwd_long_kernel<BF16, RES>), wg, dim3(256), 0, a.stream, a);
+}
+
+template <bool BF16>
+void fwd_b(const NormArgs& a) {
+    if (!a.res) fwd_t<BF16, 0>(a);
+    else if (a.res_bf16) fwd_t<BF16, 1>(a);
+    else fwd_t<BF16, 2>(a);
+}
+
+template <int NV, bool WG, bool BF16, bool DY16, bool G16>
+void bwd_r(const NormBwdArgs& a, dim3 grid) {
+    if (a.C % E)
+        hipLaunchKernelGGL((norm_bwd_kernel<NV, WG, BF16, DY16, G16, true>), grid, dim3(256), 0,
+                           a.stream, a);
+    else
+        hipLaunchKernelGGL((norm_bwd_kernel<NV, WG, BF16, DY16, G16, false>), grid, dim3(256), 0,
+                           a.stream, a);
+}
+
+template <bool BF16, bool DY16, bool G16>
+void bwd_t(const NormBwdArgs& a) {
+    const int64_t C = a.C, nrow = bwd_rows(a.R, C);
+    const dim3 grid((unsigned)nrow);
+    if (C <= 512) bwd_r<1, false, BF16, DY16, G16>(a, grid);
+    else if (C <= 1024) bwd_r<2, false, BF16, DY16, G16>(a, grid);
+    else if (C <= WAVE_MAX) bwd_r<4, false, BF16, DY16, G16>(a, grid);
+    else if (C <= 4096) bwd_r<2, true, BF16, DY16, G16>(a, grid);
+    else if (C <= WG_MAX) bwd_r<4, true, BF16, DY16, G16>(a, grid);
+    else {
+        const int64_t ncb = cdiv(C, 64 * E);
+        float* stats = a.part ? reinterpret_cast<float*>(reinterpret_cast<char*>(a.part) +
+                                up256(sizeof(float) * (size_t)(nrow * 2 * C))) : nullptr;
+        hipLaunchKernelGGL((norm_bwd_long_kernel<BF16, DY16, G16>), dim3((unsigned)a.R), dim3(256),
+                           0, a.stream, a, stats);
+        if (a.part)
+            hipLaunchKernelGGL((norm_dw_long_kernel<BF16, DY16>), dim3((unsigned)(ncb * nrow)),
+                               dim3(256), 0, a.stream, a, stats, ncb, nrow);
+    }
+}
+
+template <bool BF16>
+void bwd_b(const NormBwdArgs& a) {
+    if (a.dy_bf16) {
+        if (a.grad_bf16) bwd_t<BF16, true, true>(a);
+        else bwd_t<BF16, true, false>(a);
+    } else {
+        if (a.grad_bf16) bwd_t<BF16, false, true>(a);
+        else bwd_t<BF16, false, false>(a);
+    }
+}
+
 }  // namespace
 
 // Workspace: the partials of dw and db [bwd_rows][2 C]; beyond WG_MAX also
@@ -423,43 +517,18 @@ size_t norm_bwd_workspace_bytes(int64_t R, int64_t C) {
 }
 
 hipError_t launch_norm_fwd(const NormArgs& a) {
-    const int64_t C = a.C;
-    const dim3 wave((unsigned)cdiv(a.R, 4)), wg((unsigned)a.R);
-#define FWD(NV, WG, GRID) \
-    hipLaunchKernelGGL((norm_fwd_kernel<NV, WG>), GRID, dim3(256), 0, a.stream, a)
-    if (C <= 512) FWD(1, false, wave);
-    else if (C <= 1024) FWD(2, false, wave);
-    else if (C <= WAVE_MAX) FWD(4, false, wave);
-    else if (C <= 4096) FWD(2, true, wg);
-    else if (C <= WG_MAX) FWD(4, true, wg);
-    else hipLaunchKernelGGL(norm_fwd_long_kernel, wg, dim3(256), 0, a.stream, a);
-#undef FWD
+    if (a.in_bf16) fwd_b<true>(a);
+    else fwd_b<false>(a);
     return hipGetLastError();
 }
 
 hipError_t launch_norm_bwd(const NormBwdArgs& a) {
-    const int64_t C = a.C, nrow = bwd_rows(a.R, C);
-    const dim3 grid((unsigned)nrow);
-#define BWD(NV, WG) hipLaunchKernelGGL((norm_bwd_kernel<NV, WG>), grid, dim3(256), 0, a.stream, a)
-    if (C <= 512) BWD(1, false);
-    else if (C <= 1024) BWD(2, false);
-    else if (C <= WAVE_MAX) BWD(4, false);
-    else if (C <= 4096) BWD(2, true);
-    else if (C <= WG_MAX) BWD(4, true);
-    else {
-        const int64_t ncb = cdiv(C, 64 * E);
-        float* stats = a.part ? reinterpret_cast<float*>(reinterpret_cast<char*>(a.part) +
-                                up256(sizeof(float) * (size_t)(nrow * 2 * C))) : nullptr;
-        hipLaunchKernelGGL(norm_bwd_long_kernel, dim3((unsigned)a.R), dim3(256), 0, a.stream, a,
-                           stats);
-        if (a.part)
-            hipLaunchKernelGGL(norm_dw_long_kernel, dim3((unsigned)(ncb * nrow)), dim3(256), 0,
-                               a.stream, a, stats, ncb, nrow);
-    }
-#undef BWD
-    hipError_t e = hipGetLastError();
+    if (a.in_bf16) bwd_b<true>(a);
+    else bwd_b<false>(a);
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.part) return e;
-    return launch_sum_partials(a.part, nrow, 2 * C, a.dw, C, a.db, C, nullptr, a.stream);
+    return launch_sum_partials(a.part, bwd_rows(a.R, a.C), 2 * a.C, a.dw, a.C, a.db, a.C, nullptr,
+                               a.stream);
 }
 
 }  // namespace gdr

@@ -28,18 +28,16 @@ __device__ __forceinline__ int clampi(int64_t v, int hi) {
 
 // Row t of [state; x] for one lane's channels: t >= 0 from x, else the state
 // (or zeros without one).
-template <int EE>
-__device__ __forceinline__ void load_in(RawRow<EE>& r, const ConvArgs& a, int64_t b, int64_t t,
-                                        int64_t c, int valid) {
-    if (t >= 0)
-        row_load<EE>(r, a.x, b * a.xb + t * a.xt + c, a.in_bf16, valid);
-    else if (a.s0)
-        row_load<EE>(r, a.s0, (b * (a.K - 1) + t + a.K - 1) * a.C + c, a.in_bf16, valid);
-    else
-        row_load<EE>(r, a.x, 0, a.in_bf16, 0);
+template <int EE, bool BF16, bool RAG>
+__device__ __forceinline__ void load_in(Row<EE, BF16, RAG>& r, const ConvArgs& a, int64_t b,
+                                        int64_t t, int64_t c, int valid) {
+    const bool past = t < 0;
+    r.load(past ? a.s0 : a.x,
+           past ? (b * (a.K - 1) + t + a.K - 1) * a.C + c : b * a.xb + t * a.xt + c,
+           past && !a.s0 ? 0 : valid);
 }
 
-template <int K>
+template <int K, bool BF16, bool RAG>
 __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int64_t ncb, int64_t nstretch,
                                                        int TL) {
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
@@ -57,36 +55,35 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int64_t ncb, 
     param_load<E>(bias, a.bias + c, a.bias ? valid : 0);
     float win[K - 1][E];
     {
-        RawRow<E> r[K - 1];
+        Row<E, BF16, RAG> r[K - 1];
 #pragma unroll
-        for (int j = 0; j < K - 1; ++j) load_in<E>(r[j], a, b, t0 - (K - 1) + j, c, valid);
+        for (int j = 0; j < K - 1; ++j) load_in(r[j], a, b, t0 - (K - 1) + j, c, valid);
 #pragma unroll
-        for (int j = 0; j < K - 1; ++j) row_unpack<E>(win[j], r[j], a.in_bf16);
+        for (int j = 0; j < K - 1; ++j) r[j].unpack(win[j]);
         if (t0 == 0 && a.s_final) {
             // the lane that reads the state also writes the next one, so the
             // two may be the same buffer: all K - 1 rows are read (the state
             // rows above, or x) before the first is written
-            RawRow<E> f[K - 1];
+            Row<E, BF16, RAG> f[K - 1];
 #pragma unroll
-            for (int m = 0; m < K - 1; ++m) load_in<E>(f[m], a, b, a.T - (K - 1) + m, c, valid);
+            for (int m = 0; m < K - 1; ++m) load_in(f[m], a, b, a.T - (K - 1) + m, c, valid);
 #pragma unroll
             for (int m = 0; m < K - 1; ++m) {
                 float v[E];
-                row_unpack<E>(v, f[m], a.in_bf16);
-                row_store<E>(a.s_final, (b * (K - 1) + m) * a.C + c, a.in_bf16, v, valid);
+                f[m].unpack(v);
+                row_store<E>(a.s_final, (b * (K - 1) + m) * a.C + c, BF16, v, valid);
             }
         }
     }
     for (int64_t t = t0; t < t1; t += FWD_TOKENS) {
-        RawRow<E> r[FWD_TOKENS];
+        Row<E, BF16, RAG> r[FWD_TOKENS];
 #pragma unroll
         for (int u = 0; u < FWD_TOKENS; ++u)
-            row_load<E>(r[u], a.x, b * a.xb + (t + u < t1 ? t + u : t1 - 1) * a.xt + c, a.in_bf16,
-                        valid);
+            r[u].load(a.x, b * a.xb + (t + u < t1 ? t + u : t1 - 1) * a.xt + c, valid);
 #pragma unroll
         for (int u = 0; u < FWD_TOKENS; ++u) {
             float x[E], y[E];
-            row_unpack<E>(x, r[u], a.in_bf16);
+            r[u].unpack(x);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 float s = bias[e];
@@ -104,24 +101,23 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int64_t ncb, 
 }
 
 // One decode token: the lane shifts its own channels' state.
-template <int K>
+template <int K, bool BF16>
 __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a, int64_t ncg) {
     constexpr int SE = 4;
     const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int64_t b = id / ncg, c = (id % ncg) * SE;
     if (b >= a.B) return;
     const int valid = clampi(a.C - c, SE);
-    RawRow<SE> r[K];
+    Row<SE, BF16, true> r[K];
 #pragma unroll
-    for (int j = 0; j < K - 1; ++j)
-        row_load<SE>(r[j], a.s0, (b * (K - 1) + j) * a.C + c, a.in_bf16, valid);
-    row_load<SE>(r[K - 1], a.x, b * a.xb + c, a.in_bf16, valid);
+    for (int j = 0; j < K - 1; ++j) r[j].load(a.s0, (b * (K - 1) + j) * a.C + c, valid);
+    r[K - 1].load(a.x, b * a.xb + c, valid);
     float y[SE], x[K][SE], w[SE * K];
     param_load<SE * K>(w, a.w + c * K, valid * K);
     param_load<SE>(y, a.bias + c, a.bias ? valid : 0);
 #pragma unroll
     for (int j = 0; j < K; ++j) {
-        row_unpack<SE>(x[j], r[j], a.in_bf16);
+        r[j].unpack(x[j]);
 #pragma unroll
         for (int e = 0; e < SE; ++e)
             y[e] = __builtin_fmaf(w[e * K + j], x[j][e], y[e]);
@@ -131,7 +127,7 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a, int64_t ncg)
     row_store<SE>(a.y, b * a.C + c, a.out_bf16, y, valid);
 #pragma unroll
     for (int j = 0; j < K - 1; ++j)
-        row_store<SE>(a.s_final, (b * (K - 1) + j) * a.C + c, a.in_bf16, x[j + 1], valid);
+        row_store<SE>(a.s_final, (b * (K - 1) + j) * a.C + c, BF16, x[j + 1], valid);
 }
 
 constexpr int BE = 4;             // backward: channels per lane
@@ -142,7 +138,7 @@ constexpr int BE = 4;             // backward: channels per lane
 // The walk runs K - 1 tokens past the stretch to complete its last dx, and a
 // stretch leaves the dx of the K - 1 rows before it to its neighbour -- but
 // the first, whose earlier rows are the state's gradient.
-template <int K>
+template <int K, bool BF16, bool DY16, bool RAG>
 __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int64_t ncb, int64_t nrow,
                                                        int64_t nstretch, int TL) {
     __shared__ float red[3][64][BE * (K + 1) + 1];
@@ -169,9 +165,9 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int64_t ncb, 
             float win[K][BE], du[K][BE];
 #pragma unroll
             for (int j = 0; j < K - 1; ++j) {
-                RawRow<BE> r;
-                load_in<BE>(r, a, b, t0 - (K - 1) + j, c, valid);
-                row_unpack<BE>(win[j + 1], r, a.in_bf16);
+                Row<BE, BF16, RAG> r;
+                load_in(r, a, b, t0 - (K - 1) + j, c, valid);
+                r.unpack(win[j + 1]);
             }
 #pragma unroll
             for (int j = 0; j < K; ++j)
@@ -180,20 +176,21 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int64_t ncb, 
             const int64_t tend = t1 + K - 1;
             constexpr int U = 4;
             for (int64_t tb = t0; tb < tend; tb += U) {
-                RawRow<BE> rx[U], rd[U];
+                Row<BE, BF16, RAG> rx[U];
+                Row<BE, DY16, RAG> rd[U];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const int64_t t = tb + u;
                     const int v = t < a.T && t < tend ? valid : 0;
-                    row_load<BE>(rx[u], a.x, v ? b * a.xb + t * a.xt + c : 0, a.in_bf16, v);
-                    row_load<BE>(rd[u], a.dy, v ? b * a.yb + t * a.yt + c : 0, a.dy_bf16, v);
+                    rx[u].load(a.x, b * a.xb + t * a.xt + c, v);
+                    rd[u].load(a.dy, b * a.yb + t * a.yt + c, v);
                 }
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const int64_t t = tb + u;
                     float x[BE], d[BE];
-                    row_unpack<BE>(x, rx[u], a.in_bf16);
-                    row_unpack<BE>(d, rd[u], a.dy_bf16);
+                    rx[u].unpack(x);
+                    rd[u].unpack(d);
                     const bool mine = t < t1;     // du_t counts for dw here
                     float out[BE];
 #pragma unroll
@@ -292,6 +289,51 @@ void bwd_shape(int64_t B, int64_t T, int64_t C, int64_t& ncb, int64_t& nstretch,
     nrow = units < cap ? units : cap;
 }
 
+template <int K>
+void fwd_t(const ConvArgs& a, dim3 grid, int64_t ncb, int64_t nst, int TL) {
+    const bool rag = a.C % E != 0;
+#define FWD(BF16, RAG)                                                                           \
+    hipLaunchKernelGGL((conv_fwd_kernel<K, BF16, RAG>), grid, dim3(256), 0, a.stream, a, ncb, nst, \
+                       TL)
+    if (a.in_bf16) {
+        if (rag) FWD(true, true);
+        else FWD(true, false);
+    } else {
+        if (rag) FWD(false, true);
+        else FWD(false, false);
+    }
+#undef FWD
+}
+
+template <int K>
+void step_t(const ConvArgs& a, dim3 grid, int64_t ncg) {
+    if (a.in_bf16)
+        hipLaunchKernelGGL((conv_step_kernel<K, true>), grid, dim3(256), 0, a.stream, a, ncg);
+    else
+        hipLaunchKernelGGL((conv_step_kernel<K, false>), grid, dim3(256), 0, a.stream, a, ncg);
+}
+
+template <int K, bool BF16, bool DY16>
+void bwd_t(const ConvArgs& a, dim3 grid, int64_t ncb, int64_t nrow, int64_t nstretch, int TL) {
+    if (a.C % BE != 0)
+        hipLaunchKernelGGL((conv_bwd_kernel<K, BF16, DY16, true>), grid, dim3(256), 0, a.stream, a,
+                           ncb, nrow, nstretch, TL);
+    else
+        hipLaunchKernelGGL((conv_bwd_kernel<K, BF16, DY16, false>), grid, dim3(256), 0, a.stream, a,
+                           ncb, nrow, nstretch, TL);
+}
+
+template <int K>
+void bwd_k(const ConvArgs& a, dim3 grid, int64_t ncb, int64_t nrow, int64_t nstretch, int TL) {
+    if (a.in_bf16) {
+        if (a.dy_bf16) bwd_t<K, true, true>(a, grid, ncb, nrow, nstretch, TL);
+        else bwd_t<K, true, false>(a, grid, ncb, nrow, nstretch, TL);
+    } else {
+        if (a.dy_bf16) bwd_t<K, false, true>(a, grid, ncb, nrow, nstretch, TL);
+        else bwd_t<K, false, false>(a, grid, ncb, nrow, nstretch, TL);
+    }
+}
+
 }  // namespace
 
 size_t conv_bwd_workspace_bytes(int64_t B, int64_t T, int64_t C, int64_t K) {
@@ -311,24 +353,18 @@ hipError_t launch_conv_fwd(const ConvArgs& a) {
     const int TL = stretch_tokens(a.B, a.T, ncb, 4, 64);
     const int64_t nst = cdiv(a.T, 4 * (int64_t)TL);
     const dim3 grid((unsigned)(ncb * nst * a.B));
-    if (a.K == 4)
-        hipLaunchKernelGGL((conv_fwd_kernel<4>), grid, dim3(256), 0, a.stream, a, ncb, nst, TL);
-    else if (a.K == 3)
-        hipLaunchKernelGGL((conv_fwd_kernel<3>), grid, dim3(256), 0, a.stream, a, ncb, nst, TL);
-    else
-        hipLaunchKernelGGL((conv_fwd_kernel<2>), grid, dim3(256), 0, a.stream, a, ncb, nst, TL);
+    if (a.K == 4) fwd_t<4>(a, grid, ncb, nst, TL);
+    else if (a.K == 3) fwd_t<3>(a, grid, ncb, nst, TL);
+    else fwd_t<2>(a, grid, ncb, nst, TL);
     return hipGetLastError();
 }
 
 hipError_t launch_conv_step(const ConvArgs& a) {
     const int64_t ncg = cdiv(a.C, 4);
     const dim3 grid((unsigned)cdiv(a.B * ncg, 256));
-    if (a.K == 4)
-        hipLaunchKernelGGL((conv_step_kernel<4>), grid, dim3(256), 0, a.stream, a, ncg);
-    else if (a.K == 3)
-        hipLaunchKernelGGL((conv_step_kernel<3>), grid, dim3(256), 0, a.stream, a, ncg);
-    else
-        hipLaunchKernelGGL((conv_step_kernel<2>), grid, dim3(256), 0, a.stream, a, ncg);
+    if (a.K == 4) step_t<4>(a, grid, ncg);
+    else if (a.K == 3) step_t<3>(a, grid, ncg);
+    else step_t<2>(a, grid, ncg);
     return hipGetLastError();
 }
 
@@ -337,15 +373,9 @@ hipError_t launch_conv_bwd(const ConvArgs& a) {
     int TL;
     bwd_shape(a.B, a.T, a.C, ncb, nstretch, nrow, TL);
     const dim3 grid((unsigned)(ncb * nrow));
-    if (a.K == 4)
-        hipLaunchKernelGGL((conv_bwd_kernel<4>), grid, dim3(256), 0, a.stream, a, ncb, nrow,
-                           nstretch, TL);
-    else if (a.K == 3)
-        hipLaunchKernelGGL((conv_bwd_kernel<3>), grid, dim3(256), 0, a.stream, a, ncb, nrow,
-                           nstretch, TL);
-    else
-        hipLaunchKernelGGL((conv_bwd_kernel<2>), grid, dim3(256), 0, a.stream, a, ncb, nrow,
-                           nstretch, TL);
+    if (a.K == 4) bwd_k<4>(a, grid, ncb, nrow, nstretch, TL);
+    else if (a.K == 3) bwd_k<3>(a, grid, ncb, nrow, nstretch, TL);
+    else bwd_k<2>(a, grid, ncb, nrow, nstretch, TL);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.part) return e;
     return launch_sum_partials(a.part, nrow, a.C * (a.K + 1), a.dw, a.C * a.K, a.dbias, a.C,

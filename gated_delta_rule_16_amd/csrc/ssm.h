@@ -1,10 +1,15 @@
 // Pieces shared by the selective scan's kernels (forward, backward, token).
 //
-// Lane layout of every scan kernel: a lane holds 4 neighbouring states of one
-// channel; LPC = 1, 2, 4, 8 or 16 neighbouring lanes share the channel (N up
-// to 4 LPC states), so a wave runs 64 / LPC channels and a workgroup of four
-// waves WC = 256 / LPC.  States n >= N of the last lane have A = B = C = 0 and
-// stay 0.
+// Lane layout of the sequence kernels.  A wave is four rows of 16 lanes.  The
+// 16 lanes of a row are 16 channels; a lane holds NS neighbouring states of
+// its channel, and NG = 1, 2 or 4 rows share a channel (NS NG >= N), so a wave
+// runs CW = 64 / NG channels and a workgroup of four waves WC = 4 CW.
+// B_t[n] is then the same for all lanes of a row: one register holds it for
+// 16 / NS tokens (lane k NS + j of row r: token k, state NS (r % NG) + j), and
+// every product takes its factor by a DPP row broadcast, as part of the
+// instruction, with no read of LDS.  The sum over a channel's states crosses
+// rows: permlane swaps, 6 instructions for 4 tokens at NG = 4.
+// States n >= N have A = B = C = 0 and stay 0.
 #pragma once
 
 #include "launch.h"
@@ -25,11 +30,19 @@ __device__ __forceinline__ float xor_lane(float x) {
     return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(up, i, 0x114, 0xF, 0xA, false));
 }
 
-// One step of a halving reduction: lanes with bit M clear keep a's sum of the
-// pair (l, l ^ M), lanes with it set b's.
-template <int M>
+// One step of a halving reduction over a row of 16 lanes: lanes with bit BIT
+// clear keep a's sum over the pair of lanes, lanes with it set b's.  The pair
+// is l and l ^ 8, l ^ 7, l ^ 2, l ^ 1 for bits 3, 2, 1, 0: each of them one DPP
+// operand, and together they reach all 16 lanes.
+template <int BIT>
+__device__ __forceinline__ float pair_lane(float x) {
+    constexpr int ctrl = BIT == 3 ? 0x128 : BIT == 2 ? 0x141 : BIT == 1 ? 0x4E : 0xB1;
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
+                                         0, __builtin_bit_cast(int, x), ctrl, 0xF, 0xF, false));
+}
+template <int BIT>
 __device__ __forceinline__ float fold(float a, float b, bool bit) {
-    return (bit ? b : a) + xor_lane<M>(bit ? a : b);
+    return (bit ? b : a) + pair_lane<BIT>(bit ? a : b);
 }
 
 // The same across 16 or 32 lanes, one swap and one add.
@@ -44,44 +57,67 @@ __device__ __forceinline__ float fold32(float a, float b) {
     return __builtin_bit_cast(float, (unsigned)r[0]) + __builtin_bit_cast(float, (unsigned)r[1]);
 }
 
-// Sums s[k] (token k of 4) over the LPC lanes of each channel and stores them
-// at dst[k * pitch]; each lane stores what the halving left it, so a group of
-// 4 tokens costs few stores.  li = lane % LPC.
-template <int LPC>
-__device__ __forceinline__ void channel_sums(const float (&s)[4], int li, float* dst, int pitch) {
-    if constexpr (LPC == 1) {
+// Lane I of the lane's row of 16, in every lane (a DPP operand of the
+// instruction that uses it).
+template <int I>
+__device__ __forceinline__ float row_bcast(float x) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
+                                         0, __builtin_bit_cast(int, x), 0x150 + I, 0xF, 0xF, true));
+}
+
+// Sums s[k] (token k of 4) over the rows of each channel and stores them at
+// dst[k * pitch].  row = lane / 16.
+template <int NG>
+__device__ __forceinline__ void state_sums(const float (&s)[4], int row, float* dst, int pitch) {
+    if constexpr (NG == 1) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) dst[k * pitch] = s[k];
     } else {
-        const bool b0 = li & 1;
-        const float p0 = fold<1>(s[0], s[1], b0), p1 = fold<1>(s[2], s[3], b0);
-        if constexpr (LPC == 2) {
-            dst[(li & 1) * pitch] = p0;
-            dst[(2 + (li & 1)) * pitch] = p1;
+        const float p0 = fold16(s[0], s[1]), p1 = fold16(s[2], s[3]);
+        if constexpr (NG == 2) {
+            dst[(row & 1) * pitch] = p0;
+            dst[(2 + (row & 1)) * pitch] = p1;
         } else {
-            float r = fold<2>(p0, p1, li & 2);
-            if constexpr (LPC >= 8) r += xor_lane<4>(r);
-            if constexpr (LPC >= 16) r += xor_lane<8>(r);
-            if (LPC == 4 || li < 4) dst[(li & 3) * pitch] = r;
+            dst[row * pitch] = fold32(p0, p1);
         }
     }
 }
 
-// Four states of one lane in memory ([.., N] floats, element-aligned).
-__device__ __forceinline__ void state_load(float (&h)[4], const float* p, int valid) {
-    param_load<4>(h, p, valid);
+// Register of B or C for tokens tt .. tt + 16 / NS - 1 of a tile in LDS
+// ([token][NP] floats): this lane's element.
+template <int NS, int NG>
+__device__ __forceinline__ float row_coef(const float* tile, int tt, int lane) {
+    constexpr int NP = NS * NG;
+    const int i = lane & 15;
+    return tile[(tt + i / NS) * NP + NS * ((lane >> 4) % NG) + i % NS];
 }
-__device__ __forceinline__ void state_store(float* p, const float (&h)[4], int valid) {
-    row_store<4>(p, 0, false, h, valid);
+
+// NS states of one lane in memory ([.., N] floats, element-aligned).
+template <int NS>
+__device__ __forceinline__ void states_load(float (&h)[NS], const float* p, int valid) {
+    param_load<NS>(h, p, valid);
+}
+template <int NS>
+__device__ __forceinline__ void states_store(float* p, const float (&h)[NS], int valid) {
+    if (valid >= NS) {
+#pragma unroll
+        for (int i = 0; i < NS; i += 4)
+            *reinterpret_cast<f32x4_e4*>(p + i) = f32x4_e4{h[i], h[i + 1], h[i + 2], h[i + 3]};
+    } else {
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+            if (i < valid) p[i] = h[i];
+    }
 }
 
 // The step Delta of a token and channel.
 __device__ __forceinline__ float ssm_delta(float raw, bool sp) { return sp ? softplus(raw) : raw; }
 
-// Valid states of a lane.
-__device__ __forceinline__ int ssm_states(int64_t N, int ng) {
-    const int64_t v = N - 4 * ng;
-    return v < 0 ? 0 : v > 4 ? 4 : (int)v;
+// Valid states of a lane that starts at state n0.
+template <int NS>
+__device__ __forceinline__ int states_valid(int64_t N, int n0) {
+    const int64_t v = N - n0;
+    return v < 0 ? 0 : v > NS ? NS : (int)v;
 }
 
 __device__ __forceinline__ int ssm_left(int64_t lim, int64_t c, int e) {

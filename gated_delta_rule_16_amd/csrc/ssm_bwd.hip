@@ -7,43 +7,61 @@
 //   dx_t = Delta_t sum_n g_t B_t + D dy_t,       dA = sum_t p_t Delta_t,
 //   dDelta_t = x_t sum_n g_t B_t + sum_n p_t A,  dz_t = dout_t y_t (z sigmoid(z))',
 //
-// Two passes.  The first runs the state forward and keeps it every S = 16
-// tokens (8 bytes per state and 16 tokens of traffic instead of a state per
-// token).  The second goes backwards over blocks of S tokens: it runs a
-// block's states again from the kept one, leaving h_t and a_t of all S tokens
-// in registers (128 of them), then walks the block backwards.  Sums over the
-// states are halving reductions over a channel's lanes, 4 tokens together;
-// sums over channels (dB, dC) are halving reductions over the wave (8 values,
-// 16 lane operations at N = 16), then over the workgroup's waves in LDS, and
-// leave as one partial per workgroup, added by ssm_bc_reduce in a fixed order.
+// Two passes.  The first runs the state forward and keeps it every S = 64 / NS
+// tokens (16 at N <= 16: 8 bytes of traffic per state and 16 tokens).  The
+// second goes backwards over blocks of S tokens: it runs a block's states
+// again from the kept one, leaving h_t and a_t of all S tokens in registers
+// (128 of them), then walks the block backwards.  Lanes are laid out as in
+// the forward (ssm.h).  Sums over the states cross rows with permlane swaps;
+// sums over channels (dB, dC) are halving reductions over a row's 16 lanes
+// (22 operations a token for the 8 values of a lane at NS = 4), then over the
+// workgroup's waves in LDS, and leave as one partial per workgroup, added by
+// ssm_bc_reduce in a fixed order.
 //
 // Segments: both passes run all segments of a sequence side by side.  The
 // first starts every segment from zero and also forms the gradient that the
 // segment alone sends to its start, sum_t (prod a) C_t dy_t, from running
 // products; the second composes a segment's true start state and end
 // gradient from those and adds exp(A sum Delta) h_in to each kept state.
+#include <utility>
+
 #include "ssm.h"
 
 namespace gdr {
 
 namespace {
 
-// Tokens per block of the second pass.
-template <int LPC> constexpr int block_tokens() { return LPC == 1 ? 8 : 16; }
+// Tokens per block of the second pass: 64 / NS, and at most 8 elements to
+// stage per thread.
+template <int NS, int NG> constexpr int block_tokens() { return NG == 1 ? 8 : 64 / NS; }
+
+// One token forwards: h and, for the segment's own gradient, P and gam.
+template <int NS, int K, bool GAM, size_t... J>
+__device__ __forceinline__ void states_token(float (&h)[NS], float (&P)[NS], float (&gam)[NS],
+                                             const float (&A2)[NS], float d, float dx, float dy,
+                                             float Bq, float Cq, std::index_sequence<J...>) {
+    float aa[NS];
+    ((aa[J] = __builtin_amdgcn_exp2f(d * A2[J])), ...);
+    ((h[J] = __builtin_fmaf(aa[J], h[J], row_bcast<K * NS + J>(Bq) * dx)), ...);
+    if constexpr (GAM)
+        ((P[J] *= aa[J],
+          gam[J] = __builtin_fmaf(P[J], row_bcast<K * NS + J>(Cq) * dy, gam[J])), ...);
+}
 
 // First pass.  GAM: more than one segment.
-template <int LPC, bool GAM>
+template <int NS, int NG, bool GAM, bool BF16, bool RAG>
 __global__ __launch_bounds__(256) void ssm_bwd_states_kernel(SsmBwdArgs a, int64_t nblk,
                                                              int64_t nseg, int64_t L) {
-    constexpr int WC = 256 / LPC;
-    constexpr int TT = 8 * LPC < 32 ? 8 * LPC : 32;
-    constexpr int EPT = TT * WC / 256;
+    constexpr int NP = NS * NG, CW = 64 / NG, WC = 4 * CW;
+    constexpr int EPT = 8;
+    constexpr int TT = 256 * EPT / WC;
     constexpr int TPR = WC / EPT;
-    constexpr int NQ = TT * LPC;
+    constexpr int NQ = TT * NP / 4;
     constexpr int QPT = (2 * NQ + 255) / 256;
-    constexpr int S = block_tokens<LPC>();
+    constexpr int KT = 16 / NS;
+    constexpr int S = block_tokens<NS, NG>();
     __shared__ float2 dd[TT][WC];
-    __shared__ float4 bc[TT][2][LPC];
+    __shared__ __align__(16) float bc[2][TT * NP];
     __shared__ float ds[GAM ? TT : 1][WC];
 
     const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
@@ -57,79 +75,86 @@ __global__ __launch_bounds__(256) void ssm_bwd_states_kernel(SsmBwdArgs a, int64
     const int64_t t0 = seg * L, t1 = t0 + L < a.T ? t0 + L : a.T;
     const int64_t nsub = (a.T + S - 1) / S;
 
-    const int ng = lane % LPC, chl = wv * (64 / LPC) + lane / LPC;
+    const int row = lane >> 4, n0 = NS * (row % NG);
+    const int chl = wv * CW + (lane & 15) + 16 * (row / NG);
     const bool live = c0 + chl < Dg;
     const int64_t ch = cg + (live ? c0 + chl : 0);
-    const int nv = live ? ssm_states(a.N, ng) : 0;
-    float A2[4], h[4] = {0.f, 0.f, 0.f, 0.f}, P[4] = {1.f, 1.f, 1.f, 1.f};
-    float gam[4] = {0.f, 0.f, 0.f, 0.f};
-    param_load<4>(A2, a.A + ch * a.N + 4 * ng, nv);
+    const int nv = live ? states_valid<NS>(a.N, n0) : 0;
+    float A2[NS], h[NS], P[NS], gam[NS];
+    param_load<NS>(A2, a.A + ch * a.N + n0, nv);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) A2[j] *= kLog2e;
-    if (a.h0 && seg == 0) state_load(h, a.h0 + (b * a.D + ch) * a.N + 4 * ng, nv);
+    for (int j = 0; j < NS; ++j) {
+        A2[j] *= kLog2e;
+        h[j] = gam[j] = 0.f;
+        P[j] = 1.f;
+    }
+    if (a.h0 && seg == 0) states_load<NS>(h, a.h0 + (b * a.D + ch) * a.N + n0, nv);
 
     const int srow = tid / TPR, sc = (tid % TPR) * EPT;
     const int sv = ssm_left(Dg, c0 + sc, EPT);
     const int64_t scg = cg + c0 + sc;
     float bias[EPT];
-#pragma unroll
-    for (int e = 0; e < EPT; ++e) bias[e] = a.bias && e < sv ? a.bias[scg + e] : 0.f;
-    RawRow<EPT> rx, rt, rz, ro;
-    RawRow<4> rq[QPT];
+    param_load<EPT>(bias, a.bias + scg, a.bias ? sv : 0);
+    Row<EPT, BF16, RAG> rx, rt, rz;
+    Row<EPT, true, RAG> ro16;
+    Row<EPT, false, RAG> ro32;
+    Row<4, BF16, RAG> rq[QPT];
     auto fetch = [&](int64_t tb) {
         const int64_t t = tb + srow;
         const int v = t < t1 ? sv : 0;
-        row_load<EPT>(rx, a.x, v ? b * a.xb + t * a.xt + scg : 0, a.in_bf16, v);
-        row_load<EPT>(rt, a.dt, v ? b * a.dtb + t * a.dtt + scg : 0, a.in_bf16, v);
+        rx.load(a.x, b * a.xb + t * a.xt + scg, v);
+        rt.load(a.dt, b * a.dtb + t * a.dtt + scg, v);
         if constexpr (GAM) {
-            row_load<EPT>(ro, a.dout, v ? b * a.ob + t * a.ot + scg : 0, a.dout_bf16, v);
-            if (a.z) row_load<EPT>(rz, a.z, v ? b * a.zb + t * a.zt + scg : 0, a.in_bf16, v);
+            const int64_t oo = b * a.ob + t * a.ot + scg;
+            ro16.load(a.dout, oo, a.dout_bf16 ? v : 0);
+            ro32.load(a.dout, oo, a.dout_bf16 ? 0 : v);
+            rz.load(a.z, b * a.zb + t * a.zt + scg, a.z ? v : 0);
         }
 #pragma unroll
         for (int i = 0; i < QPT; ++i) {
             const int q = tid + 256 * i;
             const bool isc = q >= NQ;
             if (isc && !GAM) continue;
-            const int qt = (q % NQ) / LPC, qn = q % LPC;
+            const int qt = (q % NQ) / (NP / 4), qn = q % (NP / 4);
             const int64_t tq = tb + qt;
-            const int vq = q < 2 * NQ && tq < t1 ? ssm_states(a.N, qn) : 0;
-            row_load<4>(rq[i], isc ? a.Cm : a.Bm,
-                        vq ? (isc ? b * a.cb + tq * a.ct : b * a.bb + tq * a.bt) + g * a.N + 4 * qn
-                           : 0,
-                        a.in_bf16, vq);
+            const int vq = q < 2 * NQ && tq < t1 ? states_valid<4>(a.N, 4 * qn) : 0;
+            rq[i].load(isc ? a.Cm : a.Bm,
+                       (isc ? b * a.cb + tq * a.ct : b * a.bb + tq * a.bt) + g * a.N + 4 * qn, vq);
         }
     };
     fetch(t0);
     float sumd = 0.f;
     for (int64_t tb = t0; tb < t1; tb += TT) {
-        const bool tok = tb + srow < t1;
+        const int tv = tb + srow < t1 ? sv : 0;
         float x[EPT], r[EPT];
-        row_unpack<EPT>(x, rx, a.in_bf16);
-        row_unpack<EPT>(r, rt, a.in_bf16);
+        rx.unpack(x);
+        rt.unpack(r);
 #pragma unroll
         for (int e = 0; e < EPT; ++e) {
             float d = ssm_delta(r[e] + bias[e], a.softplus);
-            d = tok && e < sv ? d : 0.f;
+            d = e < tv ? d : 0.f;
             dd[srow][sc + e] = float2{d, d * x[e]};
         }
         if constexpr (GAM) {
             float o[EPT], z[EPT];
-            row_unpack<EPT>(o, ro, a.dout_bf16);
-            if (a.z) row_unpack<EPT>(z, rz, a.in_bf16);
+            if (a.dout_bf16)
+                ro16.unpack(o);
+            else
+                ro32.unpack(o);
+            rz.unpack(z);
 #pragma unroll
             for (int e = 0; e < EPT; ++e) {
-                if (a.z) o[e] *= z[e] * sigmoid(z[e]);
+                if (a.z) o[e] *= z[e] * sigmoid_fast(z[e]);
                 ds[srow][sc + e] = o[e];
             }
         }
 #pragma unroll
         for (int i = 0; i < QPT; ++i) {
             const int q = tid + 256 * i;
-            const bool isc = q >= NQ;
-            if (q >= 2 * NQ || (isc && !GAM)) continue;
+            if (q >= 2 * NQ || (q >= NQ && !GAM)) continue;
             float f[4];
-            row_unpack<4>(f, rq[i], a.in_bf16);
-            bc[(q % NQ) / LPC][isc][q % LPC] = float4{f[0], f[1], f[2], f[3]};
+            rq[i].unpack(f);
+            *reinterpret_cast<float4*>(&bc[q >= NQ][4 * (q % NQ)]) = float4{f[0], f[1], f[2], f[3]};
         }
         __syncthreads();
         if (tb + TT < t1) fetch(tb + TT);
@@ -137,71 +162,112 @@ __global__ __launch_bounds__(256) void ssm_bwd_states_kernel(SsmBwdArgs a, int64
         for (int tt = 0; tt < nt; tt += 4) {
             if (((tb + tt) & (S - 1)) == 0) {
                 const int64_t o = (b * nsub + (tb + tt) / S) * a.D + ch;
-                state_store(a.ckpt + o * a.N + 4 * ng, h, nv);
-                if (GAM && live && ng == 0) a.csum[o] = sumd;
+                states_store<NS>(a.ckpt + o * a.N + n0, h, nv);
+                if (GAM && live && n0 == 0) a.csum[o] = sumd;
             }
+            float Bq[4 / KT], Cq[4 / KT], dy[4] = {0.f, 0.f, 0.f, 0.f};
+            float2 d[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float2 d = dd[tt + k][chl];
-                const float4 B4 = bc[tt + k][0][ng];
-                const float Bv[4] = {B4.x, B4.y, B4.z, B4.w};
-                float aa[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    aa[j] = __builtin_amdgcn_exp2f(d.x * A2[j]);
-                    h[j] = __builtin_fmaf(aa[j], h[j], d.y * Bv[j]);
-                }
-                if constexpr (GAM) {
-                    const float dy = ds[tt + k][chl];
-                    const float4 C4 = bc[tt + k][1][ng];
-                    const float Cv[4] = {C4.x, C4.y, C4.z, C4.w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        P[j] *= aa[j];
-                        gam[j] = __builtin_fmaf(P[j], Cv[j] * dy, gam[j]);
-                    }
-                    sumd += d.x;
-                }
+                d[k] = dd[tt + k][chl];
+                if constexpr (GAM) dy[k] = ds[tt + k][chl];
             }
+#pragma unroll
+            for (int k = 0; k < 4 / KT; ++k) {
+                Bq[k] = row_coef<NS, NG>(bc[0], tt + k * KT, lane);
+                Cq[k] = GAM ? row_coef<NS, NG>(bc[1], tt + k * KT, lane) : 0.f;
+            }
+            constexpr auto js = std::make_index_sequence<NS>{};
+#define TOKEN(k) \
+    states_token<NS, k % KT, GAM>(h, P, gam, A2, d[k].x, d[k].y, dy[k], Bq[k / KT], Cq[k / KT], js)
+            TOKEN(0);
+            TOKEN(1);
+            TOKEN(2);
+            TOKEN(3);
+#undef TOKEN
+            if constexpr (GAM) sumd += (d[0].x + d[1].x) + (d[2].x + d[3].x);
         }
         __syncthreads();
     }
     if constexpr (GAM) {
         const int64_t o = (b * nseg + seg) * a.D + ch;
-        state_store(a.hend + o * a.N + 4 * ng, h, nv);
-        state_store(a.gstart + o * a.N + 4 * ng, gam, nv);
-        if (live && ng == 0) a.sdelta[o] = sumd;
+        states_store<NS>(a.hend + o * a.N + n0, h, nv);
+        states_store<NS>(a.gstart + o * a.N + n0, gam, nv);
+        if (live && n0 == 0) a.sdelta[o] = sumd;
     }
 }
 
-// Halving reduction over the channels of a wave: v holds 8 values per lane
-// (index i) and token; afterwards each lane holds the sum over its wave's
-// channels of value `idx` (returned by sum_index) in v[0] (and v[1] at LPC 16).
-template <int LPC>
-__device__ __forceinline__ void wave_channel_sums(float (&v)[8], int lane) {
+// A token of the second pass, forwards: a_t and h_t from h_{t-1}; returns the
+// lane's part of y.
+template <int NS, int K, size_t... J>
+__device__ __forceinline__ float fore_token(float (&aa)[NS], float (&hh)[NS],
+                                            const float (&hp)[NS], const float (&A2)[NS], float d,
+                                            float dx, float Bq, float Cq, bool y,
+                                            std::index_sequence<J...>) {
+    ((aa[J] = __builtin_amdgcn_exp2f(d * A2[J])), ...);
+    ((hh[J] = __builtin_fmaf(aa[J], hp[J], row_bcast<K * NS + J>(Bq) * dx)), ...);
+    float s = 0.f;
+    if (y) ((s = __builtin_fmaf(row_bcast<K * NS + J>(Cq), hh[J], s)), ...);
+    return s;
+}
+
+// And backwards: gr enters as a_{t+1} g_{t+1} and leaves as a_t g_t.
+template <int NS, int K, size_t... J>
+__device__ __forceinline__ void back_token(float (&gr)[NS], float (&dA)[NS], float (&pv)[2 * NS],
+                                           float& sB, float& sA, const float (&aa)[NS],
+                                           const float (&hh)[NS], const float (&hp)[NS],
+                                           const float (&A2)[NS], float d, float dx, float dy,
+                                           float Bq, float Cq, std::index_sequence<J...>) {
+    ((gr[J] = __builtin_fmaf(row_bcast<K * NS + J>(Cq), dy, gr[J])), ...);
+    ((pv[J] = hh[J] * dy, pv[NS + J] = gr[J] * dx), ...);
+    sB = 0.f;
+    ((sB = __builtin_fmaf(row_bcast<K * NS + J>(Bq), gr[J], sB)), ...);
+    float u[NS];
+    ((gr[J] *= aa[J], u[J] = gr[J] * hp[J]), ...);
+    sA = 0.f;
+    ((sA = __builtin_fmaf(u[J], A2[J], sA), dA[J] = __builtin_fmaf(u[J], d, dA[J])), ...);
+}
+
+// Halving reduction of M values over the 16 lanes of each row, then (NG < 4)
+// over the rows that hold other channels.  Lane bits 3, 2, 1, 0 choose the
+// value that a lane is left with; at M = 8 bit 0 chooses nothing, at M = 32
+// two values are left.
+template <int M, int NG>
+__device__ __forceinline__ void channel_sums(float (&v)[M], int lane) {
+    constexpr int M1 = M / 2, M2 = M / 4, M3 = M / 8, M4 = M / 16;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = fold32(v[i], v[i + 4]);
+    for (int i = 0; i < M1; ++i) v[i] = fold<3>(v[i], v[i + M1], lane & 8);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) v[i] = fold16(v[i], v[i + 2]);
-    if constexpr (LPC <= 8) v[0] = fold<8>(v[0], v[1], lane & 8);
-    if constexpr (LPC <= 4) v[0] += xor_lane<4>(v[0]);
-    if constexpr (LPC <= 2) v[0] += xor_lane<2>(v[0]);
-    if constexpr (LPC <= 1) v[0] += xor_lane<1>(v[0]);
+    for (int i = 0; i < M2; ++i) v[i] = fold<2>(v[i], v[i + M2], lane & 4);
+#pragma unroll
+    for (int i = 0; i < M3; ++i) v[i] = fold<1>(v[i], v[i + M3], lane & 2);
+    if constexpr (M4 > 0) {
+#pragma unroll
+        for (int i = 0; i < M4; ++i) v[i] = fold<0>(v[i], v[i + M4], lane & 1);
+    } else {
+        v[0] += pair_lane<0>(v[0]);
+    }
+#pragma unroll
+    for (int i = 0; i < (M4 > 0 ? M4 : 1); ++i) {
+        if constexpr (NG <= 2) v[i] = fold32(v[i], v[i]);
+        if constexpr (NG <= 1) v[i] = fold16(v[i], v[i]);
+    }
 }
 
 // Second pass.
-template <int LPC>
-__global__ __launch_bounds__(256) void ssm_bwd_kernel(SsmBwdArgs a, int64_t nblk, int64_t nseg,
-                                                      int64_t L) {
-    constexpr int WC = 256 / LPC;
-    constexpr int S = block_tokens<LPC>();
+template <int NS, int NG, bool BF16, bool RAG>
+__global__ __launch_bounds__(256, 2) void ssm_bwd_kernel(SsmBwdArgs a, int64_t nblk, int64_t nseg,
+                                                         int64_t L) {
+    constexpr int NP = NS * NG, CW = 64 / NG, WC = 4 * CW;
+    constexpr int S = block_tokens<NS, NG>();
     constexpr int EPT = S * WC / 256;
     constexpr int TPR = WC / EPT;
-    constexpr int NQ = S * LPC;
+    constexpr int NQ = S * NP / 4;
     constexpr int QPT = (2 * NQ + 255) / 256;
-    constexpr int NP = 4 * LPC;
-    __shared__ float4 st[S][WC];              // Delta, Delta x, dy, (y); then sums over n
-    __shared__ float4 bc[S][2][LPC];
+    constexpr int KT = 16 / NS;
+    __shared__ f32x4 st[S][WC];               // Delta, Delta x, dy, (y); then sums over n
+    __shared__ f32x4 raw[S][WC];              // x, dt + bias, dout, z, for the block's end
+    __shared__ __align__(16) float bc[2][S * NP];
     __shared__ float pbc[4][S][2 * NP];       // each wave's sums over its channels: dC, dB
 
     const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
@@ -215,92 +281,105 @@ __global__ __launch_bounds__(256) void ssm_bwd_kernel(SsmBwdArgs a, int64_t nblk
     const int64_t t0 = seg * L, t1 = t0 + L < a.T ? t0 + L : a.T;
     const int64_t nsub = (a.T + S - 1) / S;
 
-    const int ng = lane % LPC, chl = wv * (64 / LPC) + lane / LPC;
+    const int row = lane >> 4, n0 = NS * (row % NG);
+    const int chl = wv * CW + (lane & 15) + 16 * (row / NG);
     const bool live = c0 + chl < Dg;
     const int64_t ch = cg + (live ? c0 + chl : 0);
-    const int nv = live ? ssm_states(a.N, ng) : 0;
-    float A2[4], hin[4] = {0.f, 0.f, 0.f, 0.f}, gr[4] = {0.f, 0.f, 0.f, 0.f};
-    float dA[4] = {0.f, 0.f, 0.f, 0.f};
-    param_load<4>(A2, a.A + ch * a.N + 4 * ng, nv);
+    const int nv = live ? states_valid<NS>(a.N, n0) : 0;
+    float A2[NS], hin[NS], gr[NS], dA[NS];
+    param_load<NS>(A2, a.A + ch * a.N + n0, nv);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) A2[j] *= kLog2e;
-    const int64_t so = (b * a.D + ch) * a.N + 4 * ng;
+    for (int j = 0; j < NS; ++j) {
+        A2[j] *= kLog2e;
+        hin[j] = gr[j] = dA[j] = 0.f;
+    }
+    const int64_t so = (b * a.D + ch) * a.N + n0;
     // the segment's start state (segment 0's kept states hold h0 already)
     for (int64_t s = 0; s < seg; ++s) {
         const int64_t o = (b * nseg + s) * a.D + ch;
-        float e[4];
-        state_load(e, a.hend + o * a.N + 4 * ng, nv);
+        float e[NS];
+        states_load<NS>(e, a.hend + o * a.N + n0, nv);
         const float sd = live ? a.sdelta[o] : 0.f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            hin[j] = s == 0 ? e[j] : __builtin_fmaf(__builtin_amdgcn_exp2f(A2[j] * sd), hin[j], e[j]);
+        for (int j = 0; j < NS; ++j)
+            hin[j] = s == 0 ? e[j]
+                            : __builtin_fmaf(__builtin_amdgcn_exp2f(A2[j] * sd), hin[j], e[j]);
     }
     // gr = a_{t+1} g_{t+1} past the segment's last token
-    if (a.dh_final) state_load(gr, a.dh_final + so, nv);
+    if (a.dh_final) states_load<NS>(gr, a.dh_final + so, nv);
     for (int64_t s = nseg - 1; s > seg; --s) {
         const int64_t o = (b * nseg + s) * a.D + ch;
-        float e[4];
-        state_load(e, a.gstart + o * a.N + 4 * ng, nv);
+        float e[NS];
+        states_load<NS>(e, a.gstart + o * a.N + n0, nv);
         const float sd = live ? a.sdelta[o] : 0.f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < NS; ++j)
             gr[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(A2[j] * sd), gr[j], e[j]);
     }
 
     const int srow = tid / TPR, sc = (tid % TPR) * EPT;
     const int sv = ssm_left(Dg, c0 + sc, EPT);
     const int64_t scg = cg + c0 + sc;
-    float bias[EPT], skip[EPT], dD[EPT], dbias[EPT];
+    float dD[EPT], dbias[EPT];
 #pragma unroll
-    for (int e = 0; e < EPT; ++e) {
-        bias[e] = a.bias && e < sv ? a.bias[scg + e] : 0.f;
-        skip[e] = a.D_skip && e < sv ? a.D_skip[scg + e] : 0.f;
-        dD[e] = dbias[e] = 0.f;
-    }
+    for (int e = 0; e < EPT; ++e) dD[e] = dbias[e] = 0.f;
 
-    const int64_t first = t0 / S, last = (t1 + S - 1) / S;
-    for (int64_t sub = last - 1; sub >= first; --sub) {
+    Row<EPT, BF16, RAG> rx, rt, rz;
+    Row<EPT, true, RAG> ro16;
+    Row<EPT, false, RAG> ro32;
+    Row<4, BF16, RAG> rq[QPT];
+    float kept[NS], ksum = 0.f;
+    auto fetch = [&](int64_t sub) {
         const int64_t tb = sub * S, t = tb + srow;
         const int v = t < t1 ? sv : 0;
-        RawRow<EPT> rx, rt, rz, ro;
-        RawRow<4> rq[QPT];
-        row_load<EPT>(rx, a.x, v ? b * a.xb + t * a.xt + scg : 0, a.in_bf16, v);
-        row_load<EPT>(rt, a.dt, v ? b * a.dtb + t * a.dtt + scg : 0, a.in_bf16, v);
-        row_load<EPT>(ro, a.dout, v ? b * a.ob + t * a.ot + scg : 0, a.dout_bf16, v);
-        if (a.z) row_load<EPT>(rz, a.z, v ? b * a.zb + t * a.zt + scg : 0, a.in_bf16, v);
+        rx.load(a.x, b * a.xb + t * a.xt + scg, v);
+        rt.load(a.dt, b * a.dtb + t * a.dtt + scg, v);
+        const int64_t oo = b * a.ob + t * a.ot + scg;
+        ro16.load(a.dout, oo, a.dout_bf16 ? v : 0);
+        ro32.load(a.dout, oo, a.dout_bf16 ? 0 : v);
+        rz.load(a.z, b * a.zb + t * a.zt + scg, a.z ? v : 0);
 #pragma unroll
         for (int i = 0; i < QPT; ++i) {
             const int q = tid + 256 * i;
             const bool isc = q >= NQ;
-            const int qt = (q % NQ) / LPC, qn = q % LPC;
+            const int qt = (q % NQ) / (NP / 4), qn = q % (NP / 4);
             const int64_t tq = tb + qt;
-            const int vq = q < 2 * NQ && tq < t1 ? ssm_states(a.N, qn) : 0;
-            row_load<4>(rq[i], isc ? a.Cm : a.Bm,
-                        vq ? (isc ? b * a.cb + tq * a.ct : b * a.bb + tq * a.bt) + g * a.N + 4 * qn
-                           : 0,
-                        a.in_bf16, vq);
+            const int vq = q < 2 * NQ && tq < t1 ? states_valid<4>(a.N, 4 * qn) : 0;
+            rq[i].load(isc ? a.Cm : a.Bm,
+                       (isc ? b * a.cb + tq * a.ct : b * a.bb + tq * a.bt) + g * a.N + 4 * qn, vq);
         }
         const int64_t ko = (b * nsub + sub) * a.D + ch;
-        float hs[4];
-        state_load(hs, a.ckpt + ko * a.N + 4 * ng, nv);
-        if (seg > 0) {
-            const float sd = live ? a.csum[ko] : 0.f;
+        states_load<NS>(kept, a.ckpt + ko * a.N + n0, nv);
+        if (seg > 0) ksum = live ? a.csum[ko] : 0.f;
+    };
+
+    const int64_t first = t0 / S, last = (t1 + S - 1) / S;
+    fetch(last - 1);
+    for (int64_t sub = last - 1; sub >= first; --sub) {
+        const int64_t tb = sub * S, t = tb + srow;
+        const int v = t < t1 ? sv : 0;
+        float hs[NS];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                hs[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(A2[j] * sd), hin[j], hs[j]);
-        }
+        for (int j = 0; j < NS; ++j)
+            hs[j] = seg > 0 ? __builtin_fmaf(__builtin_amdgcn_exp2f(A2[j] * ksum), hin[j], kept[j])
+                            : kept[j];
         {
             float x[EPT], r[EPT], o[EPT], z[EPT];
-            row_unpack<EPT>(x, rx, a.in_bf16);
-            row_unpack<EPT>(r, rt, a.in_bf16);
-            row_unpack<EPT>(o, ro, a.dout_bf16);
-            if (a.z) row_unpack<EPT>(z, rz, a.in_bf16);
+            rx.unpack(x);
+            rt.unpack(r);
+            if (a.dout_bf16)
+                ro16.unpack(o);
+            else
+                ro32.unpack(o);
+            rz.unpack(z);
 #pragma unroll
             for (int e = 0; e < EPT; ++e) {
-                float d = ssm_delta(r[e] + bias[e], a.softplus);
+                r[e] += a.bias && e < sv ? a.bias[scg + e] : 0.f;
+                float d = ssm_delta(r[e], a.softplus);
                 d = e < v ? d : 0.f;
-                if (a.z) o[e] *= z[e] * sigmoid(z[e]);
-                st[srow][sc + e] = float4{d, d * x[e], o[e], 0.f};
+                const float dy = a.z ? o[e] * (z[e] * sigmoid_fast(z[e])) : o[e];
+                st[srow][sc + e] = f32x4{d, d * x[e], dy, 0.f};
+                raw[srow][sc + e] = f32x4{x[e], r[e], o[e], z[e]};
             }
         }
 #pragma unroll
@@ -308,108 +387,112 @@ __global__ __launch_bounds__(256) void ssm_bwd_kernel(SsmBwdArgs a, int64_t nblk
             const int q = tid + 256 * i;
             if (q >= 2 * NQ) continue;
             float f[4];
-            row_unpack<4>(f, rq[i], a.in_bf16);
-            bc[(q % NQ) / LPC][q >= NQ][q % LPC] = float4{f[0], f[1], f[2], f[3]};
+            rq[i].unpack(f);
+            *reinterpret_cast<float4*>(&bc[q >= NQ][4 * (q % NQ)]) = float4{f[0], f[1], f[2], f[3]};
         }
         __syncthreads();
+        if (sub > first) fetch(sub - 1);
 
         // the block's states again, all kept in registers
-        float hh[S][4], aa[S][4];
+        constexpr auto js = std::make_index_sequence<NS>{};
+        float hh[S][NS], aa[S][NS];
 #pragma unroll
         for (int tt = 0; tt < S; tt += 4) {
-            float s[4];
+            float s[4], Bq[4 / KT], Cq[4 / KT];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float4 d = st[tt + k][chl];
-                const float4 B4 = bc[tt + k][0][ng], C4 = bc[tt + k][1][ng];
-                const float Bv[4] = {B4.x, B4.y, B4.z, B4.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float p = tt + k == 0 ? hs[j] : hh[tt + k == 0 ? 0 : tt + k - 1][j];
-                    aa[tt + k][j] = __builtin_amdgcn_exp2f(d.x * A2[j]);
-                    hh[tt + k][j] = __builtin_fmaf(aa[tt + k][j], p, d.y * Bv[j]);
-                }
-                s[k] = __builtin_fmaf(C4.w, hh[tt + k][3], __builtin_fmaf(C4.z, hh[tt + k][2],
-                       __builtin_fmaf(C4.y, hh[tt + k][1], C4.x * hh[tt + k][0])));
+            for (int k = 0; k < 4 / KT; ++k) {
+                Bq[k] = row_coef<NS, NG>(bc[0], tt + k * KT, lane);
+                Cq[k] = row_coef<NS, NG>(bc[1], tt + k * KT, lane);
             }
-            if (a.z) channel_sums<LPC>(s, ng, &st[tt][chl].w, 4 * WC);
+#define TOKEN(k)                                                                               \
+    {                                                                                          \
+        const f32x4 d = st[tt + k][chl];                                                       \
+        s[k] = fore_token<NS, k % KT>(aa[tt + k], hh[tt + k],                                  \
+                                      tt + k == 0 ? hs : hh[tt + k == 0 ? 0 : tt + k - 1], A2, \
+                                      d[0], d[1], Bq[k / KT], Cq[k / KT], a.z, js);            \
+    }
+            TOKEN(0)
+            TOKEN(1)
+            TOKEN(2)
+            TOKEN(3)
+#undef TOKEN
+            if (a.z) state_sums<NG>(s, row, reinterpret_cast<float*>(&st[tt][chl]) + 3, 4 * WC);
         }
         // and backwards
-        float dAl[4] = {0.f, 0.f, 0.f, 0.f};
+        float dAl[NS];
+#pragma unroll
+        for (int j = 0; j < NS; ++j) dAl[j] = 0.f;
 #pragma unroll
         for (int tt = S - 4; tt >= 0; tt -= 4) {
-            float sB[4], sA[4];
+            float sB[4], sA[4], Bq[4 / KT], Cq[4 / KT];
 #pragma unroll
-            for (int k = 3; k >= 0; --k) {
-                const int q = tt + k;
-                const float4 d = st[q][chl];
-                const float4 B4 = bc[q][0][ng], C4 = bc[q][1][ng];
-                const float Bv[4] = {B4.x, B4.y, B4.z, B4.w};
-                const float Cv[4] = {C4.x, C4.y, C4.z, C4.w};
-                float pv[8];
-                sB[k] = sA[k] = 0.f;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float p = q == 0 ? hs[j] : hh[q == 0 ? 0 : q - 1][j];
-                    gr[j] = __builtin_fmaf(Cv[j], d.z, gr[j]);
-                    pv[j] = hh[q][j] * d.z;
-                    pv[4 + j] = gr[j] * d.y;
-                    sB[k] = __builtin_fmaf(gr[j], Bv[j], sB[k]);
-                    gr[j] *= aa[q][j];
-                    const float u = gr[j] * p;
-                    sA[k] = __builtin_fmaf(u, A2[j], sA[k]);
-                    dAl[j] = __builtin_fmaf(u, d.x, dAl[j]);
-                }
-                wave_channel_sums<LPC>(pv, lane);
-                // lane bits 5, 4 (and 3) chose the value: C or B, then its index
-                if constexpr (LPC == 16) {
-                    const int i0 = ((lane >> 5) & 1) * NP + 4 * ng + ((lane >> 4) & 1) * 2;
-                    pbc[wv][q][i0] = pv[0];
-                    pbc[wv][q][i0 + 1] = pv[1];
-                } else {
-                    const int i0 = ((lane >> 5) & 1) * NP + 4 * ng + ((lane >> 4) & 1) * 2 +
-                                   ((lane >> 3) & 1);
-                    if ((lane & 7) < LPC) pbc[wv][q][i0] = pv[0];
-                }
+            for (int k = 0; k < 4 / KT; ++k) {
+                Bq[k] = row_coef<NS, NG>(bc[0], tt + k * KT, lane);
+                Cq[k] = row_coef<NS, NG>(bc[1], tt + k * KT, lane);
             }
-            channel_sums<LPC>(sB, ng, &st[tt][chl].x, 4 * WC);
-            channel_sums<LPC>(sA, ng, &st[tt][chl].y, 4 * WC);
+#define TOKEN(k)                                                                                \
+    {                                                                                           \
+        const f32x4 d = st[tt + k][chl];                                                        \
+        float pv[2 * NS];                                                                       \
+        back_token<NS, k % KT>(gr, dAl, pv, sB[k], sA[k], aa[tt + k], hh[tt + k],               \
+                               tt + k == 0 ? hs : hh[tt + k == 0 ? 0 : tt + k - 1], A2, d[0],   \
+                               d[1], d[2], Bq[k / KT], Cq[k / KT], js);                         \
+        channel_sums<2 * NS, NG>(pv, lane);                                                     \
+        store_sums(pv, tt + k);                                                                 \
+    }
+            // lane bits 3 .. 0 chose the value: of dC or dB, then its state
+            auto store_sums = [&](const float(&pv)[2 * NS], int q) {
+                float* p = pbc[wv][q] + ((lane >> 3) & 1) * NP + n0;
+                if constexpr (NS == 4) {
+                    if ((lane & 1) == 0 && row < NG) p[((lane >> 2) & 1) * 2 + ((lane >> 1) & 1)] = pv[0];
+                } else if constexpr (NS == 8) {
+                    p[lane & 7] = pv[0];
+                } else {
+                    p[2 * (lane & 7)] = pv[0];
+                    p[2 * (lane & 7) + 1] = pv[1];
+                }
+            };
+            TOKEN(3)
+            TOKEN(2)
+            TOKEN(1)
+            TOKEN(0)
+#undef TOKEN
+            float* sp = reinterpret_cast<float*>(&st[tt][chl]);
+            state_sums<NG>(sB, row, sp, 4 * WC);
+            state_sums<NG>(sA, row, sp + 1, 4 * WC);
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) dA[j] += dAl[j];
+        for (int j = 0; j < NS; ++j) dA[j] += dAl[j];
         __syncthreads();
 
         if (v > 0) {
-            float x[EPT], r[EPT], o[EPT], z[EPT], dxv[EPT], dtv[EPT];
-            row_unpack<EPT>(x, rx, a.in_bf16);
-            row_unpack<EPT>(r, rt, a.in_bf16);
-            row_unpack<EPT>(o, ro, a.dout_bf16);
-            if (a.z) row_unpack<EPT>(z, rz, a.in_bf16);
+            float dxv[EPT], dtv[EPT], dzv[EPT];
 #pragma unroll
             for (int e = 0; e < EPT; ++e) {
-                const float4 q = st[srow][sc + e];
-                const float raw = r[e] + bias[e];
-                const float d = ssm_delta(raw, a.softplus);
-                float dy = o[e];
+                const f32x4 q = st[srow][sc + e], in = raw[srow][sc + e];
+                const float x = in[0], r = in[1], o = in[2], z = in[3];
+                const float skip = a.D_skip && e < sv ? a.D_skip[scg + e] : 0.f;
+                const float d = ssm_delta(r, a.softplus);
+                float dy = o;
                 if (a.z) {
-                    const float sg = sigmoid(z[e]);
-                    const float y = __builtin_fmaf(skip[e], x[e], q.w);
-                    dy *= z[e] * sg;
-                    z[e] = o[e] * y * sg * __builtin_fmaf(z[e], 1.f - sg, 1.f);
+                    const float sg = sigmoid_fast(z);
+                    const float y = __builtin_fmaf(skip, x, q[3]);
+                    dy *= z * sg;
+                    dzv[e] = o * y * sg * __builtin_fmaf(z, 1.f - sg, 1.f);
                 }
-                dxv[e] = __builtin_fmaf(d, q.x, skip[e] * dy);
-                float dr = __builtin_fmaf(x[e], q.x, q.y * kLn2);
-                if (a.softplus) dr *= sigmoid(raw);
+                dxv[e] = __builtin_fmaf(d, q[0], skip * dy);
+                float dr = __builtin_fmaf(x, q[0], q[1] * kLn2);
+                if (a.softplus) dr *= sigmoid(r);
                 dtv[e] = dr;
                 if (e < v) {
-                    dD[e] = __builtin_fmaf(dy, x[e], dD[e]);
+                    dD[e] = __builtin_fmaf(dy, x, dD[e]);
                     dbias[e] += dr;
                 }
             }
             const int64_t oo = (b * a.T + t) * a.D + scg;
             row_store<EPT>(a.dx, oo, a.grad_bf16, dxv, v);
             row_store<EPT>(a.ddt, oo, a.grad_bf16, dtv, v);
-            if (a.z) row_store<EPT>(a.dz, oo, a.grad_bf16, z, v);
+            if (a.z) row_store<EPT>(a.dz, oo, a.grad_bf16, dzv, v);
         }
         for (int i = tid; i < S * 2 * NP; i += 256) {
             const int q = i / (2 * NP), k = i % (2 * NP);
@@ -419,9 +502,9 @@ __global__ __launch_bounds__(256) void ssm_bwd_kernel(SsmBwdArgs a, int64_t nblk
         }
         __syncthreads();
     }
-    if (seg == 0 && a.dh0) state_store(a.dh0 + so, gr, nv);
+    if (seg == 0 && a.dh0) states_store<NS>(a.dh0 + so, gr, nv);
     float* part = a.part + (b * nseg + seg) * a.D * (a.N + 2);
-    state_store(part + ch * a.N + 4 * ng, dA, nv);
+    states_store<NS>(part + ch * a.N + n0, dA, nv);
     // dD and dbias over the thread rows of a channel, through st
     float* red = reinterpret_cast<float*>(st);
 #pragma unroll
@@ -455,13 +538,18 @@ __global__ __launch_bounds__(256) void ssm_bc_reduce(SsmBwdArgs a, int64_t nblk)
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+int64_t padded_states(int64_t N) {
+    int64_t n = 4;
+    while (n < N) n *= 2;
+    return n;
+}
+
 // Segments of the backward.  Its second pass holds two waves per SIMD, so one
 // segment does where the channels give 2048 waves; fewer channels get enough
 // segments (of at least 64 tokens) for that.
 SsmPlan bwd_plan(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N) {
     SsmPlan p;
-    p.lpc = ssm_lanes(N);
-    p.nblk = cdiv(D / G, 256 / p.lpc);
+    p.nblk = cdiv(D / G, ssm_wg_channels(N));
     const int64_t waves = 4 * B * G * p.nblk;
     int64_t n = cdiv(2048, waves);
     const int64_t most = cdiv(T, 64);
@@ -471,6 +559,9 @@ SsmPlan bwd_plan(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N) {
     p.nseg = T > 0 ? cdiv(T, p.L) : 1;
     return p;
 }
+
+// Tokens between kept states, for N states.
+int64_t kept_tokens(int64_t N) { return N <= 4 ? 8 : N <= 16 ? 16 : N <= 32 ? 8 : 4; }
 
 struct BwdLayout {
     size_t ckpt, csum, hend, gstart, sdelta, part, bcpart, total;
@@ -484,7 +575,7 @@ BwdLayout bwd_layout(const SsmPlan& p, int64_t B, int64_t T, int64_t D, int64_t 
         at += (sizeof(float) * (size_t)n + 255) & ~(size_t)255;
         return o;
     };
-    const int64_t nsub = cdiv(T, p.lpc == 1 ? 8 : 16);
+    const int64_t nsub = cdiv(T, kept_tokens(N));
     const bool many = p.nseg > 1;
     l.ckpt = take(B * nsub * D * N);
     l.csum = take(many ? B * nsub * D : 0);
@@ -492,28 +583,39 @@ BwdLayout bwd_layout(const SsmPlan& p, int64_t B, int64_t T, int64_t D, int64_t 
     l.gstart = take(many ? B * p.nseg * D * N : 0);
     l.sdelta = take(many ? B * p.nseg * D : 0);
     l.part = take(B * p.nseg * D * (N + 2));
-    l.bcpart = take(p.nblk * B * T * G * 8 * p.lpc);
+    l.bcpart = take(p.nblk * B * T * G * 2 * padded_states(N));
     l.total = at;
     return l;
 }
 
-template <int LPC>
-hipError_t launch_bwd_t(const SsmBwdArgs& a, const SsmPlan& p) {
+template <int NS, int NG, bool BF16, bool RAG>
+hipError_t launch_bwd_r(const SsmBwdArgs& a, const SsmPlan& p) {
     const dim3 grid((unsigned)(a.B * a.G * p.nblk * p.nseg));
     if (p.nseg > 1)
-        hipLaunchKernelGGL((ssm_bwd_states_kernel<LPC, true>), grid, dim3(256), 0, a.stream, a,
-                           p.nblk, p.nseg, p.L);
+        hipLaunchKernelGGL((ssm_bwd_states_kernel<NS, NG, true, BF16, RAG>), grid, dim3(256), 0,
+                           a.stream, a, p.nblk, p.nseg, p.L);
     else
-        hipLaunchKernelGGL((ssm_bwd_states_kernel<LPC, false>), grid, dim3(256), 0, a.stream, a,
-                           p.nblk, p.nseg, p.L);
+        hipLaunchKernelGGL((ssm_bwd_states_kernel<NS, NG, false, BF16, RAG>), grid, dim3(256), 0,
+                           a.stream, a, p.nblk, p.nseg, p.L);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((ssm_bwd_kernel<LPC>), grid, dim3(256), 0, a.stream, a, p.nblk, p.nseg,
-                       p.L);
-    e = hipGetLastError();
+    hipLaunchKernelGGL((ssm_bwd_kernel<NS, NG, BF16, RAG>), grid, dim3(256), 0, a.stream, a,
+                       p.nblk, p.nseg, p.L);
+    return hipGetLastError();
+}
+
+template <int NS, int NG>
+hipError_t launch_bwd_t(const SsmBwdArgs& a, const SsmPlan& p) {
+    const bool rag = (a.D / a.G) % 8 != 0 || a.N % 4 != 0;
+    hipError_t e;
+    if (a.in_bf16)
+        e = rag ? launch_bwd_r<NS, NG, true, true>(a, p) : launch_bwd_r<NS, NG, true, false>(a, p);
+    else
+        e = rag ? launch_bwd_r<NS, NG, false, true>(a, p)
+                : launch_bwd_r<NS, NG, false, false>(a, p);
     if (e != hipSuccess) return e;
-    const int64_t n = a.B * a.T * a.G * 8 * LPC;
-    hipLaunchKernelGGL((ssm_bc_reduce<4 * LPC>), dim3((unsigned)cdiv(n, 256)), dim3(256), 0,
+    const int64_t n = a.B * a.T * a.G * 2 * NS * NG;
+    hipLaunchKernelGGL((ssm_bc_reduce<NS * NG>), dim3((unsigned)cdiv(n, 256)), dim3(256), 0,
                        a.stream, a, p.nblk);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -529,7 +631,7 @@ size_t ssm_bwd_workspace_bytes(int64_t B, int64_t T, int64_t D, int64_t G, int64
 
 int64_t ssm_bwd_workgroups(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N) {
     const SsmPlan p = bwd_plan(B, T, D, G, N);
-    const int64_t n = B * G * p.nblk * p.nseg, r = cdiv(B * T * G * 8 * p.lpc, 256);
+    const int64_t n = B * G * p.nblk * p.nseg, r = cdiv(B * T * G * 2 * padded_states(N), 256);
     return n > r ? n : r;
 }
 
@@ -544,13 +646,11 @@ hipError_t launch_ssm_bwd(SsmBwdArgs a, void* ws) {
     a.sdelta = reinterpret_cast<float*>(w + l.sdelta);
     a.part = reinterpret_cast<float*>(w + l.part);
     a.bcpart = reinterpret_cast<float*>(w + l.bcpart);
-    switch (p.lpc) {
-        case 1: return launch_bwd_t<1>(a, p);
-        case 2: return launch_bwd_t<2>(a, p);
-        case 4: return launch_bwd_t<4>(a, p);
-        case 8: return launch_bwd_t<8>(a, p);
-        default: return launch_bwd_t<16>(a, p);
-    }
+    if (a.N <= 4) return launch_bwd_t<4, 1>(a, p);
+    if (a.N <= 8) return launch_bwd_t<4, 2>(a, p);
+    if (a.N <= 16) return launch_bwd_t<4, 4>(a, p);
+    if (a.N <= 32) return launch_bwd_t<8, 4>(a, p);
+    return launch_bwd_t<16, 4>(a, p);
 }
 
 }  // namespace gdr

@@ -10,9 +10,8 @@
 // and two fused adds per state and token (25 cycles per 64 of them on gfx950,
 // measured), in fp32 throughout.
 //
-// Work split: the four lanes of a channel at N = 16 hold 4 states each, which
-// fills the chip at 16384 channels and costs 2 adds per token for the sum over n.
-// A tile of tokens is staged in LDS by the whole workgroup (Delta and Delta x
+// Work split (ssm.h): rows of 16 lanes are channels, so B and C enter as row
+// broadcasts.  A tile of tokens is staged in LDS by the whole workgroup (Delta and Delta x
 // once per channel, B and C as fp32), so the token loop has no global access;
 // the next tile's loads are issued before it and land during it.
 //
@@ -21,24 +20,39 @@
 // Delta (whose exp with A is the segment's decay); the second starts from the
 // states composed of those.  It costs a second exp per state, so it is taken
 // only where the channels alone leave most of the chip idle (ssm_fwd_segs).
+#include <utility>
+
 #include "ssm.h"
 
 namespace gdr {
 
 namespace {
 
-template <int LPC, bool OUT>
+// One token of the lane's states: K is its place in the registers Bq, Cq.
+template <int NS, int K, bool OUT, size_t... J>
+__device__ __forceinline__ float scan_token(float (&h)[NS], const float (&A2)[NS], float d, float dx,
+                                            float Bq, float Cq, std::index_sequence<J...>) {
+    ((h[J] = __builtin_fmaf(__builtin_amdgcn_exp2f(d * A2[J]), h[J],
+                            row_bcast<K * NS + J>(Bq) * dx)),
+     ...);
+    float s = 0.f;
+    if constexpr (OUT) ((s = __builtin_fmaf(row_bcast<K * NS + J>(Cq), h[J], s)), ...);
+    return s;
+}
+
+template <int NS, int NG, bool OUT, bool BF16, bool RAG>
 __global__ __launch_bounds__(256) void ssm_fwd_kernel(SsmArgs a, int64_t nblk, int64_t nseg,
                                                       int64_t L) {
-    constexpr int WC = 256 / LPC;
-    constexpr int TT = 8 * LPC < 32 ? 8 * LPC : 32;   // tokens per tile
-    constexpr int EPT = TT * WC / 256;                // staged channels per thread
+    constexpr int NP = NS * NG, CW = 64 / NG, WC = 4 * CW;
+    constexpr int EPT = 8;                            // staged channels per thread
+    constexpr int TT = 256 * EPT / WC;                // tokens per tile
     constexpr int TPR = WC / EPT;                     // threads per token row
-    constexpr int NQ = TT * LPC;                      // groups of 4 of B (and of C) per tile
+    constexpr int NQ = TT * NP / 4;                   // groups of 4 of B (and of C) per tile
     constexpr int QPT = (2 * NQ + 255) / 256;
+    constexpr int KT = 16 / NS;                       // tokens per B register
     constexpr int YP = WC + 16;                       // pitch: 4 tokens' stores meet no bank twice
     __shared__ float2 dd[TT][WC];
-    __shared__ float4 bc[TT][2][LPC];
+    __shared__ __align__(16) float bc[2][TT * NP];
     __shared__ float ys[OUT ? TT : 1][YP];
 
     const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
@@ -53,31 +67,35 @@ __global__ __launch_bounds__(256) void ssm_fwd_kernel(SsmArgs a, int64_t nblk, i
     const int64_t t0 = seg * L, t1 = t0 + L < a.T ? t0 + L : a.T;
 
     // the lane's channel and states
-    const int ng = lane % LPC, chl = wv * (64 / LPC) + lane / LPC;
+    const int row = lane >> 4, n0 = NS * (row % NG);
+    const int chl = wv * CW + (lane & 15) + 16 * (row / NG);
     const bool live = c0 + chl < Dg;
     const int64_t ch = cg + (live ? c0 + chl : 0);
-    const int nv = live ? ssm_states(a.N, ng) : 0;
-    float A2[4], h[4] = {0.f, 0.f, 0.f, 0.f};
-    param_load<4>(A2, a.A + ch * a.N + 4 * ng, nv);
+    const int nv = live ? states_valid<NS>(a.N, n0) : 0;
+    float A2[NS], h[NS];
+    param_load<NS>(A2, a.A + ch * a.N + n0, nv);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) A2[j] *= kLog2e;
-    const int64_t so = (b * a.D + ch) * a.N + 4 * ng;
+    for (int j = 0; j < NS; ++j) {
+        A2[j] *= kLog2e;
+        h[j] = 0.f;
+    }
+    const int64_t so = (b * a.D + ch) * a.N + n0;
     // hend[b][0] is h0 as the first pass copied it (the second pass must not
     // read h0: another workgroup may be writing h_final, the same buffer),
     // hend[b][s] the end of segment s - 1, segment 0 started from h0
     if (!OUT || nseg == 1) {
-        if (a.h0 && seg == 0) state_load(h, a.h0 + so, nv);
+        if (a.h0 && seg == 0) states_load<NS>(h, a.h0 + so, nv);
         if constexpr (!OUT)
-            if (seg == 0) state_store(a.hend + (b * nseg * a.D + ch) * a.N + 4 * ng, h, nv);
+            if (seg == 0) states_store<NS>(a.hend + (b * nseg * a.D + ch) * a.N + n0, h, nv);
     } else {
-        state_load(h, a.hend + ((b * nseg + (seg > 0)) * a.D + ch) * a.N + 4 * ng, nv);
+        states_load<NS>(h, a.hend + ((b * nseg + (seg > 0)) * a.D + ch) * a.N + n0, nv);
         for (int64_t s = 1; s < seg; ++s) {
             const int64_t o = (b * nseg + s) * a.D + ch;
-            float e[4];
-            state_load(e, a.hend + (o + a.D) * a.N + 4 * ng, nv);
+            float e[NS];
+            states_load<NS>(e, a.hend + (o + a.D) * a.N + n0, nv);
             const float sd = live ? a.sdelta[o] : 0.f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < NS; ++j)
                 h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(A2[j] * sd), h[j], e[j]);
         }
     }
@@ -87,135 +105,129 @@ __global__ __launch_bounds__(256) void ssm_fwd_kernel(SsmArgs a, int64_t nblk, i
     const int sv = ssm_left(Dg, c0 + sc, EPT);
     const int64_t scg = cg + c0 + sc;
     float bias[EPT], skip[EPT];
-#pragma unroll
-    for (int e = 0; e < EPT; ++e) {
-        bias[e] = a.bias && e < sv ? a.bias[scg + e] : 0.f;
-        skip[e] = OUT && a.D_skip && e < sv ? a.D_skip[scg + e] : 0.f;
-    }
-    RawRow<EPT> rx, rt, rz;
-    RawRow<4> rq[QPT];
+    param_load<EPT>(bias, a.bias + scg, a.bias ? sv : 0);
+    param_load<EPT>(skip, a.D_skip + scg, OUT && a.D_skip ? sv : 0);
+    Row<EPT, BF16, RAG> rx, rt, rz;
+    Row<4, BF16, RAG> rq[QPT];
     auto fetch = [&](int64_t tb) {
         const int64_t t = tb + srow;
         const int v = t < t1 ? sv : 0;
-        row_load<EPT>(rx, a.x, v ? b * a.xb + t * a.xt + scg : 0, a.in_bf16, v);
-        row_load<EPT>(rt, a.dt, v ? b * a.dtb + t * a.dtt + scg : 0, a.in_bf16, v);
-        if (OUT && a.z) row_load<EPT>(rz, a.z, v ? b * a.zb + t * a.zt + scg : 0, a.in_bf16, v);
+        rx.load(a.x, b * a.xb + t * a.xt + scg, v);
+        rt.load(a.dt, b * a.dtb + t * a.dtt + scg, v);
+        if constexpr (OUT) rz.load(a.z, b * a.zb + t * a.zt + scg, a.z ? v : 0);
 #pragma unroll
         for (int i = 0; i < QPT; ++i) {
             const int q = tid + 256 * i;
             const bool isc = q >= NQ;
             if (isc && !OUT) continue;
-            const int qt = (q % NQ) / LPC, qn = q % LPC;
+            const int qt = (q % NQ) / (NP / 4), qn = q % (NP / 4);
             const int64_t tq = tb + qt;
-            const int vq = q < 2 * NQ && tq < t1 ? ssm_states(a.N, qn) : 0;
-            row_load<4>(rq[i], isc ? a.Cm : a.Bm,
-                        vq ? (isc ? b * a.cb + tq * a.ct : b * a.bb + tq * a.bt) + g * a.N + 4 * qn
-                           : 0,
-                        a.in_bf16, vq);
+            const int vq = q < 2 * NQ && tq < t1 ? states_valid<4>(a.N, 4 * qn) : 0;
+            rq[i].load(isc ? a.Cm : a.Bm,
+                       (isc ? b * a.cb + tq * a.ct : b * a.bb + tq * a.bt) + g * a.N + 4 * qn, vq);
         }
     };
     fetch(t0);
     float sumd = 0.f;
     for (int64_t tb = t0; tb < t1; tb += TT) {
         const int64_t t = tb + srow;
-        const bool tok = t < t1;
+        // a token past the end or a channel past the group moves nothing: its
+        // decay is exp(0) and it adds 0
+        const int tv = t < t1 ? sv : 0;
         float x[EPT], z[EPT];
-        row_unpack<EPT>(x, rx, a.in_bf16);
-        if (OUT && a.z) row_unpack<EPT>(z, rz, a.in_bf16);
+        rx.unpack(x);
+        if constexpr (OUT) rz.unpack(z);
         {
             float r[EPT];
-            row_unpack<EPT>(r, rt, a.in_bf16);
+            rt.unpack(r);
 #pragma unroll
             for (int e = 0; e < EPT; ++e) {
-                // a token past the end or a channel past the group moves nothing:
-                // its decay is exp(0) and it adds 0
                 float d = ssm_delta(r[e] + bias[e], a.softplus);
-                d = tok && e < sv ? d : 0.f;
+                d = e < tv ? d : 0.f;
                 dd[srow][sc + e] = float2{d, d * x[e]};
             }
         }
 #pragma unroll
         for (int i = 0; i < QPT; ++i) {
             const int q = tid + 256 * i;
-            const bool isc = q >= NQ;
-            if (q >= 2 * NQ || (isc && !OUT)) continue;
+            if (q >= 2 * NQ || (q >= NQ && !OUT)) continue;
             float f[4];
-            row_unpack<4>(f, rq[i], a.in_bf16);
-            bc[(q % NQ) / LPC][isc][q % LPC] = float4{f[0], f[1], f[2], f[3]};
+            rq[i].unpack(f);
+            *reinterpret_cast<float4*>(&bc[q >= NQ][4 * (q % NQ)]) = float4{f[0], f[1], f[2], f[3]};
         }
         __syncthreads();
         if (tb + TT < t1) fetch(tb + TT);
         const int nt = t1 - tb < TT ? (int)(t1 - tb) : TT;
         for (int tt = 0; tt < nt; tt += 4) {
-            float s[4];
+            float s[4], Bq[4 / KT], Cq[4 / KT];
+            float2 d[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float2 d = dd[tt + k][chl];
-                const float4 B4 = bc[tt + k][0][ng];
-                const float Bv[4] = {B4.x, B4.y, B4.z, B4.w};
+            for (int k = 0; k < 4; ++k) d[k] = dd[tt + k][chl];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(d.x * A2[j]), h[j], d.y * Bv[j]);
-                if constexpr (OUT) {
-                    const float4 C4 = bc[tt + k][1][ng];
-                    s[k] = __builtin_fmaf(C4.w, h[3], __builtin_fmaf(C4.z, h[2],
-                                          __builtin_fmaf(C4.y, h[1], C4.x * h[0])));
-                } else {
-                    sumd += d.x;
-                }
+            for (int k = 0; k < 4 / KT; ++k) {
+                Bq[k] = row_coef<NS, NG>(bc[0], tt + k * KT, lane);
+                Cq[k] = OUT ? row_coef<NS, NG>(bc[1], tt + k * KT, lane) : 0.f;
             }
-            if constexpr (OUT) channel_sums<LPC>(s, ng, &ys[tt][chl], YP);
+            constexpr auto js = std::make_index_sequence<NS>{};
+            s[0] = scan_token<NS, 0 % KT, OUT>(h, A2, d[0].x, d[0].y, Bq[0 / KT], Cq[0 / KT], js);
+            s[1] = scan_token<NS, 1 % KT, OUT>(h, A2, d[1].x, d[1].y, Bq[1 / KT], Cq[1 / KT], js);
+            s[2] = scan_token<NS, 2 % KT, OUT>(h, A2, d[2].x, d[2].y, Bq[2 / KT], Cq[2 / KT], js);
+            s[3] = scan_token<NS, 3 % KT, OUT>(h, A2, d[3].x, d[3].y, Bq[3 / KT], Cq[3 / KT], js);
+            if constexpr (OUT)
+                state_sums<NG>(s, row, &ys[tt][chl], YP);
+            else
+                sumd += (d[0].x + d[1].x) + (d[2].x + d[3].x);
         }
         __syncthreads();
         if constexpr (OUT) {
-            if (tok && sv > 0) {
+            if (tv > 0) {
                 float y[EPT];
 #pragma unroll
                 for (int e = 0; e < EPT; ++e) {
                     y[e] = __builtin_fmaf(skip[e], x[e], ys[srow][sc + e]);
-                    if (a.z) y[e] *= z[e] * sigmoid(z[e]);
+                    if (a.z) y[e] *= z[e] * sigmoid_fast(z[e]);
                 }
-                row_store<EPT>(a.y, (b * a.T + t) * a.D + scg, a.out_bf16, y, sv);
+                row_store<EPT>(a.y, (b * a.T + t) * a.D + scg, a.out_bf16, y, tv);
             }
         }
     }
     if constexpr (OUT) {
-        if (a.h_final && seg == nseg - 1) state_store(a.h_final + so, h, nv);
+        if (a.h_final && seg == nseg - 1) states_store<NS>(a.h_final + so, h, nv);
     } else {
         const int64_t o = (b * nseg + seg) * a.D + ch;
-        state_store(a.hend + (o + a.D) * a.N + 4 * ng, h, nv);
-        if (live && ng == 0) a.sdelta[o] = sumd;
+        states_store<NS>(a.hend + (o + a.D) * a.N + n0, h, nv);
+        if (live && n0 == 0) a.sdelta[o] = sumd;
     }
 }
 
 // One decode token: every lane streams its 4 states once; bound by the
 // state's HBM traffic (8 bytes per state against ~6 operations).
-template <int LPC>
+template <int LPC, bool BF16>
 __global__ __launch_bounds__(256) void ssm_step_kernel(SsmArgs a) {
     const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int ng = (int)(id % LPC);
     const int64_t bc = id / LPC;
     const bool live = bc < a.B * a.D;
     const int64_t b = live ? bc / a.D : 0, ch = live ? bc % a.D : 0;
-    const int nv = live ? ssm_states(a.N, ng) : 0;
-    float h[4], A4[4], B4[4], C4[4];
+    const int nv = live ? states_valid<4>(a.N, 4 * ng) : 0;
+    float h[4], A4[4], B4[4], C4[4], x[1], r[1], z[1];
     const int64_t so = (b * a.D + ch) * a.N + 4 * ng;
-    state_load(h, a.h0 + so, nv);
+    states_load<4>(h, a.h0 + so, nv);
     param_load<4>(A4, a.A + ch * a.N + 4 * ng, nv);
     const int64_t g = ch / (a.D / a.G);
-    RawRow<4> rb, rc;
-    RawRow<1> rx, rt, rz;
-    row_load<4>(rb, a.Bm, b * a.bb + g * a.N + 4 * ng, a.in_bf16, nv);
-    row_load<4>(rc, a.Cm, b * a.cb + g * a.N + 4 * ng, a.in_bf16, nv);
-    row_load<1>(rx, a.x, b * a.xb + ch, a.in_bf16, live);
-    row_load<1>(rt, a.dt, b * a.dtb + ch, a.in_bf16, live);
-    if (a.z) row_load<1>(rz, a.z, b * a.zb + ch, a.in_bf16, live);
-    float x[1], r[1], z[1];
-    row_unpack<1>(x, rx, a.in_bf16);
-    row_unpack<1>(r, rt, a.in_bf16);
-    row_unpack<4>(B4, rb, a.in_bf16);
-    row_unpack<4>(C4, rc, a.in_bf16);
-    const float d = ssm_delta(r[0] + (a.bias ? a.bias[ch] : 0.f), a.softplus);
+    Row<4, BF16, true> rb, rc;
+    Row<1, BF16, false> rx, rt, rz;
+    rb.load(a.Bm, b * a.bb + g * a.N + 4 * ng, nv);
+    rc.load(a.Cm, b * a.cb + g * a.N + 4 * ng, nv);
+    rx.load(a.x, b * a.xb + ch, live);
+    rt.load(a.dt, b * a.dtb + ch, live);
+    rz.load(a.z, b * a.zb + ch, live && a.z);
+    const float bias = a.bias ? a.bias[ch] : 0.f, skip = a.D_skip ? a.D_skip[ch] : 0.f;
+    rx.unpack(x);
+    rt.unpack(r);
+    rb.unpack(B4);
+    rc.unpack(C4);
+    const float d = ssm_delta(r[0] + bias, a.softplus);
     const float dx = d * x[0];
     float s = 0.f;
 #pragma unroll
@@ -223,16 +235,16 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(SsmArgs a) {
         h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(d * (A4[j] * kLog2e)), h[j], dx * B4[j]);
         s = __builtin_fmaf(C4[j], h[j], s);
     }
-    state_store(a.h_final + so, h, nv);
+    states_store<4>(a.h_final + so, h, nv);
     if constexpr (LPC >= 2) s += xor_lane<1>(s);
     if constexpr (LPC >= 4) s += xor_lane<2>(s);
     if constexpr (LPC >= 8) s += xor_lane<4>(s);
     if constexpr (LPC >= 16) s += xor_lane<8>(s);
     if (live && ng == 0) {
-        float y[1] = {a.D_skip ? __builtin_fmaf(a.D_skip[ch], x[0], s) : s};
+        float y[1] = {__builtin_fmaf(skip, x[0], s)};
         if (a.z) {
-            row_unpack<1>(z, rz, a.in_bf16);
-            y[0] *= z[0] * sigmoid(z[0]);
+            rz.unpack(z);
+            y[0] *= z[0] * sigmoid_fast(z[0]);
         }
         row_store<1>(a.y, b * a.D + ch, a.out_bf16, y, 1);
     }
@@ -240,24 +252,38 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(SsmArgs a) {
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-template <int LPC>
-hipError_t launch_fwd_t(const SsmArgs& a, const SsmPlan& p) {
+template <int NS, int NG, bool BF16, bool RAG>
+hipError_t launch_fwd_r(const SsmArgs& a, const SsmPlan& p) {
+    const int64_t wgs = a.B * a.G * p.nblk;
     if (p.nseg > 1) {
-        hipLaunchKernelGGL((ssm_fwd_kernel<LPC, false>),
-                           dim3((unsigned)(a.B * a.G * p.nblk * (p.nseg - 1))), dim3(256), 0,
-                           a.stream, a, p.nblk, p.nseg, p.L);
+        hipLaunchKernelGGL((ssm_fwd_kernel<NS, NG, false, BF16, RAG>),
+                           dim3((unsigned)(wgs * (p.nseg - 1))), dim3(256), 0, a.stream, a, p.nblk,
+                           p.nseg, p.L);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((ssm_fwd_kernel<LPC, true>), dim3((unsigned)(a.B * a.G * p.nblk * p.nseg)),
+    hipLaunchKernelGGL((ssm_fwd_kernel<NS, NG, true, BF16, RAG>), dim3((unsigned)(wgs * p.nseg)),
                        dim3(256), 0, a.stream, a, p.nblk, p.nseg, p.L);
     return hipGetLastError();
 }
 
+template <int NS, int NG>
+hipError_t launch_fwd_t(const SsmArgs& a, const SsmPlan& p) {
+    const bool rag = (a.D / a.G) % 8 != 0 || a.N % 4 != 0;
+    if (a.in_bf16)
+        return rag ? launch_fwd_r<NS, NG, true, true>(a, p)
+                   : launch_fwd_r<NS, NG, true, false>(a, p);
+    return rag ? launch_fwd_r<NS, NG, false, true>(a, p)
+               : launch_fwd_r<NS, NG, false, false>(a, p);
+}
+
 template <int LPC>
 hipError_t launch_step_t(const SsmArgs& a) {
-    hipLaunchKernelGGL((ssm_step_kernel<LPC>), dim3((unsigned)cdiv(a.B * a.D * LPC, 256)),
-                       dim3(256), 0, a.stream, a);
+    const dim3 grid((unsigned)cdiv(a.B * a.D * LPC, 256));
+    if (a.in_bf16)
+        hipLaunchKernelGGL((ssm_step_kernel<LPC, true>), grid, dim3(256), 0, a.stream, a);
+    else
+        hipLaunchKernelGGL((ssm_step_kernel<LPC, false>), grid, dim3(256), 0, a.stream, a);
     return hipGetLastError();
 }
 
@@ -269,13 +295,16 @@ int ssm_lanes(int64_t N) {
     return l;
 }
 
+// Channels of a workgroup of the sequence kernels: 16 lanes of 4 waves, times
+// the channels that rows hold side by side when N is small.
+int64_t ssm_wg_channels(int64_t N) { return N <= 4 ? 256 : N <= 8 ? 128 : 64; }
+
 // Segments of the forward.  One when the channels fill the chip: 768 waves,
 // three quarters of one per SIMD.  Below that enough segments for two waves
 // per SIMD, of at least 64 tokens.
 SsmPlan ssm_fwd_plan(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N) {
     SsmPlan p;
-    p.lpc = ssm_lanes(N);
-    p.nblk = cdiv(D / G, 256 / p.lpc);
+    p.nblk = cdiv(D / G, ssm_wg_channels(N));
     const int64_t waves = 4 * B * G * p.nblk;
     int64_t n = 1;
     if (waves < 768) n = cdiv(2048, waves);
@@ -298,13 +327,11 @@ hipError_t launch_ssm_fwd(SsmArgs a, float* ws) {
     const SsmPlan p = ssm_fwd_plan(a.B, a.T, a.D, a.G, a.N);
     a.hend = ws;
     a.sdelta = ws ? ws + a.B * p.nseg * a.D * a.N : nullptr;
-    switch (p.lpc) {
-        case 1: return launch_fwd_t<1>(a, p);
-        case 2: return launch_fwd_t<2>(a, p);
-        case 4: return launch_fwd_t<4>(a, p);
-        case 8: return launch_fwd_t<8>(a, p);
-        default: return launch_fwd_t<16>(a, p);
-    }
+    if (a.N <= 4) return launch_fwd_t<4, 1>(a, p);
+    if (a.N <= 8) return launch_fwd_t<4, 2>(a, p);
+    if (a.N <= 16) return launch_fwd_t<4, 4>(a, p);
+    if (a.N <= 32) return launch_fwd_t<8, 4>(a, p);
+    return launch_fwd_t<16, 4>(a, p);
 }
 
 hipError_t launch_ssm_step(const SsmArgs& a) {
