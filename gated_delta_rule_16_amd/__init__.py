@@ -37,6 +37,7 @@ GDR_L2NORM_QK: q and k are L2-normalised on load inside the kernels.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch  # loads the HIP runtime libgdr.so binds to
@@ -727,7 +728,10 @@ def gdr2_chunk_bwd_split(q, k, v, alpha, erase, write, s0, dout, ds_final=None, 
 
 
 def _like(name, t, dtype, shape, device):
-    """A tensor of this type and shape on ``device`` whose channels are contiguous."""
+    """A tensor of this type and shape on ``device``."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and
+            t.device == device):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -743,7 +747,10 @@ def _like(name, t, dtype, shape, device):
 def _row_strides(name, t, lead):
     """Element strides of the ``lead`` leading dimensions; the others must be
     contiguous."""
-    shape, st = t.shape, t.stride()
+    st = t.stride()
+    if t.is_contiguous():
+        return st[:lead]
+    shape = t.shape
     want = 1
     for i in range(len(shape) - 1, lead - 1, -1):
         if shape[i] != 1 and st[i] != want and t.numel():
@@ -758,29 +765,27 @@ def _whole(name, t, dtype, shape, device):
         raise ValueError(f"{name} must be contiguous")
 
 
-class _On:
-    """The tensors' device and the call's stream while a call allocates and launches."""
+_raw_stream = torch._C._cuda_getCurrentRawStream     # a stream handle with no Stream object around it
 
-    def __init__(self, device, stream):
-        self.ptr = stream.cuda_stream if stream is not None else None
-        self.device = device
-        if stream is not None and stream.device != device:
-            raise ValueError(f"stream must be on {device}, got {stream.device}")
-        self.ctx = None
-        if stream is not None:
-            self.ctx = torch.cuda.stream(stream)       # also makes its device current
-        elif device.index != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(device)
 
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        if self.ptr is None:
-            self.ptr = torch.cuda.current_stream(self.device).cuda_stream
-        return self
-
-    def __exit__(self, *exc):
-        return self.ctx.__exit__(*exc) if self.ctx is not None else None
+def _on_own_device(fn):
+    """Runs ``fn`` with its first tensor's device current, and with ``stream``
+    (default: that device's current stream) as the current stream, so that
+    what it allocates belongs there too."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        x = args[0] if args else kw.get("x")
+        if isinstance(x, torch.Tensor) and x.is_cuda:
+            if stream is not None:
+                if stream.device != x.device:
+                    raise ValueError(f"stream must be on {x.device}, got {stream.device}")
+                with torch.cuda.stream(stream):
+                    return fn(*args, **kw)
+            if x.get_device() != torch._C._cuda_getDevice():
+                with torch.cuda.device(x.device):
+                    return fn(*args, **kw)
+        return fn(*args, **kw)
+    return call
 
 
 def _first(name, t, dims):
@@ -826,6 +831,7 @@ def _i64s(*v):
     return (ctypes.c_int64 * len(v))(*v)
 
 
+@_on_own_device
 def gdr_short_conv_fwd(x, w, bias=None, s0=None, *, silu=True, out_dtype=None, y=None,
                        s_final=None, want_state=True, stream=None):
     """Short causal depthwise convolution (with SiLU) over whole sequences.
@@ -847,16 +853,16 @@ def gdr_short_conv_fwd(x, w, bias=None, s0=None, *, silu=True, out_dtype=None, y
         _whole("s0", s0, x.dtype, (B, K - 1, C), dev)
     odt = out_dtype or (x.dtype if y is None else y.dtype)
     code = _dt_of("output dtype", odt)
-    with _On(dev, stream) as on:
-        y = _buffer("y", y, odt, (B, T, C), dev)
-        if s_final is not None or want_state:
-            s_final = _buffer("s_final", s_final, x.dtype, (B, max(K - 1, 0), C), dev)
-        _run("gdr_short_conv_fwd", lib.gdr_short_conv_fwd(
-            B, T, C, K, _DT[x.dtype], _p(x), _i64s(*xs), _p(w), _p(bias), _p(s0),
-            GDR_CONV_SILU if silu else 0, code, _p(y), _p(s_final), on.ptr))
+    y = _buffer("y", y, odt, (B, T, C), dev)
+    if s_final is not None or want_state:
+        s_final = _buffer("s_final", s_final, x.dtype, (B, max(K - 1, 0), C), dev)
+    _run("gdr_short_conv_fwd", lib.gdr_short_conv_fwd(
+        B, T, C, K, _DT[x.dtype], _p(x), _i64s(*xs), _p(w), _p(bias), _p(s0),
+        GDR_CONV_SILU if silu else 0, code, _p(y), _p(s_final), _raw_stream(dev.index)))
     return y, s_final
 
 
+@_on_own_device
 def gdr_short_conv_step(x, w, bias, state, *, silu=True, out_dtype=None, y=None, stream=None):
     """One decode token of gdr_short_conv_fwd: x [N,C], state [N,K-1,C] in x's
     dtype, moved on in place.  Returns y [N,C]."""
@@ -872,11 +878,10 @@ def gdr_short_conv_step(x, w, bias, state, *, silu=True, out_dtype=None, y=None,
     _whole("state", state, x.dtype, (N, K - 1, C), dev)
     odt = out_dtype or (x.dtype if y is None else y.dtype)
     code = _dt_of("output dtype", odt)
-    with _On(dev, stream) as on:
-        y = _buffer("y", y, odt, (N, C), dev)
-        _run("gdr_short_conv_step", lib.gdr_short_conv_step(
-            N, C, K, _DT[x.dtype], _p(x), xs[0], _p(w), _p(bias), _p(state),
-            GDR_CONV_SILU if silu else 0, code, _p(y), on.ptr))
+    y = _buffer("y", y, odt, (N, C), dev)
+    _run("gdr_short_conv_step", lib.gdr_short_conv_step(
+        N, C, K, _DT[x.dtype], _p(x), xs[0], _p(w), _p(bias), _p(state),
+        GDR_CONV_SILU if silu else 0, code, _p(y), _raw_stream(dev.index)))
     return y
 
 
@@ -885,6 +890,7 @@ def gdr_short_conv_bwd_workspace_size(B, T, C, K) -> int:
     return int(lib.gdr_short_conv_bwd_workspace_size(B, T, C, K))
 
 
+@_on_own_device
 def gdr_short_conv_bwd(x, w, bias, s0, dy, ds_final=None, *, silu=True,
                        grad_dtype=torch.float32, want_dw=True, want_ds0=True, workspace=None,
                        stream=None):
@@ -910,19 +916,18 @@ def gdr_short_conv_bwd(x, w, bias, s0, dy, ds_final=None, *, silu=True,
     if ds_final is not None:
         _whole("ds_final", ds_final, torch.float32, (B, K - 1, C), dev)
     code = _dt_of("grad_dtype", grad_dtype)
-    with _On(dev, stream) as on:
-        f32 = dict(dtype=torch.float32, device=dev)
-        dx = torch.empty((B, T, C), dtype=grad_dtype, device=dev)
-        dw = torch.empty((C, K), **f32) if want_dw else None
-        db = torch.empty((C,), **f32) if want_dw and bias is not None else None
-        ds0 = torch.empty((B, max(K - 1, 0), C), **f32) if want_ds0 else None
-        if want_dw or workspace is not None:
-            workspace = _scratch(workspace, gdr_short_conv_bwd_workspace_size(B, T, C, K), dev)
-        _run("gdr_short_conv_bwd", lib.gdr_short_conv_bwd(
-            B, T, C, K, _DT[x.dtype], _p(x), _p(w), _p(bias), _p(s0), _DT[dy.dtype], _p(dy),
-            _i64s(*xs, *ys), _p(ds_final), GDR_CONV_SILU if silu else 0, code, _p(dx), _p(dw),
-            _p(db), _p(ds0), _p(workspace), 0 if workspace is None else workspace.numel(),
-            on.ptr))
+    f32 = dict(dtype=torch.float32, device=dev)
+    dx = torch.empty((B, T, C), dtype=grad_dtype, device=dev)
+    dw = torch.empty((C, K), **f32) if want_dw else None
+    db = torch.empty((C,), **f32) if want_dw and bias is not None else None
+    ds0 = torch.empty((B, max(K - 1, 0), C), **f32) if want_ds0 else None
+    if want_dw or workspace is not None:
+        workspace = _scratch(workspace, gdr_short_conv_bwd_workspace_size(B, T, C, K), dev)
+    _run("gdr_short_conv_bwd", lib.gdr_short_conv_bwd(
+        B, T, C, K, _DT[x.dtype], _p(x), _p(w), _p(bias), _p(s0), _DT[dy.dtype], _p(dy),
+        _i64s(*xs, *ys), _p(ds_final), GDR_CONV_SILU if silu else 0, code, _p(dx), _p(dw),
+        _p(db), _p(ds0), _p(workspace), 0 if workspace is None else workspace.numel(),
+        _raw_stream(dev.index)))
     return dx, dw, db, ds0
 
 
@@ -958,6 +963,7 @@ def gdr_ssm_scan_fwd_workspace_size(B, T, D, G, N) -> int:
     return int(lib.gdr_ssm_scan_fwd_workspace_size(B, T, D, G, N))
 
 
+@_on_own_device
 def gdr_ssm_scan_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, h0=None, *, softplus=True,
                      out_dtype=None, y=None, h_final=None, want_state=True, workspace=None,
                      stream=None):
@@ -975,19 +981,19 @@ def gdr_ssm_scan_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, h0=None, *,
     odt = out_dtype or (x.dtype if y is None else y.dtype)
     code = _dt_of("output dtype", odt)
     need = gdr_ssm_scan_fwd_workspace_size(B, T, Dn, G, N)
-    with _On(dev, stream) as on:
-        y = _buffer("y", y, odt, (B, T, Dn), dev)
-        if h_final is not None or want_state:
-            h_final = _buffer("h_final", h_final, torch.float32, (B, Dn, N), dev)
-        if need or workspace is not None:
-            workspace = _scratch(workspace, need, dev)
-        _run("gdr_ssm_scan_fwd", lib.gdr_ssm_scan_fwd(
-            B, T, Dn, G, N, _DT[x.dtype], _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(z),
-            _p(dt_bias), _p(h0), _i64s(*st), GDR_SSM_SOFTPLUS if softplus else 0, code, _p(y),
-            _p(h_final), _p(workspace), 0 if workspace is None else workspace.numel(), on.ptr))
+    y = _buffer("y", y, odt, (B, T, Dn), dev)
+    if h_final is not None or want_state:
+        h_final = _buffer("h_final", h_final, torch.float32, (B, Dn, N), dev)
+    if need or workspace is not None:
+        workspace = _scratch(workspace, need, dev)
+    _run("gdr_ssm_scan_fwd", lib.gdr_ssm_scan_fwd(
+        B, T, Dn, G, N, _DT[x.dtype], _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(z),
+        _p(dt_bias), _p(h0), _i64s(*st), GDR_SSM_SOFTPLUS if softplus else 0, code, _p(y),
+        _p(h_final), _p(workspace), 0 if workspace is None else workspace.numel(), _raw_stream(dev.index)))
     return y, h_final
 
 
+@_on_own_device
 def gdr_ssm_step(x, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, *, softplus=True,
                  out_dtype=None, y=None, stream=None):
     """One decode token of gdr_ssm_scan_fwd: x, dt, z [N,D], Bm, Cm [N,G,S] for
@@ -997,12 +1003,11 @@ def gdr_ssm_step(x, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, *, softp
     _whole("state", state, torch.float32, (Nq, Dn, N), dev)
     odt = out_dtype or (x.dtype if y is None else y.dtype)
     code = _dt_of("output dtype", odt)
-    with _On(dev, stream) as on:
-        y = _buffer("y", y, odt, (Nq, Dn), dev)
-        _run("gdr_ssm_step", lib.gdr_ssm_step(
-            Nq, Dn, G, N, _DT[x.dtype], _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(z),
-            _p(dt_bias), _p(state), _i64s(*st), GDR_SSM_SOFTPLUS if softplus else 0, code, _p(y),
-            on.ptr))
+    y = _buffer("y", y, odt, (Nq, Dn), dev)
+    _run("gdr_ssm_step", lib.gdr_ssm_step(
+        Nq, Dn, G, N, _DT[x.dtype], _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(z),
+        _p(dt_bias), _p(state), _i64s(*st), GDR_SSM_SOFTPLUS if softplus else 0, code, _p(y),
+        _raw_stream(dev.index)))
     return y
 
 
@@ -1011,6 +1016,7 @@ def gdr_ssm_scan_bwd_workspace_size(B, T, D, G, N) -> int:
     return int(lib.gdr_ssm_scan_bwd_workspace_size(B, T, D, G, N))
 
 
+@_on_own_device
 def gdr_ssm_scan_bwd(x, dt, A, Bm, Cm, D, z, dt_bias, h0, dout, dh_final=None, *, softplus=True,
                      grad_dtype=torch.float32, want_dh0=True, workspace=None, stream=None):
     """Reverse mode of gdr_ssm_scan_fwd for dL/dy = ``dout`` [B,T,D] (fp32 or
@@ -1027,22 +1033,21 @@ def gdr_ssm_scan_bwd(x, dt, A, Bm, Cm, D, z, dt_bias, h0, dout, dh_final=None, *
     if dh_final is not None:
         _whole("dh_final", dh_final, torch.float32, (B, Dn, N), dev)
     code = _dt_of("grad_dtype", grad_dtype)
-    with _On(dev, stream) as on:
-        f32 = dict(dtype=torch.float32, device=dev)
-        act = dict(dtype=grad_dtype, device=dev)
-        dx, ddt = torch.empty((B, T, Dn), **act), torch.empty((B, T, Dn), **act)
-        dB, dC = torch.empty((B, T, G, N), **act), torch.empty((B, T, G, N), **act)
-        dz = None if z is None else torch.empty((B, T, Dn), **act)
-        dA = torch.empty((Dn, N), **f32)
-        dD = None if D is None else torch.empty((Dn,), **f32)
-        db = None if dt_bias is None else torch.empty((Dn,), **f32)
-        dh0 = torch.empty((B, Dn, N), **f32) if want_dh0 else None
-        workspace = _scratch(workspace, gdr_ssm_scan_bwd_workspace_size(B, T, Dn, G, N), dev)
-        _run("gdr_ssm_scan_bwd", lib.gdr_ssm_scan_bwd(
-            B, T, Dn, G, N, _DT[x.dtype], _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(z),
-            _p(dt_bias), _p(h0), _DT[dout.dtype], _p(dout), _p(dh_final), _i64s(*st),
-            GDR_SSM_SOFTPLUS if softplus else 0, code, _p(dx), _p(ddt), _p(dA), _p(dB), _p(dC),
-            _p(dD), _p(dz), _p(db), _p(dh0), _p(workspace), workspace.numel(), on.ptr))
+    f32 = dict(dtype=torch.float32, device=dev)
+    act = dict(dtype=grad_dtype, device=dev)
+    dx, ddt = torch.empty((B, T, Dn), **act), torch.empty((B, T, Dn), **act)
+    dB, dC = torch.empty((B, T, G, N), **act), torch.empty((B, T, G, N), **act)
+    dz = None if z is None else torch.empty((B, T, Dn), **act)
+    dA = torch.empty((Dn, N), **f32)
+    dD = None if D is None else torch.empty((Dn,), **f32)
+    db = None if dt_bias is None else torch.empty((Dn,), **f32)
+    dh0 = torch.empty((B, Dn, N), **f32) if want_dh0 else None
+    workspace = _scratch(workspace, gdr_ssm_scan_bwd_workspace_size(B, T, Dn, G, N), dev)
+    _run("gdr_ssm_scan_bwd", lib.gdr_ssm_scan_bwd(
+        B, T, Dn, G, N, _DT[x.dtype], _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(z),
+        _p(dt_bias), _p(h0), _DT[dout.dtype], _p(dout), _p(dh_final), _i64s(*st),
+        GDR_SSM_SOFTPLUS if softplus else 0, code, _p(dx), _p(ddt), _p(dA), _p(dB), _p(dC),
+        _p(dD), _p(dz), _p(db), _p(dh0), _p(workspace), workspace.numel(), _raw_stream(dev.index)))
     return dx, ddt, dA, dB, dC, dD, dz, db, dh0
 
 
@@ -1064,6 +1069,7 @@ def _as_rows(name, t):
     return v.shape[0], C, v.stride(0)
 
 
+@_on_own_device
 def gdr_layer_norm_fwd(x, w=None, b=None, eps=1e-5, *, residual=None, out_dtype=None, y=None,
                        h=None, stream=None):
     """Layer norm over the last axis of x [..., C] (fp32 or bf16), after adding
@@ -1088,13 +1094,12 @@ def gdr_layer_norm_fwd(x, w=None, b=None, eps=1e-5, *, residual=None, out_dtype=
         _whole("b", b, torch.float32, (C,), dev)
     odt = out_dtype or (x.dtype if y is None else y.dtype)
     code = _dt_of("output dtype", odt)
-    with _On(dev, stream) as on:
-        y = _buffer("y", y, odt, x.shape, dev)
-        if residual is not None:
-            h = _buffer("h", h, rdt, x.shape, dev)
-        _run("gdr_layer_norm_fwd", lib.gdr_layer_norm_fwd(
-            R, C, _DT[x.dtype], _p(x), xr, _DT[rdt], _p(residual), rr, _p(w), _p(b), float(eps),
-            code, _p(y), _p(h), on.ptr))
+    y = _buffer("y", y, odt, x.shape, dev)
+    if residual is not None:
+        h = _buffer("h", h, rdt, x.shape, dev)
+    _run("gdr_layer_norm_fwd", lib.gdr_layer_norm_fwd(
+        R, C, _DT[x.dtype], _p(x), xr, _DT[rdt], _p(residual), rr, _p(w), _p(b), float(eps),
+        code, _p(y), _p(h), _raw_stream(dev.index)))
     return y if residual is None else (y, h)
 
 
@@ -1103,6 +1108,7 @@ def gdr_layer_norm_bwd_workspace_size(R, C) -> int:
     return int(lib.gdr_layer_norm_bwd_workspace_size(R, C))
 
 
+@_on_own_device
 def gdr_layer_norm_bwd(x, w, dy, eps=1e-5, *, dres=None, grad_dtype=torch.float32, want_dw=True,
                        workspace=None, stream=None):
     """Reverse mode of gdr_layer_norm_fwd: x [..., C] is the normalised tensor
@@ -1123,14 +1129,13 @@ def gdr_layer_norm_bwd(x, w, dy, eps=1e-5, *, dres=None, grad_dtype=torch.float3
         rr = _as_rows("dres", dres)[2]
     if w is not None:
         _whole("w", w, torch.float32, (C,), dev)
-    with _On(dev, stream) as on:
-        dx = torch.empty(x.shape, dtype=grad_dtype, device=dev)
-        f32 = dict(dtype=torch.float32, device=dev)
-        dw, db = (torch.empty((C,), **f32), torch.empty((C,), **f32)) if want_dw else (None, None)
-        if want_dw or workspace is not None:
-            workspace = _scratch(workspace, gdr_layer_norm_bwd_workspace_size(R, C), dev)
-        _run("gdr_layer_norm_bwd", lib.gdr_layer_norm_bwd(
-            R, C, _DT[x.dtype], _p(x), xr, _p(w), _DT[dy.dtype], _p(dy), yr, float(eps), code,
-            _p(dres), rr, _p(dx), _p(dw), _p(db), _p(workspace),
-            0 if workspace is None else workspace.numel(), on.ptr))
+    dx = torch.empty(x.shape, dtype=grad_dtype, device=dev)
+    f32 = dict(dtype=torch.float32, device=dev)
+    dw, db = (torch.empty((C,), **f32), torch.empty((C,), **f32)) if want_dw else (None, None)
+    if want_dw or workspace is not None:
+        workspace = _scratch(workspace, gdr_layer_norm_bwd_workspace_size(R, C), dev)
+    _run("gdr_layer_norm_bwd", lib.gdr_layer_norm_bwd(
+        R, C, _DT[x.dtype], _p(x), xr, _p(w), _DT[dy.dtype], _p(dy), yr, float(eps), code,
+        _p(dres), rr, _p(dx), _p(dw), _p(db), _p(workspace),
+        0 if workspace is None else workspace.numel(), _raw_stream(dev.index)))
     return dx, dw, db

@@ -69,7 +69,7 @@ template <bool BF16, int RES, bool RAG> struct SumIn {
                 h[e] += q[e];
                 if constexpr (RES == 1) h[e] = bf2f(f2bf(h[e]));
             }
-            row_store<E>(a.h, ho, RES == 1, h, valid);
+            row_store<E, RAG>(a.h, ho, RES == 1, h, valid);
         }
     }
 };
@@ -126,7 +126,7 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormArgs a) {
             if (a.b) y += b[e];
             h[k][e] = y;
         }
-        row_store<E>(a.y, row * a.C + c, a.out_bf16, h[k], v);
+        row_store<E, RAG>(a.y, row * a.C + c, a.out_bf16, h[k], v);
     }
 }
 
@@ -258,7 +258,7 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwdArgs a) {
                 out[e] = rstd * (dn - m1 - n * m2);
                 out[e] += q[e];
             }
-            row_store<E>(a.dx, row * a.C + c, G16, out, v);
+            row_store<E, RAG>(a.dx, row * a.C + c, G16, out, v);
         }
     }
     if (!a.part) return;
@@ -290,8 +290,8 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwdArgs a) {
             }
         }
         const int v = left(a.C, c);
-        row_store<E>(part, c, false, dw[k], v);
-        row_store<E>(part, a.C + c, false, db[k], v);
+        row_store<E, RAG>(part, c, false, dw[k], v);
+        row_store<E, RAG>(part, a.C + c, false, db[k], v);
     }
 }
 

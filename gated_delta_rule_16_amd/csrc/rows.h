@@ -94,35 +94,45 @@ template <int E, bool BF16, bool RAG> struct Row {
     }
 };
 
-// Stores channels [0, valid) of the E (bf16: round to nearest even).
-template <int E>
+// Stores channels [0, valid) of the E (bf16: round to nearest even).  Without
+// RAG valid is 0 or E.
+template <int E, bool RAG = true>
 __device__ __forceinline__ void row_store(void* base, int64_t off, bool bf16, const float (&f)[E],
                                           int valid) {
-    if (bf16) {
-        bf16_t* p = static_cast<bf16_t*>(base) + off;
-        if (valid >= E) {
-            if constexpr (E == 8) {
+    if (valid >= E) {
+        if (bf16) {
+            bf16_t* p = static_cast<bf16_t*>(base) + off;
+            if constexpr (E == 8)
                 *reinterpret_cast<u32x4_e2*>(p) = u32x4_e2{cvt_pk(f[0], f[1]), cvt_pk(f[2], f[3]),
                                                            cvt_pk(f[4], f[5]), cvt_pk(f[6], f[7])};
-            } else if constexpr (E == 4) {
+            else if constexpr (E == 4)
                 *reinterpret_cast<u32x2_e2*>(p) = u32x2_e2{cvt_pk(f[0], f[1]), cvt_pk(f[2], f[3])};
-            } else if constexpr (E == 2) {
+            else if constexpr (E == 2)
                 *reinterpret_cast<u32_e2*>(p) = cvt_pk(f[0], f[1]);
-            } else {
+            else
                 *p = f2bf(f[0]);
-            }
         } else {
+            float* p = static_cast<float*>(base) + off;
+            if constexpr (E >= 4) {
+#pragma unroll
+                for (int i = 0; i < E; i += 4)
+                    *reinterpret_cast<f32x4_e4*>(p + i) =
+                        f32x4_e4{f[i], f[i + 1], f[i + 2], f[i + 3]};
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; ++e) p[e] = f[e];
+            }
+        }
+        return;
+    }
+    if constexpr (RAG) {
+        if (bf16) {
+            bf16_t* p = static_cast<bf16_t*>(base) + off;
 #pragma unroll
             for (int e = 0; e < E; ++e)
                 if (e < valid) p[e] = f2bf(f[e]);
-        }
-    } else {
-        float* p = static_cast<float*>(base) + off;
-        if (E >= 4 && valid >= E) {
-#pragma unroll
-            for (int i = 0; i + 3 < E; i += 4)
-                *reinterpret_cast<f32x4_e4*>(p + i) = f32x4_e4{f[i], f[i + 1], f[i + 2], f[i + 3]};
         } else {
+            float* p = static_cast<float*>(base) + off;
 #pragma unroll
             for (int e = 0; e < E; ++e)
                 if (e < valid) p[e] = f[e];
@@ -140,6 +150,17 @@ __device__ __forceinline__ void param_load(float (&f)[M], const float* p, int va
             const f32x4_e4 v = *reinterpret_cast<const f32x4_e4*>(p + i);
             f[i] = v.x; f[i + 1] = v.y; f[i + 2] = v.z; f[i + 3] = v.w;
         }
+    } else {
+#pragma unroll
+        for (int i = 0; i < M; ++i) f[i] = i < valid ? p[i] : 0.f;
+    }
+}
+
+// The same for any M.
+template <int M>
+__device__ __forceinline__ void small_load(float (&f)[M], const float* p, int valid) {
+    if constexpr (M % 4 == 0) {
+        param_load<M>(f, p, valid);
     } else {
 #pragma unroll
         for (int i = 0; i < M; ++i) f[i] = i < valid ? p[i] : 0.f;

@@ -71,7 +71,7 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int64_t ncb, 
             for (int m = 0; m < K - 1; ++m) {
                 float v[E];
                 f[m].unpack(v);
-                row_store<E>(a.s_final, (b * (K - 1) + m) * a.C + c, BF16, v, valid);
+                row_store<E, RAG>(a.s_final, (b * (K - 1) + m) * a.C + c, BF16, v, valid);
             }
         }
     }
@@ -95,7 +95,7 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int64_t ncb, 
                 for (int j = 0; j + 1 < K - 1; ++j) win[j][e] = win[j + 1][e];
                 win[K - 2][e] = x[e];
             }
-            if (t + u < t1) row_store<E>(a.y, (b * a.T + t + u) * a.C + c, a.out_bf16, y, valid);
+            if (t + u < t1) row_store<E, RAG>(a.y, (b * a.T + t + u) * a.C + c, a.out_bf16, y, valid);
         }
     }
 }
@@ -236,9 +236,9 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int64_t ncb, 
                             if (e < valid) out[e] += p[e];
                     }
                     if (i >= 0)
-                        row_store<BE>(a.dx, (b * a.T + i) * a.C + c, a.grad_bf16, out, valid);
+                        row_store<BE, RAG>(a.dx, (b * a.T + i) * a.C + c, a.grad_bf16, out, valid);
                     else if (a.ds0)
-                        row_store<BE>(a.ds0, (b * (K - 1) + i + K - 1) * a.C + c, false, out,
+                        row_store<BE, RAG>(a.ds0, (b * (K - 1) + i + K - 1) * a.C + c, false, out,
                                       valid);
                 }
             }

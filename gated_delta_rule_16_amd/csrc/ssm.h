@@ -12,6 +12,8 @@
 // States n >= N have A = B = C = 0 and stay 0.
 #pragma once
 
+#include <utility>
+
 #include "launch.h"
 #include "rows.h"
 
@@ -65,10 +67,82 @@ __device__ __forceinline__ float row_bcast(float x) {
                                          0, __builtin_bit_cast(int, x), 0x150 + I, 0xF, 0xF, true));
 }
 
+// Fused adds with a row broadcast as their DPP operand, which the compiler does
+// not form from a broadcast and an fma, 4 per block.  The wait states between
+// a vector write of C and its DPP read are kept inside each block; state_sums
+// keeps its own before it swaps what a block wrote.
+//
+// h0 .. h3 += C[I .. I + 3] x0 .. x3.
+template <int I>
+__device__ __forceinline__ void row_fma4(float& h0, float& h1, float& h2, float& h3, float C,
+                                         float x0, float x1, float x2, float x3) {
+    asm("s_nop 1\n\t"
+        "v_fmac_f32_dpp %0, %4, %5 row_newbcast:%c9 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %1, %4, %6 row_newbcast:%c10 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %2, %4, %7 row_newbcast:%c11 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %3, %4, %8 row_newbcast:%c12 row_mask:0xf bank_mask:0xf"
+        : "+&v"(h0), "+&v"(h1), "+&v"(h2), "+&v"(h3)
+        : "v"(C), "v"(x0), "v"(x1), "v"(x2), "v"(x3), "n"(I), "n"(I + 1), "n"(I + 2),
+          "n"(I + 3));
+}
+// s (+)= C[I .. I + 3] . (x0 .. x3).
+template <int I, bool FIRST>
+__device__ __forceinline__ void row_dot4(float& s, float C, float x0, float x1, float x2, float x3) {
+    if constexpr (FIRST)
+        asm("s_nop 1\n\t"
+            "v_mul_f32_dpp %0, %1, %2 row_newbcast:%c6 row_mask:0xf bank_mask:0xf\n\t"
+            "v_fmac_f32_dpp %0, %1, %3 row_newbcast:%c7 row_mask:0xf bank_mask:0xf\n\t"
+            "v_fmac_f32_dpp %0, %1, %4 row_newbcast:%c8 row_mask:0xf bank_mask:0xf\n\t"
+            "v_fmac_f32_dpp %0, %1, %5 row_newbcast:%c9 row_mask:0xf bank_mask:0xf"
+            : "=&v"(s)
+            : "v"(C), "v"(x0), "v"(x1), "v"(x2), "v"(x3), "n"(I), "n"(I + 1), "n"(I + 2),
+              "n"(I + 3));
+    else
+        asm("s_nop 1\n\t"
+            "v_fmac_f32_dpp %0, %1, %2 row_newbcast:%c6 row_mask:0xf bank_mask:0xf\n\t"
+            "v_fmac_f32_dpp %0, %1, %3 row_newbcast:%c7 row_mask:0xf bank_mask:0xf\n\t"
+            "v_fmac_f32_dpp %0, %1, %4 row_newbcast:%c8 row_mask:0xf bank_mask:0xf\n\t"
+            "v_fmac_f32_dpp %0, %1, %5 row_newbcast:%c9 row_mask:0xf bank_mask:0xf"
+            : "+&v"(s)
+            : "v"(C), "v"(x0), "v"(x1), "v"(x2), "v"(x3), "n"(I), "n"(I + 1), "n"(I + 2),
+              "n"(I + 3));
+}
+
+// h[j] += C[j] x[j] of one token whose C starts at lane I, j from Q on.
+template <int NS, int I, int Q = 0>
+__device__ __forceinline__ void row_fma_each(float (&h)[NS], float C, const float (&x)[NS]) {
+    row_fma4<I + Q>(h[Q], h[Q + 1], h[Q + 2], h[Q + 3], C, x[Q], x[Q + 1], x[Q + 2], x[Q + 3]);
+    if constexpr (Q + 4 < NS) row_fma_each<NS, I, Q + 4>(h, C, x);
+}
+// h[j] += C[j] x.
+template <int NS, int I, int Q = 0>
+__device__ __forceinline__ void row_fma(float (&h)[NS], float C, float x) {
+    row_fma4<I + Q>(h[Q], h[Q + 1], h[Q + 2], h[Q + 3], C, x, x, x, x);
+    if constexpr (Q + 4 < NS) row_fma<NS, I, Q + 4>(h, C, x);
+}
+// sum_j C[j] h[j].
+template <int NS, int I, int Q = 0>
+__device__ __forceinline__ float row_dot(float C, const float (&h)[NS], float s = 0.f) {
+    row_dot4<I + Q, Q == 0>(s, C, h[Q], h[Q + 1], h[Q + 2], h[Q + 3]);
+    if constexpr (Q + 4 < NS) s = row_dot<NS, I, Q + 4>(C, h, s);
+    return s;
+}
+
+// The decays and additions of one token: K is its place in the register Bq.
+template <int NS, int K, size_t... J>
+__device__ __forceinline__ void scan_terms(float (&ea)[NS], float (&bx)[NS], const float (&A2)[NS],
+                                           float d, float dx, float Bq,
+                                           std::index_sequence<J...>) {
+    ((ea[J] = __builtin_amdgcn_exp2f(d * A2[J])), ...);
+    ((bx[J] = row_bcast<K * NS + J>(Bq) * dx), ...);
+}
+
 // Sums s[k] (token k of 4) over the rows of each channel and stores them at
 // dst[k * pitch].  row = lane / 16.
 template <int NG>
-__device__ __forceinline__ void state_sums(const float (&s)[4], int row, float* dst, int pitch) {
+__device__ __forceinline__ void state_sums(float (&s)[4], int row, float* dst, int pitch) {
+    // the sums may come from asm, whose writes the swaps must not follow at once
+    if constexpr (NG > 1) asm("s_nop 1" : "+v"(s[0]), "+v"(s[1]), "+v"(s[2]), "+v"(s[3]));
     if constexpr (NG == 1) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) dst[k * pitch] = s[k];
@@ -110,8 +184,25 @@ __device__ __forceinline__ void states_store(float* p, const float (&h)[NS], int
     }
 }
 
-// The step Delta of a token and channel.
+// The step Delta of a token and channel, and of E channels (one branch for
+// all, so their chains interleave).
 __device__ __forceinline__ float ssm_delta(float raw, bool sp) { return sp ? softplus(raw) : raw; }
+template <int E>
+__device__ __forceinline__ void ssm_deltas(float (&d)[E], const float (&raw)[E], bool sp) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) d[e] = raw[e];
+    if (sp) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) d[e] = softplus(d[e]);
+    }
+}
+
+// v[e] times z[e] sigmoid(z[e]).
+template <int E>
+__device__ __forceinline__ void ssm_gate(float (&v)[E], const float (&z)[E]) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] *= z[e] * sigmoid_fast(z[e]);
+}
 
 // Valid states of a lane that starts at state n0.
 template <int NS>

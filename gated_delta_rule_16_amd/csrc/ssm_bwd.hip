@@ -7,8 +7,8 @@
 //   dx_t = Delta_t sum_n g_t B_t + D dy_t,       dA = sum_t p_t Delta_t,
 //   dDelta_t = x_t sum_n g_t B_t + sum_n p_t A,  dz_t = dout_t y_t (z sigmoid(z))',
 //
-// Two passes.  The first runs the state forward and keeps it every S = 64 / NS
-// tokens (16 at N <= 16: 8 bytes of traffic per state and 16 tokens).  The
+// Two passes.  The first runs the state forward and keeps it every S tokens
+// (block_tokens; 16 at N = 16: 8 bytes of traffic per state and 16 tokens).  The
 // second goes backwards over blocks of S tokens: it runs a block's states
 // again from the kept one, leaving h_t and a_t of all S tokens in registers
 // (128 of them), then walks the block backwards.  Lanes are laid out as in
@@ -23,30 +23,17 @@
 // segment alone sends to its start, sum_t (prod a) C_t dy_t, from running
 // products; the second composes a segment's true start state and end
 // gradient from those and adds exp(A sum Delta) h_in to each kept state.
-#include <utility>
-
 #include "ssm.h"
 
 namespace gdr {
 
 namespace {
 
-// Tokens per block of the second pass: 64 / NS, and at most 8 elements to
-// stage per thread.
-template <int NS, int NG> constexpr int block_tokens() { return NG == 1 ? 8 : 64 / NS; }
-
-// One token forwards: h and, for the segment's own gradient, P and gam.
-template <int NS, int K, bool GAM, size_t... J>
-__device__ __forceinline__ void states_token(float (&h)[NS], float (&P)[NS], float (&gam)[NS],
-                                             const float (&A2)[NS], float d, float dx, float dy,
-                                             float Bq, float Cq, std::index_sequence<J...>) {
-    float aa[NS];
-    ((aa[J] = __builtin_amdgcn_exp2f(d * A2[J])), ...);
-    ((h[J] = __builtin_fmaf(aa[J], h[J], row_bcast<K * NS + J>(Bq) * dx)), ...);
-    if constexpr (GAM)
-        ((P[J] *= aa[J],
-          gam[J] = __builtin_fmaf(P[J], row_bcast<K * NS + J>(Cq) * dy, gam[J])), ...);
-}
+// Tokens per block of the second pass, and between kept states: what fills
+// 128 registers with h and a, but fewer where few states per channel leave a
+// workgroup many channels to stage (4 per thread; the kept states are then 4
+// bytes per channel and token as at N = 16).
+template <int NS, int NG> constexpr int block_tokens() { return NG < 4 ? 4 * NG : 64 / NS; }
 
 // First pass.  GAM: more than one segment.
 template <int NS, int NG, bool GAM, bool BF16, bool RAG>
@@ -129,11 +116,14 @@ __global__ __launch_bounds__(256) void ssm_bwd_states_kernel(SsmBwdArgs a, int64
         float x[EPT], r[EPT];
         rx.unpack(x);
         rt.unpack(r);
+        float d8[EPT];
+#pragma unroll
+        for (int e = 0; e < EPT; ++e) r[e] += bias[e];
+        ssm_deltas(d8, r, a.softplus);
 #pragma unroll
         for (int e = 0; e < EPT; ++e) {
-            float d = ssm_delta(r[e] + bias[e], a.softplus);
-            d = e < tv ? d : 0.f;
-            dd[srow][sc + e] = float2{d, d * x[e]};
+            d8[e] = e < tv ? d8[e] : 0.f;
+            dd[srow][sc + e] = float2{d8[e], d8[e] * x[e]};
         }
         if constexpr (GAM) {
             float o[EPT], z[EPT];
@@ -142,11 +132,9 @@ __global__ __launch_bounds__(256) void ssm_bwd_states_kernel(SsmBwdArgs a, int64
             else
                 ro32.unpack(o);
             rz.unpack(z);
+            if (a.z) ssm_gate(o, z);
 #pragma unroll
-            for (int e = 0; e < EPT; ++e) {
-                if (a.z) o[e] *= z[e] * sigmoid_fast(z[e]);
-                ds[srow][sc + e] = o[e];
-            }
+            for (int e = 0; e < EPT; ++e) ds[srow][sc + e] = o[e];
         }
 #pragma unroll
         for (int i = 0; i < QPT; ++i) {
@@ -178,13 +166,34 @@ __global__ __launch_bounds__(256) void ssm_bwd_states_kernel(SsmBwdArgs a, int64
                 Cq[k] = GAM ? row_coef<NS, NG>(bc[1], tt + k * KT, lane) : 0.f;
             }
             constexpr auto js = std::make_index_sequence<NS>{};
-#define TOKEN(k) \
-    states_token<NS, k % KT, GAM>(h, P, gam, A2, d[k].x, d[k].y, dy[k], Bq[k / KT], Cq[k / KT], js)
+            float ea[4][NS], bx[4][NS];
+#define TOKEN(k) scan_terms<NS, k % KT>(ea[k], bx[k], A2, d[k].x, d[k].y, Bq[k / KT], js)
             TOKEN(0);
             TOKEN(1);
             TOKEN(2);
             TOKEN(3);
 #undef TOKEN
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+#pragma unroll
+                for (int j = 0; j < NS; ++j) h[j] = __builtin_fmaf(ea[k][j], h[j], bx[k][j]);
+            }
+            if constexpr (GAM) {
+                // gam += P C dy: P in place of the decays, then the products
+                // with dy, then C by broadcast
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+#pragma unroll
+                    for (int j = 0; j < NS; ++j) {
+                        P[j] *= ea[k][j];
+                        ea[k][j] = P[j] * dy[k];
+                    }
+                }
+                row_fma_each<NS, NS * (0 % KT)>(gam, Cq[0 / KT], ea[0]);
+                row_fma_each<NS, NS * (1 % KT)>(gam, Cq[1 / KT], ea[1]);
+                row_fma_each<NS, NS * (2 % KT)>(gam, Cq[2 / KT], ea[2]);
+                row_fma_each<NS, NS * (3 % KT)>(gam, Cq[3 / KT], ea[3]);
+            }
             if constexpr (GAM) sumd += (d[0].x + d[1].x) + (d[2].x + d[3].x);
         }
         __syncthreads();
@@ -197,35 +206,29 @@ __global__ __launch_bounds__(256) void ssm_bwd_states_kernel(SsmBwdArgs a, int64
     }
 }
 
-// A token of the second pass, forwards: a_t and h_t from h_{t-1}; returns the
-// lane's part of y.
-template <int NS, int K, size_t... J>
-__device__ __forceinline__ float fore_token(float (&aa)[NS], float (&hh)[NS],
-                                            const float (&hp)[NS], const float (&A2)[NS], float d,
-                                            float dx, float Bq, float Cq, bool y,
-                                            std::index_sequence<J...>) {
-    ((aa[J] = __builtin_amdgcn_exp2f(d * A2[J])), ...);
-    ((hh[J] = __builtin_fmaf(aa[J], hp[J], row_bcast<K * NS + J>(Bq) * dx)), ...);
-    float s = 0.f;
-    if (y) ((s = __builtin_fmaf(row_bcast<K * NS + J>(Cq), hh[J], s)), ...);
-    return s;
-}
-
-// And backwards: gr enters as a_{t+1} g_{t+1} and leaves as a_t g_t.
-template <int NS, int K, size_t... J>
+// A token of the second pass, backwards: gr enters as a_{t+1} g_{t+1} and
+// leaves as a_t g_t; I is the token's place in Bq and Cq.
+template <int NS, int I>
 __device__ __forceinline__ void back_token(float (&gr)[NS], float (&dA)[NS], float (&pv)[2 * NS],
                                            float& sB, float& sA, const float (&aa)[NS],
                                            const float (&hh)[NS], const float (&hp)[NS],
                                            const float (&A2)[NS], float d, float dx, float dy,
-                                           float Bq, float Cq, std::index_sequence<J...>) {
-    ((gr[J] = __builtin_fmaf(row_bcast<K * NS + J>(Cq), dy, gr[J])), ...);
-    ((pv[J] = hh[J] * dy, pv[NS + J] = gr[J] * dx), ...);
-    sB = 0.f;
-    ((sB = __builtin_fmaf(row_bcast<K * NS + J>(Bq), gr[J], sB)), ...);
-    float u[NS];
-    ((gr[J] *= aa[J], u[J] = gr[J] * hp[J]), ...);
+                                           float Bq, float Cq) {
+    row_fma<NS, I>(gr, Cq, dy);
+#pragma unroll
+    for (int j = 0; j < NS; ++j) {
+        pv[j] = hh[j] * dy;
+        pv[NS + j] = gr[j] * dx;
+    }
+    sB = row_dot<NS, I>(Bq, gr);
     sA = 0.f;
-    ((sA = __builtin_fmaf(u[J], A2[J], sA), dA[J] = __builtin_fmaf(u[J], d, dA[J])), ...);
+#pragma unroll
+    for (int j = 0; j < NS; ++j) {
+        gr[j] *= aa[j];
+        const float u = gr[j] * hp[j];
+        sA = j == 0 ? u * A2[j] : __builtin_fmaf(u, A2[j], sA);
+        dA[j] = __builtin_fmaf(u, d, dA[j]);
+    }
 }
 
 // Halving reduction of M values over the 16 lanes of each row, then (NG < 4)
@@ -256,7 +259,7 @@ __device__ __forceinline__ void channel_sums(float (&v)[M], int lane) {
 
 // Second pass.
 template <int NS, int NG, bool BF16, bool RAG>
-__global__ __launch_bounds__(256, 2) void ssm_bwd_kernel(SsmBwdArgs a, int64_t nblk, int64_t nseg,
+__global__ __launch_bounds__(256, NS == 16 ? 1 : 2) void ssm_bwd_kernel(SsmBwdArgs a, int64_t nblk, int64_t nseg,
                                                          int64_t L) {
     constexpr int NP = NS * NG, CW = 64 / NG, WC = 4 * CW;
     constexpr int S = block_tokens<NS, NG>();
@@ -372,13 +375,19 @@ __global__ __launch_bounds__(256, 2) void ssm_bwd_kernel(SsmBwdArgs a, int64_t n
             else
                 ro32.unpack(o);
             rz.unpack(z);
+            float bias[EPT], d[EPT], dy[EPT];
+            small_load<EPT>(bias, a.bias + scg, a.bias ? sv : 0);
 #pragma unroll
             for (int e = 0; e < EPT; ++e) {
-                r[e] += a.bias && e < sv ? a.bias[scg + e] : 0.f;
-                float d = ssm_delta(r[e], a.softplus);
-                d = e < v ? d : 0.f;
-                const float dy = a.z ? o[e] * (z[e] * sigmoid_fast(z[e])) : o[e];
-                st[srow][sc + e] = f32x4{d, d * x[e], dy, 0.f};
+                r[e] += bias[e];
+                dy[e] = o[e];
+            }
+            ssm_deltas(d, r, a.softplus);
+            if (a.z) ssm_gate(dy, z);
+#pragma unroll
+            for (int e = 0; e < EPT; ++e) {
+                d[e] = e < v ? d[e] : 0.f;
+                st[srow][sc + e] = f32x4{d[e], d[e] * x[e], dy[e], 0.f};
                 raw[srow][sc + e] = f32x4{x[e], r[e], o[e], z[e]};
             }
         }
@@ -391,7 +400,6 @@ __global__ __launch_bounds__(256, 2) void ssm_bwd_kernel(SsmBwdArgs a, int64_t n
             *reinterpret_cast<float4*>(&bc[q >= NQ][4 * (q % NQ)]) = float4{f[0], f[1], f[2], f[3]};
         }
         __syncthreads();
-        if (sub > first) fetch(sub - 1);
 
         // the block's states again, all kept in registers
         constexpr auto js = std::make_index_sequence<NS>{};
@@ -404,26 +412,35 @@ __global__ __launch_bounds__(256, 2) void ssm_bwd_kernel(SsmBwdArgs a, int64_t n
                 Bq[k] = row_coef<NS, NG>(bc[0], tt + k * KT, lane);
                 Cq[k] = row_coef<NS, NG>(bc[1], tt + k * KT, lane);
             }
-#define TOKEN(k)                                                                               \
-    {                                                                                          \
-        const f32x4 d = st[tt + k][chl];                                                       \
-        s[k] = fore_token<NS, k % KT>(aa[tt + k], hh[tt + k],                                  \
-                                      tt + k == 0 ? hs : hh[tt + k == 0 ? 0 : tt + k - 1], A2, \
-                                      d[0], d[1], Bq[k / KT], Cq[k / KT], a.z, js);            \
-    }
-            TOKEN(0)
-            TOKEN(1)
-            TOKEN(2)
-            TOKEN(3)
+            f32x4 d[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) d[k] = st[tt + k][chl];
+#define TOKEN(k) scan_terms<NS, k % KT>(aa[tt + k], hh[tt + k], A2, d[k][0], d[k][1], Bq[k / KT], js)
+            TOKEN(0);
+            TOKEN(1);
+            TOKEN(2);
+            TOKEN(3);
 #undef TOKEN
-            if (a.z) state_sums<NG>(s, row, reinterpret_cast<float*>(&st[tt][chl]) + 3, 4 * WC);
+#pragma unroll
+            for (int k = tt; k < tt + 4; ++k) {
+#pragma unroll
+                for (int j = 0; j < NS; ++j)
+                    hh[k][j] = __builtin_fmaf(aa[k][j], k ? hh[k ? k - 1 : 0][j] : hs[j], hh[k][j]);
+            }
+            if (a.z) {
+                s[0] = row_dot<NS, NS * (0 % KT)>(Cq[0 / KT], hh[tt]);
+                s[1] = row_dot<NS, NS * (1 % KT)>(Cq[1 / KT], hh[tt + 1]);
+                s[2] = row_dot<NS, NS * (2 % KT)>(Cq[2 / KT], hh[tt + 2]);
+                s[3] = row_dot<NS, NS * (3 % KT)>(Cq[3 / KT], hh[tt + 3]);
+                state_sums<NG>(s, row, reinterpret_cast<float*>(&st[tt][chl]) + 3, 4 * WC);
+            }
         }
         // and backwards
-        float dAl[NS];
-#pragma unroll
-        for (int j = 0; j < NS; ++j) dAl[j] = 0.f;
 #pragma unroll
         for (int tt = S - 4; tt >= 0; tt -= 4) {
+            // half of the kept states are done with: the next block's loads
+            // take their registers
+            if (tt == (S / 2 - 4 > 0 ? S / 2 - 4 : 0) && sub > first) fetch(sub - 1);
             float sB[4], sA[4], Bq[4 / KT], Cq[4 / KT];
 #pragma unroll
             for (int k = 0; k < 4 / KT; ++k) {
@@ -434,9 +451,9 @@ __global__ __launch_bounds__(256, 2) void ssm_bwd_kernel(SsmBwdArgs a, int64_t n
     {                                                                                           \
         const f32x4 d = st[tt + k][chl];                                                        \
         float pv[2 * NS];                                                                       \
-        back_token<NS, k % KT>(gr, dAl, pv, sB[k], sA[k], aa[tt + k], hh[tt + k],               \
-                               tt + k == 0 ? hs : hh[tt + k == 0 ? 0 : tt + k - 1], A2, d[0],   \
-                               d[1], d[2], Bq[k / KT], Cq[k / KT], js);                         \
+        back_token<NS, NS*(k % KT)>(gr, dA, pv, sB[k], sA[k], aa[tt + k], hh[tt + k],           \
+                                    tt + k == 0 ? hs : hh[tt + k == 0 ? 0 : tt + k - 1], A2,    \
+                                    d[0], d[1], d[2], Bq[k / KT], Cq[k / KT]);                  \
         channel_sums<2 * NS, NG>(pv, lane);                                                     \
         store_sums(pv, tt + k);                                                                 \
     }
@@ -461,38 +478,49 @@ __global__ __launch_bounds__(256, 2) void ssm_bwd_kernel(SsmBwdArgs a, int64_t n
             state_sums<NG>(sB, row, sp, 4 * WC);
             state_sums<NG>(sA, row, sp + 1, 4 * WC);
         }
-#pragma unroll
-        for (int j = 0; j < NS; ++j) dA[j] += dAl[j];
         __syncthreads();
 
         if (v > 0) {
-            float dxv[EPT], dtv[EPT], dzv[EPT];
+            float dxv[EPT], dtv[EPT], dzv[EPT], d[EPT], r[EPT], dy[EPT], skip[EPT];
+            f32x4 q[EPT], in[EPT];
+            small_load<EPT>(skip, a.D_skip + scg, a.D_skip ? sv : 0);
 #pragma unroll
             for (int e = 0; e < EPT; ++e) {
-                const f32x4 q = st[srow][sc + e], in = raw[srow][sc + e];
-                const float x = in[0], r = in[1], o = in[2], z = in[3];
-                const float skip = a.D_skip && e < sv ? a.D_skip[scg + e] : 0.f;
-                const float d = ssm_delta(r, a.softplus);
-                float dy = o;
-                if (a.z) {
-                    const float sg = sigmoid_fast(z);
-                    const float y = __builtin_fmaf(skip, x, q[3]);
-                    dy *= z * sg;
-                    dzv[e] = o * y * sg * __builtin_fmaf(z, 1.f - sg, 1.f);
+                q[e] = st[srow][sc + e];
+                in[e] = raw[srow][sc + e];
+                r[e] = in[e][1];
+                dy[e] = in[e][2];
+            }
+            ssm_deltas(d, r, a.softplus);
+            if (a.z) {
+#pragma unroll
+                for (int e = 0; e < EPT; ++e) {
+                    const float z = in[e][3], sg = sigmoid_fast(z);
+                    const float y = __builtin_fmaf(skip[e], in[e][0], q[e][3]);
+                    dzv[e] = dy[e] * y * sg * __builtin_fmaf(z, 1.f - sg, 1.f);
+                    dy[e] *= z * sg;
                 }
-                dxv[e] = __builtin_fmaf(d, q[0], skip * dy);
-                float dr = __builtin_fmaf(x, q[0], q[1] * kLn2);
-                if (a.softplus) dr *= sigmoid(r);
-                dtv[e] = dr;
+            }
+#pragma unroll
+            for (int e = 0; e < EPT; ++e) {
+                dxv[e] = __builtin_fmaf(d[e], q[e][0], skip[e] * dy[e]);
+                dtv[e] = __builtin_fmaf(in[e][0], q[e][0], q[e][1] * kLn2);
+            }
+            if (a.softplus) {
+#pragma unroll
+                for (int e = 0; e < EPT; ++e) dtv[e] *= sigmoid(r[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < EPT; ++e) {
                 if (e < v) {
-                    dD[e] = __builtin_fmaf(dy, x, dD[e]);
-                    dbias[e] += dr;
+                    dD[e] = __builtin_fmaf(dy[e], in[e][0], dD[e]);
+                    dbias[e] += dtv[e];
                 }
             }
             const int64_t oo = (b * a.T + t) * a.D + scg;
-            row_store<EPT>(a.dx, oo, a.grad_bf16, dxv, v);
-            row_store<EPT>(a.ddt, oo, a.grad_bf16, dtv, v);
-            if (a.z) row_store<EPT>(a.dz, oo, a.grad_bf16, dzv, v);
+            row_store<EPT, RAG>(a.dx, oo, a.grad_bf16, dxv, v);
+            row_store<EPT, RAG>(a.ddt, oo, a.grad_bf16, dtv, v);
+            if (a.z) row_store<EPT, RAG>(a.dz, oo, a.grad_bf16, dzv, v);
         }
         for (int i = tid; i < S * 2 * NP; i += 256) {
             const int q = i / (2 * NP), k = i % (2 * NP);
@@ -561,7 +589,7 @@ SsmPlan bwd_plan(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N) {
 }
 
 // Tokens between kept states, for N states.
-int64_t kept_tokens(int64_t N) { return N <= 4 ? 8 : N <= 16 ? 16 : N <= 32 ? 8 : 4; }
+int64_t kept_tokens(int64_t N) { return N <= 4 ? 4 : N <= 8 ? 8 : N <= 16 ? 16 : N <= 32 ? 8 : 4; }
 
 struct BwdLayout {
     size_t ckpt, csum, hend, gstart, sdelta, part, bcpart, total;

@@ -20,25 +20,11 @@
 // Delta (whose exp with A is the segment's decay); the second starts from the
 // states composed of those.  It costs a second exp per state, so it is taken
 // only where the channels alone leave most of the chip idle (ssm_fwd_segs).
-#include <utility>
-
 #include "ssm.h"
 
 namespace gdr {
 
 namespace {
-
-// One token of the lane's states: K is its place in the registers Bq, Cq.
-template <int NS, int K, bool OUT, size_t... J>
-__device__ __forceinline__ float scan_token(float (&h)[NS], const float (&A2)[NS], float d, float dx,
-                                            float Bq, float Cq, std::index_sequence<J...>) {
-    ((h[J] = __builtin_fmaf(__builtin_amdgcn_exp2f(d * A2[J]), h[J],
-                            row_bcast<K * NS + J>(Bq) * dx)),
-     ...);
-    float s = 0.f;
-    if constexpr (OUT) ((s = __builtin_fmaf(row_bcast<K * NS + J>(Cq), h[J], s)), ...);
-    return s;
-}
 
 template <int NS, int NG, bool OUT, bool BF16, bool RAG>
 __global__ __launch_bounds__(256) void ssm_fwd_kernel(SsmArgs a, int64_t nblk, int64_t nseg,
@@ -138,13 +124,15 @@ __global__ __launch_bounds__(256) void ssm_fwd_kernel(SsmArgs a, int64_t nblk, i
         rx.unpack(x);
         if constexpr (OUT) rz.unpack(z);
         {
-            float r[EPT];
+            float r[EPT], d[EPT];
             rt.unpack(r);
 #pragma unroll
+            for (int e = 0; e < EPT; ++e) r[e] += bias[e];
+            ssm_deltas(d, r, a.softplus);
+#pragma unroll
             for (int e = 0; e < EPT; ++e) {
-                float d = ssm_delta(r[e] + bias[e], a.softplus);
-                d = e < tv ? d : 0.f;
-                dd[srow][sc + e] = float2{d, d * x[e]};
+                d[e] = e < tv ? d[e] : 0.f;
+                dd[srow][sc + e] = float2{d[e], d[e] * x[e]};
             }
         }
 #pragma unroll
@@ -158,6 +146,7 @@ __global__ __launch_bounds__(256) void ssm_fwd_kernel(SsmArgs a, int64_t nblk, i
         __syncthreads();
         if (tb + TT < t1) fetch(tb + TT);
         const int nt = t1 - tb < TT ? (int)(t1 - tb) : TT;
+        constexpr auto js = std::make_index_sequence<NS>{};
         for (int tt = 0; tt < nt; tt += 4) {
             float s[4], Bq[4 / KT], Cq[4 / KT];
             float2 d[4];
@@ -168,26 +157,38 @@ __global__ __launch_bounds__(256) void ssm_fwd_kernel(SsmArgs a, int64_t nblk, i
                 Bq[k] = row_coef<NS, NG>(bc[0], tt + k * KT, lane);
                 Cq[k] = OUT ? row_coef<NS, NG>(bc[1], tt + k * KT, lane) : 0.f;
             }
-            constexpr auto js = std::make_index_sequence<NS>{};
-            s[0] = scan_token<NS, 0 % KT, OUT>(h, A2, d[0].x, d[0].y, Bq[0 / KT], Cq[0 / KT], js);
-            s[1] = scan_token<NS, 1 % KT, OUT>(h, A2, d[1].x, d[1].y, Bq[1 / KT], Cq[1 / KT], js);
-            s[2] = scan_token<NS, 2 % KT, OUT>(h, A2, d[2].x, d[2].y, Bq[2 / KT], Cq[2 / KT], js);
-            s[3] = scan_token<NS, 3 % KT, OUT>(h, A2, d[3].x, d[3].y, Bq[3 / KT], Cq[3 / KT], js);
-            if constexpr (OUT)
+            float ea[4][NS], bx[4][NS];
+            scan_terms<NS, 0 % KT>(ea[0], bx[0], A2, d[0].x, d[0].y, Bq[0 / KT], js);
+            scan_terms<NS, 1 % KT>(ea[1], bx[1], A2, d[1].x, d[1].y, Bq[1 / KT], js);
+            scan_terms<NS, 2 % KT>(ea[2], bx[2], A2, d[2].x, d[2].y, Bq[2 / KT], js);
+            scan_terms<NS, 3 % KT>(ea[3], bx[3], A2, d[3].x, d[3].y, Bq[3 / KT], js);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+#pragma unroll
+                for (int j = 0; j < NS; ++j)
+                    bx[k][j] = __builtin_fmaf(ea[k][j], k ? bx[k ? k - 1 : 0][j] : h[j], bx[k][j]);
+            }
+            if constexpr (OUT) {
+                s[0] = row_dot<NS, NS * (0 % KT)>(Cq[0 / KT], bx[0]);
+                s[1] = row_dot<NS, NS * (1 % KT)>(Cq[1 / KT], bx[1]);
+                s[2] = row_dot<NS, NS * (2 % KT)>(Cq[2 / KT], bx[2]);
+                s[3] = row_dot<NS, NS * (3 % KT)>(Cq[3 / KT], bx[3]);
                 state_sums<NG>(s, row, &ys[tt][chl], YP);
-            else
+            } else {
                 sumd += (d[0].x + d[1].x) + (d[2].x + d[3].x);
+            }
+#pragma unroll
+            for (int j = 0; j < NS; ++j) h[j] = bx[3][j];
         }
         __syncthreads();
         if constexpr (OUT) {
             if (tv > 0) {
                 float y[EPT];
 #pragma unroll
-                for (int e = 0; e < EPT; ++e) {
+                for (int e = 0; e < EPT; ++e)
                     y[e] = __builtin_fmaf(skip[e], x[e], ys[srow][sc + e]);
-                    if (a.z) y[e] *= z[e] * sigmoid_fast(z[e]);
-                }
-                row_store<EPT>(a.y, (b * a.T + t) * a.D + scg, a.out_bf16, y, tv);
+                if (a.z) ssm_gate(y, z);
+                row_store<EPT, RAG>(a.y, (b * a.T + t) * a.D + scg, a.out_bf16, y, tv);
             }
         }
     }
