@@ -359,7 +359,7 @@ extern "C" gdr_status_t gdr_ssm_scan_fwd(int64_t B, int64_t T, int64_t D, int64_
     if (!ssm_ptrs_ok(in_dt, x, dt, A, Bm, Cm, D_skip, z, dt_bias) || !elem_ok(y, elem(out_dt)))
         return GDR_ERR_INVALID;
     const SsmPlan p = ssm_fwd_plan(B, T, D, G, N);
-    if (!workgroups_ok((double)B * G * p.nblk * p.nseg)) return GDR_ERR_INVALID;
+    if (!workgroups_ok(2.0 * B * G * p.nblk * p.nseg)) return GDR_ERR_INVALID;   // 512 threads each
     const size_t need = ssm_fwd_workspace_bytes(B, T, D, G, N);
     if (need && (!ptrs_ok({workspace}) || workspace_bytes < need)) return GDR_ERR_INVALID;
     SsmArgs a{};

@@ -69,8 +69,8 @@ __device__ __forceinline__ float row_bcast(float x) {
 
 // Fused adds with a row broadcast as their DPP operand, which the compiler does
 // not form from a broadcast and an fma, 4 per block.  The wait states between
-// a vector write of C and its DPP read are kept inside each block; state_sums
-// keeps its own before it swaps what a block wrote.
+// a vector write of C and its DPP read are kept inside each block; what a block
+// writes waits as long before state_sums swaps it (row_dots).
 //
 // h0 .. h3 += C[I .. I + 3] x0 .. x3.
 template <int I>
@@ -128,6 +128,41 @@ __device__ __forceinline__ float row_dot(float C, const float (&h)[NS], float s 
     return s;
 }
 
+// The four tokens of a register of C at NS = 4, in one block.
+__device__ __forceinline__ void row_dot_tokens(float (&s)[4], float C, const float (&h)[4][4]) {
+#define DOT4(o, a, b, c, d, i, j, k, l)                                                     \
+    "v_mul_f32_dpp " o ", %4, " a " row_newbcast:" i " row_mask:0xf bank_mask:0xf\n\t"      \
+    "v_fmac_f32_dpp " o ", %4, " b " row_newbcast:" j " row_mask:0xf bank_mask:0xf\n\t"     \
+    "v_fmac_f32_dpp " o ", %4, " c " row_newbcast:" k " row_mask:0xf bank_mask:0xf\n\t"     \
+    "v_fmac_f32_dpp " o ", %4, " d " row_newbcast:" l " row_mask:0xf bank_mask:0xf\n\t"
+    asm("s_nop 1\n\t" DOT4("%0", "%5", "%6", "%7", "%8", "0", "1", "2", "3")
+            DOT4("%1", "%9", "%10", "%11", "%12", "4", "5", "6", "7")
+                DOT4("%2", "%13", "%14", "%15", "%16", "8", "9", "10", "11")
+                    DOT4("%3", "%17", "%18", "%19", "%20", "12", "13", "14", "15") "s_nop 1"
+        : "=&v"(s[0]), "=&v"(s[1]), "=&v"(s[2]), "=&v"(s[3])
+        : "v"(C), "v"(h[0][0]), "v"(h[0][1]), "v"(h[0][2]), "v"(h[0][3]), "v"(h[1][0]),
+          "v"(h[1][1]), "v"(h[1][2]), "v"(h[1][3]), "v"(h[2][0]), "v"(h[2][1]), "v"(h[2][2]),
+          "v"(h[2][3]), "v"(h[3][0]), "v"(h[3][1]), "v"(h[3][2]), "v"(h[3][3]));
+#undef DOT4
+}
+
+// Four tokens' sums over their lane's states, C in 16 / NS tokens per register.
+template <int NS>
+__device__ __forceinline__ void row_dots(float (&s)[4], const float (&C)[NS / 4],
+                                         const float (&h)[4][NS]) {
+    if constexpr (NS == 4) {
+        row_dot_tokens(s, C[0], h);
+    } else {
+        constexpr int KT = 16 / NS;
+        s[0] = row_dot<NS, NS * (0 % KT)>(C[0 / KT], h[0]);
+        s[1] = row_dot<NS, NS * (1 % KT)>(C[1 / KT], h[1]);
+        s[2] = row_dot<NS, NS * (2 % KT)>(C[2 / KT], h[2]);
+        s[3] = row_dot<NS, NS * (3 % KT)>(C[3 / KT], h[3]);
+        // what asm wrote must not be swapped at once
+        asm("s_nop 1" : "+v"(s[0]), "+v"(s[1]), "+v"(s[2]), "+v"(s[3]));
+    }
+}
+
 // The decays and additions of one token: K is its place in the register Bq.
 template <int NS, int K, size_t... J>
 __device__ __forceinline__ void scan_terms(float (&ea)[NS], float (&bx)[NS], const float (&A2)[NS],
@@ -140,9 +175,7 @@ __device__ __forceinline__ void scan_terms(float (&ea)[NS], float (&bx)[NS], con
 // Sums s[k] (token k of 4) over the rows of each channel and stores them at
 // dst[k * pitch].  row = lane / 16.
 template <int NG>
-__device__ __forceinline__ void state_sums(float (&s)[4], int row, float* dst, int pitch) {
-    // the sums may come from asm, whose writes the swaps must not follow at once
-    if constexpr (NG > 1) asm("s_nop 1" : "+v"(s[0]), "+v"(s[1]), "+v"(s[2]), "+v"(s[3]));
+__device__ __forceinline__ void state_sums(const float (&s)[4], int row, float* dst, int pitch) {
     if constexpr (NG == 1) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) dst[k * pitch] = s[k];

@@ -428,10 +428,12 @@ __global__ __launch_bounds__(256, NS == 16 ? 1 : 2) void ssm_bwd_kernel(SsmBwdAr
                     hh[k][j] = __builtin_fmaf(aa[k][j], k ? hh[k ? k - 1 : 0][j] : hs[j], hh[k][j]);
             }
             if (a.z) {
-                s[0] = row_dot<NS, NS * (0 % KT)>(Cq[0 / KT], hh[tt]);
-                s[1] = row_dot<NS, NS * (1 % KT)>(Cq[1 / KT], hh[tt + 1]);
-                s[2] = row_dot<NS, NS * (2 % KT)>(Cq[2 / KT], hh[tt + 2]);
-                s[3] = row_dot<NS, NS * (3 % KT)>(Cq[3 / KT], hh[tt + 3]);
+                float h4[4][NS];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int j = 0; j < NS; ++j) h4[k][j] = hh[tt + k][j];
+                row_dots<NS>(s, Cq, h4);
                 state_sums<NG>(s, row, reinterpret_cast<float*>(&st[tt][chl]) + 3, 4 * WC);
             }
         }
@@ -475,6 +477,7 @@ __global__ __launch_bounds__(256, NS == 16 ? 1 : 2) void ssm_bwd_kernel(SsmBwdAr
             TOKEN(0)
 #undef TOKEN
             float* sp = reinterpret_cast<float*>(&st[tt][chl]);
+            asm("s_nop 1" : "+v"(sB[0]), "+v"(sB[1]), "+v"(sB[2]), "+v"(sB[3]));
             state_sums<NG>(sB, row, sp, 4 * WC);
             state_sums<NG>(sA, row, sp + 1, 4 * WC);
         }

@@ -27,7 +27,7 @@ namespace gdr {
 namespace {
 
 template <int NS, int NG, bool OUT, bool BF16, bool RAG>
-__global__ __launch_bounds__(256) void ssm_fwd_kernel(SsmArgs a, int64_t nblk, int64_t nseg,
+__global__ __launch_bounds__(512) void ssm_fwd_kernel(SsmArgs a, int64_t nblk, int64_t nseg,
                                                       int64_t L) {
     constexpr int NP = NS * NG, CW = 64 / NG, WC = 4 * CW;
     constexpr int EPT = 8;                            // staged channels per thread
@@ -37,11 +37,13 @@ __global__ __launch_bounds__(256) void ssm_fwd_kernel(SsmArgs a, int64_t nblk, i
     constexpr int QPT = (2 * NQ + 255) / 256;
     constexpr int KT = 16 / NS;                       // tokens per B register
     constexpr int YP = WC + 16;                       // pitch: 4 tokens' stores meet no bank twice
-    __shared__ float2 dd[TT][WC];
-    __shared__ __align__(16) float bc[2][TT * NP];
-    __shared__ float ys[OUT ? TT : 1][YP];
+    __shared__ float2 dd[2][TT][WC];
+    __shared__ __align__(16) float bc[2][2][TT * NP];
+    __shared__ float ys[2][OUT ? TT : 1][YP];
 
-    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+    const int lane = threadIdx.x & 63, tid = threadIdx.x & 255;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) & 3;
+    const bool scans = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) < 4;
     int64_t id = blockIdx.x;
     const int64_t blk = id % nblk;
     id /= nblk;
@@ -51,42 +53,99 @@ __global__ __launch_bounds__(256) void ssm_fwd_kernel(SsmArgs a, int64_t nblk, i
     const int64_t seg = id % ns, b = id / ns;
     const int64_t Dg = a.D / a.G, c0 = blk * WC, cg = g * Dg;
     const int64_t t0 = seg * L, t1 = t0 + L < a.T ? t0 + L : a.T;
+    const int64_t tiles = (t1 - t0 + TT - 1) / TT;
 
-    // the lane's channel and states
-    const int row = lane >> 4, n0 = NS * (row % NG);
-    const int chl = wv * CW + (lane & 15) + 16 * (row / NG);
-    const bool live = c0 + chl < Dg;
-    const int64_t ch = cg + (live ? c0 + chl : 0);
-    const int nv = live ? states_valid<NS>(a.N, n0) : 0;
-    float A2[NS], h[NS];
-    param_load<NS>(A2, a.A + ch * a.N + n0, nv);
+    if (scans) {
+        // the lane's channel and states
+        const int row = lane >> 4, n0 = NS * (row % NG);
+        const int chl = wv * CW + (lane & 15) + 16 * (row / NG);
+        const bool live = c0 + chl < Dg;
+        const int64_t ch = cg + (live ? c0 + chl : 0);
+        const int nv = live ? states_valid<NS>(a.N, n0) : 0;
+        float A2[NS], h[NS];
+        param_load<NS>(A2, a.A + ch * a.N + n0, nv);
 #pragma unroll
-    for (int j = 0; j < NS; ++j) {
-        A2[j] *= kLog2e;
-        h[j] = 0.f;
-    }
-    const int64_t so = (b * a.D + ch) * a.N + n0;
-    // hend[b][0] is h0 as the first pass copied it (the second pass must not
-    // read h0: another workgroup may be writing h_final, the same buffer),
-    // hend[b][s] the end of segment s - 1, segment 0 started from h0
-    if (!OUT || nseg == 1) {
-        if (a.h0 && seg == 0) states_load<NS>(h, a.h0 + so, nv);
-        if constexpr (!OUT)
-            if (seg == 0) states_store<NS>(a.hend + (b * nseg * a.D + ch) * a.N + n0, h, nv);
-    } else {
-        states_load<NS>(h, a.hend + ((b * nseg + (seg > 0)) * a.D + ch) * a.N + n0, nv);
-        for (int64_t s = 1; s < seg; ++s) {
-            const int64_t o = (b * nseg + s) * a.D + ch;
-            float e[NS];
-            states_load<NS>(e, a.hend + (o + a.D) * a.N + n0, nv);
-            const float sd = live ? a.sdelta[o] : 0.f;
-#pragma unroll
-            for (int j = 0; j < NS; ++j)
-                h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(A2[j] * sd), h[j], e[j]);
+        for (int j = 0; j < NS; ++j) {
+            A2[j] *= kLog2e;
+            h[j] = 0.f;
         }
+        const int64_t so = (b * a.D + ch) * a.N + n0;
+        // hend[b][0] is h0 as the first pass copied it (the second pass must
+        // not read h0: another workgroup may be writing h_final, the same
+        // buffer), hend[b][s] the end of segment s - 1, segment 0 started from h0
+        if (!OUT || nseg == 1) {
+            if (a.h0 && seg == 0) states_load<NS>(h, a.h0 + so, nv);
+            if constexpr (!OUT)
+                if (seg == 0) states_store<NS>(a.hend + (b * nseg * a.D + ch) * a.N + n0, h, nv);
+        } else {
+            states_load<NS>(h, a.hend + ((b * nseg + (seg > 0)) * a.D + ch) * a.N + n0, nv);
+            for (int64_t s = 1; s < seg; ++s) {
+                const int64_t o = (b * nseg + s) * a.D + ch;
+                float e[NS];
+                states_load<NS>(e, a.hend + (o + a.D) * a.N + n0, nv);
+                const float sd = live ? a.sdelta[o] : 0.f;
+#pragma unroll
+                for (int j = 0; j < NS; ++j)
+                    h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(A2[j] * sd), h[j], e[j]);
+            }
+        }
+        float sumd = 0.f;
+        __syncthreads();
+        for (int64_t i = 0; i < tiles; ++i) {
+            const int buf = (int)(i & 1);
+            const int64_t tb = t0 + i * TT;
+            const int nt = t1 - tb < TT ? (int)(t1 - tb) : TT;
+            auto group = [&](int tt) {
+                float Bq[4 / KT], Cq[4 / KT];
+                float2 d[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) d[k] = dd[buf][tt + k][chl];
+#pragma unroll
+                for (int k = 0; k < 4 / KT; ++k) {
+                    Bq[k] = row_coef<NS, NG>(bc[buf][0], tt + k * KT, lane);
+                    Cq[k] = OUT ? row_coef<NS, NG>(bc[buf][1], tt + k * KT, lane) : 0.f;
+                }
+                constexpr auto js = std::make_index_sequence<NS>{};
+                float ea[4][NS], bx[4][NS];
+                scan_terms<NS, 0 % KT>(ea[0], bx[0], A2, d[0].x, d[0].y, Bq[0 / KT], js);
+                scan_terms<NS, 1 % KT>(ea[1], bx[1], A2, d[1].x, d[1].y, Bq[1 / KT], js);
+                scan_terms<NS, 2 % KT>(ea[2], bx[2], A2, d[2].x, d[2].y, Bq[2 / KT], js);
+                scan_terms<NS, 3 % KT>(ea[3], bx[3], A2, d[3].x, d[3].y, Bq[3 / KT], js);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+#pragma unroll
+                    for (int j = 0; j < NS; ++j)
+                        bx[k][j] =
+                            __builtin_fmaf(ea[k][j], k ? bx[k ? k - 1 : 0][j] : h[j], bx[k][j]);
+                }
+                if constexpr (OUT) {
+                    float s[4];
+                    row_dots<NS>(s, Cq, bx);
+                    state_sums<NG>(s, row, &ys[buf][tt][chl], YP);
+                } else {
+                    sumd += (d[0].x + d[1].x) + (d[2].x + d[3].x);
+                }
+#pragma unroll
+                for (int j = 0; j < NS; ++j) h[j] = bx[3][j];
+            };
+            // a token past the end moves nothing, so whole groups may run
+            for (int tt = 0; tt < nt; tt += 8) {
+                group(tt);
+                group(tt + 4);
+            }
+            __syncthreads();
+        }
+        if constexpr (OUT) {
+            if (a.h_final && seg == nseg - 1) states_store<NS>(a.h_final + so, h, nv);
+        } else {
+            const int64_t o = (b * nseg + seg) * a.D + ch;
+            states_store<NS>(a.hend + (o + a.D) * a.N + n0, h, nv);
+            if (live && n0 == 0) a.sdelta[o] = sumd;
+        }
+        return;
     }
 
-    // the thread's part of the staging
+    // the other four waves: each thread's part of the staging
     const int srow = tid / TPR, sc = (tid % TPR) * EPT;
     const int sv = ssm_left(Dg, c0 + sc, EPT);
     const int64_t scg = cg + c0 + sc;
@@ -113,91 +172,76 @@ __global__ __launch_bounds__(256) void ssm_fwd_kernel(SsmArgs a, int64_t nblk, i
                        (isc ? b * a.cb + tq * a.ct : b * a.bb + tq * a.bt) + g * a.N + 4 * qn, vq);
         }
     };
-    fetch(t0);
-    float sumd = 0.f;
-    for (int64_t tb = t0; tb < t1; tb += TT) {
-        const int64_t t = tb + srow;
+    // what a tile's epilogue needs: y = (sum over n + base) factor
+    float base[EPT], factor[EPT];
+    auto stage = [&](int64_t i) {
+        const int buf = (int)(i & 1);
         // a token past the end or a channel past the group moves nothing: its
         // decay is exp(0) and it adds 0
-        const int tv = t < t1 ? sv : 0;
-        float x[EPT], z[EPT];
+        const int tv = t0 + i * TT + srow < t1 ? sv : 0;
+        float x[EPT], r[EPT], d[EPT];
         rx.unpack(x);
-        if constexpr (OUT) rz.unpack(z);
-        {
-            float r[EPT], d[EPT];
-            rt.unpack(r);
+        rt.unpack(r);
 #pragma unroll
-            for (int e = 0; e < EPT; ++e) r[e] += bias[e];
-            ssm_deltas(d, r, a.softplus);
+        for (int e = 0; e < EPT; ++e) r[e] += bias[e];
+        ssm_deltas(d, r, a.softplus);
+#pragma unroll
+        for (int e = 0; e < EPT; ++e) {
+            d[e] = (RAG ? e < tv : tv > 0) ? d[e] : 0.f;
+            dd[buf][srow][sc + e] = float2{d[e], d[e] * x[e]};
+        }
+        if constexpr (OUT) {
 #pragma unroll
             for (int e = 0; e < EPT; ++e) {
-                d[e] = e < tv ? d[e] : 0.f;
-                dd[srow][sc + e] = float2{d[e], d[e] * x[e]};
+                base[e] = skip[e] * x[e];
+                factor[e] = 1.f;
+            }
+            if (a.z) {
+                float z[EPT];
+                rz.unpack(z);
+                ssm_gate(factor, z);
             }
         }
 #pragma unroll
-        for (int i = 0; i < QPT; ++i) {
-            const int q = tid + 256 * i;
+        for (int q4 = 0; q4 < QPT; ++q4) {
+            const int q = tid + 256 * q4;
             if (q >= 2 * NQ || (q >= NQ && !OUT)) continue;
             float f[4];
-            rq[i].unpack(f);
-            *reinterpret_cast<float4*>(&bc[q >= NQ][4 * (q % NQ)]) = float4{f[0], f[1], f[2], f[3]};
+            rq[q4].unpack(f);
+            *reinterpret_cast<float4*>(&bc[buf][q >= NQ][4 * (q % NQ)]) =
+                float4{f[0], f[1], f[2], f[3]};
         }
-        __syncthreads();
-        if (tb + TT < t1) fetch(tb + TT);
-        const int nt = t1 - tb < TT ? (int)(t1 - tb) : TT;
-        constexpr auto js = std::make_index_sequence<NS>{};
-        for (int tt = 0; tt < nt; tt += 4) {
-            float s[4], Bq[4 / KT], Cq[4 / KT];
-            float2 d[4];
+    };
+    auto finish = [&](int64_t i, const float (&base)[EPT], const float (&factor)[EPT]) {
+        const int64_t t = t0 + i * TT + srow;
+        if (t < t1 && sv > 0) {
+            float y[EPT];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) d[k] = dd[tt + k][chl];
-#pragma unroll
-            for (int k = 0; k < 4 / KT; ++k) {
-                Bq[k] = row_coef<NS, NG>(bc[0], tt + k * KT, lane);
-                Cq[k] = OUT ? row_coef<NS, NG>(bc[1], tt + k * KT, lane) : 0.f;
-            }
-            float ea[4][NS], bx[4][NS];
-            scan_terms<NS, 0 % KT>(ea[0], bx[0], A2, d[0].x, d[0].y, Bq[0 / KT], js);
-            scan_terms<NS, 1 % KT>(ea[1], bx[1], A2, d[1].x, d[1].y, Bq[1 / KT], js);
-            scan_terms<NS, 2 % KT>(ea[2], bx[2], A2, d[2].x, d[2].y, Bq[2 / KT], js);
-            scan_terms<NS, 3 % KT>(ea[3], bx[3], A2, d[3].x, d[3].y, Bq[3 / KT], js);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-#pragma unroll
-                for (int j = 0; j < NS; ++j)
-                    bx[k][j] = __builtin_fmaf(ea[k][j], k ? bx[k ? k - 1 : 0][j] : h[j], bx[k][j]);
-            }
-            if constexpr (OUT) {
-                s[0] = row_dot<NS, NS * (0 % KT)>(Cq[0 / KT], bx[0]);
-                s[1] = row_dot<NS, NS * (1 % KT)>(Cq[1 / KT], bx[1]);
-                s[2] = row_dot<NS, NS * (2 % KT)>(Cq[2 / KT], bx[2]);
-                s[3] = row_dot<NS, NS * (3 % KT)>(Cq[3 / KT], bx[3]);
-                state_sums<NG>(s, row, &ys[tt][chl], YP);
-            } else {
-                sumd += (d[0].x + d[1].x) + (d[2].x + d[3].x);
-            }
-#pragma unroll
-            for (int j = 0; j < NS; ++j) h[j] = bx[3][j];
+            for (int e = 0; e < EPT; ++e) y[e] = (ys[i & 1][srow][sc + e] + base[e]) * factor[e];
+            row_store<EPT, RAG>(a.y, (b * a.T + t) * a.D + scg, a.out_bf16, y, sv);
         }
-        __syncthreads();
+    };
+    fetch(t0);
+    stage(0);
+    if (tiles > 1) fetch(t0 + TT);
+    __syncthreads();
+    for (int64_t i = 0; i < tiles; ++i) {
+        // while tile i runs: tile i + 1 is staged, tile i + 2's loads are
+        // issued, then tile i - 1 goes out
+        float pb[EPT], pf[EPT];
         if constexpr (OUT) {
-            if (tv > 0) {
-                float y[EPT];
 #pragma unroll
-                for (int e = 0; e < EPT; ++e)
-                    y[e] = __builtin_fmaf(skip[e], x[e], ys[srow][sc + e]);
-                if (a.z) ssm_gate(y, z);
-                row_store<EPT, RAG>(a.y, (b * a.T + t) * a.D + scg, a.out_bf16, y, tv);
+            for (int e = 0; e < EPT; ++e) {
+                pb[e] = base[e];
+                pf[e] = factor[e];
             }
         }
-    }
-    if constexpr (OUT) {
-        if (a.h_final && seg == nseg - 1) states_store<NS>(a.h_final + so, h, nv);
-    } else {
-        const int64_t o = (b * nseg + seg) * a.D + ch;
-        states_store<NS>(a.hend + (o + a.D) * a.N + n0, h, nv);
-        if (live && n0 == 0) a.sdelta[o] = sumd;
+        if (i + 1 < tiles) {
+            stage(i + 1);
+            if (i + 2 < tiles) fetch(t0 + (i + 2) * TT);
+        }
+        __syncthreads();
+        if constexpr (OUT) finish(i, pb, pf);
     }
 }
 
@@ -258,13 +302,13 @@ hipError_t launch_fwd_r(const SsmArgs& a, const SsmPlan& p) {
     const int64_t wgs = a.B * a.G * p.nblk;
     if (p.nseg > 1) {
         hipLaunchKernelGGL((ssm_fwd_kernel<NS, NG, false, BF16, RAG>),
-                           dim3((unsigned)(wgs * (p.nseg - 1))), dim3(256), 0, a.stream, a, p.nblk,
+                           dim3((unsigned)(wgs * (p.nseg - 1))), dim3(512), 0, a.stream, a, p.nblk,
                            p.nseg, p.L);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     hipLaunchKernelGGL((ssm_fwd_kernel<NS, NG, true, BF16, RAG>), dim3((unsigned)(wgs * p.nseg)),
-                       dim3(256), 0, a.stream, a, p.nblk, p.nseg, p.L);
+                       dim3(512), 0, a.stream, a, p.nblk, p.nseg, p.L);
     return hipGetLastError();
 }
 
