@@ -35,9 +35,10 @@ namespace {
 // bytes per channel and token as at N = 16).
 template <int NS, int NG> constexpr int block_tokens() { return NG < 4 ? 4 * NG : 64 / NS; }
 
-// First pass.  GAM: more than one segment.
+// First pass.  GAM: more than one segment.  As in the forward, four waves run
+// the states while four stage the next tile.
 template <int NS, int NG, bool GAM, bool BF16, bool RAG>
-__global__ __launch_bounds__(256) void ssm_bwd_states_kernel(SsmBwdArgs a, int64_t nblk,
+__global__ __launch_bounds__(512) void ssm_bwd_states_kernel(SsmBwdArgs a, int64_t nblk,
                                                              int64_t nseg, int64_t L) {
     constexpr int NP = NS * NG, CW = 64 / NG, WC = 4 * CW;
     constexpr int EPT = 8;
@@ -47,11 +48,13 @@ __global__ __launch_bounds__(256) void ssm_bwd_states_kernel(SsmBwdArgs a, int64
     constexpr int QPT = (2 * NQ + 255) / 256;
     constexpr int KT = 16 / NS;
     constexpr int S = block_tokens<NS, NG>();
-    __shared__ float2 dd[TT][WC];
-    __shared__ __align__(16) float bc[2][TT * NP];
-    __shared__ float ds[GAM ? TT : 1][WC];
+    __shared__ float2 dd[2][TT][WC];
+    __shared__ __align__(16) float bc[2][2][TT * NP];
+    __shared__ float ds[2][GAM ? TT : 1][WC];
 
-    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+    const int lane = threadIdx.x & 63, tid = threadIdx.x & 255;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) & 3;
+    const bool scans = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) < 4;
     int64_t id = blockIdx.x;
     const int64_t blk = id % nblk;
     id /= nblk;
@@ -60,22 +63,87 @@ __global__ __launch_bounds__(256) void ssm_bwd_states_kernel(SsmBwdArgs a, int64
     const int64_t seg = id % nseg, b = id / nseg;
     const int64_t Dg = a.D / a.G, c0 = blk * WC, cg = g * Dg;
     const int64_t t0 = seg * L, t1 = t0 + L < a.T ? t0 + L : a.T;
+    const int64_t tiles = (t1 - t0 + TT - 1) / TT;
     const int64_t nsub = (a.T + S - 1) / S;
 
-    const int row = lane >> 4, n0 = NS * (row % NG);
-    const int chl = wv * CW + (lane & 15) + 16 * (row / NG);
-    const bool live = c0 + chl < Dg;
-    const int64_t ch = cg + (live ? c0 + chl : 0);
-    const int nv = live ? states_valid<NS>(a.N, n0) : 0;
-    float A2[NS], h[NS], P[NS], gam[NS];
-    param_load<NS>(A2, a.A + ch * a.N + n0, nv);
+    if (scans) {
+        const int row = lane >> 4, n0 = NS * (row % NG);
+        const int chl = wv * CW + (lane & 15) + 16 * (row / NG);
+        const bool live = c0 + chl < Dg;
+        const int64_t ch = cg + (live ? c0 + chl : 0);
+        const int nv = live ? states_valid<NS>(a.N, n0) : 0;
+        float A2[NS], h[NS], P[NS], gam[NS];
+        param_load<NS>(A2, a.A + ch * a.N + n0, nv);
 #pragma unroll
-    for (int j = 0; j < NS; ++j) {
-        A2[j] *= kLog2e;
-        h[j] = gam[j] = 0.f;
-        P[j] = 1.f;
+        for (int j = 0; j < NS; ++j) {
+            A2[j] *= kLog2e;
+            h[j] = gam[j] = 0.f;
+            P[j] = 1.f;
+        }
+        if (a.h0 && seg == 0) states_load<NS>(h, a.h0 + (b * a.D + ch) * a.N + n0, nv);
+        float sumd = 0.f;
+        __syncthreads();
+        for (int64_t i = 0; i < tiles; ++i) {
+            const int buf = (int)(i & 1);
+            const int64_t tb = t0 + i * TT;
+            const int nt = t1 - tb < TT ? (int)(t1 - tb) : TT;
+            for (int tt = 0; tt < nt; tt += 4) {
+                if (((tb + tt) & (S - 1)) == 0) {
+                    const int64_t o = (b * nsub + (tb + tt) / S) * a.D + ch;
+                    states_store<NS>(a.ckpt + o * a.N + n0, h, nv);
+                    if (GAM && live && n0 == 0) a.csum[o] = sumd;
+                }
+                float Bq[4 / KT], Cq[4 / KT], dy[4] = {0.f, 0.f, 0.f, 0.f};
+                float2 d[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    d[k] = dd[buf][tt + k][chl];
+                    if constexpr (GAM) dy[k] = ds[buf][tt + k][chl];
+                }
+#pragma unroll
+                for (int k = 0; k < 4 / KT; ++k) {
+                    Bq[k] = row_coef<NS, NG>(bc[buf][0], tt + k * KT, lane);
+                    Cq[k] = GAM ? row_coef<NS, NG>(bc[buf][1], tt + k * KT, lane) : 0.f;
+                }
+                constexpr auto js = std::make_index_sequence<NS>{};
+                float ea[4][NS], bx[4][NS];
+                scan_terms<NS, 0 % KT>(ea[0], bx[0], A2, d[0].x, d[0].y, Bq[0 / KT], js);
+                scan_terms<NS, 1 % KT>(ea[1], bx[1], A2, d[1].x, d[1].y, Bq[1 / KT], js);
+                scan_terms<NS, 2 % KT>(ea[2], bx[2], A2, d[2].x, d[2].y, Bq[2 / KT], js);
+                scan_terms<NS, 3 % KT>(ea[3], bx[3], A2, d[3].x, d[3].y, Bq[3 / KT], js);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+#pragma unroll
+                    for (int j = 0; j < NS; ++j) h[j] = __builtin_fmaf(ea[k][j], h[j], bx[k][j]);
+                }
+                if constexpr (GAM) {
+                    // gam += P C dy: P in place of the decays, then the
+                    // products with dy, then C by broadcast
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+#pragma unroll
+                        for (int j = 0; j < NS; ++j) {
+                            P[j] *= ea[k][j];
+                            ea[k][j] = P[j] * dy[k];
+                        }
+                    }
+                    row_fma_each<NS, NS * (0 % KT)>(gam, Cq[0 / KT], ea[0]);
+                    row_fma_each<NS, NS * (1 % KT)>(gam, Cq[1 / KT], ea[1]);
+                    row_fma_each<NS, NS * (2 % KT)>(gam, Cq[2 / KT], ea[2]);
+                    row_fma_each<NS, NS * (3 % KT)>(gam, Cq[3 / KT], ea[3]);
+                    sumd += (d[0].x + d[1].x) + (d[2].x + d[3].x);
+                }
+            }
+            __syncthreads();
+        }
+        if constexpr (GAM) {
+            const int64_t o = (b * nseg + seg) * a.D + ch;
+            states_store<NS>(a.hend + o * a.N + n0, h, nv);
+            states_store<NS>(a.gstart + o * a.N + n0, gam, nv);
+            if (live && n0 == 0) a.sdelta[o] = sumd;
+        }
+        return;
     }
-    if (a.h0 && seg == 0) states_load<NS>(h, a.h0 + (b * a.D + ch) * a.N + n0, nv);
 
     const int srow = tid / TPR, sc = (tid % TPR) * EPT;
     const int sv = ssm_left(Dg, c0 + sc, EPT);
@@ -109,21 +177,19 @@ __global__ __launch_bounds__(256) void ssm_bwd_states_kernel(SsmBwdArgs a, int64
                        (isc ? b * a.cb + tq * a.ct : b * a.bb + tq * a.bt) + g * a.N + 4 * qn, vq);
         }
     };
-    fetch(t0);
-    float sumd = 0.f;
-    for (int64_t tb = t0; tb < t1; tb += TT) {
-        const int tv = tb + srow < t1 ? sv : 0;
-        float x[EPT], r[EPT];
+    auto stage = [&](int64_t i) {
+        const int buf = (int)(i & 1);
+        const int tv = t0 + i * TT + srow < t1 ? sv : 0;
+        float x[EPT], r[EPT], d[EPT];
         rx.unpack(x);
         rt.unpack(r);
-        float d8[EPT];
 #pragma unroll
         for (int e = 0; e < EPT; ++e) r[e] += bias[e];
-        ssm_deltas(d8, r, a.softplus);
+        ssm_deltas(d, r, a.softplus);
 #pragma unroll
         for (int e = 0; e < EPT; ++e) {
-            d8[e] = e < tv ? d8[e] : 0.f;
-            dd[srow][sc + e] = float2{d8[e], d8[e] * x[e]};
+            d[e] = (RAG ? e < tv : tv > 0) ? d[e] : 0.f;
+            dd[buf][srow][sc + e] = float2{d[e], d[e] * x[e]};
         }
         if constexpr (GAM) {
             float o[EPT], z[EPT];
@@ -134,75 +200,28 @@ __global__ __launch_bounds__(256) void ssm_bwd_states_kernel(SsmBwdArgs a, int64
             rz.unpack(z);
             if (a.z) ssm_gate(o, z);
 #pragma unroll
-            for (int e = 0; e < EPT; ++e) ds[srow][sc + e] = o[e];
+            for (int e = 0; e < EPT; ++e) ds[buf][srow][sc + e] = o[e];
         }
 #pragma unroll
-        for (int i = 0; i < QPT; ++i) {
-            const int q = tid + 256 * i;
+        for (int q4 = 0; q4 < QPT; ++q4) {
+            const int q = tid + 256 * q4;
             if (q >= 2 * NQ || (q >= NQ && !GAM)) continue;
             float f[4];
-            rq[i].unpack(f);
-            *reinterpret_cast<float4*>(&bc[q >= NQ][4 * (q % NQ)]) = float4{f[0], f[1], f[2], f[3]};
+            rq[q4].unpack(f);
+            *reinterpret_cast<float4*>(&bc[buf][q >= NQ][4 * (q % NQ)]) =
+                float4{f[0], f[1], f[2], f[3]};
+        }
+    };
+    fetch(t0);
+    stage(0);
+    if (tiles > 1) fetch(t0 + TT);
+    __syncthreads();
+    for (int64_t i = 0; i < tiles; ++i) {
+        if (i + 1 < tiles) {
+            stage(i + 1);
+            if (i + 2 < tiles) fetch(t0 + (i + 2) * TT);
         }
         __syncthreads();
-        if (tb + TT < t1) fetch(tb + TT);
-        const int nt = t1 - tb < TT ? (int)(t1 - tb) : TT;
-        for (int tt = 0; tt < nt; tt += 4) {
-            if (((tb + tt) & (S - 1)) == 0) {
-                const int64_t o = (b * nsub + (tb + tt) / S) * a.D + ch;
-                states_store<NS>(a.ckpt + o * a.N + n0, h, nv);
-                if (GAM && live && n0 == 0) a.csum[o] = sumd;
-            }
-            float Bq[4 / KT], Cq[4 / KT], dy[4] = {0.f, 0.f, 0.f, 0.f};
-            float2 d[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                d[k] = dd[tt + k][chl];
-                if constexpr (GAM) dy[k] = ds[tt + k][chl];
-            }
-#pragma unroll
-            for (int k = 0; k < 4 / KT; ++k) {
-                Bq[k] = row_coef<NS, NG>(bc[0], tt + k * KT, lane);
-                Cq[k] = GAM ? row_coef<NS, NG>(bc[1], tt + k * KT, lane) : 0.f;
-            }
-            constexpr auto js = std::make_index_sequence<NS>{};
-            float ea[4][NS], bx[4][NS];
-#define TOKEN(k) scan_terms<NS, k % KT>(ea[k], bx[k], A2, d[k].x, d[k].y, Bq[k / KT], js)
-            TOKEN(0);
-            TOKEN(1);
-            TOKEN(2);
-            TOKEN(3);
-#undef TOKEN
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-#pragma unroll
-                for (int j = 0; j < NS; ++j) h[j] = __builtin_fmaf(ea[k][j], h[j], bx[k][j]);
-            }
-            if constexpr (GAM) {
-                // gam += P C dy: P in place of the decays, then the products
-                // with dy, then C by broadcast
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-#pragma unroll
-                    for (int j = 0; j < NS; ++j) {
-                        P[j] *= ea[k][j];
-                        ea[k][j] = P[j] * dy[k];
-                    }
-                }
-                row_fma_each<NS, NS * (0 % KT)>(gam, Cq[0 / KT], ea[0]);
-                row_fma_each<NS, NS * (1 % KT)>(gam, Cq[1 / KT], ea[1]);
-                row_fma_each<NS, NS * (2 % KT)>(gam, Cq[2 / KT], ea[2]);
-                row_fma_each<NS, NS * (3 % KT)>(gam, Cq[3 / KT], ea[3]);
-            }
-            if constexpr (GAM) sumd += (d[0].x + d[1].x) + (d[2].x + d[3].x);
-        }
-        __syncthreads();
-    }
-    if constexpr (GAM) {
-        const int64_t o = (b * nseg + seg) * a.D + ch;
-        states_store<NS>(a.hend + o * a.N + n0, h, nv);
-        states_store<NS>(a.gstart + o * a.N + n0, gam, nv);
-        if (live && n0 == 0) a.sdelta[o] = sumd;
     }
 }
 
@@ -257,10 +276,12 @@ __device__ __forceinline__ void channel_sums(float (&v)[M], int lane) {
     }
 }
 
-// Second pass.
+// Second pass.  Four waves run the blocks, backwards; the other four stage the
+// next block meanwhile and finish the last one: its gradients from the sums
+// over n, which the running waves leave in the block's place in st.
 template <int NS, int NG, bool BF16, bool RAG>
-__global__ __launch_bounds__(256, NS == 16 ? 1 : 2) void ssm_bwd_kernel(SsmBwdArgs a, int64_t nblk, int64_t nseg,
-                                                         int64_t L) {
+__global__ __launch_bounds__(512, NS == 16 ? 1 : 2) void ssm_bwd_kernel(SsmBwdArgs a, int64_t nblk,
+                                                                       int64_t nseg, int64_t L) {
     constexpr int NP = NS * NG, CW = 64 / NG, WC = 4 * CW;
     constexpr int S = block_tokens<NS, NG>();
     constexpr int EPT = S * WC / 256;
@@ -268,12 +289,13 @@ __global__ __launch_bounds__(256, NS == 16 ? 1 : 2) void ssm_bwd_kernel(SsmBwdAr
     constexpr int NQ = S * NP / 4;
     constexpr int QPT = (2 * NQ + 255) / 256;
     constexpr int KT = 16 / NS;
-    __shared__ f32x4 st[S][WC];               // Delta, Delta x, dy, (y); then sums over n
-    __shared__ f32x4 raw[S][WC];              // x, dt + bias, dout, z, for the block's end
-    __shared__ __align__(16) float bc[2][S * NP];
-    __shared__ float pbc[4][S][2 * NP];       // each wave's sums over its channels: dC, dB
+    __shared__ f32x4 st[2][S][WC];            // Delta, Delta x, dy, (y); then sums over n
+    __shared__ __align__(16) float bc[2][2][S * NP];
+    __shared__ float pbc[2][4][S][2 * NP];    // each wave's sums over its channels: dC, dB
 
-    const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
+    const int lane = threadIdx.x & 63, tid = threadIdx.x & 255;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) & 3;
+    const bool runs = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) < 4;
     int64_t id = blockIdx.x;
     const int64_t blk = id % nblk;
     id /= nblk;
@@ -283,47 +305,157 @@ __global__ __launch_bounds__(256, NS == 16 ? 1 : 2) void ssm_bwd_kernel(SsmBwdAr
     const int64_t Dg = a.D / a.G, c0 = blk * WC, cg = g * Dg;
     const int64_t t0 = seg * L, t1 = t0 + L < a.T ? t0 + L : a.T;
     const int64_t nsub = (a.T + S - 1) / S;
+    const int64_t first = t0 / S, last = (t1 + S - 1) / S - 1;
+    float* const part = a.part + (b * nseg + seg) * a.D * (a.N + 2);
 
-    const int row = lane >> 4, n0 = NS * (row % NG);
-    const int chl = wv * CW + (lane & 15) + 16 * (row / NG);
-    const bool live = c0 + chl < Dg;
-    const int64_t ch = cg + (live ? c0 + chl : 0);
-    const int nv = live ? states_valid<NS>(a.N, n0) : 0;
-    float A2[NS], hin[NS], gr[NS], dA[NS];
-    param_load<NS>(A2, a.A + ch * a.N + n0, nv);
+    if (runs) {
+        const int row = lane >> 4, n0 = NS * (row % NG);
+        const int chl = wv * CW + (lane & 15) + 16 * (row / NG);
+        const bool live = c0 + chl < Dg;
+        const int64_t ch = cg + (live ? c0 + chl : 0);
+        const int nv = live ? states_valid<NS>(a.N, n0) : 0;
+        float A2[NS], hin[NS], gr[NS], dA[NS];
+        param_load<NS>(A2, a.A + ch * a.N + n0, nv);
 #pragma unroll
-    for (int j = 0; j < NS; ++j) {
-        A2[j] *= kLog2e;
-        hin[j] = gr[j] = dA[j] = 0.f;
+        for (int j = 0; j < NS; ++j) {
+            A2[j] *= kLog2e;
+            hin[j] = gr[j] = dA[j] = 0.f;
+        }
+        const int64_t so = (b * a.D + ch) * a.N + n0;
+        // the segment's start state (segment 0's kept states hold h0 already)
+        for (int64_t s = 0; s < seg; ++s) {
+            const int64_t o = (b * nseg + s) * a.D + ch;
+            float e[NS];
+            states_load<NS>(e, a.hend + o * a.N + n0, nv);
+            const float sd = live ? a.sdelta[o] : 0.f;
+#pragma unroll
+            for (int j = 0; j < NS; ++j)
+                hin[j] = s == 0 ? e[j]
+                                : __builtin_fmaf(__builtin_amdgcn_exp2f(A2[j] * sd), hin[j], e[j]);
+        }
+        // gr = a_{t+1} g_{t+1} past the segment's last token
+        if (a.dh_final) states_load<NS>(gr, a.dh_final + so, nv);
+        for (int64_t s = nseg - 1; s > seg; --s) {
+            const int64_t o = (b * nseg + s) * a.D + ch;
+            float e[NS];
+            states_load<NS>(e, a.gstart + o * a.N + n0, nv);
+            const float sd = live ? a.sdelta[o] : 0.f;
+#pragma unroll
+            for (int j = 0; j < NS; ++j)
+                gr[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(A2[j] * sd), gr[j], e[j]);
+        }
+        float kept[NS], ksum = 0.f;
+        auto fetch = [&](int64_t sub) {
+            const int64_t ko = (b * nsub + sub) * a.D + ch;
+            states_load<NS>(kept, a.ckpt + ko * a.N + n0, nv);
+            if (seg > 0) ksum = live ? a.csum[ko] : 0.f;
+        };
+        fetch(last);
+        __syncthreads();
+        for (int64_t sub = last; sub >= first; --sub) {
+            const int buf = (int)(sub & 1);
+            float hs[NS];
+#pragma unroll
+            for (int j = 0; j < NS; ++j)
+                hs[j] = seg > 0
+                            ? __builtin_fmaf(__builtin_amdgcn_exp2f(A2[j] * ksum), hin[j], kept[j])
+                            : kept[j];
+            // the block's states again, all kept in registers
+            constexpr auto js = std::make_index_sequence<NS>{};
+            float hh[S][NS], aa[S][NS];
+#pragma unroll
+            for (int tt = 0; tt < S; tt += 4) {
+                float Bq[4 / KT], Cq[4 / KT];
+#pragma unroll
+                for (int k = 0; k < 4 / KT; ++k) {
+                    Bq[k] = row_coef<NS, NG>(bc[buf][0], tt + k * KT, lane);
+                    Cq[k] = row_coef<NS, NG>(bc[buf][1], tt + k * KT, lane);
+                }
+                f32x4 d[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) d[k] = st[buf][tt + k][chl];
+#define TOKEN(k) scan_terms<NS, k % KT>(aa[tt + k], hh[tt + k], A2, d[k][0], d[k][1], Bq[k / KT], js)
+                TOKEN(0);
+                TOKEN(1);
+                TOKEN(2);
+                TOKEN(3);
+#undef TOKEN
+#pragma unroll
+                for (int k = tt; k < tt + 4; ++k) {
+#pragma unroll
+                    for (int j = 0; j < NS; ++j)
+                        hh[k][j] =
+                            __builtin_fmaf(aa[k][j], k ? hh[k ? k - 1 : 0][j] : hs[j], hh[k][j]);
+                }
+                if (a.z) {
+                    float s[4], h4[4][NS];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int j = 0; j < NS; ++j) h4[k][j] = hh[tt + k][j];
+                    row_dots<NS>(s, Cq, h4);
+                    state_sums<NG>(s, row, reinterpret_cast<float*>(&st[buf][tt][chl]) + 3, 4 * WC);
+                }
+            }
+            // and backwards
+#pragma unroll
+            for (int tt = S - 4; tt >= 0; tt -= 4) {
+                // half of the kept states are done with: the next block's
+                // start takes their registers
+                if (tt == (S / 2 - 4 > 0 ? S / 2 - 4 : 0) && sub > first) fetch(sub - 1);
+                float sB[4], sA[4], Bq[4 / KT], Cq[4 / KT];
+#pragma unroll
+                for (int k = 0; k < 4 / KT; ++k) {
+                    Bq[k] = row_coef<NS, NG>(bc[buf][0], tt + k * KT, lane);
+                    Cq[k] = row_coef<NS, NG>(bc[buf][1], tt + k * KT, lane);
+                }
+                // lane bits 3 .. 0 chose the value: of dC or dB, then its state
+                auto store_sums = [&](const float(&pv)[2 * NS], int q) {
+                    float* p = pbc[buf][wv][q] + ((lane >> 3) & 1) * NP + n0;
+                    if constexpr (NS == 4) {
+                        if ((lane & 1) == 0 && row < NG)
+                            p[((lane >> 2) & 1) * 2 + ((lane >> 1) & 1)] = pv[0];
+                    } else if constexpr (NS == 8) {
+                        p[lane & 7] = pv[0];
+                    } else {
+                        p[2 * (lane & 7)] = pv[0];
+                        p[2 * (lane & 7) + 1] = pv[1];
+                    }
+                };
+#define TOKEN(k)                                                                                \
+    {                                                                                           \
+        const f32x4 d = st[buf][tt + k][chl];                                                   \
+        float pv[2 * NS];                                                                       \
+        back_token<NS, NS*(k % KT)>(gr, dA, pv, sB[k], sA[k], aa[tt + k], hh[tt + k],           \
+                                    tt + k == 0 ? hs : hh[tt + k == 0 ? 0 : tt + k - 1], A2,    \
+                                    d[0], d[1], d[2], Bq[k / KT], Cq[k / KT]);                  \
+        channel_sums<2 * NS, NG>(pv, lane);                                                     \
+        store_sums(pv, tt + k);                                                                 \
     }
-    const int64_t so = (b * a.D + ch) * a.N + n0;
-    // the segment's start state (segment 0's kept states hold h0 already)
-    for (int64_t s = 0; s < seg; ++s) {
-        const int64_t o = (b * nseg + s) * a.D + ch;
-        float e[NS];
-        states_load<NS>(e, a.hend + o * a.N + n0, nv);
-        const float sd = live ? a.sdelta[o] : 0.f;
-#pragma unroll
-        for (int j = 0; j < NS; ++j)
-            hin[j] = s == 0 ? e[j]
-                            : __builtin_fmaf(__builtin_amdgcn_exp2f(A2[j] * sd), hin[j], e[j]);
-    }
-    // gr = a_{t+1} g_{t+1} past the segment's last token
-    if (a.dh_final) states_load<NS>(gr, a.dh_final + so, nv);
-    for (int64_t s = nseg - 1; s > seg; --s) {
-        const int64_t o = (b * nseg + s) * a.D + ch;
-        float e[NS];
-        states_load<NS>(e, a.gstart + o * a.N + n0, nv);
-        const float sd = live ? a.sdelta[o] : 0.f;
-#pragma unroll
-        for (int j = 0; j < NS; ++j)
-            gr[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(A2[j] * sd), gr[j], e[j]);
+                TOKEN(3)
+                TOKEN(2)
+                TOKEN(1)
+                TOKEN(0)
+#undef TOKEN
+                float* sp = reinterpret_cast<float*>(&st[buf][tt][chl]);
+                asm("s_nop 1" : "+v"(sB[0]), "+v"(sB[1]), "+v"(sB[2]), "+v"(sB[3]));
+                state_sums<NG>(sB, row, sp, 4 * WC);
+                state_sums<NG>(sA, row, sp + 1, 4 * WC);
+            }
+            __syncthreads();
+        }
+        if (seg == 0 && a.dh0) states_store<NS>(a.dh0 + so, gr, nv);
+        states_store<NS>(part + ch * a.N + n0, dA, nv);
+        __syncthreads();
+        return;
     }
 
     const int srow = tid / TPR, sc = (tid % TPR) * EPT;
     const int sv = ssm_left(Dg, c0 + sc, EPT);
     const int64_t scg = cg + c0 + sc;
-    float dD[EPT], dbias[EPT];
+    float dD[EPT], dbias[EPT], bias[EPT], skip[EPT];
+    small_load<EPT>(bias, a.bias + scg, a.bias ? sv : 0);
+    small_load<EPT>(skip, a.D_skip + scg, a.D_skip ? sv : 0);
 #pragma unroll
     for (int e = 0; e < EPT; ++e) dD[e] = dbias[e] = 0.f;
 
@@ -331,7 +463,6 @@ __global__ __launch_bounds__(256, NS == 16 ? 1 : 2) void ssm_bwd_kernel(SsmBwdAr
     Row<EPT, true, RAG> ro16;
     Row<EPT, false, RAG> ro32;
     Row<4, BF16, RAG> rq[QPT];
-    float kept[NS], ksum = 0.f;
     auto fetch = [&](int64_t sub) {
         const int64_t tb = sub * S, t = tb + srow;
         const int v = t < t1 ? sv : 0;
@@ -351,45 +482,45 @@ __global__ __launch_bounds__(256, NS == 16 ? 1 : 2) void ssm_bwd_kernel(SsmBwdAr
             rq[i].load(isc ? a.Cm : a.Bm,
                        (isc ? b * a.cb + tq * a.ct : b * a.bb + tq * a.bt) + g * a.N + 4 * qn, vq);
         }
-        const int64_t ko = (b * nsub + sub) * a.D + ch;
-        states_load<NS>(kept, a.ckpt + ko * a.N + n0, nv);
-        if (seg > 0) ksum = live ? a.csum[ko] : 0.f;
     };
-
-    const int64_t first = t0 / S, last = (t1 + S - 1) / S;
-    fetch(last - 1);
-    for (int64_t sub = last - 1; sub >= first; --sub) {
-        const int64_t tb = sub * S, t = tb + srow;
-        const int v = t < t1 ? sv : 0;
-        float hs[NS];
+    // of a staged block, until it is finished: x, Delta, its derivative, dy, and
+    // dout (z sigmoid(z))'
+    struct Held {
+        float x[EPT], d[EPT], ddr[EPT], dy[EPT], og[EPT];
+    };
+    auto stage = [&](int64_t sub, Held& k) {
+        const int buf = (int)(sub & 1);
+        const int v = sub * S + srow < t1 ? sv : 0;
+        float r[EPT], z[EPT];
+        rx.unpack(k.x);
+        rt.unpack(r);
+        if (a.dout_bf16)
+            ro16.unpack(k.dy);
+        else
+            ro32.unpack(k.dy);
+        rz.unpack(z);
 #pragma unroll
-        for (int j = 0; j < NS; ++j)
-            hs[j] = seg > 0 ? __builtin_fmaf(__builtin_amdgcn_exp2f(A2[j] * ksum), hin[j], kept[j])
-                            : kept[j];
-        {
-            float x[EPT], r[EPT], o[EPT], z[EPT];
-            rx.unpack(x);
-            rt.unpack(r);
-            if (a.dout_bf16)
-                ro16.unpack(o);
-            else
-                ro32.unpack(o);
-            rz.unpack(z);
-            float bias[EPT], d[EPT], dy[EPT];
-            small_load<EPT>(bias, a.bias + scg, a.bias ? sv : 0);
+        for (int e = 0; e < EPT; ++e) {
+            r[e] += bias[e];
+            k.ddr[e] = 1.f;
+        }
+        ssm_deltas(k.d, r, a.softplus);
+        if (a.softplus) {
 #pragma unroll
-            for (int e = 0; e < EPT; ++e) {
-                r[e] += bias[e];
-                dy[e] = o[e];
-            }
-            ssm_deltas(d, r, a.softplus);
-            if (a.z) ssm_gate(dy, z);
+            for (int e = 0; e < EPT; ++e) k.ddr[e] = sigmoid(r[e]);
+        }
+        if (a.z) {
 #pragma unroll
             for (int e = 0; e < EPT; ++e) {
-                d[e] = e < v ? d[e] : 0.f;
-                st[srow][sc + e] = f32x4{d[e], d[e] * x[e], dy[e], 0.f};
-                raw[srow][sc + e] = f32x4{x[e], r[e], o[e], z[e]};
+                const float sg = sigmoid_fast(z[e]);
+                k.og[e] = k.dy[e] * sg * __builtin_fmaf(z[e], 1.f - sg, 1.f);
+                k.dy[e] *= z[e] * sg;
             }
+        }
+#pragma unroll
+        for (int e = 0; e < EPT; ++e) {
+            k.d[e] = (RAG ? e < v : v > 0) ? k.d[e] : 0.f;
+            st[buf][srow][sc + e] = f32x4{k.d[e], k.d[e] * k.x[e], k.dy[e], 0.f};
         }
 #pragma unroll
         for (int i = 0; i < QPT; ++i) {
@@ -397,126 +528,24 @@ __global__ __launch_bounds__(256, NS == 16 ? 1 : 2) void ssm_bwd_kernel(SsmBwdAr
             if (q >= 2 * NQ) continue;
             float f[4];
             rq[i].unpack(f);
-            *reinterpret_cast<float4*>(&bc[q >= NQ][4 * (q % NQ)]) = float4{f[0], f[1], f[2], f[3]};
+            *reinterpret_cast<float4*>(&bc[buf][q >= NQ][4 * (q % NQ)]) =
+                float4{f[0], f[1], f[2], f[3]};
         }
-        __syncthreads();
-
-        // the block's states again, all kept in registers
-        constexpr auto js = std::make_index_sequence<NS>{};
-        float hh[S][NS], aa[S][NS];
-#pragma unroll
-        for (int tt = 0; tt < S; tt += 4) {
-            float s[4], Bq[4 / KT], Cq[4 / KT];
-#pragma unroll
-            for (int k = 0; k < 4 / KT; ++k) {
-                Bq[k] = row_coef<NS, NG>(bc[0], tt + k * KT, lane);
-                Cq[k] = row_coef<NS, NG>(bc[1], tt + k * KT, lane);
-            }
-            f32x4 d[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) d[k] = st[tt + k][chl];
-#define TOKEN(k) scan_terms<NS, k % KT>(aa[tt + k], hh[tt + k], A2, d[k][0], d[k][1], Bq[k / KT], js)
-            TOKEN(0);
-            TOKEN(1);
-            TOKEN(2);
-            TOKEN(3);
-#undef TOKEN
-#pragma unroll
-            for (int k = tt; k < tt + 4; ++k) {
-#pragma unroll
-                for (int j = 0; j < NS; ++j)
-                    hh[k][j] = __builtin_fmaf(aa[k][j], k ? hh[k ? k - 1 : 0][j] : hs[j], hh[k][j]);
-            }
-            if (a.z) {
-                float h4[4][NS];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-#pragma unroll
-                    for (int j = 0; j < NS; ++j) h4[k][j] = hh[tt + k][j];
-                row_dots<NS>(s, Cq, h4);
-                state_sums<NG>(s, row, reinterpret_cast<float*>(&st[tt][chl]) + 3, 4 * WC);
-            }
-        }
-        // and backwards
-#pragma unroll
-        for (int tt = S - 4; tt >= 0; tt -= 4) {
-            // half of the kept states are done with: the next block's loads
-            // take their registers
-            if (tt == (S / 2 - 4 > 0 ? S / 2 - 4 : 0) && sub > first) fetch(sub - 1);
-            float sB[4], sA[4], Bq[4 / KT], Cq[4 / KT];
-#pragma unroll
-            for (int k = 0; k < 4 / KT; ++k) {
-                Bq[k] = row_coef<NS, NG>(bc[0], tt + k * KT, lane);
-                Cq[k] = row_coef<NS, NG>(bc[1], tt + k * KT, lane);
-            }
-#define TOKEN(k)                                                                                \
-    {                                                                                           \
-        const f32x4 d = st[tt + k][chl];                                                        \
-        float pv[2 * NS];                                                                       \
-        back_token<NS, NS*(k % KT)>(gr, dA, pv, sB[k], sA[k], aa[tt + k], hh[tt + k],           \
-                                    tt + k == 0 ? hs : hh[tt + k == 0 ? 0 : tt + k - 1], A2,    \
-                                    d[0], d[1], d[2], Bq[k / KT], Cq[k / KT]);                  \
-        channel_sums<2 * NS, NG>(pv, lane);                                                     \
-        store_sums(pv, tt + k);                                                                 \
-    }
-            // lane bits 3 .. 0 chose the value: of dC or dB, then its state
-            auto store_sums = [&](const float(&pv)[2 * NS], int q) {
-                float* p = pbc[wv][q] + ((lane >> 3) & 1) * NP + n0;
-                if constexpr (NS == 4) {
-                    if ((lane & 1) == 0 && row < NG) p[((lane >> 2) & 1) * 2 + ((lane >> 1) & 1)] = pv[0];
-                } else if constexpr (NS == 8) {
-                    p[lane & 7] = pv[0];
-                } else {
-                    p[2 * (lane & 7)] = pv[0];
-                    p[2 * (lane & 7) + 1] = pv[1];
-                }
-            };
-            TOKEN(3)
-            TOKEN(2)
-            TOKEN(1)
-            TOKEN(0)
-#undef TOKEN
-            float* sp = reinterpret_cast<float*>(&st[tt][chl]);
-            asm("s_nop 1" : "+v"(sB[0]), "+v"(sB[1]), "+v"(sB[2]), "+v"(sB[3]));
-            state_sums<NG>(sB, row, sp, 4 * WC);
-            state_sums<NG>(sA, row, sp + 1, 4 * WC);
-        }
-        __syncthreads();
-
+    };
+    auto finish = [&](int64_t sub, const Held& k) {
+        const int buf = (int)(sub & 1);
+        const int64_t tb = sub * S, t = tb + srow;
+        const int v = t < t1 ? sv : 0;
         if (v > 0) {
-            float dxv[EPT], dtv[EPT], dzv[EPT], d[EPT], r[EPT], dy[EPT], skip[EPT];
-            f32x4 q[EPT], in[EPT];
-            small_load<EPT>(skip, a.D_skip + scg, a.D_skip ? sv : 0);
+            float dxv[EPT], dtv[EPT], dzv[EPT];
 #pragma unroll
             for (int e = 0; e < EPT; ++e) {
-                q[e] = st[srow][sc + e];
-                in[e] = raw[srow][sc + e];
-                r[e] = in[e][1];
-                dy[e] = in[e][2];
-            }
-            ssm_deltas(d, r, a.softplus);
-            if (a.z) {
-#pragma unroll
-                for (int e = 0; e < EPT; ++e) {
-                    const float z = in[e][3], sg = sigmoid_fast(z);
-                    const float y = __builtin_fmaf(skip[e], in[e][0], q[e][3]);
-                    dzv[e] = dy[e] * y * sg * __builtin_fmaf(z, 1.f - sg, 1.f);
-                    dy[e] *= z * sg;
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < EPT; ++e) {
-                dxv[e] = __builtin_fmaf(d[e], q[e][0], skip[e] * dy[e]);
-                dtv[e] = __builtin_fmaf(in[e][0], q[e][0], q[e][1] * kLn2);
-            }
-            if (a.softplus) {
-#pragma unroll
-                for (int e = 0; e < EPT; ++e) dtv[e] *= sigmoid(r[e]);
-            }
-#pragma unroll
-            for (int e = 0; e < EPT; ++e) {
-                if (e < v) {
-                    dD[e] = __builtin_fmaf(dy[e], in[e][0], dD[e]);
+                const f32x4 q = st[buf][srow][sc + e];
+                dxv[e] = __builtin_fmaf(k.d[e], q[0], skip[e] * k.dy[e]);
+                dtv[e] = __builtin_fmaf(k.x[e], q[0], q[1] * kLn2) * k.ddr[e];
+                dzv[e] = k.og[e] * __builtin_fmaf(skip[e], k.x[e], q[3]);
+                if (!RAG || e < v) {
+                    dD[e] = __builtin_fmaf(k.dy[e], k.x[e], dD[e]);
                     dbias[e] += dtv[e];
                 }
             }
@@ -526,18 +555,31 @@ __global__ __launch_bounds__(256, NS == 16 ? 1 : 2) void ssm_bwd_kernel(SsmBwdAr
             if (a.z) row_store<EPT, RAG>(a.dz, oo, a.grad_bf16, dzv, v);
         }
         for (int i = tid; i < S * 2 * NP; i += 256) {
-            const int q = i / (2 * NP), k = i % (2 * NP);
+            const int q = i / (2 * NP), c = i % (2 * NP);
             if (tb + q < t1)
-                a.bcpart[(((blk * a.B + b) * a.T + tb + q) * a.G + g) * 2 * NP + k] =
-                    (pbc[0][q][k] + pbc[1][q][k]) + (pbc[2][q][k] + pbc[3][q][k]);
+                a.bcpart[(((blk * a.B + b) * a.T + tb + q) * a.G + g) * 2 * NP + c] =
+                    (pbc[buf][0][q][c] + pbc[buf][1][q][c]) + (pbc[buf][2][q][c] + pbc[buf][3][q][c]);
+        }
+    };
+    Held now, next;
+    fetch(last);
+    stage(last, now);
+    if (last > first) fetch(last - 1);
+    __syncthreads();
+    for (int64_t sub = last; sub >= first; --sub) {
+        // while block sub runs; block sub + 1, which shares sub - 1's buffers,
+        // is finished already
+        if (sub > first) {
+            stage(sub - 1, next);
+            if (sub - 1 > first) fetch(sub - 2);
         }
         __syncthreads();
+        finish(sub, now);
+        now = next;
     }
-    if (seg == 0 && a.dh0) states_store<NS>(a.dh0 + so, gr, nv);
-    float* part = a.part + (b * nseg + seg) * a.D * (a.N + 2);
-    states_store<NS>(part + ch * a.N + n0, dA, nv);
-    // dD and dbias over the thread rows of a channel, through st
-    float* red = reinterpret_cast<float*>(st);
+    // dD and dbias over the thread rows of a channel, through the buffer that
+    // the last block did not use (block `first` may not be finished yet)
+    float* red = reinterpret_cast<float*>(st[(first & 1) ^ 1]);
 #pragma unroll
     for (int e = 0; e < EPT; ++e) {
         red[srow * 2 * WC + sc + e] = dD[e];
@@ -623,14 +665,14 @@ template <int NS, int NG, bool BF16, bool RAG>
 hipError_t launch_bwd_r(const SsmBwdArgs& a, const SsmPlan& p) {
     const dim3 grid((unsigned)(a.B * a.G * p.nblk * p.nseg));
     if (p.nseg > 1)
-        hipLaunchKernelGGL((ssm_bwd_states_kernel<NS, NG, true, BF16, RAG>), grid, dim3(256), 0,
+        hipLaunchKernelGGL((ssm_bwd_states_kernel<NS, NG, true, BF16, RAG>), grid, dim3(512), 0,
                            a.stream, a, p.nblk, p.nseg, p.L);
     else
-        hipLaunchKernelGGL((ssm_bwd_states_kernel<NS, NG, false, BF16, RAG>), grid, dim3(256), 0,
+        hipLaunchKernelGGL((ssm_bwd_states_kernel<NS, NG, false, BF16, RAG>), grid, dim3(512), 0,
                            a.stream, a, p.nblk, p.nseg, p.L);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((ssm_bwd_kernel<NS, NG, BF16, RAG>), grid, dim3(256), 0, a.stream, a,
+    hipLaunchKernelGGL((ssm_bwd_kernel<NS, NG, BF16, RAG>), grid, dim3(512), 0, a.stream, a,
                        p.nblk, p.nseg, p.L);
     return hipGetLastError();
 }
@@ -662,7 +704,8 @@ size_t ssm_bwd_workspace_bytes(int64_t B, int64_t T, int64_t D, int64_t G, int64
 
 int64_t ssm_bwd_workgroups(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N) {
     const SsmPlan p = bwd_plan(B, T, D, G, N);
-    const int64_t n = B * G * p.nblk * p.nseg, r = cdiv(B * T * G * 2 * padded_states(N), 256);
+    const int64_t n = 2 * B * G * p.nblk * p.nseg;    // of 512 threads
+    const int64_t r = cdiv(B * T * G * 2 * padded_states(N), 256);
     return n > r ? n : r;
 }
 
