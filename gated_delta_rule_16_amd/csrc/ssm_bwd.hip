@@ -250,29 +250,70 @@ __device__ __forceinline__ void back_token(float (&gr)[NS], float (&dA)[NS], flo
     }
 }
 
-// Halving reduction of M values over the 16 lanes of each row, then (NG < 4)
-// over the rows that hold other channels.  Lane bits 3, 2, 1, 0 choose the
-// value that a lane is left with; at M = 8 bit 0 chooses nothing, at M = 32
-// two values are left.
-template <int M, int NG>
-__device__ __forceinline__ void channel_sums(float (&v)[M], int lane) {
-    constexpr int M1 = M / 2, M2 = M / 4, M3 = M / 8, M4 = M / 16;
-#pragma unroll
-    for (int i = 0; i < M1; ++i) v[i] = fold<3>(v[i], v[i + M1], lane & 8);
-#pragma unroll
-    for (int i = 0; i < M2; ++i) v[i] = fold<2>(v[i], v[i + M2], lane & 4);
-#pragma unroll
-    for (int i = 0; i < M3; ++i) v[i] = fold<1>(v[i], v[i + M3], lane & 2);
-    if constexpr (M4 > 0) {
-#pragma unroll
-        for (int i = 0; i < M4; ++i) v[i] = fold<0>(v[i], v[i + M4], lane & 1);
+// The first two steps of a halving reduction over a row of 16 lanes, 8 values
+// to 2: lane bits 3 and 2 tell banks of 4 lanes apart, so a DPP add under a
+// bank mask writes each half, two instructions a value and no select.  Lanes
+// are left with values (v[0], v[1]) + 4 (lane bit 3) + 2 (lane bit 2).  Every
+// operand of a DPP read is written three instructions or more before it.
+__device__ __forceinline__ void row_fold_8(float (&q)[2], const float (&v)[8]) {
+    float t0, t1, t2, t3;
+#define BOTH(o, x, y, pair, lo, hi)                                                      \
+    "v_add_f32_dpp " o ", " x ", " x " " pair " row_mask:0xf bank_mask:" lo "\n\t"       \
+    "v_add_f32_dpp " o ", " y ", " y " " pair " row_mask:0xf bank_mask:" hi "\n\t"
+    asm("s_nop 1\n\t" BOTH("%2", "%6", "%10", "row_ror:8", "0x3", "0xc")
+            BOTH("%4", "%8", "%12", "row_ror:8", "0x3", "0xc")
+                BOTH("%3", "%7", "%11", "row_ror:8", "0x3", "0xc")
+                    BOTH("%5", "%9", "%13", "row_ror:8", "0x3", "0xc")
+                        BOTH("%0", "%2", "%4", "row_half_mirror", "0x5", "0xa")
+                            BOTH("%1", "%3", "%5", "row_half_mirror", "0x5", "0xa") "s_nop 1"
+        : "=&v"(q[0]), "=&v"(q[1]), "=&v"(t0), "=&v"(t1), "=&v"(t2), "=&v"(t3)
+        : "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3]), "v"(v[4]), "v"(v[5]), "v"(v[6]),
+          "v"(v[7]));
+#undef BOTH
+}
+
+// Sums of a token pair's values (the token at q, and the next) over a wave's
+// channels: pv[0 .. NS) for dC, the rest for dB.  Lane bits 3 .. 0 choose what
+// a lane is left with; at NS = 4 bit 0 chooses the token.  Lanes (and rows, NG
+// < 4) that are left with the same sum store it twice.
+template <int NS, int NG>
+__device__ __forceinline__ void channel_sums(float (*p)[2 * NS * NG], const float (&p0)[2 * NS],
+                                             const float (&p1)[2 * NS], int lane, int n0) {
+    constexpr int NP = NS * NG;
+    const int half = ((lane >> 3) & 1) * NP + n0;
+    auto rows = [](float x) {
+        if constexpr (NG <= 2) x = fold32(x, x);
+        if constexpr (NG <= 1) x = fold16(x, x);
+        return x;
+    };
+    if constexpr (NS == 4) {
+        float q0[2], q1[2];
+        row_fold_8(q0, p0);
+        row_fold_8(q1, p1);
+        const float a = fold<1>(q0[0], q0[1], lane & 2), b = fold<1>(q1[0], q1[1], lane & 2);
+        p[lane & 1][half + ((lane >> 2) & 1) * 2 + ((lane >> 1) & 1)] =
+            rows(fold<0>(a, b, lane & 1));
     } else {
-        v[0] += pair_lane<0>(v[0]);
-    }
+        // 8 values at a time: of dC and dB the states 4 i .. 4 i + 3, folded to 2
 #pragma unroll
-    for (int i = 0; i < (M4 > 0 ? M4 : 1); ++i) {
-        if constexpr (NG <= 2) v[i] = fold32(v[i], v[i]);
-        if constexpr (NG <= 1) v[i] = fold16(v[i], v[i]);
+        for (int k = 0; k < 2; ++k) {
+            const float(&pv)[2 * NS] = k ? p1 : p0;
+            float w[NS / 4];
+#pragma unroll
+            for (int i = 0; i < NS / 4; ++i) {
+                const float v[8] = {pv[4 * i],          pv[4 * i + 1],      pv[4 * i + 2],
+                                    pv[4 * i + 3],      pv[NS + 4 * i],     pv[NS + 4 * i + 1],
+                                    pv[NS + 4 * i + 2], pv[NS + 4 * i + 3]};
+                float q[2];
+                row_fold_8(q, v);
+                w[i] = fold<1>(q[0], q[1], lane & 2);
+            }
+            // bit 0 chooses the group of four states of a pair of groups
+#pragma unroll
+            for (int i = 0; i < NS / 8; ++i)
+                p[k][half + 8 * i + 4 * (lane & 1) + ((lane >> 2) & 1) * 2 + ((lane >> 1) & 1)] =
+                    rows(fold<0>(w[2 * i], w[2 * i + 1], lane & 1));
+        }
     }
 }
 
@@ -403,39 +444,25 @@ __global__ __launch_bounds__(512, NS == 16 ? 1 : 2) void ssm_bwd_kernel(SsmBwdAr
                 // half of the kept states are done with: the next block's
                 // start takes their registers
                 if (tt == (S / 2 - 4 > 0 ? S / 2 - 4 : 0) && sub > first) fetch(sub - 1);
-                float sB[4], sA[4], Bq[4 / KT], Cq[4 / KT];
+                float sB[4], sA[4], Bq[4 / KT], Cq[4 / KT], pv[4][2 * NS];
+                f32x4 d[4];
 #pragma unroll
                 for (int k = 0; k < 4 / KT; ++k) {
                     Bq[k] = row_coef<NS, NG>(bc[buf][0], tt + k * KT, lane);
                     Cq[k] = row_coef<NS, NG>(bc[buf][1], tt + k * KT, lane);
                 }
-                // lane bits 3 .. 0 chose the value: of dC or dB, then its state
-                auto store_sums = [&](const float(&pv)[2 * NS], int q) {
-                    float* p = pbc[buf][wv][q] + ((lane >> 3) & 1) * NP + n0;
-                    if constexpr (NS == 4) {
-                        if ((lane & 1) == 0 && row < NG)
-                            p[((lane >> 2) & 1) * 2 + ((lane >> 1) & 1)] = pv[0];
-                    } else if constexpr (NS == 8) {
-                        p[lane & 7] = pv[0];
-                    } else {
-                        p[2 * (lane & 7)] = pv[0];
-                        p[2 * (lane & 7) + 1] = pv[1];
-                    }
-                };
-#define TOKEN(k)                                                                                \
-    {                                                                                           \
-        const f32x4 d = st[buf][tt + k][chl];                                                   \
-        float pv[2 * NS];                                                                       \
-        back_token<NS, NS*(k % KT)>(gr, dA, pv, sB[k], sA[k], aa[tt + k], hh[tt + k],           \
-                                    tt + k == 0 ? hs : hh[tt + k == 0 ? 0 : tt + k - 1], A2,    \
-                                    d[0], d[1], d[2], Bq[k / KT], Cq[k / KT]);                  \
-        channel_sums<2 * NS, NG>(pv, lane);                                                     \
-        store_sums(pv, tt + k);                                                                 \
-    }
-                TOKEN(3)
-                TOKEN(2)
-                TOKEN(1)
-                TOKEN(0)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) d[k] = st[buf][tt + k][chl];
+#define TOKEN(k)                                                                               \
+    back_token<NS, NS*(k % KT)>(gr, dA, pv[k], sB[k], sA[k], aa[tt + k], hh[tt + k],           \
+                                tt + k == 0 ? hs : hh[tt + k == 0 ? 0 : tt + k - 1], A2,       \
+                                d[k][0], d[k][1], d[k][2], Bq[k / KT], Cq[k / KT])
+                TOKEN(3);
+                TOKEN(2);
+                channel_sums<NS, NG>(&pbc[buf][wv][tt + 2], pv[2], pv[3], lane, n0);
+                TOKEN(1);
+                TOKEN(0);
+                channel_sums<NS, NG>(&pbc[buf][wv][tt], pv[0], pv[1], lane, n0);
 #undef TOKEN
                 float* sp = reinterpret_cast<float*>(&st[buf][tt][chl]);
                 asm("s_nop 1" : "+v"(sB[0]), "+v"(sB[1]), "+v"(sB[2]), "+v"(sB[3]));
