@@ -9,9 +9,11 @@
 //
 // Bound by HBM: one pass over each tensor.  A row is held in registers
 // between its two reductions (mean, then the centred squares, so there is no
-// cancellation of mean squares): one wave per row up to 2048 channels, with no
-// barrier; one workgroup of four waves per row up to 8192; beyond that the
-// workgroup walks the row again (from L2) for each reduction.
+// cancellation of mean squares): one wave per row up to 2048 channels (1024
+// backward), with no barrier; one workgroup of four waves per row up to 8192;
+// beyond that the workgroup walks the row again (from L2) for each reduction.
+// 32768 rows of 2048 in bf16 with the residual stream: forward 99 us (5.4
+// TB/s), backward 111 us (4.8 TB/s; a copy reaches 4.9 on the same card).
 #include "launch.h"
 #include "rows.h"
 
@@ -43,6 +45,22 @@ __device__ __forceinline__ float row_total(float x, float* red) {
         x = (red[0] + red[1]) + (red[2] + red[3]);
     }
     return x;
+}
+
+// Three sums at once.
+template <bool WG>
+__device__ __forceinline__ void row_totals(float (&x)[3], float (*red)[4]) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) x[i] = wave_sum(x[i]);
+    if constexpr (WG) {
+        if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+            for (int i = 0; i < 3; ++i) red[i][threadIdx.x >> 6] = x[i];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 3; ++i) x[i] = (red[i][0] + red[i][1]) + (red[i][2] + red[i][3]);
+    }
 }
 
 __device__ __forceinline__ int left(int64_t C, int64_t c) {
@@ -80,7 +98,9 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormArgs a) {
     __shared__ float red[2][4];
     constexpr int NT = WG ? 256 : 64;
     const int id = WG ? threadIdx.x : (threadIdx.x & 63);
-    const int64_t row = WG ? blockIdx.x : (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int64_t row = WG ? blockIdx.x
+                           : (int64_t)blockIdx.x * 4 +
+                                 __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (row >= a.R) return;           // a whole wave (WG: never)
     float h[NV][E];
     float s = 0.f;
@@ -185,14 +205,17 @@ __global__ __launch_bounds__(256) void norm_fwd_long_kernel(NormArgs a) {
 
 // Backward: a persistent grid walks the rows; dw and db stay in registers
 // over all rows of a wave (WG: of the workgroup) and leave as one partial row
-// [2 C] per workgroup.
+// [2 C] per workgroup.  From 1024 channels on the workgroup shares a row: a
+// wave that holds 2048 channels of three tensors, their sums and the next row
+// leaves one wave per SIMD (32768 rows of 2048 in bf16: 126 us without
+// the next row's loads, 152 with them, 111 shared).
 template <int NV, bool WG, bool BF16, bool DY16, bool G16, bool RAG>
 __global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwdArgs a) {
     __shared__ float red[4][4];
     __shared__ float join[WG ? 1 : 3 * 64 * (2 * E + 1)];
     constexpr int NT = WG ? 256 : 64;
     const int id = WG ? threadIdx.x : (threadIdx.x & 63);
-    const int wv = threadIdx.x >> 6;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     float dw[NV][E], db[NV][E];
 #pragma unroll
     for (int k = 0; k < NV; ++k)
@@ -200,11 +223,10 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwdArgs a) {
         for (int e = 0; e < E; ++e) dw[k][e] = db[k][e] = 0.f;
     const float inv = 1.f / (float)a.C;
     const int64_t stride = (int64_t)gridDim.x * (WG ? 1 : 4);
-    for (int64_t row = WG ? blockIdx.x : (int64_t)blockIdx.x * 4 + wv; row < a.R; row += stride) {
-        float h[NV][E], d[NV][E];
-        Row<E, BF16, RAG> rh[NV];
-        Row<E, DY16, RAG> rd[NV];
-        Row<E, G16, RAG> rr[NV];
+    Row<E, BF16, RAG> rh[NV];
+    Row<E, DY16, RAG> rd[NV];
+    Row<E, G16, RAG> rr[NV];
+    auto fetch = [&](int64_t row) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int64_t c = (int64_t)(k * NT + id) * E;
@@ -213,42 +235,48 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwdArgs a) {
             rd[k].load(a.dy, row * a.yr + c, v);
             rr[k].load(a.dres, row * a.rr + c, a.dres ? v : 0);
         }
+    };
+    int64_t row = WG ? blockIdx.x : (int64_t)blockIdx.x * 4 + wv;
+    if (row < a.R) fetch(row);
+    for (; row < a.R; row += stride) {
+        float h[NV][E], d[NV][E], q[NV][E];
         float s = 0.f;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             rh[k].unpack(h[k]);
+            rd[k].unpack(d[k]);
+            rr[k].unpack(q[k]);
 #pragma unroll
             for (int e = 0; e < E; ++e) s += h[k][e];
         }
+        // the next row's loads land while this one is worked on
+        if (row + stride < a.R) fetch(row + stride);
         const float mu = row_total<WG>(s, red[0]) * inv;
-        s = 0.f;
-        float s1 = 0.f, s2 = 0.f;
+        float sums[3] = {0.f, 0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int64_t c = (int64_t)(k * NT + id) * E;
             const int v = left(a.C, c);
             float w[E];
-            rd[k].unpack(d[k]);
             if (a.w) param_load<E>(w, a.w + c, v);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 h[k][e] = e < v ? h[k][e] - mu : 0.f;
-                s = __builtin_fmaf(h[k][e], h[k][e], s);
+                sums[0] = __builtin_fmaf(h[k][e], h[k][e], sums[0]);
                 const float dn = a.w ? d[k][e] * w[e] : d[k][e];
-                s1 += dn;
-                s2 = __builtin_fmaf(dn, h[k][e], s2);
+                sums[1] += dn;
+                sums[2] = __builtin_fmaf(dn, h[k][e], sums[2]);
             }
         }
-        const float rstd = 1.f / sqrtf(row_total<WG>(s, red[1]) * inv + a.eps);
-        const float m1 = row_total<WG>(s1, red[2]) * inv;
-        const float m2 = row_total<WG>(s2, red[3]) * inv * rstd;
+        row_totals<WG>(sums, red + 1);
+        const float rstd = 1.f / sqrtf(sums[0] * inv + a.eps);
+        const float m1 = sums[1] * inv, m2 = sums[2] * inv * rstd;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int64_t c = (int64_t)(k * NT + id) * E;
             const int v = left(a.C, c);
-            float w[E], out[E], q[E];
+            float w[E], out[E];
             if (a.w) param_load<E>(w, a.w + c, v);
-            rr[k].unpack(q);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 const float n = h[k][e] * rstd;
@@ -256,7 +284,7 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwdArgs a) {
                 dw[k][e] = __builtin_fmaf(d[k][e], n, dw[k][e]);
                 db[k][e] += d[k][e];
                 out[e] = rstd * (dn - m1 - n * m2);
-                out[e] += q[e];
+                out[e] += q[k][e];
             }
             row_store<E, RAG>(a.dx, row * a.C + c, G16, out, v);
         }
@@ -370,7 +398,7 @@ template <bool BF16, bool DY16>
 __global__ __launch_bounds__(256) void norm_dw_long_kernel(NormBwdArgs a, const float* stats,
                                                            int64_t ncb, int64_t nrow) {
     __shared__ float join[3 * 64 * (2 * E + 1)];
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t cb = blockIdx.x % ncb, slot = blockIdx.x / ncb;
     const int64_t c = (cb * 64 + lane) * E;
     const int v = left(a.C, c);
@@ -419,7 +447,7 @@ __global__ __launch_bounds__(256) void norm_dw_long_kernel(NormBwdArgs a, const 
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-constexpr int64_t WAVE_MAX = 2048, WG_MAX = 8192;
+constexpr int64_t WG_MAX = 8192;
 
 // Workgroups of the backward (= partial rows).
 int64_t bwd_rows(int64_t R, int64_t C) {
@@ -428,8 +456,13 @@ int64_t bwd_rows(int64_t R, int64_t C) {
         const int64_t n = cdiv(R, 16);
         return n < cap ? n : cap;
     }
-    const int64_t n = C <= WAVE_MAX ? cdiv(R, 4) : R;
-    return n < 512 ? n : 512;
+    // a wave (up to 1024 channels) or the workgroup per row.  1024 workgroups
+    // fill the chip evenly, four to a compute unit (32768 rows of 2048 in bf16:
+    // 111 us; 139 with 512, 152 with 1536); fewer rows take fewer, so that the
+    // partials stay a small part of the traffic
+    const int64_t per = C <= 1024 ? 4 : 1, most = cdiv(R, per), want = cdiv(R, 16 * per);
+    const int64_t n = want < 256 ? 256 : want > 1024 ? 1024 : want;
+    return n < most ? n : most;
 }
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -450,7 +483,7 @@ void fwd_t(const NormArgs& a) {
     const dim3 wave((unsigned)cdiv(a.R, 4)), wg((unsigned)a.R);
     if (C <= 512) fwd_r<1, false, BF16, RES>(a, wave);
     else if (C <= 1024) fwd_r<2, false, BF16, RES>(a, wave);
-    else if (C <= WAVE_MAX) fwd_r<4, false, BF16, RES>(a, wave);
+    else if (C <= 2048) fwd_r<4, false, BF16, RES>(a, wave);
     else if (C <= 4096) fwd_r<2, true, BF16, RES>(a, wg);
     else if (C <= WG_MAX) fwd_r<4, true, BF16, RES>(a, wg);
     else
@@ -480,7 +513,7 @@ void bwd_t(const NormBwdArgs& a) {
     const dim3 grid((unsigned)nrow);
     if (C <= 512) bwd_r<1, false, BF16, DY16, G16>(a, grid);
     else if (C <= 1024) bwd_r<2, false, BF16, DY16, G16>(a, grid);
-    else if (C <= WAVE_MAX) bwd_r<4, false, BF16, DY16, G16>(a, grid);
+    else if (C <= 2048) bwd_r<1, true, BF16, DY16, G16>(a, grid);
     else if (C <= 4096) bwd_r<2, true, BF16, DY16, G16>(a, grid);
     else if (C <= WG_MAX) bwd_r<4, true, BF16, DY16, G16>(a, grid);
     else {

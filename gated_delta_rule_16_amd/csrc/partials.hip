@@ -9,27 +9,33 @@ namespace gdr {
 namespace {
 
 // out[m] = sum over p of part[p][m], one lane per m: a workgroup owns 64
-// columns, each of its four waves every fourth p, joined through LDS.  The
-// columns are cut into up to three outputs.
-__global__ __launch_bounds__(256) void sum_partials_kernel(const float* __restrict__ part,
-                                                           int64_t P, int64_t M, float* o0,
-                                                           int64_t m0, float* o1, int64_t m1,
-                                                           float* o2) {
-    __shared__ float red[4][64];
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+// columns, each of its W waves every W-th p (8 loads in flight), joined through
+// LDS.  The columns are cut into up to three outputs.
+template <int W>
+__global__ __launch_bounds__(64 * W) void sum_partials_kernel(const float* __restrict__ part,
+                                                              int64_t P, int64_t M, float* o0,
+                                                              int64_t m0, float* o1, int64_t m1,
+                                                              float* o2) {
+    __shared__ float red[W][64];
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t m = (int64_t)blockIdx.x * 64 + lane;
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (m < M) {
         int64_t p = wv;
-        for (; p + 12 < P; p += 16)
+        for (; p + 7 * W < P; p += 8 * W)
 #pragma unroll
-            for (int u = 0; u < 4; ++u) s[u] += part[(p + 4 * u) * M + m];
-        for (; p < P; p += 4) s[0] += part[p * M + m];
+            for (int u = 0; u < 8; ++u) s[u] += part[(p + u * W) * M + m];
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (p + u * W < P) s[u] += part[(p + u * W) * M + m];
     }
-    red[wv][lane] = (s[0] + s[1]) + (s[2] + s[3]);
+    red[wv][lane] = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
     __syncthreads();
     if (wv == 0 && m < M) {
-        const float v = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < W; w += 4)
+            v += (red[w][lane] + red[w + 1][lane]) + (red[w + 2][lane] + red[w + 3][lane]);
         if (m < m0) {
             if (o0) o0[m] = v;
         } else if (m < m0 + m1) {
@@ -44,8 +50,14 @@ __global__ __launch_bounds__(256) void sum_partials_kernel(const float* __restri
 
 hipError_t launch_sum_partials(const float* part, int64_t P, int64_t M, float* o0, int64_t m0,
                                float* o1, int64_t m1, float* o2, hipStream_t st) {
-    hipLaunchKernelGGL(sum_partials_kernel, dim3((unsigned)((M + 63) / 64)), dim3(256), 0, st,
-                       part, P, M, o0, m0, o1, m1, o2);
+    const dim3 grid((unsigned)((M + 63) / 64));
+    // many rows: 16 waves a workgroup (1024 rows of 4096: 17 -> 6 us)
+    if (P >= 64)
+        hipLaunchKernelGGL((sum_partials_kernel<16>), grid, dim3(1024), 0, st, part, P, M, o0, m0,
+                           o1, m1, o2);
+    else
+        hipLaunchKernelGGL((sum_partials_kernel<4>), grid, dim3(256), 0, st, part, P, M, o0, m0, o1,
+                           m1, o2);
     return hipGetLastError();
 }
 
