@@ -730,7 +730,7 @@ def gdr2_chunk_bwd_split(q, k, v, alpha, erase, write, s0, dout, ds_final=None, 
 def _like(name, t, dtype, shape, device):
     """A tensor of this type and shape on ``device``."""
     if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and
-            t.device == device):
+            t.get_device() == device.index):
         return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -748,7 +748,10 @@ def _row_strides(name, t, lead):
     """Element strides of the ``lead`` leading dimensions; the others must be
     contiguous."""
     st = t.stride()
-    if t.is_contiguous():
+    if len(st) == lead + 1:
+        if st[-1] == 1:
+            return st[:lead]
+    elif st[-1] == 1 and st[-2] == t.shape[-1]:
         return st[:lead]
     shape = t.shape
     want = 1
@@ -806,9 +809,12 @@ def _dt_of(name, dtype):
     return _DT[dtype]
 
 
-def _buffer(name, t, dtype, shape, device):
-    """A given output buffer, checked, or a new one."""
+def _buffer(name, t, dtype, shape, device, like=None):
+    """A given output buffer, checked, or a new one (``like``: a tensor that may
+    have its type and shape already, which is the quicker way to one)."""
     if t is None:
+        if like is not None and like.dtype is dtype and like.shape == shape and like.is_contiguous():
+            return torch.empty_like(like)
         return torch.empty(shape, dtype=dtype, device=device)
     _whole(name, t, dtype, shape, device)
     return t
@@ -853,9 +859,9 @@ def gdr_short_conv_fwd(x, w, bias=None, s0=None, *, silu=True, out_dtype=None, y
         _whole("s0", s0, x.dtype, (B, K - 1, C), dev)
     odt = out_dtype or (x.dtype if y is None else y.dtype)
     code = _dt_of("output dtype", odt)
-    y = _buffer("y", y, odt, (B, T, C), dev)
+    y = _buffer("y", y, odt, (B, T, C), dev, x)
     if s_final is not None or want_state:
-        s_final = _buffer("s_final", s_final, x.dtype, (B, max(K - 1, 0), C), dev)
+        s_final = _buffer("s_final", s_final, x.dtype, (B, max(K - 1, 0), C), dev, s0)
     _run("gdr_short_conv_fwd", lib.gdr_short_conv_fwd(
         B, T, C, K, _DT[x.dtype], _p(x), _i64s(*xs), _p(w), _p(bias), _p(s0),
         GDR_CONV_SILU if silu else 0, code, _p(y), _p(s_final), _raw_stream(dev.index)))
@@ -878,7 +884,7 @@ def gdr_short_conv_step(x, w, bias, state, *, silu=True, out_dtype=None, y=None,
     _whole("state", state, x.dtype, (N, K - 1, C), dev)
     odt = out_dtype or (x.dtype if y is None else y.dtype)
     code = _dt_of("output dtype", odt)
-    y = _buffer("y", y, odt, (N, C), dev)
+    y = _buffer("y", y, odt, (N, C), dev, x)
     _run("gdr_short_conv_step", lib.gdr_short_conv_step(
         N, C, K, _DT[x.dtype], _p(x), xs[0], _p(w), _p(bias), _p(state),
         GDR_CONV_SILU if silu else 0, code, _p(y), _raw_stream(dev.index)))
@@ -940,16 +946,20 @@ def _ssm_inputs(x, dt, A, Bm, Cm, D, z, dt_bias, lead):
         raise ValueError("Bm must be [..., G, N]")
     Dn, N = A.shape
     G = Bm.shape[-2]
-    rows = x.shape[:lead]
-    dtype = x.dtype
-    st = []
-    for name, t, tail in (("x", x, (Dn,)), ("dt", dt, (Dn,)), ("Bm", Bm, (G, N)),
-                          ("Cm", Cm, (G, N)), ("z", z, (Dn,))):
-        if t is None and name == "z":
-            st += [0] * lead
-            continue
-        _like(name, t, dtype, rows + tail, dev)
-        st += _row_strides(name, t, lead)
+    dtype, shape = x.dtype, x.shape
+    rows = shape[:lead]
+    if shape[-1] != Dn:
+        raise ValueError(f"x must have {Dn} channels, got {shape[-1]}")
+    _like("dt", dt, dtype, shape, dev)
+    _like("Bm", Bm, dtype, rows + (G, N), dev)
+    _like("Cm", Cm, dtype, Bm.shape, dev)
+    st = [*_row_strides("x", x, lead), *_row_strides("dt", dt, lead),
+          *_row_strides("Bm", Bm, lead), *_row_strides("Cm", Cm, lead)]
+    if z is None:
+        st += [0] * lead
+    else:
+        _like("z", z, dtype, shape, dev)
+        st += _row_strides("z", z, lead)
     _whole("A", A, torch.float32, (Dn, N), dev)
     if D is not None:
         _whole("D", D, torch.float32, (Dn,), dev)
@@ -981,9 +991,9 @@ def gdr_ssm_scan_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, h0=None, *,
     odt = out_dtype or (x.dtype if y is None else y.dtype)
     code = _dt_of("output dtype", odt)
     need = gdr_ssm_scan_fwd_workspace_size(B, T, Dn, G, N)
-    y = _buffer("y", y, odt, (B, T, Dn), dev)
+    y = _buffer("y", y, odt, (B, T, Dn), dev, dt)
     if h_final is not None or want_state:
-        h_final = _buffer("h_final", h_final, torch.float32, (B, Dn, N), dev)
+        h_final = _buffer("h_final", h_final, torch.float32, (B, Dn, N), dev, h0)
     if need or workspace is not None:
         workspace = _scratch(workspace, need, dev)
     _run("gdr_ssm_scan_fwd", lib.gdr_ssm_scan_fwd(
@@ -1003,7 +1013,7 @@ def gdr_ssm_step(x, dt, A, Bm, Cm, state, D=None, z=None, dt_bias=None, *, softp
     _whole("state", state, torch.float32, (Nq, Dn, N), dev)
     odt = out_dtype or (x.dtype if y is None else y.dtype)
     code = _dt_of("output dtype", odt)
-    y = _buffer("y", y, odt, (Nq, Dn), dev)
+    y = _buffer("y", y, odt, (Nq, Dn), dev, dt)
     _run("gdr_ssm_step", lib.gdr_ssm_step(
         Nq, Dn, G, N, _DT[x.dtype], _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(z),
         _p(dt_bias), _p(state), _i64s(*st), GDR_SSM_SOFTPLUS if softplus else 0, code, _p(y),
@@ -1094,9 +1104,9 @@ def gdr_layer_norm_fwd(x, w=None, b=None, eps=1e-5, *, residual=None, out_dtype=
         _whole("b", b, torch.float32, (C,), dev)
     odt = out_dtype or (x.dtype if y is None else y.dtype)
     code = _dt_of("output dtype", odt)
-    y = _buffer("y", y, odt, x.shape, dev)
+    y = _buffer("y", y, odt, x.shape, dev, x)
     if residual is not None:
-        h = _buffer("h", h, rdt, x.shape, dev)
+        h = _buffer("h", h, rdt, x.shape, dev, residual)
     _run("gdr_layer_norm_fwd", lib.gdr_layer_norm_fwd(
         R, C, _DT[x.dtype], _p(x), xr, _DT[rdt], _p(residual), rr, _p(w), _p(b), float(eps),
         code, _p(y), _p(h), _raw_stream(dev.index)))

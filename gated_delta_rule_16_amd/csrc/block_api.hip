@@ -384,7 +384,7 @@ extern "C" gdr_status_t gdr_ssm_step(int64_t Nseq, int64_t D, int64_t G, int64_t
     if (!ssm_ptrs_ok(in_dt, x, dt, A, Bm, Cm, D_skip, z, dt_bias) || !elem_ok(state, 4) ||
         !elem_ok(y, elem(out_dt)))
         return GDR_ERR_INVALID;
-    if (!workgroups_ok((double)Nseq * (double)D * ssm_lanes(N) / 256.0 + 1.0))
+    if (!workgroups_ok((double)ssm_step_workgroups(Nseq, D, N)))
         return GDR_ERR_INVALID;
     int64_t s[10];
     for (int i = 0; strides && i < 5; ++i) {

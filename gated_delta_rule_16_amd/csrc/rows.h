@@ -170,16 +170,11 @@ __device__ __forceinline__ void small_load(float (&f)[M], const float* p, int va
 constexpr float kLog2e = 1.44269504088896f;
 constexpr float kLn2 = 0.693147180559945f;
 
-// exp(x) for x <= 0, relative error ~2^-23 also at large |x|: the rounding
-// of x log2(e) (up to |x| 2^-24, which exp would turn into a relative error
-// |x| 2^-24) is recovered with an fma and applied to first order.  Below -120
-// the result is that of -120 (8e-53, 0 in fp32).
-__device__ __forceinline__ float exp_neg(float x) {
-    x = fmaxf(x, -120.f);
-    const float p = x * kLog2e;
-    const float r = __builtin_fmaf(x, kLog2e, -p);
-    const float e = __builtin_amdgcn_exp2f(p);
-    return __builtin_fmaf(e, r * kLn2, e);
+// exp(-|x|), 0 far down.  The argument's rounding makes its relative error
+// |x| 2^-24 (2^-21 at x = -8): no more than the sum dt + dt_bias in front of a
+// softplus has rounded off already.
+__device__ __forceinline__ float exp_neg_abs(float x) {
+    return __builtin_amdgcn_exp2f(fabsf(x) * -kLog2e);
 }
 
 // log(1 + e) for e in [0, 1] as e times a polynomial of degree 9 (fitted for
@@ -200,22 +195,22 @@ __device__ __forceinline__ float log1p_unit(float e) {
     return c * e;
 }
 
-// 1 / (1 + exp(-x)), relative error ~2^-22 at both ends.
+// 1 / (1 + exp(-x)), relative error (1 - sigmoid) |x| 2^-24 and a few steps.
 __device__ __forceinline__ float sigmoid(float x) {
-    const float e = exp_neg(-fabsf(x));
-    const float r = __builtin_amdgcn_rcpf(1.f + e);
-    return x >= 0.f ? r : e * r;
-}
-
-// The same without the correction of exp's argument: relative error
-// (1 - sigmoid) |x| 2^-24 more, a third fewer operations.
-__device__ __forceinline__ float sigmoid_fast(float x) {
     return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x * -kLog2e));
 }
 
 // softplus(x) = max(x, 0) + log(1 + exp(-|x|)); NaN stays NaN.
 __device__ __forceinline__ float softplus(float x) {
-    return (x < 0.f ? 0.f : x) + log1p_unit(exp_neg(-fabsf(x)));
+    return (x < 0.f ? 0.f : x) + log1p_unit(exp_neg_abs(x));
+}
+
+// softplus(x) and its derivative sigmoid(x), from one exp.
+__device__ __forceinline__ void softplus_grad(float x, float& y, float& dy) {
+    const float e = exp_neg_abs(x);
+    const float r = __builtin_amdgcn_rcpf(1.f + e);
+    y = (x < 0.f ? 0.f : x) + log1p_unit(e);
+    dy = x < 0.f ? e * r : r;
 }
 
 }  // namespace gdr

@@ -90,7 +90,7 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int64_t ncb, 
 #pragma unroll
                 for (int j = 0; j < K - 1; ++j) s = __builtin_fmaf(w[e * K + j], win[j][e], s);
                 s = __builtin_fmaf(w[e * K + K - 1], x[e], s);
-                y[e] = a.silu ? s * sigmoid_fast(s) : s;
+                y[e] = a.silu ? s * sigmoid(s) : s;
 #pragma unroll
                 for (int j = 0; j + 1 < K - 1; ++j) win[j][e] = win[j + 1][e];
                 win[K - 2][e] = x[e];
@@ -123,7 +123,7 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a, int64_t ncg)
             y[e] = __builtin_fmaf(w[e * K + j], x[j][e], y[e]);
     }
 #pragma unroll
-    for (int e = 0; e < SE; ++e) y[e] = a.silu ? y[e] * sigmoid_fast(y[e]) : y[e];
+    for (int e = 0; e < SE; ++e) y[e] = a.silu ? y[e] * sigmoid(y[e]) : y[e];
     row_store<SE>(a.y, b * a.C + c, a.out_bf16, y, valid);
 #pragma unroll
     for (int j = 0; j < K - 1; ++j)
@@ -206,7 +206,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int64_t ncb, 
                             float s = bias[e];
 #pragma unroll
                             for (int j = 0; j < K; ++j) s = __builtin_fmaf(w[e * K + j], win[j][e], s);
-                            const float sg = sigmoid_fast(s);
+                            const float sg = sigmoid(s);
                             g *= sg * __builtin_fmaf(s, 1.f - sg, 1.f);
                         }
                         // rows past the sequence loaded zeros, but an infinite

@@ -199,18 +199,25 @@ __device__ __forceinline__ float row_coef(const float* tile, int tt, int lane) {
     return tile[(tt + i / NS) * NP + NS * ((lane >> 4) % NG) + i % NS];
 }
 
-// NS states of one lane in memory ([.., N] floats, element-aligned).
-template <int NS>
+// NS states of one lane in memory ([.., N] floats, element-aligned).  Without
+// RAG valid is 0 or NS.
+template <int NS, bool RAG = true>
 __device__ __forceinline__ void states_load(float (&h)[NS], const float* p, int valid) {
-    param_load<NS>(h, p, valid);
+    if constexpr (RAG) {
+        param_load<NS>(h, p, valid);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NS; ++i) h[i] = 0.f;
+        if (valid > 0) param_load<NS>(h, p, NS);
+    }
 }
-template <int NS>
+template <int NS, bool RAG = true>
 __device__ __forceinline__ void states_store(float* p, const float (&h)[NS], int valid) {
     if (valid >= NS) {
 #pragma unroll
         for (int i = 0; i < NS; i += 4)
             *reinterpret_cast<f32x4_e4*>(p + i) = f32x4_e4{h[i], h[i + 1], h[i + 2], h[i + 3]};
-    } else {
+    } else if constexpr (RAG) {
 #pragma unroll
         for (int i = 0; i < NS; ++i)
             if (i < valid) p[i] = h[i];
@@ -234,7 +241,7 @@ __device__ __forceinline__ void ssm_deltas(float (&d)[E], const float (&raw)[E],
 template <int E>
 __device__ __forceinline__ void ssm_gate(float (&v)[E], const float (&z)[E]) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] *= z[e] * sigmoid_fast(z[e]);
+    for (int e = 0; e < E; ++e) v[e] *= z[e] * sigmoid(z[e]);
 }
 
 // Valid states of a lane that starts at state n0.

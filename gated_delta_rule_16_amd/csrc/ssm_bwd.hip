@@ -23,6 +23,8 @@
 // segment alone sends to its start, sum_t (prod a) C_t dy_t, from running
 // products; the second composes a segment's true start state and end
 // gradient from those and adds exp(A sum Delta) h_in to each kept state.
+#include <type_traits>
+
 #include "ssm.h"
 
 namespace gdr {
@@ -80,7 +82,7 @@ __global__ __launch_bounds__(512) void ssm_bwd_states_kernel(SsmBwdArgs a, int64
             h[j] = gam[j] = 0.f;
             P[j] = 1.f;
         }
-        if (a.h0 && seg == 0) states_load<NS>(h, a.h0 + (b * a.D + ch) * a.N + n0, nv);
+        if (a.h0 && seg == 0) states_load<NS, RAG>(h, a.h0 + (b * a.D + ch) * a.N + n0, nv);
         float sumd = 0.f;
         __syncthreads();
         for (int64_t i = 0; i < tiles; ++i) {
@@ -90,7 +92,7 @@ __global__ __launch_bounds__(512) void ssm_bwd_states_kernel(SsmBwdArgs a, int64
             for (int tt = 0; tt < nt; tt += 4) {
                 if (((tb + tt) & (S - 1)) == 0) {
                     const int64_t o = (b * nsub + (tb + tt) / S) * a.D + ch;
-                    states_store<NS>(a.ckpt + o * a.N + n0, h, nv);
+                    states_store<NS, RAG>(a.ckpt + o * a.N + n0, h, nv);
                     if (GAM && live && n0 == 0) a.csum[o] = sumd;
                 }
                 float Bq[4 / KT], Cq[4 / KT], dy[4] = {0.f, 0.f, 0.f, 0.f};
@@ -138,8 +140,8 @@ __global__ __launch_bounds__(512) void ssm_bwd_states_kernel(SsmBwdArgs a, int64
         }
         if constexpr (GAM) {
             const int64_t o = (b * nseg + seg) * a.D + ch;
-            states_store<NS>(a.hend + o * a.N + n0, h, nv);
-            states_store<NS>(a.gstart + o * a.N + n0, gam, nv);
+            states_store<NS, RAG>(a.hend + o * a.N + n0, h, nv);
+            states_store<NS, RAG>(a.gstart + o * a.N + n0, gam, nv);
             if (live && n0 == 0) a.sdelta[o] = sumd;
         }
         return;
@@ -150,20 +152,37 @@ __global__ __launch_bounds__(512) void ssm_bwd_states_kernel(SsmBwdArgs a, int64
     const int64_t scg = cg + c0 + sc;
     float bias[EPT];
     param_load<EPT>(bias, a.bias + scg, a.bias ? sv : 0);
+    // addresses of the next tile to fetch
+    using T = typename std::conditional<BF16, bf16_t, float>::type;
+    const T* px = static_cast<const T*>(a.x) + b * a.xb + (t0 + srow) * a.xt + scg;
+    const T* pt = static_cast<const T*>(a.dt) + b * a.dtb + (t0 + srow) * a.dtt + scg;
+    const T* pz = static_cast<const T*>(a.z) + b * a.zb + (t0 + srow) * a.zt + scg;
+    int64_t po = b * a.ob + (t0 + srow) * a.ot + scg;
+    const T* pq[QPT];
+#pragma unroll
+    for (int i = 0; i < QPT; ++i) {
+        const int q = tid + 256 * i, qt = (q % NQ) / (NP / 4), qn = q % (NP / 4);
+        pq[i] = q >= NQ ? static_cast<const T*>(a.Cm) + b * a.cb + (t0 + qt) * a.ct
+                        : static_cast<const T*>(a.Bm) + b * a.bb + (t0 + qt) * a.bt;
+        pq[i] += g * a.N + 4 * qn;
+    }
     Row<EPT, BF16, RAG> rx, rt, rz;
     Row<EPT, true, RAG> ro16;
     Row<EPT, false, RAG> ro32;
     Row<4, BF16, RAG> rq[QPT];
     auto fetch = [&](int64_t tb) {
-        const int64_t t = tb + srow;
-        const int v = t < t1 ? sv : 0;
-        rx.load(a.x, b * a.xb + t * a.xt + scg, v);
-        rt.load(a.dt, b * a.dtb + t * a.dtt + scg, v);
+        const int left = t1 - tb < TT ? (int)(t1 - tb) : TT;
+        const int v = srow < left ? sv : 0;
+        rx.load(px, 0, v);
+        rt.load(pt, 0, v);
+        px += TT * a.xt;
+        pt += TT * a.dtt;
         if constexpr (GAM) {
-            const int64_t oo = b * a.ob + t * a.ot + scg;
-            ro16.load(a.dout, oo, a.dout_bf16 ? v : 0);
-            ro32.load(a.dout, oo, a.dout_bf16 ? 0 : v);
-            rz.load(a.z, b * a.zb + t * a.zt + scg, a.z ? v : 0);
+            ro16.load(a.dout, po, a.dout_bf16 ? v : 0);
+            ro32.load(a.dout, po, a.dout_bf16 ? 0 : v);
+            rz.load(pz, 0, a.z ? v : 0);
+            po += TT * a.ot;
+            pz += TT * a.zt;
         }
 #pragma unroll
         for (int i = 0; i < QPT; ++i) {
@@ -171,10 +190,9 @@ __global__ __launch_bounds__(512) void ssm_bwd_states_kernel(SsmBwdArgs a, int64
             const bool isc = q >= NQ;
             if (isc && !GAM) continue;
             const int qt = (q % NQ) / (NP / 4), qn = q % (NP / 4);
-            const int64_t tq = tb + qt;
-            const int vq = q < 2 * NQ && tq < t1 ? states_valid<4>(a.N, 4 * qn) : 0;
-            rq[i].load(isc ? a.Cm : a.Bm,
-                       (isc ? b * a.cb + tq * a.ct : b * a.bb + tq * a.bt) + g * a.N + 4 * qn, vq);
+            const int vq = q < 2 * NQ && qt < left ? states_valid<4>(a.N, 4 * qn) : 0;
+            rq[i].load(pq[i], 0, vq);
+            pq[i] += TT * (isc ? a.ct : a.bt);
         }
     };
     auto stage = [&](int64_t i) {
@@ -330,7 +348,10 @@ __global__ __launch_bounds__(512, NS == 16 ? 1 : 2) void ssm_bwd_kernel(SsmBwdAr
     constexpr int NQ = S * NP / 4;
     constexpr int QPT = (2 * NQ + 255) / 256;
     constexpr int KT = 16 / NS;
-    __shared__ f32x4 st[2][S][WC];            // Delta, Delta x, dy, (y); then sums over n
+    constexpr int WP = WC + 16;               // pitch: 4 tokens' sums meet no bank twice
+    // Delta, Delta x, dy and a place for y; the sums over n of g B and of p A
+    // take the place of Delta and Delta x
+    __shared__ __align__(16) float st[2][4][S][WP];
     __shared__ __align__(16) float bc[2][2][S * NP];
     __shared__ float pbc[2][4][S][2 * NP];    // each wave's sums over its channels: dC, dB
 
@@ -367,7 +388,7 @@ __global__ __launch_bounds__(512, NS == 16 ? 1 : 2) void ssm_bwd_kernel(SsmBwdAr
         for (int64_t s = 0; s < seg; ++s) {
             const int64_t o = (b * nseg + s) * a.D + ch;
             float e[NS];
-            states_load<NS>(e, a.hend + o * a.N + n0, nv);
+            states_load<NS, RAG>(e, a.hend + o * a.N + n0, nv);
             const float sd = live ? a.sdelta[o] : 0.f;
 #pragma unroll
             for (int j = 0; j < NS; ++j)
@@ -375,11 +396,11 @@ __global__ __launch_bounds__(512, NS == 16 ? 1 : 2) void ssm_bwd_kernel(SsmBwdAr
                                 : __builtin_fmaf(__builtin_amdgcn_exp2f(A2[j] * sd), hin[j], e[j]);
         }
         // gr = a_{t+1} g_{t+1} past the segment's last token
-        if (a.dh_final) states_load<NS>(gr, a.dh_final + so, nv);
+        if (a.dh_final) states_load<NS, RAG>(gr, a.dh_final + so, nv);
         for (int64_t s = nseg - 1; s > seg; --s) {
             const int64_t o = (b * nseg + s) * a.D + ch;
             float e[NS];
-            states_load<NS>(e, a.gstart + o * a.N + n0, nv);
+            states_load<NS, RAG>(e, a.gstart + o * a.N + n0, nv);
             const float sd = live ? a.sdelta[o] : 0.f;
 #pragma unroll
             for (int j = 0; j < NS; ++j)
@@ -388,7 +409,7 @@ __global__ __launch_bounds__(512, NS == 16 ? 1 : 2) void ssm_bwd_kernel(SsmBwdAr
         float kept[NS], ksum = 0.f;
         auto fetch = [&](int64_t sub) {
             const int64_t ko = (b * nsub + sub) * a.D + ch;
-            states_load<NS>(kept, a.ckpt + ko * a.N + n0, nv);
+            states_load<NS, RAG>(kept, a.ckpt + ko * a.N + n0, nv);
             if (seg > 0) ksum = live ? a.csum[ko] : 0.f;
         };
         fetch(last);
@@ -401,21 +422,34 @@ __global__ __launch_bounds__(512, NS == 16 ? 1 : 2) void ssm_bwd_kernel(SsmBwdAr
                 hs[j] = seg > 0
                             ? __builtin_fmaf(__builtin_amdgcn_exp2f(A2[j] * ksum), hin[j], kept[j])
                             : kept[j];
+            // operands of 4 tokens, read before the group in front of them
+            // writes its sums, so that their latency is covered
+            struct Operands {
+                float d[4], dx[4], dy[4], Bq[4 / KT], Cq[4 / KT];
+            };
+            auto read = [&](Operands& o, int tt, bool back) {
+#pragma unroll
+                for (int k = 0; k < 4 / KT; ++k) {
+                    o.Bq[k] = row_coef<NS, NG>(bc[buf][0], tt + k * KT, lane);
+                    o.Cq[k] = row_coef<NS, NG>(bc[buf][1], tt + k * KT, lane);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    o.d[k] = st[buf][0][tt + k][chl];
+                    o.dx[k] = st[buf][1][tt + k][chl];
+                    if (back) o.dy[k] = st[buf][2][tt + k][chl];
+                }
+            };
             // the block's states again, all kept in registers
             constexpr auto js = std::make_index_sequence<NS>{};
             float hh[S][NS], aa[S][NS];
+            Operands o;
+            read(o, 0, S == 4);
 #pragma unroll
             for (int tt = 0; tt < S; tt += 4) {
-                float Bq[4 / KT], Cq[4 / KT];
-#pragma unroll
-                for (int k = 0; k < 4 / KT; ++k) {
-                    Bq[k] = row_coef<NS, NG>(bc[buf][0], tt + k * KT, lane);
-                    Cq[k] = row_coef<NS, NG>(bc[buf][1], tt + k * KT, lane);
-                }
-                f32x4 d[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) d[k] = st[buf][tt + k][chl];
-#define TOKEN(k) scan_terms<NS, k % KT>(aa[tt + k], hh[tt + k], A2, d[k][0], d[k][1], Bq[k / KT], js)
+                Operands next;
+                if (tt + 4 < S) read(next, tt + 4, tt + 8 >= S);
+#define TOKEN(k) scan_terms<NS, k % KT>(aa[tt + k], hh[tt + k], A2, o.d[k], o.dx[k], o.Bq[k / KT], js)
                 TOKEN(0);
                 TOKEN(1);
                 TOKEN(2);
@@ -434,29 +468,24 @@ __global__ __launch_bounds__(512, NS == 16 ? 1 : 2) void ssm_bwd_kernel(SsmBwdAr
                     for (int k = 0; k < 4; ++k)
 #pragma unroll
                         for (int j = 0; j < NS; ++j) h4[k][j] = hh[tt + k][j];
-                    row_dots<NS>(s, Cq, h4);
-                    state_sums<NG>(s, row, reinterpret_cast<float*>(&st[buf][tt][chl]) + 3, 4 * WC);
+                    row_dots<NS>(s, o.Cq, h4);
+                    state_sums<NG>(s, row, &st[buf][3][tt][chl], WP);
                 }
+                if (tt + 4 < S) o = next;
             }
-            // and backwards
+            // and backwards, from the last group, whose operands are here
 #pragma unroll
             for (int tt = S - 4; tt >= 0; tt -= 4) {
                 // half of the kept states are done with: the next block's
                 // start takes their registers
                 if (tt == (S / 2 - 4 > 0 ? S / 2 - 4 : 0) && sub > first) fetch(sub - 1);
-                float sB[4], sA[4], Bq[4 / KT], Cq[4 / KT], pv[4][2 * NS];
-                f32x4 d[4];
-#pragma unroll
-                for (int k = 0; k < 4 / KT; ++k) {
-                    Bq[k] = row_coef<NS, NG>(bc[buf][0], tt + k * KT, lane);
-                    Cq[k] = row_coef<NS, NG>(bc[buf][1], tt + k * KT, lane);
-                }
-#pragma unroll
-                for (int k = 0; k < 4; ++k) d[k] = st[buf][tt + k][chl];
+                Operands next;
+                if (tt > 0) read(next, tt - 4, true);
+                float sB[4], sA[4], pv[4][2 * NS];
 #define TOKEN(k)                                                                               \
     back_token<NS, NS*(k % KT)>(gr, dA, pv[k], sB[k], sA[k], aa[tt + k], hh[tt + k],           \
                                 tt + k == 0 ? hs : hh[tt + k == 0 ? 0 : tt + k - 1], A2,       \
-                                d[k][0], d[k][1], d[k][2], Bq[k / KT], Cq[k / KT])
+                                o.d[k], o.dx[k], o.dy[k], o.Bq[k / KT], o.Cq[k / KT])
                 TOKEN(3);
                 TOKEN(2);
                 channel_sums<NS, NG>(&pbc[buf][wv][tt + 2], pv[2], pv[3], lane, n0);
@@ -464,15 +493,15 @@ __global__ __launch_bounds__(512, NS == 16 ? 1 : 2) void ssm_bwd_kernel(SsmBwdAr
                 TOKEN(0);
                 channel_sums<NS, NG>(&pbc[buf][wv][tt], pv[0], pv[1], lane, n0);
 #undef TOKEN
-                float* sp = reinterpret_cast<float*>(&st[buf][tt][chl]);
                 asm("s_nop 1" : "+v"(sB[0]), "+v"(sB[1]), "+v"(sB[2]), "+v"(sB[3]));
-                state_sums<NG>(sB, row, sp, 4 * WC);
-                state_sums<NG>(sA, row, sp + 1, 4 * WC);
+                state_sums<NG>(sB, row, &st[buf][0][tt][chl], WP);
+                state_sums<NG>(sA, row, &st[buf][1][tt][chl], WP);
+                if (tt > 0) o = next;
             }
             __syncthreads();
         }
-        if (seg == 0 && a.dh0) states_store<NS>(a.dh0 + so, gr, nv);
-        states_store<NS>(part + ch * a.N + n0, dA, nv);
+        if (seg == 0 && a.dh0) states_store<NS, RAG>(a.dh0 + so, gr, nv);
+        states_store<NS, RAG>(part + ch * a.N + n0, dA, nv);
         __syncthreads();
         return;
     }
@@ -486,28 +515,44 @@ __global__ __launch_bounds__(512, NS == 16 ? 1 : 2) void ssm_bwd_kernel(SsmBwdAr
 #pragma unroll
     for (int e = 0; e < EPT; ++e) dD[e] = dbias[e] = 0.f;
 
+    // addresses of the next block to fetch
+    using T = typename std::conditional<BF16, bf16_t, float>::type;
+    const T* px = static_cast<const T*>(a.x) + b * a.xb + (last * S + srow) * a.xt + scg;
+    const T* pt = static_cast<const T*>(a.dt) + b * a.dtb + (last * S + srow) * a.dtt + scg;
+    const T* pz = static_cast<const T*>(a.z) + b * a.zb + (last * S + srow) * a.zt + scg;
+    int64_t po = b * a.ob + (last * S + srow) * a.ot + scg;
+    const T* pq[QPT];
+#pragma unroll
+    for (int i = 0; i < QPT; ++i) {
+        const int q = tid + 256 * i, qt = (q % NQ) / (NP / 4), qn = q % (NP / 4);
+        pq[i] = q >= NQ ? static_cast<const T*>(a.Cm) + b * a.cb + (last * S + qt) * a.ct
+                        : static_cast<const T*>(a.Bm) + b * a.bb + (last * S + qt) * a.bt;
+        pq[i] += g * a.N + 4 * qn;
+    }
     Row<EPT, BF16, RAG> rx, rt, rz;
     Row<EPT, true, RAG> ro16;
     Row<EPT, false, RAG> ro32;
     Row<4, BF16, RAG> rq[QPT];
     auto fetch = [&](int64_t sub) {
-        const int64_t tb = sub * S, t = tb + srow;
-        const int v = t < t1 ? sv : 0;
-        rx.load(a.x, b * a.xb + t * a.xt + scg, v);
-        rt.load(a.dt, b * a.dtb + t * a.dtt + scg, v);
-        const int64_t oo = b * a.ob + t * a.ot + scg;
-        ro16.load(a.dout, oo, a.dout_bf16 ? v : 0);
-        ro32.load(a.dout, oo, a.dout_bf16 ? 0 : v);
-        rz.load(a.z, b * a.zb + t * a.zt + scg, a.z ? v : 0);
+        const int left = t1 - sub * S < S ? (int)(t1 - sub * S) : S;
+        const int v = srow < left ? sv : 0;
+        rx.load(px, 0, v);
+        rt.load(pt, 0, v);
+        ro16.load(a.dout, po, a.dout_bf16 ? v : 0);
+        ro32.load(a.dout, po, a.dout_bf16 ? 0 : v);
+        rz.load(pz, 0, a.z ? v : 0);
+        px -= S * a.xt;
+        pt -= S * a.dtt;
+        po -= S * a.ot;
+        pz -= S * a.zt;
 #pragma unroll
         for (int i = 0; i < QPT; ++i) {
             const int q = tid + 256 * i;
             const bool isc = q >= NQ;
             const int qt = (q % NQ) / (NP / 4), qn = q % (NP / 4);
-            const int64_t tq = tb + qt;
-            const int vq = q < 2 * NQ && tq < t1 ? states_valid<4>(a.N, 4 * qn) : 0;
-            rq[i].load(isc ? a.Cm : a.Bm,
-                       (isc ? b * a.cb + tq * a.ct : b * a.bb + tq * a.bt) + g * a.N + 4 * qn, vq);
+            const int vq = q < 2 * NQ && qt < left ? states_valid<4>(a.N, 4 * qn) : 0;
+            rq[i].load(pq[i], 0, vq);
+            pq[i] -= S * (isc ? a.ct : a.bt);
         }
     };
     // of a staged block, until it is finished: x, Delta, its derivative, dy, and
@@ -531,15 +576,17 @@ __global__ __launch_bounds__(512, NS == 16 ? 1 : 2) void ssm_bwd_kernel(SsmBwdAr
             r[e] += bias[e];
             k.ddr[e] = 1.f;
         }
-        ssm_deltas(k.d, r, a.softplus);
         if (a.softplus) {
 #pragma unroll
-            for (int e = 0; e < EPT; ++e) k.ddr[e] = sigmoid(r[e]);
+            for (int e = 0; e < EPT; ++e) softplus_grad(r[e], k.d[e], k.ddr[e]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < EPT; ++e) k.d[e] = r[e];
         }
         if (a.z) {
 #pragma unroll
             for (int e = 0; e < EPT; ++e) {
-                const float sg = sigmoid_fast(z[e]);
+                const float sg = sigmoid(z[e]);
                 k.og[e] = k.dy[e] * sg * __builtin_fmaf(z[e], 1.f - sg, 1.f);
                 k.dy[e] *= z[e] * sg;
             }
@@ -547,7 +594,9 @@ __global__ __launch_bounds__(512, NS == 16 ? 1 : 2) void ssm_bwd_kernel(SsmBwdAr
 #pragma unroll
         for (int e = 0; e < EPT; ++e) {
             k.d[e] = (RAG ? e < v : v > 0) ? k.d[e] : 0.f;
-            st[buf][srow][sc + e] = f32x4{k.d[e], k.d[e] * k.x[e], k.dy[e], 0.f};
+            st[buf][0][srow][sc + e] = k.d[e];
+            st[buf][1][srow][sc + e] = k.d[e] * k.x[e];
+            st[buf][2][srow][sc + e] = k.dy[e];
         }
 #pragma unroll
         for (int i = 0; i < QPT; ++i) {
@@ -559,54 +608,63 @@ __global__ __launch_bounds__(512, NS == 16 ? 1 : 2) void ssm_bwd_kernel(SsmBwdAr
                 float4{f[0], f[1], f[2], f[3]};
         }
     };
+    int64_t oo = (b * a.T + last * S + srow) * a.D + scg;
+    constexpr int PPT = (S * 2 * NP + 255) / 256;     // sums of dC and dB per thread
+    const int64_t bct = a.G * 2 * NP;                 // and the partials of a token
+    float* pbo = a.bcpart + ((blk * a.B + b) * a.T + last * S) * bct + g * 2 * NP;
     auto finish = [&](int64_t sub, const Held& k) {
         const int buf = (int)(sub & 1);
-        const int64_t tb = sub * S, t = tb + srow;
-        const int v = t < t1 ? sv : 0;
+        const int left = t1 - sub * S < S ? (int)(t1 - sub * S) : S;
+        const int v = srow < left ? sv : 0;
         if (v > 0) {
             float dxv[EPT], dtv[EPT], dzv[EPT];
 #pragma unroll
             for (int e = 0; e < EPT; ++e) {
-                const f32x4 q = st[buf][srow][sc + e];
-                dxv[e] = __builtin_fmaf(k.d[e], q[0], skip[e] * k.dy[e]);
-                dtv[e] = __builtin_fmaf(k.x[e], q[0], q[1] * kLn2) * k.ddr[e];
-                dzv[e] = k.og[e] * __builtin_fmaf(skip[e], k.x[e], q[3]);
+                const float gB = st[buf][0][srow][sc + e], pA = st[buf][1][srow][sc + e];
+                dxv[e] = __builtin_fmaf(k.d[e], gB, skip[e] * k.dy[e]);
+                dtv[e] = __builtin_fmaf(k.x[e], gB, pA * kLn2) * k.ddr[e];
+                if (a.z) dzv[e] = k.og[e] * __builtin_fmaf(skip[e], k.x[e], st[buf][3][srow][sc + e]);
                 if (!RAG || e < v) {
                     dD[e] = __builtin_fmaf(k.dy[e], k.x[e], dD[e]);
                     dbias[e] += dtv[e];
                 }
             }
-            const int64_t oo = (b * a.T + t) * a.D + scg;
             row_store<EPT, RAG>(a.dx, oo, a.grad_bf16, dxv, v);
             row_store<EPT, RAG>(a.ddt, oo, a.grad_bf16, dtv, v);
             if (a.z) row_store<EPT, RAG>(a.dz, oo, a.grad_bf16, dzv, v);
         }
-        for (int i = tid; i < S * 2 * NP; i += 256) {
-            const int q = i / (2 * NP), c = i % (2 * NP);
-            if (tb + q < t1)
-                a.bcpart[(((blk * a.B + b) * a.T + tb + q) * a.G + g) * 2 * NP + c] =
+#pragma unroll
+        for (int i = 0; i < PPT; ++i) {
+            const int q = (tid + 256 * i) / (2 * NP), c = (tid + 256 * i) % (2 * NP);
+            if (q < left)
+                pbo[q * bct + c] =
                     (pbc[buf][0][q][c] + pbc[buf][1][q][c]) + (pbc[buf][2][q][c] + pbc[buf][3][q][c]);
         }
+        oo -= S * a.D;
+        pbo -= S * bct;
     };
-    Held now, next;
+    Held even, odd;
     fetch(last);
-    stage(last, now);
+    stage(last, even);
     if (last > first) fetch(last - 1);
     __syncthreads();
-    for (int64_t sub = last; sub >= first; --sub) {
-        // while block sub runs; block sub + 1, which shares sub - 1's buffers,
-        // is finished already
+    // while block sub runs, block sub - 1 is staged (in the buffers of block
+    // sub + 1, finished already) and block sub - 2's loads are issued
+    auto step = [&](int64_t sub, const Held& now, Held& next) {
         if (sub > first) {
             stage(sub - 1, next);
             if (sub - 1 > first) fetch(sub - 2);
         }
         __syncthreads();
         finish(sub, now);
-        now = next;
+    };
+    for (int64_t sub = last; sub >= first; sub -= 2) {
+        step(sub, even, odd);
+        if (sub > first) step(sub - 1, odd, even);
     }
     // dD and dbias over the thread rows of a channel, through the buffer that
     // the last block did not use (block `first` may not be finished yet)
-    float* red = reinterpret_cast<float*>(st[(first & 1) ^ 1]);
+    float* red = &st[(first & 1) ^ 1][0][0][0];
 #pragma unroll
     for (int e = 0; e < EPT; ++e) {
         red[srow * 2 * WC + sc + e] = dD[e];
@@ -706,7 +764,7 @@ hipError_t launch_bwd_r(const SsmBwdArgs& a, const SsmPlan& p) {
 
 template <int NS, int NG>
 hipError_t launch_bwd_t(const SsmBwdArgs& a, const SsmPlan& p) {
-    const bool rag = (a.D / a.G) % 8 != 0 || a.N % 4 != 0;
+    const bool rag = (a.D / a.G) % 8 != 0 || a.N % NS != 0;
     hipError_t e;
     if (a.in_bf16)
         e = rag ? launch_bwd_r<NS, NG, true, true>(a, p) : launch_bwd_r<NS, NG, true, false>(a, p);

@@ -20,6 +20,8 @@
 // Delta (whose exp with A is the segment's decay); the second starts from the
 // states composed of those.  It costs a second exp per state, so it is taken
 // only where the channels alone leave most of the chip idle (ssm_fwd_segs).
+#include <type_traits>
+
 #include "ssm.h"
 
 namespace gdr {
@@ -74,15 +76,15 @@ __global__ __launch_bounds__(512) void ssm_fwd_kernel(SsmArgs a, int64_t nblk, i
         // not read h0: another workgroup may be writing h_final, the same
         // buffer), hend[b][s] the end of segment s - 1, segment 0 started from h0
         if (!OUT || nseg == 1) {
-            if (a.h0 && seg == 0) states_load<NS>(h, a.h0 + so, nv);
+            if (a.h0 && seg == 0) states_load<NS, RAG>(h, a.h0 + so, nv);
             if constexpr (!OUT)
-                if (seg == 0) states_store<NS>(a.hend + (b * nseg * a.D + ch) * a.N + n0, h, nv);
+                if (seg == 0) states_store<NS, RAG>(a.hend + (b * nseg * a.D + ch) * a.N + n0, h, nv);
         } else {
-            states_load<NS>(h, a.hend + ((b * nseg + (seg > 0)) * a.D + ch) * a.N + n0, nv);
+            states_load<NS, RAG>(h, a.hend + ((b * nseg + (seg > 0)) * a.D + ch) * a.N + n0, nv);
             for (int64_t s = 1; s < seg; ++s) {
                 const int64_t o = (b * nseg + s) * a.D + ch;
                 float e[NS];
-                states_load<NS>(e, a.hend + (o + a.D) * a.N + n0, nv);
+                states_load<NS, RAG>(e, a.hend + (o + a.D) * a.N + n0, nv);
                 const float sd = live ? a.sdelta[o] : 0.f;
 #pragma unroll
                 for (int j = 0; j < NS; ++j)
@@ -136,10 +138,10 @@ __global__ __launch_bounds__(512) void ssm_fwd_kernel(SsmArgs a, int64_t nblk, i
             __syncthreads();
         }
         if constexpr (OUT) {
-            if (a.h_final && seg == nseg - 1) states_store<NS>(a.h_final + so, h, nv);
+            if (a.h_final && seg == nseg - 1) states_store<NS, RAG>(a.h_final + so, h, nv);
         } else {
             const int64_t o = (b * nseg + seg) * a.D + ch;
-            states_store<NS>(a.hend + (o + a.D) * a.N + n0, h, nv);
+            states_store<NS, RAG>(a.hend + (o + a.D) * a.N + n0, h, nv);
             if (live && n0 == 0) a.sdelta[o] = sumd;
         }
         return;
@@ -152,29 +154,48 @@ __global__ __launch_bounds__(512) void ssm_fwd_kernel(SsmArgs a, int64_t nblk, i
     float bias[EPT], skip[EPT];
     param_load<EPT>(bias, a.bias + scg, a.bias ? sv : 0);
     param_load<EPT>(skip, a.D_skip + scg, OUT && a.D_skip ? sv : 0);
+    // addresses of the next tile to fetch: of x, dt, z, and of B or C
+    using T = typename std::conditional<BF16, bf16_t, float>::type;
+    const T* px = static_cast<const T*>(a.x) + b * a.xb + (t0 + srow) * a.xt + scg;
+    const T* pt = static_cast<const T*>(a.dt) + b * a.dtb + (t0 + srow) * a.dtt + scg;
+    const T* pz = static_cast<const T*>(a.z) + b * a.zb + (t0 + srow) * a.zt + scg;
+    const T* pq[QPT];
+#pragma unroll
+    for (int i = 0; i < QPT; ++i) {
+        const int q = tid + 256 * i, qt = (q % NQ) / (NP / 4), qn = q % (NP / 4);
+        pq[i] = q >= NQ ? static_cast<const T*>(a.Cm) + b * a.cb + (t0 + qt) * a.ct
+                        : static_cast<const T*>(a.Bm) + b * a.bb + (t0 + qt) * a.bt;
+        pq[i] += g * a.N + 4 * qn;
+    }
     Row<EPT, BF16, RAG> rx, rt, rz;
     Row<4, BF16, RAG> rq[QPT];
     auto fetch = [&](int64_t tb) {
-        const int64_t t = tb + srow;
-        const int v = t < t1 ? sv : 0;
-        rx.load(a.x, b * a.xb + t * a.xt + scg, v);
-        rt.load(a.dt, b * a.dtb + t * a.dtt + scg, v);
-        if constexpr (OUT) rz.load(a.z, b * a.zb + t * a.zt + scg, a.z ? v : 0);
+        const int left = t1 - tb < TT ? (int)(t1 - tb) : TT;
+        const int v = srow < left ? sv : 0;
+        rx.load(px, 0, v);
+        rt.load(pt, 0, v);
+        px += TT * a.xt;
+        pt += TT * a.dtt;
+        if constexpr (OUT) {
+            rz.load(pz, 0, a.z ? v : 0);
+            pz += TT * a.zt;
+        }
 #pragma unroll
         for (int i = 0; i < QPT; ++i) {
             const int q = tid + 256 * i;
             const bool isc = q >= NQ;
             if (isc && !OUT) continue;
             const int qt = (q % NQ) / (NP / 4), qn = q % (NP / 4);
-            const int64_t tq = tb + qt;
-            const int vq = q < 2 * NQ && tq < t1 ? states_valid<4>(a.N, 4 * qn) : 0;
-            rq[i].load(isc ? a.Cm : a.Bm,
-                       (isc ? b * a.cb + tq * a.ct : b * a.bb + tq * a.bt) + g * a.N + 4 * qn, vq);
+            const int vq = q < 2 * NQ && qt < left ? states_valid<4>(a.N, 4 * qn) : 0;
+            rq[i].load(pq[i], 0, vq);
+            pq[i] += TT * (isc ? a.ct : a.bt);
         }
     };
     // what a tile's epilogue needs: y = (sum over n + base) factor
-    float base[EPT], factor[EPT];
-    auto stage = [&](int64_t i) {
+    struct Held {
+        float base[EPT], factor[EPT];
+    } even, odd;
+    auto stage = [&](int64_t i, Held& k) {
         const int buf = (int)(i & 1);
         // a token past the end or a channel past the group moves nothing: its
         // decay is exp(0) and it adds 0
@@ -193,13 +214,13 @@ __global__ __launch_bounds__(512) void ssm_fwd_kernel(SsmArgs a, int64_t nblk, i
         if constexpr (OUT) {
 #pragma unroll
             for (int e = 0; e < EPT; ++e) {
-                base[e] = skip[e] * x[e];
-                factor[e] = 1.f;
+                k.base[e] = skip[e] * x[e];
+                k.factor[e] = 1.f;
             }
             if (a.z) {
                 float z[EPT];
                 rz.unpack(z);
-                ssm_gate(factor, z);
+                ssm_gate(k.factor, z);
             }
         }
 #pragma unroll
@@ -212,54 +233,54 @@ __global__ __launch_bounds__(512) void ssm_fwd_kernel(SsmArgs a, int64_t nblk, i
                 float4{f[0], f[1], f[2], f[3]};
         }
     };
-    auto finish = [&](int64_t i, const float (&base)[EPT], const float (&factor)[EPT]) {
-        const int64_t t = t0 + i * TT + srow;
-        if (t < t1 && sv > 0) {
+    int64_t oo = (b * a.T + t0 + srow) * a.D + scg;
+    auto finish = [&](int64_t i, const Held& k) {
+        if (t0 + i * TT + srow < t1 && sv > 0) {
             float y[EPT];
 #pragma unroll
-            for (int e = 0; e < EPT; ++e) y[e] = (ys[i & 1][srow][sc + e] + base[e]) * factor[e];
-            row_store<EPT, RAG>(a.y, (b * a.T + t) * a.D + scg, a.out_bf16, y, sv);
+            for (int e = 0; e < EPT; ++e)
+                y[e] = (ys[i & 1][srow][sc + e] + k.base[e]) * k.factor[e];
+            row_store<EPT, RAG>(a.y, oo, a.out_bf16, y, sv);
         }
+        oo += TT * a.D;
     };
     fetch(t0);
-    stage(0);
+    stage(0, even);
     if (tiles > 1) fetch(t0 + TT);
     __syncthreads();
-    for (int64_t i = 0; i < tiles; ++i) {
-        // while tile i runs: tile i + 1 is staged, tile i + 2's loads are
-        // issued, then tile i - 1 goes out
-        float pb[EPT], pf[EPT];
-        if constexpr (OUT) {
-#pragma unroll
-            for (int e = 0; e < EPT; ++e) {
-                pb[e] = base[e];
-                pf[e] = factor[e];
-            }
-        }
+    // while tile i runs: tile i + 1 is staged and tile i + 2's loads are issued;
+    // then tile i goes out while tile i + 1 runs
+    auto step = [&](int64_t i, const Held& now, Held& next) {
         if (i + 1 < tiles) {
-            stage(i + 1);
+            stage(i + 1, next);
             if (i + 2 < tiles) fetch(t0 + (i + 2) * TT);
         }
         __syncthreads();
-        if constexpr (OUT) finish(i, pb, pf);
+        if constexpr (OUT) finish(i, now);
+    };
+    for (int64_t i = 0; i < tiles; i += 2) {
+        step(i, even, odd);
+        if (i + 1 < tiles) step(i + 1, odd, even);
     }
 }
 
 // One decode token: every lane streams its 4 states once; bound by the
 // state's HBM traffic (8 bytes per state against ~6 operations).
+// A workgroup takes 256 / LPC channels of one sequence.
 template <int LPC, bool BF16>
-__global__ __launch_bounds__(256) void ssm_step_kernel(SsmArgs a) {
-    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int ng = (int)(id % LPC);
-    const int64_t bc = id / LPC;
-    const bool live = bc < a.B * a.D;
-    const int64_t b = live ? bc / a.D : 0, ch = live ? bc % a.D : 0;
+__global__ __launch_bounds__(256) void ssm_step_kernel(SsmArgs a, uint32_t nblk) {
+    const uint32_t blk = blockIdx.x % nblk;
+    const int64_t b = blockIdx.x / nblk;
+    const int ng = threadIdx.x % LPC;
+    const uint32_t c = blk * (256 / LPC) + threadIdx.x / LPC;
+    const bool live = c < (uint32_t)a.D;
+    const int64_t ch = live ? c : 0;
     const int nv = live ? states_valid<4>(a.N, 4 * ng) : 0;
     float h[4], A4[4], B4[4], C4[4], x[1], r[1], z[1];
     const int64_t so = (b * a.D + ch) * a.N + 4 * ng;
     states_load<4>(h, a.h0 + so, nv);
     param_load<4>(A4, a.A + ch * a.N + 4 * ng, nv);
-    const int64_t g = ch / (a.D / a.G);
+    const int64_t g = a.G == 1 ? 0 : (uint32_t)ch / (uint32_t)(a.D / a.G);
     Row<4, BF16, true> rb, rc;
     Row<1, BF16, false> rx, rt, rz;
     rb.load(a.Bm, b * a.bb + g * a.N + 4 * ng, nv);
@@ -289,7 +310,7 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(SsmArgs a) {
         float y[1] = {__builtin_fmaf(skip, x[0], s)};
         if (a.z) {
             rz.unpack(z);
-            y[0] *= z[0] * sigmoid_fast(z[0]);
+            y[0] *= z[0] * sigmoid(z[0]);
         }
         row_store<1>(a.y, b * a.D + ch, a.out_bf16, y, 1);
     }
@@ -314,7 +335,7 @@ hipError_t launch_fwd_r(const SsmArgs& a, const SsmPlan& p) {
 
 template <int NS, int NG>
 hipError_t launch_fwd_t(const SsmArgs& a, const SsmPlan& p) {
-    const bool rag = (a.D / a.G) % 8 != 0 || a.N % 4 != 0;
+    const bool rag = (a.D / a.G) % 8 != 0 || a.N % NS != 0;
     if (a.in_bf16)
         return rag ? launch_fwd_r<NS, NG, true, true>(a, p)
                    : launch_fwd_r<NS, NG, true, false>(a, p);
@@ -324,17 +345,20 @@ hipError_t launch_fwd_t(const SsmArgs& a, const SsmPlan& p) {
 
 template <int LPC>
 hipError_t launch_step_t(const SsmArgs& a) {
-    const dim3 grid((unsigned)cdiv(a.B * a.D * LPC, 256));
+    const int64_t nblk = cdiv(a.D * LPC, 256);
+    const dim3 grid((unsigned)(a.B * nblk));
     if (a.in_bf16)
-        hipLaunchKernelGGL((ssm_step_kernel<LPC, true>), grid, dim3(256), 0, a.stream, a);
+        hipLaunchKernelGGL((ssm_step_kernel<LPC, true>), grid, dim3(256), 0, a.stream, a,
+                           (uint32_t)nblk);
     else
-        hipLaunchKernelGGL((ssm_step_kernel<LPC, false>), grid, dim3(256), 0, a.stream, a);
+        hipLaunchKernelGGL((ssm_step_kernel<LPC, false>), grid, dim3(256), 0, a.stream, a,
+                           (uint32_t)nblk);
     return hipGetLastError();
 }
 
 }  // namespace
 
-int ssm_lanes(int64_t N) {
+static int ssm_lanes(int64_t N) {
     int l = 1;
     while (4 * l < N) l *= 2;
     return l;
@@ -377,6 +401,10 @@ hipError_t launch_ssm_fwd(SsmArgs a, float* ws) {
     if (a.N <= 16) return launch_fwd_t<4, 4>(a, p);
     if (a.N <= 32) return launch_fwd_t<8, 4>(a, p);
     return launch_fwd_t<16, 4>(a, p);
+}
+
+int64_t ssm_step_workgroups(int64_t B, int64_t D, int64_t N) {
+    return B * cdiv(D * ssm_lanes(N), 256);
 }
 
 hipError_t launch_ssm_step(const SsmArgs& a) {
