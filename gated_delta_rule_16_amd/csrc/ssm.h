@@ -3,7 +3,10 @@
 // Lane layout of the sequence kernels.  A wave is four rows of 16 lanes.  The
 // 16 lanes of a row are 16 channels; a lane holds NS neighbouring states of
 // its channel, and NG = 1, 2 or 4 rows share a channel (NS NG >= N), so a wave
-// runs CW = 64 / NG channels and a workgroup of four waves WC = 4 CW.
+// runs CW = 64 / NG channels and the workgroup's NG running waves WC = 64.
+// Four more waves of the workgroup stage the tokens to come in LDS (Delta and
+// Delta x once per channel, B and C in fp32) and finish those that are done,
+// so the running waves meet no global access in their token loop.
 // B_t[n] is then the same for all lanes of a row: one register holds it for
 // 16 / NS tokens (lane k NS + j of row r: token k, state NS (r % NG) + j), and
 // every product takes its factor by a DPP row broadcast, as part of the

@@ -8,7 +8,7 @@
 //   dDelta_t = x_t sum_n g_t B_t + sum_n p_t A,  dz_t = dout_t y_t (z sigmoid(z))',
 //
 // Two passes.  The first runs the state forward and keeps it every S tokens
-// (block_tokens; 16 at N = 16: 8 bytes of traffic per state and 16 tokens).  The
+// (block_tokens; 16 up to N = 16: 8 bytes of traffic per state and 16 tokens).  The
 // second goes backwards over blocks of S tokens: it runs a block's states
 // again from the kept one, leaving h_t and a_t of all S tokens in registers
 // (128 of them), then walks the block backwards.  Lanes are laid out as in
@@ -32,31 +32,29 @@ namespace gdr {
 namespace {
 
 // Tokens per block of the second pass, and between kept states: what fills
-// 128 registers with h and a, but fewer where few states per channel leave a
-// workgroup many channels to stage (4 per thread; the kept states are then 4
-// bytes per channel and token as at N = 16).
-template <int NS, int NG> constexpr int block_tokens() { return NG < 4 ? 4 * NG : 64 / NS; }
+// 128 registers with h and a.
+template <int NS> constexpr int block_tokens() { return 64 / NS; }
 
 // First pass.  GAM: more than one segment.  As in the forward, four waves run
 // the states while four stage the next tile.
 template <int NS, int NG, bool GAM, bool BF16, bool RAG>
-__global__ __launch_bounds__(512) void ssm_bwd_states_kernel(SsmBwdArgs a, int64_t nblk,
+__global__ __launch_bounds__(64 * (NG + 4)) void ssm_bwd_states_kernel(SsmBwdArgs a, int64_t nblk,
                                                              int64_t nseg, int64_t L) {
-    constexpr int NP = NS * NG, CW = 64 / NG, WC = 4 * CW;
+    constexpr int NP = NS * NG, CW = 64 / NG, WC = NG * CW;
     constexpr int EPT = 8;
     constexpr int TT = 256 * EPT / WC;
     constexpr int TPR = WC / EPT;
     constexpr int NQ = TT * NP / 4;
     constexpr int QPT = (2 * NQ + 255) / 256;
     constexpr int KT = 16 / NS;
-    constexpr int S = block_tokens<NS, NG>();
+    constexpr int S = block_tokens<NS>();
     __shared__ float2 dd[2][TT][WC];
     __shared__ __align__(16) float bc[2][2][TT * NP];
     __shared__ float ds[2][GAM ? TT : 1][WC];
 
-    const int lane = threadIdx.x & 63, tid = threadIdx.x & 255;
-    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) & 3;
-    const bool scans = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) < 4;
+    const int lane = threadIdx.x & 63, tid = (int)threadIdx.x - 64 * NG;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const bool scans = wv < NG;
     int64_t id = blockIdx.x;
     const int64_t blk = id % nblk;
     id /= nblk;
@@ -339,10 +337,10 @@ __device__ __forceinline__ void channel_sums(float (*p)[2 * NS * NG], const floa
 // next block meanwhile and finish the last one: its gradients from the sums
 // over n, which the running waves leave in the block's place in st.
 template <int NS, int NG, bool BF16, bool RAG>
-__global__ __launch_bounds__(512, NS == 16 ? 1 : 2) void ssm_bwd_kernel(SsmBwdArgs a, int64_t nblk,
+__global__ __launch_bounds__(64 * (NG + 4), NS == 16 ? 1 : 2) void ssm_bwd_kernel(SsmBwdArgs a, int64_t nblk,
                                                                        int64_t nseg, int64_t L) {
-    constexpr int NP = NS * NG, CW = 64 / NG, WC = 4 * CW;
-    constexpr int S = block_tokens<NS, NG>();
+    constexpr int NP = NS * NG, CW = 64 / NG, WC = NG * CW;
+    constexpr int S = block_tokens<NS>();
     constexpr int EPT = S * WC / 256;
     constexpr int TPR = WC / EPT;
     constexpr int NQ = S * NP / 4;
@@ -353,11 +351,11 @@ __global__ __launch_bounds__(512, NS == 16 ? 1 : 2) void ssm_bwd_kernel(SsmBwdAr
     // take the place of Delta and Delta x
     __shared__ __align__(16) float st[2][4][S][WP];
     __shared__ __align__(16) float bc[2][2][S * NP];
-    __shared__ float pbc[2][4][S][2 * NP];    // each wave's sums over its channels: dC, dB
+    __shared__ float pbc[2][NG][S][2 * NP];   // each wave's sums over its channels: dC, dB
 
-    const int lane = threadIdx.x & 63, tid = threadIdx.x & 255;
-    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) & 3;
-    const bool runs = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) < 4;
+    const int lane = threadIdx.x & 63, tid = (int)threadIdx.x - 64 * NG;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const bool runs = wv < NG;
     int64_t id = blockIdx.x;
     const int64_t blk = id % nblk;
     id /= nblk;
@@ -636,9 +634,11 @@ __global__ __launch_bounds__(512, NS == 16 ? 1 : 2) void ssm_bwd_kernel(SsmBwdAr
 #pragma unroll
         for (int i = 0; i < PPT; ++i) {
             const int q = (tid + 256 * i) / (2 * NP), c = (tid + 256 * i) % (2 * NP);
-            if (q < left)
-                pbo[q * bct + c] =
-                    (pbc[buf][0][q][c] + pbc[buf][1][q][c]) + (pbc[buf][2][q][c] + pbc[buf][3][q][c]);
+            if (q >= left) continue;
+            float s = pbc[buf][0][q][c];
+#pragma unroll
+            for (int w = 1; w < NG; ++w) s += pbc[buf][w][q][c];
+            pbo[q * bct + c] = s;
         }
         oo -= S * a.D;
         pbo -= S * bct;
@@ -702,14 +702,13 @@ int64_t padded_states(int64_t N) {
     return n;
 }
 
-// Segments of the backward.  Its second pass holds two waves per SIMD, so one
-// segment does where the channels give 2048 waves; fewer channels get enough
-// segments (of at least 64 tokens) for that.
+// Segments of the backward: of at least 64 tokens, enough for two workgroups
+// per compute unit (B 4 T 4096 D 2048 N 16: 587 us with 512 workgroups, 630
+// with 256, 780 with 384).
 SsmPlan bwd_plan(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N) {
     SsmPlan p;
-    p.nblk = cdiv(D / G, ssm_wg_channels(N));
-    const int64_t waves = 4 * B * G * p.nblk;
-    int64_t n = cdiv(2048, waves);
+    p.nblk = cdiv(D / G, 64);
+    int64_t n = cdiv(512, B * G * p.nblk);
     const int64_t most = cdiv(T, 64);
     if (n > most) n = most;
     if (n < 1) n = 1;
@@ -718,8 +717,8 @@ SsmPlan bwd_plan(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N) {
     return p;
 }
 
-// Tokens between kept states, for N states.
-int64_t kept_tokens(int64_t N) { return N <= 4 ? 4 : N <= 8 ? 8 : N <= 16 ? 16 : N <= 32 ? 8 : 4; }
+// Tokens between kept states, for N states (block_tokens).
+int64_t kept_tokens(int64_t N) { return N <= 16 ? 16 : N <= 32 ? 8 : 4; }
 
 struct BwdLayout {
     size_t ckpt, csum, hend, gstart, sdelta, part, bcpart, total;
@@ -750,14 +749,14 @@ template <int NS, int NG, bool BF16, bool RAG>
 hipError_t launch_bwd_r(const SsmBwdArgs& a, const SsmPlan& p) {
     const dim3 grid((unsigned)(a.B * a.G * p.nblk * p.nseg));
     if (p.nseg > 1)
-        hipLaunchKernelGGL((ssm_bwd_states_kernel<NS, NG, true, BF16, RAG>), grid, dim3(512), 0,
+        hipLaunchKernelGGL((ssm_bwd_states_kernel<NS, NG, true, BF16, RAG>), grid, dim3(64 * (NG + 4)), 0,
                            a.stream, a, p.nblk, p.nseg, p.L);
     else
-        hipLaunchKernelGGL((ssm_bwd_states_kernel<NS, NG, false, BF16, RAG>), grid, dim3(512), 0,
+        hipLaunchKernelGGL((ssm_bwd_states_kernel<NS, NG, false, BF16, RAG>), grid, dim3(64 * (NG + 4)), 0,
                            a.stream, a, p.nblk, p.nseg, p.L);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((ssm_bwd_kernel<NS, NG, BF16, RAG>), grid, dim3(512), 0, a.stream, a,
+    hipLaunchKernelGGL((ssm_bwd_kernel<NS, NG, BF16, RAG>), grid, dim3(64 * (NG + 4)), 0, a.stream, a,
                        p.nblk, p.nseg, p.L);
     return hipGetLastError();
 }

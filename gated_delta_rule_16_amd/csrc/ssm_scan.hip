@@ -29,9 +29,9 @@ namespace gdr {
 namespace {
 
 template <int NS, int NG, bool OUT, bool BF16, bool RAG>
-__global__ __launch_bounds__(512) void ssm_fwd_kernel(SsmArgs a, int64_t nblk, int64_t nseg,
+__global__ __launch_bounds__(64 * (NG + 4)) void ssm_fwd_kernel(SsmArgs a, int64_t nblk, int64_t nseg,
                                                       int64_t L) {
-    constexpr int NP = NS * NG, CW = 64 / NG, WC = 4 * CW;
+    constexpr int NP = NS * NG, CW = 64 / NG, WC = NG * CW;
     constexpr int EPT = 8;                            // staged channels per thread
     constexpr int TT = 256 * EPT / WC;                // tokens per tile
     constexpr int TPR = WC / EPT;                     // threads per token row
@@ -43,9 +43,9 @@ __global__ __launch_bounds__(512) void ssm_fwd_kernel(SsmArgs a, int64_t nblk, i
     __shared__ __align__(16) float bc[2][2][TT * NP];
     __shared__ float ys[2][OUT ? TT : 1][YP];
 
-    const int lane = threadIdx.x & 63, tid = threadIdx.x & 255;
-    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) & 3;
-    const bool scans = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) < 4;
+    const int lane = threadIdx.x & 63, tid = (int)threadIdx.x - 64 * NG;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const bool scans = wv < NG;
     int64_t id = blockIdx.x;
     const int64_t blk = id % nblk;
     id /= nblk;
@@ -323,13 +323,13 @@ hipError_t launch_fwd_r(const SsmArgs& a, const SsmPlan& p) {
     const int64_t wgs = a.B * a.G * p.nblk;
     if (p.nseg > 1) {
         hipLaunchKernelGGL((ssm_fwd_kernel<NS, NG, false, BF16, RAG>),
-                           dim3((unsigned)(wgs * (p.nseg - 1))), dim3(512), 0, a.stream, a, p.nblk,
+                           dim3((unsigned)(wgs * (p.nseg - 1))), dim3(64 * (NG + 4)), 0, a.stream, a, p.nblk,
                            p.nseg, p.L);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     hipLaunchKernelGGL((ssm_fwd_kernel<NS, NG, true, BF16, RAG>), dim3((unsigned)(wgs * p.nseg)),
-                       dim3(512), 0, a.stream, a, p.nblk, p.nseg, p.L);
+                       dim3(64 * (NG + 4)), 0, a.stream, a, p.nblk, p.nseg, p.L);
     return hipGetLastError();
 }
 
@@ -364,19 +364,16 @@ static int ssm_lanes(int64_t N) {
     return l;
 }
 
-// Channels of a workgroup of the sequence kernels: 16 lanes of 4 waves, times
-// the channels that rows hold side by side when N is small.
-int64_t ssm_wg_channels(int64_t N) { return N <= 4 ? 256 : N <= 8 ? 128 : 64; }
-
-// Segments of the forward.  One when the channels fill the chip: 768 waves,
-// three quarters of one per SIMD.  Below that enough segments for two waves
-// per SIMD, of at least 64 tokens.
+// Segments of the forward.  One when the channels give 192 workgroups, three
+// quarters of one per compute unit; below that enough, of at least 64
+// tokens, for two per compute unit (B 1 T 32768 D 2048 N 16: 417 us with 512
+// workgroups, 454 with 256, 556 with 384, 885 with 128).
 SsmPlan ssm_fwd_plan(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N) {
     SsmPlan p;
-    p.nblk = cdiv(D / G, ssm_wg_channels(N));
-    const int64_t waves = 4 * B * G * p.nblk;
+    p.nblk = cdiv(D / G, 64);
+    const int64_t wgs = B * G * p.nblk;
     int64_t n = 1;
-    if (waves < 768) n = cdiv(2048, waves);
+    if (wgs < 192) n = cdiv(512, wgs);
     const int64_t most = cdiv(T, 64);
     if (n > most) n = most;
     if (n < 1) n = 1;
