@@ -813,9 +813,7 @@ def _buffer(name, t, dtype, shape, device, like=None):
     """A given output buffer, checked, or a new one (``like``: a tensor that may
     have its type and shape already, which is the quicker way to one)."""
     if t is None:
-        if like is not None and like.dtype is dtype and like.shape == shape and like.is_contiguous():
-            return torch.empty_like(like)
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _new(like, dtype, shape, device)
     _whole(name, t, dtype, shape, device)
     return t
 
@@ -827,6 +825,19 @@ def _scratch(workspace, need, device):
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     return workspace
+
+
+def _new(like, dtype, shape, device):
+    """A new tensor; of the type and shape of ``like`` where it has them already."""
+    if like is not None and like.dtype is dtype and like.shape == shape and like.is_contiguous():
+        return torch.empty_like(like)
+    return torch.empty(shape, dtype=dtype, device=device)
+
+
+@functools.lru_cache(maxsize=256)
+def _need(name, *sizes):
+    """A workspace size (a function of the sizes alone)."""
+    return int(getattr(lib, name)(*sizes))
 
 
 def _p(t):
@@ -922,13 +933,14 @@ def gdr_short_conv_bwd(x, w, bias, s0, dy, ds_final=None, *, silu=True,
     if ds_final is not None:
         _whole("ds_final", ds_final, torch.float32, (B, K - 1, C), dev)
     code = _dt_of("grad_dtype", grad_dtype)
-    f32 = dict(dtype=torch.float32, device=dev)
-    dx = torch.empty((B, T, C), dtype=grad_dtype, device=dev)
-    dw = torch.empty((C, K), **f32) if want_dw else None
-    db = torch.empty((C,), **f32) if want_dw and bias is not None else None
-    ds0 = torch.empty((B, max(K - 1, 0), C), **f32) if want_ds0 else None
+    f32 = torch.float32
+    dx = _new(dy, grad_dtype, x.shape, dev)
+    dw = torch.empty_like(w) if want_dw else None
+    db = torch.empty_like(bias) if want_dw and bias is not None else None
+    ds0 = _new(ds_final, f32, (B, max(K - 1, 0), C), dev) if want_ds0 else None
     if want_dw or workspace is not None:
-        workspace = _scratch(workspace, gdr_short_conv_bwd_workspace_size(B, T, C, K), dev)
+        workspace = _scratch(workspace, _need("gdr_short_conv_bwd_workspace_size", B, T, C, K),
+                             dev)
     _run("gdr_short_conv_bwd", lib.gdr_short_conv_bwd(
         B, T, C, K, _DT[x.dtype], _p(x), _p(w), _p(bias), _p(s0), _DT[dy.dtype], _p(dy),
         _i64s(*xs, *ys), _p(ds_final), GDR_CONV_SILU if silu else 0, code, _p(dx), _p(dw),
@@ -990,7 +1002,7 @@ def gdr_ssm_scan_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, h0=None, *,
         _whole("h0", h0, torch.float32, (B, Dn, N), dev)
     odt = out_dtype or (x.dtype if y is None else y.dtype)
     code = _dt_of("output dtype", odt)
-    need = gdr_ssm_scan_fwd_workspace_size(B, T, Dn, G, N)
+    need = _need("gdr_ssm_scan_fwd_workspace_size", B, T, Dn, G, N)
     y = _buffer("y", y, odt, (B, T, Dn), dev, dt)
     if h_final is not None or want_state:
         h_final = _buffer("h_final", h_final, torch.float32, (B, Dn, N), dev, h0)
@@ -1043,16 +1055,17 @@ def gdr_ssm_scan_bwd(x, dt, A, Bm, Cm, D, z, dt_bias, h0, dout, dh_final=None, *
     if dh_final is not None:
         _whole("dh_final", dh_final, torch.float32, (B, Dn, N), dev)
     code = _dt_of("grad_dtype", grad_dtype)
-    f32 = dict(dtype=torch.float32, device=dev)
-    act = dict(dtype=grad_dtype, device=dev)
-    dx, ddt = torch.empty((B, T, Dn), **act), torch.empty((B, T, Dn), **act)
-    dB, dC = torch.empty((B, T, G, N), **act), torch.empty((B, T, G, N), **act)
-    dz = None if z is None else torch.empty((B, T, Dn), **act)
-    dA = torch.empty((Dn, N), **f32)
-    dD = None if D is None else torch.empty((Dn,), **f32)
-    db = None if dt_bias is None else torch.empty((Dn,), **f32)
-    dh0 = torch.empty((B, Dn, N), **f32) if want_dh0 else None
-    workspace = _scratch(workspace, gdr_ssm_scan_bwd_workspace_size(B, T, Dn, G, N), dev)
+    dx = _new(dout, grad_dtype, x.shape, dev)
+    ddt = torch.empty_like(dx)
+    dz = None if z is None else torch.empty_like(dx)
+    dB = _new(Bm, grad_dtype, Bm.shape, dev)
+    dC = torch.empty_like(dB)
+    dA = torch.empty_like(A)
+    dD = None if D is None else torch.empty_like(D)
+    db = None if dt_bias is None else torch.empty_like(dt_bias)
+    dh0 = _new(dh_final, torch.float32, (B, Dn, N), dev) if want_dh0 else None
+    workspace = _scratch(workspace, _need("gdr_ssm_scan_bwd_workspace_size", B, T, Dn, G, N),
+                         dev)
     _run("gdr_ssm_scan_bwd", lib.gdr_ssm_scan_bwd(
         B, T, Dn, G, N, _DT[x.dtype], _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(z),
         _p(dt_bias), _p(h0), _DT[dout.dtype], _p(dout), _p(dh_final), _i64s(*st),
@@ -1139,11 +1152,11 @@ def gdr_layer_norm_bwd(x, w, dy, eps=1e-5, *, dres=None, grad_dtype=torch.float3
         rr = _as_rows("dres", dres)[2]
     if w is not None:
         _whole("w", w, torch.float32, (C,), dev)
-    dx = torch.empty(x.shape, dtype=grad_dtype, device=dev)
-    f32 = dict(dtype=torch.float32, device=dev)
-    dw, db = (torch.empty((C,), **f32), torch.empty((C,), **f32)) if want_dw else (None, None)
+    dx = _new(dy, grad_dtype, x.shape, dev)
+    dw = _new(w, torch.float32, (C,), dev) if want_dw else None
+    db = torch.empty_like(dw) if want_dw else None
     if want_dw or workspace is not None:
-        workspace = _scratch(workspace, gdr_layer_norm_bwd_workspace_size(R, C), dev)
+        workspace = _scratch(workspace, _need("gdr_layer_norm_bwd_workspace_size", R, C), dev)
     _run("gdr_layer_norm_bwd", lib.gdr_layer_norm_bwd(
         R, C, _DT[x.dtype], _p(x), xr, _p(w), _DT[dy.dtype], _p(dy), yr, float(eps), code,
         _p(dres), rr, _p(dx), _p(dw), _p(db), _p(workspace),

@@ -10,7 +10,8 @@
 // So the type is a template parameter, a group's words are written by its
 // load alone (lanes without a group keep the zeros set before it), and in the
 // RAG variant, for rows whose length is no multiple of E, the elements of the
-// last, partial group have registers of their own, selected at unpacking.
+// last, partial group have registers of their own, joined at unpacking.  Waves
+// without a partial group (`part` false, the same in all lanes) skip both.
 #pragma once
 
 #include "gdr_device.h"
@@ -31,8 +32,9 @@ template <int E, bool BF16, bool RAG> struct Row {
     uint32_t p[RAG ? E : 1];    // a partial group's elements
 
     // Channels [0, valid) at element offset `off`; the others become 0.  Without
-    // RAG valid is 0 or E.
-    __device__ __forceinline__ void load(const void* base, int64_t off, int valid) {
+    // RAG, or without `part`, valid is 0 or E.
+    __device__ __forceinline__ void load(const void* base, int64_t off, int valid,
+                                         bool part = true) {
 #pragma unroll
         for (int i = 0; i < W; ++i) w[i] = 0u;
         if (valid >= E) {
@@ -66,7 +68,7 @@ template <int E, bool BF16, bool RAG> struct Row {
                 }
             }
         }
-        if constexpr (RAG) {
+        if (RAG && part) {
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 p[e] = 0u;
@@ -80,19 +82,27 @@ template <int E, bool BF16, bool RAG> struct Row {
         }
     }
 
-    __device__ __forceinline__ void unpack(float (&f)[E]) const {
+    __device__ __forceinline__ void unpack(float (&f)[E], bool part = true) const {
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             if constexpr (BF16)
                 f[e] = __uint_as_float((e & 1) ? (w[e / 2] & 0xffff0000u) : (w[e / 2] << 16));
             else
                 f[e] = __uint_as_float(w[e]);
+        }
+        if (RAG && part) {
             // one of the two is 0
-            if constexpr (RAG) f[e] = __uint_as_float(__float_as_uint(f[e]) |
-                                                      (BF16 ? p[e] << 16 : p[e]));
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                f[e] = __uint_as_float(__float_as_uint(f[e]) | (BF16 ? p[e] << 16 : p[e]));
         }
     }
 };
+
+// Whether some lane of the wave holds a partial group.
+__device__ __forceinline__ bool any_partial(int valid, int e) {
+    return __builtin_amdgcn_ballot_w64(valid > 0 && valid < e) != 0;
+}
 
 // Stores channels [0, valid) of the E (bf16: round to nearest even).  Without
 // RAG valid is 0 or E.

@@ -30,11 +30,11 @@ __device__ __forceinline__ int clampi(int64_t v, int hi) {
 // (or zeros without one).
 template <int EE, bool BF16, bool RAG>
 __device__ __forceinline__ void load_in(Row<EE, BF16, RAG>& r, const ConvArgs& a, int64_t b,
-                                        int64_t t, int64_t c, int valid) {
+                                        int64_t t, int64_t c, int valid, bool part) {
     const bool past = t < 0;
     r.load(past ? a.s0 : a.x,
            past ? (b * (a.K - 1) + t + a.K - 1) * a.C + c : b * a.xb + t * a.xt + c,
-           past && !a.s0 ? 0 : valid);
+           past && !a.s0 ? 0 : valid, part);
 }
 
 template <int K, bool BF16, bool RAG>
@@ -47,6 +47,7 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int64_t ncb, 
     const int64_t st = (id % nstretch) * 4 + wv, b = id / nstretch;
     const int64_t c = (cb * 64 + lane) * E;
     const int valid = clampi(a.C - c, E);
+    const bool part = any_partial(valid, E);
     const int64_t t0 = st * TL;
     if (valid == 0 || t0 >= a.T) return;
     const int64_t t1 = t0 + TL < a.T ? t0 + TL : a.T;
@@ -57,20 +58,20 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int64_t ncb, 
     {
         Row<E, BF16, RAG> r[K - 1];
 #pragma unroll
-        for (int j = 0; j < K - 1; ++j) load_in(r[j], a, b, t0 - (K - 1) + j, c, valid);
+        for (int j = 0; j < K - 1; ++j) load_in(r[j], a, b, t0 - (K - 1) + j, c, valid, part);
 #pragma unroll
-        for (int j = 0; j < K - 1; ++j) r[j].unpack(win[j]);
+        for (int j = 0; j < K - 1; ++j) r[j].unpack(win[j], part);
         if (t0 == 0 && a.s_final) {
             // the lane that reads the state also writes the next one, so the
             // two may be the same buffer: all K - 1 rows are read (the state
             // rows above, or x) before the first is written
             Row<E, BF16, RAG> f[K - 1];
 #pragma unroll
-            for (int m = 0; m < K - 1; ++m) load_in(f[m], a, b, a.T - (K - 1) + m, c, valid);
+            for (int m = 0; m < K - 1; ++m) load_in(f[m], a, b, a.T - (K - 1) + m, c, valid, part);
 #pragma unroll
             for (int m = 0; m < K - 1; ++m) {
                 float v[E];
-                f[m].unpack(v);
+                f[m].unpack(v, part);
                 row_store<E, RAG>(a.s_final, (b * (K - 1) + m) * a.C + c, BF16, v, valid);
             }
         }
@@ -79,11 +80,11 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int64_t ncb, 
         Row<E, BF16, RAG> r[FWD_TOKENS];
 #pragma unroll
         for (int u = 0; u < FWD_TOKENS; ++u)
-            r[u].load(a.x, b * a.xb + (t + u < t1 ? t + u : t1 - 1) * a.xt + c, valid);
+            r[u].load(a.x, b * a.xb + (t + u < t1 ? t + u : t1 - 1) * a.xt + c, valid, part);
 #pragma unroll
         for (int u = 0; u < FWD_TOKENS; ++u) {
             float x[E], y[E];
-            r[u].unpack(x);
+            r[u].unpack(x, part);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 float s = bias[e];
@@ -146,6 +147,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int64_t ncb, 
     const int64_t cb = blockIdx.x % ncb, row = blockIdx.x / ncb;
     const int64_t c = (cb * 64 + lane) * BE;
     const int valid = clampi(a.C - c, BE);
+    const bool part = any_partial(valid, BE);
     float w[BE * K], bias[BE], dw[BE][K], db[BE];
     param_load<BE * K>(w, a.w + c * K, valid * K);
     param_load<BE>(bias, a.bias + c, a.bias ? valid : 0);
@@ -166,8 +168,8 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int64_t ncb, 
 #pragma unroll
             for (int j = 0; j < K - 1; ++j) {
                 Row<BE, BF16, RAG> r;
-                load_in(r, a, b, t0 - (K - 1) + j, c, valid);
-                r.unpack(win[j + 1]);
+                load_in(r, a, b, t0 - (K - 1) + j, c, valid, part);
+                r.unpack(win[j + 1], part);
             }
 #pragma unroll
             for (int j = 0; j < K; ++j)
@@ -182,15 +184,15 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int64_t ncb, 
                 for (int u = 0; u < U; ++u) {
                     const int64_t t = tb + u;
                     const int v = t < a.T && t < tend ? valid : 0;
-                    rx[u].load(a.x, b * a.xb + t * a.xt + c, v);
-                    rd[u].load(a.dy, b * a.yb + t * a.yt + c, v);
+                    rx[u].load(a.x, b * a.xb + t * a.xt + c, v, part);
+                    rd[u].load(a.dy, b * a.yb + t * a.yt + c, v, part);
                 }
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const int64_t t = tb + u;
                     float x[BE], d[BE];
-                    rx[u].unpack(x);
-                    rd[u].unpack(d);
+                    rx[u].unpack(x, part);
+                    rd[u].unpack(d, part);
                     const bool mine = t < t1;     // du_t counts for dw here
                     float out[BE];
 #pragma unroll

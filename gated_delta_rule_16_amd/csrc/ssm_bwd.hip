@@ -8,7 +8,7 @@
 //   dDelta_t = x_t sum_n g_t B_t + sum_n p_t A,  dz_t = dout_t y_t (z sigmoid(z))',
 //
 // Two passes.  The first runs the state forward and keeps it every S tokens
-// (block_tokens; 16 up to N = 16: 8 bytes of traffic per state and 16 tokens).  The
+// (block_tokens; 16 at N = 16: 8 bytes of traffic per state and 16 tokens).  The
 // second goes backwards over blocks of S tokens: it runs a block's states
 // again from the kept one, leaving h_t and a_t of all S tokens in registers
 // (128 of them), then walks the block backwards.  Lanes are laid out as in
@@ -16,7 +16,7 @@
 // sums over channels (dB, dC) are halving reductions over a row's 16 lanes
 // (22 operations a token for the 8 values of a lane at NS = 4), then over the
 // workgroup's waves in LDS, and leave as one partial per workgroup, added by
-// ssm_bc_reduce in a fixed order.
+// ssm_bwd_reduce in a fixed order.
 //
 // Segments: both passes run all segments of a sequence side by side.  The
 // first starts every segment from zero and also forms the gradient that the
@@ -32,8 +32,9 @@ namespace gdr {
 namespace {
 
 // Tokens per block of the second pass, and between kept states: what fills
-// 128 registers with h and a.
-template <int NS> constexpr int block_tokens() { return 64 / NS; }
+// 128 registers with h and a, and half of that where few states leave a
+// workgroup few running waves, so that two fit a compute unit.
+template <int NS, int NG> constexpr int block_tokens() { return NG < 4 ? 8 : 64 / NS; }
 
 // First pass.  GAM: more than one segment.  As in the forward, four waves run
 // the states while four stage the next tile.
@@ -47,7 +48,7 @@ __global__ __launch_bounds__(64 * (NG + 4)) void ssm_bwd_states_kernel(SsmBwdArg
     constexpr int NQ = TT * NP / 4;
     constexpr int QPT = (2 * NQ + 255) / 256;
     constexpr int KT = 16 / NS;
-    constexpr int S = block_tokens<NS>();
+    constexpr int S = block_tokens<NS, NG>();
     __shared__ float2 dd[2][TT][WC];
     __shared__ __align__(16) float bc[2][2][TT * NP];
     __shared__ float ds[2][GAM ? TT : 1][WC];
@@ -164,41 +165,47 @@ __global__ __launch_bounds__(64 * (NG + 4)) void ssm_bwd_states_kernel(SsmBwdArg
                         : static_cast<const T*>(a.Bm) + b * a.bb + (t0 + qt) * a.bt;
         pq[i] += g * a.N + 4 * qn;
     }
-    Row<EPT, BF16, RAG> rx, rt, rz;
-    Row<EPT, true, RAG> ro16;
-    Row<EPT, false, RAG> ro32;
-    Row<4, BF16, RAG> rq[QPT];
-    auto fetch = [&](int64_t tb) {
+    const bool part = any_partial(sv, EPT);
+    // two tiles' loads are in flight, each in its own registers
+    struct Rows {
+        Row<EPT, BF16, RAG> x, t, z;
+        Row<EPT, true, RAG> o16;
+        Row<EPT, false, RAG> o32;
+        Row<4, BF16, RAG> q[QPT];
+    } rows0, rows1;
+    auto fetch = [&](int64_t i, Rows& r) {
+        const int64_t tb = t0 + i * TT;
+        if (tb >= t1) return;
         const int left = t1 - tb < TT ? (int)(t1 - tb) : TT;
         const int v = srow < left ? sv : 0;
-        rx.load(px, 0, v);
-        rt.load(pt, 0, v);
+        r.x.load(px, 0, v, part);
+        r.t.load(pt, 0, v, part);
         px += TT * a.xt;
         pt += TT * a.dtt;
         if constexpr (GAM) {
-            ro16.load(a.dout, po, a.dout_bf16 ? v : 0);
-            ro32.load(a.dout, po, a.dout_bf16 ? 0 : v);
-            rz.load(pz, 0, a.z ? v : 0);
+            r.o16.load(a.dout, po, a.dout_bf16 ? v : 0, part);
+            r.o32.load(a.dout, po, a.dout_bf16 ? 0 : v, part);
+            r.z.load(pz, 0, a.z ? v : 0, part);
             po += TT * a.ot;
             pz += TT * a.zt;
         }
 #pragma unroll
-        for (int i = 0; i < QPT; ++i) {
-            const int q = tid + 256 * i;
+        for (int j = 0; j < QPT; ++j) {
+            const int q = tid + 256 * j;
             const bool isc = q >= NQ;
             if (isc && !GAM) continue;
             const int qt = (q % NQ) / (NP / 4), qn = q % (NP / 4);
             const int vq = q < 2 * NQ && qt < left ? states_valid<4>(a.N, 4 * qn) : 0;
-            rq[i].load(pq[i], 0, vq);
-            pq[i] += TT * (isc ? a.ct : a.bt);
+            r.q[j].load(pq[j], 0, vq);
+            pq[j] += TT * (isc ? a.ct : a.bt);
         }
     };
-    auto stage = [&](int64_t i) {
+    auto stage = [&](int64_t i, const Rows& rows) {
         const int buf = (int)(i & 1);
         const int tv = t0 + i * TT + srow < t1 ? sv : 0;
         float x[EPT], r[EPT], d[EPT];
-        rx.unpack(x);
-        rt.unpack(r);
+        rows.x.unpack(x, part);
+        rows.t.unpack(r, part);
 #pragma unroll
         for (int e = 0; e < EPT; ++e) r[e] += bias[e];
         ssm_deltas(d, r, a.softplus);
@@ -210,10 +217,10 @@ __global__ __launch_bounds__(64 * (NG + 4)) void ssm_bwd_states_kernel(SsmBwdArg
         if constexpr (GAM) {
             float o[EPT], z[EPT];
             if (a.dout_bf16)
-                ro16.unpack(o);
+                rows.o16.unpack(o, part);
             else
-                ro32.unpack(o);
-            rz.unpack(z);
+                rows.o32.unpack(o, part);
+            rows.z.unpack(z, part);
             if (a.z) ssm_gate(o, z);
 #pragma unroll
             for (int e = 0; e < EPT; ++e) ds[buf][srow][sc + e] = o[e];
@@ -223,21 +230,26 @@ __global__ __launch_bounds__(64 * (NG + 4)) void ssm_bwd_states_kernel(SsmBwdArg
             const int q = tid + 256 * q4;
             if (q >= 2 * NQ || (q >= NQ && !GAM)) continue;
             float f[4];
-            rq[q4].unpack(f);
+            rows.q[q4].unpack(f);
             *reinterpret_cast<float4*>(&bc[buf][q >= NQ][4 * (q % NQ)]) =
                 float4{f[0], f[1], f[2], f[3]};
         }
     };
-    fetch(t0);
-    stage(0);
-    if (tiles > 1) fetch(t0 + TT);
+    fetch(0, rows0);
+    fetch(1, rows1);
+    stage(0, rows0);
+    fetch(2, rows0);
     __syncthreads();
-    for (int64_t i = 0; i < tiles; ++i) {
+    auto step = [&](int64_t i, Rows& rows) {
         if (i + 1 < tiles) {
-            stage(i + 1);
-            if (i + 2 < tiles) fetch(t0 + (i + 2) * TT);
+            stage(i + 1, rows);
+            fetch(i + 3, rows);
         }
         __syncthreads();
+    };
+    for (int64_t i = 0; i < tiles; i += 2) {
+        step(i, rows1);
+        if (i + 1 < tiles) step(i + 1, rows0);
     }
 }
 
@@ -340,7 +352,7 @@ template <int NS, int NG, bool BF16, bool RAG>
 __global__ __launch_bounds__(64 * (NG + 4), NS == 16 ? 1 : 2) void ssm_bwd_kernel(SsmBwdArgs a, int64_t nblk,
                                                                        int64_t nseg, int64_t L) {
     constexpr int NP = NS * NG, CW = 64 / NG, WC = NG * CW;
-    constexpr int S = block_tokens<NS>();
+    constexpr int S = block_tokens<NS, NG>();
     constexpr int EPT = S * WC / 256;
     constexpr int TPR = WC / EPT;
     constexpr int NQ = S * NP / 4;
@@ -475,8 +487,8 @@ __global__ __launch_bounds__(64 * (NG + 4), NS == 16 ? 1 : 2) void ssm_bwd_kerne
 #pragma unroll
             for (int tt = S - 4; tt >= 0; tt -= 4) {
                 // half of the kept states are done with: the next block's
-                // start takes their registers
-                if (tt == (S / 2 - 4 > 0 ? S / 2 - 4 : 0) && sub > first) fetch(sub - 1);
+                // start takes their registers (short blocks load it at once)
+                if (tt == (S == 16 ? 4 : S - 4) && sub > first) fetch(sub - 1);
                 Operands next;
                 if (tt > 0) read(next, tt - 4, true);
                 float sB[4], sA[4], pv[4][2 * NS];
@@ -527,30 +539,35 @@ __global__ __launch_bounds__(64 * (NG + 4), NS == 16 ? 1 : 2) void ssm_bwd_kerne
                         : static_cast<const T*>(a.Bm) + b * a.bb + (last * S + qt) * a.bt;
         pq[i] += g * a.N + 4 * qn;
     }
-    Row<EPT, BF16, RAG> rx, rt, rz;
-    Row<EPT, true, RAG> ro16;
-    Row<EPT, false, RAG> ro32;
-    Row<4, BF16, RAG> rq[QPT];
-    auto fetch = [&](int64_t sub) {
+    const bool split = any_partial(sv, EPT);
+    // two blocks' loads are in flight, each in its own registers
+    struct Rows {
+        Row<EPT, BF16, RAG> x, t, z;
+        Row<EPT, true, RAG> o16;
+        Row<EPT, false, RAG> o32;
+        Row<4, BF16, RAG> q[QPT];
+    } rows0, rows1;
+    auto fetch = [&](int64_t sub, Rows& r) {
+        if (sub < first) return;
         const int left = t1 - sub * S < S ? (int)(t1 - sub * S) : S;
         const int v = srow < left ? sv : 0;
-        rx.load(px, 0, v);
-        rt.load(pt, 0, v);
-        ro16.load(a.dout, po, a.dout_bf16 ? v : 0);
-        ro32.load(a.dout, po, a.dout_bf16 ? 0 : v);
-        rz.load(pz, 0, a.z ? v : 0);
+        r.x.load(px, 0, v, split);
+        r.t.load(pt, 0, v, split);
+        r.o16.load(a.dout, po, a.dout_bf16 ? v : 0, split);
+        r.o32.load(a.dout, po, a.dout_bf16 ? 0 : v, split);
+        r.z.load(pz, 0, a.z ? v : 0, split);
         px -= S * a.xt;
         pt -= S * a.dtt;
         po -= S * a.ot;
         pz -= S * a.zt;
 #pragma unroll
-        for (int i = 0; i < QPT; ++i) {
-            const int q = tid + 256 * i;
+        for (int j = 0; j < QPT; ++j) {
+            const int q = tid + 256 * j;
             const bool isc = q >= NQ;
             const int qt = (q % NQ) / (NP / 4), qn = q % (NP / 4);
             const int vq = q < 2 * NQ && qt < left ? states_valid<4>(a.N, 4 * qn) : 0;
-            rq[i].load(pq[i], 0, vq);
-            pq[i] -= S * (isc ? a.ct : a.bt);
+            r.q[j].load(pq[j], 0, vq);
+            pq[j] -= S * (isc ? a.ct : a.bt);
         }
     };
     // of a staged block, until it is finished: x, Delta, its derivative, dy, and
@@ -558,17 +575,17 @@ __global__ __launch_bounds__(64 * (NG + 4), NS == 16 ? 1 : 2) void ssm_bwd_kerne
     struct Held {
         float x[EPT], d[EPT], ddr[EPT], dy[EPT], og[EPT];
     };
-    auto stage = [&](int64_t sub, Held& k) {
+    auto stage = [&](int64_t sub, const Rows& rows, Held& k) {
         const int buf = (int)(sub & 1);
         const int v = sub * S + srow < t1 ? sv : 0;
         float r[EPT], z[EPT];
-        rx.unpack(k.x);
-        rt.unpack(r);
+        rows.x.unpack(k.x, split);
+        rows.t.unpack(r, split);
         if (a.dout_bf16)
-            ro16.unpack(k.dy);
+            rows.o16.unpack(k.dy, split);
         else
-            ro32.unpack(k.dy);
-        rz.unpack(z);
+            rows.o32.unpack(k.dy, split);
+        rows.z.unpack(z, split);
 #pragma unroll
         for (int e = 0; e < EPT; ++e) {
             r[e] += bias[e];
@@ -601,7 +618,7 @@ __global__ __launch_bounds__(64 * (NG + 4), NS == 16 ? 1 : 2) void ssm_bwd_kerne
             const int q = tid + 256 * i;
             if (q >= 2 * NQ) continue;
             float f[4];
-            rq[i].unpack(f);
+            rows.q[i].unpack(f);
             *reinterpret_cast<float4*>(&bc[buf][q >= NQ][4 * (q % NQ)]) =
                 float4{f[0], f[1], f[2], f[3]};
         }
@@ -644,23 +661,24 @@ __global__ __launch_bounds__(64 * (NG + 4), NS == 16 ? 1 : 2) void ssm_bwd_kerne
         pbo -= S * bct;
     };
     Held even, odd;
-    fetch(last);
-    stage(last, even);
-    if (last > first) fetch(last - 1);
+    fetch(last, rows0);
+    fetch(last - 1, rows1);
+    stage(last, rows0, even);
+    fetch(last - 2, rows0);
     __syncthreads();
     // while block sub runs, block sub - 1 is staged (in the buffers of block
-    // sub + 1, finished already) and block sub - 2's loads are issued
-    auto step = [&](int64_t sub, const Held& now, Held& next) {
+    // sub + 1, finished already) and block sub - 3's loads are issued
+    auto step = [&](int64_t sub, const Held& now, Held& next, Rows& rows) {
         if (sub > first) {
-            stage(sub - 1, next);
-            if (sub - 1 > first) fetch(sub - 2);
+            stage(sub - 1, rows, next);
+            fetch(sub - 3, rows);
         }
         __syncthreads();
         finish(sub, now);
     };
     for (int64_t sub = last; sub >= first; sub -= 2) {
-        step(sub, even, odd);
-        if (sub > first) step(sub - 1, odd, even);
+        step(sub, even, odd, rows1);
+        if (sub > first) step(sub - 1, odd, even, rows0);
     }
     // dD and dbias over the thread rows of a channel, through the buffer that
     // the last block did not use (block `first` may not be finished yet)
@@ -680,18 +698,44 @@ __global__ __launch_bounds__(64 * (NG + 4), NS == 16 ? 1 : 2) void ssm_bwd_kerne
     }
 }
 
-// dB, dC [B, T, G, N] = the sum of the channel blocks' partials.
+// dB, dC [B, T, G, N] = the sum of the channel blocks' partials (the first
+// nbc workgroups), and dA, dD, ddt_bias = the sum of the P = B nseg partial rows
+// of D (N + 2) columns (the others: 64 columns each, four waves taking every
+// fourth row).  Fixed orders; one launch, since both are short.
 template <int NP>
-__global__ __launch_bounds__(256) void ssm_bc_reduce(SsmBwdArgs a, int64_t nblk) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, n = a.B * a.T * a.G * 2 * NP;
-    if (i >= n) return;
-    float s = 0.f;
-    for (int64_t k = 0; k < nblk; ++k) s += a.bcpart[k * n + i];
-    const int j = (int)(i % NP);
-    const int64_t row = i / (2 * NP);
-    if (j >= a.N) return;
-    float f[1] = {s};
-    row_store<1>((i / NP) & 1 ? a.dB : a.dC, row * a.N + j, a.grad_bf16, f, 1);
+__global__ __launch_bounds__(256) void ssm_bwd_reduce(SsmBwdArgs a, int64_t nblk, int64_t nbc,
+                                                      int64_t P) {
+    __shared__ float red[4][64];
+    if (blockIdx.x < nbc) {
+        const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, n = a.B * a.T * a.G * 2 * NP;
+        if (i >= n) return;
+        const int j = (int)(i % NP);
+        const int64_t row = i / (2 * NP);
+        if (j >= a.N) return;
+        float s = 0.f;
+        for (int64_t k = 0; k < nblk; ++k) s += a.bcpart[k * n + i];
+        float f[1] = {s};
+        row_store<1>((i / NP) & 1 ? a.dB : a.dC, row * a.N + j, a.grad_bf16, f, 1);
+        return;
+    }
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t M = a.D * (a.N + 2), m = ((int64_t)blockIdx.x - nbc) * 64 + lane;
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    if (m < M) {
+        for (int64_t p = wv; p < P; p += 16)
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (p + 4 * u < P) s[u] += a.part[(p + 4 * u) * M + m];
+    }
+    red[wv][lane] = (s[0] + s[1]) + (s[2] + s[3]);
+    __syncthreads();
+    if (wv == 0 && m < M) {
+        const float v = (red[0][lane] + red[1][lane]) + (red[2][lane] + red[3][lane]);
+        const int64_t d = m - a.D * a.N;
+        if (d < 0) a.dA[m] = v;
+        else if (d < a.D) { if (a.dD) a.dD[d] = v; }
+        else if (a.dbias) a.dbias[d - a.D] = v;
+    }
 }
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -702,13 +746,13 @@ int64_t padded_states(int64_t N) {
     return n;
 }
 
-// Segments of the backward: of at least 64 tokens, enough for two workgroups
-// per compute unit (B 4 T 4096 D 2048 N 16: 587 us with 512 workgroups, 630
+// Segments of the backward: of at least 64 tokens, up to two workgroups per
+// compute unit (B 4 T 4096 D 2048 N 16: 587 us with 512 workgroups, 630
 // with 256, 780 with 384).
 SsmPlan bwd_plan(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N) {
     SsmPlan p;
     p.nblk = cdiv(D / G, 64);
-    int64_t n = cdiv(512, B * G * p.nblk);
+    int64_t n = 512 / (B * G * p.nblk);
     const int64_t most = cdiv(T, 64);
     if (n > most) n = most;
     if (n < 1) n = 1;
@@ -718,7 +762,7 @@ SsmPlan bwd_plan(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N) {
 }
 
 // Tokens between kept states, for N states (block_tokens).
-int64_t kept_tokens(int64_t N) { return N <= 16 ? 16 : N <= 32 ? 8 : 4; }
+int64_t kept_tokens(int64_t N) { return N <= 8 ? 8 : N <= 16 ? 16 : N <= 32 ? 8 : 4; }
 
 struct BwdLayout {
     size_t ckpt, csum, hend, gstart, sdelta, part, bcpart, total;
@@ -771,13 +815,10 @@ hipError_t launch_bwd_t(const SsmBwdArgs& a, const SsmPlan& p) {
         e = rag ? launch_bwd_r<NS, NG, false, true>(a, p)
                 : launch_bwd_r<NS, NG, false, false>(a, p);
     if (e != hipSuccess) return e;
-    const int64_t n = a.B * a.T * a.G * 2 * NS * NG;
-    hipLaunchKernelGGL((ssm_bc_reduce<NS * NG>), dim3((unsigned)cdiv(n, 256)), dim3(256), 0,
-                       a.stream, a, p.nblk);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    return launch_sum_partials(a.part, a.B * p.nseg, a.D * (a.N + 2), a.dA, a.D * a.N, a.dD, a.D,
-                               a.dbias, a.stream);
+    const int64_t nbc = cdiv(a.B * a.T * a.G * 2 * NS * NG, 256);
+    hipLaunchKernelGGL((ssm_bwd_reduce<NS * NG>), dim3((unsigned)(nbc + cdiv(a.D * (a.N + 2), 64))),
+                       dim3(256), 0, a.stream, a, p.nblk, nbc, a.B * p.nseg);
+    return hipGetLastError();
 }
 
 }  // namespace
@@ -789,7 +830,7 @@ size_t ssm_bwd_workspace_bytes(int64_t B, int64_t T, int64_t D, int64_t G, int64
 int64_t ssm_bwd_workgroups(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N) {
     const SsmPlan p = bwd_plan(B, T, D, G, N);
     const int64_t n = 2 * B * G * p.nblk * p.nseg;    // of 512 threads
-    const int64_t r = cdiv(B * T * G * 2 * padded_states(N), 256);
+    const int64_t r = cdiv(B * T * G * 2 * padded_states(N), 256) + cdiv(D * (N + 2), 64);
     return n > r ? n : r;
 }
 

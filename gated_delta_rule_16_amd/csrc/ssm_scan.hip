@@ -167,42 +167,48 @@ __global__ __launch_bounds__(64 * (NG + 4)) void ssm_fwd_kernel(SsmArgs a, int64
                         : static_cast<const T*>(a.Bm) + b * a.bb + (t0 + qt) * a.bt;
         pq[i] += g * a.N + 4 * qn;
     }
-    Row<EPT, BF16, RAG> rx, rt, rz;
-    Row<4, BF16, RAG> rq[QPT];
-    auto fetch = [&](int64_t tb) {
+    const bool part = any_partial(sv, EPT);
+    // two tiles' loads are in flight, each in its own registers
+    struct Rows {
+        Row<EPT, BF16, RAG> x, t, z;
+        Row<4, BF16, RAG> q[QPT];
+    } rows0, rows1;
+    auto fetch = [&](int64_t i, Rows& r) {
+        const int64_t tb = t0 + i * TT;
+        if (tb >= t1) return;
         const int left = t1 - tb < TT ? (int)(t1 - tb) : TT;
         const int v = srow < left ? sv : 0;
-        rx.load(px, 0, v);
-        rt.load(pt, 0, v);
+        r.x.load(px, 0, v, part);
+        r.t.load(pt, 0, v, part);
         px += TT * a.xt;
         pt += TT * a.dtt;
         if constexpr (OUT) {
-            rz.load(pz, 0, a.z ? v : 0);
+            r.z.load(pz, 0, a.z ? v : 0, part);
             pz += TT * a.zt;
         }
 #pragma unroll
-        for (int i = 0; i < QPT; ++i) {
-            const int q = tid + 256 * i;
+        for (int j = 0; j < QPT; ++j) {
+            const int q = tid + 256 * j;
             const bool isc = q >= NQ;
             if (isc && !OUT) continue;
             const int qt = (q % NQ) / (NP / 4), qn = q % (NP / 4);
             const int vq = q < 2 * NQ && qt < left ? states_valid<4>(a.N, 4 * qn) : 0;
-            rq[i].load(pq[i], 0, vq);
-            pq[i] += TT * (isc ? a.ct : a.bt);
+            r.q[j].load(pq[j], 0, vq);
+            pq[j] += TT * (isc ? a.ct : a.bt);
         }
     };
     // what a tile's epilogue needs: y = (sum over n + base) factor
     struct Held {
         float base[EPT], factor[EPT];
     } even, odd;
-    auto stage = [&](int64_t i, Held& k) {
+    auto stage = [&](int64_t i, const Rows& rows, Held& k) {
         const int buf = (int)(i & 1);
         // a token past the end or a channel past the group moves nothing: its
         // decay is exp(0) and it adds 0
         const int tv = t0 + i * TT + srow < t1 ? sv : 0;
         float x[EPT], r[EPT], d[EPT];
-        rx.unpack(x);
-        rt.unpack(r);
+        rows.x.unpack(x, part);
+        rows.t.unpack(r, part);
 #pragma unroll
         for (int e = 0; e < EPT; ++e) r[e] += bias[e];
         ssm_deltas(d, r, a.softplus);
@@ -219,7 +225,7 @@ __global__ __launch_bounds__(64 * (NG + 4)) void ssm_fwd_kernel(SsmArgs a, int64
             }
             if (a.z) {
                 float z[EPT];
-                rz.unpack(z);
+                rows.z.unpack(z, part);
                 ssm_gate(k.factor, z);
             }
         }
@@ -228,7 +234,7 @@ __global__ __launch_bounds__(64 * (NG + 4)) void ssm_fwd_kernel(SsmArgs a, int64
             const int q = tid + 256 * q4;
             if (q >= 2 * NQ || (q >= NQ && !OUT)) continue;
             float f[4];
-            rq[q4].unpack(f);
+            rows.q[q4].unpack(f);
             *reinterpret_cast<float4*>(&bc[buf][q >= NQ][4 * (q % NQ)]) =
                 float4{f[0], f[1], f[2], f[3]};
         }
@@ -244,23 +250,24 @@ __global__ __launch_bounds__(64 * (NG + 4)) void ssm_fwd_kernel(SsmArgs a, int64
         }
         oo += TT * a.D;
     };
-    fetch(t0);
-    stage(0, even);
-    if (tiles > 1) fetch(t0 + TT);
+    fetch(0, rows0);
+    fetch(1, rows1);
+    stage(0, rows0, even);
+    fetch(2, rows0);
     __syncthreads();
-    // while tile i runs: tile i + 1 is staged and tile i + 2's loads are issued;
+    // while tile i runs: tile i + 1 is staged and tile i + 3's loads are issued;
     // then tile i goes out while tile i + 1 runs
-    auto step = [&](int64_t i, const Held& now, Held& next) {
+    auto step = [&](int64_t i, const Held& now, Held& next, Rows& rows) {
         if (i + 1 < tiles) {
-            stage(i + 1, next);
-            if (i + 2 < tiles) fetch(t0 + (i + 2) * TT);
+            stage(i + 1, rows, next);
+            fetch(i + 3, rows);
         }
         __syncthreads();
         if constexpr (OUT) finish(i, now);
     };
     for (int64_t i = 0; i < tiles; i += 2) {
-        step(i, even, odd);
-        if (i + 1 < tiles) step(i + 1, odd, even);
+        step(i, even, odd, rows1);
+        if (i + 1 < tiles) step(i + 1, odd, even, rows0);
     }
 }
 
@@ -373,7 +380,7 @@ SsmPlan ssm_fwd_plan(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N) {
     p.nblk = cdiv(D / G, 64);
     const int64_t wgs = B * G * p.nblk;
     int64_t n = 1;
-    if (wgs < 192) n = cdiv(512, wgs);
+    if (wgs < 192) n = 512 / wgs;
     const int64_t most = cdiv(T, 64);
     if (n > most) n = most;
     if (n < 1) n = 1;
