@@ -68,6 +68,20 @@ __device__ __forceinline__ int left(int64_t C, int64_t c) {
     return v < 0 ? 0 : v > E ? E : (int)v;
 }
 
+// A thread's group of channels at c: how many it has (0 or E).  With RAG (C no
+// multiple of E) the last group of the row is moved back to end with it; its
+// first `twice` channels are those of the group before, and count there.
+template <bool RAG>
+__device__ __forceinline__ int own_group(int64_t& c, int64_t C, int& twice) {
+    twice = 0;
+    if (c >= C) return 0;
+    if (RAG && c > C - E) {
+        twice = (int)(c - (C - E));
+        c = C - E;
+    }
+    return E;
+}
+
 // One group of channels of x (and r), and their sum h: rounded to the stored
 // type, stored.  RES: 0 none, 1 bf16, 2 fp32.
 template <bool BF16, int RES, bool RAG> struct SumIn {
@@ -77,7 +91,7 @@ template <bool BF16, int RES, bool RAG> struct SumIn {
         x.load(a.x, row * a.xr + c, valid);
         if constexpr (RES != 0) r.load(a.res, row * a.rr + c, valid);
     }
-    __device__ __forceinline__ void sum(float (&h)[E], const NormArgs& a, int64_t ho, int valid) {
+    __device__ __forceinline__ void sum(float (&h)[E]) {
         x.unpack(h);
         if constexpr (RES != 0) {
             float q[E];
@@ -87,7 +101,6 @@ template <bool BF16, int RES, bool RAG> struct SumIn {
                 h[e] += q[e];
                 if constexpr (RES == 1) h[e] = bf2f(f2bf(h[e]));
             }
-            row_store<E, RAG>(a.h, ho, RES == 1, h, valid);
         }
     }
 };
@@ -104,41 +117,41 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormArgs a) {
     if (row >= a.R) return;           // a whole wave (WG: never)
     float h[NV][E];
     float s = 0.f;
-    SumIn<BF16, RES, RAG> in[NV];
+    SumIn<BF16, RES, false> in[NV];
+    int64_t at[NV];
+    int v[NV], twice[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        const int64_t c = (int64_t)(k * NT + id) * E;
-        in[k].load(a, row, c, left(a.C, c));
+        at[k] = (int64_t)(k * NT + id) * E;
+        v[k] = own_group<RAG>(at[k], a.C, twice[k]);
+        in[k].load(a, row, at[k], v[k]);
     }
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        const int64_t c = (int64_t)(k * NT + id) * E;
-        in[k].sum(h[k], a, row * a.C + c, left(a.C, c));
+        in[k].sum(h[k]);
+#pragma unroll
+        for (int e = 0; e < E; ++e) s += !RAG || e >= twice[k] ? h[k][e] : 0.f;
     }
-#pragma unroll
-    for (int k = 0; k < NV; ++k)
-#pragma unroll
-        for (int e = 0; e < E; ++e) s += h[k][e];
     const float inv = 1.f / (float)a.C;
     const float mu = row_total<WG>(s, red[0]) * inv;
     s = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        const int v = left(a.C, (int64_t)(k * NT + id) * E);
+        // after the sum's barrier: h may be the residual, which a moved group
+        // of another wave has read by now
+        if constexpr (RES != 0) row_store<E, false>(a.h, row * a.C + at[k], RES == 1, h[k], v[k]);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             h[k][e] -= mu;
-            if (e < v) s = __builtin_fmaf(h[k][e], h[k][e], s);
+            if (v[k] > 0 && (!RAG || e >= twice[k])) s = __builtin_fmaf(h[k][e], h[k][e], s);
         }
     }
     const float rstd = 1.f / sqrtf(row_total<WG>(s, red[1]) * inv + a.eps);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        const int64_t c = (int64_t)(k * NT + id) * E;
-        const int v = left(a.C, c);
         float w[E], b[E];
-        if (a.w) param_load<E>(w, a.w + c, v);
-        if (a.b) param_load<E>(b, a.b + c, v);
+        if (a.w) param_load<E>(w, a.w + at[k], v[k]);
+        if (a.b) param_load<E>(b, a.b + at[k], v[k]);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             float y = h[k][e] * rstd;
@@ -146,7 +159,7 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormArgs a) {
             if (a.b) y += b[e];
             h[k][e] = y;
         }
-        row_store<E, RAG>(a.y, row * a.C + c, a.out_bf16, h[k], v);
+        row_store<E, false>(a.y, row * a.C + at[k], a.out_bf16, h[k], v[k]);
     }
 }
 
@@ -163,7 +176,8 @@ __global__ __launch_bounds__(256) void norm_fwd_long_kernel(NormArgs a) {
         SumIn<BF16, RES, true> in;
         float h[E];
         in.load(a, row, c, left(a.C, c));
-        in.sum(h, a, row * a.C + c, left(a.C, c));
+        in.sum(h);
+        if constexpr (RES != 0) row_store<E>(a.h, row * a.C + c, RES == 1, h, left(a.C, c));
 #pragma unroll
         for (int e = 0; e < E; ++e) s += h[e];
     }
@@ -223,17 +237,22 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwdArgs a) {
         for (int e = 0; e < E; ++e) dw[k][e] = db[k][e] = 0.f;
     const float inv = 1.f / (float)a.C;
     const int64_t stride = (int64_t)gridDim.x * (WG ? 1 : 4);
-    Row<E, BF16, RAG> rh[NV];
-    Row<E, DY16, RAG> rd[NV];
-    Row<E, G16, RAG> rr[NV];
+    int64_t at[NV];
+    int v[NV], twice[NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        at[k] = (int64_t)(k * NT + id) * E;
+        v[k] = own_group<RAG>(at[k], a.C, twice[k]);
+    }
+    Row<E, BF16, false> rh[NV];
+    Row<E, DY16, false> rd[NV];
+    Row<E, G16, false> rr[NV];
     auto fetch = [&](int64_t row) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int64_t c = (int64_t)(k * NT + id) * E;
-            const int v = left(a.C, c);
-            rh[k].load(a.x, row * a.xr + c, v);
-            rd[k].load(a.dy, row * a.yr + c, v);
-            rr[k].load(a.dres, row * a.rr + c, a.dres ? v : 0);
+            rh[k].load(a.x, row * a.xr + at[k], v[k]);
+            rd[k].load(a.dy, row * a.yr + at[k], v[k]);
+            rr[k].load(a.dres, row * a.rr + at[k], a.dres ? v[k] : 0);
         }
     };
     int64_t row = WG ? blockIdx.x : (int64_t)blockIdx.x * 4 + wv;
@@ -247,7 +266,7 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwdArgs a) {
             rd[k].unpack(d[k]);
             rr[k].unpack(q[k]);
 #pragma unroll
-            for (int e = 0; e < E; ++e) s += h[k][e];
+            for (int e = 0; e < E; ++e) s += !RAG || e >= twice[k] ? h[k][e] : 0.f;
         }
         // the next row's loads land while this one is worked on
         if (row + stride < a.R) fetch(row + stride);
@@ -255,13 +274,12 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwdArgs a) {
         float sums[3] = {0.f, 0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int64_t c = (int64_t)(k * NT + id) * E;
-            const int v = left(a.C, c);
             float w[E];
-            if (a.w) param_load<E>(w, a.w + c, v);
+            if (a.w) param_load<E>(w, a.w + at[k], v[k]);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                h[k][e] = e < v ? h[k][e] - mu : 0.f;
+                h[k][e] = v[k] > 0 ? h[k][e] - mu : 0.f;
+                if (RAG && e < twice[k]) continue;
                 sums[0] = __builtin_fmaf(h[k][e], h[k][e], sums[0]);
                 const float dn = a.w ? d[k][e] * w[e] : d[k][e];
                 sums[1] += dn;
@@ -273,10 +291,8 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwdArgs a) {
         const float m1 = sums[1] * inv, m2 = sums[2] * inv * rstd;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
-            const int64_t c = (int64_t)(k * NT + id) * E;
-            const int v = left(a.C, c);
             float w[E], out[E];
-            if (a.w) param_load<E>(w, a.w + c, v);
+            if (a.w) param_load<E>(w, a.w + at[k], v[k]);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 const float n = h[k][e] * rstd;
@@ -286,14 +302,13 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwdArgs a) {
                 out[e] = rstd * (dn - m1 - n * m2);
                 out[e] += q[k][e];
             }
-            row_store<E, RAG>(a.dx, row * a.C + c, G16, out, v);
+            row_store<E, false>(a.dx, row * a.C + at[k], G16, out, v[k]);
         }
     }
     if (!a.part) return;
     float* part = a.part + (int64_t)blockIdx.x * 2 * a.C;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-        const int64_t c = (int64_t)(k * NT + id) * E;
         if constexpr (!WG) {
             // the four waves hold the same channels: join them, group by group
             if (k > 0) __syncthreads();
@@ -317,9 +332,8 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwdArgs a) {
                 }
             }
         }
-        const int v = left(a.C, c);
-        row_store<E, RAG>(part, c, false, dw[k], v);
-        row_store<E, RAG>(part, a.C + c, false, db[k], v);
+        row_store<E, false>(part, at[k], false, dw[k], v[k]);
+        row_store<E, false>(part, a.C + at[k], false, db[k], v[k]);
     }
 }
 
@@ -449,9 +463,13 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 constexpr int64_t WG_MAX = 8192;
 
+// Whether a row is held in registers: not beyond WG_MAX channels, nor under one
+// group of them.
+bool fits(int64_t C) { return C >= E && C <= WG_MAX; }
+
 // Workgroups of the backward (= partial rows).
 int64_t bwd_rows(int64_t R, int64_t C) {
-    if (C > WG_MAX) {
+    if (!fits(C)) {
         const int64_t cap = cdiv(2048, cdiv(C, 64 * E));
         const int64_t n = cdiv(R, 16);
         return n < cap ? n : cap;
@@ -481,13 +499,13 @@ template <bool BF16, int RES>
 void fwd_t(const NormArgs& a) {
     const int64_t C = a.C;
     const dim3 wave((unsigned)cdiv(a.R, 4)), wg((unsigned)a.R);
-    if (C <= 512) fwd_r<1, false, BF16, RES>(a, wave);
+    if (!fits(C))
+        hipLaunchKernelGGL((norm_fwd_long_kernel<BF16, RES>), wg, dim3(256), 0, a.stream, a);
+    else if (C <= 512) fwd_r<1, false, BF16, RES>(a, wave);
     else if (C <= 1024) fwd_r<2, false, BF16, RES>(a, wave);
     else if (C <= 2048) fwd_r<4, false, BF16, RES>(a, wave);
     else if (C <= 4096) fwd_r<2, true, BF16, RES>(a, wg);
-    else if (C <= WG_MAX) fwd_r<4, true, BF16, RES>(a, wg);
-    else
-        hipLaunchKernelGGL((norm_fwd_long_kernel<BF16, RES>), wg, dim3(256), 0, a.stream, a);
+    else fwd_r<4, true, BF16, RES>(a, wg);
 }
 
 template <bool BF16>
@@ -511,12 +529,13 @@ template <bool BF16, bool DY16, bool G16>
 void bwd_t(const NormBwdArgs& a) {
     const int64_t C = a.C, nrow = bwd_rows(a.R, C);
     const dim3 grid((unsigned)nrow);
-    if (C <= 512) bwd_r<1, false, BF16, DY16, G16>(a, grid);
-    else if (C <= 1024) bwd_r<2, false, BF16, DY16, G16>(a, grid);
-    else if (C <= 2048) bwd_r<1, true, BF16, DY16, G16>(a, grid);
-    else if (C <= 4096) bwd_r<2, true, BF16, DY16, G16>(a, grid);
-    else if (C <= WG_MAX) bwd_r<4, true, BF16, DY16, G16>(a, grid);
-    else {
+    if (fits(C)) {
+        if (C <= 512) bwd_r<1, false, BF16, DY16, G16>(a, grid);
+        else if (C <= 1024) bwd_r<2, false, BF16, DY16, G16>(a, grid);
+        else if (C <= 2048) bwd_r<1, true, BF16, DY16, G16>(a, grid);
+        else if (C <= 4096) bwd_r<2, true, BF16, DY16, G16>(a, grid);
+        else bwd_r<4, true, BF16, DY16, G16>(a, grid);
+    } else {
         const int64_t ncb = cdiv(C, 64 * E);
         float* stats = a.part ? reinterpret_cast<float*>(reinterpret_cast<char*>(a.part) +
                                 up256(sizeof(float) * (size_t)(nrow * 2 * C))) : nullptr;
@@ -541,11 +560,11 @@ void bwd_b(const NormBwdArgs& a) {
 
 }  // namespace
 
-// Workspace: the partials of dw and db [bwd_rows][2 C]; beyond WG_MAX also
-// each row's mean and rstd.
+// Workspace: the partials of dw and db [bwd_rows][2 C], and each row's mean and
+// rstd where the row is not held in registers.
 size_t norm_bwd_workspace_bytes(int64_t R, int64_t C) {
     size_t n = up256(sizeof(float) * (size_t)(bwd_rows(R, C) * 2 * C));
-    if (C > WG_MAX) n += sizeof(float) * (size_t)(2 * R);
+    if (!fits(C)) n += sizeof(float) * (size_t)(2 * R);
     return n;
 }
 

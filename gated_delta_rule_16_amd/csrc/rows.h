@@ -9,9 +9,11 @@
 // with another value: the merge is a copy, and the copy waits for the load.
 // So the type is a template parameter, a group's words are written by its
 // load alone (lanes without a group keep the zeros set before it), and in the
-// RAG variant, for rows whose length is no multiple of E, the elements of the
-// last, partial group have registers of their own, joined at unpacking.  Waves
-// without a partial group (`part` false, the same in all lanes) skip both.
+// RAG variant the elements of a partial group have registers of their own,
+// joined at unpacking.  The variant is for the shortest rows: elsewhere the
+// last group of a row of any length is moved back to end with the row, and
+// the channels that it then shares with the group before it are worked on
+// twice, to the same result.
 #pragma once
 
 #include "gdr_device.h"
@@ -32,9 +34,8 @@ template <int E, bool BF16, bool RAG> struct Row {
     uint32_t p[RAG ? E : 1];    // a partial group's elements
 
     // Channels [0, valid) at element offset `off`; the others become 0.  Without
-    // RAG, or without `part`, valid is 0 or E.
-    __device__ __forceinline__ void load(const void* base, int64_t off, int valid,
-                                         bool part = true) {
+    // RAG valid is 0 or E.
+    __device__ __forceinline__ void load(const void* base, int64_t off, int valid) {
 #pragma unroll
         for (int i = 0; i < W; ++i) w[i] = 0u;
         if (valid >= E) {
@@ -68,7 +69,7 @@ template <int E, bool BF16, bool RAG> struct Row {
                 }
             }
         }
-        if (RAG && part) {
+        if constexpr (RAG) {
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 p[e] = 0u;
@@ -82,7 +83,7 @@ template <int E, bool BF16, bool RAG> struct Row {
         }
     }
 
-    __device__ __forceinline__ void unpack(float (&f)[E], bool part = true) const {
+    __device__ __forceinline__ void unpack(float (&f)[E]) const {
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             if constexpr (BF16)
@@ -90,7 +91,7 @@ template <int E, bool BF16, bool RAG> struct Row {
             else
                 f[e] = __uint_as_float(w[e]);
         }
-        if (RAG && part) {
+        if constexpr (RAG) {
             // one of the two is 0
 #pragma unroll
             for (int e = 0; e < E; ++e)
@@ -98,11 +99,6 @@ template <int E, bool BF16, bool RAG> struct Row {
         }
     }
 };
-
-// Whether some lane of the wave holds a partial group.
-__device__ __forceinline__ bool any_partial(int valid, int e) {
-    return __builtin_amdgcn_ballot_w64(valid > 0 && valid < e) != 0;
-}
 
 // Stores channels [0, valid) of the E (bf16: round to nearest even).  Without
 // RAG valid is 0 or E.

@@ -26,15 +26,25 @@ __device__ __forceinline__ int clampi(int64_t v, int hi) {
     return v < 0 ? 0 : v > hi ? hi : (int)v;
 }
 
+// A lane's group of channels at c: how many it has.  Without RAG the last
+// group of the row is moved back to end with it, and is full too.
+template <int EE, bool RAG>
+__device__ __forceinline__ int own_group(int64_t& c, int64_t C) {
+    if constexpr (RAG) return clampi(C - c, EE);
+    if (c >= C) return 0;
+    if (c > C - EE) c = C - EE;
+    return EE;
+}
+
 // Row t of [state; x] for one lane's channels: t >= 0 from x, else the state
 // (or zeros without one).
 template <int EE, bool BF16, bool RAG>
 __device__ __forceinline__ void load_in(Row<EE, BF16, RAG>& r, const ConvArgs& a, int64_t b,
-                                        int64_t t, int64_t c, int valid, bool part) {
+                                        int64_t t, int64_t c, int valid) {
     const bool past = t < 0;
     r.load(past ? a.s0 : a.x,
            past ? (b * (a.K - 1) + t + a.K - 1) * a.C + c : b * a.xb + t * a.xt + c,
-           past && !a.s0 ? 0 : valid, part);
+           past && !a.s0 ? 0 : valid);
 }
 
 template <int K, bool BF16, bool RAG>
@@ -45,9 +55,8 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int64_t ncb, 
     const int64_t cb = id % ncb;
     id /= ncb;
     const int64_t st = (id % nstretch) * 4 + wv, b = id / nstretch;
-    const int64_t c = (cb * 64 + lane) * E;
-    const int valid = clampi(a.C - c, E);
-    const bool part = any_partial(valid, E);
+    int64_t c = (cb * 64 + lane) * E;
+    const int valid = own_group<E, RAG>(c, a.C);
     const int64_t t0 = st * TL;
     if (valid == 0 || t0 >= a.T) return;
     const int64_t t1 = t0 + TL < a.T ? t0 + TL : a.T;
@@ -58,20 +67,20 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int64_t ncb, 
     {
         Row<E, BF16, RAG> r[K - 1];
 #pragma unroll
-        for (int j = 0; j < K - 1; ++j) load_in(r[j], a, b, t0 - (K - 1) + j, c, valid, part);
+        for (int j = 0; j < K - 1; ++j) load_in(r[j], a, b, t0 - (K - 1) + j, c, valid);
 #pragma unroll
-        for (int j = 0; j < K - 1; ++j) r[j].unpack(win[j], part);
+        for (int j = 0; j < K - 1; ++j) r[j].unpack(win[j]);
         if (t0 == 0 && a.s_final) {
             // the lane that reads the state also writes the next one, so the
             // two may be the same buffer: all K - 1 rows are read (the state
             // rows above, or x) before the first is written
             Row<E, BF16, RAG> f[K - 1];
 #pragma unroll
-            for (int m = 0; m < K - 1; ++m) load_in(f[m], a, b, a.T - (K - 1) + m, c, valid, part);
+            for (int m = 0; m < K - 1; ++m) load_in(f[m], a, b, a.T - (K - 1) + m, c, valid);
 #pragma unroll
             for (int m = 0; m < K - 1; ++m) {
                 float v[E];
-                f[m].unpack(v, part);
+                f[m].unpack(v);
                 row_store<E, RAG>(a.s_final, (b * (K - 1) + m) * a.C + c, BF16, v, valid);
             }
         }
@@ -80,11 +89,11 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int64_t ncb, 
         Row<E, BF16, RAG> r[FWD_TOKENS];
 #pragma unroll
         for (int u = 0; u < FWD_TOKENS; ++u)
-            r[u].load(a.x, b * a.xb + (t + u < t1 ? t + u : t1 - 1) * a.xt + c, valid, part);
+            r[u].load(a.x, b * a.xb + (t + u < t1 ? t + u : t1 - 1) * a.xt + c, valid);
 #pragma unroll
         for (int u = 0; u < FWD_TOKENS; ++u) {
             float x[E], y[E];
-            r[u].unpack(x, part);
+            r[u].unpack(x);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 float s = bias[e];
@@ -145,9 +154,8 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int64_t ncb, 
     __shared__ float red[3][64][BE * (K + 1) + 1];
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t cb = blockIdx.x % ncb, row = blockIdx.x / ncb;
-    const int64_t c = (cb * 64 + lane) * BE;
-    const int valid = clampi(a.C - c, BE);
-    const bool part = any_partial(valid, BE);
+    int64_t c = (cb * 64 + lane) * BE;
+    const int valid = own_group<BE, RAG>(c, a.C);
     float w[BE * K], bias[BE], dw[BE][K], db[BE];
     param_load<BE * K>(w, a.w + c * K, valid * K);
     param_load<BE>(bias, a.bias + c, a.bias ? valid : 0);
@@ -168,8 +176,8 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int64_t ncb, 
 #pragma unroll
             for (int j = 0; j < K - 1; ++j) {
                 Row<BE, BF16, RAG> r;
-                load_in(r, a, b, t0 - (K - 1) + j, c, valid, part);
-                r.unpack(win[j + 1], part);
+                load_in(r, a, b, t0 - (K - 1) + j, c, valid);
+                r.unpack(win[j + 1]);
             }
 #pragma unroll
             for (int j = 0; j < K; ++j)
@@ -184,15 +192,15 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int64_t ncb, 
                 for (int u = 0; u < U; ++u) {
                     const int64_t t = tb + u;
                     const int v = t < a.T && t < tend ? valid : 0;
-                    rx[u].load(a.x, b * a.xb + t * a.xt + c, v, part);
-                    rd[u].load(a.dy, b * a.yb + t * a.yt + c, v, part);
+                    rx[u].load(a.x, b * a.xb + t * a.xt + c, v);
+                    rd[u].load(a.dy, b * a.yb + t * a.yt + c, v);
                 }
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const int64_t t = tb + u;
                     float x[BE], d[BE];
-                    rx[u].unpack(x, part);
-                    rd[u].unpack(d, part);
+                    rx[u].unpack(x);
+                    rd[u].unpack(d);
                     const bool mine = t < t1;     // du_t counts for dw here
                     float out[BE];
 #pragma unroll
@@ -293,7 +301,9 @@ void bwd_shape(int64_t B, int64_t T, int64_t C, int64_t& ncb, int64_t& nstretch,
 
 template <int K>
 void fwd_t(const ConvArgs& a, dim3 grid, int64_t ncb, int64_t nst, int TL) {
-    const bool rag = a.C % E != 0;
+    // a moved group reads channels that another lane also writes back: not where
+    // the state's buffer is the next one's
+    const bool rag = a.C < E || (a.C % E != 0 && a.s_final && a.s_final == a.s0);
 #define FWD(BF16, RAG)                                                                           \
     hipLaunchKernelGGL((conv_fwd_kernel<K, BF16, RAG>), grid, dim3(256), 0, a.stream, a, ncb, nst, \
                        TL)
@@ -317,7 +327,7 @@ void step_t(const ConvArgs& a, dim3 grid, int64_t ncg) {
 
 template <int K, bool BF16, bool DY16>
 void bwd_t(const ConvArgs& a, dim3 grid, int64_t ncb, int64_t nrow, int64_t nstretch, int TL) {
-    if (a.C % BE != 0)
+    if (a.C < BE)
         hipLaunchKernelGGL((conv_bwd_kernel<K, BF16, DY16, true>), grid, dim3(256), 0, a.stream, a,
                            ncb, nrow, nstretch, TL);
     else

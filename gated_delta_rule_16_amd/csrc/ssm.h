@@ -227,6 +227,48 @@ __device__ __forceinline__ void states_store(float* p, const float (&h)[NS], int
     }
 }
 
+constexpr int WC = 64;   // channels per workgroup
+
+// The first channel, in its group of Dg, of a workgroup's WC.  Where Dg is no
+// multiple of 8 the last block is moved back to end with the group, so that the
+// rows of all blocks are loaded and stored whole; what it then shares with the
+// block before it comes out the same from both.  RAG, for groups of fewer than
+// WC channels, loads element by element instead.
+template <bool RAG> __device__ __forceinline__ int64_t first_channel(int64_t blk, int64_t Dg) {
+    return !RAG && Dg % 8 != 0 && blk * WC > Dg - WC ? Dg - WC : blk * WC;
+}
+
+// Groups of 4 of B and C: 64 channels and the states of a token are staged by
+// threads that each hold 4 states.  Where N is no multiple of 4 the last group
+// starts at N - 4; with NG = 1 (N <= 4) it is loaded element by element.
+template <int NG> __device__ __forceinline__ int quad_start(int64_t N, int qn) {
+    return NG == 1 || 4 * qn + 4 <= N ? 4 * qn : (int)N - 4;
+}
+template <int NG> __device__ __forceinline__ int quad_valid(int64_t N, int qn) {
+    return NG == 1 ? (int)N : 4 * qn < N ? 4 : 0;
+}
+// Group q = token * NP / 4 + qn of a tile [token][NP] in LDS.
+template <int NP, int NG>
+__device__ __forceinline__ void quad_write(float* tile, int q, int64_t N, const float (&f)[4]) {
+    if (NG == 1 || N % 4 == 0) {
+        *reinterpret_cast<float4*>(&tile[4 * q]) = float4{f[0], f[1], f[2], f[3]};
+    } else {
+        const int qn = q % (NP / 4);
+        float* p = tile + q / (NP / 4) * NP + quad_start<NG>(N, qn);
+        if (4 * qn < N) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p[e] = f[e];
+        }
+    }
+}
+// The states n >= N of ROWS rows of NP, which quad_write leaves alone where N
+// is no multiple of 4.
+template <int NP, int ROWS>
+__device__ __forceinline__ void quad_clear(float* rows, int64_t N, int tid) {
+    for (int i = tid; i < ROWS * NP; i += 256)
+        if (i % NP >= N) rows[i] = 0.f;
+}
+
 // The step Delta of a token and channel, and of E channels (one branch for
 // all, so their chains interleave).
 __device__ __forceinline__ float ssm_delta(float raw, bool sp) { return sp ? softplus(raw) : raw; }

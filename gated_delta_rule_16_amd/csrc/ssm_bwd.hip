@@ -41,7 +41,7 @@ template <int NS, int NG> constexpr int block_tokens() { return NG < 4 ? 8 : 64 
 template <int NS, int NG, bool GAM, bool BF16, bool RAG>
 __global__ __launch_bounds__(64 * (NG + 4)) void ssm_bwd_states_kernel(SsmBwdArgs a, int64_t nblk,
                                                              int64_t nseg, int64_t L) {
-    constexpr int NP = NS * NG, CW = 64 / NG, WC = NG * CW;
+    constexpr int NP = NS * NG, CW = WC / NG;
     constexpr int EPT = 8;
     constexpr int TT = 256 * EPT / WC;
     constexpr int TPR = WC / EPT;
@@ -62,7 +62,8 @@ __global__ __launch_bounds__(64 * (NG + 4)) void ssm_bwd_states_kernel(SsmBwdArg
     const int64_t g = id % a.G;
     id /= a.G;
     const int64_t seg = id % nseg, b = id / nseg;
-    const int64_t Dg = a.D / a.G, c0 = blk * WC, cg = g * Dg;
+    const int64_t Dg = a.D / a.G, cg = g * Dg;
+    const int64_t c0 = first_channel<RAG>(blk, Dg);
     const int64_t t0 = seg * L, t1 = t0 + L < a.T ? t0 + L : a.T;
     const int64_t tiles = (t1 - t0 + TT - 1) / TT;
     const int64_t nsub = (a.T + S - 1) / S;
@@ -81,7 +82,7 @@ __global__ __launch_bounds__(64 * (NG + 4)) void ssm_bwd_states_kernel(SsmBwdArg
             h[j] = gam[j] = 0.f;
             P[j] = 1.f;
         }
-        if (a.h0 && seg == 0) states_load<NS, RAG>(h, a.h0 + (b * a.D + ch) * a.N + n0, nv);
+        if (a.h0 && seg == 0) states_load<NS>(h, a.h0 + (b * a.D + ch) * a.N + n0, nv);
         float sumd = 0.f;
         __syncthreads();
         for (int64_t i = 0; i < tiles; ++i) {
@@ -91,7 +92,7 @@ __global__ __launch_bounds__(64 * (NG + 4)) void ssm_bwd_states_kernel(SsmBwdArg
             for (int tt = 0; tt < nt; tt += 4) {
                 if (((tb + tt) & (S - 1)) == 0) {
                     const int64_t o = (b * nsub + (tb + tt) / S) * a.D + ch;
-                    states_store<NS, RAG>(a.ckpt + o * a.N + n0, h, nv);
+                    states_store<NS>(a.ckpt + o * NP + n0, h, live ? NS : 0);
                     if (GAM && live && n0 == 0) a.csum[o] = sumd;
                 }
                 float Bq[4 / KT], Cq[4 / KT], dy[4] = {0.f, 0.f, 0.f, 0.f};
@@ -139,8 +140,8 @@ __global__ __launch_bounds__(64 * (NG + 4)) void ssm_bwd_states_kernel(SsmBwdArg
         }
         if constexpr (GAM) {
             const int64_t o = (b * nseg + seg) * a.D + ch;
-            states_store<NS, RAG>(a.hend + o * a.N + n0, h, nv);
-            states_store<NS, RAG>(a.gstart + o * a.N + n0, gam, nv);
+            states_store<NS>(a.hend + o * NP + n0, h, live ? NS : 0);
+            states_store<NS>(a.gstart + o * NP + n0, gam, live ? NS : 0);
             if (live && n0 == 0) a.sdelta[o] = sumd;
         }
         return;
@@ -163,29 +164,28 @@ __global__ __launch_bounds__(64 * (NG + 4)) void ssm_bwd_states_kernel(SsmBwdArg
         const int q = tid + 256 * i, qt = (q % NQ) / (NP / 4), qn = q % (NP / 4);
         pq[i] = q >= NQ ? static_cast<const T*>(a.Cm) + b * a.cb + (t0 + qt) * a.ct
                         : static_cast<const T*>(a.Bm) + b * a.bb + (t0 + qt) * a.bt;
-        pq[i] += g * a.N + 4 * qn;
+        pq[i] += g * a.N + quad_start<NG>(a.N, qn);
     }
-    const bool part = any_partial(sv, EPT);
     // two tiles' loads are in flight, each in its own registers
     struct Rows {
         Row<EPT, BF16, RAG> x, t, z;
         Row<EPT, true, RAG> o16;
         Row<EPT, false, RAG> o32;
-        Row<4, BF16, RAG> q[QPT];
+        Row<4, BF16, NG == 1> q[QPT];
     } rows0, rows1;
     auto fetch = [&](int64_t i, Rows& r) {
         const int64_t tb = t0 + i * TT;
         if (tb >= t1) return;
         const int left = t1 - tb < TT ? (int)(t1 - tb) : TT;
         const int v = srow < left ? sv : 0;
-        r.x.load(px, 0, v, part);
-        r.t.load(pt, 0, v, part);
+        r.x.load(px, 0, v);
+        r.t.load(pt, 0, v);
         px += TT * a.xt;
         pt += TT * a.dtt;
         if constexpr (GAM) {
-            r.o16.load(a.dout, po, a.dout_bf16 ? v : 0, part);
-            r.o32.load(a.dout, po, a.dout_bf16 ? 0 : v, part);
-            r.z.load(pz, 0, a.z ? v : 0, part);
+            r.o16.load(a.dout, po, a.dout_bf16 ? v : 0);
+            r.o32.load(a.dout, po, a.dout_bf16 ? 0 : v);
+            r.z.load(pz, 0, a.z ? v : 0);
             po += TT * a.ot;
             pz += TT * a.zt;
         }
@@ -195,7 +195,7 @@ __global__ __launch_bounds__(64 * (NG + 4)) void ssm_bwd_states_kernel(SsmBwdArg
             const bool isc = q >= NQ;
             if (isc && !GAM) continue;
             const int qt = (q % NQ) / (NP / 4), qn = q % (NP / 4);
-            const int vq = q < 2 * NQ && qt < left ? states_valid<4>(a.N, 4 * qn) : 0;
+            const int vq = q < 2 * NQ && qt < left ? quad_valid<NG>(a.N, qn) : 0;
             r.q[j].load(pq[j], 0, vq);
             pq[j] += TT * (isc ? a.ct : a.bt);
         }
@@ -204,8 +204,8 @@ __global__ __launch_bounds__(64 * (NG + 4)) void ssm_bwd_states_kernel(SsmBwdArg
         const int buf = (int)(i & 1);
         const int tv = t0 + i * TT + srow < t1 ? sv : 0;
         float x[EPT], r[EPT], d[EPT];
-        rows.x.unpack(x, part);
-        rows.t.unpack(r, part);
+        rows.x.unpack(x);
+        rows.t.unpack(r);
 #pragma unroll
         for (int e = 0; e < EPT; ++e) r[e] += bias[e];
         ssm_deltas(d, r, a.softplus);
@@ -217,10 +217,10 @@ __global__ __launch_bounds__(64 * (NG + 4)) void ssm_bwd_states_kernel(SsmBwdArg
         if constexpr (GAM) {
             float o[EPT], z[EPT];
             if (a.dout_bf16)
-                rows.o16.unpack(o, part);
+                rows.o16.unpack(o);
             else
-                rows.o32.unpack(o, part);
-            rows.z.unpack(z, part);
+                rows.o32.unpack(o);
+            rows.z.unpack(z);
             if (a.z) ssm_gate(o, z);
 #pragma unroll
             for (int e = 0; e < EPT; ++e) ds[buf][srow][sc + e] = o[e];
@@ -231,10 +231,10 @@ __global__ __launch_bounds__(64 * (NG + 4)) void ssm_bwd_states_kernel(SsmBwdArg
             if (q >= 2 * NQ || (q >= NQ && !GAM)) continue;
             float f[4];
             rows.q[q4].unpack(f);
-            *reinterpret_cast<float4*>(&bc[buf][q >= NQ][4 * (q % NQ)]) =
-                float4{f[0], f[1], f[2], f[3]};
+            quad_write<NP, NG>(bc[buf][q >= NQ], q % NQ, a.N, f);
         }
     };
+    quad_clear<NP, 4 * TT>(&bc[0][0][0], a.N, tid);
     fetch(0, rows0);
     fetch(1, rows1);
     stage(0, rows0);
@@ -260,12 +260,13 @@ __device__ __forceinline__ void back_token(float (&gr)[NS], float (&dA)[NS], flo
                                            float& sB, float& sA, const float (&aa)[NS],
                                            const float (&hh)[NS], const float (&hp)[NS],
                                            const float (&A2)[NS], float d, float dx, float dy,
-                                           float Bq, float Cq) {
+                                           float Bq, float Cq, bool own) {
     row_fma<NS, I>(gr, Cq, dy);
+    const float ody = own ? dy : 0.f, odx = own ? dx : 0.f;
 #pragma unroll
     for (int j = 0; j < NS; ++j) {
-        pv[j] = hh[j] * dy;
-        pv[NS + j] = gr[j] * dx;
+        pv[j] = hh[j] * ody;
+        pv[NS + j] = gr[j] * odx;
     }
     sB = row_dot<NS, I>(Bq, gr);
     sA = 0.f;
@@ -351,7 +352,7 @@ __device__ __forceinline__ void channel_sums(float (*p)[2 * NS * NG], const floa
 template <int NS, int NG, bool BF16, bool RAG>
 __global__ __launch_bounds__(64 * (NG + 4), NS == 16 ? 1 : 2) void ssm_bwd_kernel(SsmBwdArgs a, int64_t nblk,
                                                                        int64_t nseg, int64_t L) {
-    constexpr int NP = NS * NG, CW = 64 / NG, WC = NG * CW;
+    constexpr int NP = NS * NG, CW = WC / NG;
     constexpr int S = block_tokens<NS, NG>();
     constexpr int EPT = S * WC / 256;
     constexpr int TPR = WC / EPT;
@@ -374,7 +375,8 @@ __global__ __launch_bounds__(64 * (NG + 4), NS == 16 ? 1 : 2) void ssm_bwd_kerne
     const int64_t g = id % a.G;
     id /= a.G;
     const int64_t seg = id % nseg, b = id / nseg;
-    const int64_t Dg = a.D / a.G, c0 = blk * WC, cg = g * Dg;
+    const int64_t Dg = a.D / a.G, cg = g * Dg;
+    const int64_t c0 = first_channel<RAG>(blk, Dg);
     const int64_t t0 = seg * L, t1 = t0 + L < a.T ? t0 + L : a.T;
     const int64_t nsub = (a.T + S - 1) / S;
     const int64_t first = t0 / S, last = (t1 + S - 1) / S - 1;
@@ -384,6 +386,8 @@ __global__ __launch_bounds__(64 * (NG + 4), NS == 16 ? 1 : 2) void ssm_bwd_kerne
         const int row = lane >> 4, n0 = NS * (row % NG);
         const int chl = wv * CW + (lane & 15) + 16 * (row / NG);
         const bool live = c0 + chl < Dg;
+        // a channel that the block shares with the one before counts there
+        const bool own = c0 + chl >= blk * WC;
         const int64_t ch = cg + (live ? c0 + chl : 0);
         const int nv = live ? states_valid<NS>(a.N, n0) : 0;
         float A2[NS], hin[NS], gr[NS], dA[NS];
@@ -398,7 +402,7 @@ __global__ __launch_bounds__(64 * (NG + 4), NS == 16 ? 1 : 2) void ssm_bwd_kerne
         for (int64_t s = 0; s < seg; ++s) {
             const int64_t o = (b * nseg + s) * a.D + ch;
             float e[NS];
-            states_load<NS, RAG>(e, a.hend + o * a.N + n0, nv);
+            states_load<NS, false>(e, a.hend + o * NP + n0, live);
             const float sd = live ? a.sdelta[o] : 0.f;
 #pragma unroll
             for (int j = 0; j < NS; ++j)
@@ -406,11 +410,11 @@ __global__ __launch_bounds__(64 * (NG + 4), NS == 16 ? 1 : 2) void ssm_bwd_kerne
                                 : __builtin_fmaf(__builtin_amdgcn_exp2f(A2[j] * sd), hin[j], e[j]);
         }
         // gr = a_{t+1} g_{t+1} past the segment's last token
-        if (a.dh_final) states_load<NS, RAG>(gr, a.dh_final + so, nv);
+        if (a.dh_final) states_load<NS>(gr, a.dh_final + so, nv);
         for (int64_t s = nseg - 1; s > seg; --s) {
             const int64_t o = (b * nseg + s) * a.D + ch;
             float e[NS];
-            states_load<NS, RAG>(e, a.gstart + o * a.N + n0, nv);
+            states_load<NS, false>(e, a.gstart + o * NP + n0, live);
             const float sd = live ? a.sdelta[o] : 0.f;
 #pragma unroll
             for (int j = 0; j < NS; ++j)
@@ -419,7 +423,7 @@ __global__ __launch_bounds__(64 * (NG + 4), NS == 16 ? 1 : 2) void ssm_bwd_kerne
         float kept[NS], ksum = 0.f;
         auto fetch = [&](int64_t sub) {
             const int64_t ko = (b * nsub + sub) * a.D + ch;
-            states_load<NS, RAG>(kept, a.ckpt + ko * a.N + n0, nv);
+            states_load<NS, false>(kept, a.ckpt + ko * NP + n0, live);
             if (seg > 0) ksum = live ? a.csum[ko] : 0.f;
         };
         fetch(last);
@@ -495,7 +499,7 @@ __global__ __launch_bounds__(64 * (NG + 4), NS == 16 ? 1 : 2) void ssm_bwd_kerne
 #define TOKEN(k)                                                                               \
     back_token<NS, NS*(k % KT)>(gr, dA, pv[k], sB[k], sA[k], aa[tt + k], hh[tt + k],           \
                                 tt + k == 0 ? hs : hh[tt + k == 0 ? 0 : tt + k - 1], A2,       \
-                                o.d[k], o.dx[k], o.dy[k], o.Bq[k / KT], o.Cq[k / KT])
+                                o.d[k], o.dx[k], o.dy[k], o.Bq[k / KT], o.Cq[k / KT], own)
                 TOKEN(3);
                 TOKEN(2);
                 channel_sums<NS, NG>(&pbc[buf][wv][tt + 2], pv[2], pv[3], lane, n0);
@@ -510,8 +514,8 @@ __global__ __launch_bounds__(64 * (NG + 4), NS == 16 ? 1 : 2) void ssm_bwd_kerne
             }
             __syncthreads();
         }
-        if (seg == 0 && a.dh0) states_store<NS, RAG>(a.dh0 + so, gr, nv);
-        states_store<NS, RAG>(part + ch * a.N + n0, dA, nv);
+        if (seg == 0 && a.dh0) states_store<NS>(a.dh0 + so, gr, nv);
+        states_store<NS>(part + ch * a.N + n0, dA, nv);
         __syncthreads();
         return;
     }
@@ -537,25 +541,24 @@ __global__ __launch_bounds__(64 * (NG + 4), NS == 16 ? 1 : 2) void ssm_bwd_kerne
         const int q = tid + 256 * i, qt = (q % NQ) / (NP / 4), qn = q % (NP / 4);
         pq[i] = q >= NQ ? static_cast<const T*>(a.Cm) + b * a.cb + (last * S + qt) * a.ct
                         : static_cast<const T*>(a.Bm) + b * a.bb + (last * S + qt) * a.bt;
-        pq[i] += g * a.N + 4 * qn;
+        pq[i] += g * a.N + quad_start<NG>(a.N, qn);
     }
-    const bool split = any_partial(sv, EPT);
     // two blocks' loads are in flight, each in its own registers
     struct Rows {
         Row<EPT, BF16, RAG> x, t, z;
         Row<EPT, true, RAG> o16;
         Row<EPT, false, RAG> o32;
-        Row<4, BF16, RAG> q[QPT];
+        Row<4, BF16, NG == 1> q[QPT];
     } rows0, rows1;
     auto fetch = [&](int64_t sub, Rows& r) {
         if (sub < first) return;
         const int left = t1 - sub * S < S ? (int)(t1 - sub * S) : S;
         const int v = srow < left ? sv : 0;
-        r.x.load(px, 0, v, split);
-        r.t.load(pt, 0, v, split);
-        r.o16.load(a.dout, po, a.dout_bf16 ? v : 0, split);
-        r.o32.load(a.dout, po, a.dout_bf16 ? 0 : v, split);
-        r.z.load(pz, 0, a.z ? v : 0, split);
+        r.x.load(px, 0, v);
+        r.t.load(pt, 0, v);
+        r.o16.load(a.dout, po, a.dout_bf16 ? v : 0);
+        r.o32.load(a.dout, po, a.dout_bf16 ? 0 : v);
+        r.z.load(pz, 0, a.z ? v : 0);
         px -= S * a.xt;
         pt -= S * a.dtt;
         po -= S * a.ot;
@@ -565,7 +568,7 @@ __global__ __launch_bounds__(64 * (NG + 4), NS == 16 ? 1 : 2) void ssm_bwd_kerne
             const int q = tid + 256 * j;
             const bool isc = q >= NQ;
             const int qt = (q % NQ) / (NP / 4), qn = q % (NP / 4);
-            const int vq = q < 2 * NQ && qt < left ? states_valid<4>(a.N, 4 * qn) : 0;
+            const int vq = q < 2 * NQ && qt < left ? quad_valid<NG>(a.N, qn) : 0;
             r.q[j].load(pq[j], 0, vq);
             pq[j] -= S * (isc ? a.ct : a.bt);
         }
@@ -579,13 +582,13 @@ __global__ __launch_bounds__(64 * (NG + 4), NS == 16 ? 1 : 2) void ssm_bwd_kerne
         const int buf = (int)(sub & 1);
         const int v = sub * S + srow < t1 ? sv : 0;
         float r[EPT], z[EPT];
-        rows.x.unpack(k.x, split);
-        rows.t.unpack(r, split);
+        rows.x.unpack(k.x);
+        rows.t.unpack(r);
         if (a.dout_bf16)
-            rows.o16.unpack(k.dy, split);
+            rows.o16.unpack(k.dy);
         else
-            rows.o32.unpack(k.dy, split);
-        rows.z.unpack(z, split);
+            rows.o32.unpack(k.dy);
+        rows.z.unpack(z);
 #pragma unroll
         for (int e = 0; e < EPT; ++e) {
             r[e] += bias[e];
@@ -619,8 +622,7 @@ __global__ __launch_bounds__(64 * (NG + 4), NS == 16 ? 1 : 2) void ssm_bwd_kerne
             if (q >= 2 * NQ) continue;
             float f[4];
             rows.q[i].unpack(f);
-            *reinterpret_cast<float4*>(&bc[buf][q >= NQ][4 * (q % NQ)]) =
-                float4{f[0], f[1], f[2], f[3]};
+            quad_write<NP, NG>(bc[buf][q >= NQ], q % NQ, a.N, f);
         }
     };
     int64_t oo = (b * a.T + last * S + srow) * a.D + scg;
@@ -661,6 +663,7 @@ __global__ __launch_bounds__(64 * (NG + 4), NS == 16 ? 1 : 2) void ssm_bwd_kerne
         pbo -= S * bct;
     };
     Held even, odd;
+    quad_clear<NP, 4 * S>(&bc[0][0][0], a.N, tid);
     fetch(last, rows0);
     fetch(last - 1, rows1);
     stage(last, rows0, even);
@@ -740,12 +743,6 @@ __global__ __launch_bounds__(256) void ssm_bwd_reduce(SsmBwdArgs a, int64_t nblk
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-int64_t padded_states(int64_t N) {
-    int64_t n = 4;
-    while (n < N) n *= 2;
-    return n;
-}
-
 // Segments of the backward: of at least 64 tokens, up to two workgroups per
 // compute unit (B 4 T 4096 D 2048 N 16: 587 us with 512 workgroups, 630
 // with 256, 780 with 384).
@@ -778,13 +775,14 @@ BwdLayout bwd_layout(const SsmPlan& p, int64_t B, int64_t T, int64_t D, int64_t 
     };
     const int64_t nsub = cdiv(T, kept_tokens(N));
     const bool many = p.nseg > 1;
-    l.ckpt = take(B * nsub * D * N);
+    const int64_t NP = ssm_padded_states(N);
+    l.ckpt = take(B * nsub * D * NP);
     l.csum = take(many ? B * nsub * D : 0);
-    l.hend = take(many ? B * p.nseg * D * N : 0);
-    l.gstart = take(many ? B * p.nseg * D * N : 0);
+    l.hend = take(many ? B * p.nseg * D * NP : 0);
+    l.gstart = take(many ? B * p.nseg * D * NP : 0);
     l.sdelta = take(many ? B * p.nseg * D : 0);
     l.part = take(B * p.nseg * D * (N + 2));
-    l.bcpart = take(p.nblk * B * T * G * 2 * padded_states(N));
+    l.bcpart = take(p.nblk * B * T * G * 2 * NP);
     l.total = at;
     return l;
 }
@@ -807,7 +805,8 @@ hipError_t launch_bwd_r(const SsmBwdArgs& a, const SsmPlan& p) {
 
 template <int NS, int NG>
 hipError_t launch_bwd_t(const SsmBwdArgs& a, const SsmPlan& p) {
-    const bool rag = (a.D / a.G) % 8 != 0 || a.N % NS != 0;
+    const int64_t Dg = a.D / a.G;
+    const bool rag = Dg % 8 != 0 && Dg < WC;
     hipError_t e;
     if (a.in_bf16)
         e = rag ? launch_bwd_r<NS, NG, true, true>(a, p) : launch_bwd_r<NS, NG, true, false>(a, p);
@@ -830,7 +829,7 @@ size_t ssm_bwd_workspace_bytes(int64_t B, int64_t T, int64_t D, int64_t G, int64
 int64_t ssm_bwd_workgroups(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N) {
     const SsmPlan p = bwd_plan(B, T, D, G, N);
     const int64_t n = 2 * B * G * p.nblk * p.nseg;    // of 512 threads
-    const int64_t r = cdiv(B * T * G * 2 * padded_states(N), 256) + cdiv(D * (N + 2), 64);
+    const int64_t r = cdiv(B * T * G * 2 * ssm_padded_states(N), 256) + cdiv(D * (N + 2), 64);
     return n > r ? n : r;
 }
 

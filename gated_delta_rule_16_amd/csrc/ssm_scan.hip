@@ -31,7 +31,7 @@ namespace {
 template <int NS, int NG, bool OUT, bool BF16, bool RAG>
 __global__ __launch_bounds__(64 * (NG + 4)) void ssm_fwd_kernel(SsmArgs a, int64_t nblk, int64_t nseg,
                                                       int64_t L) {
-    constexpr int NP = NS * NG, CW = 64 / NG, WC = NG * CW;
+    constexpr int NP = NS * NG, CW = WC / NG;
     constexpr int EPT = 8;                            // staged channels per thread
     constexpr int TT = 256 * EPT / WC;                // tokens per tile
     constexpr int TPR = WC / EPT;                     // threads per token row
@@ -53,7 +53,8 @@ __global__ __launch_bounds__(64 * (NG + 4)) void ssm_fwd_kernel(SsmArgs a, int64
     id /= a.G;
     const int64_t ns = OUT ? nseg : nseg - 1;         // the last segment's end state is not needed
     const int64_t seg = id % ns, b = id / ns;
-    const int64_t Dg = a.D / a.G, c0 = blk * WC, cg = g * Dg;
+    const int64_t Dg = a.D / a.G, cg = g * Dg;
+    const int64_t c0 = first_channel<RAG>(blk, Dg);
     const int64_t t0 = seg * L, t1 = t0 + L < a.T ? t0 + L : a.T;
     const int64_t tiles = (t1 - t0 + TT - 1) / TT;
 
@@ -76,15 +77,15 @@ __global__ __launch_bounds__(64 * (NG + 4)) void ssm_fwd_kernel(SsmArgs a, int64
         // not read h0: another workgroup may be writing h_final, the same
         // buffer), hend[b][s] the end of segment s - 1, segment 0 started from h0
         if (!OUT || nseg == 1) {
-            if (a.h0 && seg == 0) states_load<NS, RAG>(h, a.h0 + so, nv);
+            if (a.h0 && seg == 0) states_load<NS>(h, a.h0 + so, nv);
             if constexpr (!OUT)
-                if (seg == 0) states_store<NS, RAG>(a.hend + (b * nseg * a.D + ch) * a.N + n0, h, nv);
+                if (seg == 0) states_store<NS>(a.hend + (b * nseg * a.D + ch) * NP + n0, h, live ? NS : 0);
         } else {
-            states_load<NS, RAG>(h, a.hend + ((b * nseg + (seg > 0)) * a.D + ch) * a.N + n0, nv);
+            states_load<NS, false>(h, a.hend + ((b * nseg + (seg > 0)) * a.D + ch) * NP + n0, live);
             for (int64_t s = 1; s < seg; ++s) {
                 const int64_t o = (b * nseg + s) * a.D + ch;
                 float e[NS];
-                states_load<NS, RAG>(e, a.hend + (o + a.D) * a.N + n0, nv);
+                states_load<NS, false>(e, a.hend + (o + a.D) * NP + n0, live);
                 const float sd = live ? a.sdelta[o] : 0.f;
 #pragma unroll
                 for (int j = 0; j < NS; ++j)
@@ -138,10 +139,10 @@ __global__ __launch_bounds__(64 * (NG + 4)) void ssm_fwd_kernel(SsmArgs a, int64
             __syncthreads();
         }
         if constexpr (OUT) {
-            if (a.h_final && seg == nseg - 1) states_store<NS, RAG>(a.h_final + so, h, nv);
+            if (a.h_final && seg == nseg - 1) states_store<NS>(a.h_final + so, h, nv);
         } else {
             const int64_t o = (b * nseg + seg) * a.D + ch;
-            states_store<NS, RAG>(a.hend + (o + a.D) * a.N + n0, h, nv);
+            states_store<NS>(a.hend + (o + a.D) * NP + n0, h, live ? NS : 0);
             if (live && n0 == 0) a.sdelta[o] = sumd;
         }
         return;
@@ -165,25 +166,24 @@ __global__ __launch_bounds__(64 * (NG + 4)) void ssm_fwd_kernel(SsmArgs a, int64
         const int q = tid + 256 * i, qt = (q % NQ) / (NP / 4), qn = q % (NP / 4);
         pq[i] = q >= NQ ? static_cast<const T*>(a.Cm) + b * a.cb + (t0 + qt) * a.ct
                         : static_cast<const T*>(a.Bm) + b * a.bb + (t0 + qt) * a.bt;
-        pq[i] += g * a.N + 4 * qn;
+        pq[i] += g * a.N + quad_start<NG>(a.N, qn);
     }
-    const bool part = any_partial(sv, EPT);
     // two tiles' loads are in flight, each in its own registers
     struct Rows {
         Row<EPT, BF16, RAG> x, t, z;
-        Row<4, BF16, RAG> q[QPT];
+        Row<4, BF16, NG == 1> q[QPT];
     } rows0, rows1;
     auto fetch = [&](int64_t i, Rows& r) {
         const int64_t tb = t0 + i * TT;
         if (tb >= t1) return;
         const int left = t1 - tb < TT ? (int)(t1 - tb) : TT;
         const int v = srow < left ? sv : 0;
-        r.x.load(px, 0, v, part);
-        r.t.load(pt, 0, v, part);
+        r.x.load(px, 0, v);
+        r.t.load(pt, 0, v);
         px += TT * a.xt;
         pt += TT * a.dtt;
         if constexpr (OUT) {
-            r.z.load(pz, 0, a.z ? v : 0, part);
+            r.z.load(pz, 0, a.z ? v : 0);
             pz += TT * a.zt;
         }
 #pragma unroll
@@ -192,7 +192,7 @@ __global__ __launch_bounds__(64 * (NG + 4)) void ssm_fwd_kernel(SsmArgs a, int64
             const bool isc = q >= NQ;
             if (isc && !OUT) continue;
             const int qt = (q % NQ) / (NP / 4), qn = q % (NP / 4);
-            const int vq = q < 2 * NQ && qt < left ? states_valid<4>(a.N, 4 * qn) : 0;
+            const int vq = q < 2 * NQ && qt < left ? quad_valid<NG>(a.N, qn) : 0;
             r.q[j].load(pq[j], 0, vq);
             pq[j] += TT * (isc ? a.ct : a.bt);
         }
@@ -207,8 +207,8 @@ __global__ __launch_bounds__(64 * (NG + 4)) void ssm_fwd_kernel(SsmArgs a, int64
         // decay is exp(0) and it adds 0
         const int tv = t0 + i * TT + srow < t1 ? sv : 0;
         float x[EPT], r[EPT], d[EPT];
-        rows.x.unpack(x, part);
-        rows.t.unpack(r, part);
+        rows.x.unpack(x);
+        rows.t.unpack(r);
 #pragma unroll
         for (int e = 0; e < EPT; ++e) r[e] += bias[e];
         ssm_deltas(d, r, a.softplus);
@@ -225,7 +225,7 @@ __global__ __launch_bounds__(64 * (NG + 4)) void ssm_fwd_kernel(SsmArgs a, int64
             }
             if (a.z) {
                 float z[EPT];
-                rows.z.unpack(z, part);
+                rows.z.unpack(z);
                 ssm_gate(k.factor, z);
             }
         }
@@ -235,8 +235,7 @@ __global__ __launch_bounds__(64 * (NG + 4)) void ssm_fwd_kernel(SsmArgs a, int64
             if (q >= 2 * NQ || (q >= NQ && !OUT)) continue;
             float f[4];
             rows.q[q4].unpack(f);
-            *reinterpret_cast<float4*>(&bc[buf][q >= NQ][4 * (q % NQ)]) =
-                float4{f[0], f[1], f[2], f[3]};
+            quad_write<NP, NG>(bc[buf][q >= NQ], q % NQ, a.N, f);
         }
     };
     int64_t oo = (b * a.T + t0 + srow) * a.D + scg;
@@ -250,6 +249,7 @@ __global__ __launch_bounds__(64 * (NG + 4)) void ssm_fwd_kernel(SsmArgs a, int64
         }
         oo += TT * a.D;
     };
+    quad_clear<NP, 4 * TT>(&bc[0][0][0], a.N, tid);
     fetch(0, rows0);
     fetch(1, rows1);
     stage(0, rows0, even);
@@ -342,7 +342,11 @@ hipError_t launch_fwd_r(const SsmArgs& a, const SsmPlan& p) {
 
 template <int NS, int NG>
 hipError_t launch_fwd_t(const SsmArgs& a, const SsmPlan& p) {
-    const bool rag = (a.D / a.G) % 8 != 0 || a.N % NS != 0;
+    const int64_t Dg = a.D / a.G;
+    // a moved block reads states that another one also writes back: not where
+    // h0's buffer is h_final's
+    const bool rag =
+        Dg % 8 != 0 && (Dg < WC || (p.nseg == 1 && a.h_final && a.h_final == a.h0));
     if (a.in_bf16)
         return rag ? launch_fwd_r<NS, NG, true, true>(a, p)
                    : launch_fwd_r<NS, NG, true, false>(a, p);
@@ -371,6 +375,12 @@ static int ssm_lanes(int64_t N) {
     return l;
 }
 
+int64_t ssm_padded_states(int64_t N) {
+    int64_t n = 4;
+    while (n < N) n *= 2;
+    return n;
+}
+
 // Segments of the forward.  One when the channels give 192 workgroups, three
 // quarters of one per compute unit; below that enough, of at least 64
 // tokens, for two per compute unit (B 1 T 32768 D 2048 N 16: 417 us with 512
@@ -390,16 +400,16 @@ SsmPlan ssm_fwd_plan(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N) {
 }
 
 // Workspace of the forward with nseg > 1: the states at segment starts as
-// above [B, nseg, D, N], then the sums of Delta [B, nseg, D].
+// above [B, nseg, D, N padded], then the sums of Delta [B, nseg, D].
 size_t ssm_fwd_workspace_bytes(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N) {
     const SsmPlan p = ssm_fwd_plan(B, T, D, G, N);
-    return p.nseg > 1 ? sizeof(float) * (size_t)(B * p.nseg * D * (N + 1)) : 0;
+    return p.nseg > 1 ? sizeof(float) * (size_t)(B * p.nseg * D * (ssm_padded_states(N) + 1)) : 0;
 }
 
 hipError_t launch_ssm_fwd(SsmArgs a, float* ws) {
     const SsmPlan p = ssm_fwd_plan(a.B, a.T, a.D, a.G, a.N);
     a.hend = ws;
-    a.sdelta = ws ? ws + a.B * p.nseg * a.D * a.N : nullptr;
+    a.sdelta = ws ? ws + a.B * p.nseg * a.D * ssm_padded_states(a.N) : nullptr;
     if (a.N <= 4) return launch_fwd_t<4, 1>(a, p);
     if (a.N <= 8) return launch_fwd_t<4, 2>(a, p);
     if (a.N <= 16) return launch_fwd_t<4, 4>(a, p);

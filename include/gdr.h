@@ -648,7 +648,8 @@ gdr_status_t gdr2_chunk_bwd_ex(int64_t B, int64_t T, int64_t H, int64_t Dk,
  *   - the gradients of activations are written in grad_dt (GDR_F32 or
  *     GDR_BF16), those of parameters and states in fp32.  Every sum runs in a
  *     fixed order: equal calls give equal bits;
- *   - outputs must not overlap inputs or each other unless a call says so;
+ *   - outputs must not overlap inputs or each other unless a call says so (an
+ *     output at an input's address is then refused);
  *   - the device of the tensors must be the current device.
  */
 
@@ -767,8 +768,8 @@ gdr_status_t gdr_ssm_step(int64_t Nseq, int64_t D, int64_t G, int64_t N,
  * {x, dt, Bm, Cm, z, dout}.  Writes dx, ddt [B, T, D], dB, dC [B, T, G, N]
  * and dz [B, T, D] (NULL without z) in grad_dt, and in fp32 dA [D, N], dD and
  * ddt_bias [D] and dh0 [B, D, N] (each of the last three may be NULL).  The
- * states are run again from the inputs; the workspace holds one state in 16
- * tokens and the partial sums.
+ * states are run again from the inputs; the workspace holds one state in 8 or
+ * 16 tokens and the partial sums.
  */
 size_t gdr_ssm_scan_bwd_workspace_size(int64_t B, int64_t T, int64_t D,
                                        int64_t G, int64_t N);

@@ -197,3 +197,25 @@ def test_binding_refuses_cpu_tensors(gdr):
             call()
     with pytest.raises(TypeError):
         gdr.gdr_layer_norm_fwd([1.0])
+
+
+B16 = A16 + 4096       # other fake addresses
+C16 = A16 + 8192
+
+
+@pytest.mark.parametrize("name,kw", [
+    ("conv", dict(x=A16, y=A16)), ("conv", dict(s0=B16, y=B16)), ("conv", dict(y=B16, sf=A16)),
+    ("conv", dict(y=B16, sf=B16, x=C16)), ("conv_step", dict(s=B16)), ("conv_step", dict(y=B16)),
+    ("conv_bwd", dict(dy=B16)), ("conv_bwd", dict(dy=B16, dx=B16)),
+    ("conv_bwd", dict(dy=B16, dx=C16, dsf=B16 + 64, ds0=B16 + 64)),
+    ("scan", dict()), ("scan", dict(z=B16, y=B16)), ("scan", dict(h0=B16, y=B16)),
+    ("step", dict(s=B16)), ("step", dict(s=B16, y=B16)),
+    ("scan_bwd", dict(dx=B16, dd=B16 + 64, dB=B16 + 128)), ("scan_bwd", dict(do=B16, dx=B16)),
+    ("norm", dict(r=B16, h=A16, y=C16, rs=16)), ("norm", dict(r=B16, h=C16, y=C16, rs=16)),
+    ("norm", dict(r=B16, h=C16, y=B16, rs=16)), ("norm", dict(xs=32)), ("norm", dict(odt=F32)),
+    ("norm", dict(y=C16, r=B16, h=B16, rs=32)), ("norm_bwd", dict(dy=B16)),
+    ("norm_bwd", dict(dy=B16, dx=B16)), ("norm_bwd", dict(dy=B16, dx=C16, dr=C16, rs=32)),
+])
+def test_outputs_at_inputs(gdr, name, kw):
+    """What cannot be done in place is refused, not done wrongly."""
+    assert globals()[name](gdr, **kw) == 1
