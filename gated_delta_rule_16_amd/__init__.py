@@ -768,7 +768,8 @@ def _whole(name, t, dtype, shape, device):
         raise ValueError(f"{name} must be contiguous")
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream     # a stream handle with no Stream object around it
+# a stream handle with no Stream object around it
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _on_own_device(fn):
@@ -828,9 +829,9 @@ def _scratch(workspace, need, device):
 
 
 def _new(like, dtype, shape, device):
-    """A new tensor; of the type and shape of ``like`` where it has them already."""
-    if like is not None and like.dtype is dtype and like.shape == shape and like.is_contiguous():
-        return torch.empty_like(like)
+    """A new tensor; from ``like`` where that has its shape (half the host time)."""
+    if like is not None and like.shape == shape and like.is_contiguous():
+        return torch.empty_like(like, dtype=dtype)
     return torch.empty(shape, dtype=dtype, device=device)
 
 
@@ -1011,7 +1012,8 @@ def gdr_ssm_scan_fwd(x, dt, A, Bm, Cm, D=None, z=None, dt_bias=None, h0=None, *,
     _run("gdr_ssm_scan_fwd", lib.gdr_ssm_scan_fwd(
         B, T, Dn, G, N, _DT[x.dtype], _p(x), _p(dt), _p(A), _p(Bm), _p(Cm), _p(D), _p(z),
         _p(dt_bias), _p(h0), _i64s(*st), GDR_SSM_SOFTPLUS if softplus else 0, code, _p(y),
-        _p(h_final), _p(workspace), 0 if workspace is None else workspace.numel(), _raw_stream(dev.index)))
+        _p(h_final), _p(workspace), 0 if workspace is None else workspace.numel(),
+        _raw_stream(dev.index)))
     return y, h_final
 
 

@@ -242,10 +242,10 @@ hipError_t launch_ssm_step(const SsmArgs& a);        // h0 and h_final the state
 size_t ssm_bwd_workspace_bytes(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N);
 int64_t ssm_bwd_workgroups(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N);
 hipError_t launch_ssm_bwd(SsmBwdArgs a, void* ws);
-// out[m] = sum_p part[p][m] over P rows of M columns, cut into three outputs
-// of m0, m1 and the remaining columns (any may be NULL).
+// out[m] = sum_p part[p][m] over P rows of M columns, cut into two outputs of m0
+// and M - m0 columns (either may be NULL).
 hipError_t launch_sum_partials(const float* part, int64_t P, int64_t M, float* o0, int64_t m0,
-                               float* o1, int64_t m1, float* o2, hipStream_t st);
+                               float* o1, hipStream_t st);
 // Copy s0 (or zeros) into s_final for an empty sequence.
 hipError_t launch_state_copy(const float* s0, float* s_final, int64_t n, hipStream_t st);
 

@@ -422,7 +422,7 @@ __global__ __launch_bounds__(256) void norm_dw_long_kernel(NormBwdArgs a, const 
     if (v > 0)
         for (int64_t row = slot * 4 + wv; row < a.R; row += nrow * 4) {
             Row<E, BF16, true> rh;
-        Row<E, DY16, true> rd;
+            Row<E, DY16, true> rd;
             float h[E], d[E];
             rh.load(a.x, row * a.xr + c, v);
             rd.load(a.dy, row * a.yr + c, v);
@@ -579,7 +579,7 @@ hipError_t launch_norm_bwd(const NormBwdArgs& a) {
     else bwd_b<false>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.part) return e;
-    return launch_sum_partials(a.part, bwd_rows(a.R, a.C), 2 * a.C, a.dw, a.C, a.db, a.C, nullptr,
+    return launch_sum_partials(a.part, bwd_rows(a.R, a.C), 2 * a.C, a.dw, a.C, a.db,
                                a.stream);
 }
 

@@ -1,6 +1,5 @@
-// Sums of per-workgroup partial gradients, and of the scan's per-block B and
-// C gradients.  Every sum runs in a fixed order, so results do not vary from
-// run to run.
+// Sums of the workgroups' partial gradients of parameters (convolution, layer
+// norm), in a fixed order, so results do not vary from run to run.
 #include "launch.h"
 #include "rows.h"
 
@@ -10,12 +9,11 @@ namespace {
 
 // out[m] = sum over p of part[p][m], one lane per m: a workgroup owns 64
 // columns, each of its W waves every W-th p (8 loads in flight), joined through
-// LDS.  The columns are cut into up to three outputs.
+// LDS.  The first m0 columns go to o0, the others to o1 (either may be NULL).
 template <int W>
 __global__ __launch_bounds__(64 * W) void sum_partials_kernel(const float* __restrict__ part,
                                                               int64_t P, int64_t M, float* o0,
-                                                              int64_t m0, float* o1, int64_t m1,
-                                                              float* o2) {
+                                                              int64_t m0, float* o1) {
     __shared__ float red[W][64];
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t m = (int64_t)blockIdx.x * 64 + lane;
@@ -38,10 +36,8 @@ __global__ __launch_bounds__(64 * W) void sum_partials_kernel(const float* __res
             v += (red[w][lane] + red[w + 1][lane]) + (red[w + 2][lane] + red[w + 3][lane]);
         if (m < m0) {
             if (o0) o0[m] = v;
-        } else if (m < m0 + m1) {
-            if (o1) o1[m - m0] = v;
-        } else if (o2) {
-            o2[m - m0 - m1] = v;
+        } else if (o1) {
+            o1[m - m0] = v;
         }
     }
 }
@@ -49,15 +45,15 @@ __global__ __launch_bounds__(64 * W) void sum_partials_kernel(const float* __res
 }  // namespace
 
 hipError_t launch_sum_partials(const float* part, int64_t P, int64_t M, float* o0, int64_t m0,
-                               float* o1, int64_t m1, float* o2, hipStream_t st) {
+                               float* o1, hipStream_t st) {
     const dim3 grid((unsigned)((M + 63) / 64));
     // many rows: 16 waves a workgroup (1024 rows of 4096: 17 -> 6 us)
     if (P >= 64)
         hipLaunchKernelGGL((sum_partials_kernel<16>), grid, dim3(1024), 0, st, part, P, M, o0, m0,
-                           o1, m1, o2);
+                           o1);
     else
-        hipLaunchKernelGGL((sum_partials_kernel<4>), grid, dim3(256), 0, st, part, P, M, o0, m0, o1,
-                           m1, o2);
+        hipLaunchKernelGGL((sum_partials_kernel<4>), grid, dim3(256), 0, st, part, P, M, o0, m0,
+                           o1);
     return hipGetLastError();
 }
 

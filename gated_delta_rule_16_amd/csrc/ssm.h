@@ -2,8 +2,9 @@
 //
 // Lane layout of the sequence kernels.  A wave is four rows of 16 lanes.  The
 // 16 lanes of a row are 16 channels; a lane holds NS neighbouring states of
-// its channel, and NG = 1, 2 or 4 rows share a channel (NS NG >= N), so a wave
-// runs CW = 64 / NG channels and the workgroup's NG running waves WC = 64.
+// its channel, and NG = 1, 2 or 4 rows share a channel (NS NG >= N: 4 states a
+// lane up to N = 16, then 8 and 16), so a wave runs CW = 64 / NG channels and
+// the workgroup's NG running waves WC = 64.
 // Four more waves of the workgroup stage the tokens to come in LDS (Delta and
 // Delta x once per channel, B and C in fp32) and finish those that are done,
 // so the running waves meet no global access in their token loop.
@@ -26,9 +27,10 @@ namespace gdr {
 template <int M>
 __device__ __forceinline__ float xor_lane(float x) {
     const int i = __builtin_bit_cast(int, x);
-    if constexpr (M == 1) return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, i, 0xB1, 0xF, 0xF, false));
-    if constexpr (M == 2) return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, i, 0x4E, 0xF, 0xF, false));
-    if constexpr (M == 8) return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, i, 0x128, 0xF, 0xF, false));
+    constexpr int ctrl = M == 1 ? 0xB1 : M == 2 ? 0x4E : 0x128;
+    if constexpr (M != 4)
+        return __builtin_bit_cast(float,
+                                  __builtin_amdgcn_update_dpp(0, i, ctrl, 0xF, 0xF, false));
     static_assert(M == 1 || M == 2 || M == 4 || M == 8, "lane distance");
     // banks 0 and 2 of a row read 4 lanes up (row_shl 4), banks 1 and 3 down
     const int up = __builtin_amdgcn_update_dpp(0, i, 0x104, 0xF, 0x5, false);

@@ -644,7 +644,8 @@ gdr_status_t gdr2_chunk_bwd_ex(int64_t B, int64_t T, int64_t H, int64_t Dk,
  *     A stride is in [0, 2^40].  Everything without a stride is contiguous;
  *   - every pointer needs only its element's alignment (workspaces 16 bytes);
  *   - sizes are free: channels, lengths and states of any count within the
- *     stated limits, no multiple of anything;
+ *     stated limits, no multiple of anything.  A launch has at most 2^24
+ *     workgroups (layer norm: one per row or fewer); larger calls are refused;
  *   - the gradients of activations are written in grad_dt (GDR_F32 or
  *     GDR_BF16), those of parameters and states in fp32.  Every sum runs in a
  *     fixed order: equal calls give equal bits;
