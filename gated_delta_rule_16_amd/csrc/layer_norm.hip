@@ -10,10 +10,11 @@
 // Bound by HBM: one pass over each tensor.  A row is held in registers
 // between its two reductions (mean, then the centred squares, so there is no
 // cancellation of mean squares): one wave per row up to 2048 channels (1024
-// backward), with no barrier; one workgroup of four waves per row up to 8192;
-// beyond that the workgroup walks the row again (from L2) for each reduction.
+// backward), with no barrier; a workgroup of four waves per row up to 8192, of
+// eight up to 16384; beyond that the workgroup walks the row again (from L2) for
+// each reduction.
 // 32768 rows of 2048 in bf16 with the residual stream: forward 99 us (5.4
-// TB/s), backward 111 us (4.8 TB/s; a copy reaches 4.9 on the same card).
+// TB/s), backward 107 us (5.0 TB/s; a copy reaches 4.9 on the same card).
 #include "launch.h"
 #include "rows.h"
 
@@ -22,6 +23,8 @@ namespace gdr {
 namespace {
 
 constexpr int E = 8;              // channels per lane and access
+
+constexpr int threads(int WR) { return WR == 8 ? 512 : 256; }
 
 __device__ __forceinline__ float wave_sum(float x) {
     x += dpp_mov<0xB1>(x);
@@ -33,33 +36,40 @@ __device__ __forceinline__ float wave_sum(float x) {
     return x;
 }
 
-// Sum over the row's threads: its wave (WG false), or the workgroup.  `red`
+// A sum over WR waves of a row, in a fixed order.
+template <int WR> __device__ __forceinline__ float join_waves(const float* red) {
+    float x = (red[0] + red[1]) + (red[2] + red[3]);
+    if constexpr (WR == 8) x += (red[4] + red[5]) + (red[6] + red[7]);
+    return x;
+}
+
+// Sum over the row's threads: WR waves of a workgroup, or one wave.  `red`
 // is one of alternating slots, so one barrier per sum suffices: a slot is
 // written again only after the barrier of the sum in between.
-template <bool WG>
+template <int WR>
 __device__ __forceinline__ float row_total(float x, float* red) {
     x = wave_sum(x);
-    if constexpr (WG) {
+    if constexpr (WR > 1) {
         if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
         __syncthreads();
-        x = (red[0] + red[1]) + (red[2] + red[3]);
+        x = join_waves<WR>(red);
     }
     return x;
 }
 
 // Three sums at once.
-template <bool WG>
-__device__ __forceinline__ void row_totals(float (&x)[3], float (*red)[4]) {
+template <int WR>
+__device__ __forceinline__ void row_totals(float (&x)[3], float (*red)[8]) {
 #pragma unroll
     for (int i = 0; i < 3; ++i) x[i] = wave_sum(x[i]);
-    if constexpr (WG) {
+    if constexpr (WR > 1) {
         if ((threadIdx.x & 63) == 0) {
 #pragma unroll
             for (int i = 0; i < 3; ++i) red[i][threadIdx.x >> 6] = x[i];
         }
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 3; ++i) x[i] = (red[i][0] + red[i][1]) + (red[i][2] + red[i][3]);
+        for (int i = 0; i < 3; ++i) x[i] = join_waves<WR>(red[i]);
     }
 }
 
@@ -105,11 +115,13 @@ template <bool BF16, int RES, bool RAG> struct SumIn {
     }
 };
 
-// NV groups of 8 channels per thread; WG: a workgroup per row, else a wave.
-template <int NV, bool WG, bool BF16, int RES, bool RAG>
-__global__ __launch_bounds__(256) void norm_fwd_kernel(NormArgs a) {
-    __shared__ float red[2][4];
-    constexpr int NT = WG ? 256 : 64;
+// NV groups of 8 channels per thread, WR waves per row (1: four rows to a
+// workgroup).
+template <int NV, int WR, bool BF16, int RES, bool RAG>
+__global__ __launch_bounds__(threads(WR)) void norm_fwd_kernel(NormArgs a) {
+    __shared__ float red[2][8];
+    constexpr bool WG = WR > 1;
+    constexpr int NT = 64 * WR;
     const int id = WG ? threadIdx.x : (threadIdx.x & 63);
     const int64_t row = WG ? blockIdx.x
                            : (int64_t)blockIdx.x * 4 +
@@ -133,7 +145,7 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormArgs a) {
         for (int e = 0; e < E; ++e) s += !RAG || e >= twice[k] ? h[k][e] : 0.f;
     }
     const float inv = 1.f / (float)a.C;
-    const float mu = row_total<WG>(s, red[0]) * inv;
+    const float mu = row_total<WR>(s, red[0]) * inv;
     s = 0.f;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -146,7 +158,7 @@ __global__ __launch_bounds__(256) void norm_fwd_kernel(NormArgs a) {
             if (v[k] > 0 && (!RAG || e >= twice[k])) s = __builtin_fmaf(h[k][e], h[k][e], s);
         }
     }
-    const float rstd = 1.f / sqrtf(row_total<WG>(s, red[1]) * inv + a.eps);
+    const float rstd = 1.f / sqrtf(row_total<WR>(s, red[1]) * inv + a.eps);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         float w[E], b[E];
@@ -185,7 +197,7 @@ __global__ __launch_bounds__(256) void norm_fwd_long_kernel(NormArgs a) {
     constexpr bool sbf = RES ? RES == 1 : BF16;
     const int64_t so = row * (RES ? a.C : a.xr);
     const float inv = 1.f / (float)a.C;
-    const float mu = row_total<true>(s, red[0]) * inv;
+    const float mu = row_total<4>(s, red[0]) * inv;
     s = 0.f;
     for (int64_t c = (int64_t)threadIdx.x * E; c < a.C; c += step) {
         Row<E, sbf, true> r;
@@ -197,7 +209,7 @@ __global__ __launch_bounds__(256) void norm_fwd_long_kernel(NormArgs a) {
         for (int e = 0; e < E; ++e)
             if (e < v) s = __builtin_fmaf(h[e] - mu, h[e] - mu, s);
     }
-    const float rstd = 1.f / sqrtf(row_total<true>(s, red[1]) * inv + a.eps);
+    const float rstd = 1.f / sqrtf(row_total<4>(s, red[1]) * inv + a.eps);
     for (int64_t c = (int64_t)threadIdx.x * E; c < a.C; c += step) {
         Row<E, sbf, true> r;
         float h[E], w[E], b[E];
@@ -221,13 +233,16 @@ __global__ __launch_bounds__(256) void norm_fwd_long_kernel(NormArgs a) {
 // over all rows of a wave (WG: of the workgroup) and leave as one partial row
 // [2 C] per workgroup.  From 1024 channels on the workgroup shares a row: a
 // wave that holds 2048 channels of three tensors, their sums and the next row
-// leaves one wave per SIMD (32768 rows of 2048 in bf16: 126 us without
-// the next row's loads, 152 with them, 111 shared).
-template <int NV, bool WG, bool BF16, bool DY16, bool G16, bool RAG>
-__global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwdArgs a) {
-    __shared__ float red[4][4];
+// leaves one wave per SIMD (32768 rows of 2048 in bf16: 126 us without the next
+// row's loads, 152 with them, 111 shared; 107 with the weights kept in registers
+// too).  Eight waves leave no registers for the next row's loads (2113 rows of
+// 15613 in fp32: 250 us with them, 137 without).
+template <int NV, int WR, bool BF16, bool DY16, bool G16, bool RAG>
+__global__ __launch_bounds__(threads(WR)) void norm_bwd_kernel(NormBwdArgs a) {
+    constexpr bool WG = WR > 1, AHEAD = WR < 8;
+    __shared__ float red[4][8];
     __shared__ float join[WG ? 1 : 3 * 64 * (2 * E + 1)];
-    constexpr int NT = WG ? 256 : 64;
+    constexpr int NT = 64 * WR;
     const int id = WG ? threadIdx.x : (threadIdx.x & 63);
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     float dw[NV][E], db[NV][E];
@@ -247,6 +262,26 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwdArgs a) {
     Row<E, BF16, false> rh[NV];
     Row<E, DY16, false> rd[NV];
     Row<E, G16, false> rr[NV];
+    // the weights of a thread's channels: kept where they are few
+    constexpr bool KEEP = NV <= 2;
+    float kept[KEEP ? NV : 1][E];
+    auto load_weights = [&](float (&w)[E], int k) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) w[e] = 1.f;
+        if (a.w) param_load<E>(w, a.w + at[k], v[k]);
+    };
+    auto weights = [&](float (&w)[E], int k) {
+        if constexpr (KEEP) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) w[e] = kept[k][e];
+        } else {
+            load_weights(w, k);
+        }
+    };
+    if constexpr (KEEP) {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) load_weights(kept[k], k);
+    }
     auto fetch = [&](int64_t row) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
@@ -256,8 +291,9 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwdArgs a) {
         }
     };
     int64_t row = WG ? blockIdx.x : (int64_t)blockIdx.x * 4 + wv;
-    if (row < a.R) fetch(row);
+    if (AHEAD && row < a.R) fetch(row);
     for (; row < a.R; row += stride) {
+        if (!AHEAD) fetch(row);
         float h[NV][E], d[NV][E], q[NV][E];
         float s = 0.f;
 #pragma unroll
@@ -269,34 +305,34 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(NormBwdArgs a) {
             for (int e = 0; e < E; ++e) s += !RAG || e >= twice[k] ? h[k][e] : 0.f;
         }
         // the next row's loads land while this one is worked on
-        if (row + stride < a.R) fetch(row + stride);
-        const float mu = row_total<WG>(s, red[0]) * inv;
+        if (AHEAD && row + stride < a.R) fetch(row + stride);
+        const float mu = row_total<WR>(s, red[0]) * inv;
         float sums[3] = {0.f, 0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             float w[E];
-            if (a.w) param_load<E>(w, a.w + at[k], v[k]);
+            weights(w, k);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 h[k][e] = v[k] > 0 ? h[k][e] - mu : 0.f;
                 if (RAG && e < twice[k]) continue;
                 sums[0] = __builtin_fmaf(h[k][e], h[k][e], sums[0]);
-                const float dn = a.w ? d[k][e] * w[e] : d[k][e];
+                const float dn = d[k][e] * w[e];
                 sums[1] += dn;
                 sums[2] = __builtin_fmaf(dn, h[k][e], sums[2]);
             }
         }
-        row_totals<WG>(sums, red + 1);
+        row_totals<WR>(sums, red + 1);
         const float rstd = 1.f / sqrtf(sums[0] * inv + a.eps);
         const float m1 = sums[1] * inv, m2 = sums[2] * inv * rstd;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             float w[E], out[E];
-            if (a.w) param_load<E>(w, a.w + at[k], v[k]);
+            weights(w, k);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 const float n = h[k][e] * rstd;
-                const float dn = a.w ? d[k][e] * w[e] : d[k][e];
+                const float dn = d[k][e] * w[e];
                 dw[k][e] = __builtin_fmaf(d[k][e], n, dw[k][e]);
                 db[k][e] += d[k][e];
                 out[e] = rstd * (dn - m1 - n * m2);
@@ -354,7 +390,7 @@ __global__ __launch_bounds__(256) void norm_bwd_long_kernel(NormBwdArgs a, float
 #pragma unroll
         for (int e = 0; e < E; ++e) s += h[e];
     }
-    const float mu = row_total<true>(s, red[0]) * inv;
+    const float mu = row_total<4>(s, red[0]) * inv;
     s = 0.f;
     float s1 = 0.f, s2 = 0.f;
     for (int64_t c = (int64_t)threadIdx.x * E; c < a.C; c += step) {
@@ -376,9 +412,9 @@ __global__ __launch_bounds__(256) void norm_bwd_long_kernel(NormBwdArgs a, float
             s2 = __builtin_fmaf(dn, x, s2);
         }
     }
-    const float rstd = 1.f / sqrtf(row_total<true>(s, red[1]) * inv + a.eps);
-    const float m1 = row_total<true>(s1, red[2]) * inv;
-    const float m2 = row_total<true>(s2, red[3]) * inv * rstd;
+    const float rstd = 1.f / sqrtf(row_total<4>(s, red[1]) * inv + a.eps);
+    const float m1 = row_total<4>(s1, red[2]) * inv;
+    const float m2 = row_total<4>(s2, red[3]) * inv * rstd;
     if (stats && threadIdx.x == 0) {
         stats[2 * row] = mu;
         stats[2 * row + 1] = rstd;
@@ -461,7 +497,7 @@ __global__ __launch_bounds__(256) void norm_dw_long_kernel(NormBwdArgs a, const 
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-constexpr int64_t WG_MAX = 8192;
+constexpr int64_t WG_MAX = 16384;
 
 // Whether a row is held in registers: not beyond WG_MAX channels, nor under one
 // group of them.
@@ -485,13 +521,13 @@ int64_t bwd_rows(int64_t R, int64_t C) {
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-template <int NV, bool WG, bool BF16, int RES>
+template <int NV, int WR, bool BF16, int RES>
 void fwd_r(const NormArgs& a, dim3 grid) {
     if (a.C % E)
-        hipLaunchKernelGGL((norm_fwd_kernel<NV, WG, BF16, RES, true>), grid, dim3(256), 0, a.stream,
-                           a);
+        hipLaunchKernelGGL((norm_fwd_kernel<NV, WR, BF16, RES, true>), grid, dim3(threads(WR)), 0,
+                           a.stream, a);
     else
-        hipLaunchKernelGGL((norm_fwd_kernel<NV, WG, BF16, RES, false>), grid, dim3(256), 0,
+        hipLaunchKernelGGL((norm_fwd_kernel<NV, WR, BF16, RES, false>), grid, dim3(threads(WR)), 0,
                            a.stream, a);
 }
 
@@ -501,11 +537,12 @@ void fwd_t(const NormArgs& a) {
     const dim3 wave((unsigned)cdiv(a.R, 4)), wg((unsigned)a.R);
     if (!fits(C))
         hipLaunchKernelGGL((norm_fwd_long_kernel<BF16, RES>), wg, dim3(256), 0, a.stream, a);
-    else if (C <= 512) fwd_r<1, false, BF16, RES>(a, wave);
-    else if (C <= 1024) fwd_r<2, false, BF16, RES>(a, wave);
-    else if (C <= 2048) fwd_r<4, false, BF16, RES>(a, wave);
-    else if (C <= 4096) fwd_r<2, true, BF16, RES>(a, wg);
-    else fwd_r<4, true, BF16, RES>(a, wg);
+    else if (C <= 512) fwd_r<1, 1, BF16, RES>(a, wave);
+    else if (C <= 1024) fwd_r<2, 1, BF16, RES>(a, wave);
+    else if (C <= 2048) fwd_r<4, 1, BF16, RES>(a, wave);
+    else if (C <= 4096) fwd_r<2, 4, BF16, RES>(a, wg);
+    else if (C <= 8192) fwd_r<4, 4, BF16, RES>(a, wg);
+    else fwd_r<4, 8, BF16, RES>(a, wg);
 }
 
 template <bool BF16>
@@ -515,14 +552,14 @@ void fwd_b(const NormArgs& a) {
     else fwd_t<BF16, 2>(a);
 }
 
-template <int NV, bool WG, bool BF16, bool DY16, bool G16>
+template <int NV, int WR, bool BF16, bool DY16, bool G16>
 void bwd_r(const NormBwdArgs& a, dim3 grid) {
     if (a.C % E)
-        hipLaunchKernelGGL((norm_bwd_kernel<NV, WG, BF16, DY16, G16, true>), grid, dim3(256), 0,
-                           a.stream, a);
+        hipLaunchKernelGGL((norm_bwd_kernel<NV, WR, BF16, DY16, G16, true>), grid,
+                           dim3(threads(WR)), 0, a.stream, a);
     else
-        hipLaunchKernelGGL((norm_bwd_kernel<NV, WG, BF16, DY16, G16, false>), grid, dim3(256), 0,
-                           a.stream, a);
+        hipLaunchKernelGGL((norm_bwd_kernel<NV, WR, BF16, DY16, G16, false>), grid,
+                           dim3(threads(WR)), 0, a.stream, a);
 }
 
 template <bool BF16, bool DY16, bool G16>
@@ -530,11 +567,12 @@ void bwd_t(const NormBwdArgs& a) {
     const int64_t C = a.C, nrow = bwd_rows(a.R, C);
     const dim3 grid((unsigned)nrow);
     if (fits(C)) {
-        if (C <= 512) bwd_r<1, false, BF16, DY16, G16>(a, grid);
-        else if (C <= 1024) bwd_r<2, false, BF16, DY16, G16>(a, grid);
-        else if (C <= 2048) bwd_r<1, true, BF16, DY16, G16>(a, grid);
-        else if (C <= 4096) bwd_r<2, true, BF16, DY16, G16>(a, grid);
-        else bwd_r<4, true, BF16, DY16, G16>(a, grid);
+        if (C <= 512) bwd_r<1, 1, BF16, DY16, G16>(a, grid);
+        else if (C <= 1024) bwd_r<2, 1, BF16, DY16, G16>(a, grid);
+        else if (C <= 2048) bwd_r<1, 4, BF16, DY16, G16>(a, grid);
+        else if (C <= 4096) bwd_r<2, 4, BF16, DY16, G16>(a, grid);
+        else if (C <= 8192) bwd_r<4, 4, BF16, DY16, G16>(a, grid);
+        else bwd_r<4, 8, BF16, DY16, G16>(a, grid);
     } else {
         const int64_t ncb = cdiv(C, 64 * E);
         float* stats = a.part ? reinterpret_cast<float*>(reinterpret_cast<char*>(a.part) +

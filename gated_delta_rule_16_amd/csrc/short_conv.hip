@@ -38,6 +38,24 @@ __device__ __forceinline__ int own_group(int64_t& c, int64_t C) {
     return EE;
 }
 
+// How the lanes of a wave lie over channels and tokens.
+//   WIDE: 64 groups of channels of one stretch of tokens; the token's address is
+//     the wave's, in scalar registers.
+//   PACKED: rows of at most 32 groups of channels: gl lanes (a power of two) to a
+//     stretch, and 64 / gl stretches to a wave (bf16, K 2, B 59 T 12693 C 78:
+//     47 us against 135 WIDE; at C 2048 the lanes' own token addresses would
+//     cost the backward 123 us instead of 94).
+//   RAGGED: the same with any number of channels, element by element at a row's
+//     end: fewer channels than one group, or a state written in place.
+enum Form { WIDE, PACKED, RAGGED };
+
+// Lanes per stretch for C channels in groups of EE.
+template <int EE> int group_lanes(int64_t C) {
+    int gl = 1;
+    while (gl < 64 && (int64_t)gl * EE < C) gl *= 2;
+    return gl;
+}
+
 // Row t of [state; x] for one lane's channels: t >= 0 from x, else the state
 // (or zeros without one).
 template <int EE, bool BF16, bool RAG>
@@ -49,15 +67,20 @@ __device__ __forceinline__ void load_in(Row<EE, BF16, RAG>& r, const ConvArgs& a
            past && !a.s0 ? 0 : valid);
 }
 
-template <int K, bool BF16, bool RAG>
-__global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int64_t ncb, int64_t nstretch,
-                                                       int TL) {
+template <int K, bool BF16, Form FORM>
+__global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int64_t ncb, int64_t nunit,
+                                                       int TL, int gl) {
+    constexpr bool RAG = FORM == RAGGED;
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int64_t id = blockIdx.x;
     const int64_t cb = id % ncb;
     id /= ncb;
-    const int64_t st = (id % nstretch) * 4 + wv, b = id / nstretch;
-    int64_t c = (cb * 64 + lane) * E;
+    const int64_t b = id / nunit;
+    int64_t st = (id % nunit) * 4 + wv, c = (cb * 64 + lane) * E;
+    if constexpr (FORM != WIDE) {
+        st = st * (64 / gl) + lane / gl;
+        c = (cb * gl + lane % gl) * E;
+    }
     const int valid = own_group<E, RAG>(c, a.C);
     const int64_t t0 = st * TL;
     if (valid == 0 || t0 >= a.T) return;
@@ -151,13 +174,14 @@ constexpr int BE = 4;             // backward: channels per lane
 // The walk runs K - 1 tokens past the stretch to complete its last dx, and a
 // stretch leaves the dx of the K - 1 rows before it to its neighbour -- but
 // the first, whose earlier rows are the state's gradient.
-template <int K, bool BF16, bool DY16, bool RAG>
+template <int K, bool BF16, bool DY16, Form FORM>
 __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int64_t ncb, int64_t nrow,
-                                                       int64_t nstretch, int TL) {
+                                                       int64_t nunit, int TL, int gl) {
+    constexpr bool RAG = FORM == RAGGED;
     __shared__ float red[3][64][BE * (K + 1) + 1];
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t cb = blockIdx.x % ncb, row = blockIdx.x / ncb;
-    int64_t c = (cb * 64 + lane) * BE;
+    int64_t c = FORM == WIDE ? (cb * 64 + lane) * BE : (cb * gl + lane % gl) * BE;
     const int valid = own_group<BE, RAG>(c, a.C);
     float w[BE * K], bias[BE], dw[BE][K], db[BE];
     param_load<BE * K>(w, a.w + c * K, valid * K);
@@ -168,10 +192,12 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int64_t ncb, 
 #pragma unroll
         for (int j = 0; j < K; ++j) dw[e][j] = 0.f;
     }
-    const int64_t units = a.B * nstretch;
+    const int64_t units = a.B * nunit;
     if (valid > 0)
         for (int64_t un = row; un < units; un += nrow) {
-            const int64_t b = un / nstretch, t0 = ((un % nstretch) * 4 + wv) * TL;
+            const int64_t b = un / nunit;
+            int64_t t0 = ((un % nunit) * 4 + wv) * TL;
+            if constexpr (FORM != WIDE) t0 = t0 * (64 / gl) + lane / gl * TL;
             if (t0 >= a.T) continue;
             const int64_t t1 = t0 + TL < a.T ? t0 + TL : a.T;
             // x window: rows t - K + 1 .. t; du window: du_{t-K+1} .. du_t
@@ -258,6 +284,16 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int64_t ncb, 
             }
         }
     if (!a.part) return;
+    if constexpr (FORM != WIDE) {
+        // over the wave's stretches, to all of their lanes
+        for (int d = gl; d < 64; d *= 2)
+#pragma unroll
+            for (int e = 0; e < BE; ++e) {
+                db[e] += __shfl_xor(db[e], d, 64);
+#pragma unroll
+                for (int j = 0; j < K; ++j) dw[e][j] += __shfl_xor(dw[e][j], d, 64);
+            }
+    }
     if (wv > 0) {
 #pragma unroll
         for (int e = 0; e < BE; ++e) {
@@ -267,7 +303,7 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int64_t ncb, 
         }
     }
     __syncthreads();
-    if (wv == 0 && valid > 0) {
+    if (wv == 0 && valid > 0 && (FORM == WIDE || lane < gl)) {
         float* p = a.part + row * a.C * (K + 1);
 #pragma unroll
         for (int e = 0; e < BE; ++e) {
@@ -284,39 +320,51 @@ __global__ __launch_bounds__(256) void conv_bwd_kernel(ConvArgs a, int64_t ncb, 
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Tokens per wave's stretch: long enough that the K - 1 rows read twice are
-// few, short enough that the launch fills the chip.
-int stretch_tokens(int64_t B, int64_t T, int64_t ncb, int lo, int hi) {
-    int TL = hi;
-    while (TL > lo && B * ncb * cdiv(T, TL) < 8192) TL /= 2;
-    return TL;
+struct Shape {
+    int64_t ncb, nunit;     // blocks of channels; of 4 waves' stretches
+    int TL, gl;
+};
+
+// The launch for groups of EE channels.  A stretch of TL tokens, between lo and
+// hi: long enough that the K - 1 rows read twice are few, short enough that the
+// launch fills the chip.
+template <int EE>
+Shape shape(int64_t B, int64_t T, int64_t C, int lo, int hi) {
+    Shape s;
+    s.gl = group_lanes<EE>(C);
+    s.ncb = cdiv(C, 64 * EE);
+    const int64_t per = 64 / s.gl;              // stretches per wave
+    s.TL = hi;
+    while (s.TL > lo && B * s.ncb * cdiv(T, s.TL * per) < 8192) s.TL /= 2;
+    s.nunit = cdiv(T, 4 * per * s.TL);
+    return s;
 }
+Shape fwd_shape(int64_t B, int64_t T, int64_t C) { return shape<E>(B, T, C, 4, 64); }
+Shape bwd_shape(int64_t B, int64_t T, int64_t C) { return shape<BE>(B, T, C, 8, 64); }
 
 // Backward: workgroup rows (partials of dw) for the launch.
-void bwd_shape(int64_t B, int64_t T, int64_t C, int64_t& ncb, int64_t& nstretch, int64_t& nrow,
-               int& TL) {
-    ncb = cdiv(C, 64 * BE);
-    TL = stretch_tokens(B, T, ncb, 8, 64);
-    nstretch = cdiv(T, 4 * (int64_t)TL);
-    const int64_t units = B * nstretch;
-    const int64_t cap = cdiv(4096, ncb);
-    nrow = units < cap ? units : cap;
+int64_t bwd_rows(const Shape& s, int64_t B) {
+    const int64_t units = B * s.nunit, cap = cdiv(4096, s.ncb);
+    return units < cap ? units : cap;
 }
 
 template <int K>
-void fwd_t(const ConvArgs& a, dim3 grid, int64_t ncb, int64_t nst, int TL) {
+void fwd_t(const ConvArgs& a, dim3 grid, const Shape& s) {
     // a moved group reads channels that another lane also writes back: not where
     // the state's buffer is the next one's
     const bool rag = a.C < E || (a.C % E != 0 && a.s_final && a.s_final == a.s0);
-#define FWD(BF16, RAG)                                                                           \
-    hipLaunchKernelGGL((conv_fwd_kernel<K, BF16, RAG>), grid, dim3(256), 0, a.stream, a, ncb, nst, \
-                       TL)
+    const bool packed = s.gl < 64;
+#define FWD(BF16, FORM)                                                                           \
+    hipLaunchKernelGGL((conv_fwd_kernel<K, BF16, FORM>), grid, dim3(256), 0, a.stream, a, s.ncb, \
+                       s.nunit, s.TL, s.gl)
     if (a.in_bf16) {
-        if (rag) FWD(true, true);
-        else FWD(true, false);
+        if (rag) FWD(true, RAGGED);
+        else if (packed) FWD(true, PACKED);
+        else FWD(true, WIDE);
     } else {
-        if (rag) FWD(false, true);
-        else FWD(false, false);
+        if (rag) FWD(false, RAGGED);
+        else if (packed) FWD(false, PACKED);
+        else FWD(false, WIDE);
     }
 #undef FWD
 }
@@ -330,48 +378,44 @@ void step_t(const ConvArgs& a, dim3 grid, int64_t ncg) {
 }
 
 template <int K, bool BF16, bool DY16>
-void bwd_t(const ConvArgs& a, dim3 grid, int64_t ncb, int64_t nrow, int64_t nstretch, int TL) {
-    if (a.C < BE)
-        hipLaunchKernelGGL((conv_bwd_kernel<K, BF16, DY16, true>), grid, dim3(256), 0, a.stream, a,
-                           ncb, nrow, nstretch, TL);
-    else
-        hipLaunchKernelGGL((conv_bwd_kernel<K, BF16, DY16, false>), grid, dim3(256), 0, a.stream, a,
-                           ncb, nrow, nstretch, TL);
+void bwd_t(const ConvArgs& a, dim3 grid, const Shape& s, int64_t nrow) {
+#define BWD(FORM)                                                                                \
+    hipLaunchKernelGGL((conv_bwd_kernel<K, BF16, DY16, FORM>), grid, dim3(256), 0, a.stream, a, \
+                       s.ncb, nrow, s.nunit, s.TL, s.gl)
+    if (a.C < BE) BWD(RAGGED);
+    else if (s.gl < 64) BWD(PACKED);
+    else BWD(WIDE);
+#undef BWD
 }
 
 template <int K>
-void bwd_k(const ConvArgs& a, dim3 grid, int64_t ncb, int64_t nrow, int64_t nstretch, int TL) {
+void bwd_k(const ConvArgs& a, dim3 grid, const Shape& s, int64_t nrow) {
     if (a.in_bf16) {
-        if (a.dy_bf16) bwd_t<K, true, true>(a, grid, ncb, nrow, nstretch, TL);
-        else bwd_t<K, true, false>(a, grid, ncb, nrow, nstretch, TL);
+        if (a.dy_bf16) bwd_t<K, true, true>(a, grid, s, nrow);
+        else bwd_t<K, true, false>(a, grid, s, nrow);
     } else {
-        if (a.dy_bf16) bwd_t<K, false, true>(a, grid, ncb, nrow, nstretch, TL);
-        else bwd_t<K, false, false>(a, grid, ncb, nrow, nstretch, TL);
+        if (a.dy_bf16) bwd_t<K, false, true>(a, grid, s, nrow);
+        else bwd_t<K, false, false>(a, grid, s, nrow);
     }
 }
 
 }  // namespace
 
 size_t conv_bwd_workspace_bytes(int64_t B, int64_t T, int64_t C, int64_t K) {
-    int64_t ncb, nstretch, nrow;
-    int TL;
-    bwd_shape(B, T, C, ncb, nstretch, nrow, TL);
-    return sizeof(float) * (size_t)(nrow * C * (K + 1));
+    return sizeof(float) * (size_t)(bwd_rows(bwd_shape(B, T, C), B) * C * (K + 1));
 }
 
 int64_t conv_workgroups(int64_t B, int64_t T, int64_t C) {
-    const int64_t ncb = cdiv(C, 64 * E);
-    return ncb * B * cdiv(T, 4 * (int64_t)stretch_tokens(B, T, ncb, 4, 64));
+    const Shape s = fwd_shape(B, T, C);
+    return s.ncb * B * s.nunit;
 }
 
 hipError_t launch_conv_fwd(const ConvArgs& a) {
-    const int64_t ncb = cdiv(a.C, 64 * E);
-    const int TL = stretch_tokens(a.B, a.T, ncb, 4, 64);
-    const int64_t nst = cdiv(a.T, 4 * (int64_t)TL);
-    const dim3 grid((unsigned)(ncb * nst * a.B));
-    if (a.K == 4) fwd_t<4>(a, grid, ncb, nst, TL);
-    else if (a.K == 3) fwd_t<3>(a, grid, ncb, nst, TL);
-    else fwd_t<2>(a, grid, ncb, nst, TL);
+    const Shape s = fwd_shape(a.B, a.T, a.C);
+    const dim3 grid((unsigned)(s.ncb * s.nunit * a.B));
+    if (a.K == 4) fwd_t<4>(a, grid, s);
+    else if (a.K == 3) fwd_t<3>(a, grid, s);
+    else fwd_t<2>(a, grid, s);
     return hipGetLastError();
 }
 
@@ -385,13 +429,12 @@ hipError_t launch_conv_step(const ConvArgs& a) {
 }
 
 hipError_t launch_conv_bwd(const ConvArgs& a) {
-    int64_t ncb, nstretch, nrow;
-    int TL;
-    bwd_shape(a.B, a.T, a.C, ncb, nstretch, nrow, TL);
-    const dim3 grid((unsigned)(ncb * nrow));
-    if (a.K == 4) bwd_k<4>(a, grid, ncb, nrow, nstretch, TL);
-    else if (a.K == 3) bwd_k<3>(a, grid, ncb, nrow, nstretch, TL);
-    else bwd_k<2>(a, grid, ncb, nrow, nstretch, TL);
+    const Shape s = bwd_shape(a.B, a.T, a.C);
+    const int64_t nrow = bwd_rows(s, a.B);
+    const dim3 grid((unsigned)(s.ncb * nrow));
+    if (a.K == 4) bwd_k<4>(a, grid, s, nrow);
+    else if (a.K == 3) bwd_k<3>(a, grid, s, nrow);
+    else bwd_k<2>(a, grid, s, nrow);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.part) return e;
     return launch_sum_partials(a.part, nrow, a.C * (a.K + 1), a.dw, a.C * a.K, a.dbias,

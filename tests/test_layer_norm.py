@@ -152,3 +152,11 @@ def test_bwd_options_and_empty(gdr_lib):
     assert gdr_lib.gdr_layer_norm_fwd(x[:0], w).shape == (0, 300)
     torch.cuda.synchronize()
     assert dx.shape == (0, 300) and not dw.any() and not db.any()
+
+
+@pytest.mark.parametrize("C", [8192, 8193, 12000, 16379, 16384, 16385])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_longest_rows_in_registers(gdr_lib, C, dt):
+    i = make(40, C, dt, C)
+    check_fwd(gdr_lib, i, dt, dt)
+    check_bwd(gdr_lib, i, dt, dt, True)

@@ -179,3 +179,12 @@ def test_bwd_repeats_bit_for_bit_and_empty(gdr_lib):
     dx, dw, db, ds0 = gdr_lib.gdr_short_conv_bwd(e, a[1], a[2], a[3], e, a[5])
     torch.cuda.synchronize()
     assert dx.shape == e.shape and not dw.any() and not db.any() and torch.equal(ds0, a[5])
+
+
+@pytest.mark.parametrize("C", [4, 12, 17, 33, 100, 130, 255, 256, 300])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_narrow_rows(gdr_lib, C, dt):
+    """Few channels: several stretches of tokens share a wave."""
+    i = make(3, 333, C, 4, dt, C)
+    check_fwd(gdr_lib, i, 4, True, dt)
+    check_bwd(gdr_lib, i, 4, True, dt, dt)
