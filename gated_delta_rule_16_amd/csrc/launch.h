@@ -234,6 +234,7 @@ hipError_t launch_norm_fwd(const NormArgs& a);
 hipError_t launch_norm_bwd(const NormBwdArgs& a);
 size_t norm_bwd_workspace_bytes(int64_t R, int64_t C);
 int64_t ssm_padded_states(int64_t N);
+int64_t ssm_most_segments(int64_t T);
 int64_t ssm_step_workgroups(int64_t B, int64_t D, int64_t N);
 SsmPlan ssm_fwd_plan(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N);
 size_t ssm_fwd_workspace_bytes(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N);

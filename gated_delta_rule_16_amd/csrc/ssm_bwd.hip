@@ -403,26 +403,18 @@ __global__ __launch_bounds__(64 * (NG + 4), NS == 16 ? 1 : 2) void ssm_bwd_kerne
         }
         const int64_t so = (b * a.D + ch) * a.N + n0;
         // the segment's start state (segment 0's kept states hold h0 already)
-        for (int64_t s = 0; s < seg; ++s) {
-            const int64_t o = (b * nseg + s) * a.D + ch;
-            float e[NS];
-            states_load<NS, false>(e, a.hend + o * NP + n0, live);
-            const float sd = live ? a.sdelta[o] : 0.f;
-#pragma unroll
-            for (int j = 0; j < NS; ++j)
-                hin[j] = s == 0 ? e[j]
-                                : __builtin_fmaf(__builtin_amdgcn_exp2f(A2[j] * sd), hin[j], e[j]);
+        if (seg > 0) {
+            const int64_t o = b * nseg * a.D + ch;
+            states_load<NS, false>(hin, a.hend + o * NP + n0, live);
+            compose<NS>(hin, A2, a.hend + (o + a.D) * NP + n0, a.D * NP, a.sdelta + o + a.D, a.D,
+                        seg - 1, live);
         }
         // gr = a_{t+1} g_{t+1} past the segment's last token
         if (a.dh_final) states_load<NS>(gr, a.dh_final + so, nv);
-        for (int64_t s = nseg - 1; s > seg; --s) {
-            const int64_t o = (b * nseg + s) * a.D + ch;
-            float e[NS];
-            states_load<NS, false>(e, a.gstart + o * NP + n0, live);
-            const float sd = live ? a.sdelta[o] : 0.f;
-#pragma unroll
-            for (int j = 0; j < NS; ++j)
-                gr[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(A2[j] * sd), gr[j], e[j]);
+        if (seg < nseg - 1) {
+            const int64_t o = (b * nseg + nseg - 1) * a.D + ch;
+            compose<NS>(gr, A2, a.gstart + o * NP + n0, -a.D * NP, a.sdelta + o, -a.D,
+                        nseg - 1 - seg, live);
         }
         float kept[NS], ksum = 0.f;
         auto fetch = [&](int64_t sub) {
@@ -749,14 +741,13 @@ __global__ __launch_bounds__(256) void ssm_bwd_reduce(SsmBwdArgs a, int64_t nblk
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Segments of the backward: of at least 64 tokens, up to two workgroups per
-// compute unit (B 4 T 4096 D 2048 N 16: 587 us with 512 workgroups, 630
-// with 256, 780 with 384).
+// Segments of the backward: up to two workgroups per compute unit (B 4 T 4096
+// D 2048 N 16: 587 us with 512 workgroups, 630 with 256, 780 with 384).
 SsmPlan bwd_plan(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N) {
     SsmPlan p;
     p.nblk = cdiv(D / G, 64);
     int64_t n = 512 / (B * G * p.nblk);
-    const int64_t most = cdiv(T, 64);
+    const int64_t most = ssm_most_segments(T);
     if (n > most) n = most;
     if (n < 1) n = 1;
     p.L = cdiv(cdiv(T, n), 32) * 32;

@@ -85,15 +85,9 @@ __global__ __launch_bounds__(64 * (NG + 4)) void ssm_fwd_kernel(SsmArgs a, int64
                     states_store<NS>(a.hend + (b * nseg * a.D + ch) * NP + n0, h, live ? NS : 0);
         } else {
             states_load<NS, false>(h, a.hend + ((b * nseg + (seg > 0)) * a.D + ch) * NP + n0, live);
-            for (int64_t s = 1; s < seg; ++s) {
-                const int64_t o = (b * nseg + s) * a.D + ch;
-                float e[NS];
-                states_load<NS, false>(e, a.hend + (o + a.D) * NP + n0, live);
-                const float sd = live ? a.sdelta[o] : 0.f;
-#pragma unroll
-                for (int j = 0; j < NS; ++j)
-                    h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(A2[j] * sd), h[j], e[j]);
-            }
+            const int64_t o = (b * nseg + 1) * a.D + ch;
+            compose<NS>(h, A2, a.hend + (o + a.D) * NP + n0, a.D * NP, a.sdelta + o, a.D, seg - 1,
+                        live);
         }
         float sumd = 0.f;
         __syncthreads();
@@ -386,17 +380,27 @@ int64_t ssm_padded_states(int64_t N) {
     return n;
 }
 
+// A segment costs 0.1 us at the head of every other one, and a token 0.05 us:
+// about sqrt(T / 2) segments balance the two (B 1 T 32768 D 16 N 16 forward: 50 us
+// with 128, 71 with 64, 73 with 512; backward 111, 172, 185).  At least 64 tokens.
+int64_t ssm_most_segments(int64_t T) {
+    const int64_t n = (T + 63) / 64;
+    int64_t r = 1;
+    while (r < n && r < 512 && 2 * (r + 1) * (r + 1) <= T) ++r;
+    return r;
+}
+
 // Segments of the forward.  One when the channels give 192 workgroups, three
-// quarters of one per compute unit; below that enough, of at least 64
-// tokens, for two per compute unit (B 1 T 32768 D 2048 N 16: 417 us with 512
-// workgroups, 454 with 256, 556 with 384, 885 with 128).
+// quarters of one per compute unit; below that enough for two per compute unit
+// (B 1 T 32768 D 2048 N 16: 417 us with 512 workgroups, 454 with 256, 556 with
+// 384, 885 with 128).
 SsmPlan ssm_fwd_plan(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N) {
     SsmPlan p;
     p.nblk = cdiv(D / G, 64);
     const int64_t wgs = B * G * p.nblk;
     int64_t n = 1;
     if (wgs < 192) n = 512 / wgs;
-    const int64_t most = cdiv(T, 64);
+    const int64_t most = ssm_most_segments(T);
     if (n > most) n = most;
     if (n < 1) n = 1;
     p.L = cdiv(cdiv(T, n), 32) * 32;

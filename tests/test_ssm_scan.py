@@ -314,3 +314,12 @@ def test_bwd_repeats_bit_for_bit(gdr_lib):
     one, two = gdr_lib.gdr_ssm_scan_bwd(*a), gdr_lib.gdr_ssm_scan_bwd(*a)
     torch.cuda.synchronize()
     assert all(torch.equal(p, q) for p, q in zip(one, two))
+
+
+@pytest.mark.parametrize("N,D", [(16, 20), (3, 70), (40, 9)])
+def test_many_segments(gdr_lib, N, D):
+    """A long sequence of few channels: more segments than one batch of their
+    states, forward and backward."""
+    i = make(1, 4000, D, 1, N, "f32", N, slow=0.05)
+    check_fwd(gdr_lib, i)
+    check_bwd(gdr_lib, i)
