@@ -175,6 +175,8 @@ extern "C" gdr_status_t gdr_short_conv_bwd(int64_t B, int64_t T, int64_t C, int6
     if (sums && (!ptrs_ok({workspace}) ||
                  workspace_bytes < conv_bwd_workspace_bytes(B, T, C, K)))
         return GDR_ERR_INVALID;
+    // the second launch: up to 1024 threads for 64 columns
+    if (sums && !workgroups_ok((double)C * (double)(K + 1) / 16.0)) return GDR_ERR_INVALID;
     ConvArgs a{};
     a.B = B;
     a.T = T;

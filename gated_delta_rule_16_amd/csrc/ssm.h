@@ -216,13 +216,13 @@ __device__ __forceinline__ void states_load(float (&h)[NS], const float* p, int 
         if (valid > 0) param_load<NS>(h, p, NS);
     }
 }
-template <int NS, bool RAG = true>
+template <int NS>
 __device__ __forceinline__ void states_store(float* p, const float (&h)[NS], int valid) {
     if (valid >= NS) {
 #pragma unroll
         for (int i = 0; i < NS; i += 4)
             *reinterpret_cast<f32x4_e4*>(p + i) = f32x4_e4{h[i], h[i + 1], h[i + 2], h[i + 3]};
-    } else if constexpr (RAG) {
+    } else {
 #pragma unroll
         for (int i = 0; i < NS; ++i)
             if (i < valid) p[i] = h[i];

@@ -219,3 +219,11 @@ C16 = A16 + 8192
 def test_outputs_at_inputs(gdr, name, kw):
     """What cannot be done in place is refused, not done wrongly."""
     assert globals()[name](gdr, **kw) == 1
+
+
+def test_conv_bwd_of_more_channels_than_its_sums_launch(gdr):
+    """The sums of dw over 2^28 channels would not fit a launch: refused before
+    anything runs."""
+    C = 1 << 28
+    need = gdr.gdr_short_conv_bwd_workspace_size(1, 1, C, 4)
+    assert conv_bwd(gdr, B=1, T=1, C=C, dy=B16, dx=C16, nb=need) == 1
