@@ -1,9 +1,10 @@
 """Python binding of libgdr, the gfx950 gated delta rule library.
 
 Argument marshalling only: every step of every operation runs in the HIP
-kernels behind the C ABI declared in ``include/gdr.h``.  PyTorch supplies
-device memory and the current HIP stream.  There is no CPU or PyTorch
-fallback — importing this package without the built ``libgdr.so`` fails.
+kernels behind the C ABI declared in ``include/gdr.h`` and (the operators
+around the mixer) ``include/gdr_block.h``.  PyTorch supplies device memory
+and the current HIP stream.  There is no CPU or PyTorch fallback — importing
+this package without the built ``libgdr.so`` fails.
 
 Functions mirror the C calls:
 

@@ -1,11 +1,11 @@
-// C ABI of the operators around the token mixer (declared in gdr.h): short
+// C ABI of the operators around the token mixer (declared in gdr_block.h): short
 // causal convolution, selective state space scan, layer norm.  Host-side
 // validation and dispatch; an error status means nothing was launched.
 #include <initializer_list>
 
-#include "../../include/gdr.h"
+#include "../../include/gdr_block.h"
 #include "api_checks.h"
-#include "launch.h"
+#include "block_launch.h"
 
 using namespace gdr;
 

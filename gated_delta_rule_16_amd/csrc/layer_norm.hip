@@ -15,7 +15,7 @@
 // each reduction.
 // 32768 rows of 2048 in bf16 with the residual stream: forward 99 us (5.4
 // TB/s), backward 107 us (5.0 TB/s; a copy reaches 4.9 on the same card).
-#include "launch.h"
+#include "block_launch.h"
 #include "rows.h"
 
 namespace gdr {

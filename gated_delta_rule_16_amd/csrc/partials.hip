@@ -1,6 +1,6 @@
 // Sums of the workgroups' partial gradients of parameters (convolution, layer
 // norm), in a fixed order, so results do not vary from run to run.
-#include "launch.h"
+#include "block_launch.h"
 #include "rows.h"
 
 namespace gdr {

@@ -18,7 +18,7 @@
 
 #include <utility>
 
-#include "launch.h"
+#include "block_launch.h"
 #include "rows.h"
 
 namespace gdr {

@@ -1,6 +1,8 @@
 """Argument checks of the operators around the mixer, on the CPU: nothing is
 launched (fake device addresses, and calls that end before a launch)."""
 import ctypes
+import os
+import re
 
 import pytest
 
@@ -227,3 +229,17 @@ def test_conv_bwd_of_more_channels_than_its_sums_launch(gdr):
     C = 1 << 28
     need = gdr.gdr_short_conv_bwd_workspace_size(1, 1, C, 4)
     assert conv_bwd(gdr, B=1, T=1, C=C, dy=B16, dx=C16, nb=need) == 1
+
+
+def test_header_and_library_agree(gdr):
+    """Every function that gdr_block.h declares is exported, and bound under its
+    own name where it is a call of the user's; constants are the binding's."""
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include",
+                        "gdr_block.h")
+    src = re.sub(r"/\*.*?\*/", "", open(path).read(), flags=re.S)
+    names = re.findall(r"^(?:gdr_status_t|size_t)\s+(gdr_[a-z_]+)\s*\(", src, flags=re.M)
+    assert len(names) == 12
+    for n in names:
+        assert getattr(gdr.lib, n) and callable(getattr(gdr, n)) and n in gdr.__all__
+    for name, value in re.findall(r"#define (GDR_[A-Z_]+) (\d+)u?$", src, flags=re.M):
+        assert getattr(gdr, name) == int(value), name
