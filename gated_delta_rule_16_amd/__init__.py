@@ -1063,6 +1063,9 @@ def gdr_ssm_scan_bwd(x, dt, A, Bm, Cm, D, z, dt_bias, h0, dout, dh_final=None, *
     dz = None if z is None else torch.empty_like(dx)
     dB = _new(Bm, grad_dtype, Bm.shape, dev)
     dC = torch.empty_like(dB)
+    if Dn == 0:             # sums over no channels, which the C call leaves alone
+        dB.zero_()
+        dC.zero_()
     dA = torch.empty_like(A)
     dD = None if D is None else torch.empty_like(D)
     db = None if dt_bias is None else torch.empty_like(dt_bias)

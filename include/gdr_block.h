@@ -145,9 +145,11 @@ gdr_status_t gdr_ssm_step(int64_t Nseq, int64_t D, int64_t G, int64_t N,
  * y, dh_final [B, D, N] fp32 or NULL that of h_final; strides
  * {x, dt, Bm, Cm, z, dout}.  Writes dx, ddt [B, T, D], dB, dC [B, T, G, N]
  * and dz [B, T, D] (NULL without z) in grad_dt, and in fp32 dA [D, N], dD and
- * ddt_bias [D] and dh0 [B, D, N] (each of the last three may be NULL).  The
- * states are run again from the inputs; the workspace holds one state in 8 or
- * 16 tokens and the partial sums.
+ * ddt_bias [D] and dh0 [B, D, N] (each of the last three may be NULL).
+ * Without channels (D == 0) nothing is launched, as in every call: dB and dC,
+ * which have elements even then, are the caller's to clear.  The states are
+ * run again from the inputs; the workspace holds one state in 8 or 16 tokens
+ * and the partial sums.
  */
 size_t gdr_ssm_scan_bwd_workspace_size(int64_t B, int64_t T, int64_t D,
                                        int64_t G, int64_t N);
