@@ -229,6 +229,15 @@ __device__ __forceinline__ void states_store(float* p, const float (&h)[NS], int
     }
 }
 
+// The exponent's rate per unit of Delta, A log2 e.  -inf becomes fp32's lowest
+// value (so A = -inf, and finite A below -2.36e38, act as -2.36e38): a step of 0,
+// which padded tokens and empty sums have, then leaves the state as it is, and a
+// decayed state's gradient 0 stays 0, where 0 x inf would be NaN.  NaN stays NaN.
+__device__ __forceinline__ float decay_rate(float A) {
+    const float r = A * kLog2e;
+    return r < -3.402823466e38f ? -3.402823466e38f : r;
+}
+
 constexpr int WC = 64;   // channels per workgroup
 
 // The first channel, in its group of Dg, of a workgroup's WC.  Where Dg is no

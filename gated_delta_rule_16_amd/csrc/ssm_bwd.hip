@@ -80,7 +80,7 @@ __global__ __launch_bounds__(64 * (NG + 4)) void ssm_bwd_states_kernel(SsmBwdArg
         param_load<NS>(A2, a.A + ch * a.N + n0, nv);
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
-            A2[j] *= kLog2e;
+            A2[j] = decay_rate(A2[j]);
             h[j] = gam[j] = 0.f;
             P[j] = 1.f;
         }
@@ -398,7 +398,7 @@ __global__ __launch_bounds__(64 * (NG + 4), NS == 16 ? 1 : 2) void ssm_bwd_kerne
         param_load<NS>(A2, a.A + ch * a.N + n0, nv);
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
-            A2[j] *= kLog2e;
+            A2[j] = decay_rate(A2[j]);
             hin[j] = gr[j] = dA[j] = 0.f;
         }
         const int64_t so = (b * a.D + ch) * a.N + n0;
@@ -636,7 +636,10 @@ __global__ __launch_bounds__(64 * (NG + 4), NS == 16 ? 1 : 2) void ssm_bwd_kerne
             for (int e = 0; e < EPT; ++e) {
                 const float gB = st[buf][0][srow][sc + e], pA = st[buf][1][srow][sc + e];
                 dxv[e] = __builtin_fmaf(k.d[e], gB, skip[e] * k.dy[e]);
-                dtv[e] = __builtin_fmaf(k.x[e], gB, pA * kLn2) * k.ddr[e];
+                // a padded token's sums with a rate of fp32's lowest value may overflow
+                dtv[e] = k.ddr[e] == 0.f
+                             ? 0.f
+                             : __builtin_fmaf(k.x[e], gB, pA * kLn2) * k.ddr[e];
                 if (a.z)
                     dzv[e] = k.og[e] * __builtin_fmaf(skip[e], k.x[e], st[buf][3][srow][sc + e]);
                 if (!RAG || e < v) {

@@ -71,7 +71,7 @@ __global__ __launch_bounds__(64 * (NG + 4)) void ssm_fwd_kernel(SsmArgs a, int64
         param_load<NS>(A2, a.A + ch * a.N + n0, nv);
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
-            A2[j] *= kLog2e;
+            A2[j] = decay_rate(A2[j]);
             h[j] = 0.f;
         }
         const int64_t so = (b * a.D + ch) * a.N + n0;
@@ -303,7 +303,7 @@ __global__ __launch_bounds__(256) void ssm_step_kernel(SsmArgs a, uint32_t nblk)
     float s = 0.f;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(d * (A4[j] * kLog2e)), h[j], dx * B4[j]);
+        h[j] = __builtin_fmaf(__builtin_amdgcn_exp2f(d * decay_rate(A4[j])), h[j], dx * B4[j]);
         s = __builtin_fmaf(C4[j], h[j], s);
     }
     states_store<4>(a.h_final + so, h, nv);

@@ -104,7 +104,8 @@ gdr_status_t gdr_short_conv_bwd(int64_t B, int64_t T, int64_t C, int64_t K,
  *   x, dt, z  [B, T, D] in_dt; z may be NULL
  *   Bm, Cm    [B, T, G, N] in_dt, [G, N] contiguous
  *   strides   {x, dt, Bm, Cm, z}
- *   A         [D, N] fp32, <= 0 in use (not checked)
+ *   A         [D, N] fp32, <= 0 in use (not checked).  -inf and values below
+ *             -2.36e38 act as -2.36e38: any Delta above 1e-36 forgets at once
  *   D_skip, dt_bias  [D] fp32 or NULL (zeros)
  *   h0        [B, D, N] fp32 or NULL (zeros)
  *   y         [B, T, D] out_dt

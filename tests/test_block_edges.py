@@ -44,3 +44,116 @@ def test_scan_bwd_of_no_channels(gdr_lib, grad, G):
         (B, T, 0), (B, T, 0), (0, N), (B, T, G, N), (B, T, G, N), (0,), (B, T, 0), (0,), (B, 0, N)]
     for v in (o[3], o[4]):
         assert v.dtype == grad and not v.any()
+
+
+# ---- states that forget at once -----------------------------------------------------
+
+
+def forgetting(seed, B, T, D, N, dt):
+    t = draw(seed)
+    i = [t(B, T, D, dtype=dt), t(B, T, D, dtype=dt), -torch.exp(t(D, N, scale=0.7)),
+         t(B, T, 1, N, dtype=dt), t(B, T, 1, N, dtype=dt), t(D), t(B, T, D, dtype=dt),
+         t(D, shift=-3.0), t(B, D, N)]
+    return i, t(B, T, D, dtype=dt), t(B, D, N)
+
+
+def n64(t):
+    return None if t is None else t.detach().cpu().double().numpy()
+
+
+def close(name, got, want, bound):
+    err = np.abs(n64(got) - want)
+    over = err - bound
+    assert got.shape == want.shape and np.isfinite(err).all() and over.max() <= 0, \
+        f"{name}: error {err.max():.3e}, worst over its bound by {over.max():.3e}"
+
+
+@pytest.mark.parametrize("A", [float("-inf"), LOWEST])
+@pytest.mark.parametrize("T,D,N", [(1, 70, 16), (5, 70, 16), (8, 9, 3), (30, 130, 7), (75, 70, 33),
+                                   (700, 70, 16)])
+@pytest.mark.parametrize("dt", [F32, BF])
+def test_scan_that_forgets_at_once(gdr_lib, A, T, D, N, dt):
+    """A of minus infinity, or fp32's lowest value: with the steps of these
+    tokens (all above 1e-9) the decay is 0, as it is in fp64 at A = -1e30, where
+    the reference takes it.  Padded tokens, ends of segments and of the tensors
+    inside a block meet steps of 0."""
+    a, do, dh = forgetting(T + N, 2, T, D, N, dt)
+    a[2][:, 0] = A
+    a[2][5 % D] = A
+    y, h = gdr_lib.gdr_ssm_scan_fwd(*a, out_dtype=F32)
+    o = gdr_lib.gdr_ssm_scan_bwd(*a, do, dh)
+    torch.cuda.synchronize()
+    ref = [n64(v) for v in a]
+    ref[2] = np.maximum(ref[2], -1e30)
+    assert np.logaddexp(ref[1] + ref[7], 0).min() > 1e-9
+    want, wh, _ = R.scan_fwd(*ref)
+    my, mh, _ = R.scan_fwd(*ref, majorant=True)
+    close("y", y, want, R.scan_bound(my, T, "f32", want))
+    close("h", h, wh, R.scan_bound(mh, T))
+    ref += [n64(do), n64(dh)]
+    want, maj = R.scan_bwd(*ref), R.scan_bwd(*ref, majorant=True)
+    for k, g in zip(("dx", "ddt", "dA", "dB", "dC", "dD", "dz", "db", "dh0"), o):
+        steps = 2 * T + (D if k in ("dB", "dC") else 2 * T if k in ("dA", "dD", "db") else 0)
+        close(k, g, want[k], R.scan_bound(maj[k], steps))
+
+
+@pytest.mark.parametrize("A", [float("-inf"), LOWEST])
+@pytest.mark.parametrize("T", [40, 700])
+def test_padded_tokens_of_states_that_forget_at_once(gdr_lib, A, T):
+    """dt at minus infinity is a step of 0 there too: the state passes, the
+    token's own gradients are 0 whatever arrives at it, and all others are those
+    of the tokens before it."""
+    D = 70
+    a, do, dh = forgetting(6, 2, T, D, 16, BF)
+    a[2][:, 0] = A
+    a[1][:, T - 13:] = float("-inf")
+    do[:, T - 13:] = 0
+    y, h = gdr_lib.gdr_ssm_scan_fwd(*a, out_dtype=F32)
+    o = gdr_lib.gdr_ssm_scan_bwd(*a, do, dh)
+    torch.cuda.synchronize()
+    assert not o[1][:, T - 13:].any() and not o[0][:, T - 13:].any()
+    part = [v[:, :T - 13] if k in (0, 1, 3, 4, 6) else v for k, v in enumerate(a)]
+    ref = [n64(v) for v in part]
+    ref[2] = np.maximum(ref[2], -1e30)
+    want, wh, _ = R.scan_fwd(*ref)
+    my, mh, _ = R.scan_fwd(*ref, majorant=True)
+    close("y", y[:, :T - 13], want, R.scan_bound(my, T, "f32", want))
+    close("h", h, wh, R.scan_bound(mh, T))
+    ref += [n64(do[:, :T - 13]), n64(dh)]
+    want, maj = R.scan_bwd(*ref), R.scan_bwd(*ref, majorant=True)
+    for k, g in zip(("dx", "ddt", "dA", "dB", "dC", "dD", "dz", "db", "dh0"), o):
+        steps = 2 * T + (D if k in ("dB", "dC") else 2 * T if k in ("dA", "dD", "db") else 0)
+        g = g[:, :T - 13] if g.shape[1:2] == (T,) else g
+        close(k, g, want[k], R.scan_bound(maj[k], steps))
+
+
+@pytest.mark.parametrize("A", [float("-inf"), LOWEST])
+def test_token_that_forgets_at_once(gdr_lib, A):
+    """The decode token: a step above 0 forgets, a step of 0 (dt at minus
+    infinity, a padded sequence) keeps the state bit for bit."""
+    a, _, _ = forgetting(3, 2, 1, 70, 16, BF)
+    a[2][:, 0] = A
+    a[1][1] = float("-inf")
+    h = a[8].clone()
+    st = [v[:, 0] if k in (0, 1, 3, 4, 6) else v for k, v in enumerate(a)]
+    y = gdr_lib.gdr_ssm_step(*st[:5], h, *st[5:8], out_dtype=F32)
+    torch.cuda.synchronize()
+    assert torch.equal(h[1], a[8][1]) and torch.isfinite(y).all()
+    ref = [n64(v[:1]) if k in (0, 1, 3, 4, 6, 8) else n64(v) for k, v in enumerate(a)]
+    ref[2] = np.maximum(ref[2], -1e30)
+    want, wh, _ = R.scan_fwd(*ref)
+    my, mh, _ = R.scan_fwd(*ref, majorant=True)
+    close("y", y[:1].unsqueeze(1), want, R.scan_bound(my, 1, "f32", want))
+    close("h", h[:1], wh, R.scan_bound(mh, 1))
+
+
+def test_scan_of_a_rate_that_is_no_number(gdr_lib):
+    """NaN in A is not taken for a value: it reaches its channel, and no other."""
+    a, _, _ = forgetting(4, 2, 50, 70, 16, BF)
+    want, hw = gdr_lib.gdr_ssm_scan_fwd(*a)
+    a[2][7, 2] = float("nan")
+    y, h = gdr_lib.gdr_ssm_scan_fwd(*a)
+    torch.cuda.synchronize()
+    other = torch.arange(70, device="cuda") != 7
+    assert torch.equal(y[..., other], want[..., other]) and torch.isnan(y[..., 7]).all()
+    assert torch.equal(h[:, other], hw[:, other]) and torch.isnan(h[:, 7, 2]).all()
