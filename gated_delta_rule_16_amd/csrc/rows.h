@@ -83,6 +83,38 @@ template <int E, bool BF16, bool RAG> struct Row {
         }
     }
 
+    // The same channels to memory, bit for bit (a store of the unpacked values
+    // would make signalling NaNs quiet).
+    __device__ __forceinline__ void copy_to(void* base, int64_t off, int valid) const {
+        static_assert(E == 4 || E == 8, "group size");
+        if (valid >= E) {
+            if constexpr (BF16) {
+                bf16_t* q = static_cast<bf16_t*>(base) + off;
+                if constexpr (E == 8)
+                    *reinterpret_cast<u32x4_e2*>(q) = u32x4_e2{w[0], w[1], w[2], w[3]};
+                else
+                    *reinterpret_cast<u32x2_e2*>(q) = u32x2_e2{w[0], w[1]};
+            } else {
+                uint32_t* q = static_cast<uint32_t*>(base) + off;
+#pragma unroll
+                for (int i = 0; i < E; i += 4)
+                    *reinterpret_cast<u32x4_e4*>(q + i) =
+                        u32x4_e4{w[i], w[i + 1], w[i + 2], w[i + 3]};
+            }
+        }
+        if constexpr (RAG) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                if (valid < E && e < valid) {
+                    if constexpr (BF16)
+                        static_cast<bf16_t*>(base)[off + e] = (bf16_t)p[e];
+                    else
+                        static_cast<uint32_t*>(base)[off + e] = p[e];
+                }
+            }
+        }
+    }
+
     __device__ __forceinline__ void unpack(float (&f)[E]) const {
 #pragma unroll
         for (int e = 0; e < E; ++e) {

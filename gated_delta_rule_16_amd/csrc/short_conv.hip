@@ -103,11 +103,8 @@ __global__ __launch_bounds__(256) void conv_fwd_kernel(ConvArgs a, int64_t ncb, 
 #pragma unroll
             for (int m = 0; m < K - 1; ++m) load_in(f[m], a, b, a.T - (K - 1) + m, c, valid);
 #pragma unroll
-            for (int m = 0; m < K - 1; ++m) {
-                float v[E];
-                f[m].unpack(v);
-                row_store<E, RAG>(a.s_final, (b * (K - 1) + m) * a.C + c, BF16, v, valid);
-            }
+            for (int m = 0; m < K - 1; ++m)
+                f[m].copy_to(a.s_final, (b * (K - 1) + m) * a.C + c, valid);
         }
     }
     for (int64_t t = t0; t < t1; t += FWD_TOKENS) {
@@ -163,7 +160,7 @@ __global__ __launch_bounds__(256) void conv_step_kernel(ConvArgs a, int64_t ncg)
     row_store<SE>(a.y, b * a.C + c, a.out_bf16, y, valid);
 #pragma unroll
     for (int j = 0; j < K - 1; ++j)
-        row_store<SE>(a.s_final, (b * (K - 1) + j) * a.C + c, BF16, x[j + 1], valid);
+        r[j + 1].copy_to(a.s_final, (b * (K - 1) + j) * a.C + c, valid);
 }
 
 constexpr int BE = 4;             // backward: channels per lane

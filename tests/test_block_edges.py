@@ -157,3 +157,45 @@ def test_scan_of_a_rate_that_is_no_number(gdr_lib):
     other = torch.arange(70, device="cuda") != 7
     assert torch.equal(y[..., other], want[..., other]) and torch.isnan(y[..., 7]).all()
     assert torch.equal(h[:, other], hw[:, other]) and torch.isnan(h[:, 7, 2]).all()
+
+
+# ---- the convolution's state is a copy ------------------------------------------------
+
+
+@pytest.mark.parametrize("C", [8192, 5000, 259, 6])
+@pytest.mark.parametrize("K", [2, 4])
+def test_conv_state_keeps_every_bit(gdr_lib, C, K):
+    """Every bit pattern of bf16 (signalling NaNs among them) goes through the
+    state as it is: from x, from the old state, and one token at a time."""
+    n = K - 1
+    B = -(-65536 // (n * C))
+    bits = torch.arange(B * n * C, dtype=torch.int32, device="cuda").to(torch.int16)
+    rows = bits.view(B, n, C).view(BF)
+    w = draw(5)(C, K)
+    x = torch.cat([torch.zeros(B, 5, C, dtype=BF, device="cuda"), rows], 1)
+    _, sf = gdr_lib.gdr_short_conv_fwd(x, w)
+    _, kept = gdr_lib.gdr_short_conv_fwd(x[:, :1], w, s0=rows)
+    st = torch.zeros_like(rows)
+    held = rows.clone()
+    for t in range(n):
+        gdr_lib.gdr_short_conv_step(rows[:, t], w, None, st)
+    gdr_lib.gdr_short_conv_fwd(x[:, :1], w, s0=held, s_final=held)
+    torch.cuda.synchronize()
+
+    def same(a, b):
+        return torch.equal(a.contiguous().view(torch.int16), b.contiguous().view(torch.int16))
+
+    assert same(sf, rows) and same(st, rows)
+    if n > 1:
+        assert same(kept[:, :n - 1], rows[:, 1:]) and same(held[:, :n - 1], rows[:, 1:])
+
+
+def test_conv_state_keeps_every_bit_in_fp32(gdr_lib):
+    word = torch.tensor([0x7f800001, 0x7fc12345, 1, 0x007fffff, -1, -0x7fffffff, -0x400001],
+                        dtype=torch.int32, device="cuda").repeat(5).view(1, 1, 35)
+    x, w = word.view(F32), draw(6)(35, 2)
+    _, sf = gdr_lib.gdr_short_conv_fwd(x, w)
+    st = torch.zeros_like(x)
+    gdr_lib.gdr_short_conv_step(x[:, 0], w, None, st)
+    torch.cuda.synchronize()
+    assert torch.equal(sf.view(torch.int32), word) and torch.equal(st.view(torch.int32), word)
