@@ -226,6 +226,7 @@ extern "C" gdr_status_t gdr_layer_norm_fwd(int64_t R, int64_t C, gdr_dtype_t in_
     if (!elem_ok(x, elem(in_dt)) || !elem_ok(y, elem(out_dt)) || !opt_elem(w, 4) ||
         !opt_elem(b, 4) || !opt_elem(res, elem(res_dt)) || (res && !elem_ok(h, elem(res_dt))))
         return GDR_ERR_INVALID;
+    if (norm_fwd_work_items(R, C) > (double)kMaxWorkItems) return GDR_ERR_INVALID;
     if (!apart(y, {res, h}) || !apart(h, {x})) return GDR_ERR_INVALID;
     if (y == x && (in_dt != out_dt || x_stride != C)) return GDR_ERR_INVALID;
     if (res && h == res && res_stride != C) return GDR_ERR_INVALID;

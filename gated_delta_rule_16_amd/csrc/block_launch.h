@@ -96,6 +96,7 @@ size_t conv_bwd_workspace_bytes(int64_t B, int64_t T, int64_t C, int64_t K);
 int64_t conv_workgroups(int64_t B, int64_t T, int64_t C);
 hipError_t launch_norm_fwd(const NormArgs& a);
 hipError_t launch_norm_bwd(const NormBwdArgs& a);
+double norm_fwd_work_items(int64_t R, int64_t C);
 size_t norm_bwd_workspace_bytes(int64_t R, int64_t C);
 int64_t ssm_padded_states(int64_t N);
 int64_t ssm_most_segments(int64_t T);

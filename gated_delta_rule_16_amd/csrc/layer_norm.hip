@@ -519,6 +519,9 @@ int64_t bwd_rows(int64_t R, int64_t C) {
     return n < most ? n : most;
 }
 
+// Whether a workgroup of eight waves takes a row.
+bool wide(int64_t C) { return fits(C) && C > 8192; }
+
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 template <int NV, int WR, bool BF16, int RES>
@@ -541,7 +544,7 @@ void fwd_t(const NormArgs& a) {
     else if (C <= 1024) fwd_r<2, 1, BF16, RES>(a, wave);
     else if (C <= 2048) fwd_r<4, 1, BF16, RES>(a, wave);
     else if (C <= 4096) fwd_r<2, 4, BF16, RES>(a, wg);
-    else if (C <= 8192) fwd_r<4, 4, BF16, RES>(a, wg);
+    else if (!wide(C)) fwd_r<4, 4, BF16, RES>(a, wg);
     else fwd_r<4, 8, BF16, RES>(a, wg);
 }
 
@@ -571,7 +574,7 @@ void bwd_t(const NormBwdArgs& a) {
         else if (C <= 1024) bwd_r<2, 1, BF16, DY16, G16>(a, grid);
         else if (C <= 2048) bwd_r<1, 4, BF16, DY16, G16>(a, grid);
         else if (C <= 4096) bwd_r<2, 4, BF16, DY16, G16>(a, grid);
-        else if (C <= 8192) bwd_r<4, 4, BF16, DY16, G16>(a, grid);
+        else if (!wide(C)) bwd_r<4, 4, BF16, DY16, G16>(a, grid);
         else bwd_r<4, 8, BF16, DY16, G16>(a, grid);
     } else {
         const int64_t ncb = cdiv(C, 64 * E);
@@ -597,6 +600,12 @@ void bwd_b(const NormBwdArgs& a) {
 }
 
 }  // namespace
+
+// Work-items of the forward, a workgroup per row (or fewer: one wave up to 2048
+// channels).
+double norm_fwd_work_items(int64_t R, int64_t C) {
+    return (double)R * (wide(C) ? threads(8) : threads(1));
+}
 
 // Workspace: the partials of dw and db [bwd_rows][2 C], and each row's mean and
 // rstd where the row is not held in registers.

@@ -21,8 +21,10 @@ extern "C" {
  *     A stride is in [0, 2^40].  Everything without a stride is contiguous;
  *   - every pointer needs only its element's alignment (workspaces 16 bytes);
  *   - sizes are free: channels, lengths and states of any count within the
- *     stated limits, no multiple of anything.  A launch has at most 2^24
- *     workgroups (layer norm: one per row or fewer); larger calls are refused;
+ *     stated limits, no multiple of anything.  A launch has fewer than 2^32
+ *     work-items, in workgroups of 256 (the scan's of up to 512); larger calls
+ *     are refused.  Layer norm counts a workgroup per row, forward of 512 from
+ *     8193 to 16384 channels: fewer than 2^24 rows, there fewer than 2^23;
  *   - the gradients of activations are written in grad_dt (GDR_F32 or
  *     GDR_BF16), those of parameters and states in fp32.  Every sum runs in a
  *     fixed order: equal calls give equal bits;
