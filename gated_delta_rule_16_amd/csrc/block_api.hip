@@ -16,11 +16,18 @@ size_t elem(gdr_dtype_t d) { return d == GDR_BF16 ? 2 : 4; }
 // NULL, or aligned to its element.
 bool opt_elem(const void* p, size_t bytes) { return !p || elem_ok(p, bytes); }
 
-// Whether `out` starts at none of the tensors `others` (NULL ones aside): what a
-// call cannot do in place it refuses.
-bool apart(const void* out, std::initializer_list<const void*> others) {
-    for (const void* p : others)
-        if (out && p == out) return false;
+using Ptrs = std::initializer_list<const void*>;
+
+// Whether none of the outputs starts at an input or at another output (NULL ones
+// aside): what a call cannot do in place it refuses.
+bool apart(Ptrs outs, Ptrs ins) {
+    for (const void* const* o = outs.begin(); o != outs.end(); ++o) {
+        if (!*o) continue;
+        for (const void* p : ins)
+            if (p == *o) return false;
+        for (const void* const* q = outs.begin(); q != o; ++q)
+            if (*q == *o) return false;
+    }
     return true;
 }
 
@@ -85,7 +92,7 @@ extern "C" gdr_status_t gdr_short_conv_fwd(int64_t B, int64_t T, int64_t C, int6
         return s_final ? copy_or_zero(s0, s_final, B * (K - 1) * C * (int64_t)ie, stream) : GDR_OK;
     if (!elem_ok(x, ie) || !elem_ok(y, elem(out_dt)) || !elem_ok(w, 4) || !opt_elem(bias, 4))
         return GDR_ERR_INVALID;
-    if (!apart(y, {x, s0, s_final}) || !apart(s_final, {x})) return GDR_ERR_INVALID;
+    if (!apart({y, s_final}, {x, w, bias}) || !apart({y}, {s0})) return GDR_ERR_INVALID;
     if (!workgroups_ok((double)conv_workgroups(B, T, C))) return GDR_ERR_INVALID;
     ConvArgs a{};
     a.B = B;
@@ -117,7 +124,7 @@ extern "C" gdr_status_t gdr_short_conv_step(int64_t N, int64_t C, int64_t K, gdr
     if (!elem_ok(x, elem(in_dt)) || !elem_ok(state, elem(in_dt)) || !elem_ok(y, elem(out_dt)) ||
         !elem_ok(w, 4) || !opt_elem(bias, 4))
         return GDR_ERR_INVALID;
-    if (!apart(y, {x, state}) || !apart(state, {x})) return GDR_ERR_INVALID;
+    if (!apart({y, state}, {x, w, bias})) return GDR_ERR_INVALID;
     if (!workgroups_ok((double)N * (double)((C + 3) / 4) / 256.0 + 1.0)) return GDR_ERR_INVALID;
     ConvArgs a{};
     a.B = N;
@@ -170,8 +177,9 @@ extern "C" gdr_status_t gdr_short_conv_bwd(int64_t B, int64_t T, int64_t C, int6
     if (!elem_ok(x, ie) || !elem_ok(w, 4) || !opt_elem(bias, 4) || !opt_elem(s0, ie) ||
         !elem_ok(dy, elem(dy_dt)) || !elem_ok(dx, elem(grad_dt)))
         return GDR_ERR_INVALID;
-    if (!apart(dx, {x, dy, s0}) || !apart(ds0, {ds_final, dx})) return GDR_ERR_INVALID;
     const bool sums = dw || dbias;
+    if (!apart({dx, dw, dbias, ds0, sums ? workspace : nullptr}, {x, w, bias, s0, dy, ds_final}))
+        return GDR_ERR_INVALID;
     if (sums && (!ptrs_ok({workspace}) ||
                  workspace_bytes < conv_bwd_workspace_bytes(B, T, C, K)))
         return GDR_ERR_INVALID;
@@ -227,7 +235,10 @@ extern "C" gdr_status_t gdr_layer_norm_fwd(int64_t R, int64_t C, gdr_dtype_t in_
         !opt_elem(b, 4) || !opt_elem(res, elem(res_dt)) || (res && !elem_ok(h, elem(res_dt))))
         return GDR_ERR_INVALID;
     if (norm_fwd_work_items(R, C) > (double)kMaxWorkItems) return GDR_ERR_INVALID;
-    if (!apart(y, {res, h}) || !apart(h, {x})) return GDR_ERR_INVALID;
+    // y may be x and h may be res
+    if (!apart({y, res ? h : nullptr}, {w, b}) || !apart({y}, {res}) ||
+        (res && !apart({h}, {x})))
+        return GDR_ERR_INVALID;
     if (y == x && (in_dt != out_dt || x_stride != C)) return GDR_ERR_INVALID;
     if (res && h == res && res_stride != C) return GDR_ERR_INVALID;
     NormArgs a{};
@@ -276,8 +287,11 @@ extern "C" gdr_status_t gdr_layer_norm_bwd(int64_t R, int64_t C, gdr_dtype_t in_
     if (!elem_ok(x, elem(in_dt)) || !elem_ok(dy, elem(dy_dt)) || !elem_ok(dx, elem(grad_dt)) ||
         !opt_elem(w, 4) || !opt_elem(dres, elem(grad_dt)))
         return GDR_ERR_INVALID;
-    if (!apart(dx, {x, dy}) || (dres && dx == dres && dres_stride != C)) return GDR_ERR_INVALID;
     const bool sums = dw || db;
+    const void* const ws = sums ? workspace : nullptr;
+    if (!apart({dx, dw, db, ws}, {x, w, dy}) || !apart({dw, db, ws}, {dres}) ||
+        (dres && dx == dres && dres_stride != C))
+        return GDR_ERR_INVALID;
     if (sums && (!ptrs_ok({workspace}) || workspace_bytes < norm_bwd_workspace_bytes(R, C)))
         return GDR_ERR_INVALID;
     NormBwdArgs a{};
@@ -378,11 +392,13 @@ extern "C" gdr_status_t gdr_ssm_scan_fwd(int64_t B, int64_t T, int64_t D, int64_
     if (T == 0) return h_final ? copy_or_zero(h0, h_final, B * D * N * 4, stream) : GDR_OK;
     if (!ssm_ptrs_ok(in_dt, x, dt, A, Bm, Cm, D_skip, z, dt_bias) || !elem_ok(y, elem(out_dt)))
         return GDR_ERR_INVALID;
-    if (!apart(y, {x, dt, Bm, Cm, z, h0, h_final})) return GDR_ERR_INVALID;
     const SsmPlan p = ssm_fwd_plan(B, T, D, G, N);
     if (!workgroups_ok(2.0 * B * G * p.nblk * p.nseg)) return GDR_ERR_INVALID;   // 512 threads each
     const size_t need = ssm_fwd_workspace_bytes(B, T, D, G, N);
     if (need && (!ptrs_ok({workspace}) || workspace_bytes < need)) return GDR_ERR_INVALID;
+    const void* const ws = need ? workspace : nullptr;
+    if (!apart({y, h_final, ws}, {x, dt, A, Bm, Cm, D_skip, z, dt_bias}) || !apart({y, ws}, {h0}))
+        return GDR_ERR_INVALID;
     SsmArgs a{};
     ssm_fill(a, B, T, D, G, N, in_dt, x, dt, A, Bm, Cm, D_skip, z, dt_bias, h0, flags, strides);
     a.out_bf16 = out_dt == GDR_BF16;
@@ -405,7 +421,7 @@ extern "C" gdr_status_t gdr_ssm_step(int64_t Nseq, int64_t D, int64_t G, int64_t
     if (!ssm_ptrs_ok(in_dt, x, dt, A, Bm, Cm, D_skip, z, dt_bias) || !elem_ok(state, 4) ||
         !elem_ok(y, elem(out_dt)))
         return GDR_ERR_INVALID;
-    if (!apart(y, {x, dt, Bm, Cm, z, state})) return GDR_ERR_INVALID;
+    if (!apart({y, state}, {x, dt, A, Bm, Cm, D_skip, z, dt_bias})) return GDR_ERR_INVALID;
     if (!workgroups_ok((double)ssm_step_workgroups(Nseq, D, N))) return GDR_ERR_INVALID;
     int64_t s[10];
     for (int i = 0; strides && i < 5; ++i) {
@@ -458,10 +474,9 @@ extern "C" gdr_status_t gdr_ssm_scan_bwd(int64_t B, int64_t T, int64_t D, int64_
         !elem_ok(dout, elem(dout_dt)) || !elem_ok(dx, ge) || !elem_ok(ddt, ge) ||
         !elem_ok(dB, ge) || !elem_ok(dC, ge) || (z && !elem_ok(dz, ge)))
         return GDR_ERR_INVALID;
-    for (const void* o : {(const void*)dx, (const void*)ddt, (const void*)dB, (const void*)dC,
-                          (const void*)dz})
-        if (!apart(o, {x, dt, Bm, Cm, z, dout})) return GDR_ERR_INVALID;
-    if (!apart(dh0, {h0, dh_final})) return GDR_ERR_INVALID;
+    if (!apart({dx, ddt, dA, dB, dC, dD, z ? dz : nullptr, ddt_bias, dh0, workspace},
+               {x, dt, A, Bm, Cm, D_skip, z, dt_bias, h0, dout, dh_final}))
+        return GDR_ERR_INVALID;
     if (!workgroups_ok((double)ssm_bwd_workgroups(B, T, D, G, N))) return GDR_ERR_INVALID;
     if (!ptrs_ok({workspace}) || workspace_bytes < ssm_bwd_workspace_bytes(B, T, D, G, N))
         return GDR_ERR_INVALID;

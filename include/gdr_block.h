@@ -28,8 +28,9 @@ extern "C" {
  *   - the gradients of activations are written in grad_dt (GDR_F32 or
  *     GDR_BF16), those of parameters and states in fp32.  Every sum runs in a
  *     fixed order: equal calls give equal bits;
- *   - outputs must not overlap inputs or each other unless a call says so (an
- *     output at an input's address is then refused);
+ *   - outputs and workspaces must not overlap inputs or each other unless a
+ *     call says so.  One that starts where an input or another of them starts
+ *     is refused; the caller sees to the rest;
  *   - the device of the tensors must be the current device.
  */
 

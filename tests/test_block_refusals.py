@@ -13,3 +13,48 @@ def test_norm_of_more_rows_than_a_launch_holds(gdr, R, C):
     """A workgroup per row, of 512 threads from 8193 to 16384 channels: 2^32
     work-items are refused, not handed to a launch that fails."""
     assert norm(gdr, R=R, C=C, xs=C, y=B16) == 1
+
+
+# ---- an output (or the workspace) where another tensor of the call starts -------------
+#
+# Every tensor has an address of its own, all arguments are valid, and one output
+# at a time is put on each other tensor in turn.
+
+
+def at(names):
+    return {n: A16 + 4096 * (k + 1) for k, n in enumerate(names.split())}
+
+
+CALLS = {
+    # call, fixed arguments, inputs, outputs, pairs that may be one buffer
+    "conv": (conv, dict(), "x w b s0", "y sf", {("sf", "s0")}),
+    "conv_step": (conv_step, dict(), "x w b", "s y", set()),
+    "conv_bwd": (conv_bwd, dict(), "x w b s0 dy dsf", "dx dw db ds0 ws", set()),
+    "norm": (norm, dict(rs=16), "x r w b", "y h", {("y", "x"), ("h", "r")}),
+    "norm_bwd": (norm_bwd, dict(rs=16), "x w dy dr", "dx dw db ws", {("dx", "dr")}),
+    # 512 tokens of 16 channels: segments, and a workspace
+    "scan": (scan, dict(T=512, nb=1 << 40), "x d A Bm Cm D_ z b h0", "y hf ws", {("hf", "h0")}),
+    "step": (step, dict(), "x d A Bm Cm D_ z b", "s y", set()),
+    "scan_bwd": (scan_bwd, dict(), "x d A Bm Cm D_ z b h0 do dh",
+                 "dx dd dA dB dC dD dz db dh0 ws", set()),
+}
+
+
+def pairs():
+    for name, (_, _, ins, outs, same) in CALLS.items():
+        for o in outs.split():
+            for p in (ins + " " + outs).split():
+                if o != p and (o, p) not in same:
+                    yield name, o, p
+
+
+@pytest.mark.parametrize("name,out,other", list(pairs()))
+def test_outputs_on_other_tensors(gdr, name, out, other):
+    call, kw, ins, outs, _ = CALLS[name]
+    where = at(ins + " " + outs)
+    where[out] = where[other]
+    assert call(gdr, **{**kw, **where}) == 1
+
+
+def test_the_workspace_of_segments_is_needed(gdr):
+    assert gdr.gdr_ssm_scan_fwd_workspace_size(1, 512, 16, 1, 16) > 0
