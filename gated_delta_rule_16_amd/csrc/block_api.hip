@@ -145,8 +145,16 @@ extern "C" gdr_status_t gdr_short_conv_step(int64_t N, int64_t C, int64_t K, gdr
     return from_hip(launch_conv_step(a));
 }
 
+// The second launch of the convolution's backward: up to 1024 threads for 64
+// columns.
+static bool conv_sums_ok(int64_t C, int64_t K) {
+    return workgroups_ok((double)C * (double)(K + 1) / 16.0);
+}
+
 extern "C" size_t gdr_short_conv_bwd_workspace_size(int64_t B, int64_t T, int64_t C, int64_t K) {
-    if (B <= 0 || T <= 0 || C <= 0 || K < 2 || K > 4 || !conv_sizes_ok(B, T, C)) return 0;
+    if (B <= 0 || T <= 0 || C <= 0 ||
+        conv_check(B, T, C, K, GDR_F32, GDR_F32, 0) != GDR_OK || !conv_sums_ok(C, K))
+        return 0;
     return conv_bwd_workspace_bytes(B, T, C, K);
 }
 
@@ -183,8 +191,7 @@ extern "C" gdr_status_t gdr_short_conv_bwd(int64_t B, int64_t T, int64_t C, int6
     if (sums && (!ptrs_ok({workspace}) ||
                  workspace_bytes < conv_bwd_workspace_bytes(B, T, C, K)))
         return GDR_ERR_INVALID;
-    // the second launch: up to 1024 threads for 64 columns
-    if (sums && !workgroups_ok((double)C * (double)(K + 1) / 16.0)) return GDR_ERR_INVALID;
+    if (sums && !conv_sums_ok(C, K)) return GDR_ERR_INVALID;
     ConvArgs a{};
     a.B = B;
     a.T = T;
@@ -261,7 +268,7 @@ extern "C" gdr_status_t gdr_layer_norm_fwd(int64_t R, int64_t C, gdr_dtype_t in_
 }
 
 extern "C" size_t gdr_layer_norm_bwd_workspace_size(int64_t R, int64_t C) {
-    if (R <= 0 || C <= 0 || C > GDR_NORM_MAX_C || !sizes_ok(R, C, 1)) return 0;
+    if (R <= 0 || C <= 0 || norm_check(R, C, GDR_F32, GDR_F32, GDR_F32, 0.f) != GDR_OK) return 0;
     return norm_bwd_workspace_bytes(R, C);
 }
 
@@ -441,6 +448,7 @@ extern "C" gdr_status_t gdr_ssm_step(int64_t Nseq, int64_t D, int64_t G, int64_t
 extern "C" size_t gdr_ssm_scan_bwd_workspace_size(int64_t B, int64_t T, int64_t D, int64_t G,
                                                   int64_t N) {
     if (!ssm_sizes_ok(B, T, D, G, N) || N > GDR_SSM_MAX_N || B == 0 || D == 0 || T == 0) return 0;
+    if (!workgroups_ok((double)ssm_bwd_workgroups(B, T, D, G, N))) return 0;
     return ssm_bwd_workspace_bytes(B, T, D, G, N);
 }
 

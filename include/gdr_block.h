@@ -153,7 +153,7 @@ gdr_status_t gdr_ssm_step(int64_t Nseq, int64_t D, int64_t G, int64_t N,
  * Without channels (D == 0) nothing is launched, as in every call: dB and dC,
  * which have elements even then, are the caller's to clear.  The states are
  * run again from the inputs; the workspace holds one state in 8 or 16 tokens
- * and the partial sums.
+ * and the partial sums.  Its size is 0 for arguments the call rejects.
  */
 size_t gdr_ssm_scan_bwd_workspace_size(int64_t B, int64_t T, int64_t D,
                                        int64_t G, int64_t N);
@@ -203,6 +203,7 @@ gdr_status_t gdr_layer_norm_fwd(int64_t R, int64_t C, gdr_dtype_t in_dt,
  * [R, C] grad_dt, the gradient that reaches h past the norm, when given; dx
  * may be dres itself with dres_stride == C) and dw, db [C] fp32, each of
  * which may be NULL.  The workspace (partial sums) may be NULL when both are.
+ * Its size is 0 for arguments the call rejects.
  */
 size_t gdr_layer_norm_bwd_workspace_size(int64_t R, int64_t C);
 

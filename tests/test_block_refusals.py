@@ -58,3 +58,21 @@ def test_outputs_on_other_tensors(gdr, name, out, other):
 
 def test_the_workspace_of_segments_is_needed(gdr):
     assert gdr.gdr_ssm_scan_fwd_workspace_size(1, 512, 16, 1, 16) > 0
+
+
+@pytest.mark.parametrize("name,sizes,call,kw", [
+    ("gdr_short_conv_bwd_workspace_size", (1, 1, 1 << 28, 4), conv_bwd,
+     dict(B=1, T=1, C=1 << 28, dy=B16, dx=C16)),
+    ("gdr_short_conv_bwd_workspace_size", (1 << 31, 1 << 31, 1, 4), conv_bwd,
+     dict(B=1 << 31, T=1 << 31, C=1, dy=B16, dx=C16)),
+    ("gdr_layer_norm_bwd_workspace_size", ((1 << 24) + 1, 16), norm_bwd,
+     dict(R=(1 << 24) + 1, dy=B16, dx=C16)),
+    ("gdr_ssm_scan_bwd_workspace_size", (1 << 30, 1, 64, 1, 16), scan_bwd,
+     dict(B=1 << 30, T=1, D=64)),
+    ("gdr_ssm_scan_fwd_workspace_size", (1 << 30, 1, 64, 1, 16), scan,
+     dict(B=1 << 30, T=1, D=64, y=B16)),
+])
+def test_no_workspace_for_what_is_refused(gdr, name, sizes, call, kw):
+    """Sizes that the call refuses need no workspace, so nobody allocates one."""
+    assert getattr(gdr.lib, name)(*sizes) == 0
+    assert call(gdr, **kw) == 1
