@@ -228,6 +228,9 @@ static gdr_status_t norm_check(int64_t R, int64_t C, gdr_dtype_t a, gdr_dtype_t 
     return GDR_OK;
 }
 
+// Whether rows `stride` apart lie as the contiguous output's do (one row always).
+static bool packed(int64_t R, int64_t C, int64_t stride) { return R == 1 || stride == C; }
+
 extern "C" gdr_status_t gdr_layer_norm_fwd(int64_t R, int64_t C, gdr_dtype_t in_dt, const void* x,
                                            int64_t x_stride, gdr_dtype_t res_dt, const void* res,
                                            int64_t res_stride, const float* w, const float* b,
@@ -246,8 +249,8 @@ extern "C" gdr_status_t gdr_layer_norm_fwd(int64_t R, int64_t C, gdr_dtype_t in_
     if (!apart({y, res ? h : nullptr}, {w, b}) || !apart({y}, {res}) ||
         (res && !apart({h}, {x})))
         return GDR_ERR_INVALID;
-    if (y == x && (in_dt != out_dt || x_stride != C)) return GDR_ERR_INVALID;
-    if (res && h == res && res_stride != C) return GDR_ERR_INVALID;
+    if (y == x && (in_dt != out_dt || !packed(R, C, x_stride))) return GDR_ERR_INVALID;
+    if (res && h == res && !packed(R, C, res_stride)) return GDR_ERR_INVALID;
     NormArgs a{};
     a.R = R;
     a.C = C;
@@ -297,7 +300,7 @@ extern "C" gdr_status_t gdr_layer_norm_bwd(int64_t R, int64_t C, gdr_dtype_t in_
     const bool sums = dw || db;
     const void* const ws = sums ? workspace : nullptr;
     if (!apart({dx, dw, db, ws}, {x, w, dy}) || !apart({dw, db, ws}, {dres}) ||
-        (dres && dx == dres && dres_stride != C))
+        (dres && dx == dres && !packed(R, C, dres_stride)))
         return GDR_ERR_INVALID;
     if (sums && (!ptrs_ok({workspace}) || workspace_bytes < norm_bwd_workspace_bytes(R, C)))
         return GDR_ERR_INVALID;

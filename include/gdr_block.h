@@ -181,9 +181,10 @@ gdr_status_t gdr_ssm_scan_bwd(int64_t B, int64_t T, int64_t D, int64_t G,
  *
  *   x         [R, C] in_dt, x_stride elements from row to row
  *   res, h    [R, C] res_dt, res with res_stride; both NULL without residual.
- *             h may be res itself (with res_stride == C)
+ *             h may be res itself (with res_stride == C, or one row)
  *   w, b      [C] fp32 or NULL (ones, zeros)
- *   y         [R, C] out_dt; may be x itself (same dtype, x_stride == C)
+ *   y         [R, C] out_dt; may be x itself (same dtype, x_stride == C or one
+ *             row)
  *   eps       >= 0
  *
  * Statistics in fp32, the variance from centred values.
@@ -201,9 +202,9 @@ gdr_status_t gdr_layer_norm_fwd(int64_t R, int64_t C, gdr_dtype_t in_dt,
  * Reverse mode: x is the normalised tensor (h where a residual was added), dy
  * [R, C] dy_dt the gradient of y.  Writes dx [R, C] grad_dt (plus dres
  * [R, C] grad_dt, the gradient that reaches h past the norm, when given; dx
- * may be dres itself with dres_stride == C) and dw, db [C] fp32, each of
- * which may be NULL.  The workspace (partial sums) may be NULL when both are.
- * Its size is 0 for arguments the call rejects.
+ * may be dres itself with dres_stride == C or one row) and dw, db [C] fp32,
+ * each of which may be NULL.  The workspace (partial sums) may be NULL when
+ * both are.  Its size is 0 for arguments the call rejects.
  */
 size_t gdr_layer_norm_bwd_workspace_size(int64_t R, int64_t C);
 

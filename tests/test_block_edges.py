@@ -199,3 +199,23 @@ def test_conv_state_keeps_every_bit_in_fp32(gdr_lib):
     gdr_lib.gdr_short_conv_step(x[:, 0], w, None, st)
     torch.cuda.synchronize()
     assert torch.equal(sf.view(torch.int32), word) and torch.equal(st.view(torch.int32), word)
+
+
+# ---- one row -----------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("C", [5, 24, 2049, 9001])
+def test_one_row_of_a_wider_tensor_in_place(gdr_lib, C):
+    """A single row is contiguous whatever lies behind it: a decode step's row
+    of a wider buffer is its own output."""
+    t = draw(7)
+    wide, rwide, w = t(3, C + 16), t(3, C + 16), t(C)
+    x, r = wide[:1, :C], rwide[:1, :C]
+    y, h = gdr_lib.gdr_layer_norm_fwd(x, w, residual=r)
+    behind = wide.clone(), rwide.clone()
+    y2, h2 = gdr_lib.gdr_layer_norm_fwd(x, w, residual=r, y=x, h=r)
+    torch.cuda.synchronize()
+    assert y2 is x and h2 is r and torch.equal(y, x) and torch.equal(h, r)
+    for now, before in zip((wide, rwide), behind):
+        now[:1, :C] = before[:1, :C]
+        assert torch.equal(now, before)
