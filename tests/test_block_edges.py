@@ -219,3 +219,44 @@ def test_one_row_of_a_wider_tensor_in_place(gdr_lib, C):
     for now, before in zip((wide, rwide), behind):
         now[:1, :C] = before[:1, :C]
         assert torch.equal(now, before)
+
+
+# ---- the chain's last stage -------------------------------------------------------------
+
+
+def gate64(o, g, w, eps):
+    """The output gate, and its bound: the mean square errs by 66 U (64 squares
+    and their sum, no cancellation), its root by half of that and 8 U more,
+    sigmoid by 2 |g| U (the exponent's argument) and 6 U, five products by one
+    step each."""
+    ms = (o * o).mean(-1, keepdims=True) + eps
+    y = o / np.sqrt(ms) * (1.0 if w is None else w) * g * R.sigmoid(g)
+    return y, (33 + 8 + 6 + 5 + 2 * np.abs(g)) * R.U * np.abs(y) * 1.05 + 1e-30
+
+
+@pytest.mark.parametrize("weight", [True, False])
+def test_gate_of_a_projections_slice(gdr_lib, weight):
+    """Norm, projection, convolution, delta rule and output gate, the gate's
+    branch the projection's last columns: the gate against fp64 on the bits of
+    o and of that slice.  Neighbouring columns, or g without its sigmoid, are
+    far outside the bound."""
+    B, T, H, d, C = 2, 70, 2, 64, 96
+    t = draw(8)
+    x = gdr_lib.gdr_layer_norm_fwd(t(B, T, C, dtype=BF), t(C, scale=0.2, shift=1), t(C))
+    wide = (x.float() @ t(C, 4 * H * d, scale=C ** -0.5)).to(BF)
+    u, _ = gdr_lib.gdr_short_conv_fwd(wide[..., :3 * H * d], t(3 * H * d, 4, scale=0.6))
+    q, k, v = (s.unflatten(-1, (H, d)).contiguous() for s in u.split(H * d, -1))
+    q, k = (torch.nn.functional.normalize(s.float(), dim=-1).to(BF) for s in (q, k))
+    ab = torch.sigmoid(t(2, B, T, H) + 1)
+    o, _ = gdr_lib.gdr_chunk_fwd(q, k, v, ab[0].contiguous(), ab[1].contiguous(), None,
+                                 out_dtype=F32)
+    g = wide[..., 3 * H * d:].reshape(B * T, H, d).contiguous()
+    w = t(d, scale=0.2, shift=1) if weight else None
+    y = gdr_lib.gdr_output_gate(o.reshape(B * T, H, d), g, w, 1e-6, out_dtype=F32)
+    torch.cuda.synchronize()
+    oo, gg = n64(o).reshape(B * T, H, d), n64(g)
+    want, bound = gate64(oo, gg, n64(w), 1e-6)
+    close("gate", y, want, bound)
+    for wrong in (gate64(oo, n64(wide[..., 2 * H * d:3 * H * d]).reshape(gg.shape), n64(w), 1e-6),
+                  (want / R.sigmoid(gg), bound)):
+        assert (np.abs(n64(y) - wrong[0]) > bound).mean() > 0.9
