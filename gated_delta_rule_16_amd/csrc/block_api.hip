@@ -329,7 +329,9 @@ extern "C" gdr_status_t gdr_layer_norm_bwd(int64_t R, int64_t C, gdr_dtype_t in_
 static bool ssm_sizes_ok(int64_t B, int64_t T, int64_t D, int64_t G, int64_t N) {
     if (B < 0 || T < 0 || D < 0 || G < 1 || N < 1) return false;
     if (D % G != 0) return false;
-    // the largest tensor or workspace has at most 4 elements per state and token
+    // offsets stay far below 2^63: the kept states take at most 4 floats per
+    // state (N = 1) and 8 tokens, the partials of dB and dC at most 8 per element
+    // of Bm and block of 64 channels
     return conv_sizes_ok(B, T, D) && (double)B * (double)T * (double)D * (double)N < 1.0e16 &&
            (double)B * (double)(T + 64) * (double)G * (double)N < 1.0e16;
 }

@@ -216,8 +216,8 @@ __device__ __forceinline__ float exp_neg_abs(float x) {
 }
 
 // log(1 + e) for e in [0, 1] as e times a polynomial of degree 9 (fitted for
-// the smallest relative error over [0, 1], 5e-9 before rounding, 1.2e-7 as
-// evaluated).  Relative error stays ~2^-23 for small e, where log(1 + e)
+// the smallest relative error over [0, 1]: 1.2e-8 with these coefficients, 1.3e-7
+// as evaluated).  Relative error stays ~2^-23 for small e, where log(1 + e)
 // would lose it, and no transcendental is used.
 __device__ __forceinline__ float log1p_unit(float e) {
     float c = -0.00324386684f;

@@ -13,7 +13,7 @@
 // along the tokens of its stretch with the last K - 1 inputs in registers, so
 // every input is read once but for the K - 1 rows where stretches meet.  B 8
 // T 4096 K 4 with SiLU in bf16: forward at C 6144 162 us (5.0 TB/s), backward at
-// C 2048 94 us (4.3 TB/s); a copy reaches 4.9 on the same card.
+// C 2048 93 us (4.3 TB/s); a copy reaches 4.9 to 5.4 on the same card.
 #include "block_launch.h"
 #include "rows.h"
 

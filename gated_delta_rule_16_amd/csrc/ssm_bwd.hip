@@ -16,8 +16,8 @@
 // sums over channels (dB, dC) are halving reductions over a row's 16 lanes
 // (22 operations a token for the 8 values of a lane at NS = 4), then over the
 // workgroup's waves in LDS, and leave as one partial per workgroup, added by
-// ssm_bwd_reduce in a fixed order.  B 4 T 4096 D 2048 N 16, gated, bf16: 590 us,
-// of which the first pass 167 (vector ALU busy in all cycles), the second 400
+// ssm_bwd_reduce in a fixed order.  B 4 T 4096 D 2048 N 16, gated, bf16: 594 us,
+// of which the first pass 159 (vector ALU busy in all cycles), the second 414
 // (in 85%: the rest waits for LDS at the ends of blocks) and the sums 19.
 //
 // Segments: both passes run all segments of a sequence side by side.  The

@@ -14,14 +14,14 @@
 // broadcasts.  A tile of tokens is staged in LDS by waves that do nothing else
 // (Delta and Delta x once per channel, B and C as fp32), so the token loop has
 // no global access; two tiles' loads are in flight.  B 8 T 4096 D 2048 N 16,
-// gated, bf16: 261 us, 2.1 TB/s, with the vector ALU busy in 99% of the cycles
+// gated, bf16: 264 us, 2.0 TB/s, with the vector ALU busy in 95% of the cycles
 // (437 us where the scanning waves also staged).
 //
 // Few channels: the sequence is cut into segments that run side by side.  A
 // first pass leaves each segment's end state from zero and the sum of its
 // Delta (whose exp with A is the segment's decay); the second starts from the
 // states composed of those.  It costs a second exp per state, so it is taken
-// only where the channels alone leave most of the chip idle (ssm_fwd_segs).
+// only where the channels alone leave most of the chip idle (ssm_fwd_plan).
 #include <type_traits>
 
 #include "ssm.h"

@@ -152,8 +152,10 @@ gdr_status_t gdr_ssm_step(int64_t Nseq, int64_t D, int64_t G, int64_t N,
  * ddt_bias [D] and dh0 [B, D, N] (each of the last three may be NULL).
  * Without channels (D == 0) nothing is launched, as in every call: dB and dC,
  * which have elements even then, are the caller's to clear.  The states are
- * run again from the inputs; the workspace holds one state in 8 or 16 tokens
- * and the partial sums.  Its size is 0 for arguments the call rejects.
+ * run again from the inputs; the workspace holds one state in S tokens and the
+ * partial sums, mainly 4 B T P (D / S + 2 G ceil(D / (64 G))) bytes, where P is
+ * N rounded up to 4, 8, 16, 32 or 64 and S = 8, 8, 16, 8 or 4.  Its size is 0
+ * for arguments the call rejects.
  */
 size_t gdr_ssm_scan_bwd_workspace_size(int64_t B, int64_t T, int64_t D,
                                        int64_t G, int64_t N);
