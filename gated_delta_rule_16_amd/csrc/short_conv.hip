@@ -324,7 +324,10 @@ struct Shape {
 
 // The launch for groups of EE channels.  A stretch of TL tokens, between lo and
 // hi: long enough that the K - 1 rows read twice are few, short enough that the
-// launch fills the chip.
+// launch fills the chip: halved while it has fewer than 8192 waves.  bf16 K 4,
+// forward / backward in us with 8192, 2048 and 32768: B 8 T 4096 C 6144 163 / 260,
+// 172 / 260, 155 / 263; B 8 T 4096 C 2048 52 / 90, 47 / 90, 56 / 114; B 4 T 1024
+// C 6144 24 / 48, 20 / 37, 24 / 48: no one bound is best for all of them.
 template <int EE>
 Shape shape(int64_t B, int64_t T, int64_t C, int lo, int hi) {
     Shape s;
