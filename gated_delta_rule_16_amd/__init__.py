@@ -1,9 +1,10 @@
 """Python binding of libgdr, the gfx950 gated delta rule library.
 
 Argument marshalling only: every step of every operation runs in the HIP
-kernels behind the C ABI declared in ``include/gdr.h`` and (the operators
-around the mixer) ``include/gdr_block.h``.  PyTorch supplies device memory
-and the current HIP stream.  There is no CPU or PyTorch fallback — importing
+kernels behind the C ABI declared in ``include/gdr.h``, (the operators around
+the mixer) ``include/gdr_block.h`` and (linear attention, rotary positions, RMS
+norm) ``include/gdr_linear.h``.  PyTorch supplies device memory and the current
+HIP stream.  There is no CPU or PyTorch fallback — importing
 this package without the built ``libgdr.so`` fails.
 
 Functions mirror the C calls:
@@ -32,6 +33,16 @@ Functions mirror the C calls:
     gdr_layer_norm_fwd(x, w=None, b=None, eps=1e-5, residual=None, ...) -> y or (y, h)
     gdr_layer_norm_bwd(x, w, dy, eps=1e-5, dres=None, ...)      -> (dx, dw, db)
 
+    gdr_linear_attn_fwd(q, k, v, log_decay=None, s0=None, ...)  -> (o, s_final)
+    gdr_linear_attn_step(q, k, v, log_decay, state, ...)        -> o
+    gdr_linear_attn_bwd(q, k, v, log_decay, s0, dout, ds_final=None, ...)
+        -> (dq, dk, dv, dlog_decay, ds0)
+    gdr_rotary(q, k, positions, freqs, ...)                     -> (q', k')
+    gdr_rotary_frequencies(rot, base=10000.0, ...)              -> freqs
+    gdr_rms_norm_fwd(x, w=None, eps=1e-6, residual=None, ...)   -> y or (y, h)
+    gdr_rms_norm_quant(x, w=None, eps=1e-6, residual=None, ...) -> (q, scales) or (q, scales, h)
+    gdr_rms_norm_bwd(x, w, dy, eps=1e-6, dres=None, ...)        -> (dx, dw)
+
 ``l2norm_qk=True`` calls the ``_ex`` variant of the same C function with
 GDR_L2NORM_QK: q and k are L2-normalised on load inside the kernels.
 """
@@ -57,6 +68,10 @@ __all__ = ["gdr_chunk_fwd", "gdr_recurrent_step", "gdr2_chunk_fwd", "gdr_output_
            "gdr_ssm_scan_fwd_workspace_size", "gdr_ssm_step", "gdr_ssm_scan_bwd",
            "gdr_ssm_scan_bwd_workspace_size", "gdr_layer_norm_fwd", "gdr_layer_norm_bwd",
            "gdr_layer_norm_bwd_workspace_size",
+           "gdr_linear_attn_fwd", "gdr_linear_attn_fwd_workspace_size", "gdr_linear_attn_step",
+           "gdr_linear_attn_bwd", "gdr_linear_attn_bwd_workspace_size", "gdr_rotary",
+           "gdr_rotary_frequencies", "gdr_rms_norm_fwd", "gdr_rms_norm_quant", "gdr_rms_norm_bwd",
+           "gdr_rms_norm_bwd_workspace_size",
            "GdrError", "status_string", "lib", "LIB_PATH", "GDR_F32",
            "GDR_BF16", "GDR_L2NORM_QK", "GDR_SPLIT_FP32_STATES", "GDR_CONV_SILU",
            "GDR_SSM_SOFTPLUS", "GDR_SSM_MAX_N", "GDR_NORM_MAX_C"]
@@ -78,6 +93,12 @@ GDR_CONV_SILU = 1
 GDR_SSM_SOFTPLUS = 1
 GDR_SSM_MAX_N = 64
 GDR_NORM_MAX_C = 1048576
+GDR_LA_HEAD_DECAY = 1
+GDR_LA_MAX_D = 128
+GDR_ROTARY_INTERLEAVED = 1
+GDR_ROTARY_INVERSE = 2
+GDR_ROTARY_MAX_D = 1024
+GDR_RMS_MAX_C = 1048576
 _I64, _P, _E, _U = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_uint32
 
 lib.gdr_chunk_fwd.argtypes = [_I64] * 5 + [_E] + [_P] * 6 + [_E, _P, _P, _P]
@@ -170,6 +191,33 @@ lib.gdr_layer_norm_bwd_workspace_size.restype = ctypes.c_size_t
 lib.gdr_layer_norm_bwd.argtypes = [_I64, _I64, _E, _P, _I64, _P, _E, _P, _I64, _F, _E, _P, _I64,
                                    _P, _P, _P, _P, _Z, _P]
 lib.gdr_layer_norm_bwd.restype = ctypes.c_int
+_D = ctypes.c_double
+lib.gdr_linear_attn_fwd_workspace_size.argtypes = [_I64] * 5 + [_E]
+lib.gdr_linear_attn_fwd_workspace_size.restype = ctypes.c_size_t
+lib.gdr_linear_attn_fwd.argtypes = ([_I64] * 6 + [_E] + [_P] * 6 + [_F, _U, _E] + [_P] * 3 +
+                                    [_Z, _P])
+lib.gdr_linear_attn_fwd.restype = ctypes.c_int
+lib.gdr_linear_attn_step.argtypes = [_I64] * 5 + [_E] + [_P] * 6 + [_F, _U, _E, _P, _P]
+lib.gdr_linear_attn_step.restype = ctypes.c_int
+lib.gdr_linear_attn_bwd_workspace_size.argtypes = [_I64] * 6 + [_E]
+lib.gdr_linear_attn_bwd_workspace_size.restype = ctypes.c_size_t
+lib.gdr_linear_attn_bwd.argtypes = ([_I64] * 6 + [_E] + [_P] * 8 + [_F, _U, _E] + [_P] * 6 +
+                                    [_Z, _P])
+lib.gdr_linear_attn_bwd.restype = ctypes.c_int
+lib.gdr_rotary.argtypes = ([_I64] * 6 + [_E] + [_P] * 4 + [_I64, _I64, _P, _F, _U] + [_P] * 3)
+lib.gdr_rotary.restype = ctypes.c_int
+lib.gdr_rotary_frequencies.argtypes = [_I64, _D, _E, _D, _D, _D, _D, _P]
+lib.gdr_rotary_frequencies.restype = ctypes.c_int
+lib.gdr_rms_norm_fwd.argtypes = [_I64, _I64, _E, _P, _I64, _E, _P, _I64, _P, _F, _E, _P, _P, _P]
+lib.gdr_rms_norm_fwd.restype = ctypes.c_int
+lib.gdr_rms_norm_quant.argtypes = [_I64, _I64, _E, _P, _I64, _E, _P, _I64, _P, _F, _E, _I64, _P,
+                                   _P, _P, _P]
+lib.gdr_rms_norm_quant.restype = ctypes.c_int
+lib.gdr_rms_norm_bwd_workspace_size.argtypes = [_I64, _I64]
+lib.gdr_rms_norm_bwd_workspace_size.restype = ctypes.c_size_t
+lib.gdr_rms_norm_bwd.argtypes = [_I64, _I64, _E, _P, _I64, _P, _E, _P, _I64, _F, _E, _P, _I64, _P,
+                                 _P, _P, _Z, _P]
+lib.gdr_rms_norm_bwd.restype = ctypes.c_int
 lib.gdr_status_string.argtypes = [ctypes.c_int]
 lib.gdr_status_string.restype = ctypes.c_char_p
 lib.gdr_version.restype = ctypes.c_int
@@ -779,7 +827,7 @@ def _on_own_device(fn):
     what it allocates belongs there too."""
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
-        x = args[0] if args else kw.get("x")
+        x = args[0] if args else kw.get("x", kw.get("q"))
         if isinstance(x, torch.Tensor) and x.is_cuda:
             if stream is not None:
                 if stream.device != x.device:
@@ -1168,3 +1216,304 @@ def gdr_layer_norm_bwd(x, w, dy, eps=1e-5, *, dres=None, grad_dtype=torch.float3
         _p(dres), rr, _p(dx), _p(dw), _p(db), _p(workspace),
         0 if workspace is None else workspace.numel(), _raw_stream(dev.index)))
     return dx, dw, db
+
+
+# ---- linear attention, rotary positions, RMS norm ----------------------------------
+
+
+def _heads(name, t, dtype, shape, device, lead):
+    """Strides of the ``lead`` leading dimensions and the head's of [.., heads, d]."""
+    _like(name, t, dtype, shape, device)
+    st = t.stride()
+    if shape[-1] > 1 and st[-1] != 1 and t.numel():
+        raise ValueError(f"{name} must have contiguous channels")
+    return st[:lead + 1]
+
+
+def _la_inputs(q, k, v, log_decay, lead):
+    """Checks shared by linear attention's calls; returns (device, sizes, strides,
+    flags)."""
+    dev = _first("q", q, lead + 2)
+    _first("k", k, lead + 2)
+    _first("v", v, lead + 2)
+    Hk, Dk = q.shape[lead:]
+    H, Dv = v.shape[lead:]
+    qs = _heads("q", q, q.dtype, q.shape, dev, lead)
+    ks = _heads("k", k, q.dtype, q.shape, dev, lead)
+    vs = _heads("v", v, q.dtype, (*q.shape[:lead], H, Dv), dev, lead)
+    flags = 0
+    if log_decay is not None:
+        if isinstance(log_decay, torch.Tensor) and log_decay.dim() == 1:
+            flags = GDR_LA_HEAD_DECAY
+            _whole("log_decay", log_decay, torch.float32, (H,), dev)
+        else:
+            _whole("log_decay", log_decay, torch.float32, (*q.shape[:lead], H), dev)
+    return dev, (*q.shape[:lead], H, Hk, Dk, Dv), (*qs, *ks, *vs), flags
+
+
+def gdr_linear_attn_fwd_workspace_size(B, T, H, Dk, Dv, dtype) -> int:
+    """Bytes of device workspace gdr_linear_attn_fwd needs (0: none)."""
+    return int(lib.gdr_linear_attn_fwd_workspace_size(B, T, H, Dk, Dv, _DT[dtype]))
+
+
+@_on_own_device
+def gdr_linear_attn_fwd(q, k, v, log_decay=None, s0=None, *, scale=1.0, out_dtype=None, o=None,
+                        s_final=None, want_state=True, workspace=None, stream=None):
+    """Linear attention with a decay per head over whole sequences:
+    S_t = exp(log_decay_t) S_{t-1} + v_t k_t^T, o_t = scale S_t q_t.
+
+    q, k [B,T,Hk,Dk], v [B,T,H,Dv] in one dtype, fp32 or bf16 (batch, token and
+    head strides free), Hk dividing H; log_decay fp32 [B,T,H], or [H] for a fixed
+    decay per head, or None; s0 [B,H,Dv,Dk] fp32 or None.  Dk, Dv multiples of 8 up
+    to 128.  Returns (o [B,T,H,Dv], s_final [B,H,Dv,Dk] or None); ``s_final`` may
+    be passed in (it may be ``s0`` itself)."""
+    dev, (B, T, H, Hk, Dk, Dv), st, flags = _la_inputs(q, k, v, log_decay, 2)
+    if s0 is not None:
+        _whole("s0", s0, torch.float32, (B, H, Dv, Dk), dev)
+    odt = out_dtype or (q.dtype if o is None else o.dtype)
+    code = _dt_of("output dtype", odt)
+    o = _buffer("o", o, odt, (B, T, H, Dv), dev)
+    if s_final is not None or want_state:
+        s_final = _buffer("s_final", s_final, torch.float32, (B, H, Dv, Dk), dev, s0)
+    need = _need("gdr_linear_attn_fwd_workspace_size", B, T, H, Dk, Dv, _DT[q.dtype])
+    if need or workspace is not None:
+        workspace = _scratch(workspace, need, dev)
+    _run("gdr_linear_attn_fwd", lib.gdr_linear_attn_fwd(
+        B, T, H, Hk, Dk, Dv, _DT[q.dtype], _p(q), _p(k), _p(v), _i64s(*st), _p(log_decay), _p(s0),
+        float(scale), flags, code, _p(o), _p(s_final), _p(workspace),
+        0 if workspace is None else workspace.numel(), _raw_stream(dev.index)))
+    return o, s_final
+
+
+@_on_own_device
+def gdr_linear_attn_step(q, k, v, log_decay, state, *, scale=1.0, out_dtype=None, o=None,
+                         stream=None):
+    """One decode token of gdr_linear_attn_fwd: q, k [N,Hk,Dk], v [N,H,Dv],
+    log_decay [N,H] or [H] or None, state [N,H,Dv,Dk] fp32, moved on in place.
+    Returns o [N,H,Dv]."""
+    dev, (N, H, Hk, Dk, Dv), st, flags = _la_inputs(q, k, v, log_decay, 1)
+    _whole("state", state, torch.float32, (N, H, Dv, Dk), dev)
+    odt = out_dtype or (q.dtype if o is None else o.dtype)
+    code = _dt_of("output dtype", odt)
+    o = _buffer("o", o, odt, (N, H, Dv), dev, v)
+    _run("gdr_linear_attn_step", lib.gdr_linear_attn_step(
+        N, H, Hk, Dk, Dv, _DT[q.dtype], _p(q), _p(k), _p(v), _i64s(*st), _p(log_decay), _p(state),
+        float(scale), flags, code, _p(o), _raw_stream(dev.index)))
+    return o
+
+
+def gdr_linear_attn_bwd_workspace_size(B, T, H, Hk, Dk, Dv, dtype) -> int:
+    """Bytes of device workspace gdr_linear_attn_bwd needs."""
+    return int(lib.gdr_linear_attn_bwd_workspace_size(B, T, H, Hk, Dk, Dv, _DT[dtype]))
+
+
+@_on_own_device
+def gdr_linear_attn_bwd(q, k, v, log_decay, s0, dout, ds_final=None, *, scale=1.0,
+                        grad_dtype=torch.float32, want_ddecay=True, want_ds0=True,
+                        workspace=None, stream=None):
+    """Reverse mode of gdr_linear_attn_fwd for dL/do = ``dout`` [B,T,H,Dv] in q's
+    dtype (strides free) and dL/ds_final = ``ds_final`` [B,H,Dv,Dk] fp32 or None.
+    Returns (dq, dk [B,T,Hk,Dk], dv [B,T,H,Dv] in ``grad_dtype``, dlog_decay shaped
+    as log_decay, ds0 [B,H,Dv,Dk]), the last two fp32; dlog_decay is None without
+    log_decay or ``want_ddecay``, ds0 without ``want_ds0``."""
+    dev, (B, T, H, Hk, Dk, Dv), st, flags = _la_inputs(q, k, v, log_decay, 2)
+    if s0 is not None:
+        _whole("s0", s0, torch.float32, (B, H, Dv, Dk), dev)
+    _first("dout", dout, 4)
+    dst = _heads("dout", dout, q.dtype, (B, T, H, Dv), dev, 2)
+    if ds_final is not None:
+        _whole("ds_final", ds_final, torch.float32, (B, H, Dv, Dk), dev)
+    code = _dt_of("grad_dtype", grad_dtype)
+    dq = torch.empty(q.shape, dtype=grad_dtype, device=dev)
+    dk = torch.empty(q.shape, dtype=grad_dtype, device=dev)
+    dv = _new(dout, grad_dtype, v.shape, dev)
+    dg = torch.empty_like(log_decay) if want_ddecay and log_decay is not None else None
+    ds0 = _new(ds_final, torch.float32, (B, H, Dv, Dk), dev) if want_ds0 else None
+    workspace = _scratch(workspace, _need("gdr_linear_attn_bwd_workspace_size", B, T, H, Hk, Dk,
+                                          Dv, _DT[q.dtype]), dev)
+    _run("gdr_linear_attn_bwd", lib.gdr_linear_attn_bwd(
+        B, T, H, Hk, Dk, Dv, _DT[q.dtype], _p(q), _p(k), _p(v), _i64s(*st, *dst), _p(log_decay),
+        _p(s0), _p(dout), _p(ds_final), float(scale), flags, code, _p(dq), _p(dk), _p(dv), _p(dg),
+        _p(ds0), _p(workspace), workspace.numel(), _raw_stream(dev.index)))
+    return dq, dk, dv, dg, ds0
+
+
+_SCALINGS = {None: 0, "linear": 1, "base": 2, "parts": 3}
+
+
+def gdr_rotary_frequencies(rot, base=10000.0, *, scaling=None, factor=1.0, low=1.0, high=32.0,
+                           original=4096, device=None):
+    """The rates of ``rot`` turned channels, fp64 [rot / 2] on ``device`` (default:
+    the current GPU).  ``scaling`` for contexts ``factor`` times longer than
+    ``original`` tokens: "linear" (positions interpolated), "base" (a larger base)
+    or "parts" (interpolated below ``low`` turns in the original context, kept from
+    ``high`` on; the outputs' scale 0.1 ln(factor) + 1 that goes with it is
+    gdr_rotary's ``scale``)."""
+    if scaling not in _SCALINGS:
+        raise ValueError(f"unknown scaling {scaling!r}")
+    rot = int(rot)
+    if not 0 < rot <= GDR_ROTARY_MAX_D:
+        raise ValueError(f"rot must be in 1 .. {GDR_ROTARY_MAX_D}, got {rot}")
+    out = torch.empty(rot // 2, dtype=torch.float64)
+    _run("gdr_rotary_frequencies", lib.gdr_rotary_frequencies(
+        rot, float(base), _SCALINGS[scaling], float(factor), float(low), float(high),
+        float(original), _p(out)))
+    return out.to("cuda" if device is None else device)
+
+
+@_on_own_device
+def gdr_rotary(q, k, positions, freqs, *, interleaved=False, scale=1.0, inverse=False, q_out=None,
+               k_out=None, stream=None):
+    """Rotary positions: the first 2 len(freqs) channels of every head of q
+    [B,T,Hq,D] and k [B,T,Hk,D] (fp32 or bf16, strides free; or [N,H,D], a token per
+    sequence; k may be None) turned as pairs by position times ``freqs`` (fp64, from
+    gdr_rotary_frequencies), halves apart or ``interleaved``, and multiplied by
+    ``scale``.  ``positions``: int64 [B,T] ([N]), or [T] for all sequences, or the
+    first position as an int.  ``inverse`` turns back: the reverse mode, for the
+    outputs' gradients.  Returns (q', k') in new tensors or in ``q_out`` and
+    ``k_out``, which may be q and k themselves."""
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    lead = q.dim() - 2
+    if lead not in (1, 2):
+        raise ValueError(f"q must have 3 or 4 dimensions, got {q.dim()}")
+    dev = _first("q", q, lead + 2)
+    Hq, D = q.shape[lead:]
+    B, T = q.shape[0], (q.shape[1] if lead == 2 else 1)
+
+    def strides(name, t, heads):
+        s = _heads(name, t, q.dtype, (*q.shape[:lead], heads, D), dev, lead)
+        return s if lead == 2 else (s[0], 0, s[1])
+
+    def out(name, t, like, heads):
+        if t is None:
+            t = torch.empty((*q.shape[:lead], heads, D), dtype=q.dtype, device=dev)
+        return t, strides(name, t, heads)
+
+    qs = strides("q", q, Hq)
+    q_out, qos = out("q_out", q_out, q, Hq)
+    Hk, ks, kos = 0, (0, 0, 0), (0, 0, 0)
+    if k is not None:
+        _first("k", k, lead + 2)
+        Hk = k.shape[lead]
+        ks = strides("k", k, Hk)
+        k_out, kos = out("k_out", k_out, k, Hk)
+    elif k_out is not None:
+        raise ValueError("k_out needs k")
+    if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1:
+        raise ValueError("freqs must be a [rot / 2] tensor")
+    _whole("freqs", freqs, torch.float64, freqs.shape, dev)
+    pos, ps, start = None, 0, 0
+    if isinstance(positions, torch.Tensor):
+        pos = positions
+        if lead == 2 and pos.dim() == 1:
+            _whole("positions", pos, torch.int64, (T,), dev)
+        else:
+            _like("positions", pos, torch.int64, q.shape[:lead], dev)
+            ps = pos.stride(0)
+            if lead == 2 and T > 1 and pos.stride(1) != 1:
+                raise ValueError("positions must have contiguous tokens")
+    else:
+        start = int(positions)
+    flags = (GDR_ROTARY_INTERLEAVED if interleaved else 0) | (GDR_ROTARY_INVERSE if inverse else 0)
+    _run("gdr_rotary", lib.gdr_rotary(
+        B, T, Hq, Hk, D, 2 * freqs.shape[0], _DT[q.dtype], _p(q), _p(k),
+        _i64s(*qs, *ks, *qos, *kos), _p(pos), ps, start, _p(freqs), float(scale), flags, _p(q_out),
+        _p(k_out), _raw_stream(dev.index)))
+    return q_out, k_out
+
+
+def _rms_inputs(x, w, residual, h):
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    dev = _first("x", x, x.dim())
+    R, C, xr = _as_rows("x", x)
+    rdt, rr = x.dtype, 0
+    if residual is not None:
+        _first("residual", residual, x.dim())
+        _like("residual", residual, residual.dtype, x.shape, dev)
+        rdt, rr = residual.dtype, _as_rows("residual", residual)[2]
+        h = _buffer("h", h, rdt, x.shape, dev, residual)
+    elif h is not None:
+        raise ValueError("h needs a residual")
+    if w is not None:
+        _whole("w", w, torch.float32, (C,), dev)
+    return dev, R, C, xr, rdt, rr, h
+
+
+@_on_own_device
+def gdr_rms_norm_fwd(x, w=None, eps=1e-6, *, residual=None, out_dtype=None, y=None, h=None,
+                     stream=None):
+    """RMS norm over the last axis of x [..., C] (fp32 or bf16), after adding
+    ``residual`` (its own dtype) when given.  w [C] fp32 or None (ones).  Returns y,
+    or (y, h) with the sum h in the residual's dtype.  x and residual may be row
+    slices (one stride from row to row); ``y`` may be x and ``h`` may be residual
+    itself."""
+    dev, R, C, xr, rdt, rr, h = _rms_inputs(x, w, residual, h)
+    odt = out_dtype or (x.dtype if y is None else y.dtype)
+    code = _dt_of("output dtype", odt)
+    y = _buffer("y", y, odt, x.shape, dev, x)
+    _run("gdr_rms_norm_fwd", lib.gdr_rms_norm_fwd(
+        R, C, _DT[x.dtype], _p(x), xr, _DT[rdt], _p(residual), rr, _p(w), float(eps), code, _p(y),
+        _p(h), _raw_stream(dev.index)))
+    return y if residual is None else (y, h)
+
+
+_Q8 = {torch.float8_e4m3fn: 0, torch.int8: 1}
+
+
+@_on_own_device
+def gdr_rms_norm_quant(x, w=None, eps=1e-6, *, residual=None, group=None,
+                       out_dtype=torch.float8_e4m3fn, y=None, scales=None, h=None, stream=None):
+    """gdr_rms_norm_fwd with y in 8 bits (float8_e4m3fn or int8) and fp32 scales, one
+    per row or per ``group`` (32, 64 or 128) channels: y = q scales.  Returns (q
+    [..., C], scales [..., C / group] or [..., 1]), and h with a residual."""
+    dev, R, C, xr, rdt, rr, h = _rms_inputs(x, w, residual, h)
+    odt = out_dtype if y is None else y.dtype
+    if odt not in _Q8:
+        raise TypeError(f"unsupported output dtype {odt}")
+    if group is not None and (group not in (32, 64, 128) or C % group):
+        raise ValueError(f"group must be 32, 64 or 128 and divide {C}, got {group}")
+    y = _buffer("y", y, odt, x.shape, dev, x)
+    scales = _buffer("scales", scales, torch.float32, (*x.shape[:-1], C // group if group else 1),
+                     dev)
+    _run("gdr_rms_norm_quant", lib.gdr_rms_norm_quant(
+        R, C, _DT[x.dtype], _p(x), xr, _DT[rdt], _p(residual), rr, _p(w), float(eps), _Q8[odt],
+        group or 0, _p(y), _p(scales), _p(h), _raw_stream(dev.index)))
+    return (y, scales) if residual is None else (y, scales, h)
+
+
+def gdr_rms_norm_bwd_workspace_size(R, C) -> int:
+    """Bytes of device workspace gdr_rms_norm_bwd needs for dw."""
+    return int(lib.gdr_rms_norm_bwd_workspace_size(R, C))
+
+
+@_on_own_device
+def gdr_rms_norm_bwd(x, w, dy, eps=1e-6, *, dres=None, grad_dtype=torch.float32, want_dw=True,
+                     workspace=None, stream=None):
+    """Reverse mode of gdr_rms_norm_fwd: x [..., C] is the normalised tensor (h where
+    a residual was added), dy [..., C] the gradient of y (fp32 or bf16), ``dres``
+    [..., C] in ``grad_dtype`` or None the gradient that reaches x past the norm.
+    Returns (dx in ``grad_dtype``, dw [C] fp32), dw None without ``want_dw``."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    dev = _first("x", x, x.dim())
+    R, C, xr = _as_rows("x", x)
+    _first("dy", dy, x.dim())
+    _like("dy", dy, dy.dtype, x.shape, dev)
+    yr = _as_rows("dy", dy)[2]
+    code, rr = _dt_of("grad_dtype", grad_dtype), 0
+    if dres is not None:
+        _like("dres", dres, grad_dtype, x.shape, dev)
+        rr = _as_rows("dres", dres)[2]
+    if w is not None:
+        _whole("w", w, torch.float32, (C,), dev)
+    dx = _new(dy, grad_dtype, x.shape, dev)
+    dw = _new(w, torch.float32, (C,), dev) if want_dw else None
+    if want_dw or workspace is not None:
+        workspace = _scratch(workspace, _need("gdr_rms_norm_bwd_workspace_size", R, C), dev)
+    _run("gdr_rms_norm_bwd", lib.gdr_rms_norm_bwd(
+        R, C, _DT[x.dtype], _p(x), xr, _p(w), _DT[dy.dtype], _p(dy), yr, float(eps), code,
+        _p(dres), rr, _p(dx), _p(dw), _p(workspace), 0 if workspace is None else workspace.numel(),
+        _raw_stream(dev.index)))
+    return dx, dw

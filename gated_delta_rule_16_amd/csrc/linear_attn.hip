@@ -1,0 +1,745 @@
+// gdr_linear_attn_fwd / _bwd: linear attention with a decay per head,
+//
+//   S_t = e^{g_t} S_{t-1} + v_t k_t^T,   o_t = s S_t q_t,
+//
+// in chunks of C tokens.  With L the running sum of g inside a chunk,
+//
+//   P_ij = s (q_i . k_j) e^{L_i - L_j}  (j <= i),
+//   o_i  = sum_j P_ij v_j + s e^{L_i} S q_i,
+//   S'   = e^{L_C} S + sum_j e^{L_C - L_j} v_j k_j^T.
+//
+// The backward is the same chain three times, with the tensors in other places
+// (G_t the gradient of S_t, carried backwards in time):
+//
+//   dq_i = s sum_{j <= i} e^{L_i - L_j} (do_i . v_j) k_j + ..      from S^T, forwards
+//   dk_j = s sum_{i >= j} e^{L_i - L_j} (do_i . v_j) q_i + ..      from G^T, backwards
+//   dv_j = s sum_{i >= j} e^{L_i - L_j} (q_i . k_j) do_i + ..      from G, backwards
+//
+// and the decay's gradient is what the exponents of all pairs around a token say:
+// dg_t = sum_{i >= t} (q_i . dq_i - k_i . dk_i) + <dS_T, S_T>.
+//
+// A workgroup follows one (sequence, head) for 64 of the out channels; wave w keeps
+// the state of channels 16 w .. 16 w + 15 in registers, transposed, in the layout of
+// a product's result, which is also that of the next product's operand.
+#include "linear_chain.h"
+
+namespace gdr {
+namespace la {
+namespace {
+
+template <class P, int KD> struct Shared {
+    typename P::T x[P::C * KD], y[P::C * KD], z[P::C * ZB];
+    typename P::T p[P::NT][P::C * P::C];
+    float lh[P::C], ll[P::C], enter[P::C], leave[P::C];
+    float total;
+    int bad;
+};
+
+template <class P, int KD, bool OUT>
+__global__ __launch_bounds__(256) void chain_kernel(LaChain a) {
+    constexpr int C = P::C, NU = KD / 16, NK = KD / 32, NI = C / 16, NJ = C / 32;
+    typedef Tile<P, KD> TX;
+    typedef Tile<P, ZB> TZ;
+    typedef Tile<P, C> TP;
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    Shared<P, KD>& s = *reinterpret_cast<Shared<P, KD>*>(smem);
+
+    Place at;
+    if (!place(a, blockIdx.x, at)) return;
+    const LaJob& jb = a.job[at.job];
+    const bool back = jb.back;
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, m = lane & 15;
+    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t ta = at.seg * a.L, tb = ta + a.L < a.T ? ta + a.L : a.T;
+    const int64_t nc = (tb - ta + C - 1) / C;
+    const int64_t bh = at.b * a.H + at.h;
+    constexpr size_t es = sizeof(typename P::T);
+    const void* xb = OUT ? head_base(jb.x, at.b, at.h, es) : nullptr;
+    const void* yb = head_base(jb.y, at.b, at.h, es);
+    const void* zb = static_cast<const char*>(head_base(jb.z, at.b, at.h, es)) + at.zb * ZB * es;
+    const int zw = jb.zd - at.zb * ZB;                  // channels of z here (may exceed 64)
+    const int zc = at.zb * ZB + 16 * wv;                // this wave's first channel
+
+    // state, transposed: tile u = 2 k + h, row 4 g + r, is channel 32 k + 8 g + 4 h + r
+    // of x and y, column m channel zc + m
+    f32x4 H[NU];
+    auto hoff = [&](int u, int r) {
+        return (int64_t)(zc + m) * jb.hz + (int64_t)(32 * (u >> 1) + 8 * g + 4 * (u & 1) + r) * jb.hk;
+    };
+    auto hok = [&](int u) { return zc + m < jb.zd && 32 * (u >> 1) + 8 * g < jb.kd; };
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+        H[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (OUT && jb.h_in && hok(u)) {
+            const float* p = jb.h_in + (at.seg * a.B * a.H + bh) * a.state;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) H[u][r] = p[hoff(u, r)];
+        }
+    }
+    auto h_store = [&](float* p, float f) {
+#pragma unroll
+        for (int u = 0; u < NU; ++u)
+            if (hok(u)) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) p[hoff(u, r)] = H[u][r] * f;
+            }
+    };
+
+    Stage<P, KD> sx, sy;
+    Stage<P, ZB> sz;
+    double gl = 0.0, run = 0.0;
+    // chunk n of the chain: tokens [t0, t1), rows from the first on (back: the last)
+    auto bounds = [&](int64_t n, int64_t& t0, int& len, int64_t& first) {
+        t0 = ta + (back ? nc - 1 - n : n) * C;
+        len = (int)(tb - t0 < C ? tb - t0 : C);
+        first = back ? t0 + len - 1 : t0;
+    };
+    auto fetch = [&](int64_t n) {
+        int64_t t0, first;
+        int len;
+        bounds(n, t0, len, first);
+        const int dir = back ? -1 : 1;
+        if constexpr (OUT) sx.load(xb, first, dir, jb.x.st, len, jb.kd, tid);
+        sy.load(yb, first, dir, jb.y.st, len, jb.kd, tid);
+        sz.load(zb, first, dir, jb.z.st, len, zw, tid);
+        gl = 0.0;
+        if (tid < C && tid < len)
+            gl = decay2(a, at.b, at.h, back ? first - tid + 1 : first + tid);
+    };
+    fetch(0);
+
+    if constexpr (OUT) {
+        // tiles above the diagonal stay 0
+        for (int i = tid; i < P::NT * C * C; i += 256) (&s.p[0][0])[i] = 0;
+    }
+    for (int64_t n = 0; n < nc; ++n) {
+        int64_t t0, first;
+        int len;
+        bounds(n, t0, len, first);
+        __syncthreads();                // the last chunk's tiles are read
+        if constexpr (OUT) sx.put(s.x, tid);
+        sy.put(s.y, tid);
+        sz.put(s.z, tid);
+        if (tid == 0) s.bad = 0;
+        if (wv == 0) {
+            // running sums in 64 bits: the differences of far lower sums than their
+            // own size decide the factors behind a reset
+            double l = gl;
+#pragma unroll
+            for (int d = 1; d < C; d *= 2) {
+                const double v = __shfl_up(l, d, 64);
+                l += lane >= d ? v : 0.0;
+            }
+            const double end = __shfl(l, C - 1, 64);
+            if (lane < C) {
+                s.lh[lane] = (float)l;
+                s.ll[lane] = (float)(l - (double)(float)l);
+                s.enter[lane] = jb.inter * __builtin_amdgcn_exp2f((float)l);
+                s.leave[lane] = jb.upd * __builtin_amdgcn_exp2f((float)(end - l));
+            }
+            if (lane == 0) s.total = __builtin_amdgcn_exp2f((float)end);
+            run += end;
+        }
+        const bool mybad = OUT && sz.bad();
+        if (n + 1 < nc) fetch(n + 1);
+        __syncthreads();
+        if (mybad) s.bad = 1;
+
+        f32x4 O[NI];
+        typename P::Frag zf[NJ];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) zf[j] = TZ::col8(s.z, lane, 32 * j, 16 * wv, 4);
+        if constexpr (OUT) {
+            // P^T tiles (j <= i): row 4 g + r is j, column m is i
+            int t = 0;
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+#pragma unroll
+                for (int j = 0; j <= i; ++j, ++t) {
+                    if ((t & 3) != wv) continue;
+                    f32x4 c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int k = 0; k < NK; ++k)
+                        c = P::mma(TX::row8(s.y, 16 * j + m, 4 * k + g),
+                                   TX::row8(s.x, 16 * i + m, 4 * k + g), c);
+                    const float lh = s.lh[16 * i + m], ll = s.ll[16 * i + m];
+                    float v[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int jj = 16 * j + 4 * g + r;
+                        const float d = __builtin_amdgcn_exp2f((lh - s.lh[jj]) + (ll - s.ll[jj]));
+                        v[r] = jj <= 16 * i + m ? c[r] * d * jb.pair : 0.f;
+                    }
+                    const int jj = 16 * j + 4 * g;
+                    if constexpr (P::is_bf16) {
+                        float e[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+                        for (int q = 0; q < P::NT; ++q) {
+                            const uint32_t w0 = cvt_pk(e[0], e[1]), w1 = cvt_pk(e[2], e[3]);
+                            *reinterpret_cast<uint2*>(TP::piece(s.p[q], 16 * i + m, jj >> 3) +
+                                                      (jj & 7)) = uint2{w0, w1};
+                            e[0] -= __uint_as_float(w0 << 16);
+                            e[1] -= __uint_as_float(w0 & 0xffff0000u);
+                            e[2] -= __uint_as_float(w1 << 16);
+                            e[3] -= __uint_as_float(w1 & 0xffff0000u);
+                        }
+                    } else {
+                        *reinterpret_cast<f32x4*>(TP::piece(s.p[0], 16 * i + m, jj >> 2)) =
+                            f32x4{v[0], v[1], v[2], v[3]};
+                    }
+                }
+            // out^T (row 4 g + r: channel, column m: token) from the start state
+#pragma unroll
+            for (int i = 0; i < NI; ++i) O[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < NK; ++k) {
+                typename P::Terms ht;
+                P::split(f32x8{H[2 * k][0], H[2 * k][1], H[2 * k][2], H[2 * k][3], H[2 * k + 1][0],
+                               H[2 * k + 1][1], H[2 * k + 1][2], H[2 * k + 1][3]}, ht);
+#pragma unroll
+                for (int i = 0; i < NI; ++i)
+                    O[i] = P::mma(ht, TX::row8(s.x, 16 * i + m, 4 * k + g), O[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < NI; ++i) O[i] *= s.enter[16 * i + m];
+            __syncthreads();
+            if (s.bad == 0) {
+#pragma unroll
+                for (int i = 0; i < NI; ++i)
+#pragma unroll
+                    for (int j = 0; j <= i / 2; ++j)
+#pragma unroll
+                        for (int q = P::NT - 1; q >= 0; --q)
+                            O[i] = P::mma(zf[j], TP::row8(s.p[q], 16 * i + m, 4 * j + g), O[i]);
+            } else {
+                // a value of z that is no number must not meet the zeros of tokens
+                // before it: one by one
+                for (int i = 0; i < NI; ++i)
+                    for (int j = 0; j <= 16 * i + m; ++j) {
+                        float pv = 0.f;
+                        if constexpr (P::is_bf16) {
+                            for (int q = P::NT - 1; q >= 0; --q)
+                                pv += bf2f(*(TP::piece(s.p[q], 16 * i + m, j >> 3) + (j & 7)));
+                        } else {
+                            pv = *(TP::piece(s.p[0], 16 * i + m, j >> 2) + (j & 3));
+                        }
+                        for (int r = 0; r < 4; ++r) {
+                            const int c = 16 * wv + 4 * g + r;
+                            float zv;
+                            if constexpr (P::is_bf16)
+                                zv = bf2f(*(TZ::piece(s.z, j, c >> 3) + (c & 7)));
+                            else
+                                zv = *(TZ::piece(s.z, j, c >> 2) + (c & 3));
+                            const f32x4 old = O[0];
+                            (void)old;
+#pragma unroll
+                            for (int ii = 0; ii < NI; ++ii)
+                                if (ii == i) {
+#pragma unroll
+                                    for (int rr = 0; rr < 4; ++rr)
+                                        if (rr == r) O[ii][rr] = __builtin_fmaf(pv, zv, O[ii][rr]);
+                                }
+                        }
+                    }
+            }
+            // to memory
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int row = 16 * i + m, c = zc + 4 * g;
+                const int64_t t = back ? first - row : first + row;
+                const bool ok = row < len && c < jb.zd;
+                if (jb.dots) {
+                    float d = 0.f;
+                    if (ok) {
+                        const typename P::T* rp = static_cast<const typename P::T*>(
+                            head_base(jb.r, at.b, at.h, es)) + t * jb.r.st + c;
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            float rv;
+                            if constexpr (P::is_bf16) rv = bf2f(rp[r]);
+                            else rv = rp[r];
+                            d = __builtin_fmaf(rv, O[i][r], d);
+                        }
+                    }
+                    d += __shfl_xor(d, 16, 64);
+                    d += __shfl_xor(d, 32, 64);
+                    if (g == 0 && row < len && zc < jb.zd)
+                        jb.dots[(((int64_t)(zc >> 4) * a.B + at.b) * a.T + t) * a.H + at.h] = d;
+                }
+                if (ok) {
+                    const int64_t off = at.b * jb.ob + t * jb.ot + at.h * jb.oh + c;
+                    const float v[4] = {O[i][0], O[i][1], O[i][2], O[i][3]};
+                    row_store<4, false>(jb.out, off, jb.out_bf16, v, 4);
+                }
+            }
+        }
+        // the state at the chunk's end
+        const float tot = s.total;
+        typename P::Terms zt[NJ];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            f32x8 v = P::widen(zf[j]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] *= s.leave[32 * j + 8 * g + i];
+            P::split(v, zt[j]);
+        }
+#pragma unroll
+        for (int u = 0; u < NU; ++u) {
+            H[u] *= tot;
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+                H[u] = P::mma(TX::col8(s.y, lane, 32 * j, 32 * (u >> 1) + 4 * (u & 1), 8), zt[j],
+                              H[u]);
+        }
+        if (OUT && jb.keep) {
+            const int64_t mark = back ? t0 : t0 + len;
+            if (back ? (mark > 0 && mark % a.every == 0)
+                     : (mark < a.T ? mark % a.every == 0 : jb.keep_end))
+                h_store(jb.keep + (((mark + a.every - 1) / a.every - 1) * a.B * a.H + bh) * a.state,
+                        1.f);
+        }
+    }
+    if constexpr (OUT) {
+        if (jb.h_out && at.seg == (back ? 0 : a.nseg - 1)) {
+            float f = 1.f;
+            if (jb.end_decay) f = __builtin_amdgcn_exp2f((float)decay2(a, at.b, at.h, 0));
+            h_store(jb.h_out + bh * a.state, f);
+        }
+    } else {
+        h_store(jb.h_out + (at.seg * a.B * a.H + bh) * a.state, 1.f);
+        if (jb.seg_decay && at.zb == 0 && tid == 0)
+            jb.seg_decay[at.seg * a.B * a.H + bh] = __builtin_amdgcn_exp2f((float)run);
+    }
+}
+
+// Segments' own end states, in place, to their start states:
+// in(first) = h0, in(next) = decay in + own.
+__global__ __launch_bounds__(256) void compose_kernel(float* buf, const float* decay,
+                                                      const float* h0, int64_t BH, int64_t state,
+                                                      int64_t nseg, bool back) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= BH * state) return;
+    const int64_t bh = i / state;
+    float h = h0 ? h0[i] : 0.f;
+    for (int64_t c = 0; c < nseg; ++c) {
+        const int64_t p = back ? nseg - 1 - c : c;
+        float own = 0.f, d = 0.f;
+        if (c + 1 < nseg) {
+            own = buf[p * BH * state + i];
+            d = decay[p * BH + bh];
+        }
+        buf[p * BH * state + i] = h;
+        h = d * h + own;
+    }
+}
+
+// Sums over the heads that share one: part [rows, Hk, share, D] to out [rows, Hk, D].
+__global__ __launch_bounds__(256) void share_kernel(const float* part, void* out, bool bf16,
+                                                    int64_t n, int64_t share, int64_t D) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = i / (D / 4), c = i % (D / 4) * 4;
+        f32x4 x = {0.f, 0.f, 0.f, 0.f};
+        for (int64_t k = 0; k < share; ++k)
+            x += *reinterpret_cast<const f32x4*>(part + (row * share + k) * D + c);
+        const float v[4] = {x[0], x[1], x[2], x[3]};
+        row_store<4, false>(out, row * D + c, bf16, v, 4);
+    }
+}
+
+struct DecayGrad {
+    int64_t B, T, H, every, nblk, state;
+    int nq;                         // slots of either sum
+    const float *q, *k;             // [nq][B][T][H] sums of q . dq and k . dk
+    const float *skeep, *gkeep;     // states after, gradients before each block's end
+    const float* ds_final;
+    const float* g;
+    bool g_head;
+    float* dg;                      // [B, T, H], or per head:
+    double* part;                   // [B nblk][H]
+};
+
+// dg of one block of tokens of a (sequence, head): what all pairs across its end say,
+// <G, S> there, and the running sum of q . dq - k . dk from the end, in 64 bits.
+__global__ __launch_bounds__(256) void decay_grad_kernel(DecayGrad a) {
+    __shared__ double red[4], scan[256];
+    const int64_t id = blockIdx.x;
+    const int64_t h = id % a.H, b = id / a.H % a.B, p = id / a.H / a.B;
+    const int64_t bh = b * a.H + h;
+    const int tid = threadIdx.x;
+    const int64_t t0 = p * a.every, t1 = t0 + a.every < a.T ? t0 + a.every : a.T;
+    const float* G = p + 1 < a.nblk ? a.gkeep + (p * a.B * a.H + bh) * a.state
+                     : a.ds_final ? a.ds_final + bh * a.state : nullptr;
+    double tail = 0.0;
+    if (G) {
+        const float* S = a.skeep + (p * a.B * a.H + bh) * a.state;
+        for (int64_t i = tid; i < a.state; i += 256) tail += (double)G[i] * (double)S[i];
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) tail += __shfl_xor(tail, d, 64);
+    if ((tid & 63) == 0) red[tid >> 6] = tail;
+    __syncthreads();
+    tail = (red[0] + red[1]) + (red[2] + red[3]);
+    auto rate = [&](int64_t t) {
+        const float g = a.g_head ? a.g[h] : a.g[(b * a.T + t) * a.H + h];
+        return g < kLeast ? kLeast : g;
+    };
+    if (p + 1 < a.nblk) tail *= (double)__builtin_amdgcn_exp2f(rate(t1) * kLog2e);
+    double carry = tail, sum = 0.0;
+    for (int64_t hi = t1; hi > t0; hi -= 256) {
+        const int64_t t = hi - 1 - tid;             // thread 0: the last token
+        double e = 0.0;
+        if (t >= t0) {
+            const int64_t n = a.B * a.T * a.H, o = (b * a.T + t) * a.H + h;
+            for (int i = 0; i < a.nq; ++i) e += (double)a.q[i * n + o] - (double)a.k[i * n + o];
+        }
+        __syncthreads();
+        scan[tid] = e;
+        __syncthreads();
+        for (int d = 1; d < 256; d *= 2) {
+            const double v = tid >= d ? scan[tid - d] : 0.0;
+            __syncthreads();
+            scan[tid] += v;
+            __syncthreads();
+        }
+        if (t >= t0) {
+            // a decay of 0 has no gradient
+            const double d = rate(t) < -104.f ? 0.0 : carry + scan[tid];
+            sum += d;
+            if (a.dg) a.dg[(b * a.T + t) * a.H + h] = (float)d;
+        }
+        carry += scan[255];
+    }
+    if (a.part) {
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d, 64);
+        __syncthreads();
+        if ((tid & 63) == 0) red[tid >> 6] = sum;
+        __syncthreads();
+        if (tid == 0) a.part[(b * a.nblk + p) * a.H + h] = (red[0] + red[1]) + (red[2] + red[3]);
+    }
+}
+
+__global__ __launch_bounds__(64) void head_sum_kernel(const double* part, float* dg, int64_t n,
+                                                      int64_t H) {
+    double s = 0.0;
+    for (int64_t i = threadIdx.x; i < n; i += 64) s += part[i * H + blockIdx.x];
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) s += __shfl_xor(s, d, 64);
+    if (threadIdx.x == 0) dg[blockIdx.x] = (float)s;
+}
+
+template <class P, int KD, bool OUT> hipError_t launch_kd(const LaChain& a) {
+    int64_t per = 0;
+    for (int j = 0; j < a.njobs; ++j) per += (a.job[j].zd + ZB - 1) / ZB;
+    const int64_t grid = (a.B * a.H * a.nseg + 7) / 8 * 8 * per;
+    constexpr size_t lds = sizeof(Shared<P, KD>);
+    static_assert(lds <= 160 * 1024, "LDS");
+    hipLaunchKernelGGL((chain_kernel<P, KD, OUT>), dim3((unsigned)grid), dim3(256), lds, a.stream,
+                       a);
+    return hipGetLastError();
+}
+
+template <class P, bool OUT> hipError_t launch_p(const LaChain& a, int kd) {
+    return kd <= 64 ? launch_kd<P, 64, OUT>(a) : launch_kd<P, 128, OUT>(a);
+}
+
+// Jobs of one contraction width (all of a.job have the same side of 64).
+hipError_t launch_chain(const LaChain& a, bool out) {
+    const int kd = a.job[0].kd;
+    if (a.bf16) return out ? launch_p<Bf16, true>(a, kd) : launch_p<Bf16, false>(a, kd);
+    return out ? launch_p<F32, true>(a, kd) : launch_p<F32, false>(a, kd);
+}
+
+struct Plan {
+    int64_t L, nseg;
+};
+
+// Segments: as many as give the chip about `want` workgroups, of at least 4 chunks.
+Plan plan(int64_t T, int64_t units, int64_t want) {
+    int64_t nseg = units > 0 ? want / units : 1;
+    const int64_t most = T / 256;
+    if (nseg > most) nseg = most;
+    if (nseg < 1) nseg = 1;
+    int64_t L = (T + nseg - 1) / nseg;
+    L = (L + 63) / 64 * 64;
+    return {L, (T + L - 1) / L};
+}
+
+int64_t blocks(int64_t d) { return (d + ZB - 1) / ZB; }
+
+Plan fwd_plan(int64_t B, int64_t T, int64_t H, int64_t Dv) {
+    return plan(T, B * H * blocks(Dv), 256);
+}
+
+// Kept states are at whole numbers of `every` tokens, which divides a segment.
+Plan bwd_plan(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, int64_t& every) {
+    Plan p = plan(T, B * H * (2 * blocks(Dk) + blocks(Dv)), 512);
+    every = p.L;
+    if (p.L > 1024) {
+        p.L = (p.L + 1023) / 1024 * 1024;
+        p.nseg = (T + p.L - 1) / p.L;
+        every = 1024;
+    }
+    return p;
+}
+
+constexpr size_t up16(size_t n) { return (n + 15) / 16 * 16; }
+
+LaJob job(const LaTensor& x, const LaTensor& y, const LaTensor& z, int64_t kd, int64_t zd) {
+    LaJob j{};
+    j.x = x;
+    j.y = y;
+    j.z = z;
+    j.kd = (int)kd;
+    j.zd = (int)zd;
+    j.pair = j.inter = j.upd = 1.f;
+    return j;
+}
+
+LaChain chain(const LaArgs& a, const Plan& p) {
+    LaChain c{};
+    c.B = a.B;
+    c.T = a.T;
+    c.H = a.H;
+    c.L = p.L;
+    c.nseg = p.nseg;
+    c.every = p.L;
+    c.bf16 = a.bf16;
+    c.g = a.g;
+    c.g_head = a.g_head;
+    c.state = a.Dk * a.Dv;
+    c.stream = a.stream;
+    return c;
+}
+
+// Start states of all segments of a job (its h_in, hz and hk as for the whole
+// chain) into buf.
+hipError_t segment_states(LaChain c, LaJob j, float* buf, float* decay) {
+    const float* h0 = j.h_in;
+    j.h_in = nullptr;
+    j.h_out = buf;
+    j.seg_decay = decay;
+    j.out = nullptr;
+    j.keep = j.dots = nullptr;
+    c.njobs = 1;
+    c.job[0] = j;
+    hipError_t e = launch_chain(c, false);
+    if (e != hipSuccess) return e;
+    const int64_t n = c.B * c.H * c.state;
+    hipLaunchKernelGGL(compose_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, c.stream,
+                       buf, decay, h0, c.B * c.H, c.state, c.nseg, j.back);
+    return hipGetLastError();
+}
+
+}  // namespace
+}  // namespace la
+
+using namespace la;
+
+int64_t la_fwd_workgroups(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, bool bf16) {
+    const Plan p = fwd_plan(B, T, H, Dv);
+    const int64_t chain = (B * H * p.nseg + 7) / 8 * 8 * blocks(Dv);
+    const int64_t states = p.nseg > 1 ? (B * H * Dk * Dv + 255) / 256 : 0;
+    return chain > states ? chain : states;
+}
+
+size_t la_fwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, bool bf16) {
+    const Plan p = fwd_plan(B, T, H, Dv);
+    if (p.nseg == 1) return 0;
+    return up16(4 * (size_t)(p.nseg * B * H) * (size_t)(Dk * Dv)) + up16(4 * (size_t)(p.nseg * B * H));
+}
+
+hipError_t launch_la_fwd(const LaArgs& a) {
+    const Plan p = fwd_plan(a.B, a.T, a.H, a.Dv);
+    LaChain c = chain(a, p);
+    LaJob j = job(a.q, a.k, a.v, a.Dk, a.Dv);
+    j.pair = j.inter = a.scale;
+    j.out = a.o;
+    j.ob = a.T * a.H * a.Dv;
+    j.ot = a.H * a.Dv;
+    j.oh = a.Dv;
+    j.out_bf16 = a.out_bf16;
+    j.h_in = a.s0;
+    j.hz = a.Dk;
+    j.hk = 1;
+    if (p.nseg > 1) {
+        float* buf = static_cast<float*>(a.workspace);
+        float* decay = buf + up16(4 * (size_t)(p.nseg * a.B * a.H) * (size_t)c.state) / 4;
+        const hipError_t e = segment_states(c, j, buf, decay);
+        if (e != hipSuccess) return e;
+        j.h_in = buf;
+    }
+    j.h_out = a.s_final;
+    c.njobs = 1;
+    c.job[0] = j;
+    return launch_chain(c, true);
+}
+
+namespace {
+
+// Parts of the backward's workspace, in bytes from its start.
+struct BwdSpace {
+    size_t s, sdec, g, gdec, sk, gk, qd, kd, part, dq, dk, end;
+};
+
+BwdSpace bwd_space(const Plan& p, int64_t every, int64_t B, int64_t T, int64_t H, int64_t Hk,
+                   int64_t Dk, int64_t Dv) {
+    BwdSpace o{};
+    size_t n = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = n;
+        n += up16(bytes);
+        return at;
+    };
+    const size_t bh = (size_t)(B * H), state = 4 * (size_t)(Dk * Dv) * bh;
+    const size_t nblk = (size_t)((T + every - 1) / every);
+    o.s = take(p.nseg > 1 ? state * p.nseg : 0);
+    o.sdec = take(p.nseg > 1 ? 4 * bh * p.nseg : 0);
+    o.g = take(p.nseg > 1 ? state * p.nseg : 0);
+    o.gdec = take(p.nseg > 1 ? 4 * bh * p.nseg : 0);
+    o.sk = take(state * nblk);
+    o.gk = take(state * (nblk - 1));
+    const size_t dots = 4 * bh * (size_t)T * (size_t)((Dk + 15) / 16);
+    o.qd = take(dots);
+    o.kd = take(dots);
+    o.part = take(8 * bh * nblk);
+    const size_t heads = H != Hk ? 4 * bh * (size_t)T * (size_t)Dk : 0;
+    o.dq = take(heads);
+    o.dk = take(heads);
+    o.end = n;
+    return o;
+}
+
+}  // namespace
+
+int64_t la_bwd_workgroups(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, bool bf16) {
+    int64_t every;
+    const Plan p = bwd_plan(B, T, H, Dk, Dv, every);
+    const int64_t chain = (B * H * p.nseg + 7) / 8 * 8 * (2 * blocks(Dk) + blocks(Dv));
+    const int64_t states = (B * H * Dk * Dv + 255) / 256;
+    const int64_t sums = B * H * ((T + every - 1) / every);
+    const int64_t most = chain > states ? chain : states;
+    return most > sums ? most : sums;
+}
+
+size_t la_bwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Hk, int64_t Dk, int64_t Dv,
+                              bool bf16) {
+    int64_t every;
+    const Plan p = bwd_plan(B, T, H, Dk, Dv, every);
+    return bwd_space(p, every, B, T, H, Hk, Dk, Dv).end;
+}
+
+hipError_t launch_la_bwd(const LaArgs& a) {
+    int64_t every;
+    const Plan p = bwd_plan(a.B, a.T, a.H, a.Dk, a.Dv, every);
+    const BwdSpace w = bwd_space(p, every, a.B, a.T, a.H, a.Hk, a.Dk, a.Dv);
+    char* ws = static_cast<char*>(a.workspace);
+    auto f32 = [&](size_t at) { return reinterpret_cast<float*>(ws + at); };
+    LaChain c = chain(a, p);
+    c.every = every;
+
+    LaJob jq = job(a.dout, a.v, a.k, a.Dv, a.Dk);
+    jq.pair = jq.inter = a.scale;
+    jq.h_in = a.s0;
+    jq.hz = 1;
+    jq.hk = a.Dk;
+    LaJob jk = job(a.v, a.dout, a.q, a.Dv, a.Dk);
+    jk.back = true;
+    jk.pair = jk.upd = a.scale;
+    jk.h_in = a.ds_final;
+    jk.hz = 1;
+    jk.hk = a.Dk;
+    LaJob jv = job(a.k, a.q, a.dout, a.Dk, a.Dv);
+    jv.back = true;
+    jv.pair = jv.upd = a.scale;
+    jv.h_in = a.ds_final;
+    jv.hz = a.Dk;
+    jv.hk = 1;
+
+    hipError_t e;
+    if (p.nseg > 1) {
+        if ((e = segment_states(c, jq, f32(w.s), f32(w.sdec))) != hipSuccess) return e;
+        if ((e = segment_states(c, jv, f32(w.g), f32(w.gdec))) != hipSuccess) return e;
+        jq.h_in = f32(w.s);
+        jk.h_in = jv.h_in = f32(w.g);
+    }
+    const bool own = a.H == a.Hk;
+    jq.out = own ? a.dq : f32(w.dq);
+    jk.out = own ? a.dk : f32(w.dk);
+    for (LaJob* j : {&jq, &jk}) {
+        j->ob = a.T * a.H * a.Dk;
+        j->ot = a.H * a.Dk;
+        j->oh = a.Dk;
+        j->out_bf16 = own && a.grad_bf16;
+    }
+    jv.out = a.dv;
+    jv.ob = a.T * a.H * a.Dv;
+    jv.ot = a.H * a.Dv;
+    jv.oh = a.Dv;
+    jv.out_bf16 = a.grad_bf16;
+    jv.h_out = a.ds0;
+    jv.end_decay = true;
+    if (a.dg) {
+        jq.keep = f32(w.sk);
+        jq.keep_end = a.ds_final != nullptr;
+        jk.keep = f32(w.gk);
+        jq.r = a.q;
+        jq.dots = f32(w.qd);
+        jk.r = a.k;
+        jk.dots = f32(w.kd);
+    }
+    if ((a.Dk <= 64) == (a.Dv <= 64)) {
+        c.njobs = 3;
+        c.job[0] = jq;
+        c.job[1] = jk;
+        c.job[2] = jv;
+        if ((e = launch_chain(c, true)) != hipSuccess) return e;
+    } else {
+        c.njobs = 2;
+        c.job[0] = jq;
+        c.job[1] = jk;
+        if ((e = launch_chain(c, true)) != hipSuccess) return e;
+        c.njobs = 1;
+        c.job[0] = jv;
+        if ((e = launch_chain(c, true)) != hipSuccess) return e;
+    }
+    if (!own) {
+        const int64_t n = a.B * a.T * a.Hk * (a.Dk / 4);
+        for (int i = 0; i < 2; ++i) {
+            hipLaunchKernelGGL(share_kernel, dim3(stride_blocks(n)), dim3(256), 0, a.stream,
+                               f32(i ? w.dk : w.dq), i ? a.dk : a.dq, a.grad_bf16, n, a.H / a.Hk,
+                               a.Dk);
+            if ((e = hipGetLastError()) != hipSuccess) return e;
+        }
+    }
+    if (a.dg) {
+        DecayGrad d{};
+        d.B = a.B;
+        d.T = a.T;
+        d.H = a.H;
+        d.every = every;
+        d.nblk = (a.T + every - 1) / every;
+        d.state = c.state;
+        d.nq = (int)((a.Dk + 15) / 16);
+        d.q = f32(w.qd);
+        d.k = f32(w.kd);
+        d.skeep = f32(w.sk);
+        d.gkeep = f32(w.gk);
+        d.ds_final = a.ds_final;
+        d.g = a.g;
+        d.g_head = a.g_head;
+        d.dg = a.g_head ? nullptr : a.dg;
+        d.part = a.g_head ? reinterpret_cast<double*>(ws + w.part) : nullptr;
+        hipLaunchKernelGGL(decay_grad_kernel, dim3((unsigned)(a.B * a.H * d.nblk)), dim3(256), 0,
+                           a.stream, d);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        if (a.g_head) {
+            hipLaunchKernelGGL(head_sum_kernel, dim3((unsigned)a.H), dim3(64), 0, a.stream, d.part,
+                               a.dg, a.B * d.nblk, a.H);
+            if ((e = hipGetLastError()) != hipSuccess) return e;
+        }
+    }
+    return hipSuccess;
+}
+
+}  // namespace gdr
