@@ -95,6 +95,7 @@ GDR_SSM_MAX_N = 64
 GDR_NORM_MAX_C = 1048576
 GDR_LA_HEAD_DECAY = 1
 GDR_LA_MAX_D = 128
+GDR_LA_MAX_TOKEN_STRIDE = 8388608
 GDR_ROTARY_INTERLEAVED = 1
 GDR_ROTARY_INVERSE = 2
 GDR_ROTARY_MAX_D = 1024

@@ -82,10 +82,17 @@ gdr_status_t la_check(int64_t B, int64_t T, int64_t H, int64_t Hk, int64_t Dk, i
         return GDR_ERR_UNSUPPORTED;
     if (Dk < 8 || Dv < 8 || Dk % 8 || Dv % 8 || Dk > GDR_LA_MAX_D || Dv > GDR_LA_MAX_D)
         return GDR_ERR_UNSUPPORTED;
-    if (H > 0 && (Hk == 0 || H % Hk)) return GDR_ERR_INVALID;
+    if (H > GDR_MAX_HEADS || (H > 0 && (Hk == 0 || H % Hk))) return GDR_ERR_INVALID;
     // room for every product of sizes that the launchers form
     if (T > ((int64_t)1 << 40) || !product_ok({B, T + 1024, H, 1 << 16})) return GDR_ERR_INVALID;
     return GDR_OK;
+}
+
+// Token strides: 64 tokens of a chunk lie within 32-bit byte offsets.
+bool token_strides_ok(const int64_t* s, int n) {
+    for (int i = 0; s && i < n; ++i)
+        if (s[3 * i + 1] > GDR_LA_MAX_TOKEN_STRIDE) return false;
+    return true;
 }
 
 bool la_nothing(int64_t B, int64_t H) { return B == 0 || H == 0; }
@@ -109,7 +116,7 @@ extern "C" gdr_status_t gdr_linear_attn_fwd(int64_t B, int64_t T, int64_t H, int
                                             size_t workspace_bytes, hipStream_t stream) {
     const gdr_status_t st = la_check(B, T, H, Hk, Dk, Dv, in_dt, out_dt, flags);
     if (st != GDR_OK) return st;
-    if (!strides_ok(strides, 9)) return GDR_ERR_INVALID;
+    if (!strides_ok(strides, 9) || !token_strides_ok(strides, 3)) return GDR_ERR_INVALID;
     if (la_nothing(B, H)) return GDR_OK;
     if (!opt_elem(s0, 4) || !opt_elem(s_final, 4)) return GDR_ERR_INVALID;
     if (T == 0) return s_final ? copy_or_zero(s0, s_final, B * H * Dk * Dv, stream) : GDR_OK;
@@ -209,7 +216,7 @@ extern "C" gdr_status_t gdr_linear_attn_bwd(int64_t B, int64_t T, int64_t H, int
                                             hipStream_t stream) {
     const gdr_status_t st = la_check(B, T, H, Hk, Dk, Dv, in_dt, grad_dt, flags);
     if (st != GDR_OK) return st;
-    if (!strides_ok(strides, 12)) return GDR_ERR_INVALID;
+    if (!strides_ok(strides, 12) || !token_strides_ok(strides, 4)) return GDR_ERR_INVALID;
     if (H == 0) return GDR_OK;
     if (!opt_elem(s0, 4) || !opt_elem(ds_final, 4) || !opt_elem(ds0, 4) ||
         !opt_elem(dlog_decay, 4) || !opt_elem(log_decay, 4) || (dlog_decay && T && B && !log_decay))

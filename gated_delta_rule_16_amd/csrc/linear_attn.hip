@@ -18,9 +18,11 @@
 // and the decay's gradient is what the exponents of all pairs around a token say:
 // dg_t = sum_{i >= t} (q_i . dq_i - k_i . dk_i) + <dS_T, S_T>.
 //
-// A workgroup follows one (sequence, head) for 64 of the out channels; wave w keeps
-// the state of channels 16 w .. 16 w + 15 in registers, transposed, in the layout of
-// a product's result, which is also that of the next product's operand.
+// A workgroup of two teams follows one (sequence, head) for 64 of the out channels.
+// Team A (four waves) brings the next chunk from memory to LDS and forms its P; team
+// B carries the state: its wave w keeps channels 16 w .. 16 w + 15 in registers,
+// transposed, in the layout of a product's result, which is also that of the next
+// product's operand.  While A works on chunk n, B works on chunk n - 1.
 #include "linear_chain.h"
 
 namespace gdr {
@@ -28,19 +30,69 @@ namespace la {
 namespace {
 
 template <class P, int KD> struct Shared {
-    typename P::T x[P::C * KD], y[P::C * KD], z[P::C * ZB];
+    typename P::T x[2][P::C * KD], y[2][P::C * KD], z[2][P::C * ZB];
     typename P::T p[P::NT][P::C * P::C];
-    float lh[P::C], ll[P::C], enter[P::C], leave[P::C];
-    float total;
-    int bad;
+    float lh[2][P::C], ll[2][P::C], enter[2][P::C], leave[2][P::C];
+    float total[2];
+    int64_t bad[2];         // 1 + the last chunk with a z that is no number
 };
 
-template <class P, int KD, bool OUT>
-__global__ __launch_bounds__(256) void chain_kernel(LaChain a) {
+// Tile (i, j) of P^T (row 4 g + r: token j, column m: token i) into s.p.
+template <class P, int KD, int I, int J>
+__device__ __forceinline__ void p_tile(Shared<P, KD>& s, int buf, int lane, float scale,
+                                       const typename Tile<P, KD>::Rows& rows,
+                                       const typename P::Frag (&xf)[KD / 32]) {
+    const int g = lane >> 4, m = lane & 15;
+    f32x4 c = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < KD / 32; ++k) c = P::mma(rows.get(s.y[buf], J, k), xf[k], c);
+    const float lh = s.lh[buf][16 * I + m], ll = s.ll[buf][16 * I + m];
+    const f32x4 jh = *reinterpret_cast<const f32x4*>(&s.lh[buf][16 * J + 4 * g]);
+    const f32x4 jl = *reinterpret_cast<const f32x4*>(&s.ll[buf][16 * J + 4 * g]);
+    float v[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        v[r] = c[r] * (__builtin_amdgcn_exp2f((lh - jh[r]) + (ll - jl[r])) * scale);
+        if (I == J && 4 * g + r > m) v[r] = 0.f;
+    }
+    typedef Tile<P, P::C> TP;
+    const int to = TP::at(m, 16 * J + 4 * g) + 16 * I * P::C;
+    if constexpr (P::is_bf16) {
+#pragma unroll
+        for (int q = 0; q < P::NT; ++q) {
+            const uint32_t w0 = cvt_pk(v[0], v[1]), w1 = cvt_pk(v[2], v[3]);
+            *reinterpret_cast<uint2*>(s.p[q] + to) = uint2{w0, w1};
+            v[0] -= __uint_as_float(w0 << 16);
+            v[1] -= __uint_as_float(w0 & 0xffff0000u);
+            v[2] -= __uint_as_float(w1 << 16);
+            v[3] -= __uint_as_float(w1 & 0xffff0000u);
+        }
+    } else {
+        *reinterpret_cast<f32x4*>(s.p[0] + to) = f32x4{v[0], v[1], v[2], v[3]};
+    }
+}
+
+// Tiles (I, J0 .. J1) of P^T.
+template <class P, int KD, int I, int J0, int J1>
+__device__ __forceinline__ void p_row(Shared<P, KD>& s, int buf, int lane, float scale,
+                                      const typename Tile<P, KD>::Rows& rows) {
+    typename P::Frag xf[KD / 32];
+#pragma unroll
+    for (int k = 0; k < KD / 32; ++k) xf[k] = rows.get(s.x[buf], I, k);
+    p_tile<P, KD, I, J0>(s, buf, lane, scale, rows, xf);
+    if constexpr (J1 > J0) p_tile<P, KD, I, J0 + 1>(s, buf, lane, scale, rows, xf);
+    if constexpr (J1 > J0 + 1) p_tile<P, KD, I, J0 + 2>(s, buf, lane, scale, rows, xf);
+}
+
+// OUT: out is wanted (else the states at segments' ends alone).  GRAD: jobs may have
+// kept states and dots.
+template <class P, int KD, bool OUT, bool GRAD>
+__global__ __launch_bounds__(512) void chain_kernel(LaChain a) {
     constexpr int C = P::C, NU = KD / 16, NK = KD / 32, NI = C / 16, NJ = C / 32;
     typedef Tile<P, KD> TX;
     typedef Tile<P, ZB> TZ;
     typedef Tile<P, C> TP;
+    typedef typename P::T T;
     extern __shared__ __attribute__((aligned(16))) char smem[];
     Shared<P, KD>& s = *reinterpret_cast<Shared<P, KD>*>(smem);
 
@@ -48,25 +100,125 @@ __global__ __launch_bounds__(256) void chain_kernel(LaChain a) {
     if (!place(a, blockIdx.x, at)) return;
     const LaJob& jb = a.job[at.job];
     const bool back = jb.back;
-    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, m = lane & 15;
-    const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t ta = at.seg * a.L, tb = ta + a.L < a.T ? ta + a.L : a.T;
     const int64_t nc = (tb - ta + C - 1) / C;
     const int64_t bh = at.b * a.H + at.h;
-    constexpr size_t es = sizeof(typename P::T);
-    const void* xb = OUT ? head_base(jb.x, at.b, at.h, es) : nullptr;
-    const void* yb = head_base(jb.y, at.b, at.h, es);
-    const void* zb = static_cast<const char*>(head_base(jb.z, at.b, at.h, es)) + at.zb * ZB * es;
-    const int zw = jb.zd - at.zb * ZB;                  // channels of z here (may exceed 64)
-    const int zc = at.zb * ZB + 16 * wv;                // this wave's first channel
+    // chunk n of the chain: tokens t0 .. t0 + len - 1, rows from the first on (back:
+    // from the last)
+    auto bounds = [&](int64_t n, int64_t& t0, int& len) {
+        t0 = ta + (back ? nc - 1 - n : n) * C;
+        len = (int)(tb - t0 < C ? tb - t0 : C);
+    };
 
+    if constexpr (OUT) {
+        // tiles above the diagonal stay 0
+        for (int i = threadIdx.x; i < P::NT * C * C; i += 512) (&s.p[0][0])[i] = 0;
+        if (threadIdx.x < 2) s.bad[threadIdx.x] = 0;
+        lds_barrier();
+    }
+
+    if (wv >= 4) {
+        // ---- team A ----
+        const int tid = threadIdx.x - 256;
+        const char* xb = OUT ? static_cast<const char*>(head_base(jb.x, at.b, at.h, sizeof(T)))
+                             : nullptr;
+        const char* yb = static_cast<const char*>(head_base(jb.y, at.b, at.h, sizeof(T)));
+        const char* zb = static_cast<const char*>(head_base(jb.z, at.b, at.h, sizeof(T))) +
+                         at.zb * ZB * sizeof(T);
+        const int64_t xt = jb.x.st, yt = jb.y.st, zt = jb.z.st;
+        const float pair = jb.pair, inter = jb.inter, upd = jb.upd;
+        Stage<P, KD> sx, sy;
+        Stage<P, ZB> sz;
+        if constexpr (OUT) sx.init(tid, jb.kd, xt, back);
+        sy.init(tid, jb.kd, yt, back);
+        sz.init(tid, jb.zd - at.zb * ZB, zt, back);
+        typename TX::Rows rows;
+        rows.init(lane);
+        float gl = 0.f;
+        double run = 0.0;
+        auto fetch = [&](int64_t n) {
+            int64_t t0;
+            int len;
+            bounds(n, t0, len);
+            if (wv == 7) {
+                gl = 0.f;
+                if (lane < len)
+                    gl = decay_of(a, at.b, at.h, back ? t0 + len - lane : t0 + lane);
+            }
+            if constexpr (OUT) sx.load(xb + t0 * xt * (int)sizeof(T), xt, len, back);
+            sy.load(yb + t0 * yt * (int)sizeof(T), yt, len, back);
+            sz.load(zb + t0 * zt * (int)sizeof(T), zt, len, back);
+        };
+        fetch(0);
+        for (int64_t n = 0; n < nc; ++n) {
+            const int buf = (int)(n & 1);
+            int64_t t0;
+            int len;
+            bounds(n, t0, len);
+            if (wv == 7) {
+                // running sums in 64 bits: behind a reset, the differences of sums far
+                // larger than themselves decide the factors
+                double l = base2(gl);
+#pragma unroll
+                for (int d = 1; d < C; d *= 2) {
+                    const double v = __shfl_up(l, d, 64);
+                    l += lane >= d ? v : 0.0;
+                }
+                const double end = __shfl(l, C - 1, 64);
+                if (lane < C) {
+                    s.lh[buf][lane] = (float)l;
+                    s.ll[buf][lane] = (float)(l - (double)(float)l);
+                    s.enter[buf][lane] = inter * __builtin_amdgcn_exp2f((float)l);
+                    s.leave[buf][lane] = upd * __builtin_amdgcn_exp2f((float)(end - l));
+                }
+                if (lane == 0) s.total[buf] = __builtin_amdgcn_exp2f((float)end);
+                run += end;
+            }
+            if constexpr (OUT) {
+                sx.put(s.x[buf], len);
+            }
+            sy.put(s.y[buf], len);
+            sz.put(s.z[buf], len);
+            if (OUT && sz.bad()) s.bad[buf] = n + 1;
+            if (n + 1 < nc) fetch(n + 1);
+            lds_barrier();
+            if constexpr (OUT) {
+                if constexpr (NI == 4) {
+                    if (wv == 4) p_row<P, KD, 3, 0, 1>(s, buf, lane, pair, rows);
+                    if (wv == 5) p_row<P, KD, 3, 2, 3>(s, buf, lane, pair, rows);
+                    if (wv == 6) p_row<P, KD, 2, 0, 2>(s, buf, lane, pair, rows);
+                    if (wv == 7) {
+                        p_row<P, KD, 1, 0, 1>(s, buf, lane, pair, rows);
+                        p_row<P, KD, 0, 0, 0>(s, buf, lane, pair, rows);
+                    }
+                } else {
+                    static_assert(NI == 2, "two or four tiles of tokens");
+                    if (wv == 4) p_row<P, KD, 1, 0, 0>(s, buf, lane, pair, rows);
+                    if (wv == 5) p_row<P, KD, 1, 1, 1>(s, buf, lane, pair, rows);
+                    if (wv == 6) p_row<P, KD, 0, 0, 0>(s, buf, lane, pair, rows);
+                }
+                lds_barrier();
+            }
+        }
+        // B's last chunk
+        lds_barrier();
+        if constexpr (OUT) lds_barrier();
+        if (!OUT && jb.seg_decay && at.zb == 0 && wv == 7 && lane == 0)
+            jb.seg_decay[at.seg * a.B * a.H + bh] = __builtin_amdgcn_exp2f((float)run);
+        return;
+    }
+
+    // ---- team B ----
+    const int zd = jb.zd, zc = at.zb * ZB + 16 * wv;    // this wave's first channel
     // state, transposed: tile u = 2 k + h, row 4 g + r, is channel 32 k + 8 g + 4 h + r
     // of x and y, column m channel zc + m
     f32x4 H[NU];
     auto hoff = [&](int u, int r) {
         return (int64_t)(zc + m) * jb.hz + (int64_t)(32 * (u >> 1) + 8 * g + 4 * (u & 1) + r) * jb.hk;
     };
-    auto hok = [&](int u) { return zc + m < jb.zd && 32 * (u >> 1) + 8 * g < jb.kd; };
+    auto hok = [&](int u) { return zc + m < zd && 32 * (u >> 1) + 8 * g < jb.kd; };
 #pragma unroll
     for (int u = 0; u < NU; ++u) {
         H[u] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -84,110 +236,51 @@ __global__ __launch_bounds__(256) void chain_kernel(LaChain a) {
                 for (int r = 0; r < 4; ++r) p[hoff(u, r)] = H[u][r] * f;
             }
     };
+    typename TX::Rows rows;
+    typename TX::Cols cols;
+    typename TZ::Col16 zcol;
+    typename TP::Rows prow;
+    rows.init(lane);
+    cols.init(lane);
+    zcol.init(lane, 16 * wv);
+    prow.init(lane);
+    const bool mine = zc + 4 * g < zd;                  // whether the lane has out channels
+    const bool out16 = jb.out_bf16;
+    const size_t oe = out16 ? 2 : 4;
+    const uint32_t ot = (uint32_t)(jb.ot * (int64_t)oe);
+    char* ob = OUT ? static_cast<char*>(jb.out) + (at.b * jb.ob + at.h * jb.oh + zc + 4 * g) * oe
+                   : nullptr;
+    const bool dots = GRAD && jb.dots;
+    const char* rb = dots ? static_cast<const char*>(head_base(jb.r, at.b, at.h, sizeof(T))) +
+                                (zc + 4 * g) * sizeof(T)
+                          : nullptr;
+    const uint32_t rt = dots ? (uint32_t)(jb.r.st * sizeof(T)) : 0u;
+    float* const db = dots ? jb.dots + ((int64_t)(zc >> 4) * a.B + at.b) * a.T * a.H + at.h : nullptr;
+    float* const keep = GRAD ? jb.keep : nullptr;
 
-    Stage<P, KD> sx, sy;
-    Stage<P, ZB> sz;
-    double gl = 0.0, run = 0.0;
-    // chunk n of the chain: tokens [t0, t1), rows from the first on (back: the last)
-    auto bounds = [&](int64_t n, int64_t& t0, int& len, int64_t& first) {
-        t0 = ta + (back ? nc - 1 - n : n) * C;
-        len = (int)(tb - t0 < C ? tb - t0 : C);
-        first = back ? t0 + len - 1 : t0;
-    };
-    auto fetch = [&](int64_t n) {
-        int64_t t0, first;
-        int len;
-        bounds(n, t0, len, first);
-        const int dir = back ? -1 : 1;
-        if constexpr (OUT) sx.load(xb, first, dir, jb.x.st, len, jb.kd, tid);
-        sy.load(yb, first, dir, jb.y.st, len, jb.kd, tid);
-        sz.load(zb, first, dir, jb.z.st, len, zw, tid);
-        gl = 0.0;
-        if (tid < C && tid < len)
-            gl = decay2(a, at.b, at.h, back ? first - tid + 1 : first + tid);
-    };
-    fetch(0);
-
-    if constexpr (OUT) {
-        // tiles above the diagonal stay 0
-        for (int i = tid; i < P::NT * C * C; i += 256) (&s.p[0][0])[i] = 0;
-    }
+    lds_barrier();
+    if constexpr (OUT) lds_barrier();
     for (int64_t n = 0; n < nc; ++n) {
-        int64_t t0, first;
+        const int buf = (int)(n & 1);
+        int64_t t0;
         int len;
-        bounds(n, t0, len, first);
-        __syncthreads();                // the last chunk's tiles are read
-        if constexpr (OUT) sx.put(s.x, tid);
-        sy.put(s.y, tid);
-        sz.put(s.z, tid);
-        if (tid == 0) s.bad = 0;
-        if (wv == 0) {
-            // running sums in 64 bits: the differences of far lower sums than their
-            // own size decide the factors behind a reset
-            double l = gl;
-#pragma unroll
-            for (int d = 1; d < C; d *= 2) {
-                const double v = __shfl_up(l, d, 64);
-                l += lane >= d ? v : 0.0;
-            }
-            const double end = __shfl(l, C - 1, 64);
-            if (lane < C) {
-                s.lh[lane] = (float)l;
-                s.ll[lane] = (float)(l - (double)(float)l);
-                s.enter[lane] = jb.inter * __builtin_amdgcn_exp2f((float)l);
-                s.leave[lane] = jb.upd * __builtin_amdgcn_exp2f((float)(end - l));
-            }
-            if (lane == 0) s.total = __builtin_amdgcn_exp2f((float)end);
-            run += end;
-        }
-        const bool mybad = OUT && sz.bad();
-        if (n + 1 < nc) fetch(n + 1);
-        __syncthreads();
-        if (mybad) s.bad = 1;
-
-        f32x4 O[NI];
+        bounds(n, t0, len);
         typename P::Frag zf[NJ];
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) zf[j] = TZ::col8(s.z, lane, 32 * j, 16 * wv, 4);
+        for (int j = 0; j < NJ; ++j) zf[j] = zcol.get(s.z[buf], j);
+        f32x4 O[NI];
         if constexpr (OUT) {
-            // P^T tiles (j <= i): row 4 g + r is j, column m is i
-            int t = 0;
+            Row<4, P::is_bf16, false> rr[GRAD ? NI : 1];
+            if constexpr (GRAD) {
+                if (dots) {
 #pragma unroll
-            for (int i = 0; i < NI; ++i)
-#pragma unroll
-                for (int j = 0; j <= i; ++j, ++t) {
-                    if ((t & 3) != wv) continue;
-                    f32x4 c = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int k = 0; k < NK; ++k)
-                        c = P::mma(TX::row8(s.y, 16 * j + m, 4 * k + g),
-                                   TX::row8(s.x, 16 * i + m, 4 * k + g), c);
-                    const float lh = s.lh[16 * i + m], ll = s.ll[16 * i + m];
-                    float v[4];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int jj = 16 * j + 4 * g + r;
-                        const float d = __builtin_amdgcn_exp2f((lh - s.lh[jj]) + (ll - s.ll[jj]));
-                        v[r] = jj <= 16 * i + m ? c[r] * d * jb.pair : 0.f;
-                    }
-                    const int jj = 16 * j + 4 * g;
-                    if constexpr (P::is_bf16) {
-                        float e[4] = {v[0], v[1], v[2], v[3]};
-#pragma unroll
-                        for (int q = 0; q < P::NT; ++q) {
-                            const uint32_t w0 = cvt_pk(e[0], e[1]), w1 = cvt_pk(e[2], e[3]);
-                            *reinterpret_cast<uint2*>(TP::piece(s.p[q], 16 * i + m, jj >> 3) +
-                                                      (jj & 7)) = uint2{w0, w1};
-                            e[0] -= __uint_as_float(w0 << 16);
-                            e[1] -= __uint_as_float(w0 & 0xffff0000u);
-                            e[2] -= __uint_as_float(w1 << 16);
-                            e[3] -= __uint_as_float(w1 & 0xffff0000u);
-                        }
-                    } else {
-                        *reinterpret_cast<f32x4*>(TP::piece(s.p[0], 16 * i + m, jj >> 2)) =
-                            f32x4{v[0], v[1], v[2], v[3]};
+                    for (int i = 0; i < NI; ++i) {
+                        const int row = 16 * i + m < len ? 16 * i + m : len - 1;
+                        rr[i].load(rb + t0 * jb.r.st * (int)sizeof(T) +
+                                       (back ? len - 1 - row : row) * rt, 0, mine ? 4 : 0);
                     }
                 }
+            }
             // out^T (row 4 g + r: channel, column m: token) from the start state
 #pragma unroll
             for (int i = 0; i < NI; ++i) O[i] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -196,119 +289,120 @@ __global__ __launch_bounds__(256) void chain_kernel(LaChain a) {
                 typename P::Terms ht;
                 P::split(f32x8{H[2 * k][0], H[2 * k][1], H[2 * k][2], H[2 * k][3], H[2 * k + 1][0],
                                H[2 * k + 1][1], H[2 * k + 1][2], H[2 * k + 1][3]}, ht);
+                typename P::Frag xf[NI];
 #pragma unroll
-                for (int i = 0; i < NI; ++i)
-                    O[i] = P::mma(ht, TX::row8(s.x, 16 * i + m, 4 * k + g), O[i]);
+                for (int i = 0; i < NI; ++i) xf[i] = rows.get(s.x[buf], i, k);
+#pragma unroll
+                for (int q = P::NT - 1; q >= 0; --q)
+#pragma unroll
+                    for (int i = 0; i < NI; ++i) O[i] = P::mma(ht.t[q], xf[i], O[i]);
             }
 #pragma unroll
-            for (int i = 0; i < NI; ++i) O[i] *= s.enter[16 * i + m];
-            __syncthreads();
-            if (s.bad == 0) {
+            for (int i = 0; i < NI; ++i) O[i] *= s.enter[buf][16 * i + m];
+            if (__builtin_expect(s.bad[buf] != n + 1, 1)) {
 #pragma unroll
-                for (int i = 0; i < NI; ++i)
+                for (int j = 0; j < NJ; ++j)
 #pragma unroll
-                    for (int j = 0; j <= i / 2; ++j)
+                    for (int q = P::NT - 1; q >= 0; --q)
 #pragma unroll
-                        for (int q = P::NT - 1; q >= 0; --q)
-                            O[i] = P::mma(zf[j], TP::row8(s.p[q], 16 * i + m, 4 * j + g), O[i]);
+                        for (int i = 2 * j; i < NI; ++i)
+                            O[i] = P::mma(zf[j], prow.get(s.p[q], i, j), O[i]);
             } else {
-                // a value of z that is no number must not meet the zeros of tokens
+                // a value of z that is no number must not meet the zeros of the tokens
                 // before it: one by one
+#pragma unroll
                 for (int i = 0; i < NI; ++i)
                     for (int j = 0; j <= 16 * i + m; ++j) {
                         float pv = 0.f;
-                        if constexpr (P::is_bf16) {
-                            for (int q = P::NT - 1; q >= 0; --q)
-                                pv += bf2f(*(TP::piece(s.p[q], 16 * i + m, j >> 3) + (j & 7)));
-                        } else {
-                            pv = *(TP::piece(s.p[0], 16 * i + m, j >> 2) + (j & 3));
+#pragma unroll
+                        for (int q = P::NT - 1; q >= 0; --q) {
+                            const T w = s.p[q][TP::at(16 * i + m, j)];
+                            if constexpr (P::is_bf16) pv += bf2f(w);
+                            else pv += w;
                         }
+#pragma unroll
                         for (int r = 0; r < 4; ++r) {
-                            const int c = 16 * wv + 4 * g + r;
+                            const T w = s.z[buf][TZ::at(j, 16 * wv + 4 * g + r)];
                             float zv;
-                            if constexpr (P::is_bf16)
-                                zv = bf2f(*(TZ::piece(s.z, j, c >> 3) + (c & 7)));
-                            else
-                                zv = *(TZ::piece(s.z, j, c >> 2) + (c & 3));
-                            const f32x4 old = O[0];
-                            (void)old;
-#pragma unroll
-                            for (int ii = 0; ii < NI; ++ii)
-                                if (ii == i) {
-#pragma unroll
-                                    for (int rr = 0; rr < 4; ++rr)
-                                        if (rr == r) O[ii][rr] = __builtin_fmaf(pv, zv, O[ii][rr]);
-                                }
+                            if constexpr (P::is_bf16) zv = bf2f(w);
+                            else zv = w;
+                            O[i][r] = __builtin_fmaf(pv, zv, O[i][r]);
                         }
                     }
             }
-            // to memory
+            lds_barrier();
+            if constexpr (GRAD) {
+                if (dots) {
+#pragma unroll
+                    for (int i = 0; i < NI; ++i) {
+                        const int row = 16 * i + m;
+                        float rv[4], d = 0.f;
+                        rr[i].unpack(rv);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) d = __builtin_fmaf(rv[r], O[i][r], d);
+                        d += __shfl_xor(d, 16, 64);
+                        d += __shfl_xor(d, 32, 64);
+                        if (g == 0 && row < len && zc < zd)
+                            db[(t0 + (back ? len - 1 - row : row)) * a.H] = d;
+                    }
+                }
+            }
+            char* oc = ob + t0 * ot;
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
-                const int row = 16 * i + m, c = zc + 4 * g;
-                const int64_t t = back ? first - row : first + row;
-                const bool ok = row < len && c < jb.zd;
-                if (jb.dots) {
-                    float d = 0.f;
-                    if (ok) {
-                        const typename P::T* rp = static_cast<const typename P::T*>(
-                            head_base(jb.r, at.b, at.h, es)) + t * jb.r.st + c;
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            float rv;
-                            if constexpr (P::is_bf16) rv = bf2f(rp[r]);
-                            else rv = rp[r];
-                            d = __builtin_fmaf(rv, O[i][r], d);
-                        }
-                    }
-                    d += __shfl_xor(d, 16, 64);
-                    d += __shfl_xor(d, 32, 64);
-                    if (g == 0 && row < len && zc < jb.zd)
-                        jb.dots[(((int64_t)(zc >> 4) * a.B + at.b) * a.T + t) * a.H + at.h] = d;
-                }
-                if (ok) {
-                    const int64_t off = at.b * jb.ob + t * jb.ot + at.h * jb.oh + c;
-                    const float v[4] = {O[i][0], O[i][1], O[i][2], O[i][3]};
-                    row_store<4, false>(jb.out, off, jb.out_bf16, v, 4);
+                const int row = 16 * i + m;
+                if (row < len && mine) {
+                    char* p = oc + (uint32_t)(back ? len - 1 - row : row) * ot;
+                    if (out16)
+                        *reinterpret_cast<u32x2_e2*>(p) =
+                            u32x2_e2{cvt_pk(O[i][0], O[i][1]), cvt_pk(O[i][2], O[i][3])};
+                    else
+                        *reinterpret_cast<f32x4_e4*>(p) = O[i];
                 }
             }
         }
         // the state at the chunk's end
-        const float tot = s.total;
+        const float tot = s.total[buf];
         typename P::Terms zt[NJ];
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
             f32x8 v = P::widen(zf[j]);
+            const f32x4 l0 = *reinterpret_cast<const f32x4*>(&s.leave[buf][32 * j + 8 * g]);
+            const f32x4 l1 = *reinterpret_cast<const f32x4*>(&s.leave[buf][32 * j + 8 * g + 4]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] *= s.leave[32 * j + 8 * g + i];
+            for (int i = 0; i < 8; ++i) v[i] *= i < 4 ? l0[i & 3] : l1[i & 3];
             P::split(v, zt[j]);
         }
 #pragma unroll
-        for (int u = 0; u < NU; ++u) {
-            H[u] *= tot;
+        for (int u = 0; u < NU; ++u) H[u] *= tot;
 #pragma unroll
-            for (int j = 0; j < NJ; ++j)
-                H[u] = P::mma(TX::col8(s.y, lane, 32 * j, 32 * (u >> 1) + 4 * (u & 1), 8), zt[j],
-                              H[u]);
+        for (int j = 0; j < NJ; ++j) {
+            typename P::Frag yf[NU];
+#pragma unroll
+            for (int u = 0; u < NU; ++u) yf[u] = cols.get(s.y[buf], j, u >> 1, u & 1);
+#pragma unroll
+            for (int q = P::NT - 1; q >= 0; --q)
+#pragma unroll
+                for (int u = 0; u < NU; ++u) H[u] = P::mma(yf[u], zt[j].t[q], H[u]);
         }
-        if (OUT && jb.keep) {
+        if (GRAD && keep) {
             const int64_t mark = back ? t0 : t0 + len;
             if (back ? (mark > 0 && mark % a.every == 0)
                      : (mark < a.T ? mark % a.every == 0 : jb.keep_end))
-                h_store(jb.keep + (((mark + a.every - 1) / a.every - 1) * a.B * a.H + bh) * a.state,
+                h_store(keep + (((mark + a.every - 1) / a.every - 1) * a.B * a.H + bh) * a.state,
                         1.f);
         }
+        lds_barrier();
     }
     if constexpr (OUT) {
         if (jb.h_out && at.seg == (back ? 0 : a.nseg - 1)) {
             float f = 1.f;
-            if (jb.end_decay) f = __builtin_amdgcn_exp2f((float)decay2(a, at.b, at.h, 0));
+            if (jb.end_decay)
+                f = __builtin_amdgcn_exp2f((float)base2(decay_of(a, at.b, at.h, 0)));
             h_store(jb.h_out + bh * a.state, f);
         }
     } else {
         h_store(jb.h_out + (at.seg * a.B * a.H + bh) * a.state, 1.f);
-        if (jb.seg_decay && at.zb == 0 && tid == 0)
-            jb.seg_decay[at.seg * a.B * a.H + bh] = __builtin_amdgcn_exp2f((float)run);
     }
 }
 
@@ -428,26 +522,34 @@ __global__ __launch_bounds__(64) void head_sum_kernel(const double* part, float*
     if (threadIdx.x == 0) dg[blockIdx.x] = (float)s;
 }
 
-template <class P, int KD, bool OUT> hipError_t launch_kd(const LaChain& a) {
+template <class P, int KD, bool OUT, bool GRAD> hipError_t launch_kd(const LaChain& a) {
     int64_t per = 0;
     for (int j = 0; j < a.njobs; ++j) per += (a.job[j].zd + ZB - 1) / ZB;
     const int64_t grid = (a.B * a.H * a.nseg + 7) / 8 * 8 * per;
     constexpr size_t lds = sizeof(Shared<P, KD>);
     static_assert(lds <= 160 * 1024, "LDS");
-    hipLaunchKernelGGL((chain_kernel<P, KD, OUT>), dim3((unsigned)grid), dim3(256), lds, a.stream,
-                       a);
+    const hipError_t e = hipFuncSetAttribute((const void*)chain_kernel<P, KD, OUT, GRAD>,
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((chain_kernel<P, KD, OUT, GRAD>), dim3((unsigned)grid), dim3(512), lds,
+                       a.stream, a);
     return hipGetLastError();
 }
 
-template <class P, bool OUT> hipError_t launch_p(const LaChain& a, int kd) {
-    return kd <= 64 ? launch_kd<P, 64, OUT>(a) : launch_kd<P, 128, OUT>(a);
+template <class P, bool OUT, bool GRAD> hipError_t launch_p(const LaChain& a) {
+    return a.job[0].kd <= 64 ? launch_kd<P, 64, OUT, GRAD>(a) : launch_kd<P, 128, OUT, GRAD>(a);
 }
 
-// Jobs of one contraction width (all of a.job have the same side of 64).
-hipError_t launch_chain(const LaChain& a, bool out) {
-    const int kd = a.job[0].kd;
-    if (a.bf16) return out ? launch_p<Bf16, true>(a, kd) : launch_p<Bf16, false>(a, kd);
-    return out ? launch_p<F32, true>(a, kd) : launch_p<F32, false>(a, kd);
+template <class P> hipError_t launch_chain_p(const LaChain& a) {
+    if (!a.job[0].out) return launch_p<P, false, false>(a);
+    for (int j = 0; j < a.njobs; ++j)
+        if (a.job[j].keep || a.job[j].dots) return launch_p<P, true, true>(a);
+    return launch_p<P, true, false>(a);
+}
+
+// Jobs of one contraction width (all of a.job are on the same side of 64).
+hipError_t launch_chain(const LaChain& a) {
+    return a.bf16 ? launch_chain_p<Bf16>(a) : launch_chain_p<F32>(a);
 }
 
 struct Plan {
@@ -523,7 +625,7 @@ hipError_t segment_states(LaChain c, LaJob j, float* buf, float* decay) {
     j.keep = j.dots = nullptr;
     c.njobs = 1;
     c.job[0] = j;
-    hipError_t e = launch_chain(c, false);
+    hipError_t e = launch_chain(c);
     if (e != hipSuccess) return e;
     const int64_t n = c.B * c.H * c.state;
     hipLaunchKernelGGL(compose_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, c.stream,
@@ -536,9 +638,10 @@ hipError_t segment_states(LaChain c, LaJob j, float* buf, float* decay) {
 
 using namespace la;
 
+// The largest launch of a call, in workgroups of 256.
 int64_t la_fwd_workgroups(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, bool bf16) {
     const Plan p = fwd_plan(B, T, H, Dv);
-    const int64_t chain = (B * H * p.nseg + 7) / 8 * 8 * blocks(Dv);
+    const int64_t chain = 2 * ((B * H * p.nseg + 7) / 8 * 8 * blocks(Dv));
     const int64_t states = p.nseg > 1 ? (B * H * Dk * Dv + 255) / 256 : 0;
     return chain > states ? chain : states;
 }
@@ -572,7 +675,7 @@ hipError_t launch_la_fwd(const LaArgs& a) {
     j.h_out = a.s_final;
     c.njobs = 1;
     c.job[0] = j;
-    return launch_chain(c, true);
+    return launch_chain(c);
 }
 
 namespace {
@@ -615,7 +718,7 @@ BwdSpace bwd_space(const Plan& p, int64_t every, int64_t B, int64_t T, int64_t H
 int64_t la_bwd_workgroups(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, bool bf16) {
     int64_t every;
     const Plan p = bwd_plan(B, T, H, Dk, Dv, every);
-    const int64_t chain = (B * H * p.nseg + 7) / 8 * 8 * (2 * blocks(Dk) + blocks(Dv));
+    const int64_t chain = 2 * ((B * H * p.nseg + 7) / 8 * 8 * (2 * blocks(Dk) + blocks(Dv)));
     const int64_t states = (B * H * Dk * Dv + 255) / 256;
     const int64_t sums = B * H * ((T + every - 1) / every);
     const int64_t most = chain > states ? chain : states;
@@ -693,15 +796,15 @@ hipError_t launch_la_bwd(const LaArgs& a) {
         c.job[0] = jq;
         c.job[1] = jk;
         c.job[2] = jv;
-        if ((e = launch_chain(c, true)) != hipSuccess) return e;
+        if ((e = launch_chain(c)) != hipSuccess) return e;
     } else {
         c.njobs = 2;
         c.job[0] = jq;
         c.job[1] = jk;
-        if ((e = launch_chain(c, true)) != hipSuccess) return e;
+        if ((e = launch_chain(c)) != hipSuccess) return e;
         c.njobs = 1;
         c.job[0] = jv;
-        if ((e = launch_chain(c, true)) != hipSuccess) return e;
+        if ((e = launch_chain(c)) != hipSuccess) return e;
     }
     if (!own) {
         const int64_t n = a.B * a.T * a.Hk * (a.Dk / 4);

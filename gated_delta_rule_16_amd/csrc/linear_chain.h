@@ -26,7 +26,7 @@ struct Bf16 {
     static constexpr int NT = 3;
     typedef bf16x8 Frag;
     struct Terms {
-        bf16x8 t[NT];
+        bf16x8 t[NT];               // the largest first
     };
     static __device__ __forceinline__ void split(const f32x8& x, Terms& o) {
         uint32_t w[NT][4];
@@ -59,17 +59,6 @@ struct Bf16 {
     static __device__ __forceinline__ f32x4 mma(const Frag& a, const Frag& b, const f32x4& c) {
         return mfma16(a, b, c);
     }
-    // the smallest terms first
-    static __device__ __forceinline__ f32x4 mma(const Terms& a, const Frag& b, f32x4 c) {
-#pragma unroll
-        for (int n = NT - 1; n >= 0; --n) c = mfma16(a.t[n], b, c);
-        return c;
-    }
-    static __device__ __forceinline__ f32x4 mma(const Frag& a, const Terms& b, f32x4 c) {
-#pragma unroll
-        for (int n = NT - 1; n >= 0; --n) c = mfma16(a, b.t[n], c);
-        return c;
-    }
 };
 
 // fp32 inputs: chunks of 32 tokens on the fp32 matrix cores.  A lane's 8 elements of
@@ -91,106 +80,165 @@ struct F32 {
         for (int i = 0; i < 8; ++i) c = mfma_f32(a[i], b[i], c);
         return c;
     }
-    static __device__ __forceinline__ f32x4 mma(const Terms& a, const Frag& b, const f32x4& c) {
-        return mma(a.t[0], b, c);
-    }
-    static __device__ __forceinline__ f32x4 mma(const Frag& a, const Terms& b, const f32x4& c) {
-        return mma(a, b.t[0], c);
-    }
 };
 
-// A tile of rows of W elements in LDS.
+// A tile of rows of W elements in LDS, and where a lane (g = lane / 16, m = lane % 16)
+// finds its operands in it.  The swizzle repeats every 8 rows, so offsets are a few
+// registers per lane and the rest constants.
 template <class P, int W> struct Tile {
     typedef typename P::T T;
     static constexpr int PPR = W / P::EP;           // 16-byte pieces per row
-    static __device__ __forceinline__ T* piece(T* t, int row, int c) {
-        return t + row * W + ((c ^ (swz(row) & (PPR - 1))) * P::EP);
+    static __device__ __forceinline__ int at(int row, int col) {
+        return row * W + (((col / P::EP) ^ swz(row)) * P::EP) + col % P::EP;
     }
-    static __device__ __forceinline__ const T* piece(const T* t, int row, int c) {
-        return t + row * W + ((c ^ (swz(row) & (PPR - 1))) * P::EP);
-    }
-    // elements 8 c8 .. 8 c8 + 7 of a row
-    static __device__ __forceinline__ typename P::Frag row8(const T* t, int row, int c8) {
-        if constexpr (P::is_bf16) {
-            return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(piece(t, row, c8)));
-        } else {
-            const f32x4 a = *reinterpret_cast<const f32x4*>(piece(t, row, 2 * c8));
-            const f32x4 b = *reinterpret_cast<const f32x4*>(piece(t, row, 2 * c8 + 1));
-            return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-        }
-    }
-    // rows row0 + 8 g .. + 7 of one column per lane m, which is
-    // col0 + step (m / 4) + m % 4 (g = lane / 16, m = lane % 16)
-    static __device__ __forceinline__ typename P::Frag col8(const T* t, int lane, int row0,
-                                                            int col0, int step) {
-        const int g = lane >> 4, m = lane & 15;
-        if constexpr (P::is_bf16) {
-            // lane 4 r + c of a group points at 4 columns of row r (lds_tr16)
-            const int r = row0 + 8 * g + (m >> 2), c = col0 + step * (m & 3);
-            const s16x4 a = lds_tr16(piece(t, r, c >> 3) + (c & 7));
-            const s16x4 b = lds_tr16(piece(t, r + 4, c >> 3) + (c & 7));
-            typedef short s16x8 __attribute__((ext_vector_type(8)));
-            const s16x8 v = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-            return __builtin_bit_cast(bf16x8, v);
-        } else {
-            const int c = col0 + step * (m >> 2) + (m & 3);
-            f32x8 v;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int r = row0 + 8 * g + i;
-                v[i] = *(piece(t, r, c >> 2) + (c & 3));
+
+    // Elements 32 k + 8 g .. + 7 of row 16 i + m.
+    struct Rows {
+        int o[2];
+        __device__ __forceinline__ void init(int lane) {
+            const int g = lane >> 4, m = lane & 15;
+            if constexpr (P::is_bf16) {             // k's lowest bit meets the swizzle
+                o[0] = at(m, 8 * g);
+                o[1] = W == 32 ? 0 : m * W + (((4 + g) ^ swz(m)) * P::EP);
+            } else {                                // two pieces
+                o[0] = at(m, 8 * g);
+                o[1] = at(m, 8 * g + 4);
             }
-            return v;
         }
+        __device__ __forceinline__ typename P::Frag get(const T* t, int i, int k) const {
+            if constexpr (P::is_bf16) {
+                return __builtin_bit_cast(
+                    bf16x8, *reinterpret_cast<const u32x4*>(t + 16 * i * W + (k >> 1) * 64 + o[k & 1]));
+            } else {
+                const T* p = t + 16 * i * W + 32 * k;
+                const f32x4 a = *reinterpret_cast<const f32x4*>(p + o[0]);
+                const f32x4 b = *reinterpret_cast<const f32x4*>(p + o[1]);
+                return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+            }
+        }
+    };
+
+    // Rows 32 j + 8 g .. + 7 of column 32 k + 4 h + 8 (m / 4) + m % 4.
+    struct Cols {
+        int o[P::is_bf16 ? 4 : 2];
+        __device__ __forceinline__ void init(int lane) {
+            const int g = lane >> 4, m = lane & 15;
+            if constexpr (P::is_bf16) {
+                // lane 4 r + c of a group points at 4 columns of row r (lds_tr16)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int r = 8 * g + (m >> 2) + 4 * (q & 1), c = (m & 3) + 4 * (q >> 1);
+                    o[q] = r * W + ((c ^ swz(r)) * P::EP);
+                }
+            } else {
+                o[0] = g;
+                o[1] = 8 * (m >> 2) + (m & 3);
+            }
+        }
+        __device__ __forceinline__ typename P::Frag get(const T* t, int j, int k, int h) const {
+            if constexpr (P::is_bf16) {
+                const T* p = t + 32 * j * W + (k >> 1) * 64 + 4 * h;
+                return pair(lds_tr16(p + o[2 * (k & 1)]), lds_tr16(p + o[2 * (k & 1) + 1]));
+            } else {
+                f32x8 v;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    v[i] = t[at(32 * j + 8 * o[0] + i, 32 * k + 4 * h + o[1])];
+                return v;
+            }
+        }
+    };
+
+    // Rows 32 j + 8 g .. + 7 of column col0 + m (col0 a multiple of 16).
+    struct Col16 {
+        int o[2];
+        __device__ __forceinline__ void init(int lane, int col0) {
+            const int g = lane >> 4, m = lane & 15;
+            if constexpr (P::is_bf16) {
+                o[0] = at(8 * g + (m >> 2), col0 + 4 * (m & 3));
+                o[1] = at(8 * g + (m >> 2) + 4, col0 + 4 * (m & 3));
+            } else {
+                o[0] = g;
+                o[1] = col0 + m;
+            }
+        }
+        __device__ __forceinline__ typename P::Frag get(const T* t, int j) const {
+            if constexpr (P::is_bf16) {
+                const T* p = t + 32 * j * W;
+                return pair(lds_tr16(p + o[0]), lds_tr16(p + o[1]));
+            } else {
+                f32x8 v;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = t[at(32 * j + 8 * o[0] + i, o[1])];
+                return v;
+            }
+        }
+    };
+
+    static __device__ __forceinline__ bf16x8 pair(const s16x4& a, const s16x4& b) {
+        typedef short s16x8 __attribute__((ext_vector_type(8)));
+        return __builtin_bit_cast(bf16x8, s16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]});
     }
 };
 
-// The pieces of a [C, W] tile that one of 256 threads moves from memory.
+// The pieces of a [C, W] tile that one of 256 threads moves from memory: piece i is
+// row row0 + i C / N of the chunk, 16 bytes at channel col.
 template <class P, int W> struct Stage {
     static constexpr int PPR = W / P::EP;
-    static constexpr int N = P::C * PPR / 256;
+    static constexpr int N = P::C * PPR / 256, STEP = P::C / N;
+    static_assert(STEP % 8 == 0, "the swizzle repeats every 8 rows");
     u32x4 w[N];
-    // Rows are tokens t, t + dir, ..; rows from len on and channels from `width` on
-    // become 0.  `base`: of token 0.
-    __device__ __forceinline__ void load(const void* base, int64_t t, int dir, int64_t st, int len,
-                                         int width, int tid) {
+    int row0, col, to;
+    bool wide;                      // whether the tensor has these channels
+    uint32_t off;                   // bytes from a whole chunk's first token
+    uint32_t step;                  // bytes from piece to piece
+    __device__ __forceinline__ void init(int tid, int width, int64_t st, bool back) {
+        row0 = tid / PPR;
+        const int c = tid % PPR * P::EP;
+        wide = c < width;
+        col = wide ? c : 0;
+        to = Tile<P, W>::at(row0, c);
+        const uint32_t sb = (uint32_t)(st * sizeof(typename P::T));
+        off = (back ? P::C - 1 - row0 : row0) * sb + col * (uint32_t)sizeof(typename P::T);
+        step = STEP * sb;
+    }
+    // `chunk`: the first token's first channel.  Rows from len on are loaded as the
+    // last one, and cleared by put.
+    __device__ __forceinline__ void load(const char* chunk, int64_t st, int len, bool back) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int id = tid + 256 * i, row = id / PPR, c = id % PPR;
-            w[i] = u32x4{0u, 0u, 0u, 0u};
-            if (row < len && c * P::EP < width) {
-                const typename P::T* p = static_cast<const typename P::T*>(base) +
-                                         (t + dir * row) * st + c * P::EP;
-                if constexpr (P::is_bf16)
-                    w[i] = *reinterpret_cast<const u32x4_e2*>(p);
-                else
-                    w[i] = *reinterpret_cast<const u32x4_e4*>(p);
+            uint32_t o = back ? off - i * step : off + i * step;
+            if (len < P::C) {
+                const int r = row0 + i * STEP < len ? row0 + i * STEP : len - 1;
+                o = (uint32_t)((back ? len - 1 - r : r) * st + col) *
+                    (uint32_t)sizeof(typename P::T);
             }
+            if constexpr (P::is_bf16)
+                w[i] = *reinterpret_cast<const u32x4_e2*>(chunk + o);
+            else
+                w[i] = *reinterpret_cast<const u32x4_e4*>(chunk + o);
         }
     }
-    __device__ __forceinline__ void put(typename P::T* tile, int tid) const {
+    __device__ __forceinline__ void put(typename P::T* tile, int len) {
+        const u32x4 zero = {0u, 0u, 0u, 0u};
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int id = tid + 256 * i, row = id / PPR, c = id % PPR;
-            *reinterpret_cast<u32x4*>(Tile<P, W>::piece(tile, row, c)) = w[i];
+            if (!wide || (len < P::C && row0 + i * STEP >= len)) w[i] = zero;
+            *reinterpret_cast<u32x4*>(tile + to + i * STEP * W) = w[i];
         }
     }
     // Whether an element is infinite or no number.
     __device__ __forceinline__ bool bad() const {
-        uint32_t any = 0;
+        bool any = false;
 #pragma unroll
         for (int i = 0; i < N; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const uint32_t v = w[i][j];
-                if constexpr (P::is_bf16) {
-                    any |= (v & 0x7f80u) == 0x7f80u;
-                    any |= (v & 0x7f800000u) == 0x7f800000u;
-                } else {
-                    any |= (v & 0x7f800000u) == 0x7f800000u;
-                }
+                any |= (v & 0x7f800000u) == 0x7f800000u;
+                if constexpr (P::is_bf16) any |= (v & 0x7f80u) == 0x7f80u;
             }
-        return any != 0;
+        return any;
     }
 };
 
@@ -225,12 +273,15 @@ __device__ __forceinline__ const void* head_base(const LaTensor& t, int64_t b, i
     return static_cast<const char*>(t.p) + (b * t.sb + h / t.share * t.sh) * elem;
 }
 
-// Log decay (base 2) that the state goes through before token t is added.
-__device__ __forceinline__ double decay2(const LaChain& a, int64_t b, int64_t h, int64_t t) {
-    if (!a.g || t >= a.T) return 0.0;
-    float g = a.g_head ? a.g[h] : a.g[(b * a.T + t) * a.H + h];
-    g = g < kLeast ? kLeast : g;
-    return (double)g * 1.4426950408889634;
+// Log decay that the state goes through before token t is added, as it lies in
+// memory (a value that is waited for only where it is used), and in base 2.
+__device__ __forceinline__ float decay_of(const LaChain& a, int64_t b, int64_t h, int64_t t) {
+    if (!a.g || t >= a.T) return 0.f;
+    return a.g_head ? a.g[h] : a.g[(b * a.T + t) * a.H + h];
+}
+
+__device__ __forceinline__ double base2(float g) {
+    return (double)(g < kLeast ? kLeast : g) * 1.4426950408889634;
 }
 
 }  // namespace la

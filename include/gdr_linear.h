@@ -38,10 +38,11 @@ extern "C" {
  * and q its B and C, v its x times the step).
  *
  *   B, T      sequences, tokens (each >= 0)
- *   H, Hk     heads of v, g, o and the state; heads of q and k, each shared by
- *             H / Hk consecutive heads (Hk divides H)
+ *   H, Hk     heads of v, g, o and the state (at most GDR_MAX_HEADS); heads of q
+ *             and k, each shared by H / Hk consecutive heads (Hk divides H)
  *   Dk, Dv    multiples of 8, at most GDR_LA_MAX_D
- *   q, k      [B, T, Hk, Dk] in_dt;  v [B, T, H, Dv] in_dt; strides {q, k, v}
+ *   q, k      [B, T, Hk, Dk] in_dt;  v [B, T, H, Dv] in_dt; strides {q, k, v},
+ *             those of tokens at most GDR_LA_MAX_TOKEN_STRIDE
  *   log_decay g, fp32: [B, T, H], or [H] with GDR_LA_HEAD_DECAY, or NULL (no
  *             decay).  Meant to be <= 0; minus infinity (anything below -10000)
  *             forgets all tokens before, as at the first token of a packed
@@ -59,6 +60,7 @@ extern "C" {
  */
 #define GDR_LA_HEAD_DECAY 1u
 #define GDR_LA_MAX_D 128
+#define GDR_LA_MAX_TOKEN_STRIDE 8388608
 
 size_t gdr_linear_attn_fwd_workspace_size(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv,
                                           gdr_dtype_t in_dt);
