@@ -40,7 +40,7 @@ template <class P, int KD> struct Shared {
 // Tile (i, j) of P^T (row 4 g + r: token j, column m: token i) into s.p.
 template <class P, int KD, int I, int J>
 __device__ __forceinline__ void p_tile(Shared<P, KD>& s, int buf, int lane, float scale,
-                                       const typename Tile<P, KD>::Rows& rows,
+                                       const typename Tile<P, KD, BOTH>::Rows& rows,
                                        const typename P::Frag (&xf)[KD / 32]) {
     const int g = lane >> 4, m = lane & 15;
     f32x4 c = {0.f, 0.f, 0.f, 0.f};
@@ -55,7 +55,7 @@ __device__ __forceinline__ void p_tile(Shared<P, KD>& s, int buf, int lane, floa
         v[r] = c[r] * (__builtin_amdgcn_exp2f((lh - jh[r]) + (ll - jl[r])) * scale);
         if (I == J && 4 * g + r > m) v[r] = 0.f;
     }
-    typedef Tile<P, P::C> TP;
+    typedef Tile<P, P::C, ROWS> TP;
     const int to = TP::at(m, 16 * J + 4 * g) + 16 * I * P::C;
     if constexpr (P::is_bf16) {
 #pragma unroll
@@ -75,13 +75,14 @@ __device__ __forceinline__ void p_tile(Shared<P, KD>& s, int buf, int lane, floa
 // Tiles (I, J0 .. J1) of P^T.
 template <class P, int KD, int I, int J0, int J1>
 __device__ __forceinline__ void p_row(Shared<P, KD>& s, int buf, int lane, float scale,
-                                      const typename Tile<P, KD>::Rows& rows) {
+                                      const typename Tile<P, KD, ROWS>::Rows& xrow,
+                                      const typename Tile<P, KD, BOTH>::Rows& yrow) {
     typename P::Frag xf[KD / 32];
 #pragma unroll
-    for (int k = 0; k < KD / 32; ++k) xf[k] = rows.get(s.x[buf], I, k);
-    p_tile<P, KD, I, J0>(s, buf, lane, scale, rows, xf);
-    if constexpr (J1 > J0) p_tile<P, KD, I, J0 + 1>(s, buf, lane, scale, rows, xf);
-    if constexpr (J1 > J0 + 1) p_tile<P, KD, I, J0 + 2>(s, buf, lane, scale, rows, xf);
+    for (int k = 0; k < KD / 32; ++k) xf[k] = xrow.get(s.x[buf], I, k);
+    p_tile<P, KD, I, J0>(s, buf, lane, scale, yrow, xf);
+    if constexpr (J1 > J0) p_tile<P, KD, I, J0 + 1>(s, buf, lane, scale, yrow, xf);
+    if constexpr (J1 > J0 + 1) p_tile<P, KD, I, J0 + 2>(s, buf, lane, scale, yrow, xf);
 }
 
 // OUT: out is wanted (else the states at segments' ends alone).  GRAD: jobs may have
@@ -89,9 +90,10 @@ __device__ __forceinline__ void p_row(Shared<P, KD>& s, int buf, int lane, float
 template <class P, int KD, bool OUT, bool GRAD>
 __global__ __launch_bounds__(512) void chain_kernel(LaChain a) {
     constexpr int C = P::C, NU = KD / 16, NK = KD / 32, NI = C / 16, NJ = C / 32;
-    typedef Tile<P, KD> TX;
-    typedef Tile<P, ZB> TZ;
-    typedef Tile<P, C> TP;
+    typedef Tile<P, KD, ROWS> TX;
+    typedef Tile<P, KD, BOTH> TY;
+    typedef Tile<P, ZB, COLS> TZ;
+    typedef Tile<P, C, ROWS> TP;
     typedef typename P::T T;
     extern __shared__ __attribute__((aligned(16))) char smem[];
     Shared<P, KD>& s = *reinterpret_cast<Shared<P, KD>*>(smem);
@@ -129,30 +131,37 @@ __global__ __launch_bounds__(512) void chain_kernel(LaChain a) {
                          at.zb * ZB * sizeof(T);
         const int64_t xt = jb.x.st, yt = jb.y.st, zt = jb.z.st;
         const float pair = jb.pair, inter = jb.inter, upd = jb.upd;
-        Stage<P, KD> sx, sy;
-        Stage<P, ZB> sz;
-        if constexpr (OUT) sx.init(tid, jb.kd, xt, back);
-        sy.init(tid, jb.kd, yt, back);
-        sz.init(tid, jb.zd - at.zb * ZB, zt, back);
-        typename TX::Rows rows;
-        rows.init(lane);
-        float gl = 0.f;
+        // two chunks on their way: the next but one is asked for before the next is
+        // waited for
+        struct Coming {
+            Stage<P, KD, ROWS> x;
+            Stage<P, KD, BOTH> y;
+            Stage<P, ZB, COLS> z;
+            float g;
+        } even, odd;
+        if constexpr (OUT) even.x.init(tid, jb.kd, xt, back);
+        even.y.init(tid, jb.kd, yt, back);
+        even.z.init(tid, jb.zd - at.zb * ZB, zt, back);
+        odd = even;
+        typename TX::Rows xrow;
+        typename TY::Rows yrow;
+        xrow.init(lane);
+        yrow.init(lane);
         double run = 0.0;
-        auto fetch = [&](int64_t n) {
+        auto fetch = [&](int64_t n, Coming& c) {
             int64_t t0;
             int len;
             bounds(n, t0, len);
             if (wv == 7) {
-                gl = 0.f;
+                c.g = 0.f;
                 if (lane < len)
-                    gl = decay_of(a, at.b, at.h, back ? t0 + len - lane : t0 + lane);
+                    c.g = decay_of(a, at.b, at.h, back ? t0 + len - lane : t0 + lane);
             }
-            if constexpr (OUT) sx.load(xb + t0 * xt * (int)sizeof(T), xt, len, back);
-            sy.load(yb + t0 * yt * (int)sizeof(T), yt, len, back);
-            sz.load(zb + t0 * zt * (int)sizeof(T), zt, len, back);
+            if constexpr (OUT) c.x.load(xb + t0 * xt * (int)sizeof(T), xt, len, back);
+            c.y.load(yb + t0 * yt * (int)sizeof(T), yt, len, back);
+            c.z.load(zb + t0 * zt * (int)sizeof(T), zt, len, back);
         };
-        fetch(0);
-        for (int64_t n = 0; n < nc; ++n) {
+        auto turn = [&](int64_t n, Coming& c) {
             const int buf = (int)(n & 1);
             int64_t t0;
             int len;
@@ -160,13 +169,7 @@ __global__ __launch_bounds__(512) void chain_kernel(LaChain a) {
             if (wv == 7) {
                 // running sums in 64 bits: behind a reset, the differences of sums far
                 // larger than themselves decide the factors
-                double l = base2(gl);
-#pragma unroll
-                for (int d = 1; d < C; d *= 2) {
-                    const double v = __shfl_up(l, d, 64);
-                    l += lane >= d ? v : 0.0;
-                }
-                const double end = __shfl(l, C - 1, 64);
+                const double l = wave_scan64(base2(c.g)), end = lane64(l, C - 1);
                 if (lane < C) {
                     s.lh[buf][lane] = (float)l;
                     s.ll[buf][lane] = (float)(l - (double)(float)l);
@@ -176,31 +179,35 @@ __global__ __launch_bounds__(512) void chain_kernel(LaChain a) {
                 if (lane == 0) s.total[buf] = __builtin_amdgcn_exp2f((float)end);
                 run += end;
             }
-            if constexpr (OUT) {
-                sx.put(s.x[buf], len);
-            }
-            sy.put(s.y[buf], len);
-            sz.put(s.z[buf], len);
-            if (OUT && sz.bad()) s.bad[buf] = n + 1;
-            if (n + 1 < nc) fetch(n + 1);
+            if constexpr (OUT) c.x.put(s.x[buf], len);
+            c.y.put(s.y[buf], len);
+            c.z.put(s.z[buf], len);
+            if (OUT && c.z.bad()) s.bad[buf] = n + 1;
+            if (n + 2 < nc) fetch(n + 2, c);
             lds_barrier();
             if constexpr (OUT) {
                 if constexpr (NI == 4) {
-                    if (wv == 4) p_row<P, KD, 3, 0, 1>(s, buf, lane, pair, rows);
-                    if (wv == 5) p_row<P, KD, 3, 2, 3>(s, buf, lane, pair, rows);
-                    if (wv == 6) p_row<P, KD, 2, 0, 2>(s, buf, lane, pair, rows);
-                    if (wv == 7) {
-                        p_row<P, KD, 1, 0, 1>(s, buf, lane, pair, rows);
-                        p_row<P, KD, 0, 0, 0>(s, buf, lane, pair, rows);
+                    if (wv == 4) p_row<P, KD, 3, 0, 2>(s, buf, lane, pair, xrow, yrow);
+                    if (wv == 5) {
+                        p_row<P, KD, 1, 0, 1>(s, buf, lane, pair, xrow, yrow);
+                        p_row<P, KD, 3, 3, 3>(s, buf, lane, pair, xrow, yrow);
                     }
+                    if (wv == 6) p_row<P, KD, 2, 0, 2>(s, buf, lane, pair, xrow, yrow);
+                    if (wv == 7) p_row<P, KD, 0, 0, 0>(s, buf, lane, pair, xrow, yrow);
                 } else {
                     static_assert(NI == 2, "two or four tiles of tokens");
-                    if (wv == 4) p_row<P, KD, 1, 0, 0>(s, buf, lane, pair, rows);
-                    if (wv == 5) p_row<P, KD, 1, 1, 1>(s, buf, lane, pair, rows);
-                    if (wv == 6) p_row<P, KD, 0, 0, 0>(s, buf, lane, pair, rows);
+                    if (wv == 4) p_row<P, KD, 1, 0, 0>(s, buf, lane, pair, xrow, yrow);
+                    if (wv == 5) p_row<P, KD, 1, 1, 1>(s, buf, lane, pair, xrow, yrow);
+                    if (wv == 6) p_row<P, KD, 0, 0, 0>(s, buf, lane, pair, xrow, yrow);
                 }
                 lds_barrier();
             }
+        };
+        fetch(0, even);
+        if (nc > 1) fetch(1, odd);
+        for (int64_t n = 0; n < nc; n += 2) {
+            turn(n, even);
+            if (n + 1 < nc) turn(n + 1, odd);
         }
         // B's last chunk
         lds_barrier();
@@ -237,7 +244,7 @@ __global__ __launch_bounds__(512) void chain_kernel(LaChain a) {
             }
     };
     typename TX::Rows rows;
-    typename TX::Cols cols;
+    typename TY::Cols cols;
     typename TZ::Col16 zcol;
     typename TP::Rows prow;
     rows.init(lane);

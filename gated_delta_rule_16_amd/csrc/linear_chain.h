@@ -12,9 +12,22 @@ namespace la {
 constexpr int ZB = 64;              // channels of z and out per workgroup
 constexpr float kLeast = -1e4f;     // log decays from here on are a reset: exp is 0
 
-// 16-byte pieces of a tile's row are permuted by the row, so that rows read at one
-// column, and 4x4 blocks read transposed, meet different banks.
-__device__ __forceinline__ int swz(int row) { return ((row & 3) << 1) | ((row >> 2) & 1); }
+// Tiles in LDS.  The 16-byte pieces of a row are permuted by the row so that operands
+// meet different banks: rows read 16 bytes a lane (8 lanes a cycle: 0-3 with 20-23,
+// 4-7 with 16-19 and so on), and 4x4 blocks read transposed (16 lanes a cycle).
+enum TileKind {
+    ROWS,       // read by rows only
+    BOTH,       // by rows, and transposed 8 columns apart (bf16: odd rows also keep
+                // the halves of their pieces swapped)
+    COLS        // read transposed only, 16 neighbouring columns at once
+};
+
+template <int KIND> __device__ __forceinline__ int swz(int row) {
+    if constexpr (KIND == ROWS) return row & 7;
+    else if constexpr (KIND == BOTH)
+        return (row & 1) | ((row & 4) >> 1) | ((row & 2) << 1);
+    else return ((row & 3) << 1) | ((row >> 2) & 1);
+}
 
 // bf16 inputs: chunks of 64 tokens on the bf16 matrix cores.  A computed operand
 // enters as NT bf16 terms (24 bits with three).
@@ -85,30 +98,39 @@ struct F32 {
 // A tile of rows of W elements in LDS, and where a lane (g = lane / 16, m = lane % 16)
 // finds its operands in it.  The swizzle repeats every 8 rows, so offsets are a few
 // registers per lane and the rest constants.
-template <class P, int W> struct Tile {
+template <class P, int W, int KIND> struct Tile {
     typedef typename P::T T;
     static constexpr int PPR = W / P::EP;           // 16-byte pieces per row
+    static constexpr bool SWAP = KIND == BOTH && P::is_bf16;
+    static __device__ __forceinline__ int piece(int row, int c) {
+        return row * W + (c ^ swz<KIND>(row)) * P::EP;
+    }
     static __device__ __forceinline__ int at(int row, int col) {
-        return row * W + (((col / P::EP) ^ swz(row)) * P::EP) + col % P::EP;
+        const int e = col % P::EP;
+        return piece(row, col / P::EP) + (SWAP ? e ^ ((row & 1) * 4) : e);
     }
 
     // Elements 32 k + 8 g .. + 7 of row 16 i + m.
     struct Rows {
         int o[2];
+        bool swap;
         __device__ __forceinline__ void init(int lane) {
             const int g = lane >> 4, m = lane & 15;
+            swap = SWAP && (m & 1);
             if constexpr (P::is_bf16) {             // k's lowest bit meets the swizzle
-                o[0] = at(m, 8 * g);
-                o[1] = W == 32 ? 0 : m * W + (((4 + g) ^ swz(m)) * P::EP);
+                o[0] = piece(m, g);
+                o[1] = m * W + ((4 + g) ^ swz<KIND>(m)) * P::EP;
             } else {                                // two pieces
-                o[0] = at(m, 8 * g);
-                o[1] = at(m, 8 * g + 4);
+                o[0] = piece(m, 2 * g);
+                o[1] = piece(m, 2 * g + 1);
             }
         }
         __device__ __forceinline__ typename P::Frag get(const T* t, int i, int k) const {
             if constexpr (P::is_bf16) {
-                return __builtin_bit_cast(
-                    bf16x8, *reinterpret_cast<const u32x4*>(t + 16 * i * W + (k >> 1) * 64 + o[k & 1]));
+                u32x4 v = *reinterpret_cast<const u32x4*>(t + 16 * i * W + (k >> 1) * 64 + o[k & 1]);
+                if constexpr (SWAP)
+                    v = swap ? u32x4{v[2], v[3], v[0], v[1]} : v;
+                return __builtin_bit_cast(bf16x8, v);
             } else {
                 const T* p = t + 16 * i * W + 32 * k;
                 const f32x4 a = *reinterpret_cast<const f32x4*>(p + o[0]);
@@ -120,16 +142,16 @@ template <class P, int W> struct Tile {
 
     // Rows 32 j + 8 g .. + 7 of column 32 k + 4 h + 8 (m / 4) + m % 4.
     struct Cols {
-        int o[P::is_bf16 ? 4 : 2];
+        int o[P::is_bf16 ? 8 : 2];
         __device__ __forceinline__ void init(int lane) {
             const int g = lane >> 4, m = lane & 15;
             if constexpr (P::is_bf16) {
-                // lane 4 r + c of a group points at 4 columns of row r (lds_tr16)
+                // lane 4 r + c of a group points at 4 columns of row r (lds_tr16):
+                // by row half, k's lowest bit and h
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int r = 8 * g + (m >> 2) + 4 * (q & 1), c = (m & 3) + 4 * (q >> 1);
-                    o[q] = r * W + ((c ^ swz(r)) * P::EP);
-                }
+                for (int q = 0; q < 8; ++q)
+                    o[q] = at(8 * g + (m >> 2) + 4 * (q & 1),
+                              32 * ((q >> 1) & 1) + 4 * (q >> 2) + 8 * (m & 3));
             } else {
                 o[0] = g;
                 o[1] = 8 * (m >> 2) + (m & 3);
@@ -137,8 +159,9 @@ template <class P, int W> struct Tile {
         }
         __device__ __forceinline__ typename P::Frag get(const T* t, int j, int k, int h) const {
             if constexpr (P::is_bf16) {
-                const T* p = t + 32 * j * W + (k >> 1) * 64 + 4 * h;
-                return pair(lds_tr16(p + o[2 * (k & 1)]), lds_tr16(p + o[2 * (k & 1) + 1]));
+                const T* p = t + 32 * j * W + (k >> 1) * 64;
+                const int q = 2 * (k & 1) + 4 * h;
+                return pair(lds_tr16(p + o[q]), lds_tr16(p + o[q + 1]));
             } else {
                 f32x8 v;
 #pragma unroll
@@ -183,21 +206,22 @@ template <class P, int W> struct Tile {
 
 // The pieces of a [C, W] tile that one of 256 threads moves from memory: piece i is
 // row row0 + i C / N of the chunk, 16 bytes at channel col.
-template <class P, int W> struct Stage {
+template <class P, int W, int KIND> struct Stage {
     static constexpr int PPR = W / P::EP;
     static constexpr int N = P::C * PPR / 256, STEP = P::C / N;
     static_assert(STEP % 8 == 0, "the swizzle repeats every 8 rows");
     u32x4 w[N];
     int row0, col, to;
-    bool wide;                      // whether the tensor has these channels
+    bool wide, narrow;              // whether the tensor has these channels, all of W
     uint32_t off;                   // bytes from a whole chunk's first token
     uint32_t step;                  // bytes from piece to piece
     __device__ __forceinline__ void init(int tid, int width, int64_t st, bool back) {
         row0 = tid / PPR;
         const int c = tid % PPR * P::EP;
         wide = c < width;
+        narrow = width < W;
         col = wide ? c : 0;
-        to = Tile<P, W>::at(row0, c);
+        to = Tile<P, W, KIND>::piece(row0, tid % PPR);
         const uint32_t sb = (uint32_t)(st * sizeof(typename P::T));
         off = (back ? P::C - 1 - row0 : row0) * sb + col * (uint32_t)sizeof(typename P::T);
         step = STEP * sb;
@@ -220,11 +244,17 @@ template <class P, int W> struct Stage {
         }
     }
     __device__ __forceinline__ void put(typename P::T* tile, int len) {
-        const u32x4 zero = {0u, 0u, 0u, 0u};
+        if (narrow || len < P::C) {
+            const u32x4 zero = {0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (!wide || row0 + i * STEP >= len) w[i] = zero;
+        }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            if (!wide || (len < P::C && row0 + i * STEP >= len)) w[i] = zero;
-            *reinterpret_cast<u32x4*>(tile + to + i * STEP * W) = w[i];
+            u32x4 v = w[i];
+            if constexpr (Tile<P, W, KIND>::SWAP) v = (row0 & 1) ? u32x4{v[2], v[3], v[0], v[1]} : v;
+            *reinterpret_cast<u32x4*>(tile + to + i * STEP * W) = v;
         }
     }
     // Whether an element is infinite or no number.
@@ -282,6 +312,35 @@ __device__ __forceinline__ float decay_of(const LaChain& a, int64_t b, int64_t h
 
 __device__ __forceinline__ double base2(float g) {
     return (double)(g < kLeast ? kLeast : g) * 1.4426950408889634;
+}
+
+// Inclusive sums over the 64 lanes of a wave in 64 bits: rows of 16 by row_shr 1, 2, 4,
+// 8, then across rows by row_bcast 15 and 31.
+template <int CTRL, int ROW_MASK = 0xF> __device__ __forceinline__ double dpp_mov64(double x) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROW_MASK,
+                                                              0xF, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL,
+                                                              ROW_MASK, 0xF, false);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+__device__ __forceinline__ double wave_scan64(double x) {
+    x += dpp_mov64<0x111>(x);
+    x += dpp_mov64<0x112>(x);
+    x += dpp_mov64<0x114>(x);
+    x += dpp_mov64<0x118>(x);
+    x += dpp_mov64<0x142, 0xA>(x);
+    x += dpp_mov64<0x143, 0xC>(x);
+    return x;
+}
+
+// The value of one lane, for all.
+__device__ __forceinline__ double lane64(double x, int lane) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), lane);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 
 }  // namespace la
