@@ -31,8 +31,12 @@ namespace {
 
 template <class P, int KD> struct Shared {
     typename P::T x[2][P::C * KD], y[2][P::C * KD], z[2][P::C * ZB];
-    typename P::T p[P::NT][P::C * P::C];
-    float lh[2][P::C], ll[2][P::C], enter[2][P::C], leave[2][P::C];
+    typename P::T p[P::NO][P::C * P::C];
+    // the running log decay (base 2) in two terms, and factors: from the chunk's start,
+    // to its end, from the last token of the tile of 16 before, to the end of the own
+    // tile, and between the end of tile j and the last token before tile i
+    float lh[2][P::C], ll[2][P::C], enter[2][P::C], leave[2][P::C], row[2][P::C], col[2][P::C];
+    float gap[2][P::C / 16][P::C / 16];
     float total[2];
     int64_t bad[2];         // 1 + the last chunk with a z that is no number
 };
@@ -46,29 +50,32 @@ __device__ __forceinline__ void p_tile(Shared<P, KD>& s, int buf, int lane, floa
     f32x4 c = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int k = 0; k < KD / 32; ++k) c = P::mma(rows.get(s.y[buf], J, k), xf[k], c);
-    const float lh = s.lh[buf][16 * I + m], ll = s.ll[buf][16 * I + m];
-    const f32x4 jh = *reinterpret_cast<const f32x4*>(&s.lh[buf][16 * J + 4 * g]);
-    const f32x4 jl = *reinterpret_cast<const f32x4*>(&s.ll[buf][16 * J + 4 * g]);
-    float v[4];
+    f32x4 v;
+    if constexpr (I == J) {
+        const float lh = s.lh[buf][16 * I + m], ll = s.ll[buf][16 * I + m];
+        const f32x4 jh = *reinterpret_cast<const f32x4*>(&s.lh[buf][16 * J + 4 * g]);
+        const f32x4 jl = *reinterpret_cast<const f32x4*>(&s.ll[buf][16 * J + 4 * g]);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        v[r] = c[r] * (__builtin_amdgcn_exp2f((lh - jh[r]) + (ll - jl[r])) * scale);
-        if (I == J && 4 * g + r > m) v[r] = 0.f;
+        for (int r = 0; r < 4; ++r) {
+            v[r] = c[r] * (__builtin_amdgcn_exp2f((lh - jh[r]) + (ll - jl[r])) * scale);
+            if (4 * g + r > m) v[r] = 0.f;
+        }
+    } else {
+        // three factors of at most 1 in place of an exponential per pair
+        const float f = s.row[buf][16 * I + m] * s.gap[buf][I][J] * scale;
+        v = c * (*reinterpret_cast<const f32x4*>(&s.col[buf][16 * J + 4 * g]) * f);
     }
     typedef Tile<P, P::C, ROWS> TP;
     const int to = TP::at(m, 16 * J + 4 * g) + 16 * I * P::C;
     if constexpr (P::is_bf16) {
+        uint32_t w0[P::NO], w1[P::NO];
+        P::template split_pair<P::NO>(v[0], v[1], w0);
+        P::template split_pair<P::NO>(v[2], v[3], w1);
 #pragma unroll
-        for (int q = 0; q < P::NT; ++q) {
-            const uint32_t w0 = cvt_pk(v[0], v[1]), w1 = cvt_pk(v[2], v[3]);
-            *reinterpret_cast<uint2*>(s.p[q] + to) = uint2{w0, w1};
-            v[0] -= __uint_as_float(w0 << 16);
-            v[1] -= __uint_as_float(w0 & 0xffff0000u);
-            v[2] -= __uint_as_float(w1 << 16);
-            v[3] -= __uint_as_float(w1 & 0xffff0000u);
-        }
+        for (int q = 0; q < P::NO; ++q)
+            *reinterpret_cast<uint2*>(s.p[q] + to) = uint2{w0[q], w1[q]};
     } else {
-        *reinterpret_cast<f32x4*>(s.p[0] + to) = f32x4{v[0], v[1], v[2], v[3]};
+        *reinterpret_cast<f32x4*>(s.p[0] + to) = v;
     }
 }
 
@@ -116,7 +123,7 @@ __global__ __launch_bounds__(512) void chain_kernel(LaChain a) {
 
     if constexpr (OUT) {
         // tiles above the diagonal stay 0
-        for (int i = threadIdx.x; i < P::NT * C * C; i += 512) (&s.p[0][0])[i] = 0;
+        for (int i = threadIdx.x; i < P::NO * C * C; i += 512) (&s.p[0][0])[i] = 0;
         if (threadIdx.x < 2) s.bad[threadIdx.x] = 0;
         lds_barrier();
     }
@@ -170,7 +177,23 @@ __global__ __launch_bounds__(512) void chain_kernel(LaChain a) {
                 // running sums in 64 bits: behind a reset, the differences of sums far
                 // larger than themselves decide the factors
                 const double l = wave_scan64(base2(c.g)), end = lane64(l, C - 1);
+                double before = 0.0, own = end;     // L before this lane's tile, at its end
+                double last = 0.0;                  // at the end of tile i - 1
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    const double e = i + 1 < NI ? lane64(l, 16 * i + 15) : end;
+                    if (g == i) {
+                        before = last;
+                        own = e;
+                    }
+                    last = e;
+                }
                 if (lane < C) {
+                    s.row[buf][lane] = __builtin_amdgcn_exp2f((float)(l - before));
+                    s.col[buf][lane] = __builtin_amdgcn_exp2f((float)(own - l));
+                    // lane 16 i + j: gap of tiles i and j < i
+                    const double to = __shfl(l, 16 * m + 15, 64);
+                    if (m < g) s.gap[buf][g][m] = __builtin_amdgcn_exp2f((float)(before - to));
                     s.lh[buf][lane] = (float)l;
                     s.ll[buf][lane] = (float)(l - (double)(float)l);
                     s.enter[buf][lane] = inter * __builtin_amdgcn_exp2f((float)l);
@@ -255,8 +278,8 @@ __global__ __launch_bounds__(512) void chain_kernel(LaChain a) {
     const bool out16 = jb.out_bf16;
     const size_t oe = out16 ? 2 : 4;
     const uint32_t ot = (uint32_t)(jb.ot * (int64_t)oe);
-    char* ob = OUT ? static_cast<char*>(jb.out) + (at.b * jb.ob + at.h * jb.oh + zc + 4 * g) * oe
-                   : nullptr;
+    char* ob = OUT ? static_cast<char*>(jb.out) + (at.b * jb.ob + at.h * jb.oh) * oe : nullptr;
+    const uint32_t to = (back ? C - 1 - m : m) * ot + (zc + 4 * g) * (uint32_t)oe;
     const bool dots = GRAD && jb.dots;
     const char* rb = dots ? static_cast<const char*>(head_base(jb.r, at.b, at.h, sizeof(T))) +
                                 (zc + 4 * g) * sizeof(T)
@@ -293,14 +316,15 @@ __global__ __launch_bounds__(512) void chain_kernel(LaChain a) {
             for (int i = 0; i < NI; ++i) O[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int k = 0; k < NK; ++k) {
-                typename P::Terms ht;
-                P::split(f32x8{H[2 * k][0], H[2 * k][1], H[2 * k][2], H[2 * k][3], H[2 * k + 1][0],
-                               H[2 * k + 1][1], H[2 * k + 1][2], H[2 * k + 1][3]}, ht);
+                Terms<typename P::Frag, P::NO> ht;
+                P::template split<P::NO>(
+                    f32x8{H[2 * k][0], H[2 * k][1], H[2 * k][2], H[2 * k][3], H[2 * k + 1][0],
+                          H[2 * k + 1][1], H[2 * k + 1][2], H[2 * k + 1][3]}, ht);
                 typename P::Frag xf[NI];
 #pragma unroll
                 for (int i = 0; i < NI; ++i) xf[i] = rows.get(s.x[buf], i, k);
 #pragma unroll
-                for (int q = P::NT - 1; q >= 0; --q)
+                for (int q = P::NO - 1; q >= 0; --q)
 #pragma unroll
                     for (int i = 0; i < NI; ++i) O[i] = P::mma(ht.t[q], xf[i], O[i]);
             }
@@ -310,7 +334,7 @@ __global__ __launch_bounds__(512) void chain_kernel(LaChain a) {
 #pragma unroll
                 for (int j = 0; j < NJ; ++j)
 #pragma unroll
-                    for (int q = P::NT - 1; q >= 0; --q)
+                    for (int q = P::NO - 1; q >= 0; --q)
 #pragma unroll
                         for (int i = 2 * j; i < NI; ++i)
                             O[i] = P::mma(zf[j], prow.get(s.p[q], i, j), O[i]);
@@ -322,7 +346,7 @@ __global__ __launch_bounds__(512) void chain_kernel(LaChain a) {
                     for (int j = 0; j <= 16 * i + m; ++j) {
                         float pv = 0.f;
 #pragma unroll
-                        for (int q = P::NT - 1; q >= 0; --q) {
+                        for (int q = P::NO - 1; q >= 0; --q) {
                             const T w = s.p[q][TP::at(16 * i + m, j)];
                             if constexpr (P::is_bf16) pv += bf2f(w);
                             else pv += w;
@@ -355,22 +379,24 @@ __global__ __launch_bounds__(512) void chain_kernel(LaChain a) {
                 }
             }
             char* oc = ob + t0 * ot;
+            if (mine) {
 #pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                const int row = 16 * i + m;
-                if (row < len && mine) {
-                    char* p = oc + (uint32_t)(back ? len - 1 - row : row) * ot;
+                for (int i = 0; i < NI; ++i) {
+                    const int row = 16 * i + m;
+                    if (len < C && row >= len) continue;
+                    const uint32_t off = to + (back ? (uint32_t)(len - C - 16 * i) * ot
+                                                    : (uint32_t)(16 * i) * ot);
                     if (out16)
-                        *reinterpret_cast<u32x2_e2*>(p) =
+                        *reinterpret_cast<u32x2_e2*>(oc + off) =
                             u32x2_e2{cvt_pk(O[i][0], O[i][1]), cvt_pk(O[i][2], O[i][3])};
                     else
-                        *reinterpret_cast<f32x4_e4*>(p) = O[i];
+                        *reinterpret_cast<f32x4_e4*>(oc + off) = O[i];
                 }
             }
         }
         // the state at the chunk's end
         const float tot = s.total[buf];
-        typename P::Terms zt[NJ];
+        Terms<typename P::Frag, P::NS> zt[NJ];
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
             f32x8 v = P::widen(zf[j]);
@@ -378,7 +404,7 @@ __global__ __launch_bounds__(512) void chain_kernel(LaChain a) {
             const f32x4 l1 = *reinterpret_cast<const f32x4*>(&s.leave[buf][32 * j + 8 * g + 4]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] *= i < 4 ? l0[i & 3] : l1[i & 3];
-            P::split(v, zt[j]);
+            P::template split<P::NS>(v, zt[j]);
         }
 #pragma unroll
         for (int u = 0; u < NU; ++u) H[u] *= tot;
@@ -388,7 +414,7 @@ __global__ __launch_bounds__(512) void chain_kernel(LaChain a) {
 #pragma unroll
             for (int u = 0; u < NU; ++u) yf[u] = cols.get(s.y[buf], j, u >> 1, u & 1);
 #pragma unroll
-            for (int q = P::NT - 1; q >= 0; --q)
+            for (int q = P::NS - 1; q >= 0; --q)
 #pragma unroll
                 for (int u = 0; u < NU; ++u) H[u] = P::mma(yf[u], zt[j].t[q], H[u]);
         }
@@ -556,7 +582,10 @@ template <class P> hipError_t launch_chain_p(const LaChain& a) {
 
 // Jobs of one contraction width (all of a.job are on the same side of 64).
 hipError_t launch_chain(const LaChain& a) {
-    return a.bf16 ? launch_chain_p<Bf16>(a) : launch_chain_p<F32>(a);
+    if (!a.bf16) return launch_chain_p<F32>(a);
+    bool fine = false;          // whether an out is used in more than 16 bits
+    for (int j = 0; j < a.njobs; ++j) fine |= a.job[j].out && (!a.job[j].out_bf16 || a.job[j].dots);
+    return fine ? launch_chain_p<Bf16<3>>(a) : launch_chain_p<Bf16<2>>(a);
 }
 
 struct Plan {

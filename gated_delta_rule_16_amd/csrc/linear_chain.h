@@ -29,35 +29,45 @@ template <int KIND> __device__ __forceinline__ int swz(int row) {
     else return ((row & 3) << 1) | ((row >> 2) & 1);
 }
 
-// bf16 inputs: chunks of 64 tokens on the bf16 matrix cores.  A computed operand
-// enters as NT bf16 terms (24 bits with three).
-struct Bf16 {
+// A computed operand of a product: N bf16 terms, the largest first (or fp32 itself).
+template <class F, int N> struct Terms {
+    F t[N];
+};
+
+// bf16 inputs: chunks of 64 tokens on the bf16 matrix cores.  A computed operand of the
+// state enters as three bf16 terms (24 bits); one of out as NO terms: three, or two
+// (2^-17 of the operand) where out is rounded to bf16, 2^-9 of itself.
+template <int NO_> struct Bf16 {
     typedef bf16_t T;
     static constexpr bool is_bf16 = true;
     static constexpr int C = 64;
     static constexpr int EP = 8;    // elements per 16 bytes
-    static constexpr int NT = 3;
+    static constexpr int NO = NO_, NS = 3;
     typedef bf16x8 Frag;
-    struct Terms {
-        bf16x8 t[NT];               // the largest first
-    };
-    static __device__ __forceinline__ void split(const f32x8& x, Terms& o) {
-        uint32_t w[NT][4];
+    // x in N terms each.  The residuals x - hi come from dot products of the packed
+    // terms with (-1, 0) and (0, -1), exact as in split2.
+    template <int N>
+    static __device__ __forceinline__ void split_pair(float a, float b, uint32_t (&w)[N]) {
+        uint32_t ka, kb;
+        asm("s_mov_b32 %0, 0xbf80" : "=s"(ka));
+        asm("s_mov_b32 %0, 0xbf800000" : "=s"(kb));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float a = x[2 * i], b = x[2 * i + 1];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                w[n][i] = cvt_pk(a, b);
-                if (n + 1 < NT) {
-                    a -= __uint_as_float(w[n][i] << 16);
-                    b -= __uint_as_float(w[n][i] & 0xffff0000u);
-                }
+        for (int n = 0; n < N; ++n) {
+            w[n] = cvt_pk(a, b);
+            if (n + 1 < N) {
+                const bf16x2_t h = __builtin_bit_cast(bf16x2_t, w[n]);
+                a = __builtin_amdgcn_fdot2_f32_bf16(h, __builtin_bit_cast(bf16x2_t, ka), a, false);
+                b = __builtin_amdgcn_fdot2_f32_bf16(h, __builtin_bit_cast(bf16x2_t, kb), b, false);
             }
         }
+    }
+    template <int N> static __device__ __forceinline__ void split(const f32x8& x, Terms<Frag, N>& o) {
+        uint32_t w[4][N];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-            o.t[n] = __builtin_bit_cast(bf16x8, u32x4{w[n][0], w[n][1], w[n][2], w[n][3]});
+        for (int i = 0; i < 4; ++i) split_pair<N>(x[2 * i], x[2 * i + 1], w[i]);
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            o.t[n] = __builtin_bit_cast(bf16x8, u32x4{w[0][n], w[1][n], w[2][n], w[3][n]});
     }
     static __device__ __forceinline__ f32x8 widen(const Frag& f) {
         const u32x4 w = __builtin_bit_cast(u32x4, f);
@@ -72,6 +82,11 @@ struct Bf16 {
     static __device__ __forceinline__ f32x4 mma(const Frag& a, const Frag& b, const f32x4& c) {
         return mfma16(a, b, c);
     }
+    // Whether one of two packed values is infinite or no number: an exponent of all
+    // ones carries into the sign's place.
+    static __device__ __forceinline__ uint32_t bad(uint32_t v) {
+        return ((v & 0x7fff7fffu) + 0x00800080u) & 0x80008000u;
+    }
 };
 
 // fp32 inputs: chunks of 32 tokens on the fp32 matrix cores.  A lane's 8 elements of
@@ -81,17 +96,19 @@ struct F32 {
     static constexpr bool is_bf16 = false;
     static constexpr int C = 32;
     static constexpr int EP = 4;
-    static constexpr int NT = 1;
+    static constexpr int NO = 1, NS = 1;
     typedef f32x8 Frag;
-    struct Terms {
-        f32x8 t[1];
-    };
-    static __device__ __forceinline__ void split(const f32x8& x, Terms& o) { o.t[0] = x; }
+    template <int N> static __device__ __forceinline__ void split(const f32x8& x, Terms<Frag, N>& o) {
+        o.t[0] = x;
+    }
     static __device__ __forceinline__ f32x8 widen(const Frag& f) { return f; }
     static __device__ __forceinline__ f32x4 mma(const Frag& a, const Frag& b, f32x4 c) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) c = mfma_f32(a[i], b[i], c);
         return c;
+    }
+    static __device__ __forceinline__ uint32_t bad(uint32_t v) {
+        return ((v & 0x7fffffffu) + 0x00800000u) & 0x80000000u;
     }
 };
 
@@ -259,16 +276,12 @@ template <class P, int W, int KIND> struct Stage {
     }
     // Whether an element is infinite or no number.
     __device__ __forceinline__ bool bad() const {
-        bool any = false;
+        uint32_t any = 0;
 #pragma unroll
         for (int i = 0; i < N; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t v = w[i][j];
-                any |= (v & 0x7f800000u) == 0x7f800000u;
-                if constexpr (P::is_bf16) any |= (v & 0x7f80u) == 0x7f80u;
-            }
-        return any;
+            for (int j = 0; j < 4; ++j) any |= P::bad(w[i][j]);
+        return any != 0;
     }
 };
 

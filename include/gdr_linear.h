@@ -55,7 +55,8 @@ extern "C" {
  *
  * fp32 inputs are computed in fp32.  bf16 inputs run on the bf16 matrix cores with
  * fp32 accumulation; every computed operand enters as three bf16 terms, so products
- * carry the 24 bits of fp32.  Decays come from sums in 64 bits.  A value of v that
+ * carry the 24 bits of fp32 (two terms, 2^-17 of the operand, in products that only a
+ * bf16 o, dq, dk or dv takes).  Decays come from sums in 64 bits.  A value of v that
  * is infinite or no number reaches no token before it.
  */
 #define GDR_LA_HEAD_DECAY 1u
