@@ -41,15 +41,11 @@ template <class P, int KD> struct Shared {
     int64_t bad[2];         // 1 + the last chunk with a z that is no number
 };
 
-// Tile (i, j) of P^T (row 4 g + r: token j, column m: token i) into s.p.
+// A tile of P^T (row 4 g + r: token j, column m: token i) from its products.
 template <class P, int KD, int I, int J>
-__device__ __forceinline__ void p_tile(Shared<P, KD>& s, int buf, int lane, float scale,
-                                       const typename Tile<P, KD, BOTH>::Rows& rows,
-                                       const typename P::Frag (&xf)[KD / 32]) {
+__device__ __forceinline__ void p_store(Shared<P, KD>& s, int buf, int lane, float scale,
+                                        const f32x4& c) {
     const int g = lane >> 4, m = lane & 15;
-    f32x4 c = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int k = 0; k < KD / 32; ++k) c = P::mma(rows.get(s.y[buf], J, k), xf[k], c);
     f32x4 v;
     if constexpr (I == J) {
         const float lh = s.lh[buf][16 * I + m], ll = s.ll[buf][16 * I + m];
@@ -79,17 +75,25 @@ __device__ __forceinline__ void p_tile(Shared<P, KD>& s, int buf, int lane, floa
     }
 }
 
-// Tiles (I, J0 .. J1) of P^T.
-template <class P, int KD, int I, int J0, int J1>
-__device__ __forceinline__ void p_row(Shared<P, KD>& s, int buf, int lane, float scale,
-                                      const typename Tile<P, KD, ROWS>::Rows& xrow,
-                                      const typename Tile<P, KD, BOTH>::Rows& yrow) {
-    typename P::Frag xf[KD / 32];
+// Up to three tiles of P^T, (I0, J0) to (I2, J2) (I negative: none): all operands are
+// read before anything is written, so nothing waits for a tile before it.
+template <class P, int KD, int I0, int J0, int I1 = -1, int J1 = 0, int I2 = -1, int J2 = 0>
+__device__ __forceinline__ void p_tiles(Shared<P, KD>& s, int buf, int lane, float scale,
+                                        const typename Tile<P, KD, ROWS>::Rows& xrow,
+                                        const typename Tile<P, KD, BOTH>::Rows& yrow) {
+    constexpr int N = I1 < 0 ? 1 : I2 < 0 ? 2 : 3;
+    constexpr int I[3] = {I0, I1, I2}, J[3] = {J0, J1, J2};
+    f32x4 c[N];
 #pragma unroll
-    for (int k = 0; k < KD / 32; ++k) xf[k] = xrow.get(s.x[buf], I, k);
-    p_tile<P, KD, I, J0>(s, buf, lane, scale, yrow, xf);
-    if constexpr (J1 > J0) p_tile<P, KD, I, J0 + 1>(s, buf, lane, scale, yrow, xf);
-    if constexpr (J1 > J0 + 1) p_tile<P, KD, I, J0 + 2>(s, buf, lane, scale, yrow, xf);
+    for (int t = 0; t < N; ++t) c[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < KD / 32; ++k)
+#pragma unroll
+        for (int t = 0; t < N; ++t)
+            c[t] = P::mma(yrow.get(s.y[buf], J[t], k), xrow.get(s.x[buf], I[t], k), c[t]);
+    p_store<P, KD, I0, J0>(s, buf, lane, scale, c[0]);
+    if constexpr (N > 1) p_store<P, KD, I1, J1>(s, buf, lane, scale, c[1]);
+    if constexpr (N > 2) p_store<P, KD, I2, J2>(s, buf, lane, scale, c[2]);
 }
 
 // OUT: out is wanted (else the states at segments' ends alone).  GRAD: jobs may have
@@ -210,18 +214,17 @@ __global__ __launch_bounds__(512) void chain_kernel(LaChain a) {
             lds_barrier();
             if constexpr (OUT) {
                 if constexpr (NI == 4) {
-                    if (wv == 4) p_row<P, KD, 3, 0, 2>(s, buf, lane, pair, xrow, yrow);
-                    if (wv == 5) {
-                        p_row<P, KD, 1, 0, 1>(s, buf, lane, pair, xrow, yrow);
-                        p_row<P, KD, 3, 3, 3>(s, buf, lane, pair, xrow, yrow);
-                    }
-                    if (wv == 6) p_row<P, KD, 2, 0, 2>(s, buf, lane, pair, xrow, yrow);
-                    if (wv == 7) p_row<P, KD, 0, 0, 0>(s, buf, lane, pair, xrow, yrow);
+                    if (wv == 4)
+                        p_tiles<P, KD, 3, 0, 3, 1, 3, 2>(s, buf, lane, pair, xrow, yrow);
+                    if (wv == 5)
+                        p_tiles<P, KD, 2, 0, 2, 1, 2, 2>(s, buf, lane, pair, xrow, yrow);
+                    if (wv == 6) p_tiles<P, KD, 1, 0, 1, 1>(s, buf, lane, pair, xrow, yrow);
+                    if (wv == 7) p_tiles<P, KD, 3, 3, 0, 0>(s, buf, lane, pair, xrow, yrow);
                 } else {
                     static_assert(NI == 2, "two or four tiles of tokens");
-                    if (wv == 4) p_row<P, KD, 1, 0, 0>(s, buf, lane, pair, xrow, yrow);
-                    if (wv == 5) p_row<P, KD, 1, 1, 1>(s, buf, lane, pair, xrow, yrow);
-                    if (wv == 6) p_row<P, KD, 0, 0, 0>(s, buf, lane, pair, xrow, yrow);
+                    if (wv == 4) p_tiles<P, KD, 1, 0>(s, buf, lane, pair, xrow, yrow);
+                    if (wv == 5) p_tiles<P, KD, 1, 1>(s, buf, lane, pair, xrow, yrow);
+                    if (wv == 6) p_tiles<P, KD, 0, 0>(s, buf, lane, pair, xrow, yrow);
                 }
                 lds_barrier();
             }
@@ -378,21 +381,6 @@ __global__ __launch_bounds__(512) void chain_kernel(LaChain a) {
                     }
                 }
             }
-            char* oc = ob + t0 * ot;
-            if (mine) {
-#pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    const int row = 16 * i + m;
-                    if (len < C && row >= len) continue;
-                    const uint32_t off = to + (back ? (uint32_t)(len - C - 16 * i) * ot
-                                                    : (uint32_t)(16 * i) * ot);
-                    if (out16)
-                        *reinterpret_cast<u32x2_e2*>(oc + off) =
-                            u32x2_e2{cvt_pk(O[i][0], O[i][1]), cvt_pk(O[i][2], O[i][3])};
-                    else
-                        *reinterpret_cast<f32x4_e4*>(oc + off) = O[i];
-                }
-            }
         }
         // the state at the chunk's end
         const float tot = s.total[buf];
@@ -417,6 +405,24 @@ __global__ __launch_bounds__(512) void chain_kernel(LaChain a) {
             for (int q = P::NS - 1; q >= 0; --q)
 #pragma unroll
                 for (int u = 0; u < NU; ++u) H[u] = P::mma(yf[u], zt[j].t[q], H[u]);
+        }
+        if constexpr (OUT) {
+            // stores come last: at the stage's start they would queue behind A's loads
+            char* oc = ob + t0 * ot;
+            if (mine) {
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    const int row = 16 * i + m;
+                    if (len < C && row >= len) continue;
+                    const uint32_t off = to + (back ? (uint32_t)(len - C - 16 * i) * ot
+                                                    : (uint32_t)(16 * i) * ot);
+                    if (out16)
+                        *reinterpret_cast<u32x2_e2*>(oc + off) =
+                            u32x2_e2{cvt_pk(O[i][0], O[i][1]), cvt_pk(O[i][2], O[i][3])};
+                    else
+                        *reinterpret_cast<f32x4_e4*>(oc + off) = O[i];
+                }
+            }
         }
         if (GRAD && keep) {
             const int64_t mark = back ? t0 : t0 + len;

@@ -13,21 +13,17 @@ constexpr int ZB = 64;              // channels of z and out per workgroup
 constexpr float kLeast = -1e4f;     // log decays from here on are a reset: exp is 0
 
 // Tiles in LDS.  The 16-byte pieces of a row are permuted by the row so that operands
-// meet different banks: rows read 16 bytes a lane (8 lanes a cycle: 0-3 with 20-23,
-// 4-7 with 16-19 and so on), and 4x4 blocks read transposed (16 lanes a cycle).
+// meet different banks (64 of 4 bytes).  Rows read 16 bytes a lane go by lanes 0-3,
+// 12-15, 20-23 and 24-27, then 4-11, 16-19 and 28-31, and so on; blocks read
+// transposed, 8 bytes a lane, go by lanes 0-31 and 32-63.  With these orders every
+// read below is free of conflicts (measured; one of 8 rows for all kinds cost 868 of
+// 2474 LDS cycles a chunk).
 enum TileKind {
     ROWS,       // read by rows only
-    BOTH,       // by rows, and transposed 8 columns apart (bf16: odd rows also keep
+    BOTH,       // by rows, and transposed 8 columns apart (bf16: some rows also keep
                 // the halves of their pieces swapped)
     COLS        // read transposed only, 16 neighbouring columns at once
 };
-
-template <int KIND> __device__ __forceinline__ int swz(int row) {
-    if constexpr (KIND == ROWS) return row & 7;
-    else if constexpr (KIND == BOTH)
-        return (row & 1) | ((row & 4) >> 1) | ((row & 2) << 1);
-    else return ((row & 3) << 1) | ((row >> 2) & 1);
-}
 
 // A computed operand of a product: N bf16 terms, the largest first (or fp32 itself).
 template <class F, int N> struct Terms {
@@ -113,45 +109,58 @@ struct F32 {
 };
 
 // A tile of rows of W elements in LDS, and where a lane (g = lane / 16, m = lane % 16)
-// finds its operands in it.  The swizzle repeats every 8 rows, so offsets are a few
-// registers per lane and the rest constants.
+// finds its operands in it.
 template <class P, int W, int KIND> struct Tile {
     typedef typename P::T T;
     static constexpr int PPR = W / P::EP;           // 16-byte pieces per row
     static constexpr bool SWAP = KIND == BOTH && P::is_bf16;
+    static __device__ __forceinline__ int swizzle(int row) {
+        if constexpr (!P::is_bf16) return row & (PPR - 1) & 15;
+        else if constexpr (KIND == ROWS) return row & (PPR - 1);
+        else if constexpr (KIND == COLS) return (row & 2) | ((row & 8) >> 1);
+        else {
+            const int s = ((row & 2) << 1) | ((row & 4) >> 1);
+            return PPR == 16 ? s | (row & 9) : s;
+        }
+    }
+    static __device__ __forceinline__ bool swapped(int row) {
+        return SWAP && (PPR == 16 ? row & 1 : row & 8);
+    }
     static __device__ __forceinline__ int piece(int row, int c) {
-        return row * W + (c ^ swz<KIND>(row)) * P::EP;
+        return row * W + (c ^ swizzle(row)) * P::EP;
     }
     static __device__ __forceinline__ int at(int row, int col) {
         const int e = col % P::EP;
-        return piece(row, col / P::EP) + (SWAP ? e ^ ((row & 1) * 4) : e);
+        return piece(row, col / P::EP) + (swapped(row) ? e ^ 4 : e);
     }
 
-    // Elements 32 k + 8 g .. + 7 of row 16 i + m.
+    // Elements 32 k + 8 g .. + 7 of row 16 i + m (the swizzle repeats every 16 rows).
     struct Rows {
-        int o[2];
+        int o[P::is_bf16 ? W / 32 : 2 * (W / 32)];
         bool swap;
         __device__ __forceinline__ void init(int lane) {
             const int g = lane >> 4, m = lane & 15;
-            swap = SWAP && (m & 1);
-            if constexpr (P::is_bf16) {             // k's lowest bit meets the swizzle
-                o[0] = piece(m, g);
-                o[1] = m * W + ((4 + g) ^ swz<KIND>(m)) * P::EP;
-            } else {                                // two pieces
-                o[0] = piece(m, 2 * g);
-                o[1] = piece(m, 2 * g + 1);
+            swap = swapped(m);
+#pragma unroll
+            for (int k = 0; k < W / 32; ++k) {
+                if constexpr (P::is_bf16) {
+                    o[k] = piece(m, 4 * k + g);
+                } else {
+                    o[2 * k] = piece(m, 8 * k + 2 * g);
+                    o[2 * k + 1] = piece(m, 8 * k + 2 * g + 1);
+                }
             }
         }
         __device__ __forceinline__ typename P::Frag get(const T* t, int i, int k) const {
+            const T* p = t + 16 * i * W;
             if constexpr (P::is_bf16) {
-                u32x4 v = *reinterpret_cast<const u32x4*>(t + 16 * i * W + (k >> 1) * 64 + o[k & 1]);
+                u32x4 v = *reinterpret_cast<const u32x4*>(p + o[k]);
                 if constexpr (SWAP)
                     v = swap ? u32x4{v[2], v[3], v[0], v[1]} : v;
                 return __builtin_bit_cast(bf16x8, v);
             } else {
-                const T* p = t + 16 * i * W + 32 * k;
-                const f32x4 a = *reinterpret_cast<const f32x4*>(p + o[0]);
-                const f32x4 b = *reinterpret_cast<const f32x4*>(p + o[1]);
+                const f32x4 a = *reinterpret_cast<const f32x4*>(p + o[2 * k]);
+                const f32x4 b = *reinterpret_cast<const f32x4*>(p + o[2 * k + 1]);
                 return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
             }
         }
@@ -159,16 +168,16 @@ template <class P, int W, int KIND> struct Tile {
 
     // Rows 32 j + 8 g .. + 7 of column 32 k + 4 h + 8 (m / 4) + m % 4.
     struct Cols {
-        int o[P::is_bf16 ? 8 : 2];
+        int o[P::is_bf16 ? W / 8 : 2];
         __device__ __forceinline__ void init(int lane) {
             const int g = lane >> 4, m = lane & 15;
             if constexpr (P::is_bf16) {
-                // lane 4 r + c of a group points at 4 columns of row r (lds_tr16):
-                // by row half, k's lowest bit and h
+                // lane 4 r + c of a group points at 4 columns of row r (lds_tr16): by
+                // k, h and row half
 #pragma unroll
-                for (int q = 0; q < 8; ++q)
+                for (int q = 0; q < W / 8; ++q)
                     o[q] = at(8 * g + (m >> 2) + 4 * (q & 1),
-                              32 * ((q >> 1) & 1) + 4 * (q >> 2) + 8 * (m & 3));
+                              32 * (q >> 2) + 4 * ((q >> 1) & 1) + 8 * (m & 3));
             } else {
                 o[0] = g;
                 o[1] = 8 * (m >> 2) + (m & 3);
@@ -176,8 +185,8 @@ template <class P, int W, int KIND> struct Tile {
         }
         __device__ __forceinline__ typename P::Frag get(const T* t, int j, int k, int h) const {
             if constexpr (P::is_bf16) {
-                const T* p = t + 32 * j * W + (k >> 1) * 64;
-                const int q = 2 * (k & 1) + 4 * h;
+                const T* p = t + 32 * j * W;
+                const int q = 4 * k + 2 * h;
                 return pair(lds_tr16(p + o[q]), lds_tr16(p + o[q + 1]));
             } else {
                 f32x8 v;
@@ -226,9 +235,9 @@ template <class P, int W, int KIND> struct Tile {
 template <class P, int W, int KIND> struct Stage {
     static constexpr int PPR = W / P::EP;
     static constexpr int N = P::C * PPR / 256, STEP = P::C / N;
-    static_assert(STEP % 8 == 0, "the swizzle repeats every 8 rows");
+    typedef Tile<P, W, KIND> Tl;
     u32x4 w[N];
-    int row0, col, to;
+    int row0, col, c0;
     bool wide, narrow;              // whether the tensor has these channels, all of W
     uint32_t off;                   // bytes from a whole chunk's first token
     uint32_t step;                  // bytes from piece to piece
@@ -238,7 +247,7 @@ template <class P, int W, int KIND> struct Stage {
         wide = c < width;
         narrow = width < W;
         col = wide ? c : 0;
-        to = Tile<P, W, KIND>::piece(row0, tid % PPR);
+        c0 = tid % PPR;
         const uint32_t sb = (uint32_t)(st * sizeof(typename P::T));
         off = (back ? P::C - 1 - row0 : row0) * sb + col * (uint32_t)sizeof(typename P::T);
         step = STEP * sb;
@@ -270,8 +279,12 @@ template <class P, int W, int KIND> struct Stage {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             u32x4 v = w[i];
-            if constexpr (Tile<P, W, KIND>::SWAP) v = (row0 & 1) ? u32x4{v[2], v[3], v[0], v[1]} : v;
-            *reinterpret_cast<u32x4*>(tile + to + i * STEP * W) = v;
+            if constexpr (Tl::SWAP) v = Tl::swapped(row0) ? u32x4{v[2], v[3], v[0], v[1]} : v;
+            // the swizzle repeats every 16 rows
+            if constexpr (STEP % 16 == 0)
+                *reinterpret_cast<u32x4*>(tile + Tl::piece(row0, c0) + i * STEP * W) = v;
+            else
+                *reinterpret_cast<u32x4*>(tile + Tl::piece(row0 + i * STEP, c0)) = v;
         }
     }
     // Whether an element is infinite or no number.
