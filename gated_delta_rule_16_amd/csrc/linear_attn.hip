@@ -18,11 +18,17 @@
 // and the decay's gradient is what the exponents of all pairs around a token say:
 // dg_t = sum_{i >= t} (q_i . dq_i - k_i . dk_i) + <dS_T, S_T>.
 //
-// A workgroup of two teams follows one (sequence, head) for 64 of the out channels.
-// Team A (four waves) brings the next chunk from memory to LDS and forms its P; team
-// B carries the state: its wave w keeps channels 16 w .. 16 w + 15 in registers,
-// transposed, in the layout of a product's result, which is also that of the next
-// product's operand.  While A works on chunk n, B works on chunk n - 1.
+// A workgroup of 16 waves follows one (sequence, head) for 64 of the out channels, in
+// three teams (a wave of U and L and two of O to a SIMD) and two stages a chunk:
+//
+//   L (4 waves)  brings tiles: chunk n to LDS in stage 1; it asks for chunk n + 2 in
+//                both (40 KB at once would be more than a compute unit has in flight)
+//   U (4 waves)  carries the state: S through chunk n - 1, then S to LDS
+//   O (8 waves)  forms the out: out of chunk n - 1, then P of chunk n; one of its waves
+//                the factors of chunk n + 1
+//
+// Wave w of U keeps channels 16 w .. 16 w + 15 of the state in registers, transposed, in
+// the layout of a product's result, which is also that of the next product's operand.
 #include "linear_chain.h"
 
 namespace gdr {
@@ -31,80 +37,323 @@ namespace {
 
 template <class P, int KD> struct Shared {
     typename P::T x[2][P::C * KD], y[2][P::C * KD], z[2][P::C * ZB];
-    typename P::T p[P::NO][P::C * P::C];
-    // the running log decay (base 2) in two terms, and factors: from the chunk's start,
-    // to its end, from the last token of the tile of 16 before, to the end of the own
-    // tile, and between the end of tile j and the last token before tile i
-    float lh[2][P::C], ll[2][P::C], enter[2][P::C], leave[2][P::C], row[2][P::C], col[2][P::C];
+    typename P::T p[P::NO][PTile<P>::SIZE];
+    typename P::T h[P::NO][ZB * KD];        // the state's terms, rows of z's channels
+    // factors of the running log decay: from the chunk's start, to its end
+    float enter[2][P::C], leave[2][P::C], total[2];
+    int bad[2];             // 1 + the last chunk with a z that is no number
+    // the running log decay (base 2) in two terms; factors from the last token of the
+    // tile of 16 before, to the end of the own tile, and between the end of tile j and
+    // the last token before tile i
+    float lh[2][P::C], ll[2][P::C], row[2][P::C], col[2][P::C];
     float gap[2][P::C / 16][P::C / 16];
-    float total[2];
-    int64_t bad[2];         // 1 + the last chunk with a z that is no number
 };
 
-// A tile of P^T (row 4 g + r: token j, column m: token i) from its products.
-template <class P, int KD, int I, int J>
-__device__ __forceinline__ void p_store(Shared<P, KD>& s, int buf, int lane, float scale,
-                                        const f32x4& c) {
-    const int g = lane >> 4, m = lane & 15;
-    f32x4 v;
-    if constexpr (I == J) {
-        const float lh = s.lh[buf][16 * I + m], ll = s.ll[buf][16 * I + m];
-        const f32x4 jh = *reinterpret_cast<const f32x4*>(&s.lh[buf][16 * J + 4 * g]);
-        const f32x4 jl = *reinterpret_cast<const f32x4*>(&s.ll[buf][16 * J + 4 * g]);
+// What the states alone need of it.
+template <class P, int KD> struct StatesShared {
+    typename P::T y[2][P::C * KD], z[2][P::C * ZB];
+    float leave[2][P::C], total[2];
+};
+
+// Operands of tile (i, j) of P^T, and the tile from them (row 4 g + r: token j, column
+// m: token i).  They are read a tile ahead of their use.
+template <class P, int KD> struct PTileWork {
+    static constexpr int NK = KD / 32;
+    typename P::Frag xf[NK], yf[NK];
+    __device__ __forceinline__ void read(const typename P::T* x, const typename P::T* y, int i,
+                                         int j, const typename Tile<P, KD, ROWS>::Rows& xrow,
+                                         const typename Tile<P, KD, BOTH>::Rows& yrow) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            v[r] = c[r] * (__builtin_amdgcn_exp2f((lh - jh[r]) + (ll - jl[r])) * scale);
-            if (4 * g + r > m) v[r] = 0.f;
+        for (int k = 0; k < NK; ++k) {
+            xf[k] = xrow.raw(x, i, k);
+            yf[k] = yrow.raw(y, j, k);
         }
-    } else {
-        // three factors of at most 1 in place of an exponential per pair
-        const float f = s.row[buf][16 * I + m] * s.gap[buf][I][J] * scale;
-        v = c * (*reinterpret_cast<const f32x4*>(&s.col[buf][16 * J + 4 * g]) * f);
     }
-    typedef Tile<P, P::C, ROWS> TP;
-    const int to = TP::at(m, 16 * J + 4 * g) + 16 * I * P::C;
-    if constexpr (P::is_bf16) {
-        uint32_t w0[P::NO], w1[P::NO];
-        P::template split_pair<P::NO>(v[0], v[1], w0);
-        P::template split_pair<P::NO>(v[2], v[3], w1);
+    __device__ __forceinline__ void write(Shared<P, KD>& s, int pb, int i, int j, int lane,
+                                          float scale,
+                                          const typename Tile<P, KD, BOTH>::Rows& yrow) {
+        const int g = lane >> 4, m = lane & 15;
+        f32x4 c = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int q = 0; q < P::NO; ++q)
-            *reinterpret_cast<uint2*>(s.p[q] + to) = uint2{w0[q], w1[q]};
-    } else {
-        *reinterpret_cast<f32x4*>(s.p[0] + to) = v;
+        for (int k = 0; k < NK; ++k) c = P::mma(yrow.order(yf[k]), xf[k], c);
+        f32x4 v;
+        if (i == j) {
+            const float lh = s.lh[pb][16 * i + m], ll = s.ll[pb][16 * i + m];
+            const f32x4 jh = *reinterpret_cast<const f32x4*>(&s.lh[pb][16 * j + 4 * g]);
+            const f32x4 jl = *reinterpret_cast<const f32x4*>(&s.ll[pb][16 * j + 4 * g]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                v[r] = c[r] * (__builtin_amdgcn_exp2f((lh - jh[r]) + (ll - jl[r])) * scale);
+                if (4 * g + r > m) v[r] = 0.f;
+            }
+        } else {
+            // three factors of at most 1 in place of an exponential per pair
+            const float f = s.row[pb][16 * i + m] * s.gap[pb][i][j] * scale;
+            v = c * (*reinterpret_cast<const f32x4*>(&s.col[pb][16 * j + 4 * g]) * f);
+        }
+        typedef PTile<P> TP;
+        const int to = TP::piece(m, ((j & 1) * 16 + 4 * g) / P::EP) + 4 * g % P::EP +
+                       TP::tile(i, j);
+        if constexpr (P::is_bf16) {
+            uint32_t w0[P::NO], w1[P::NO];
+            P::template split_pair<P::NO>(v[0], v[1], w0);
+            P::template split_pair<P::NO>(v[2], v[3], w1);
+#pragma unroll
+            for (int q = 0; q < P::NO; ++q)
+                *reinterpret_cast<uint2*>(s.p[q] + to) = uint2{w0[q], w1[q]};
+        } else {
+            *reinterpret_cast<f32x4*>(s.p[0] + to) = v;
+        }
     }
-}
+};
 
-// Up to three tiles of P^T, (I0, J0) to (I2, J2) (I negative: none): all operands are
-// read before anything is written, so nothing waits for a tile before it.
-template <class P, int KD, int I0, int J0, int I1 = -1, int J1 = 0, int I2 = -1, int J2 = 0>
-__device__ __forceinline__ void p_tiles(Shared<P, KD>& s, int buf, int lane, float scale,
-                                        const typename Tile<P, KD, ROWS>::Rows& xrow,
-                                        const typename Tile<P, KD, BOTH>::Rows& yrow) {
-    constexpr int N = I1 < 0 ? 1 : I2 < 0 ? 2 : 3;
-    constexpr int I[3] = {I0, I1, I2}, J[3] = {J0, J1, J2};
-    f32x4 c[N];
-#pragma unroll
-    for (int t = 0; t < N; ++t) c[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int k = 0; k < KD / 32; ++k)
-#pragma unroll
-        for (int t = 0; t < N; ++t)
-            c[t] = P::mma(yrow.get(s.y[buf], J[t], k), xrow.get(s.x[buf], I[t], k), c[t]);
-    p_store<P, KD, I0, J0>(s, buf, lane, scale, c[0]);
-    if constexpr (N > 1) p_store<P, KD, I1, J1>(s, buf, lane, scale, c[1]);
-    if constexpr (N > 2) p_store<P, KD, I2, J2>(s, buf, lane, scale, c[2]);
-}
+// Team L: tiles and factors of the chunks, from memory to LDS.
+template <class P, int KD, bool OUT> struct Bringer {
+    typedef typename P::T T;
+    // what is on its way for one chunk
+    struct Coming {
+        Stage<P, KD, ROWS> x;
+        Stage<P, KD, BOTH> y;
+        Stage<P, ZB, COLS> z;
+    };
+    const char *xb, *yb, *zb;
+    int64_t xt, yt, zt;
+    bool back;
 
-// OUT: out is wanted (else the states at segments' ends alone).  GRAD: jobs may have
-// kept states and dots.
-template <class P, int KD, bool OUT, bool GRAD>
-__global__ __launch_bounds__(512) void chain_kernel(LaChain a) {
-    constexpr int C = P::C, NU = KD / 16, NK = KD / 32, NI = C / 16, NJ = C / 32;
+    __device__ __forceinline__ Bringer(const Place& at, const LaJob& jb, int tid, Coming& c)
+        : back(jb.back) {
+        xb = OUT ? static_cast<const char*>(head_base(jb.x, at.b, at.h, sizeof(T))) : nullptr;
+        yb = static_cast<const char*>(head_base(jb.y, at.b, at.h, sizeof(T)));
+        zb = static_cast<const char*>(head_base(jb.z, at.b, at.h, sizeof(T))) +
+             at.zb * ZB * sizeof(T);
+        xt = jb.x.st;
+        yt = jb.y.st;
+        zt = jb.z.st;
+        if constexpr (OUT) c.x.init(tid, jb.kd, xt, back);
+        c.y.init(tid, jb.kd, yt, back);
+        c.z.init(tid, jb.zd - at.zb * ZB, zt, back);
+    }
+    __device__ __forceinline__ void ask_x(int64_t t0, int len, Coming& c) {
+        if constexpr (OUT) c.x.load(xb + t0 * xt * (int)sizeof(T), xt, len, back);
+    }
+    __device__ __forceinline__ void ask_yz(int64_t t0, int len, Coming& c) {
+        c.y.load(yb + t0 * yt * (int)sizeof(T), yt, len, back);
+        c.z.load(zb + t0 * zt * (int)sizeof(T), zt, len, back);
+    }
+    template <class S> __device__ __forceinline__ void put_yz(S& s, int64_t n, int len, Coming& c) {
+        const int buf = (int)(n & 1);
+        c.y.put(s.y[buf], len);
+        c.z.put(s.z[buf], len);
+        if constexpr (OUT) {
+            if (c.z.bad()) s.bad[buf] = (int)(n + 1);
+        }
+    }
+};
+
+// The factors of the chunks' decays, by one wave.
+template <class P, bool OUT> struct Decays {
+    static constexpr int C = P::C, NI = C / 16;
+    const LaChain& a;
+    const Place& at;
+    int lane;
+    float inter, upd;
+    bool back;
+    float next;                     // the lane's log decay of the chunk to be scanned next
+    double run;
+
+    __device__ __forceinline__ Decays(const LaChain& a_, const Place& at_, const LaJob& jb,
+                                      int lane_)
+        : a(a_), at(at_), lane(lane_), inter(jb.inter), upd(jb.upd), back(jb.back), next(0.f),
+          run(0.0) {}
+    __device__ __forceinline__ void ask(int64_t t0, int len) {
+        next = 0.f;
+        if (lane < len) next = decay_of(a, at.b, at.h, back ? t0 + len - lane : t0 + lane);
+    }
+    // Factors of chunk n.  Running sums are in 64 bits: behind a reset, the differences
+    // of sums far larger than themselves decide the factors.
+    template <class S> __device__ __forceinline__ void scan(S& s, int64_t n) {
+        const int buf = (int)(n & 1), g = lane >> 4, m = lane & 15;
+        const double l = wave_scan64(base2(next)), end = lane64(l, C - 1);
+        double before = 0.0, own = end;     // L before this lane's tile, at its end
+        double last = 0.0;                  // at the end of tile i - 1
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const double e = i + 1 < NI ? lane64(l, 16 * i + 15) : end;
+            if (g == i) {
+                before = last;
+                own = e;
+            }
+            last = e;
+        }
+        if (lane < C) {
+            if constexpr (OUT) {
+                s.row[buf][lane] = __builtin_amdgcn_exp2f((float)(l - before));
+                s.col[buf][lane] = __builtin_amdgcn_exp2f((float)(own - l));
+                // lane 16 i + j: gap of tiles i and j < i
+                const double to = __shfl(l, 16 * m + 15, 64);
+                if (m < g) s.gap[buf][g][m] = __builtin_amdgcn_exp2f((float)(before - to));
+                s.lh[buf][lane] = (float)l;
+                s.ll[buf][lane] = (float)(l - (double)(float)l);
+                s.enter[buf][lane] = inter * __builtin_amdgcn_exp2f((float)l);
+            }
+            s.leave[buf][lane] = upd * __builtin_amdgcn_exp2f((float)(end - l));
+        }
+        if (lane == 0) s.total[buf] = __builtin_amdgcn_exp2f((float)end);
+        run += end;
+    }
+};
+
+// Team U: the state of 16 channels of z per wave, transposed: tile u = 2 k + h, row
+// 4 g + r, is channel 32 k + 8 g + 4 h + r of x and y, column m channel zc + m.
+template <class P, int KD> struct State {
+    typedef Tile<P, KD, BOTH> TY;
+    typedef Tile<P, ZB, COLS> TZ;
+    static constexpr int NU = KD / 16, NJ = P::C / 32;
+    f32x4 H[NU];
+    Terms<typename P::Frag, P::NS> zt[NJ];
+    float tot;
+    int g, m, zc, zd, kd;
+    int64_t hz, hk;
+    typename TY::Cols cols;
+    typename TZ::Col16 zcol;
+
+    __device__ __forceinline__ State(const LaJob& jb, int zb, int tid) {
+        const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+        g = lane >> 4;
+        m = lane & 15;
+        zc = zb * ZB + 16 * w;
+        zd = jb.zd;
+        kd = jb.kd;
+        hz = jb.hz;
+        hk = jb.hk;
+        cols.init(lane);
+        zcol.init(lane, 16 * w);
+#pragma unroll
+        for (int u = 0; u < NU; ++u) H[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    __device__ __forceinline__ bool has(int u) const {
+        return zc + m < zd && 32 * (u >> 1) + 8 * g < kd;
+    }
+    // The lane's first element of the state in memory.  Formed anew where it is used:
+    // all the offsets, kept over the loop, would not leave registers for the rest.
+    __device__ __forceinline__ int first() const {
+        int e = (zc + m) * (int)hz + 8 * g * (int)hk;
+        asm volatile("" : "+v"(e));
+        return e;
+    }
+    __device__ __forceinline__ void load(const float* p) {
+        p += first();
+#pragma unroll
+        for (int u = 0; u < NU; ++u)
+            if (has(u)) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) H[u][r] = p[(32 * (u >> 1) + 4 * (u & 1) + r) * (int)hk];
+            }
+    }
+    __device__ __forceinline__ void store(float* p, float f) const {
+        p += first();
+#pragma unroll
+        for (int u = 0; u < NU; ++u)
+            if (has(u)) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    p[(32 * (u >> 1) + 4 * (u & 1) + r) * (int)hk] = H[u][r] * f;
+            }
+    }
+    // z of the chunk in `buf`, scaled to the chunk's end, as terms
+    template <class S> __device__ __forceinline__ void take(const S& s, int buf) {
+        tot = s.total[buf];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            f32x8 v = P::widen(zcol.get(s.z[buf], j));
+            const f32x4 l0 = *reinterpret_cast<const f32x4*>(&s.leave[buf][32 * j + 8 * g]);
+            const f32x4 l1 = *reinterpret_cast<const f32x4*>(&s.leave[buf][32 * j + 8 * g + 4]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] *= i < 4 ? l0[i & 3] : l1[i & 3];
+            P::template split<P::NS>(v, zt[j]);
+        }
+    }
+    // through that chunk
+    template <class S> __device__ __forceinline__ void move(const S& s, int buf) {
+#pragma unroll
+        for (int u = 0; u < NU; ++u) H[u] *= tot;
+        // four tiles at a time, the next four's operands on their way: more would not
+        // fit the registers, and a spill waits behind L's loads
+        constexpr int NG = NJ * NU / 4;
+        typename P::Frag yf[2][4];
+        auto fetch = [&](int i) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int u = i % (NU / 4) * 4 + e;
+                yf[i & 1][e] = cols.get(s.y[buf], i / (NU / 4), u >> 1, u & 1);
+            }
+        };
+        fetch(0);
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+            if (i + 1 < NG) fetch(i + 1);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int q = P::NS - 1; q >= 0; --q)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int u = i % (NU / 4) * 4 + e;
+                    H[u] = P::mma(yf[i & 1][e], zt[i / (NU / 4)].t[q], H[u]);
+                }
+        }
+    }
+    // its terms to LDS, rows of z's channels
+    __device__ __forceinline__ void show(Shared<P, KD>& s, int w) const {
+        typedef Tile<P, KD, ROWS> TH;
+        int m = this->m;                // places formed anew, as in first()
+        asm volatile("" : "+v"(m));
+#pragma unroll
+        for (int k = 0; k < KD / 32; ++k) {
+            const f32x8 v = {H[2 * k][0], H[2 * k][1], H[2 * k][2], H[2 * k][3],
+                             H[2 * k + 1][0], H[2 * k + 1][1], H[2 * k + 1][2], H[2 * k + 1][3]};
+            if constexpr (P::is_bf16) {
+                Terms<typename P::Frag, P::NO> t;
+                P::template split<P::NO>(v, t);
+#pragma unroll
+                for (int q = 0; q < P::NO; ++q)
+                    *reinterpret_cast<u32x4*>(s.h[q] + 16 * w * KD + TH::piece(m, 4 * k + g)) =
+                        __builtin_bit_cast(u32x4, t.t[q]);
+            } else {
+                *reinterpret_cast<f32x4*>(s.h[0] + 16 * w * KD + TH::piece(m, 8 * k + 2 * g)) =
+                    H[2 * k];
+                *reinterpret_cast<f32x4*>(s.h[0] + 16 * w * KD + TH::piece(m, 8 * k + 2 * g + 1)) =
+                    H[2 * k + 1];
+            }
+        }
+    }
+};
+
+// Tokens [ta, tb) of a segment in chunks, in the chain's order.
+struct Chunks {
+    int64_t ta, tb, nc;
+    int C;
+    bool back;
+    __device__ __forceinline__ Chunks(const LaChain& a, const Place& at, bool back_, int C_)
+        : C(C_), back(back_) {
+        ta = at.seg * a.L;
+        tb = ta + a.L < a.T ? ta + a.L : a.T;
+        nc = (tb - ta + C - 1) / C;
+    }
+    // chunk n: tokens t0 .. t0 + len - 1, rows from the first on (back: from the last)
+    __device__ __forceinline__ void get(int64_t n, int64_t& t0, int& len) const {
+        t0 = ta + (back ? nc - 1 - n : n) * C;
+        len = (int)(tb - t0 < C ? tb - t0 : C);
+    }
+};
+
+// The chain's out (and its states).  GRAD: jobs may have kept states and dots.
+template <class P, int KD, bool GRAD>
+__global__ __launch_bounds__(1024) void chain_kernel(LaChain a) {
+    constexpr int C = P::C, NK = KD / 32, NI = C / 16, NT = NI / 2;
     typedef Tile<P, KD, ROWS> TX;
     typedef Tile<P, KD, BOTH> TY;
     typedef Tile<P, ZB, COLS> TZ;
-    typedef Tile<P, C, ROWS> TP;
+    typedef PTile<P> TP;
     typedef typename P::T T;
     extern __shared__ __attribute__((aligned(16))) char smem[];
     Shared<P, KD>& s = *reinterpret_cast<Shared<P, KD>*>(smem);
@@ -112,268 +361,220 @@ __global__ __launch_bounds__(512) void chain_kernel(LaChain a) {
     Place at;
     if (!place(a, blockIdx.x, at)) return;
     const LaJob& jb = a.job[at.job];
-    const bool back = jb.back;
-    const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
+    const Chunks ch(a, at, jb.back, C);
+    const int64_t nc = ch.nc, bh = at.b * a.H + at.h;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int64_t ta = at.seg * a.L, tb = ta + a.L < a.T ? ta + a.L : a.T;
-    const int64_t nc = (tb - ta + C - 1) / C;
-    const int64_t bh = at.b * a.H + at.h;
-    // chunk n of the chain: tokens t0 .. t0 + len - 1, rows from the first on (back:
-    // from the last)
-    auto bounds = [&](int64_t n, int64_t& t0, int& len) {
-        t0 = ta + (back ? nc - 1 - n : n) * C;
-        len = (int)(tb - t0 < C ? tb - t0 : C);
-    };
+    const bool back = jb.back;
 
-    if constexpr (OUT) {
-        // tiles above the diagonal stay 0
-        for (int i = threadIdx.x; i < P::NO * C * C; i += 512) (&s.p[0][0])[i] = 0;
-        if (threadIdx.x < 2) s.bad[threadIdx.x] = 0;
-        lds_barrier();
-    }
+    // tiles above the diagonal stay 0
+    for (int i = threadIdx.x; i < P::NO * TP::SIZE; i += 1024) (&s.p[0][0])[i] = 0;
+    if (threadIdx.x < 2) s.bad[threadIdx.x] = 0;
 
-    if (wv >= 4) {
-        // ---- team A ----
-        const int tid = threadIdx.x - 256;
-        const char* xb = OUT ? static_cast<const char*>(head_base(jb.x, at.b, at.h, sizeof(T)))
-                             : nullptr;
-        const char* yb = static_cast<const char*>(head_base(jb.y, at.b, at.h, sizeof(T)));
-        const char* zb = static_cast<const char*>(head_base(jb.z, at.b, at.h, sizeof(T))) +
-                         at.zb * ZB * sizeof(T);
-        const int64_t xt = jb.x.st, yt = jb.y.st, zt = jb.z.st;
-        const float pair = jb.pair, inter = jb.inter, upd = jb.upd;
-        // two chunks on their way: the next but one is asked for before the next is
-        // waited for
-        struct Coming {
-            Stage<P, KD, ROWS> x;
-            Stage<P, KD, BOTH> y;
-            Stage<P, ZB, COLS> z;
-            float g;
-        } even, odd;
-        if constexpr (OUT) even.x.init(tid, jb.kd, xt, back);
-        even.y.init(tid, jb.kd, yt, back);
-        even.z.init(tid, jb.zd - at.zb * ZB, zt, back);
+    if (wv >= 12) {
+        // ---- team L ----
+        typedef Bringer<P, KD, true> L;
+        typename L::Coming even, odd;
+        L l(at, jb, threadIdx.x - 768, even);
         odd = even;
-        typename TX::Rows xrow;
-        typename TY::Rows yrow;
-        xrow.init(lane);
-        yrow.init(lane);
-        double run = 0.0;
-        auto fetch = [&](int64_t n, Coming& c) {
-            int64_t t0;
-            int len;
-            bounds(n, t0, len);
-            if (wv == 7) {
-                c.g = 0.f;
-                if (lane < len)
-                    c.g = decay_of(a, at.b, at.h, back ? t0 + len - lane : t0 + lane);
-            }
-            if constexpr (OUT) c.x.load(xb + t0 * xt * (int)sizeof(T), xt, len, back);
-            c.y.load(yb + t0 * yt * (int)sizeof(T), yt, len, back);
-            c.z.load(zb + t0 * zt * (int)sizeof(T), zt, len, back);
-        };
-        auto turn = [&](int64_t n, Coming& c) {
-            const int buf = (int)(n & 1);
-            int64_t t0;
-            int len;
-            bounds(n, t0, len);
-            if (wv == 7) {
-                // running sums in 64 bits: behind a reset, the differences of sums far
-                // larger than themselves decide the factors
-                const double l = wave_scan64(base2(c.g)), end = lane64(l, C - 1);
-                double before = 0.0, own = end;     // L before this lane's tile, at its end
-                double last = 0.0;                  // at the end of tile i - 1
-#pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    const double e = i + 1 < NI ? lane64(l, 16 * i + 15) : end;
-                    if (g == i) {
-                        before = last;
-                        own = e;
-                    }
-                    last = e;
-                }
-                if (lane < C) {
-                    s.row[buf][lane] = __builtin_amdgcn_exp2f((float)(l - before));
-                    s.col[buf][lane] = __builtin_amdgcn_exp2f((float)(own - l));
-                    // lane 16 i + j: gap of tiles i and j < i
-                    const double to = __shfl(l, 16 * m + 15, 64);
-                    if (m < g) s.gap[buf][g][m] = __builtin_amdgcn_exp2f((float)(before - to));
-                    s.lh[buf][lane] = (float)l;
-                    s.ll[buf][lane] = (float)(l - (double)(float)l);
-                    s.enter[buf][lane] = inter * __builtin_amdgcn_exp2f((float)l);
-                    s.leave[buf][lane] = upd * __builtin_amdgcn_exp2f((float)(end - l));
-                }
-                if (lane == 0) s.total[buf] = __builtin_amdgcn_exp2f((float)end);
-                run += end;
-            }
-            if constexpr (OUT) c.x.put(s.x[buf], len);
-            c.y.put(s.y[buf], len);
-            c.z.put(s.z[buf], len);
-            if (OUT && c.z.bad()) s.bad[buf] = n + 1;
-            if (n + 2 < nc) fetch(n + 2, c);
-            lds_barrier();
-            if constexpr (OUT) {
-                if constexpr (NI == 4) {
-                    if (wv == 4)
-                        p_tiles<P, KD, 3, 0, 3, 1, 3, 2>(s, buf, lane, pair, xrow, yrow);
-                    if (wv == 5)
-                        p_tiles<P, KD, 2, 0, 2, 1, 2, 2>(s, buf, lane, pair, xrow, yrow);
-                    if (wv == 6) p_tiles<P, KD, 1, 0, 1, 1>(s, buf, lane, pair, xrow, yrow);
-                    if (wv == 7) p_tiles<P, KD, 3, 3, 0, 0>(s, buf, lane, pair, xrow, yrow);
-                } else {
-                    static_assert(NI == 2, "two or four tiles of tokens");
-                    if (wv == 4) p_tiles<P, KD, 1, 0>(s, buf, lane, pair, xrow, yrow);
-                    if (wv == 5) p_tiles<P, KD, 1, 1>(s, buf, lane, pair, xrow, yrow);
-                    if (wv == 6) p_tiles<P, KD, 0, 0>(s, buf, lane, pair, xrow, yrow);
-                }
-                lds_barrier();
-            }
-        };
-        fetch(0, even);
-        if (nc > 1) fetch(1, odd);
-        for (int64_t n = 0; n < nc; n += 2) {
-            turn(n, even);
-            if (n + 1 < nc) turn(n + 1, odd);
+        int64_t t0;
+        int len;
+        ch.get(0, t0, len);
+        l.ask_x(t0, len, even);
+        l.ask_yz(t0, len, even);
+        if (nc > 1) {
+            ch.get(1, t0, len);
+            l.ask_x(t0, len, odd);
+            l.ask_yz(t0, len, odd);
         }
-        // B's last chunk
         lds_barrier();
-        if constexpr (OUT) lds_barrier();
-        if (!OUT && jb.seg_decay && at.zb == 0 && wv == 7 && lane == 0)
-            jb.seg_decay[at.seg * a.B * a.H + bh] = __builtin_amdgcn_exp2f((float)run);
+        auto turn = [&](int64_t n, typename L::Coming& c) {
+            int64_t t0, t2 = 0;
+            int len, len2 = 0;
+            if (n + 2 < nc) ch.get(n + 2, t2, len2);
+            if (n < nc) {
+                ch.get(n, t0, len);
+                c.x.put(s.x[n & 1], len);
+                if (n + 2 < nc) l.ask_x(t2, len2, c);
+                l.put_yz(s, n, len, c);
+            }
+            lds_barrier();
+            if (n + 2 < nc) l.ask_yz(t2, len2, c);
+            lds_barrier();
+        };
+        for (int64_t n = 0; n <= nc; n += 2) {
+            turn(n, even);
+            if (n + 1 <= nc) turn(n + 1, odd);
+        }
+        return;
+    }
+    if (wv >= 8) {
+        // ---- team U ----
+        State<P, KD> st(jb, at.zb, threadIdx.x - 512);
+        if (jb.h_in) st.load(jb.h_in + (at.seg * a.B * a.H + bh) * a.state);
+        float* const keep = GRAD ? jb.keep : nullptr;
+        lds_barrier();
+        for (int64_t n = 0; n <= nc; ++n) {
+            if (n > 0) st.move(s, (int)((n - 1) & 1));
+            lds_barrier();
+            if (n < nc) {
+                st.show(s, wv - 8);
+                st.take(s, (int)(n & 1));
+            }
+            if (GRAD && keep && n > 0) {
+                int64_t t0;
+                int len;
+                ch.get(n - 1, t0, len);
+                const int64_t mark = back ? t0 : t0 + len;
+                if (back ? (mark > 0 && mark % a.every == 0)
+                         : (mark < a.T ? mark % a.every == 0 : jb.keep_end))
+                    st.store(keep + (((mark + a.every - 1) / a.every - 1) * a.B * a.H + bh) *
+                                        a.state, 1.f);
+            }
+            lds_barrier();
+        }
+        if (jb.h_out && at.seg == (back ? 0 : a.nseg - 1)) {
+            float f = 1.f;
+            if (jb.end_decay)
+                f = __builtin_amdgcn_exp2f((float)base2(decay_of(a, at.b, at.h, 0)));
+            st.store(jb.h_out + bh * a.state, f);
+        }
         return;
     }
 
-    // ---- team B ----
-    const int zd = jb.zd, zc = at.zb * ZB + 16 * wv;    // this wave's first channel
-    // state, transposed: tile u = 2 k + h, row 4 g + r, is channel 32 k + 8 g + 4 h + r
-    // of x and y, column m channel zc + m
-    f32x4 H[NU];
-    auto hoff = [&](int u, int r) {
-        return (int64_t)(zc + m) * jb.hz + (int64_t)(32 * (u >> 1) + 8 * g + 4 * (u & 1) + r) * jb.hk;
-    };
-    auto hok = [&](int u) { return zc + m < zd && 32 * (u >> 1) + 8 * g < jb.kd; };
-#pragma unroll
-    for (int u = 0; u < NU; ++u) {
-        H[u] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (OUT && jb.h_in && hok(u)) {
-            const float* p = jb.h_in + (at.seg * a.B * a.H + bh) * a.state;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) H[u][r] = p[hoff(u, r)];
-        }
-    }
-    auto h_store = [&](float* p, float f) {
-#pragma unroll
-        for (int u = 0; u < NU; ++u)
-            if (hok(u)) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r) p[hoff(u, r)] = H[u][r] * f;
-            }
-    };
-    typename TX::Rows rows;
-    typename TY::Cols cols;
+    // ---- team O: 16 channels of z (wave & 3), token tiles {0, 2} or {1, 3} (fp32: 0 or
+    // 1), which are as many 32-deep contractions ----
+    const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
+    const int zg = wv & 3, half = wv >> 2;
+    auto tile = [&](int t) { return half + 2 * t; };
+    typename TX::Rows xrow;
+    typename TY::Rows yrow;
     typename TZ::Col16 zcol;
     typename TP::Rows prow;
-    rows.init(lane);
-    cols.init(lane);
-    zcol.init(lane, 16 * wv);
+    xrow.init(lane);
+    yrow.init(lane);
+    zcol.init(lane, 16 * zg);
     prow.init(lane);
+    const int zd = jb.zd, zc = at.zb * ZB + 16 * zg;
     const bool mine = zc + 4 * g < zd;                  // whether the lane has out channels
     const bool out16 = jb.out_bf16;
     const size_t oe = out16 ? 2 : 4;
     const uint32_t ot = (uint32_t)(jb.ot * (int64_t)oe);
-    char* ob = OUT ? static_cast<char*>(jb.out) + (at.b * jb.ob + at.h * jb.oh) * oe : nullptr;
-    const uint32_t to = (back ? C - 1 - m : m) * ot + (zc + 4 * g) * (uint32_t)oe;
+    char* ob = static_cast<char*>(jb.out) + (at.b * jb.ob + at.h * jb.oh + zc + 4 * g) * oe;
     const bool dots = GRAD && jb.dots;
     const char* rb = dots ? static_cast<const char*>(head_base(jb.r, at.b, at.h, sizeof(T))) +
                                 (zc + 4 * g) * sizeof(T)
                           : nullptr;
     const uint32_t rt = dots ? (uint32_t)(jb.r.st * sizeof(T)) : 0u;
     float* const db = dots ? jb.dots + ((int64_t)(zc >> 4) * a.B + at.b) * a.T * a.H + at.h : nullptr;
-    float* const keep = GRAD ? jb.keep : nullptr;
-
-    lds_barrier();
-    if constexpr (OUT) lds_barrier();
-    for (int64_t n = 0; n < nc; ++n) {
-        const int buf = (int)(n & 1);
+    // the wave's tiles of P, at most two: of the ten in bf16, of the three in fp32
+    const int pi = NI == 4 ? (0x32132233 >> (4 * wv)) & 3 : (wv == 1 ? 0 : 1);
+    const int pj = NI == 4 ? (0x32021010 >> (4 * wv)) & 3 : (wv == 2 ? 1 : 0);
+    const int np = NI == 4 ? (wv < 2 ? 2 : 1) : (wv < 3 ? 1 : 0);
+    const float pair = jb.pair;
+    Decays<P, true> dec(a, at, jb, lane);
+    if (wv == 3) {
         int64_t t0;
         int len;
-        bounds(n, t0, len);
-        typename P::Frag zf[NJ];
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) zf[j] = zcol.get(s.z[buf], j);
-        f32x4 O[NI];
-        if constexpr (OUT) {
-            Row<4, P::is_bf16, false> rr[GRAD ? NI : 1];
+        ch.get(0, t0, len);
+        dec.ask(t0, len);
+        dec.scan(s, 0);
+        if (nc > 1) {
+            ch.get(1, t0, len);
+            dec.ask(t0, len);
+        }
+    }
+
+    lds_barrier();
+    for (int64_t n = 0; n <= nc; ++n) {
+        f32x4 O[NT];
+        int64_t t0 = 0;
+        int len = 0;
+        Row<4, P::is_bf16, false> rr[GRAD ? NT : 1];
+        if (n > 0) {
+            const int buf = (int)((n - 1) & 1);
+            ch.get(n - 1, t0, len);
             if constexpr (GRAD) {
                 if (dots) {
 #pragma unroll
-                    for (int i = 0; i < NI; ++i) {
-                        const int row = 16 * i + m < len ? 16 * i + m : len - 1;
-                        rr[i].load(rb + t0 * jb.r.st * (int)sizeof(T) +
+                    for (int t = 0; t < NT; ++t) {
+                        int row = 16 * tile(t) + m;
+                        row = row < len ? row : len - 1;
+                        rr[t].load(rb + t0 * jb.r.st * (int)sizeof(T) +
                                        (back ? len - 1 - row : row) * rt, 0, mine ? 4 : 0);
                     }
                 }
             }
             // out^T (row 4 g + r: channel, column m: token) from the start state
+            typename P::Frag xf[2][NT], hf[2][P::NO];
+            auto fetch = [&](int k) {
 #pragma unroll
-            for (int i = 0; i < NI; ++i) O[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+                for (int t = 0; t < NT; ++t) xf[k & 1][t] = xrow.raw(s.x[buf], tile(t), k);
+#pragma unroll
+                for (int q = 0; q < P::NO; ++q) hf[k & 1][q] = xrow.raw(s.h[q], zg, k);
+            };
+#pragma unroll
+            for (int t = 0; t < NT; ++t) O[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+            fetch(0);
 #pragma unroll
             for (int k = 0; k < NK; ++k) {
-                Terms<typename P::Frag, P::NO> ht;
-                P::template split<P::NO>(
-                    f32x8{H[2 * k][0], H[2 * k][1], H[2 * k][2], H[2 * k][3], H[2 * k + 1][0],
-                          H[2 * k + 1][1], H[2 * k + 1][2], H[2 * k + 1][3]}, ht);
-                typename P::Frag xf[NI];
-#pragma unroll
-                for (int i = 0; i < NI; ++i) xf[i] = rows.get(s.x[buf], i, k);
+                if (k + 1 < NK) fetch(k + 1);
 #pragma unroll
                 for (int q = P::NO - 1; q >= 0; --q)
 #pragma unroll
-                    for (int i = 0; i < NI; ++i) O[i] = P::mma(ht.t[q], xf[i], O[i]);
+                    for (int t = 0; t < NT; ++t) O[t] = P::mma(hf[k & 1][q], xf[k & 1][t], O[t]);
             }
 #pragma unroll
-            for (int i = 0; i < NI; ++i) O[i] *= s.enter[buf][16 * i + m];
-            if (__builtin_expect(s.bad[buf] != n + 1, 1)) {
+            for (int t = 0; t < NT; ++t) O[t] *= s.enter[buf][16 * tile(t) + m];
+            if (__builtin_expect(s.bad[buf] != (int)n, 1)) {
 #pragma unroll
-                for (int j = 0; j < NJ; ++j)
+                for (int j = 0; j < NT; ++j) {
+                    const typename P::Frag zf = zcol.get(s.z[buf], j);
 #pragma unroll
                     for (int q = P::NO - 1; q >= 0; --q)
 #pragma unroll
-                        for (int i = 2 * j; i < NI; ++i)
-                            O[i] = P::mma(zf[j], prow.get(s.p[q], i, j), O[i]);
+                        for (int t = j; t < NT; ++t)
+                            O[t] = P::mma(zf, prow.get(s.p[q], tile(t), j), O[t]);
+                }
             } else {
                 // a value of z that is no number must not meet the zeros of the tokens
                 // before it: one by one
 #pragma unroll
-                for (int i = 0; i < NI; ++i)
-                    for (int j = 0; j <= 16 * i + m; ++j) {
+                for (int t = 0; t < NT; ++t) {
+                    const int i = 16 * tile(t) + m;
+                    for (int j = 0; j <= i; ++j) {
                         float pv = 0.f;
 #pragma unroll
                         for (int q = P::NO - 1; q >= 0; --q) {
-                            const T w = s.p[q][TP::at(16 * i + m, j)];
+                            const T w = s.p[q][TP::at(i, j)];
                             if constexpr (P::is_bf16) pv += bf2f(w);
                             else pv += w;
                         }
 #pragma unroll
                         for (int r = 0; r < 4; ++r) {
-                            const T w = s.z[buf][TZ::at(j, 16 * wv + 4 * g + r)];
+                            const T w = s.z[buf][TZ::at(j, 16 * zg + 4 * g + r)];
                             float zv;
                             if constexpr (P::is_bf16) zv = bf2f(w);
                             else zv = w;
-                            O[i][r] = __builtin_fmaf(pv, zv, O[i][r]);
+                            O[t][r] = __builtin_fmaf(pv, zv, O[t][r]);
                         }
                     }
+                }
             }
-            lds_barrier();
+        }
+        lds_barrier();
+        PTileWork<P, KD> pw;
+        const int nb = (int)(n & 1);
+        if (n < nc && np > 0) pw.read(s.x[nb], s.y[nb], pi, pj, xrow, yrow);
+        if (n > 0) {
             if constexpr (GRAD) {
                 if (dots) {
 #pragma unroll
-                    for (int i = 0; i < NI; ++i) {
-                        const int row = 16 * i + m;
+                    for (int t = 0; t < NT; ++t) {
+                        const int row = 16 * tile(t) + m;
                         float rv[4], d = 0.f;
-                        rr[i].unpack(rv);
+                        rr[t].unpack(rv);
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) d = __builtin_fmaf(rv[r], O[i][r], d);
+                        for (int r = 0; r < 4; ++r) d = __builtin_fmaf(rv[r], O[t][r], d);
                         d += __shfl_xor(d, 16, 64);
                         d += __shfl_xor(d, 32, 64);
                         if (g == 0 && row < len && zc < zd)
@@ -381,68 +582,100 @@ __global__ __launch_bounds__(512) void chain_kernel(LaChain a) {
                     }
                 }
             }
-        }
-        // the state at the chunk's end
-        const float tot = s.total[buf];
-        Terms<typename P::Frag, P::NS> zt[NJ];
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            f32x8 v = P::widen(zf[j]);
-            const f32x4 l0 = *reinterpret_cast<const f32x4*>(&s.leave[buf][32 * j + 8 * g]);
-            const f32x4 l1 = *reinterpret_cast<const f32x4*>(&s.leave[buf][32 * j + 8 * g + 4]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] *= i < 4 ? l0[i & 3] : l1[i & 3];
-            P::template split<P::NS>(v, zt[j]);
-        }
-#pragma unroll
-        for (int u = 0; u < NU; ++u) H[u] *= tot;
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            typename P::Frag yf[NU];
-#pragma unroll
-            for (int u = 0; u < NU; ++u) yf[u] = cols.get(s.y[buf], j, u >> 1, u & 1);
-#pragma unroll
-            for (int q = P::NS - 1; q >= 0; --q)
-#pragma unroll
-                for (int u = 0; u < NU; ++u) H[u] = P::mma(yf[u], zt[j].t[q], H[u]);
-        }
-        if constexpr (OUT) {
-            // stores come last: at the stage's start they would queue behind A's loads
             char* oc = ob + t0 * ot;
-            if (mine) {
 #pragma unroll
-                for (int i = 0; i < NI; ++i) {
-                    const int row = 16 * i + m;
-                    if (len < C && row >= len) continue;
-                    const uint32_t off = to + (back ? (uint32_t)(len - C - 16 * i) * ot
-                                                    : (uint32_t)(16 * i) * ot);
+            for (int t = 0; t < NT; ++t) {
+                const int row = 16 * tile(t) + m;
+                if (mine && row < len) {
+                    const uint32_t off = (uint32_t)(back ? len - 1 - row : row) * ot;
                     if (out16)
                         *reinterpret_cast<u32x2_e2*>(oc + off) =
-                            u32x2_e2{cvt_pk(O[i][0], O[i][1]), cvt_pk(O[i][2], O[i][3])};
+                            u32x2_e2{cvt_pk(O[t][0], O[t][1]), cvt_pk(O[t][2], O[t][3])};
                     else
-                        *reinterpret_cast<f32x4_e4*>(oc + off) = O[i];
+                        *reinterpret_cast<f32x4_e4*>(oc + off) = O[t];
                 }
             }
         }
-        if (GRAD && keep) {
-            const int64_t mark = back ? t0 : t0 + len;
-            if (back ? (mark > 0 && mark % a.every == 0)
-                     : (mark < a.T ? mark % a.every == 0 : jb.keep_end))
-                h_store(keep + (((mark + a.every - 1) / a.every - 1) * a.B * a.H + bh) * a.state,
-                        1.f);
+        if (n < nc && np > 0) {
+            pw.write(s, nb, pi, pj, lane, pair, yrow);
+            if (np > 1) {
+                pw.read(s.x[nb], s.y[nb], wv, wv, xrow, yrow);
+                pw.write(s, nb, wv, wv, lane, pair, yrow);
+            }
+        }
+        if (wv == 3 && n + 1 < nc) {
+            dec.scan(s, n + 1);
+            if (n + 2 < nc) {
+                int64_t t2;
+                int len2;
+                ch.get(n + 2, t2, len2);
+                dec.ask(t2, len2);
+            }
         }
         lds_barrier();
     }
-    if constexpr (OUT) {
-        if (jb.h_out && at.seg == (back ? 0 : a.nseg - 1)) {
-            float f = 1.f;
-            if (jb.end_decay)
-                f = __builtin_amdgcn_exp2f((float)base2(decay_of(a, at.b, at.h, 0)));
-            h_store(jb.h_out + bh * a.state, f);
+}
+
+// The states at the segments' ends alone, and the segments' decays.
+template <class P, int KD>
+__global__ __launch_bounds__(512) void states_kernel(LaChain a) {
+    __shared__ StatesShared<P, KD> s;
+    Place at;
+    if (!place(a, blockIdx.x, at)) return;
+    const LaJob& jb = a.job[0];
+    const Chunks ch(a, at, jb.back, P::C);
+    const int64_t nc = ch.nc, bh = at.b * a.H + at.h;
+    const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (wv >= 4) {
+        typedef Bringer<P, KD, false> L;
+        typename L::Coming even, odd;
+        L l(at, jb, threadIdx.x - 256, even);
+        odd = even;
+        Decays<P, false> dec(a, at, jb, threadIdx.x & 63);
+        int64_t t0;
+        int len;
+        ch.get(0, t0, len);
+        if (wv == 7) dec.ask(t0, len);
+        l.ask_yz(t0, len, even);
+        if (nc > 1) {
+            ch.get(1, t0, len);
+            l.ask_yz(t0, len, odd);
         }
-    } else {
-        h_store(jb.h_out + (at.seg * a.B * a.H + bh) * a.state, 1.f);
+        auto turn = [&](int64_t n, typename L::Coming& c) {
+            int64_t t0;
+            int len;
+            if (wv == 7) {
+                dec.scan(s, n);
+                if (n + 1 < nc) {
+                    ch.get(n + 1, t0, len);
+                    dec.ask(t0, len);
+                }
+            }
+            ch.get(n, t0, len);
+            l.put_yz(s, n, len, c);
+            if (n + 2 < nc) {
+                ch.get(n + 2, t0, len);
+                l.ask_yz(t0, len, c);
+            }
+            lds_barrier();
+        };
+        for (int64_t n = 0; n < nc; n += 2) {
+            turn(n, even);
+            if (n + 1 < nc) turn(n + 1, odd);
+        }
+        lds_barrier();              // U's last chunk
+        if (at.zb == 0 && threadIdx.x == 512 - 64)
+            jb.seg_decay[at.seg * a.B * a.H + bh] = __builtin_amdgcn_exp2f((float)dec.run);
+        return;
     }
+    State<P, KD> st(jb, at.zb, threadIdx.x);
+    lds_barrier();
+    for (int64_t n = 0; n < nc; ++n) {
+        st.take(s, (int)(n & 1));
+        st.move(s, (int)(n & 1));
+        lds_barrier();
+    }
+    st.store(jb.h_out + (at.seg * a.B * a.H + bh) * a.state, 1.f);
 }
 
 // Segments' own end states, in place, to their start states:
@@ -561,29 +794,31 @@ __global__ __launch_bounds__(64) void head_sum_kernel(const double* part, float*
     if (threadIdx.x == 0) dg[blockIdx.x] = (float)s;
 }
 
-template <class P, int KD, bool OUT, bool GRAD> hipError_t launch_kd(const LaChain& a) {
+template <class Fn> hipError_t launch_one(Fn* fn, const LaChain& a, int threads, size_t lds) {
     int64_t per = 0;
     for (int j = 0; j < a.njobs; ++j) per += (a.job[j].zd + ZB - 1) / ZB;
     const int64_t grid = (a.B * a.H * a.nseg + 7) / 8 * 8 * per;
-    constexpr size_t lds = sizeof(Shared<P, KD>);
-    static_assert(lds <= 160 * 1024, "LDS");
-    const hipError_t e = hipFuncSetAttribute((const void*)chain_kernel<P, KD, OUT, GRAD>,
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((chain_kernel<P, KD, OUT, GRAD>), dim3((unsigned)grid), dim3(512), lds,
-                       a.stream, a);
+    if (lds) {
+        const hipError_t e = hipFuncSetAttribute(
+            (const void*)fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(fn, dim3((unsigned)grid), dim3(threads), lds, a.stream, a);
     return hipGetLastError();
 }
 
-template <class P, bool OUT, bool GRAD> hipError_t launch_p(const LaChain& a) {
-    return a.job[0].kd <= 64 ? launch_kd<P, 64, OUT, GRAD>(a) : launch_kd<P, 128, OUT, GRAD>(a);
+template <class P, int KD> hipError_t launch_kd(const LaChain& a) {
+    constexpr size_t lds = sizeof(Shared<P, KD>);
+    static_assert(lds <= 160 * 1024, "LDS");
+    if (!a.job[0].out) return launch_one(states_kernel<P, KD>, a, 512, 0);
+    for (int j = 0; j < a.njobs; ++j)
+        if (a.job[j].keep || a.job[j].dots)
+            return launch_one(chain_kernel<P, KD, true>, a, 1024, lds);
+    return launch_one(chain_kernel<P, KD, false>, a, 1024, lds);
 }
 
 template <class P> hipError_t launch_chain_p(const LaChain& a) {
-    if (!a.job[0].out) return launch_p<P, false, false>(a);
-    for (int j = 0; j < a.njobs; ++j)
-        if (a.job[j].keep || a.job[j].dots) return launch_p<P, true, true>(a);
-    return launch_p<P, true, false>(a);
+    return a.job[0].kd <= 64 ? launch_kd<P, 64>(a) : launch_kd<P, 128>(a);
 }
 
 // Jobs of one contraction width (all of a.job are on the same side of 64).
@@ -683,7 +918,7 @@ using namespace la;
 // The largest launch of a call, in workgroups of 256.
 int64_t la_fwd_workgroups(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, bool bf16) {
     const Plan p = fwd_plan(B, T, H, Dv);
-    const int64_t chain = 2 * ((B * H * p.nseg + 7) / 8 * 8 * blocks(Dv));
+    const int64_t chain = 4 * ((B * H * p.nseg + 7) / 8 * 8 * blocks(Dv));
     const int64_t states = p.nseg > 1 ? (B * H * Dk * Dv + 255) / 256 : 0;
     return chain > states ? chain : states;
 }
@@ -760,7 +995,7 @@ BwdSpace bwd_space(const Plan& p, int64_t every, int64_t B, int64_t T, int64_t H
 int64_t la_bwd_workgroups(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, bool bf16) {
     int64_t every;
     const Plan p = bwd_plan(B, T, H, Dk, Dv, every);
-    const int64_t chain = 2 * ((B * H * p.nseg + 7) / 8 * 8 * (2 * blocks(Dk) + blocks(Dv)));
+    const int64_t chain = 4 * ((B * H * p.nseg + 7) / 8 * 8 * (2 * blocks(Dk) + blocks(Dv)));
     const int64_t states = (B * H * Dk * Dv + 255) / 256;
     const int64_t sums = B * H * ((T + every - 1) / every);
     const int64_t most = chain > states ? chain : states;

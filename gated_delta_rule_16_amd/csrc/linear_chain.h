@@ -151,13 +151,22 @@ template <class P, int W, int KIND> struct Tile {
                 }
             }
         }
+        // as it lies, and with its halves in order
+        __device__ __forceinline__ typename P::Frag order(const typename P::Frag& f) const {
+            if constexpr (SWAP) {
+                const u32x4 v = __builtin_bit_cast(u32x4, f);
+                return __builtin_bit_cast(bf16x8, swap ? u32x4{v[2], v[3], v[0], v[1]} : v);
+            } else {
+                return f;
+            }
+        }
         __device__ __forceinline__ typename P::Frag get(const T* t, int i, int k) const {
+            return order(raw(t, i, k));
+        }
+        __device__ __forceinline__ typename P::Frag raw(const T* t, int i, int k) const {
             const T* p = t + 16 * i * W;
             if constexpr (P::is_bf16) {
-                u32x4 v = *reinterpret_cast<const u32x4*>(p + o[k]);
-                if constexpr (SWAP)
-                    v = swap ? u32x4{v[2], v[3], v[0], v[1]} : v;
-                return __builtin_bit_cast(bf16x8, v);
+                return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(p + o[k]));
             } else {
                 const f32x4 a = *reinterpret_cast<const f32x4*>(p + o[2 * k]);
                 const f32x4 b = *reinterpret_cast<const f32x4*>(p + o[2 * k + 1]);
@@ -230,6 +239,46 @@ template <class P, int W, int KIND> struct Tile {
     }
 };
 
+// P (its tiles of 16 x 16 tokens on and below the diagonal, and those above it that
+// share a 32-deep contraction with them, which stay 0) in LDS, 32 columns at a time:
+// rows 0 .. C - 1 of columns 0 .. 31, then (bf16) rows 32 .. 63 of columns 32 .. 63.
+template <class P> struct PTile {
+    typedef typename P::T T;
+    static constexpr int SIZE = P::is_bf16 ? 64 * 32 + 32 * 32 : 32 * 32;
+    static __device__ __forceinline__ int piece(int row, int c) {
+        // four pieces a row in bf16, eight in fp32
+        return row * 32 + (c ^ (P::is_bf16 ? ((row & 8) ? 3 : 0) : (row & 7))) * P::EP;
+    }
+    // Offset of tile (i, j) beyond that of its lane.
+    static constexpr int tile(int i, int j) { return j / 2 * (32 * 32) + 16 * i * 32; }
+    static __device__ __forceinline__ int at(int row, int col) {
+        return piece(row % 16, col % 32 / P::EP) + col % P::EP + tile(row / 16, col / 16);
+    }
+    // Elements 32 j + 8 g .. + 7 of row 16 i + m.
+    struct Rows {
+        int o[P::is_bf16 ? 1 : 2];
+        __device__ __forceinline__ void init(int lane) {
+            const int g = lane >> 4, m = lane & 15;
+            if constexpr (P::is_bf16) {
+                o[0] = piece(m, g);
+            } else {
+                o[0] = piece(m, 2 * g);
+                o[1] = piece(m, 2 * g + 1);
+            }
+        }
+        __device__ __forceinline__ typename P::Frag get(const T* t, int i, int j) const {
+            const T* p = t + tile(i, 2 * j);
+            if constexpr (P::is_bf16) {
+                return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(p + o[0]));
+            } else {
+                const f32x4 a = *reinterpret_cast<const f32x4*>(p + o[0]);
+                const f32x4 b = *reinterpret_cast<const f32x4*>(p + o[1]);
+                return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+            }
+        }
+    };
+};
+
 // The pieces of a [C, W] tile that one of 256 threads moves from memory: piece i is
 // row row0 + i C / N of the chunk, 16 bytes at channel col.
 template <class P, int W, int KIND> struct Stage {
@@ -240,7 +289,6 @@ template <class P, int W, int KIND> struct Stage {
     int row0, col, c0;
     bool wide, narrow;              // whether the tensor has these channels, all of W
     uint32_t off;                   // bytes from a whole chunk's first token
-    uint32_t step;                  // bytes from piece to piece
     __device__ __forceinline__ void init(int tid, int width, int64_t st, bool back) {
         row0 = tid / PPR;
         const int c = tid % PPR * P::EP;
@@ -250,23 +298,33 @@ template <class P, int W, int KIND> struct Stage {
         c0 = tid % PPR;
         const uint32_t sb = (uint32_t)(st * sizeof(typename P::T));
         off = (back ? P::C - 1 - row0 : row0) * sb + col * (uint32_t)sizeof(typename P::T);
-        step = STEP * sb;
     }
     // `chunk`: the first token's first channel.  Rows from len on are loaded as the
     // last one, and cleared by put.
     __device__ __forceinline__ void load(const char* chunk, int64_t st, int len, bool back) {
+        const char* at[N];
+        uint32_t o[N];
+        const int64_t pass = (back ? -STEP : STEP) * st * (int)sizeof(typename P::T);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            uint32_t o = back ? off - i * step : off + i * step;
-            if (len < P::C) {
+            at[i] = chunk + i * pass;
+            o[i] = off;
+        }
+        if (len < P::C) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
                 const int r = row0 + i * STEP < len ? row0 + i * STEP : len - 1;
-                o = (uint32_t)((back ? len - 1 - r : r) * st + col) *
-                    (uint32_t)sizeof(typename P::T);
+                at[i] = chunk;
+                o[i] = (uint32_t)((back ? len - 1 - r : r) * st + col) *
+                       (uint32_t)sizeof(typename P::T);
             }
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
             if constexpr (P::is_bf16)
-                w[i] = *reinterpret_cast<const u32x4_e2*>(chunk + o);
+                w[i] = *reinterpret_cast<const u32x4_e2*>(at[i] + o[i]);
             else
-                w[i] = *reinterpret_cast<const u32x4_e4*>(chunk + o);
+                w[i] = *reinterpret_cast<const u32x4_e4*>(at[i] + o[i]);
         }
     }
     __device__ __forceinline__ void put(typename P::T* tile, int len) {
