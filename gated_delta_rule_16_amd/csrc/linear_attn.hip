@@ -63,19 +63,28 @@ template <class P, int KD> struct PTileWork {
     __device__ __forceinline__ void read(const typename P::T* x, const typename P::T* y, int i,
                                          int j, const typename Tile<P, KD, ROWS>::Rows& xrow,
                                          const typename Tile<P, KD, BOTH>::Rows& yrow) {
+        if constexpr (P::is_bf16) {         // fp32: too many registers
 #pragma unroll
-        for (int k = 0; k < NK; ++k) {
-            xf[k] = xrow.raw(x, i, k);
-            yf[k] = yrow.raw(y, j, k);
+            for (int k = 0; k < NK; ++k) {
+                xf[k] = xrow.raw(x, i, k);
+                yf[k] = yrow.raw(y, j, k);
+            }
         }
     }
     __device__ __forceinline__ void write(Shared<P, KD>& s, int pb, int i, int j, int lane,
                                           float scale,
+                                          const typename Tile<P, KD, ROWS>::Rows& xrow,
                                           const typename Tile<P, KD, BOTH>::Rows& yrow) {
         const int g = lane >> 4, m = lane & 15;
         f32x4 c = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int k = 0; k < NK; ++k) c = P::mma(yrow.order(yf[k]), xf[k], c);
+        for (int k = 0; k < NK; ++k) {
+            if constexpr (!P::is_bf16) {
+                xf[k] = xrow.raw(s.x[pb], i, k);
+                yf[k] = yrow.raw(s.y[pb], j, k);
+            }
+            c = P::mma(yrow.order(yf[k]), xf[k], c);
+        }
         f32x4 v;
         if (i == j) {
             const float lh = s.lh[pb][16 * i + m], ll = s.ll[pb][16 * i + m];
@@ -277,15 +286,15 @@ template <class P, int KD> struct State {
     template <class S> __device__ __forceinline__ void move(const S& s, int buf) {
 #pragma unroll
         for (int u = 0; u < NU; ++u) H[u] *= tot;
-        // four tiles at a time, the next four's operands on their way: more would not
-        // fit the registers, and a spill waits behind L's loads
-        constexpr int NG = NJ * NU / 4;
-        typename P::Frag yf[2][4];
+        // four tiles (fp32: two) at a time, the next ones' operands on their way: more
+        // would not fit the registers, and a spill waits behind L's loads
+        constexpr int W = P::is_bf16 ? 4 : 2, NG = NJ * NU / W;
+        typename P::Frag yf[2][W];
         auto fetch = [&](int i) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int u = i % (NU / 4) * 4 + e;
-                yf[i & 1][e] = cols.get(s.y[buf], i / (NU / 4), u >> 1, u & 1);
+            for (int e = 0; e < W; ++e) {
+                const int u = i % (NU / W) * W + e;
+                yf[i & 1][e] = cols.get(s.y[buf], i / (NU / W), u >> 1, u & 1);
             }
         };
         fetch(0);
@@ -296,9 +305,9 @@ template <class P, int KD> struct State {
 #pragma unroll
             for (int q = P::NS - 1; q >= 0; --q)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int u = i % (NU / 4) * 4 + e;
-                    H[u] = P::mma(yf[i & 1][e], zt[i / (NU / 4)].t[q], H[u]);
+                for (int e = 0; e < W; ++e) {
+                    const int u = i % (NU / W) * W + e;
+                    H[u] = P::mma(yf[i & 1][e], zt[i / (NU / W)].t[q], H[u]);
                 }
         }
     }
@@ -465,7 +474,8 @@ __global__ __launch_bounds__(1024) void chain_kernel(LaChain a) {
                                 (zc + 4 * g) * sizeof(T)
                           : nullptr;
     const uint32_t rt = dots ? (uint32_t)(jb.r.st * sizeof(T)) : 0u;
-    float* const db = dots ? jb.dots + ((int64_t)(zc >> 4) * a.B + at.b) * a.T * a.H + at.h : nullptr;
+    float* const db = dots ? jb.dots + (((int64_t)(zc >> 4) * a.B + at.b) * a.H + at.h) * a.T
+                           : nullptr;
     // the wave's tiles of P, at most two: of the ten in bf16, of the three in fp32
     const int pi = NI == 4 ? (0x32132233 >> (4 * wv)) & 3 : (wv == 1 ? 0 : 1);
     const int pj = NI == 4 ? (0x32021010 >> (4 * wv)) & 3 : (wv == 2 ? 1 : 0);
@@ -578,7 +588,7 @@ __global__ __launch_bounds__(1024) void chain_kernel(LaChain a) {
                         d += __shfl_xor(d, 16, 64);
                         d += __shfl_xor(d, 32, 64);
                         if (g == 0 && row < len && zc < zd)
-                            db[(t0 + (back ? len - 1 - row : row)) * a.H] = d;
+                            db[t0 + (back ? len - 1 - row : row)] = d;
                     }
                 }
             }
@@ -597,10 +607,10 @@ __global__ __launch_bounds__(1024) void chain_kernel(LaChain a) {
             }
         }
         if (n < nc && np > 0) {
-            pw.write(s, nb, pi, pj, lane, pair, yrow);
+            pw.write(s, nb, pi, pj, lane, pair, xrow, yrow);
             if (np > 1) {
                 pw.read(s.x[nb], s.y[nb], wv, wv, xrow, yrow);
-                pw.write(s, nb, wv, wv, lane, pair, yrow);
+                pw.write(s, nb, wv, wv, lane, pair, xrow, yrow);
             }
         }
         if (wv == 3 && n + 1 < nc) {
@@ -622,7 +632,7 @@ __global__ __launch_bounds__(512) void states_kernel(LaChain a) {
     __shared__ StatesShared<P, KD> s;
     Place at;
     if (!place(a, blockIdx.x, at)) return;
-    const LaJob& jb = a.job[0];
+    const LaJob& jb = a.job[at.job];
     const Chunks ch(a, at, jb.back, P::C);
     const int64_t nc = ch.nc, bh = at.b * a.H + at.h;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -679,43 +689,70 @@ __global__ __launch_bounds__(512) void states_kernel(LaChain a) {
 }
 
 // Segments' own end states, in place, to their start states:
-// in(first) = h0, in(next) = decay in + own.
-__global__ __launch_bounds__(256) void compose_kernel(float* buf, const float* decay,
-                                                      const float* h0, int64_t BH, int64_t state,
-                                                      int64_t nseg, bool back) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= BH * state) return;
-    const int64_t bh = i / state;
-    float h = h0 ? h0[i] : 0.f;
-    for (int64_t c = 0; c < nseg; ++c) {
-        const int64_t p = back ? nseg - 1 - c : c;
-        float own = 0.f, d = 0.f;
-        if (c + 1 < nseg) {
-            own = buf[p * BH * state + i];
-            d = decay[p * BH + bh];
+// in(first) = h0, in(next) = decay in + own.  Up to two chains at once.
+struct Compose {
+    int64_t BH, state, nseg;
+    float* buf[2];
+    const float *decay[2], *h0[2];
+    bool back[2];
+};
+
+__global__ __launch_bounds__(256) void compose_kernel(Compose a) {
+    const int k = blockIdx.y;
+    const int64_t n = a.BH * a.state, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= n) return;
+    const int64_t bh = i / a.state, last = a.nseg - 1;
+    float* buf = a.buf[k] + i;
+    const float* decay = a.decay[k] + bh;
+    float h = a.h0[k] ? a.h0[k][i] : 0.f;
+    const bool back = a.back[k];
+    // batches of loads: a store would hold back the next segment's
+    for (int64_t c = 0; c <= last; c += 8) {
+        float own[8], d[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int64_t p = back ? last - c - e : c + e;
+            own[e] = d[e] = 0.f;
+            if (c + e < last) {
+                own[e] = buf[p * n];
+                d[e] = decay[p * a.BH];
+            }
         }
-        buf[p * BH * state + i] = h;
-        h = d * h + own;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int64_t p = back ? last - c - e : c + e;
+            if (c + e <= last) buf[p * n] = h;
+            h = d[e] * h + own[e];
+        }
     }
 }
 
-// Sums over the heads that share one: part [rows, Hk, share, D] to out [rows, Hk, D].
-__global__ __launch_bounds__(256) void share_kernel(const float* part, void* out, bool bf16,
-                                                    int64_t n, int64_t share, int64_t D) {
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const int64_t row = i / (D / 4), c = i % (D / 4) * 4;
+// Sums over the heads that share one: part [rows, Hk, share, D] to out [rows, Hk, D],
+// for dq and dk at once.
+struct Share {
+    const float* part[2];
+    void* out[2];
+    bool bf16;
+    int64_t n, share, D;
+};
+
+__global__ __launch_bounds__(256) void share_kernel(Share a) {
+    const float* part = a.part[blockIdx.y];
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < a.n;
+         i += (int64_t)gridDim.x * 256) {
+        const int64_t row = i / (a.D / 4), c = i % (a.D / 4) * 4;
         f32x4 x = {0.f, 0.f, 0.f, 0.f};
-        for (int64_t k = 0; k < share; ++k)
-            x += *reinterpret_cast<const f32x4*>(part + (row * share + k) * D + c);
+        for (int64_t k = 0; k < a.share; ++k)
+            x += *reinterpret_cast<const f32x4*>(part + (row * a.share + k) * a.D + c);
         const float v[4] = {x[0], x[1], x[2], x[3]};
-        row_store<4, false>(out, row * D + c, bf16, v, 4);
+        row_store<4, false>(a.out[blockIdx.y], row * a.D + c, a.bf16, v, 4);
     }
 }
 
 struct DecayGrad {
     int64_t B, T, H, every, nblk, state;
     int nq;                         // slots of either sum
-    const float *q, *k;             // [nq][B][T][H] sums of q . dq and k . dk
+    const float *q, *k;             // [nq][B][H][T] sums of q . dq and k . dk
     const float *skeep, *gkeep;     // states after, gradients before each block's end
     const float* ds_final;
     const float* g;
@@ -727,7 +764,7 @@ struct DecayGrad {
 // dg of one block of tokens of a (sequence, head): what all pairs across its end say,
 // <G, S> there, and the running sum of q . dq - k . dk from the end, in 64 bits.
 __global__ __launch_bounds__(256) void decay_grad_kernel(DecayGrad a) {
-    __shared__ double red[4], scan[256];
+    __shared__ double red[4], part[2][4];
     const int64_t id = blockIdx.x;
     const int64_t h = id % a.H, b = id / a.H % a.B, p = id / a.H / a.B;
     const int64_t bh = b * a.H + h;
@@ -738,7 +775,15 @@ __global__ __launch_bounds__(256) void decay_grad_kernel(DecayGrad a) {
     double tail = 0.0;
     if (G) {
         const float* S = a.skeep + (p * a.B * a.H + bh) * a.state;
-        for (int64_t i = tid; i < a.state; i += 256) tail += (double)G[i] * (double)S[i];
+        // the state's size is a multiple of 64 floats, its place in the caller's
+        // memory any
+#pragma unroll 4
+        for (int64_t i = 4 * tid; i < a.state; i += 1024) {
+            const f32x4_e4 x = *reinterpret_cast<const f32x4_e4*>(G + i);
+            const f32x4 y = *reinterpret_cast<const f32x4*>(S + i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) tail += (double)x[e] * (double)y[e];
+        }
     }
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) tail += __shfl_xor(tail, d, 64);
@@ -751,29 +796,41 @@ __global__ __launch_bounds__(256) void decay_grad_kernel(DecayGrad a) {
     };
     if (p + 1 < a.nblk) tail *= (double)__builtin_amdgcn_exp2f(rate(t1) * kLog2e);
     double carry = tail, sum = 0.0;
-    for (int64_t hi = t1; hi > t0; hi -= 256) {
+    const int wv = tid >> 6;
+    const int64_t n = a.B * a.H * a.T, row = bh * a.T;
+    int turn = 0;
+    for (int64_t hi = t1; hi > t0; hi -= 256, turn ^= 1) {
         const int64_t t = hi - 1 - tid;             // thread 0: the last token
         double e = 0.0;
         if (t >= t0) {
-            const int64_t n = a.B * a.T * a.H, o = (b * a.T + t) * a.H + h;
-            for (int i = 0; i < a.nq; ++i) e += (double)a.q[i * n + o] - (double)a.k[i * n + o];
+            // all loads at once, without branches between them
+            float x[16];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int64_t o = (i < a.nq ? i : 0) * n + row + t;
+                x[2 * i] = a.q[o];
+                x[2 * i + 1] = a.k[o];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                e += i < a.nq ? (double)x[2 * i] - (double)x[2 * i + 1] : 0.0;
         }
+        e = wave_scan64(e);
+        if ((tid & 63) == 63) part[turn][wv] = e;
         __syncthreads();
-        scan[tid] = e;
-        __syncthreads();
-        for (int d = 1; d < 256; d *= 2) {
-            const double v = tid >= d ? scan[tid - d] : 0.0;
-            __syncthreads();
-            scan[tid] += v;
-            __syncthreads();
+        double before = 0.0, all = 0.0;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            before += w < wv ? part[turn][w] : 0.0;
+            all += part[turn][w];
         }
         if (t >= t0) {
             // a decay of 0 has no gradient
-            const double d = rate(t) < -104.f ? 0.0 : carry + scan[tid];
+            const double d = rate(t) < -104.f ? 0.0 : carry + before + e;
             sum += d;
             if (a.dg) a.dg[(b * a.T + t) * a.H + h] = (float)d;
         }
-        carry += scan[255];
+        carry += all;
     }
     if (a.part) {
 #pragma unroll
@@ -833,26 +890,29 @@ struct Plan {
     int64_t L, nseg;
 };
 
-// Segments: as many as give the chip about `want` workgroups, of at least 4 chunks.
-Plan plan(int64_t T, int64_t units, int64_t want) {
-    int64_t nseg = units > 0 ? want / units : 1;
-    const int64_t most = T / 256;
+// Segments: as many as fill the chip (a workgroup to each of 256 compute units), of at
+// least two chunks.  A second pass over k and v and the states' round trip cost less
+// than idle units: fp32 B3 T1025 H6 72 x 40 82 us with 4 segments, 49 with 14.
+Plan plan(int64_t T, int64_t units, bool bf16) {
+    const int64_t most = T / (bf16 ? 128 : 64);
+    int64_t nseg = 256 / units;
     if (nseg > most) nseg = most;
     if (nseg < 1) nseg = 1;
+    const int64_t C = bf16 ? Bf16<3>::C : F32::C;
     int64_t L = (T + nseg - 1) / nseg;
-    L = (L + 63) / 64 * 64;
+    L = (L + C - 1) / C * C;
     return {L, (T + L - 1) / L};
 }
 
 int64_t blocks(int64_t d) { return (d + ZB - 1) / ZB; }
 
-Plan fwd_plan(int64_t B, int64_t T, int64_t H, int64_t Dv) {
-    return plan(T, B * H * blocks(Dv), 256);
+Plan fwd_plan(int64_t B, int64_t T, int64_t H, int64_t Dv, bool bf16) {
+    return plan(T, B * H * blocks(Dv), bf16);
 }
 
 // Kept states are at whole numbers of `every` tokens, which divides a segment.
-Plan bwd_plan(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, int64_t& every) {
-    Plan p = plan(T, B * H * (2 * blocks(Dk) + blocks(Dv)), 512);
+Plan bwd_plan(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, bool bf16, int64_t& every) {
+    Plan p = plan(T, B * H * (2 * blocks(Dk) + blocks(Dv)), bf16);
     every = p.L;
     if (p.L > 1024) {
         p.L = (p.L + 1023) / 1024 * 1024;
@@ -891,22 +951,34 @@ LaChain chain(const LaArgs& a, const Plan& p) {
     return c;
 }
 
-// Start states of all segments of a job (its h_in, hz and hk as for the whole
-// chain) into buf.
-hipError_t segment_states(LaChain c, LaJob j, float* buf, float* decay) {
-    const float* h0 = j.h_in;
-    j.h_in = nullptr;
-    j.h_out = buf;
-    j.seg_decay = decay;
-    j.out = nullptr;
-    j.keep = j.dots = nullptr;
-    c.njobs = 1;
-    c.job[0] = j;
-    hipError_t e = launch_chain(c);
-    if (e != hipSuccess) return e;
-    const int64_t n = c.B * c.H * c.state;
-    hipLaunchKernelGGL(compose_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, c.stream,
-                       buf, decay, h0, c.B * c.H, c.state, c.nseg, j.back);
+// Start states of all segments of one or two jobs (their h_in, hz and hk as for the
+// whole chain) into buf.
+hipError_t segment_states(LaChain c, const LaJob* jobs, int n, float* const* buf,
+                          float* const* decay) {
+    Compose m{};
+    m.BH = c.B * c.H;
+    m.state = c.state;
+    m.nseg = c.nseg;
+    const bool both = n == 2 && (jobs[0].kd <= 64) == (jobs[1].kd <= 64);
+    for (int i = 0; i < n; ++i) {
+        LaJob j = jobs[i];
+        m.buf[i] = buf[i];
+        m.decay[i] = decay[i];
+        m.h0[i] = j.h_in;
+        m.back[i] = j.back;
+        j.h_in = nullptr;
+        j.h_out = buf[i];
+        j.seg_decay = decay[i];
+        j.out = nullptr;
+        j.keep = j.dots = nullptr;
+        c.job[both ? i : 0] = j;
+        c.njobs = both ? 2 : 1;
+        if (both && i == 0) continue;
+        const hipError_t e = launch_chain(c);
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(compose_kernel, dim3((unsigned)((m.BH * m.state + 255) / 256), n), dim3(256),
+                       0, c.stream, m);
     return hipGetLastError();
 }
 
@@ -917,20 +989,20 @@ using namespace la;
 
 // The largest launch of a call, in workgroups of 256.
 int64_t la_fwd_workgroups(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, bool bf16) {
-    const Plan p = fwd_plan(B, T, H, Dv);
+    const Plan p = fwd_plan(B, T, H, Dv, bf16);
     const int64_t chain = 4 * ((B * H * p.nseg + 7) / 8 * 8 * blocks(Dv));
     const int64_t states = p.nseg > 1 ? (B * H * Dk * Dv + 255) / 256 : 0;
     return chain > states ? chain : states;
 }
 
 size_t la_fwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, bool bf16) {
-    const Plan p = fwd_plan(B, T, H, Dv);
+    const Plan p = fwd_plan(B, T, H, Dv, bf16);
     if (p.nseg == 1) return 0;
     return up16(4 * (size_t)(p.nseg * B * H) * (size_t)(Dk * Dv)) + up16(4 * (size_t)(p.nseg * B * H));
 }
 
 hipError_t launch_la_fwd(const LaArgs& a) {
-    const Plan p = fwd_plan(a.B, a.T, a.H, a.Dv);
+    const Plan p = fwd_plan(a.B, a.T, a.H, a.Dv, a.bf16);
     LaChain c = chain(a, p);
     LaJob j = job(a.q, a.k, a.v, a.Dk, a.Dv);
     j.pair = j.inter = a.scale;
@@ -945,7 +1017,7 @@ hipError_t launch_la_fwd(const LaArgs& a) {
     if (p.nseg > 1) {
         float* buf = static_cast<float*>(a.workspace);
         float* decay = buf + up16(4 * (size_t)(p.nseg * a.B * a.H) * (size_t)c.state) / 4;
-        const hipError_t e = segment_states(c, j, buf, decay);
+        const hipError_t e = segment_states(c, &j, 1, &buf, &decay);
         if (e != hipSuccess) return e;
         j.h_in = buf;
     }
@@ -994,7 +1066,7 @@ BwdSpace bwd_space(const Plan& p, int64_t every, int64_t B, int64_t T, int64_t H
 
 int64_t la_bwd_workgroups(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, bool bf16) {
     int64_t every;
-    const Plan p = bwd_plan(B, T, H, Dk, Dv, every);
+    const Plan p = bwd_plan(B, T, H, Dk, Dv, bf16, every);
     const int64_t chain = 4 * ((B * H * p.nseg + 7) / 8 * 8 * (2 * blocks(Dk) + blocks(Dv)));
     const int64_t states = (B * H * Dk * Dv + 255) / 256;
     const int64_t sums = B * H * ((T + every - 1) / every);
@@ -1005,13 +1077,13 @@ int64_t la_bwd_workgroups(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t D
 size_t la_bwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Hk, int64_t Dk, int64_t Dv,
                               bool bf16) {
     int64_t every;
-    const Plan p = bwd_plan(B, T, H, Dk, Dv, every);
+    const Plan p = bwd_plan(B, T, H, Dk, Dv, bf16, every);
     return bwd_space(p, every, B, T, H, Hk, Dk, Dv).end;
 }
 
 hipError_t launch_la_bwd(const LaArgs& a) {
     int64_t every;
-    const Plan p = bwd_plan(a.B, a.T, a.H, a.Dk, a.Dv, every);
+    const Plan p = bwd_plan(a.B, a.T, a.H, a.Dk, a.Dv, a.bf16, every);
     const BwdSpace w = bwd_space(p, every, a.B, a.T, a.H, a.Hk, a.Dk, a.Dv);
     char* ws = static_cast<char*>(a.workspace);
     auto f32 = [&](size_t at) { return reinterpret_cast<float*>(ws + at); };
@@ -1038,8 +1110,10 @@ hipError_t launch_la_bwd(const LaArgs& a) {
 
     hipError_t e;
     if (p.nseg > 1) {
-        if ((e = segment_states(c, jq, f32(w.s), f32(w.sdec))) != hipSuccess) return e;
-        if ((e = segment_states(c, jv, f32(w.g), f32(w.gdec))) != hipSuccess) return e;
+        const LaJob jobs[2] = {jq, jv};
+        float* const buf[2] = {f32(w.s), f32(w.g)};
+        float* const decay[2] = {f32(w.sdec), f32(w.gdec)};
+        if ((e = segment_states(c, jobs, 2, buf, decay)) != hipSuccess) return e;
         jq.h_in = f32(w.s);
         jk.h_in = jv.h_in = f32(w.g);
     }
@@ -1084,13 +1158,17 @@ hipError_t launch_la_bwd(const LaArgs& a) {
         if ((e = launch_chain(c)) != hipSuccess) return e;
     }
     if (!own) {
-        const int64_t n = a.B * a.T * a.Hk * (a.Dk / 4);
-        for (int i = 0; i < 2; ++i) {
-            hipLaunchKernelGGL(share_kernel, dim3(stride_blocks(n)), dim3(256), 0, a.stream,
-                               f32(i ? w.dk : w.dq), i ? a.dk : a.dq, a.grad_bf16, n, a.H / a.Hk,
-                               a.Dk);
-            if ((e = hipGetLastError()) != hipSuccess) return e;
-        }
+        Share m{};
+        m.part[0] = f32(w.dq);
+        m.part[1] = f32(w.dk);
+        m.out[0] = a.dq;
+        m.out[1] = a.dk;
+        m.bf16 = a.grad_bf16;
+        m.n = a.B * a.T * a.Hk * (a.Dk / 4);
+        m.share = a.H / a.Hk;
+        m.D = a.Dk;
+        hipLaunchKernelGGL(share_kernel, dim3(stride_blocks(m.n), 2), dim3(256), 0, a.stream, m);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (a.dg) {
         DecayGrad d{};
