@@ -284,6 +284,7 @@ template <class P, int KD> struct State {
     }
     // through that chunk
     template <class S> __device__ __forceinline__ void move(const S& s, int buf) {
+        cols.fresh();
 #pragma unroll
         for (int u = 0; u < NU; ++u) H[u] *= tot;
         // four tiles (fp32: two) at a time, the next ones' operands on their way: more
@@ -500,6 +501,8 @@ __global__ __launch_bounds__(1024) void chain_kernel(LaChain a) {
         int64_t t0 = 0;
         int len = 0;
         Row<4, P::is_bf16, false> rr[GRAD ? NT : 1];
+        xrow.fresh();
+        yrow.fresh();
         if (n > 0) {
             const int buf = (int)((n - 1) & 1);
             ch.get(n - 1, t0, len);

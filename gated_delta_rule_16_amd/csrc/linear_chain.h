@@ -134,23 +134,20 @@ template <class P, int W, int KIND> struct Tile {
         return piece(row, col / P::EP) + (swapped(row) ? e ^ 4 : e);
     }
 
+    // A lane's first element of an operand; the others differ in bits that the swizzle
+    // leaves alone or flips alike, so they are one exclusive or away.  fresh() keeps the
+    // compiler from holding all of them in registers over a loop.
+
     // Elements 32 k + 8 g .. + 7 of row 16 i + m (the swizzle repeats every 16 rows).
     struct Rows {
-        int o[P::is_bf16 ? W / 32 : 2 * (W / 32)];
+        int o;
         bool swap;
         __device__ __forceinline__ void init(int lane) {
             const int g = lane >> 4, m = lane & 15;
             swap = swapped(m);
-#pragma unroll
-            for (int k = 0; k < W / 32; ++k) {
-                if constexpr (P::is_bf16) {
-                    o[k] = piece(m, 4 * k + g);
-                } else {
-                    o[2 * k] = piece(m, 8 * k + 2 * g);
-                    o[2 * k + 1] = piece(m, 8 * k + 2 * g + 1);
-                }
-            }
+            o = piece(m, 8 / P::EP * g);
         }
+        __device__ __forceinline__ void fresh() { asm volatile("" : "+v"(o)); }
         // as it lies, and with its halves in order
         __device__ __forceinline__ typename P::Frag order(const typename P::Frag& f) const {
             if constexpr (SWAP) {
@@ -160,16 +157,14 @@ template <class P, int W, int KIND> struct Tile {
                 return f;
             }
         }
-        __device__ __forceinline__ typename P::Frag get(const T* t, int i, int k) const {
-            return order(raw(t, i, k));
-        }
         __device__ __forceinline__ typename P::Frag raw(const T* t, int i, int k) const {
             const T* p = t + 16 * i * W;
             if constexpr (P::is_bf16) {
-                return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(p + o[k]));
+                return __builtin_bit_cast(bf16x8,
+                                          *reinterpret_cast<const u32x4*>(p + (o ^ (32 * k))));
             } else {
-                const f32x4 a = *reinterpret_cast<const f32x4*>(p + o[2 * k]);
-                const f32x4 b = *reinterpret_cast<const f32x4*>(p + o[2 * k + 1]);
+                const f32x4 a = *reinterpret_cast<const f32x4*>(p + (o ^ (32 * k)));
+                const f32x4 b = *reinterpret_cast<const f32x4*>(p + (o ^ (32 * k + 4)));
                 return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
             }
         }
@@ -177,31 +172,31 @@ template <class P, int W, int KIND> struct Tile {
 
     // Rows 32 j + 8 g .. + 7 of column 32 k + 4 h + 8 (m / 4) + m % 4.
     struct Cols {
-        int o[P::is_bf16 ? W / 8 : 2];
+        int o[P::is_bf16 ? 2 : 8];
         __device__ __forceinline__ void init(int lane) {
             const int g = lane >> 4, m = lane & 15;
             if constexpr (P::is_bf16) {
-                // lane 4 r + c of a group points at 4 columns of row r (lds_tr16): by
-                // k, h and row half
-#pragma unroll
-                for (int q = 0; q < W / 8; ++q)
-                    o[q] = at(8 * g + (m >> 2) + 4 * (q & 1),
-                              32 * (q >> 2) + 4 * ((q >> 1) & 1) + 8 * (m & 3));
+                // lane 4 r + c of a group points at 4 columns of row r (lds_tr16)
+                o[0] = at(8 * g + (m >> 2), 8 * (m & 3));
+                o[1] = at(8 * g + (m >> 2) + 4, 8 * (m & 3));
             } else {
-                o[0] = g;
-                o[1] = 8 * (m >> 2) + (m & 3);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] = at(8 * g + i, 8 * (m >> 2) + (m & 3));
             }
         }
+        __device__ __forceinline__ void fresh() {
+#pragma unroll
+            for (int i = 0; i < (P::is_bf16 ? 2 : 8); ++i) asm volatile("" : "+v"(o[i]));
+        }
         __device__ __forceinline__ typename P::Frag get(const T* t, int j, int k, int h) const {
+            const T* p = t + 32 * j * W;
+            const int f = 32 * k + 4 * h;
             if constexpr (P::is_bf16) {
-                const T* p = t + 32 * j * W;
-                const int q = 4 * k + 2 * h;
-                return pair(lds_tr16(p + o[q]), lds_tr16(p + o[q + 1]));
+                return pair(lds_tr16(p + (o[0] ^ f)), lds_tr16(p + (o[1] ^ f)));
             } else {
                 f32x8 v;
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    v[i] = t[at(32 * j + 8 * o[0] + i, 32 * k + 4 * h + o[1])];
+                for (int i = 0; i < 8; ++i) v[i] = p[o[i] ^ f];
                 return v;
             }
         }
