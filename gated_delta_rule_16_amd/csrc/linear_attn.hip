@@ -66,8 +66,8 @@ template <class P, int KD> struct PTileWork {
         if constexpr (P::is_bf16) {         // fp32: too many registers
 #pragma unroll
             for (int k = 0; k < NK; ++k) {
-                xf[k] = xrow.raw(x, i, k);
-                yf[k] = yrow.raw(y, j, k);
+                xf[k] = xrow.get(x, i, k);
+                yf[k] = yrow.get(y, j, k);
             }
         }
     }
@@ -80,10 +80,10 @@ template <class P, int KD> struct PTileWork {
 #pragma unroll
         for (int k = 0; k < NK; ++k) {
             if constexpr (!P::is_bf16) {
-                xf[k] = xrow.raw(s.x[pb], i, k);
-                yf[k] = yrow.raw(s.y[pb], j, k);
+                xf[k] = xrow.get(s.x[pb], i, k);
+                yf[k] = yrow.get(s.y[pb], j, k);
             }
-            c = P::mma(yrow.order(yf[k]), xf[k], c);
+            c = P::mma(yf[k], xf[k], c);
         }
         f32x4 v;
         if (i == j) {
@@ -123,7 +123,7 @@ template <class P, int KD, bool OUT> struct Bringer {
     struct Coming {
         Stage<P, KD, ROWS> x;
         Stage<P, KD, BOTH> y;
-        Stage<P, ZB, COLS> z;
+        Stage<P, ZB, BOTH> z;
     };
     const char *xb, *yb, *zb;
     int64_t xt, yt, zt;
@@ -212,22 +212,23 @@ template <class P, bool OUT> struct Decays {
     }
 };
 
-// Team U: the state of 16 channels of z per wave, transposed: tile u = 2 k + h, row
-// 4 g + r, is channel 32 k + 8 g + 4 h + r of x and y, column m channel zc + m.
+// Team U: the state of 16 channels of z per wave, transposed: row 4 g + r of tile u is
+// channel 16 u + 4 g + r of x and y, column m channel zc + m of z.
 template <class P, int KD> struct State {
     typedef Tile<P, KD, BOTH> TY;
-    typedef Tile<P, ZB, COLS> TZ;
+    typedef Tile<P, ZB, BOTH> TZ;
     static constexpr int NU = KD / 16, NJ = P::C / 32;
     f32x4 H[NU];
     Terms<typename P::Frag, P::NS> zt[NJ];
     float tot;
-    int g, m, zc, zd, kd;
+    int g, m, w, zc, zd, kd;
     int64_t hz, hk;
     typename TY::Cols cols;
-    typename TZ::Col16 zcol;
+    typename TZ::Cols zcol;
 
     __device__ __forceinline__ State(const LaJob& jb, int zb, int tid) {
-        const int lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+        const int lane = tid & 63;
+        w = __builtin_amdgcn_readfirstlane(tid >> 6);
         g = lane >> 4;
         m = lane & 15;
         zc = zb * ZB + 16 * w;
@@ -236,17 +237,17 @@ template <class P, int KD> struct State {
         hz = jb.hz;
         hk = jb.hk;
         cols.init(lane);
-        zcol.init(lane, 16 * w);
+        zcol.init(lane);
 #pragma unroll
         for (int u = 0; u < NU; ++u) H[u] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
     __device__ __forceinline__ bool has(int u) const {
-        return zc + m < zd && 32 * (u >> 1) + 8 * g < kd;
+        return zc + m < zd && 16 * u + 4 * g < kd;
     }
     // The lane's first element of the state in memory.  Formed anew where it is used:
     // all the offsets, kept over the loop, would not leave registers for the rest.
     __device__ __forceinline__ int first() const {
-        int e = (zc + m) * (int)hz + 8 * g * (int)hk;
+        int e = (zc + m) * (int)hz + 4 * g * (int)hk;
         asm volatile("" : "+v"(e));
         return e;
     }
@@ -256,7 +257,7 @@ template <class P, int KD> struct State {
         for (int u = 0; u < NU; ++u)
             if (has(u)) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) H[u][r] = p[(32 * (u >> 1) + 4 * (u & 1) + r) * (int)hk];
+                for (int r = 0; r < 4; ++r) H[u][r] = p[(16 * u + r) * (int)hk];
             }
     }
     __device__ __forceinline__ void store(float* p, float f) const {
@@ -266,19 +267,29 @@ template <class P, int KD> struct State {
             if (has(u)) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    p[(32 * (u >> 1) + 4 * (u & 1) + r) * (int)hk] = H[u][r] * f;
+                    p[(16 * u + r) * (int)hk] = H[u][r] * f;
             }
     }
-    // z of the chunk in `buf`, scaled to the chunk's end, as terms
-    template <class S> __device__ __forceinline__ void take(const S& s, int buf) {
+    // z of the chunk in `buf`, scaled to the chunk's end, as terms: read, and scaled
+    struct Taken {
+        typename P::Frag z[NJ];
+        f32x4 l[NJ][2];
+    };
+    template <class S> __device__ __forceinline__ void read(const S& s, int buf, Taken& t) {
         tot = s.total[buf];
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-            f32x8 v = P::widen(zcol.get(s.z[buf], j));
-            const f32x4 l0 = *reinterpret_cast<const f32x4*>(&s.leave[buf][32 * j + 8 * g]);
-            const f32x4 l1 = *reinterpret_cast<const f32x4*>(&s.leave[buf][32 * j + 8 * g + 4]);
+            t.z[j] = zcol.get(s.z[buf], j, w);
+            t.l[j][0] = *reinterpret_cast<const f32x4*>(&s.leave[buf][32 * j + 8 * g]);
+            t.l[j][1] = *reinterpret_cast<const f32x4*>(&s.leave[buf][32 * j + 8 * g + 4]);
+        }
+    }
+    __device__ __forceinline__ void take(const Taken& t) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] *= i < 4 ? l0[i & 3] : l1[i & 3];
+        for (int j = 0; j < NJ; ++j) {
+            f32x8 v = P::widen(t.z[j]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] *= t.l[j][i / 4][i % 4];
             P::template split<P::NS>(v, zt[j]);
         }
     }
@@ -295,7 +306,7 @@ template <class P, int KD> struct State {
 #pragma unroll
             for (int e = 0; e < W; ++e) {
                 const int u = i % (NU / W) * W + e;
-                yf[i & 1][e] = cols.get(s.y[buf], i / (NU / W), u >> 1, u & 1);
+                yf[i & 1][e] = cols.get(s.y[buf], i / (NU / W), u);
             }
         };
         fetch(0);
@@ -313,26 +324,22 @@ template <class P, int KD> struct State {
         }
     }
     // its terms to LDS, rows of z's channels
-    __device__ __forceinline__ void show(Shared<P, KD>& s, int w) const {
+    __device__ __forceinline__ void show(Shared<P, KD>& s) const {
         typedef Tile<P, KD, ROWS> TH;
-        int m = this->m;                // places formed anew, as in first()
-        asm volatile("" : "+v"(m));
+        int o = TH::at(m, 4 * g);
+        asm volatile("" : "+v"(o));         // as in first()
 #pragma unroll
-        for (int k = 0; k < KD / 32; ++k) {
-            const f32x8 v = {H[2 * k][0], H[2 * k][1], H[2 * k][2], H[2 * k][3],
-                             H[2 * k + 1][0], H[2 * k + 1][1], H[2 * k + 1][2], H[2 * k + 1][3]};
+        for (int u = 0; u < NU; ++u) {
+            const int to = (o ^ (16 * u)) + 16 * w * KD;
             if constexpr (P::is_bf16) {
-                Terms<typename P::Frag, P::NO> t;
-                P::template split<P::NO>(v, t);
+                uint32_t w0[P::NO], w1[P::NO];
+                P::template split_pair<P::NO>(H[u][0], H[u][1], w0);
+                P::template split_pair<P::NO>(H[u][2], H[u][3], w1);
 #pragma unroll
                 for (int q = 0; q < P::NO; ++q)
-                    *reinterpret_cast<u32x4*>(s.h[q] + 16 * w * KD + TH::piece(m, 4 * k + g)) =
-                        __builtin_bit_cast(u32x4, t.t[q]);
+                    *reinterpret_cast<uint2*>(s.h[q] + to) = uint2{w0[q], w1[q]};
             } else {
-                *reinterpret_cast<f32x4*>(s.h[0] + 16 * w * KD + TH::piece(m, 8 * k + 2 * g)) =
-                    H[2 * k];
-                *reinterpret_cast<f32x4*>(s.h[0] + 16 * w * KD + TH::piece(m, 8 * k + 2 * g + 1)) =
-                    H[2 * k + 1];
+                *reinterpret_cast<f32x4*>(s.h[0] + to) = H[u];
             }
         }
     }
@@ -362,7 +369,7 @@ __global__ __launch_bounds__(1024) void chain_kernel(LaChain a) {
     constexpr int C = P::C, NK = KD / 32, NI = C / 16, NT = NI / 2;
     typedef Tile<P, KD, ROWS> TX;
     typedef Tile<P, KD, BOTH> TY;
-    typedef Tile<P, ZB, COLS> TZ;
+    typedef Tile<P, ZB, BOTH> TZ;
     typedef PTile<P> TP;
     typedef typename P::T T;
     extern __shared__ __attribute__((aligned(16))) char smem[];
@@ -427,8 +434,10 @@ __global__ __launch_bounds__(1024) void chain_kernel(LaChain a) {
             if (n > 0) st.move(s, (int)((n - 1) & 1));
             lds_barrier();
             if (n < nc) {
-                st.show(s, wv - 8);
-                st.take(s, (int)(n & 1));
+                typename State<P, KD>::Taken t;
+                st.read(s, (int)(n & 1), t);
+                st.show(s);
+                st.take(t);
             }
             if (GRAD && keep && n > 0) {
                 int64_t t0;
@@ -458,11 +467,11 @@ __global__ __launch_bounds__(1024) void chain_kernel(LaChain a) {
     auto tile = [&](int t) { return half + 2 * t; };
     typename TX::Rows xrow;
     typename TY::Rows yrow;
-    typename TZ::Col16 zcol;
+    typename TZ::Cols zcol;
     typename TP::Rows prow;
     xrow.init(lane);
     yrow.init(lane);
-    zcol.init(lane, 16 * zg);
+    zcol.init(lane);
     prow.init(lane);
     const int zd = jb.zd, zc = at.zb * ZB + 16 * zg;
     const bool mine = zc + 4 * g < zd;                  // whether the lane has out channels
@@ -477,10 +486,12 @@ __global__ __launch_bounds__(1024) void chain_kernel(LaChain a) {
     const uint32_t rt = dots ? (uint32_t)(jb.r.st * sizeof(T)) : 0u;
     float* const db = dots ? jb.dots + (((int64_t)(zc >> 4) * a.B + at.b) * a.H + at.h) * a.T
                            : nullptr;
-    // the wave's tiles of P, at most two: of the ten in bf16, of the three in fp32
-    const int pi = NI == 4 ? (0x32132233 >> (4 * wv)) & 3 : (wv == 1 ? 0 : 1);
-    const int pj = NI == 4 ? (0x32021010 >> (4 * wv)) & 3 : (wv == 2 ? 1 : 0);
-    const int np = NI == 4 ? (wv < 2 ? 2 : 1) : (wv < 3 ? 1 : 0);
+    // the wave's tiles of P, at most two: of the ten in bf16, of the three in fp32.
+    // Wave 3 has none: the factors are its part
+    const int pi = NI == 4 ? (0x32130233 >> (4 * wv)) & 3 : (wv == 1 ? 0 : 1);
+    const int pj = NI == 4 ? (0x32020010 >> (4 * wv)) & 3 : (wv == 2 ? 1 : 0);
+    const int qi = wv, qj = wv == 2 ? 1 : wv;
+    const int np = NI == 4 ? (wv < 3 ? 2 : wv == 3 ? 0 : 1) : (wv < 3 ? 1 : 0);
     const float pair = jb.pair;
     Decays<P, true> dec(a, at, jb, lane);
     if (wv == 3) {
@@ -521,9 +532,9 @@ __global__ __launch_bounds__(1024) void chain_kernel(LaChain a) {
             typename P::Frag xf[2][NT], hf[2][P::NO];
             auto fetch = [&](int k) {
 #pragma unroll
-                for (int t = 0; t < NT; ++t) xf[k & 1][t] = xrow.raw(s.x[buf], tile(t), k);
+                for (int t = 0; t < NT; ++t) xf[k & 1][t] = xrow.get(s.x[buf], tile(t), k);
 #pragma unroll
-                for (int q = 0; q < P::NO; ++q) hf[k & 1][q] = xrow.raw(s.h[q], zg, k);
+                for (int q = 0; q < P::NO; ++q) hf[k & 1][q] = xrow.get(s.h[q], zg, k);
             };
 #pragma unroll
             for (int t = 0; t < NT; ++t) O[t] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -541,7 +552,7 @@ __global__ __launch_bounds__(1024) void chain_kernel(LaChain a) {
             if (__builtin_expect(s.bad[buf] != (int)n, 1)) {
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
-                    const typename P::Frag zf = zcol.get(s.z[buf], j);
+                    const typename P::Frag zf = zcol.get(s.z[buf], j, zg);
 #pragma unroll
                     for (int q = P::NO - 1; q >= 0; --q)
 #pragma unroll
@@ -612,8 +623,8 @@ __global__ __launch_bounds__(1024) void chain_kernel(LaChain a) {
         if (n < nc && np > 0) {
             pw.write(s, nb, pi, pj, lane, pair, xrow, yrow);
             if (np > 1) {
-                pw.read(s.x[nb], s.y[nb], wv, wv, xrow, yrow);
-                pw.write(s, nb, wv, wv, lane, pair, xrow, yrow);
+                pw.read(s.x[nb], s.y[nb], qi, qj, xrow, yrow);
+                pw.write(s, nb, qi, qj, lane, pair, xrow, yrow);
             }
         }
         if (wv == 3 && n + 1 < nc) {
@@ -684,7 +695,9 @@ __global__ __launch_bounds__(512) void states_kernel(LaChain a) {
     State<P, KD> st(jb, at.zb, threadIdx.x);
     lds_barrier();
     for (int64_t n = 0; n < nc; ++n) {
-        st.take(s, (int)(n & 1));
+        typename State<P, KD>::Taken t;
+        st.read(s, (int)(n & 1), t);
+        st.take(t);
         st.move(s, (int)(n & 1));
         lds_barrier();
     }

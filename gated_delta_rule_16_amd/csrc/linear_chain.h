@@ -20,9 +20,7 @@ constexpr float kLeast = -1e4f;     // log decays from here on are a reset: exp 
 // 2474 LDS cycles a chunk).
 enum TileKind {
     ROWS,       // read by rows only
-    BOTH,       // by rows, and transposed 8 columns apart (bf16: some rows also keep
-                // the halves of their pieces swapped)
-    COLS        // read transposed only, 16 neighbouring columns at once
+    BOTH        // by rows, and transposed, 16 neighbouring columns at once
 };
 
 // A computed operand of a product: N bf16 terms, the largest first (or fp32 itself).
@@ -113,25 +111,17 @@ struct F32 {
 template <class P, int W, int KIND> struct Tile {
     typedef typename P::T T;
     static constexpr int PPR = W / P::EP;           // 16-byte pieces per row
-    static constexpr bool SWAP = KIND == BOTH && P::is_bf16;
     static __device__ __forceinline__ int swizzle(int row) {
         if constexpr (!P::is_bf16) return row & (PPR - 1) & 15;
         else if constexpr (KIND == ROWS) return row & (PPR - 1);
-        else if constexpr (KIND == COLS) return (row & 2) | ((row & 8) >> 1);
-        else {
-            const int s = ((row & 2) << 1) | ((row & 4) >> 1);
-            return PPR == 16 ? s | (row & 9) : s;
-        }
-    }
-    static __device__ __forceinline__ bool swapped(int row) {
-        return SWAP && (PPR == 16 ? row & 1 : row & 8);
+        else if constexpr (PPR == 16) return ((row & 3) << 1) | (row & 8);
+        else return (row & 2) | ((row & 8) >> 1);
     }
     static __device__ __forceinline__ int piece(int row, int c) {
         return row * W + (c ^ swizzle(row)) * P::EP;
     }
     static __device__ __forceinline__ int at(int row, int col) {
-        const int e = col % P::EP;
-        return piece(row, col / P::EP) + (swapped(row) ? e ^ 4 : e);
+        return piece(row, col / P::EP) + col % P::EP;
     }
 
     // A lane's first element of an operand; the others differ in bits that the swizzle
@@ -141,23 +131,12 @@ template <class P, int W, int KIND> struct Tile {
     // Elements 32 k + 8 g .. + 7 of row 16 i + m (the swizzle repeats every 16 rows).
     struct Rows {
         int o;
-        bool swap;
         __device__ __forceinline__ void init(int lane) {
             const int g = lane >> 4, m = lane & 15;
-            swap = swapped(m);
             o = piece(m, 8 / P::EP * g);
         }
         __device__ __forceinline__ void fresh() { asm volatile("" : "+v"(o)); }
-        // as it lies, and with its halves in order
-        __device__ __forceinline__ typename P::Frag order(const typename P::Frag& f) const {
-            if constexpr (SWAP) {
-                const u32x4 v = __builtin_bit_cast(u32x4, f);
-                return __builtin_bit_cast(bf16x8, swap ? u32x4{v[2], v[3], v[0], v[1]} : v);
-            } else {
-                return f;
-            }
-        }
-        __device__ __forceinline__ typename P::Frag raw(const T* t, int i, int k) const {
+        __device__ __forceinline__ typename P::Frag get(const T* t, int i, int k) const {
             const T* p = t + 16 * i * W;
             if constexpr (P::is_bf16) {
                 return __builtin_bit_cast(bf16x8,
@@ -170,59 +149,33 @@ template <class P, int W, int KIND> struct Tile {
         }
     };
 
-    // Rows 32 j + 8 g .. + 7 of column 32 k + 4 h + 8 (m / 4) + m % 4.
+    // Rows 32 j + 8 g .. + 7 of column 16 u + m.
     struct Cols {
         int o[P::is_bf16 ? 2 : 8];
         __device__ __forceinline__ void init(int lane) {
             const int g = lane >> 4, m = lane & 15;
             if constexpr (P::is_bf16) {
                 // lane 4 r + c of a group points at 4 columns of row r (lds_tr16)
-                o[0] = at(8 * g + (m >> 2), 8 * (m & 3));
-                o[1] = at(8 * g + (m >> 2) + 4, 8 * (m & 3));
+                o[0] = at(8 * g + (m >> 2), 4 * (m & 3));
+                o[1] = at(8 * g + (m >> 2) + 4, 4 * (m & 3));
             } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = at(8 * g + i, 8 * (m >> 2) + (m & 3));
+                for (int i = 0; i < 8; ++i) o[i] = at(8 * g + i, m);
             }
         }
         __device__ __forceinline__ void fresh() {
 #pragma unroll
             for (int i = 0; i < (P::is_bf16 ? 2 : 8); ++i) asm volatile("" : "+v"(o[i]));
         }
-        __device__ __forceinline__ typename P::Frag get(const T* t, int j, int k, int h) const {
+        __device__ __forceinline__ typename P::Frag get(const T* t, int j, int u) const {
             const T* p = t + 32 * j * W;
-            const int f = 32 * k + 4 * h;
+            const int f = 16 * u;
             if constexpr (P::is_bf16) {
                 return pair(lds_tr16(p + (o[0] ^ f)), lds_tr16(p + (o[1] ^ f)));
             } else {
                 f32x8 v;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[i] = p[o[i] ^ f];
-                return v;
-            }
-        }
-    };
-
-    // Rows 32 j + 8 g .. + 7 of column col0 + m (col0 a multiple of 16).
-    struct Col16 {
-        int o[2];
-        __device__ __forceinline__ void init(int lane, int col0) {
-            const int g = lane >> 4, m = lane & 15;
-            if constexpr (P::is_bf16) {
-                o[0] = at(8 * g + (m >> 2), col0 + 4 * (m & 3));
-                o[1] = at(8 * g + (m >> 2) + 4, col0 + 4 * (m & 3));
-            } else {
-                o[0] = g;
-                o[1] = col0 + m;
-            }
-        }
-        __device__ __forceinline__ typename P::Frag get(const T* t, int j) const {
-            if constexpr (P::is_bf16) {
-                const T* p = t + 32 * j * W;
-                return pair(lds_tr16(p + o[0]), lds_tr16(p + o[1]));
-            } else {
-                f32x8 v;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = t[at(32 * j + 8 * o[0] + i, o[1])];
                 return v;
             }
         }
@@ -331,8 +284,7 @@ template <class P, int W, int KIND> struct Stage {
         }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            u32x4 v = w[i];
-            if constexpr (Tl::SWAP) v = Tl::swapped(row0) ? u32x4{v[2], v[3], v[0], v[1]} : v;
+            const u32x4 v = w[i];
             // the swizzle repeats every 16 rows
             if constexpr (STEP % 16 == 0)
                 *reinterpret_cast<u32x4*>(tile + Tl::piece(row0, c0) + i * STEP * W) = v;
