@@ -586,6 +586,16 @@ __global__ __launch_bounds__(1024) void chain_kernel(LaChain a) {
             }
         }
         lds_barrier();
+        // before the stores: the wait for the decays would be one for these too
+        if (wv == 3 && n + 1 < nc) {
+            dec.scan(s, n + 1);
+            if (n + 2 < nc) {
+                int64_t t2;
+                int len2;
+                ch.get(n + 2, t2, len2);
+                dec.ask(t2, len2);
+            }
+        }
         PTileWork<P, KD> pw;
         const int nb = (int)(n & 1);
         if (n < nc && np > 0) pw.read(s.x[nb], s.y[nb], pi, pj, xrow, yrow);
@@ -625,15 +635,6 @@ __global__ __launch_bounds__(1024) void chain_kernel(LaChain a) {
             if (np > 1) {
                 pw.read(s.x[nb], s.y[nb], qi, qj, xrow, yrow);
                 pw.write(s, nb, qi, qj, lane, pair, xrow, yrow);
-            }
-        }
-        if (wv == 3 && n + 1 < nc) {
-            dec.scan(s, n + 1);
-            if (n + 2 < nc) {
-                int64_t t2;
-                int len2;
-                ch.get(n + 2, t2, len2);
-                dec.ask(t2, len2);
             }
         }
         lds_barrier();
