@@ -108,10 +108,9 @@ struct RotaryArgs {
     const double* freqs;
     float scale;
     hipStream_t stream;
-    // by rotary_shape: units of 8 channels per head, those that turn first; heads
-    // per thread and groups of them
-    int units, turning, hper;
-    int64_t groups;
+    // by rotary_shape: units of 8 channels per head, those that turn first; tokens
+    // per workgroup
+    int units, turning, tokens;
 };
 
 // RMS norm: rows of C channels, x and res with a stride per row.

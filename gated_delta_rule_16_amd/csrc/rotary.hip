@@ -1,9 +1,10 @@
 // gdr_rotary: the first channels of every head of q and k as pairs, turned by
 // position times rate.
 //
-// Bound by HBM: one read and one write of every element.  A thread takes 8 channels
-// (and, in the half layout, the 8 of their partners) of one token, forms the 8 (4)
-// angles' sine and cosine once, and walks several heads with them.
+// Bound by HBM: one read and one write of every element.  A workgroup takes a few
+// tokens: it forms the sines and cosines of their angles once, in LDS, and its threads
+// walk the heads side by side, 8 channels (in the half layout with the 8 of their
+// partners) to a thread, so a wave reads consecutive memory.
 #include "linear_launch.h"
 #include "mfma_common.h"
 #include "rows.h"
@@ -13,6 +14,7 @@ namespace gdr {
 namespace {
 
 constexpr int E = 8;
+constexpr int TB = 4;       // tokens with their loads in flight at once
 
 // sin and cos of t quarter turns.  The reduction is in 64 bits; the rest is at most
 // half a quarter turn, where the Taylor series to x^9 and x^10 err by 2e-9.
@@ -37,72 +39,107 @@ __device__ __forceinline__ void sincos_quarters(double t, float& s, float& c) {
     c = (k == 1 || k == 2) ? -b : b;
 }
 
-// Threads: head group outermost, then tokens, then units of 8 channels: first those
-// that turn (half layout: 8 pairs each), then those that are copied.
+// An item is 8 channels of a head: `turning` of its units turn (half layout: 8 pairs
+// each), the others are copied.  A thread keeps its item over its tokens.
 template <bool BF16, bool INTER, bool RAG>
 __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a) {
-    const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    const int64_t per = a.B * a.T * a.units;
-    if (id >= per * a.groups) return;
-    const int unit = (int)(id % a.units);
-    const int64_t tok = id / a.units % (a.B * a.T);
-    const int64_t b = tok / a.T, t = tok % a.T;
-    const int h0 = (int)(id / per) * a.hper;
-    int h1 = h0 + a.hper;
-    if (h1 > a.Hq + a.Hk) h1 = (int)(a.Hq + a.Hk);
-
-    const bool turns = unit < a.turning;
-    const int half = (int)a.rot / 2;
-    const int c0 = turns ? unit * E : (int)a.rot + (unit - a.turning) * E;
-    const int end = turns ? (INTER ? (int)a.rot : half) : (int)a.D;
-    const int v0 = end - c0 < E ? end - c0 : E;
-    const int v1 = !INTER && turns ? v0 : 0;          // partners
     constexpr int NF = INTER ? E / 2 : E;
-    float sn[NF], cs[NF];
-    if (turns) {
-        const int64_t pos = a.positions ? a.positions[b * a.pos_stride + t] : a.start + t;
-        const double p = (double)pos * 0.6366197723675814;
-#pragma unroll
-        for (int f = 0; f < NF; ++f) {
-            const int i = (INTER ? c0 / 2 : c0) + f;
-            sincos_quarters(p * (i < half ? a.freqs[i] : 0.0), sn[f], cs[f]);
-            sn[f] *= a.inverse ? -a.scale : a.scale;
-            cs[f] *= a.scale;
-        }
+    extern __shared__ __attribute__((aligned(16))) char smem[];
+    struct Token {
+        int64_t qi, qo, ki, ko;
+        double pos;
+    };
+    Token* const tokens = reinterpret_cast<Token*>(smem);
+    float2* const turn = reinterpret_cast<float2*>(smem + a.tokens * sizeof(Token));
+    const int tid = threadIdx.x, half = (int)a.rot / 2;
+    const int64_t n = a.B * a.T, first = (int64_t)blockIdx.x * a.tokens;
+    const int nt = (int)(n - first < a.tokens ? n - first : a.tokens);
+    if (tid < nt) {
+        const int64_t b = (first + tid) / a.T, t = (first + tid) % a.T;
+        Token k;
+        k.qi = b * a.q.ib + t * a.q.it;
+        k.qo = b * a.q.ob + t * a.q.ot;
+        k.ki = b * a.k.ib + t * a.k.it;
+        k.ko = b * a.k.ob + t * a.k.ot;
+        // in quarter turns per unit of rate
+        k.pos = (double)(a.positions ? a.positions[b * a.pos_stride + t] : a.start + t) *
+                0.6366197723675814;
+        tokens[tid] = k;
     }
-#pragma unroll 4
-    for (int h = h0; h < h1; ++h) {
-        const bool isq = h < a.Hq;
-        const RotarySide& s = isq ? a.q : a.k;
-        const int64_t hh = isq ? h : h - a.Hq;
-        const int64_t in = b * s.ib + t * s.it + hh * s.ih + c0;
-        const int64_t out = b * s.ob + t * s.ot + hh * s.oh + c0;
-        Row<E, BF16, RAG> r0, r1;
-        r0.load(s.in, in, v0);
-        r1.load(s.in, in + half, v1);
-        if (!turns) {
-            r0.copy_to(s.out, out, v0);
-            continue;
-        }
-        float x[E], y[E];
-        r0.unpack(x);
-        if constexpr (INTER) {
+    __syncthreads();
+    for (int i = tid; i < nt * half; i += 256) {
+        float s, c;
+        sincos_quarters(tokens[i / half].pos * a.freqs[i % half], s, c);
+        turn[i] = float2{c * a.scale, s * (a.inverse ? -a.scale : a.scale)};
+    }
+    __syncthreads();
+    const int heads = (int)(a.Hq + a.Hk), items = heads * a.units;
+    // fewer items than threads: several tokens side by side
+    const int side = items >= 256 ? 1 : 256 / items;
+    const int t0 = side > 1 ? tid / items : 0;
+    if (t0 >= side) return;
+    for (int item = side > 1 ? tid % items : tid; item < items; item += 256) {
+        const int unit = item % a.units, h = item / a.units;
+        const bool isq = h < a.Hq, turns = unit < a.turning;
+        const void* const in = isq ? a.q.in : a.k.in;
+        void* const out = isq ? a.q.out : a.k.out;
+        const int c0 = turns ? unit * E : (int)a.rot + (unit - a.turning) * E;
+        const int end = turns ? (INTER ? (int)a.rot : half) : (int)a.D;
+        const int v0 = end - c0 < E ? end - c0 : E;
+        const int v1 = !INTER && turns ? v0 : 0;          // partners
+        const int64_t hi = (isq ? h * a.q.ih : (h - a.Hq) * a.k.ih) + c0;
+        const int64_t ho = (isq ? h * a.q.oh : (h - a.Hq) * a.k.oh) + c0;
+        const int f0 = INTER ? c0 / 2 : c0;
+        // all loads of a few tokens before the first store (which a later load of the
+        // same memory would have to wait for)
+        for (int tb = t0; tb < nt; tb += TB * side) {
+            Row<E, BF16, RAG> r0[TB], r1[INTER ? 1 : TB];
 #pragma unroll
-            for (int f = 0; f < NF; ++f) {
-                y[2 * f] = x[2 * f] * cs[f] - x[2 * f + 1] * sn[f];
-                y[2 * f + 1] = x[2 * f] * sn[f] + x[2 * f + 1] * cs[f];
+            for (int i = 0; i < TB; ++i) {
+                const int t = tb + i * side;
+                const Token& k = tokens[t < nt ? t : tb];
+                const int64_t at = (isq ? k.qi : k.ki) + hi;
+                r0[i].load(in, at, t < nt ? v0 : 0);
+                if constexpr (!INTER) r1[i].load(in, at + half, t < nt ? v1 : 0);
             }
-            row_store<E, RAG>(s.out, out, BF16, y, v0);
-        } else {
-            float w[E], z[E];
-            r1.unpack(w);
 #pragma unroll
-            for (int f = 0; f < NF; ++f) {
-                y[f] = x[f] * cs[f] - w[f] * sn[f];
-                z[f] = x[f] * sn[f] + w[f] * cs[f];
+            for (int i = 0; i < TB; ++i) {
+                const int t = tb + i * side;
+                if (t >= nt) break;
+                const int64_t at = (isq ? tokens[t].qo : tokens[t].ko) + ho;
+                if (!turns) {
+                    r0[i].copy_to(out, at, v0);
+                    continue;
+                }
+                float cs[NF], sn[NF];
+#pragma unroll
+                for (int f = 0; f < NF; ++f) {
+                    const int g = !RAG || f0 + f < half ? f0 + f : half - 1;
+                    const float2 v = turn[t * half + g];
+                    cs[f] = v.x;
+                    sn[f] = v.y;
+                }
+                float x[E], y[E];
+                r0[i].unpack(x);
+                if constexpr (INTER) {
+#pragma unroll
+                    for (int f = 0; f < NF; ++f) {
+                        y[2 * f] = x[2 * f] * cs[f] - x[2 * f + 1] * sn[f];
+                        y[2 * f + 1] = x[2 * f] * sn[f] + x[2 * f + 1] * cs[f];
+                    }
+                    row_store<E, RAG>(out, at, BF16, y, v0);
+                } else {
+                    float w[E], z[E];
+                    r1[i].unpack(w);
+#pragma unroll
+                    for (int f = 0; f < NF; ++f) {
+                        y[f] = x[f] * cs[f] - w[f] * sn[f];
+                        z[f] = x[f] * sn[f] + w[f] * cs[f];
+                    }
+                    row_store<E, RAG>(out, at, BF16, y, v0);
+                    row_store<E, RAG>(out, at + half, BF16, z, v1);
+                }
             }
-            row_store<E, RAG>(s.out, out, BF16, y, v0);
-            row_store<E, RAG>(s.out, out + half, BF16, z, v1);
         }
     }
 }
@@ -111,30 +148,37 @@ int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 template <bool BF16, bool INTER> void go(const RotaryArgs& a, dim3 grid) {
     const bool whole = (INTER ? a.rot : a.rot / 2) % E == 0 && (a.D - a.rot) % E == 0;
-    if (whole) hipLaunchKernelGGL((rotary_kernel<BF16, INTER, false>), grid, dim3(256), 0, a.stream, a);
-    else hipLaunchKernelGGL((rotary_kernel<BF16, INTER, true>), grid, dim3(256), 0, a.stream, a);
+    const size_t lds = a.tokens * (5 * 8 + 8 * (size_t)(a.rot / 2));
+    if (whole)
+        hipLaunchKernelGGL((rotary_kernel<BF16, INTER, false>), grid, dim3(256), lds, a.stream, a);
+    else
+        hipLaunchKernelGGL((rotary_kernel<BF16, INTER, true>), grid, dim3(256), lds, a.stream, a);
 }
 
 }  // namespace
 
-// Units and head groups of a call.  In place, what does not turn is left alone.
+// Units and tokens per workgroup of a call.  In place, what does not turn is left
+// alone.
 void rotary_shape(RotaryArgs& a) {
     a.turning = (int)cdiv(a.interleaved ? a.rot : a.rot / 2, E);
     const bool same = a.q.in == a.q.out && (a.Hk == 0 || a.k.in == a.k.out);
     a.units = a.turning + (same ? 0 : (int)cdiv(a.D - a.rot, E));
-    const int64_t heads = a.Hq + a.Hk, threads = a.B * a.T * a.units;
-    int64_t hper = 16;
-    while (hper > 1 && threads * cdiv(heads, hper) < 65536) hper /= 2;
-    a.hper = (int)hper;
-    a.groups = cdiv(heads, hper);
+    // 8 items a thread, sines and cosines in 32 KB, and no fewer workgroups than twice
+    // the compute units where that leaves them tokens
+    int64_t n = 2048 / ((a.Hq + a.Hk) * a.units);
+    const int64_t most = 4096 / (a.rot / 2), few = a.B * a.T / 512;
+    if (n > most) n = most;
+    if (n > few) n = few;
+    if (n > 64) n = 64;
+    a.tokens = (int)(n < 1 ? 1 : n);
 }
 
 double rotary_work_items(const RotaryArgs& a) {
-    return (double)a.B * (double)a.T * a.units * (double)a.groups + 256.0;
+    return ((double)a.B * (double)a.T / a.tokens + 1.0) * 256.0;
 }
 
 hipError_t launch_rotary(const RotaryArgs& a) {
-    const dim3 grid((unsigned)cdiv(a.B * a.T * a.units * a.groups, 256));
+    const dim3 grid((unsigned)cdiv(a.B * a.T, a.tokens));
     if (a.bf16) {
         if (a.interleaved) go<true, true>(a, grid);
         else go<true, false>(a, grid);
