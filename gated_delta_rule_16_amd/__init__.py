@@ -1375,42 +1375,32 @@ def gdr_rotary(q, k, positions, freqs, *, interleaved=False, scale=1.0, inverse=
     ``k_out``, which may be q and k themselves."""
     if not isinstance(q, torch.Tensor):
         raise TypeError("q must be a torch.Tensor")
-    lead = q.dim() - 2
+    shape = q.shape
+    lead = len(shape) - 2
     if lead not in (1, 2):
         raise ValueError(f"q must have 3 or 4 dimensions, got {q.dim()}")
     dev = _first("q", q, lead + 2)
-    Hq, D = q.shape[lead:]
-    B, T = q.shape[0], (q.shape[1] if lead == 2 else 1)
-
-    def strides(name, t, heads):
-        s = _heads(name, t, q.dtype, (*q.shape[:lead], heads, D), dev, lead)
-        return s if lead == 2 else (s[0], 0, s[1])
-
-    def out(name, t, like, heads):
-        if t is None:
-            t = torch.empty((*q.shape[:lead], heads, D), dtype=q.dtype, device=dev)
-        return t, strides(name, t, heads)
-
-    qs = strides("q", q, Hq)
-    q_out, qos = out("q_out", q_out, q, Hq)
-    Hk, ks, kos = 0, (0, 0, 0), (0, 0, 0)
-    if k is not None:
-        _first("k", k, lead + 2)
-        Hk = k.shape[lead]
-        ks = strides("k", k, Hk)
-        k_out, kos = out("k_out", k_out, k, Hk)
-    elif k_out is not None:
-        raise ValueError("k_out needs k")
+    Hq, D = shape[lead], shape[lead + 1]
+    B, T = shape[0], (shape[1] if lead == 2 else 1)
     if not isinstance(freqs, torch.Tensor) or freqs.dim() != 1:
         raise ValueError("freqs must be a [rot / 2] tensor")
     _whole("freqs", freqs, torch.float64, freqs.shape, dev)
+    st, q_out = _rotary_side("q", q, q_out, shape, lead, T)
+    ks, Hk = (0,) * 6, 0
+    if k is not None:
+        _first("k", k, lead + 2)
+        Hk = k.shape[lead]
+        _like("k", k, q.dtype, shape[:lead] + (Hk, D), dev)
+        ks, k_out = _rotary_side("k", k, k_out, k.shape, lead, T)
+    elif k_out is not None:
+        raise ValueError("k_out needs k")
     pos, ps, start = None, 0, 0
     if isinstance(positions, torch.Tensor):
         pos = positions
         if lead == 2 and pos.dim() == 1:
-            _whole("positions", pos, torch.int64, (T,), dev)
+            _whole("positions", pos, torch.int64, shape[1:2], dev)
         else:
-            _like("positions", pos, torch.int64, q.shape[:lead], dev)
+            _like("positions", pos, torch.int64, shape[:lead], dev)
             ps = pos.stride(0)
             if lead == 2 and T > 1 and pos.stride(1) != 1:
                 raise ValueError("positions must have contiguous tokens")
@@ -1418,10 +1408,32 @@ def gdr_rotary(q, k, positions, freqs, *, interleaved=False, scale=1.0, inverse=
         start = int(positions)
     flags = (GDR_ROTARY_INTERLEAVED if interleaved else 0) | (GDR_ROTARY_INVERSE if inverse else 0)
     _run("gdr_rotary", lib.gdr_rotary(
-        B, T, Hq, Hk, D, 2 * freqs.shape[0], _DT[q.dtype], _p(q), _p(k),
-        _i64s(*qs, *ks, *qos, *kos), _p(pos), ps, start, _p(freqs), float(scale), flags, _p(q_out),
-        _p(k_out), _raw_stream(dev.index)))
+        B, T, Hq, Hk, D, 2 * freqs.shape[0], _DT[q.dtype], q.data_ptr(), _p(k),
+        _ROTARY_STRIDES(*st[:3], *ks[:3], *st[3:], *ks[3:]), _p(pos), ps, start, freqs.data_ptr(),
+        scale, flags, q_out.data_ptr(), _p(k_out), _raw_stream(dev.index)))
     return q_out, k_out
+
+
+_ROTARY_STRIDES = ctypes.c_int64 * 12
+
+
+def _rotary_side(name, t, out, shape, lead, T):
+    """Strides per sequence, token and head of q or k and of its output, and that."""
+    H, D = shape[lead], shape[lead + 1]
+    st = t.stride()
+    if D > 1 and st[-1] != 1 and t.numel():
+        raise ValueError(f"{name} must have contiguous channels")
+    if out is None:
+        out = torch.empty(shape, dtype=t.dtype, device=t.device)
+        so = (T * H * D, H * D, D)
+        return (st[:3] if lead == 2 else (st[0], 0, st[1])) + so, out
+    _like(name + "_out", out, t.dtype, shape, t.device)
+    so = out.stride()
+    if D > 1 and so[-1] != 1 and out.numel():
+        raise ValueError(f"{name}_out must have contiguous channels")
+    if lead == 2:
+        return st[:3] + so[:3], out
+    return (st[0], 0, st[1], so[0], 0, so[1]), out
 
 
 def _rms_inputs(x, w, residual, h):

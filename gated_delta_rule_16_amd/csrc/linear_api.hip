@@ -279,7 +279,7 @@ extern "C" gdr_status_t gdr_rotary(int64_t B, int64_t T, int64_t Hq, int64_t Hk,
         return GDR_ERR_UNSUPPORTED;
     if (rot <= 0 || rot % 2 || rot > D) return GDR_ERR_INVALID;
     if (!strides_ok(strides, 12) || !strides_ok(&pos_stride, 1) || !product_ok({B, T, Hq + Hk, D}) ||
-        Hq + Hk > ((int64_t)1 << 30))
+        Hq + Hk > GDR_MAX_HEADS)
         return GDR_ERR_INVALID;
     if (B == 0 || T == 0 || Hq + Hk == 0) return GDR_OK;
     const size_t e = elem(dt);

@@ -115,7 +115,7 @@ gdr_status_t gdr_linear_attn_bwd(int64_t B, int64_t T, int64_t H, int64_t Hk, in
  * back: the reverse mode, for the gradients of the outputs.
  *
  *   q, k      [B, T, Hq, D], [B, T, Hk, D] dt (k NULL with Hk = 0); strides
- *             {q, k, q_out, k_out}
+ *             {q, k, q_out, k_out}; Hq + Hk at most GDR_MAX_HEADS
  *   rot       even, 0 < rot <= D <= GDR_ROTARY_MAX_D
  *   positions [B, T] int64 with pos_stride elements from sequence to sequence
  *             (0: shared), or NULL: start + t
