@@ -1410,7 +1410,7 @@ def gdr_rotary(q, k, positions, freqs, *, interleaved=False, scale=1.0, inverse=
     _run("gdr_rotary", lib.gdr_rotary(
         B, T, Hq, Hk, D, 2 * freqs.shape[0], _DT[q.dtype], q.data_ptr(), _p(k),
         _ROTARY_STRIDES(*st[:3], *ks[:3], *st[3:], *ks[3:]), _p(pos), ps, start, freqs.data_ptr(),
-        scale, flags, q_out.data_ptr(), _p(k_out), _raw_stream(dev.index)))
+        float(scale), flags, q_out.data_ptr(), _p(k_out), _raw_stream(dev.index)))
     return q_out, k_out
 
 

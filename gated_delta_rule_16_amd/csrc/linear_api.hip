@@ -1,6 +1,8 @@
 // C ABI of linear attention, rotary positions and RMS norm (declared in
 // gdr_linear.h).  Host-side validation and dispatch; an error status means nothing
 // was launched.
+#include <algorithm>
+#include <array>
 #include <cmath>
 #include <initializer_list>
 
@@ -35,6 +37,20 @@ bool apart(Ptrs outs, Ptrs ins) {
 bool strides_ok(const int64_t* s, int n) {
     for (int i = 0; s && i < n; ++i)
         if (s[i] < 0 || s[i] > ((int64_t)1 << 40)) return false;
+    return true;
+}
+
+// Whether the rows of `d` elements at every multiple of the strides lie apart: by
+// growing stride, each passes what the dimensions before it take up.
+bool places_apart(std::array<int64_t, 3> n, std::array<int64_t, 3> stride, int64_t d) {
+    std::array<int, 3> order{0, 1, 2};
+    std::sort(order.begin(), order.end(), [&](int i, int j) { return stride[i] < stride[j]; });
+    double span = (double)d;
+    for (int i : order) {
+        if (n[i] <= 1) continue;
+        if ((double)stride[i] < span) return false;
+        span += (double)stride[i] * (double)(n[i] - 1);
+    }
     return true;
 }
 
@@ -278,8 +294,8 @@ extern "C" gdr_status_t gdr_rotary(int64_t B, int64_t T, int64_t Hq, int64_t Hk,
         D > GDR_ROTARY_MAX_D)
         return GDR_ERR_UNSUPPORTED;
     if (rot <= 0 || rot % 2 || rot > D) return GDR_ERR_INVALID;
-    if (!strides_ok(strides, 12) || !strides_ok(&pos_stride, 1) || !product_ok({B, T, Hq + Hk, D}) ||
-        Hq + Hk > GDR_MAX_HEADS)
+    if (Hq > GDR_MAX_HEADS || Hk > GDR_MAX_HEADS - Hq || !strides_ok(strides, 12) ||
+        !strides_ok(&pos_stride, 1) || !product_ok({B, T, Hq + Hk, D}))
         return GDR_ERR_INVALID;
     if (B == 0 || T == 0 || Hq + Hk == 0) return GDR_OK;
     const size_t e = elem(dt);
@@ -306,9 +322,11 @@ extern "C" gdr_status_t gdr_rotary(int64_t B, int64_t T, int64_t Hq, int64_t Hk,
     a.k = {k, k_out, ki.sb, ki.st, ki.sh, ko.sb, ko.st, ko.sh};
     for (const RotarySide* s : {&a.q, &a.k}) {
         if (!s->out) continue;
+        const int64_t heads = s == &a.q ? Hq : Hk;
+        if (!places_apart({B, T, heads}, {s->ob, s->ot, s->oh}, D)) return GDR_ERR_INVALID;
         // in place: every element where it was
         if (s->in == s->out && ((B > 1 && s->ib != s->ob) || (T > 1 && s->it != s->ot) ||
-                                ((s == &a.q ? Hq : Hk) > 1 && s->ih != s->oh)))
+                                (heads > 1 && s->ih != s->oh)))
             return GDR_ERR_INVALID;
     }
     if (!apart({q_out, k_out}, {positions, freqs}) || !apart({q_out}, {k}) || !apart({k_out}, {q}))

@@ -89,8 +89,9 @@ gdr_status_t gdr_linear_attn_step(int64_t N, int64_t H, int64_t Hk, int64_t Dk, 
  * dv [B, T, H, Dv] in grad_dt, and in fp32 dlog_decay (shaped as log_decay; NULL:
  * not wanted, as without log_decay; 0 where the decay itself is 0) and
  * ds0 [B, H, Dv, Dk] (or NULL).  The workspace holds states at every 1024 tokens
- * or fewer (twice 4 B H Dv Dk bytes each), 8 B T H ceil(Dk / 16) bytes for the
- * decay's gradient and, where Hk < H, 8 B T H Dk bytes for dq and dk of each head.
+ * or fewer (at most twice 4 B H Dv Dk bytes each; twice that where a sequence runs as
+ * segments), 8 B T H ceil(Dk / 16) bytes for the decay's gradient and, where Hk < H,
+ * 8 B T H Dk bytes for dq and dk of each head.
  * Workspace sizes are 0 for arguments the calls reject.
  */
 size_t gdr_linear_attn_bwd_workspace_size(int64_t B, int64_t T, int64_t H, int64_t Hk, int64_t Dk,
@@ -120,7 +121,9 @@ gdr_status_t gdr_linear_attn_bwd(int64_t B, int64_t T, int64_t H, int64_t Hk, in
  *   positions [B, T] int64 with pos_stride elements from sequence to sequence
  *             (0: shared), or NULL: start + t
  *   freqs     [rot / 2] double (device), as from gdr_rotary_frequencies
- *   q_out, k_out  like q and k; may be q and k themselves with equal strides
+ *   q_out, k_out  like q and k, their heads at places of their own (each stride
+ *             passes what the smaller ones span); may be q and k themselves with
+ *             equal strides
  *
  * Angles are formed and reduced in 64 bits, sine and cosine are within 2^-22.
  */
