@@ -427,7 +427,12 @@ __global__ __launch_bounds__(1024) void chain_kernel(LaChain a) {
     if (wv >= 8) {
         // ---- team U ----
         State<P, KD> st(jb, at.zb, threadIdx.x - 512);
-        if (jb.h_in) st.load(jb.h_in + (at.seg * a.B * a.H + bh) * a.state);
+        if (at.seg == (back ? a.nseg - 1 : 0)) {
+            if (jb.h_in) st.load(jb.h_in + bh * a.state);
+        } else {
+            const int64_t mark = back ? ch.tb : ch.ta;
+            st.load(jb.h_seg + ((mark / jb.h_every - 1) * a.B * a.H + bh) * a.state);
+        }
         float* const keep = GRAD ? jb.keep : nullptr;
         lds_barrier();
         for (int64_t n = 0; n <= nc; ++n) {
@@ -648,8 +653,10 @@ __global__ __launch_bounds__(512) void states_kernel(LaChain a) {
     Place at;
     if (!place(a, blockIdx.x, at)) return;
     const LaJob& jb = a.job[at.job];
+    if (at.seg == (jb.back ? 0 : a.nseg - 1)) return;       // no segment behind it
     const Chunks ch(a, at, jb.back, P::C);
-    const int64_t nc = ch.nc, bh = at.b * a.H + at.h;
+    const int64_t nc = ch.nc;
+    const int64_t to = (at.seg - (jb.back ? 1 : 0)) * a.B * a.H + at.b * a.H + at.h;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     if (wv >= 4) {
         typedef Bringer<P, KD, false> L;
@@ -690,7 +697,7 @@ __global__ __launch_bounds__(512) void states_kernel(LaChain a) {
         }
         lds_barrier();              // U's last chunk
         if (at.zb == 0 && threadIdx.x == 512 - 64)
-            jb.seg_decay[at.seg * a.B * a.H + bh] = __builtin_amdgcn_exp2f((float)dec.run);
+            jb.seg_decay[to] = __builtin_amdgcn_exp2f((float)dec.run);
         return;
     }
     State<P, KD> st(jb, at.zb, threadIdx.x);
@@ -702,13 +709,13 @@ __global__ __launch_bounds__(512) void states_kernel(LaChain a) {
         st.move(s, (int)(n & 1));
         lds_barrier();
     }
-    st.store(jb.h_out + (at.seg * a.B * a.H + bh) * a.state, 1.f);
+    st.store(jb.h_out + to * a.state, 1.f);
 }
 
-// Segments' own end states, in place, to their start states:
-// in(first) = h0, in(next) = decay in + own.  Up to two chains at once.
+// States at the marks between segments, in place, from the segments' own (as from a
+// start of zeros): at(next) = decay at(this) + own.  Up to two chains at once.
 struct Compose {
-    int64_t BH, state, nseg;
+    int64_t BH, state, marks;
     float* buf[2];
     const float *decay[2], *h0[2];
     bool back[2];
@@ -718,28 +725,27 @@ __global__ __launch_bounds__(256) void compose_kernel(Compose a) {
     const int k = blockIdx.y;
     const int64_t n = a.BH * a.state, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= n) return;
-    const int64_t bh = i / a.state, last = a.nseg - 1;
     float* buf = a.buf[k] + i;
-    const float* decay = a.decay[k] + bh;
+    const float* decay = a.decay[k] + i / a.state;
     float h = a.h0[k] ? a.h0[k][i] : 0.f;
     const bool back = a.back[k];
     // batches of loads: a store would hold back the next segment's
-    for (int64_t c = 0; c <= last; c += 8) {
+    for (int64_t c = 0; c < a.marks; c += 8) {
         float own[8], d[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int64_t p = back ? last - c - e : c + e;
+            const int64_t p = back ? a.marks - 1 - c - e : c + e;
             own[e] = d[e] = 0.f;
-            if (c + e < last) {
+            if (c + e < a.marks) {
                 own[e] = buf[p * n];
                 d[e] = decay[p * a.BH];
             }
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int64_t p = back ? last - c - e : c + e;
-            if (c + e <= last) buf[p * n] = h;
+            const int64_t p = back ? a.marks - 1 - c - e : c + e;
             h = d[e] * h + own[e];
+            if (c + e < a.marks) buf[p * n] = h;
         }
     }
 }
@@ -903,40 +909,76 @@ hipError_t launch_chain(const LaChain& a) {
     return fine ? launch_chain_p<Bf16<3>>(a) : launch_chain_p<Bf16<2>>(a);
 }
 
+// Segments of L tokens, and the marks between them.
 struct Plan {
-    int64_t L, nseg;
+    int64_t L, nseg, marks;
 };
+
+constexpr int kUnits = 256;         // compute units
+
+int64_t blocks(int64_t d) { return (d + ZB - 1) / ZB; }
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t chunk(bool bf16) { return bf16 ? Bf16<3>::C : F32::C; }
 
 // Segments: as many as fill the chip (a workgroup to each of 256 compute units), of at
 // least two chunks.  A second pass over k and v and the states' round trip cost less
 // than idle units: fp32 B3 T1025 H6 72 x 40 82 us with 4 segments, 49 with 14.
-Plan plan(int64_t T, int64_t units, bool bf16) {
-    const int64_t most = T / (bf16 ? 128 : 64);
-    int64_t nseg = 256 / units;
+// `grain`: a segment's tokens are a multiple of it, or fewer.
+Plan plan(int64_t T, int64_t units, bool bf16, int64_t grain) {
+    const int64_t C = chunk(bf16), most = T / (2 * C);
+    int64_t nseg = kUnits / units;
     if (nseg > most) nseg = most;
     if (nseg < 1) nseg = 1;
-    const int64_t C = bf16 ? Bf16<3>::C : F32::C;
-    int64_t L = (T + nseg - 1) / nseg;
-    L = (L + C - 1) / C * C;
-    return {L, (T + L - 1) / L};
+    int64_t L = cdiv(cdiv(T, nseg), C) * C;
+    if (L > grain) L = cdiv(L, grain) * grain;
+    nseg = cdiv(T, L);
+    return {L, nseg, nseg - 1};
 }
-
-int64_t blocks(int64_t d) { return (d + ZB - 1) / ZB; }
 
 Plan fwd_plan(int64_t B, int64_t T, int64_t H, int64_t Dv, bool bf16) {
-    return plan(T, B * H * blocks(Dv), bf16);
+    return plan(T, B * H * blocks(Dv), bf16, chunk(bf16));
 }
 
-// Kept states are at whole numbers of `every` tokens, which divides a segment.
-Plan bwd_plan(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, bool bf16, int64_t& every) {
-    Plan p = plan(T, B * H * (2 * blocks(Dk) + blocks(Dv)), bf16);
-    every = p.L;
-    if (p.L > 1024) {
-        p.L = (p.L + 1023) / 1024 * 1024;
-        p.nseg = (T + p.L - 1) / p.L;
-        every = 1024;
+// The backward's chains.  dq, dk and dv side by side, in segments p; or dq and dk first,
+// and dv in segments pv that start where dk's chain has left states anyway.
+struct BwdPlan {
+    Plan p, pv;
+    bool apart;
+    int64_t every, nblk;            // kept states: at whole numbers of `every` tokens
+};
+
+// Rounds of the chip times the chunks of a segment and what a workgroup's start costs.
+double chain_cost(int64_t workgroups, int64_t L, bool bf16) {
+    return (double)cdiv(workgroups, kUnits) * ((double)cdiv(L, chunk(bf16)) + 4.0);
+}
+
+BwdPlan bwd_plan(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, bool bf16) {
+    const int64_t BH = B * H, nk = BH * 2 * blocks(Dk), nv = BH * blocks(Dv);
+    // a pass over the states alone takes half the time
+    auto states = [&](const Plan& p) {
+        return p.nseg > 1 ? 0.5 * chain_cost(p.marks * (nk / 2 + nv), p.L, bf16) + 4.0 : 0.0;
+    };
+    auto every = [](const Plan& p) { return p.L > 1024 ? (int64_t)1024 : p.L; };
+    BwdPlan one{}, two{};
+    one.p = plan(T, nk + nv, bf16, 1024);
+    one.every = every(one.p);
+    one.nblk = cdiv(T, one.every);
+    two.p = plan(T, nk, bf16, 1024);
+    two.apart = true;
+    two.every = every(two.p);
+    two.nblk = cdiv(T, two.every);
+    double best = 0.0;
+    for (int64_t n = 1; n <= two.nblk && n <= 64; ++n) {
+        const int64_t L = cdiv(two.nblk, n) * two.every, nseg = cdiv(T, L);
+        const double c = chain_cost(nv * nseg, L, bf16);
+        if (n > 1 && c >= best) continue;
+        best = c;
+        two.pv = {L, nseg, nseg - 1};
     }
-    return p;
+    if ((Dk <= 64) != (Dv <= 64)) return two;       // two launches in any case
+    const double c1 = chain_cost((nk + nv) * one.p.nseg, one.p.L, bf16) + states(one.p);
+    const double c2 = chain_cost(nk * two.p.nseg, two.p.L, bf16) + states(two.p) + best;
+    return c2 < c1 ? two : one;
 }
 
 constexpr size_t up16(size_t n) { return (n + 15) / 16 * 16; }
@@ -959,7 +1001,6 @@ LaChain chain(const LaArgs& a, const Plan& p) {
     c.H = a.H;
     c.L = p.L;
     c.nseg = p.nseg;
-    c.every = p.L;
     c.bf16 = a.bf16;
     c.g = a.g;
     c.g_head = a.g_head;
@@ -968,22 +1009,23 @@ LaChain chain(const LaArgs& a, const Plan& p) {
     return c;
 }
 
-// Start states of all segments of one or two jobs (their h_in, hz and hk as for the
-// whole chain) into buf.
-hipError_t segment_states(LaChain c, const LaJob* jobs, int n, float* const* buf,
+// Start states of the segments behind the first, of one or two jobs (h_in, hz and hk as
+// for the whole chain), into buf, and the jobs set to start from them.
+hipError_t segment_states(LaChain c, const Plan& p, LaJob* const* jobs, int n, float* const* buf,
                           float* const* decay) {
     Compose m{};
     m.BH = c.B * c.H;
     m.state = c.state;
-    m.nseg = c.nseg;
-    const bool both = n == 2 && (jobs[0].kd <= 64) == (jobs[1].kd <= 64);
+    m.marks = p.marks;
+    const bool both = n == 2 && (jobs[0]->kd <= 64) == (jobs[1]->kd <= 64);
     for (int i = 0; i < n; ++i) {
-        LaJob j = jobs[i];
+        LaJob j = *jobs[i];
         m.buf[i] = buf[i];
         m.decay[i] = decay[i];
         m.h0[i] = j.h_in;
         m.back[i] = j.back;
-        j.h_in = nullptr;
+        jobs[i]->h_seg = buf[i];
+        jobs[i]->h_every = p.L;
         j.h_out = buf[i];
         j.seg_decay = decay[i];
         j.out = nullptr;
@@ -994,8 +1036,8 @@ hipError_t segment_states(LaChain c, const LaJob* jobs, int n, float* const* buf
         const hipError_t e = launch_chain(c);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(compose_kernel, dim3((unsigned)((m.BH * m.state + 255) / 256), n), dim3(256),
-                       0, c.stream, m);
+    hipLaunchKernelGGL(compose_kernel, dim3((unsigned)cdiv(m.BH * m.state, 256), n), dim3(256), 0,
+                       c.stream, m);
     return hipGetLastError();
 }
 
@@ -1007,15 +1049,15 @@ using namespace la;
 // The largest launch of a call, in workgroups of 256.
 int64_t la_fwd_workgroups(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, bool bf16) {
     const Plan p = fwd_plan(B, T, H, Dv, bf16);
-    const int64_t chain = 4 * ((B * H * p.nseg + 7) / 8 * 8 * blocks(Dv));
-    const int64_t states = p.nseg > 1 ? (B * H * Dk * Dv + 255) / 256 : 0;
+    const int64_t chain = 4 * ((B * H * (p.marks + p.nseg) + 7) / 8 * 8 * blocks(Dv));
+    const int64_t states = p.nseg > 1 ? cdiv(B * H * Dk * Dv, 256) : 0;
     return chain > states ? chain : states;
 }
 
 size_t la_fwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, bool bf16) {
     const Plan p = fwd_plan(B, T, H, Dv, bf16);
-    if (p.nseg == 1) return 0;
-    return up16(4 * (size_t)(p.nseg * B * H) * (size_t)(Dk * Dv)) + up16(4 * (size_t)(p.nseg * B * H));
+    const size_t n = 4 * (size_t)(p.marks * B * H);
+    return up16(n * (size_t)(Dk * Dv)) + up16(n);
 }
 
 hipError_t launch_la_fwd(const LaArgs& a) {
@@ -1033,10 +1075,10 @@ hipError_t launch_la_fwd(const LaArgs& a) {
     j.hk = 1;
     if (p.nseg > 1) {
         float* buf = static_cast<float*>(a.workspace);
-        float* decay = buf + up16(4 * (size_t)(p.nseg * a.B * a.H) * (size_t)c.state) / 4;
-        const hipError_t e = segment_states(c, &j, 1, &buf, &decay);
+        float* decay = buf + up16(4 * (size_t)(p.marks * a.B * a.H) * (size_t)c.state) / 4;
+        LaJob* const jobs[1] = {&j};
+        const hipError_t e = segment_states(c, p, jobs, 1, &buf, &decay);
         if (e != hipSuccess) return e;
-        j.h_in = buf;
     }
     j.h_out = a.s_final;
     c.njobs = 1;
@@ -1051,8 +1093,8 @@ struct BwdSpace {
     size_t s, sdec, g, gdec, sk, gk, qd, kd, part, dq, dk, end;
 };
 
-BwdSpace bwd_space(const Plan& p, int64_t every, int64_t B, int64_t T, int64_t H, int64_t Hk,
-                   int64_t Dk, int64_t Dv) {
+BwdSpace bwd_space(const BwdPlan& p, int64_t B, int64_t T, int64_t H, int64_t Hk, int64_t Dk,
+                   int64_t Dv) {
     BwdSpace o{};
     size_t n = 0;
     auto take = [&](size_t bytes) {
@@ -1061,11 +1103,11 @@ BwdSpace bwd_space(const Plan& p, int64_t every, int64_t B, int64_t T, int64_t H
         return at;
     };
     const size_t bh = (size_t)(B * H), state = 4 * (size_t)(Dk * Dv) * bh;
-    const size_t nblk = (size_t)((T + every - 1) / every);
-    o.s = take(p.nseg > 1 ? state * p.nseg : 0);
-    o.sdec = take(p.nseg > 1 ? 4 * bh * p.nseg : 0);
-    o.g = take(p.nseg > 1 ? state * p.nseg : 0);
-    o.gdec = take(p.nseg > 1 ? 4 * bh * p.nseg : 0);
+    const size_t nblk = (size_t)p.nblk, marks = (size_t)p.p.marks;
+    o.s = take(state * marks);
+    o.sdec = take(4 * bh * marks);
+    o.g = take(state * marks);
+    o.gdec = take(4 * bh * marks);
     o.sk = take(state * nblk);
     o.gk = take(state * (nblk - 1));
     const size_t dots = 4 * bh * (size_t)T * (size_t)((Dk + 15) / 16);
@@ -1082,30 +1124,27 @@ BwdSpace bwd_space(const Plan& p, int64_t every, int64_t B, int64_t T, int64_t H
 }  // namespace
 
 int64_t la_bwd_workgroups(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, bool bf16) {
-    int64_t every;
-    const Plan p = bwd_plan(B, T, H, Dk, Dv, bf16, every);
-    const int64_t chain = 4 * ((B * H * p.nseg + 7) / 8 * 8 * (2 * blocks(Dk) + blocks(Dv)));
-    const int64_t states = (B * H * Dk * Dv + 255) / 256;
-    const int64_t sums = B * H * ((T + every - 1) / every);
+    const BwdPlan p = bwd_plan(B, T, H, Dk, Dv, bf16);
+    const int64_t segs = p.p.nseg + p.p.marks + p.pv.nseg;
+    const int64_t chain = 4 * ((B * H * segs + 7) / 8 * 8 * (2 * blocks(Dk) + blocks(Dv)));
+    const int64_t states = cdiv(B * H * Dk * Dv, 256);
+    const int64_t sums = B * H * p.nblk;
     const int64_t most = chain > states ? chain : states;
     return most > sums ? most : sums;
 }
 
 size_t la_bwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Hk, int64_t Dk, int64_t Dv,
                               bool bf16) {
-    int64_t every;
-    const Plan p = bwd_plan(B, T, H, Dk, Dv, bf16, every);
-    return bwd_space(p, every, B, T, H, Hk, Dk, Dv).end;
+    return bwd_space(bwd_plan(B, T, H, Dk, Dv, bf16), B, T, H, Hk, Dk, Dv).end;
 }
 
 hipError_t launch_la_bwd(const LaArgs& a) {
-    int64_t every;
-    const Plan p = bwd_plan(a.B, a.T, a.H, a.Dk, a.Dv, a.bf16, every);
-    const BwdSpace w = bwd_space(p, every, a.B, a.T, a.H, a.Hk, a.Dk, a.Dv);
+    const BwdPlan p = bwd_plan(a.B, a.T, a.H, a.Dk, a.Dv, a.bf16);
+    const BwdSpace w = bwd_space(p, a.B, a.T, a.H, a.Hk, a.Dk, a.Dv);
     char* ws = static_cast<char*>(a.workspace);
     auto f32 = [&](size_t at) { return reinterpret_cast<float*>(ws + at); };
-    LaChain c = chain(a, p);
-    c.every = every;
+    LaChain c = chain(a, p.p);
+    c.every = p.every;
 
     LaJob jq = job(a.dout, a.v, a.k, a.Dv, a.Dk);
     jq.pair = jq.inter = a.scale;
@@ -1126,13 +1165,13 @@ hipError_t launch_la_bwd(const LaArgs& a) {
     jv.hk = 1;
 
     hipError_t e;
-    if (p.nseg > 1) {
-        const LaJob jobs[2] = {jq, jv};
+    if (p.p.nseg > 1) {
+        LaJob* const jobs[2] = {&jq, &jv};
         float* const buf[2] = {f32(w.s), f32(w.g)};
         float* const decay[2] = {f32(w.sdec), f32(w.gdec)};
-        if ((e = segment_states(c, jobs, 2, buf, decay)) != hipSuccess) return e;
-        jq.h_in = f32(w.s);
-        jk.h_in = jv.h_in = f32(w.g);
+        if ((e = segment_states(c, p.p, jobs, 2, buf, decay)) != hipSuccess) return e;
+        jk.h_seg = jv.h_seg;
+        jk.h_every = jv.h_every;
     }
     const bool own = a.H == a.Hk;
     jq.out = own ? a.dq : f32(w.dq);
@@ -1153,23 +1192,22 @@ hipError_t launch_la_bwd(const LaArgs& a) {
     if (a.dg) {
         jq.keep = f32(w.sk);
         jq.keep_end = a.ds_final != nullptr;
-        jk.keep = f32(w.gk);
         jq.r = a.q;
         jq.dots = f32(w.qd);
         jk.r = a.k;
         jk.dots = f32(w.kd);
     }
-    if ((a.Dk <= 64) == (a.Dv <= 64)) {
-        c.njobs = 3;
-        c.job[0] = jq;
-        c.job[1] = jk;
-        c.job[2] = jv;
-        if ((e = launch_chain(c)) != hipSuccess) return e;
-    } else {
-        c.njobs = 2;
-        c.job[0] = jq;
-        c.job[1] = jk;
-        if ((e = launch_chain(c)) != hipSuccess) return e;
+    if (a.dg || p.apart) jk.keep = f32(w.gk);
+    c.njobs = p.apart ? 2 : 3;
+    c.job[0] = jq;
+    c.job[1] = jk;
+    c.job[2] = jv;
+    if ((e = launch_chain(c)) != hipSuccess) return e;
+    if (p.apart) {
+        jv.h_seg = jk.keep;
+        jv.h_every = p.every;
+        c.L = p.pv.L;
+        c.nseg = p.pv.nseg;
         c.njobs = 1;
         c.job[0] = jv;
         if ((e = launch_chain(c)) != hipSuccess) return e;
@@ -1192,8 +1230,8 @@ hipError_t launch_la_bwd(const LaArgs& a) {
         d.B = a.B;
         d.T = a.T;
         d.H = a.H;
-        d.every = every;
-        d.nblk = (a.T + every - 1) / every;
+        d.every = p.every;
+        d.nblk = p.nblk;
         d.state = c.state;
         d.nq = (int)((a.Dk + 15) / 16);
         d.q = f32(w.qd);

@@ -29,9 +29,12 @@ struct LaJob {
     void* out;
     int64_t ob, ot, oh;
     bool out_bf16;
-    // states: start per (segment, sequence, head) or NULL; end: of the last segment
-    // (out NULL: of every segment, with its decay in seg_decay)
-    const float* h_in;
+    // states: start [B, H, ..] of the chain (NULL: zeros), and of its segments behind
+    // the first [mark / h_every - 1, B, H, ..], mark the token between them and the
+    // segment before; end [B, H, ..] (out NULL: the own states of all segments but
+    // the last [.., B, H, ..], as from zeros, with their decays in seg_decay)
+    const float *h_in, *h_seg;
+    int64_t h_every;
     float* h_out;
     float* seg_decay;
     int64_t hz, hk;

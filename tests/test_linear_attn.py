@@ -135,6 +135,22 @@ def test_kept_states_of_one_segment(gdr_lib):
     check_bwd(gdr_lib, a, do, ds)
 
 
+@pytest.mark.parametrize("B,T,H,Hk,Dk,Dv", [(2, 2300, 1, 1, 128, 64), (130, 2100, 1, 1, 8, 72),
+                                            (43, 3200, 3, 1, 8, 16)])
+@pytest.mark.parametrize("decay", ["token", "none"])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_gradients_from_kept_states(gdr_lib, B, T, H, Hk, Dk, Dv, decay, dt):
+    """dv in a launch of its own, in segments that start from the states that dk's
+    chain has left, with and without a decay's gradient."""
+    a, do, ds = make(8, B, T, H, Hk, Dk, Dv, dt, decay, state=B < 100)
+    want = check_bwd(gdr_lib, a, do, ds)
+    got = gdr_lib.gdr_linear_attn_bwd(*a, do, ds, scale=0.3, want_ddecay=False, want_ds0=False)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got[:3], want[:3]))
+    if dt == "bf16" and decay == "none":        # products in fewer terms
+        check_bwd(gdr_lib, a, do, ds, grad=dt)
+
+
 @pytest.mark.parametrize("reset", [0.02, 0.3, 1.0])
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_resets(gdr_lib, reset, dt):
