@@ -49,9 +49,9 @@ template <class P, int KD> struct Shared {
     float gap[2][P::C / 16][P::C / 16];
 };
 
-// What the states alone need of it.
-template <class P, int KD> struct StatesShared {
-    typename P::T y[2][P::C * KD], z[2][P::C * ZB];
+// What the states alone need of it, for NZ blocks of z's channels.
+template <class P, int KD, int NZ> struct StatesShared {
+    typename P::T y[2][P::C * KD], z[2][NZ * P::C * ZB];
     float leave[2][P::C], total[2];
 };
 
@@ -116,14 +116,14 @@ template <class P, int KD> struct PTileWork {
     }
 };
 
-// Team L: tiles and factors of the chunks, from memory to LDS.
-template <class P, int KD, bool OUT> struct Bringer {
+// Team L: tiles of the chunks, from memory to LDS; of z, NZ blocks of channels.
+template <class P, int KD, bool OUT, int NZ> struct Bringer {
     typedef typename P::T T;
     // what is on its way for one chunk
     struct Coming {
         Stage<P, KD, ROWS> x;
         Stage<P, KD, BOTH> y;
-        Stage<P, ZB, BOTH> z;
+        Stage<P, ZB, BOTH> z[NZ];
     };
     const char *xb, *yb, *zb;
     int64_t xt, yt, zt;
@@ -134,27 +134,31 @@ template <class P, int KD, bool OUT> struct Bringer {
         xb = OUT ? static_cast<const char*>(head_base(jb.x, at.b, at.h, sizeof(T))) : nullptr;
         yb = static_cast<const char*>(head_base(jb.y, at.b, at.h, sizeof(T)));
         zb = static_cast<const char*>(head_base(jb.z, at.b, at.h, sizeof(T))) +
-             at.zb * ZB * sizeof(T);
+             at.zb * NZ * ZB * sizeof(T);
         xt = jb.x.st;
         yt = jb.y.st;
         zt = jb.z.st;
         if constexpr (OUT) c.x.init(tid, jb.kd, xt, back);
         c.y.init(tid, jb.kd, yt, back);
-        c.z.init(tid, jb.zd - at.zb * ZB, zt, back);
+#pragma unroll
+        for (int i = 0; i < NZ; ++i) c.z[i].init(tid, jb.zd - (at.zb * NZ + i) * ZB, zt, back);
     }
     __device__ __forceinline__ void ask_x(int64_t t0, int len, Coming& c) {
         if constexpr (OUT) c.x.load(xb + t0 * xt * (int)sizeof(T), xt, len, back);
     }
     __device__ __forceinline__ void ask_yz(int64_t t0, int len, Coming& c) {
         c.y.load(yb + t0 * yt * (int)sizeof(T), yt, len, back);
-        c.z.load(zb + t0 * zt * (int)sizeof(T), zt, len, back);
+#pragma unroll
+        for (int i = 0; i < NZ; ++i)
+            c.z[i].load(zb + (t0 * zt + i * ZB) * (int)sizeof(T), zt, len, back);
     }
     template <class S> __device__ __forceinline__ void put_yz(S& s, int64_t n, int len, Coming& c) {
         const int buf = (int)(n & 1);
         c.y.put(s.y[buf], len);
-        c.z.put(s.z[buf], len);
+#pragma unroll
+        for (int i = 0; i < NZ; ++i) c.z[i].put(s.z[buf] + i * P::C * ZB, len);
         if constexpr (OUT) {
-            if (c.z.bad()) s.bad[buf] = (int)(n + 1);
+            if (c.z[0].bad()) s.bad[buf] = (int)(n + 1);
         }
     }
 };
@@ -226,12 +230,13 @@ template <class P, int KD> struct State {
     typename TY::Cols cols;
     typename TZ::Cols zcol;
 
-    __device__ __forceinline__ State(const LaJob& jb, int zb, int tid) {
+    // of z's channels from `first` on
+    __device__ __forceinline__ State(const LaJob& jb, int first, int tid) {
         const int lane = tid & 63;
         w = __builtin_amdgcn_readfirstlane(tid >> 6);
         g = lane >> 4;
         m = lane & 15;
-        zc = zb * ZB + 16 * w;
+        zc = first + 16 * w;
         zd = jb.zd;
         kd = jb.kd;
         hz = jb.hz;
@@ -253,6 +258,12 @@ template <class P, int KD> struct State {
     }
     __device__ __forceinline__ void load(const float* p) {
         p += first();
+        if (hk == 1) {
+#pragma unroll
+            for (int u = 0; u < NU; ++u)
+                if (has(u)) H[u] = *reinterpret_cast<const f32x4_e4*>(p + 16 * u);
+            return;
+        }
 #pragma unroll
         for (int u = 0; u < NU; ++u)
             if (has(u)) {
@@ -262,6 +273,12 @@ template <class P, int KD> struct State {
     }
     __device__ __forceinline__ void store(float* p, float f) const {
         p += first();
+        if (hk == 1) {
+#pragma unroll
+            for (int u = 0; u < NU; ++u)
+                if (has(u)) *reinterpret_cast<f32x4_e4*>(p + 16 * u) = H[u] * f;
+            return;
+        }
 #pragma unroll
         for (int u = 0; u < NU; ++u)
             if (has(u)) {
@@ -279,7 +296,7 @@ template <class P, int KD> struct State {
         tot = s.total[buf];
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-            t.z[j] = zcol.get(s.z[buf], j, w);
+            t.z[j] = zcol.get(s.z[buf] + w / 4 * (P::C * ZB), j, w % 4);
             t.l[j][0] = *reinterpret_cast<const f32x4*>(&s.leave[buf][32 * j + 8 * g]);
             t.l[j][1] = *reinterpret_cast<const f32x4*>(&s.leave[buf][32 * j + 8 * g + 4]);
         }
@@ -376,7 +393,7 @@ __global__ __launch_bounds__(1024) void chain_kernel(LaChain a) {
     Shared<P, KD>& s = *reinterpret_cast<Shared<P, KD>*>(smem);
 
     Place at;
-    if (!place(a, blockIdx.x, at)) return;
+    if (!place(a, blockIdx.x, ZB, at)) return;
     const LaJob& jb = a.job[at.job];
     const Chunks ch(a, at, jb.back, C);
     const int64_t nc = ch.nc, bh = at.b * a.H + at.h;
@@ -389,7 +406,7 @@ __global__ __launch_bounds__(1024) void chain_kernel(LaChain a) {
 
     if (wv >= 12) {
         // ---- team L ----
-        typedef Bringer<P, KD, true> L;
+        typedef Bringer<P, KD, true, 1> L;
         typename L::Coming even, odd;
         L l(at, jb, threadIdx.x - 768, even);
         odd = even;
@@ -426,12 +443,12 @@ __global__ __launch_bounds__(1024) void chain_kernel(LaChain a) {
     }
     if (wv >= 8) {
         // ---- team U ----
-        State<P, KD> st(jb, at.zb, threadIdx.x - 512);
+        State<P, KD> st(jb, at.zb * ZB, threadIdx.x - 512);
         if (at.seg == (back ? a.nseg - 1 : 0)) {
             if (jb.h_in) st.load(jb.h_in + bh * a.state);
         } else {
-            const int64_t mark = back ? ch.tb : ch.ta;
-            st.load(jb.h_seg + ((mark / jb.h_every - 1) * a.B * a.H + bh) * a.state);
+            const int64_t slot = (at.seg + (back ? 1 : 0)) * jb.h_step - 1;
+            st.load(jb.h_seg + (slot * a.B * a.H + bh) * a.state);
         }
         float* const keep = GRAD ? jb.keep : nullptr;
         lds_barrier();
@@ -646,28 +663,30 @@ __global__ __launch_bounds__(1024) void chain_kernel(LaChain a) {
     }
 }
 
-// The states at the segments' ends alone, and the segments' decays.
-template <class P, int KD>
-__global__ __launch_bounds__(512) void states_kernel(LaChain a) {
-    __shared__ StatesShared<P, KD> s;
+// The states at the segments' ends alone, and the segments' decays.  A workgroup has up
+// to 128 channels of z, so that y is read once: bound by what its compute unit has of
+// loads in flight, it took 92 us instead of XX with 64 (B1 T32768 H16, heads of 128).
+template <class P, int KD, int NZ>
+__global__ __launch_bounds__(256 + 256 * NZ) void states_kernel(LaChain a) {
+    __shared__ StatesShared<P, KD, NZ> s;
     Place at;
-    if (!place(a, blockIdx.x, at)) return;
+    if (!place(a, blockIdx.x, NZ * ZB, at)) return;
     const LaJob& jb = a.job[at.job];
     if (at.seg == (jb.back ? 0 : a.nseg - 1)) return;       // no segment behind it
     const Chunks ch(a, at, jb.back, P::C);
     const int64_t nc = ch.nc;
     const int64_t to = (at.seg - (jb.back ? 1 : 0)) * a.B * a.H + at.b * a.H + at.h;
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (wv >= 4) {
-        typedef Bringer<P, KD, false> L;
+    if (wv >= 4 * NZ) {
+        typedef Bringer<P, KD, false, NZ> L;
         typename L::Coming even, odd;
-        L l(at, jb, threadIdx.x - 256, even);
+        L l(at, jb, threadIdx.x - 256 * NZ, even);
         odd = even;
         Decays<P, false> dec(a, at, jb, threadIdx.x & 63);
         int64_t t0;
         int len;
         ch.get(0, t0, len);
-        if (wv == 7) dec.ask(t0, len);
+        if (wv == 4 * NZ + 3) dec.ask(t0, len);
         l.ask_yz(t0, len, even);
         if (nc > 1) {
             ch.get(1, t0, len);
@@ -676,7 +695,7 @@ __global__ __launch_bounds__(512) void states_kernel(LaChain a) {
         auto turn = [&](int64_t n, typename L::Coming& c) {
             int64_t t0;
             int len;
-            if (wv == 7) {
+            if (wv == 4 * NZ + 3) {
                 dec.scan(s, n);
                 if (n + 1 < nc) {
                     ch.get(n + 1, t0, len);
@@ -696,11 +715,11 @@ __global__ __launch_bounds__(512) void states_kernel(LaChain a) {
             if (n + 1 < nc) turn(n + 1, odd);
         }
         lds_barrier();              // U's last chunk
-        if (at.zb == 0 && threadIdx.x == 512 - 64)
+        if (at.zb == 0 && threadIdx.x == 256 * NZ + 192)
             jb.seg_decay[to] = __builtin_amdgcn_exp2f((float)dec.run);
         return;
     }
-    State<P, KD> st(jb, at.zb, threadIdx.x);
+    State<P, KD> st(jb, at.zb * NZ * ZB, threadIdx.x);
     lds_barrier();
     for (int64_t n = 0; n < nc; ++n) {
         typename State<P, KD>::Taken t;
@@ -722,6 +741,7 @@ struct Compose {
 };
 
 __global__ __launch_bounds__(256) void compose_kernel(Compose a) {
+    constexpr int N = 16;
     const int k = blockIdx.y;
     const int64_t n = a.BH * a.state, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= n) return;
@@ -730,10 +750,10 @@ __global__ __launch_bounds__(256) void compose_kernel(Compose a) {
     float h = a.h0[k] ? a.h0[k][i] : 0.f;
     const bool back = a.back[k];
     // batches of loads: a store would hold back the next segment's
-    for (int64_t c = 0; c < a.marks; c += 8) {
-        float own[8], d[8];
+    for (int64_t c = 0; c < a.marks; c += N) {
+        float own[N], d[N];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < N; ++e) {
             const int64_t p = back ? a.marks - 1 - c - e : c + e;
             own[e] = d[e] = 0.f;
             if (c + e < a.marks) {
@@ -742,7 +762,7 @@ __global__ __launch_bounds__(256) void compose_kernel(Compose a) {
             }
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < N; ++e) {
             const int64_t p = back ? a.marks - 1 - c - e : c + e;
             h = d[e] * h + own[e];
             if (c + e < a.marks) buf[p * n] = h;
@@ -874,9 +894,11 @@ __global__ __launch_bounds__(64) void head_sum_kernel(const double* part, float*
     if (threadIdx.x == 0) dg[blockIdx.x] = (float)s;
 }
 
-template <class Fn> hipError_t launch_one(Fn* fn, const LaChain& a, int threads, size_t lds) {
+// Workgroups of `width` channels of z.
+template <class Fn>
+hipError_t launch_one(Fn* fn, const LaChain& a, int width, int threads, size_t lds) {
     int64_t per = 0;
-    for (int j = 0; j < a.njobs; ++j) per += (a.job[j].zd + ZB - 1) / ZB;
+    for (int j = 0; j < a.njobs; ++j) per += (a.job[j].zd + width - 1) / width;
     const int64_t grid = (a.B * a.H * a.nseg + 7) / 8 * 8 * per;
     if (lds) {
         const hipError_t e = hipFuncSetAttribute(
@@ -890,11 +912,10 @@ template <class Fn> hipError_t launch_one(Fn* fn, const LaChain& a, int threads,
 template <class P, int KD> hipError_t launch_kd(const LaChain& a) {
     constexpr size_t lds = sizeof(Shared<P, KD>);
     static_assert(lds <= 160 * 1024, "LDS");
-    if (!a.job[0].out) return launch_one(states_kernel<P, KD>, a, 512, 0);
     for (int j = 0; j < a.njobs; ++j)
         if (a.job[j].keep || a.job[j].dots)
-            return launch_one(chain_kernel<P, KD, true>, a, 1024, lds);
-    return launch_one(chain_kernel<P, KD, false>, a, 1024, lds);
+            return launch_one(chain_kernel<P, KD, true>, a, ZB, 1024, lds);
+    return launch_one(chain_kernel<P, KD, false>, a, ZB, 1024, lds);
 }
 
 template <class P> hipError_t launch_chain_p(const LaChain& a) {
@@ -909,9 +930,23 @@ hipError_t launch_chain(const LaChain& a) {
     return fine ? launch_chain_p<Bf16<3>>(a) : launch_chain_p<Bf16<2>>(a);
 }
 
-// Segments of L tokens, and the marks between them.
+// The own end states of all segments but the last, of jobs of one contraction width and
+// one width of z.
+template <class P, int KD> hipError_t launch_states_kd(const LaChain& a) {
+    if (a.job[0].zd <= ZB) return launch_one(states_kernel<P, KD, 1>, a, ZB, 512, 0);
+    return launch_one(states_kernel<P, KD, 2>, a, 2 * ZB, 768, 0);
+}
+
+hipError_t launch_states(const LaChain& a) {
+    if (!a.bf16)
+        return a.job[0].kd <= 64 ? launch_states_kd<F32, 64>(a) : launch_states_kd<F32, 128>(a);
+    return a.job[0].kd <= 64 ? launch_states_kd<Bf16<3>, 64>(a)
+                             : launch_states_kd<Bf16<3>, 128>(a);
+}
+
+// Segments of L tokens; their start states at the marks between segments of Ls.
 struct Plan {
-    int64_t L, nseg, marks;
+    int64_t L, nseg, Ls, marks;
 };
 
 constexpr int kUnits = 256;         // compute units
@@ -932,7 +967,9 @@ Plan plan(int64_t T, int64_t units, bool bf16, int64_t grain) {
     int64_t L = cdiv(cdiv(T, nseg), C) * C;
     if (L > grain) L = cdiv(L, grain) * grain;
     nseg = cdiv(T, L);
-    return {L, nseg, nseg - 1};
+    // two blocks of channels to a workgroup for the states alone: half segments
+    const int64_t Ls = L % (2 * C) == 0 ? L / 2 : L;
+    return {L, nseg, Ls, nseg > 1 ? cdiv(T, Ls) - 1 : 0};
 }
 
 Plan fwd_plan(int64_t B, int64_t T, int64_t H, int64_t Dv, bool bf16) {
@@ -956,7 +993,7 @@ BwdPlan bwd_plan(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, bool b
     const int64_t BH = B * H, nk = BH * 2 * blocks(Dk), nv = BH * blocks(Dv);
     // a pass over the states alone takes half the time
     auto states = [&](const Plan& p) {
-        return p.nseg > 1 ? 0.5 * chain_cost(p.marks * (nk / 2 + nv), p.L, bf16) + 4.0 : 0.0;
+        return p.nseg > 1 ? 0.5 * chain_cost(p.marks * (nk / 2 + nv), p.Ls, bf16) + 4.0 : 0.0;
     };
     auto every = [](const Plan& p) { return p.L > 1024 ? (int64_t)1024 : p.L; };
     BwdPlan one{}, two{};
@@ -973,7 +1010,7 @@ BwdPlan bwd_plan(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, bool b
         const double c = chain_cost(nv * nseg, L, bf16);
         if (n > 1 && c >= best) continue;
         best = c;
-        two.pv = {L, nseg, nseg - 1};
+        two.pv = {L, nseg, L, 0};
     }
     if ((Dk <= 64) != (Dv <= 64)) return two;       // two launches in any case
     const double c1 = chain_cost((nk + nv) * one.p.nseg, one.p.L, bf16) + states(one.p);
@@ -1017,6 +1054,8 @@ hipError_t segment_states(LaChain c, const Plan& p, LaJob* const* jobs, int n, f
     m.BH = c.B * c.H;
     m.state = c.state;
     m.marks = p.marks;
+    c.L = p.Ls;
+    c.nseg = p.marks + 1;
     const bool both = n == 2 && (jobs[0]->kd <= 64) == (jobs[1]->kd <= 64);
     for (int i = 0; i < n; ++i) {
         LaJob j = *jobs[i];
@@ -1025,15 +1064,13 @@ hipError_t segment_states(LaChain c, const Plan& p, LaJob* const* jobs, int n, f
         m.h0[i] = j.h_in;
         m.back[i] = j.back;
         jobs[i]->h_seg = buf[i];
-        jobs[i]->h_every = p.L;
+        jobs[i]->h_step = p.L / p.Ls;
         j.h_out = buf[i];
         j.seg_decay = decay[i];
-        j.out = nullptr;
-        j.keep = j.dots = nullptr;
         c.job[both ? i : 0] = j;
         c.njobs = both ? 2 : 1;
         if (both && i == 0) continue;
-        const hipError_t e = launch_chain(c);
+        const hipError_t e = launch_states(c);
         if (e != hipSuccess) return e;
     }
     hipLaunchKernelGGL(compose_kernel, dim3((unsigned)cdiv(m.BH * m.state, 256), n), dim3(256), 0,
@@ -1171,7 +1208,7 @@ hipError_t launch_la_bwd(const LaArgs& a) {
         float* const decay[2] = {f32(w.sdec), f32(w.gdec)};
         if ((e = segment_states(c, p.p, jobs, 2, buf, decay)) != hipSuccess) return e;
         jk.h_seg = jv.h_seg;
-        jk.h_every = jv.h_every;
+        jk.h_step = jv.h_step;
     }
     const bool own = a.H == a.Hk;
     jq.out = own ? a.dq : f32(w.dq);
@@ -1205,7 +1242,7 @@ hipError_t launch_la_bwd(const LaArgs& a) {
     if ((e = launch_chain(c)) != hipSuccess) return e;
     if (p.apart) {
         jv.h_seg = jk.keep;
-        jv.h_every = p.every;
+        jv.h_step = p.pv.L / p.every;
         c.L = p.pv.L;
         c.nseg = p.pv.nseg;
         c.njobs = 1;

@@ -310,28 +310,32 @@ struct Place {
     int job, zb;
 };
 
-__device__ __forceinline__ bool place(const LaChain& a, int64_t id, Place& o) {
-    int nz[3], per = 0;
+// Workgroup id, where each has `width` channels of z.
+__device__ __forceinline__ bool place(const LaChain& a, uint32_t id, int width, Place& o) {
+    uint32_t nz[3], per = 0;
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
-        nz[j] = j < a.njobs ? (a.job[j].zd + ZB - 1) / ZB : 0;
+        nz[j] = j < a.njobs ? (a.job[j].zd + width - 1) / width : 0;
         per += nz[j];
     }
-    const int64_t grp = id / (8 * per) * 8 + id % 8;
-    int k = (int)(id / 8 % per);
-    if (grp >= a.B * a.H * a.nseg) return false;
+    // a grid, and so every count here, is below 2^24
+    const uint32_t H = (uint32_t)a.H, B = (uint32_t)a.B;
+    const uint32_t row = id / 8, grp = row / per * 8 + id % 8, bh = grp / H;
+    uint32_t k = row % per;
+    o.seg = bh / B;
+    if (o.seg >= a.nseg) return false;
     o.job = 0;
     while (k >= nz[o.job]) k -= nz[o.job++];
     o.zb = k;
-    o.h = grp % a.H;
-    o.b = grp / a.H % a.B;
-    o.seg = grp / a.H / a.B;
+    o.h = grp % H;
+    o.b = bh % B;
     return true;
 }
 
 __device__ __forceinline__ const void* head_base(const LaTensor& t, int64_t b, int64_t h,
                                                  size_t elem) {
-    return static_cast<const char*>(t.p) + (b * t.sb + h / t.share * t.sh) * elem;
+    const int64_t at = (uint32_t)h / (uint32_t)t.share;
+    return static_cast<const char*>(t.p) + (b * t.sb + at * t.sh) * elem;
 }
 
 // Log decay that the state goes through before token t is added, as it lies in

@@ -25,16 +25,16 @@ struct LaJob {
     int kd, zd;
     bool back;
     float pair, inter, upd;
-    // out [B, T, H, zd] or [B, T, H / share, zd] (NULL: the states only)
+    // out [B, T, H, zd] or [B, T, H / share, zd]
     void* out;
     int64_t ob, ot, oh;
     bool out_bf16;
     // states: start [B, H, ..] of the chain (NULL: zeros), and of its segments behind
-    // the first [mark / h_every - 1, B, H, ..], mark the token between them and the
-    // segment before; end [B, H, ..] (out NULL: the own states of all segments but
-    // the last [.., B, H, ..], as from zeros, with their decays in seg_decay)
+    // the first [slot, B, H, ..], h_step slots a segment, the last of each the state
+    // between it and the next (backwards: the one before); end [B, H, ..] (for the states alone: the own ones of all
+    // segments but the last [.., B, H, ..], as from zeros, their decays in seg_decay)
     const float *h_in, *h_seg;
-    int64_t h_every;
+    int64_t h_step;
     float* h_out;
     float* seg_decay;
     int64_t hz, hk;
