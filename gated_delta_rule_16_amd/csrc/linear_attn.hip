@@ -55,33 +55,37 @@ template <class P, int KD, int NZ> struct StatesShared {
     float leave[2][P::C], total[2];
 };
 
-// Operands of tile (i, j) of P^T, and the tile from them (row 4 g + r: token j, column
-// m: token i).  They are read a tile ahead of their use.
+// Tile (i, j) of P^T (row 4 g + r: token j, column m: token i) and its operands, which
+// are read a tile ahead of their use.
 template <class P, int KD> struct PTileWork {
     static constexpr int NK = KD / 32;
     typename P::Frag xf[NK], yf[NK];
-    __device__ __forceinline__ void read(const typename P::T* x, const typename P::T* y, int i,
-                                         int j, const typename Tile<P, KD, ROWS>::Rows& xrow,
-                                         const typename Tile<P, KD, BOTH>::Rows& yrow) {
+    typename Tile<P, KD, ROWS>::Rows x;
+    typename Tile<P, KD, BOTH>::Rows y;
+    __device__ __forceinline__ void init(int lane) {
+        x.init(lane);
+        y.init(lane);
+    }
+    __device__ __forceinline__ void read(const Shared<P, KD>& s, int pb, int i, int j) {
+        x.of(s.x[pb] + 16 * i * KD);
+        y.of(s.y[pb] + 16 * j * KD);
         if constexpr (P::is_bf16) {         // fp32: too many registers
 #pragma unroll
             for (int k = 0; k < NK; ++k) {
-                xf[k] = xrow.get(x, i, k);
-                yf[k] = yrow.get(y, j, k);
+                xf[k] = x.get(0, k);
+                yf[k] = y.get(0, k);
             }
         }
     }
     __device__ __forceinline__ void write(Shared<P, KD>& s, int pb, int i, int j, int lane,
-                                          float scale,
-                                          const typename Tile<P, KD, ROWS>::Rows& xrow,
-                                          const typename Tile<P, KD, BOTH>::Rows& yrow) {
+                                          float scale) {
         const int g = lane >> 4, m = lane & 15;
         f32x4 c = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < NK; ++k) {
             if constexpr (!P::is_bf16) {
-                xf[k] = xrow.get(s.x[pb], i, k);
-                yf[k] = yrow.get(s.y[pb], j, k);
+                xf[k] = x.get(0, k);
+                yf[k] = y.get(0, k);
             }
             c = P::mma(yf[k], xf[k], c);
         }
@@ -229,6 +233,7 @@ template <class P, int KD> struct State {
     int64_t hz, hk;
     typename TY::Cols cols;
     typename TZ::Cols zcol;
+    uint32_t ho;                    // the wave's part of the terms in LDS
 
     // of z's channels from `first` on
     __device__ __forceinline__ State(const LaJob& jb, int first, int tid) {
@@ -242,7 +247,7 @@ template <class P, int KD> struct State {
         hz = jb.hz;
         hk = jb.hk;
         cols.init(lane);
-        zcol.init(lane);
+        zcol.init(lane, w % 4);
 #pragma unroll
         for (int u = 0; u < NU; ++u) H[u] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
@@ -294,9 +299,10 @@ template <class P, int KD> struct State {
     };
     template <class S> __device__ __forceinline__ void read(const S& s, int buf, Taken& t) {
         tot = s.total[buf];
+        zcol.of(s.z[buf] + w / 4 * (P::C * ZB));
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-            t.z[j] = zcol.get(s.z[buf] + w / 4 * (P::C * ZB), j, w % 4);
+            t.z[j] = zcol.get(j, 0);
             t.l[j][0] = *reinterpret_cast<const f32x4*>(&s.leave[buf][32 * j + 8 * g]);
             t.l[j][1] = *reinterpret_cast<const f32x4*>(&s.leave[buf][32 * j + 8 * g + 4]);
         }
@@ -312,7 +318,7 @@ template <class P, int KD> struct State {
     }
     // through that chunk
     template <class S> __device__ __forceinline__ void move(const S& s, int buf) {
-        cols.fresh();
+        cols.of(s.y[buf]);
 #pragma unroll
         for (int u = 0; u < NU; ++u) H[u] *= tot;
         // four tiles (fp32: two) at a time, the next ones' operands on their way: more
@@ -323,7 +329,7 @@ template <class P, int KD> struct State {
 #pragma unroll
             for (int e = 0; e < W; ++e) {
                 const int u = i % (NU / W) * W + e;
-                yf[i & 1][e] = cols.get(s.y[buf], i / (NU / W), u);
+                yf[i & 1][e] = cols.get(i / (NU / W), u);
             }
         };
         fetch(0);
@@ -340,23 +346,25 @@ template <class P, int KD> struct State {
                 }
         }
     }
-    // its terms to LDS, rows of z's channels
-    __device__ __forceinline__ void show(Shared<P, KD>& s) const {
-        typedef Tile<P, KD, ROWS> TH;
-        int o = TH::at(m, 4 * g);
-        asm volatile("" : "+v"(o));         // as in first()
+    // its terms to LDS, rows of z's channels: where, and all of it
+    __device__ __forceinline__ void shows(const Shared<P, KD>& s) {
+        ho = lds_at(s.h[0]) +
+             (Tile<P, KD, ROWS>::at(m, 4 * g) + 16 * w * KD) * (uint32_t)sizeof(typename P::T);
+    }
+    __device__ __forceinline__ void show() {
+        asm volatile("" : "+v"(ho));        // as in first()
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
-            const int to = (o ^ (16 * u)) + 16 * w * KD;
+            const uint32_t to = ho ^ (16 * u * (uint32_t)sizeof(typename P::T));
             if constexpr (P::is_bf16) {
                 uint32_t w0[P::NO], w1[P::NO];
                 P::template split_pair<P::NO>(H[u][0], H[u][1], w0);
                 P::template split_pair<P::NO>(H[u][2], H[u][3], w1);
 #pragma unroll
                 for (int q = 0; q < P::NO; ++q)
-                    *reinterpret_cast<uint2*>(s.h[q] + to) = uint2{w0[q], w1[q]};
+                    lds_set(to, q * ZB * KD * 2, u32x2{w0[q], w1[q]});
             } else {
-                *reinterpret_cast<f32x4*>(s.h[0] + to) = H[u];
+                lds_set(to, 0, H[u]);
             }
         }
     }
@@ -385,11 +393,10 @@ template <class P, int KD, bool GRAD>
 __global__ __launch_bounds__(1024) void chain_kernel(LaChain a) {
     constexpr int C = P::C, NK = KD / 32, NI = C / 16, NT = NI / 2;
     typedef Tile<P, KD, ROWS> TX;
-    typedef Tile<P, KD, BOTH> TY;
     typedef Tile<P, ZB, BOTH> TZ;
     typedef PTile<P> TP;
     typedef typename P::T T;
-    extern __shared__ __attribute__((aligned(16))) char smem[];
+    extern __shared__ __attribute__((aligned(512))) char smem[];
     Shared<P, KD>& s = *reinterpret_cast<Shared<P, KD>*>(smem);
 
     Place at;
@@ -444,6 +451,7 @@ __global__ __launch_bounds__(1024) void chain_kernel(LaChain a) {
     if (wv >= 8) {
         // ---- team U ----
         State<P, KD> st(jb, at.zb * ZB, threadIdx.x - 512);
+        st.shows(s);
         if (at.seg == (back ? a.nseg - 1 : 0)) {
             if (jb.h_in) st.load(jb.h_in + bh * a.state);
         } else {
@@ -458,7 +466,7 @@ __global__ __launch_bounds__(1024) void chain_kernel(LaChain a) {
             if (n < nc) {
                 typename State<P, KD>::Taken t;
                 st.read(s, (int)(n & 1), t);
-                st.show(s);
+                st.show();
                 st.take(t);
             }
             if (GRAD && keep && n > 0) {
@@ -487,14 +495,16 @@ __global__ __launch_bounds__(1024) void chain_kernel(LaChain a) {
     const int lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
     const int zg = wv & 3, half = wv >> 2;
     auto tile = [&](int t) { return half + 2 * t; };
-    typename TX::Rows xrow;
-    typename TY::Rows yrow;
+    typename TX::Rows xrow, hrow;
     typename TZ::Cols zcol;
     typename TP::Rows prow;
+    PTileWork<P, KD> pw;
     xrow.init(lane);
-    yrow.init(lane);
-    zcol.init(lane);
-    prow.init(lane);
+    hrow.init(lane);
+    hrow.of(s.h[0] + 16 * zg * KD);
+    zcol.init(lane, zg);
+    prow.init(lane, s.p[0] + TP::tile(half, 0));
+    pw.init(lane);
     const int zd = jb.zd, zc = at.zb * ZB + 16 * zg;
     const bool mine = zc + 4 * g < zd;                  // whether the lane has out channels
     const bool out16 = jb.out_bf16;
@@ -534,8 +544,6 @@ __global__ __launch_bounds__(1024) void chain_kernel(LaChain a) {
         int64_t t0 = 0;
         int len = 0;
         Row<4, P::is_bf16, false> rr[GRAD ? NT : 1];
-        xrow.fresh();
-        yrow.fresh();
         if (n > 0) {
             const int buf = (int)((n - 1) & 1);
             ch.get(n - 1, t0, len);
@@ -552,11 +560,13 @@ __global__ __launch_bounds__(1024) void chain_kernel(LaChain a) {
             }
             // out^T (row 4 g + r: channel, column m: token) from the start state
             typename P::Frag xf[2][NT], hf[2][P::NO];
+            xrow.of(s.x[buf] + 16 * half * KD);
+            hrow.fresh();
             auto fetch = [&](int k) {
 #pragma unroll
-                for (int t = 0; t < NT; ++t) xf[k & 1][t] = xrow.get(s.x[buf], tile(t), k);
+                for (int t = 0; t < NT; ++t) xf[k & 1][t] = xrow.get(2 * t, k);
 #pragma unroll
-                for (int q = 0; q < P::NO; ++q) hf[k & 1][q] = xrow.get(s.h[q], zg, k);
+                for (int q = 0; q < P::NO; ++q) hf[k & 1][q] = hrow.get(ZB / 16 * q, k);
             };
 #pragma unroll
             for (int t = 0; t < NT; ++t) O[t] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -572,14 +582,15 @@ __global__ __launch_bounds__(1024) void chain_kernel(LaChain a) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) O[t] *= s.enter[buf][16 * tile(t) + m];
             if (__builtin_expect(s.bad[buf] != (int)n, 1)) {
+                zcol.of(s.z[buf]);
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
-                    const typename P::Frag zf = zcol.get(s.z[buf], j, zg);
+                    const typename P::Frag zf = zcol.get(j, 0);
 #pragma unroll
                     for (int q = P::NO - 1; q >= 0; --q)
 #pragma unroll
                         for (int t = j; t < NT; ++t)
-                            O[t] = P::mma(zf, prow.get(s.p[q], tile(t), j), O[t]);
+                            O[t] = P::mma(zf, prow.get(q * TP::SIZE, 2 * t, j), O[t]);
                 }
             } else {
                 // a value of z that is no number must not meet the zeros of the tokens
@@ -618,9 +629,8 @@ __global__ __launch_bounds__(1024) void chain_kernel(LaChain a) {
                 dec.ask(t2, len2);
             }
         }
-        PTileWork<P, KD> pw;
         const int nb = (int)(n & 1);
-        if (n < nc && np > 0) pw.read(s.x[nb], s.y[nb], pi, pj, xrow, yrow);
+        if (n < nc && np > 0) pw.read(s, nb, pi, pj);
         if (n > 0) {
             if constexpr (GRAD) {
                 if (dots) {
@@ -653,10 +663,10 @@ __global__ __launch_bounds__(1024) void chain_kernel(LaChain a) {
             }
         }
         if (n < nc && np > 0) {
-            pw.write(s, nb, pi, pj, lane, pair, xrow, yrow);
+            pw.write(s, nb, pi, pj, lane, pair);
             if (np > 1) {
-                pw.read(s.x[nb], s.y[nb], qi, qj, xrow, yrow);
-                pw.write(s, nb, qi, qj, lane, pair, xrow, yrow);
+                pw.read(s, nb, qi, qj);
+                pw.write(s, nb, qi, qj, lane, pair);
             }
         }
         lds_barrier();
@@ -668,7 +678,7 @@ __global__ __launch_bounds__(1024) void chain_kernel(LaChain a) {
 // loads in flight, it took 92 us instead of XX with 64 (B1 T32768 H16, heads of 128).
 template <class P, int KD, int NZ>
 __global__ __launch_bounds__(256 + 256 * NZ) void states_kernel(LaChain a) {
-    __shared__ StatesShared<P, KD, NZ> s;
+    __shared__ __attribute__((aligned(512))) StatesShared<P, KD, NZ> s;
     Place at;
     if (!place(a, blockIdx.x, NZ * ZB, at)) return;
     const LaJob& jb = a.job[at.job];

@@ -106,6 +106,33 @@ struct F32 {
     }
 };
 
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// LDS by byte addresses, so that a base, a constant and an exclusive or make an operand's
+// address in one instruction.
+template <class V> __device__ __forceinline__ V lds_get(uint32_t at, uint32_t more) {
+    typedef __attribute__((address_space(3))) const char lds_c;
+    typedef __attribute__((address_space(3))) const V lds_v;
+    return *(lds_v*)((lds_c*)(uintptr_t)at + more);
+}
+
+__device__ __forceinline__ s16x4 lds_tr16_at(uint32_t at, uint32_t more) {
+    typedef __attribute__((address_space(3))) char lds_c;
+    typedef __attribute__((address_space(3))) s16x4 lds_v;
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v*)((lds_c*)(uintptr_t)at + more));
+}
+
+template <class V> __device__ __forceinline__ void lds_set(uint32_t at, uint32_t more, const V& v) {
+    typedef __attribute__((address_space(3))) char lds_c;
+    typedef __attribute__((address_space(3))) V lds_v;
+    *(lds_v*)((lds_c*)(uintptr_t)at + more) = v;
+}
+
+__device__ __forceinline__ uint32_t lds_at(const void* p) {
+    typedef __attribute__((address_space(3))) const char lds_c;
+    return (uint32_t)(uintptr_t)(lds_c*)p;
+}
+
 // A tile of rows of W elements in LDS, and where a lane (g = lane / 16, m = lane % 16)
 // finds its operands in it.
 template <class P, int W, int KIND> struct Tile {
@@ -124,58 +151,59 @@ template <class P, int W, int KIND> struct Tile {
         return piece(row, col / P::EP) + col % P::EP;
     }
 
-    // A lane's first element of an operand; the others differ in bits that the swizzle
-    // leaves alone or flips alike, so they are one exclusive or away.  fresh() keeps the
-    // compiler from holding all of them in registers over a loop.
+    // A lane's first element of an operand, as an LDS address in bytes; the others
+    // differ in bits that the swizzle leaves alone or flips alike, so they are one
+    // exclusive or away (tiles lie at multiples of 512 bytes), and rows a constant.
+    // fresh() keeps the compiler from holding all of them in registers over a loop.
 
     // Elements 32 k + 8 g .. + 7 of row 16 i + m (the swizzle repeats every 16 rows).
     struct Rows {
-        int o;
+        uint32_t o, a;
         __device__ __forceinline__ void init(int lane) {
             const int g = lane >> 4, m = lane & 15;
-            o = piece(m, 8 / P::EP * g);
+            o = piece(m, 8 / P::EP * g) * (uint32_t)sizeof(T);
         }
-        __device__ __forceinline__ void fresh() { asm volatile("" : "+v"(o)); }
-        __device__ __forceinline__ typename P::Frag get(const T* t, int i, int k) const {
-            const T* p = t + 16 * i * W;
+        __device__ __forceinline__ void of(const T* t) { a = o + lds_at(t); }
+        __device__ __forceinline__ void fresh() { asm volatile("" : "+v"(a)); }
+        __device__ __forceinline__ typename P::Frag get(int i, int k) const {
+            const uint32_t row = 16 * i * W * (uint32_t)sizeof(T);
             if constexpr (P::is_bf16) {
-                return __builtin_bit_cast(bf16x8,
-                                          *reinterpret_cast<const u32x4*>(p + (o ^ (32 * k))));
+                return __builtin_bit_cast(bf16x8, lds_get<u32x4>(a ^ (64 * k), row));
             } else {
-                const f32x4 a = *reinterpret_cast<const f32x4*>(p + (o ^ (32 * k)));
-                const f32x4 b = *reinterpret_cast<const f32x4*>(p + (o ^ (32 * k + 4)));
-                return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+                const f32x4 x = lds_get<f32x4>(a ^ (128 * k), row);
+                const f32x4 y = lds_get<f32x4>(a ^ (128 * k + 16), row);
+                return f32x8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
             }
         }
     };
 
-    // Rows 32 j + 8 g .. + 7 of column 16 u + m.
+    // Rows 32 j + 8 g .. + 7 of column 16 u + m; `column` 16 more.
     struct Cols {
-        int o[P::is_bf16 ? 2 : 8];
-        __device__ __forceinline__ void init(int lane) {
+        static constexpr int N = P::is_bf16 ? 2 : 8;
+        uint32_t o[N], a[N];
+        __device__ __forceinline__ void init(int lane, int column = 0) {
             const int g = lane >> 4, m = lane & 15;
-            if constexpr (P::is_bf16) {
-                // lane 4 r + c of a group points at 4 columns of row r (lds_tr16)
-                o[0] = at(8 * g + (m >> 2), 4 * (m & 3));
-                o[1] = at(8 * g + (m >> 2) + 4, 4 * (m & 3));
-            } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = at(8 * g + i, m);
+            for (int i = 0; i < N; ++i) {
+                // bf16: lane 4 r + c of a group points at 4 columns of row r (lds_tr16)
+                const int e = P::is_bf16 ? at(8 * g + (m >> 2) + 4 * i, 4 * (m & 3))
+                                         : at(8 * g + i, m);
+                o[i] = (e ^ (16 * column)) * (uint32_t)sizeof(T);
             }
         }
-        __device__ __forceinline__ void fresh() {
+        __device__ __forceinline__ void of(const T* t) {
 #pragma unroll
-            for (int i = 0; i < (P::is_bf16 ? 2 : 8); ++i) asm volatile("" : "+v"(o[i]));
+            for (int i = 0; i < N; ++i) a[i] = o[i] + lds_at(t);
         }
-        __device__ __forceinline__ typename P::Frag get(const T* t, int j, int u) const {
-            const T* p = t + 32 * j * W;
-            const int f = 16 * u;
+        __device__ __forceinline__ typename P::Frag get(int j, int u) const {
+            const uint32_t row = 32 * j * W * (uint32_t)sizeof(T);
+            const uint32_t f = 16 * u * (uint32_t)sizeof(T);
             if constexpr (P::is_bf16) {
-                return pair(lds_tr16(p + (o[0] ^ f)), lds_tr16(p + (o[1] ^ f)));
+                return pair(lds_tr16_at(a[0] ^ f, row), lds_tr16_at(a[1] ^ f, row));
             } else {
                 f32x8 v;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = p[o[i] ^ f];
+                for (int i = 0; i < 8; ++i) v[i] = lds_get<float>(a[i] ^ f, row);
                 return v;
             }
         }
@@ -202,26 +230,24 @@ template <class P> struct PTile {
     static __device__ __forceinline__ int at(int row, int col) {
         return piece(row % 16, col % 32 / P::EP) + col % P::EP + tile(row / 16, col / 16);
     }
-    // Elements 32 j + 8 g .. + 7 of row 16 i + m.
+    // Elements 32 j + 8 g .. + 7 of row 16 i + m, as in Tile.
     struct Rows {
-        int o[P::is_bf16 ? 1 : 2];
-        __device__ __forceinline__ void init(int lane) {
+        static constexpr int N = P::is_bf16 ? 1 : 2;
+        uint32_t a[N];
+        __device__ __forceinline__ void init(int lane, const T* t) {
             const int g = lane >> 4, m = lane & 15;
-            if constexpr (P::is_bf16) {
-                o[0] = piece(m, g);
-            } else {
-                o[0] = piece(m, 2 * g);
-                o[1] = piece(m, 2 * g + 1);
-            }
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                a[i] = lds_at(t) + piece(m, N * g + i) * (uint32_t)sizeof(T);
         }
-        __device__ __forceinline__ typename P::Frag get(const T* t, int i, int j) const {
-            const T* p = t + tile(i, 2 * j);
+        // of the term that lies `t` elements behind the first
+        __device__ __forceinline__ typename P::Frag get(int t, int i, int j) const {
+            const uint32_t at = (t + tile(i, 2 * j)) * (uint32_t)sizeof(T);
             if constexpr (P::is_bf16) {
-                return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(p + o[0]));
+                return __builtin_bit_cast(bf16x8, lds_get<u32x4>(a[0], at));
             } else {
-                const f32x4 a = *reinterpret_cast<const f32x4*>(p + o[0]);
-                const f32x4 b = *reinterpret_cast<const f32x4*>(p + o[1]);
-                return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+                const f32x4 x = lds_get<f32x4>(a[0], at), y = lds_get<f32x4>(a[1], at);
+                return f32x8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
             }
         }
     };
@@ -234,7 +260,8 @@ template <class P, int W, int KIND> struct Stage {
     static constexpr int N = P::C * PPR / 256, STEP = P::C / N;
     typedef Tile<P, W, KIND> Tl;
     u32x4 w[N];
-    int row0, col, c0;
+    int row0, col;
+    uint32_t to;                    // bytes into the tile
     bool wide, narrow;              // whether the tensor has these channels, all of W
     uint32_t off;                   // bytes from a whole chunk's first token
     __device__ __forceinline__ void init(int tid, int width, int64_t st, bool back) {
@@ -243,7 +270,7 @@ template <class P, int W, int KIND> struct Stage {
         wide = c < width;
         narrow = width < W;
         col = wide ? c : 0;
-        c0 = tid % PPR;
+        to = Tl::piece(row0, tid % PPR) * (uint32_t)sizeof(typename P::T);
         const uint32_t sb = (uint32_t)(st * sizeof(typename P::T));
         off = (back ? P::C - 1 - row0 : row0) * sb + col * (uint32_t)sizeof(typename P::T);
     }
@@ -282,15 +309,15 @@ template <class P, int W, int KIND> struct Stage {
             for (int i = 0; i < N; ++i)
                 if (!wide || row0 + i * STEP >= len) w[i] = zero;
         }
+        const uint32_t at = lds_at(tile) + to;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const u32x4 v = w[i];
-            // the swizzle repeats every 16 rows
-            if constexpr (STEP % 16 == 0)
-                *reinterpret_cast<u32x4*>(tile + Tl::piece(row0, c0) + i * STEP * W) = v;
-            else
-                *reinterpret_cast<u32x4*>(tile + Tl::piece(row0 + i * STEP, c0)) = v;
-        }
+        for (int i = 0; i < N; ++i)
+            lds_set(at ^ flip(i), i * STEP * W * (uint32_t)sizeof(typename P::T), w[i]);
+    }
+    // What row0 + i STEP changes in the swizzle (which repeats every 16 rows).
+    static constexpr uint32_t flip(int i) {
+        if constexpr (STEP % 16 == 0) return 0;
+        else return (Tl::swizzle(STEP) * (i & 1)) * 16;
     }
     // Whether an element is infinite or no number.
     __device__ __forceinline__ bool bad() const {
