@@ -42,11 +42,8 @@ template <class P, int KD> struct Shared {
     // factors of the running log decay: from the chunk's start, to its end
     float enter[2][P::C], leave[2][P::C], total[2];
     int bad[2];             // 1 + the last chunk with a z that is no number
-    // the running log decay (base 2) in two terms; factors from the last token of the
-    // tile of 16 before, to the end of the own tile, and between the end of tile j and
-    // the last token before tile i
-    float lh[2][P::C], ll[2][P::C], row[2][P::C], col[2][P::C];
-    float gap[2][P::C / 16][P::C / 16];
+    // the running log decay (base 2) in two terms
+    float lh[2][P::C], ll[2][P::C];
 };
 
 // What the states alone need of it, for NZ blocks of z's channels.
@@ -77,9 +74,7 @@ template <class P, int KD> struct PTileWork {
             }
         }
     }
-    __device__ __forceinline__ void write(Shared<P, KD>& s, int pb, int i, int j, int lane,
-                                          float scale) {
-        const int g = lane >> 4, m = lane & 15;
+    __device__ __forceinline__ f32x4 product() {
         f32x4 c = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < NK; ++k) {
@@ -89,20 +84,20 @@ template <class P, int KD> struct PTileWork {
             }
             c = P::mma(yf[k], xf[k], c);
         }
+        return c;
+    }
+    __device__ __forceinline__ void write(Shared<P, KD>& s, int pb, int i, int j, int lane,
+                                          float scale, const f32x4& c) {
+        const int g = lane >> 4, m = lane & 15;
+        const float lh = s.lh[pb][16 * i + m], ll = s.ll[pb][16 * i + m];
+        const f32x4 jh = *reinterpret_cast<const f32x4*>(&s.lh[pb][16 * j + 4 * g]);
+        const f32x4 jl = *reinterpret_cast<const f32x4*>(&s.ll[pb][16 * j + 4 * g]);
+        const int past = 16 * (i - j) + m - 4 * g;      // tokens j on which i looks back
         f32x4 v;
-        if (i == j) {
-            const float lh = s.lh[pb][16 * i + m], ll = s.ll[pb][16 * i + m];
-            const f32x4 jh = *reinterpret_cast<const f32x4*>(&s.lh[pb][16 * j + 4 * g]);
-            const f32x4 jl = *reinterpret_cast<const f32x4*>(&s.ll[pb][16 * j + 4 * g]);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                v[r] = c[r] * (__builtin_amdgcn_exp2f((lh - jh[r]) + (ll - jl[r])) * scale);
-                if (4 * g + r > m) v[r] = 0.f;
-            }
-        } else {
-            // three factors of at most 1 in place of an exponential per pair
-            const float f = s.row[pb][16 * i + m] * s.gap[pb][i][j] * scale;
-            v = c * (*reinterpret_cast<const f32x4*>(&s.col[pb][16 * j + 4 * g]) * f);
+        for (int r = 0; r < 4; ++r) {
+            v[r] = c[r] * (__builtin_amdgcn_exp2f((lh - jh[r]) + (ll - jl[r])) * scale);
+            if (r > past) v[r] = 0.f;
         }
         typedef PTile<P> TP;
         const int to = TP::piece(m, ((j & 1) * 16 + 4 * g) / P::EP) + 4 * g % P::EP +
@@ -169,7 +164,7 @@ template <class P, int KD, bool OUT, int NZ> struct Bringer {
 
 // The factors of the chunks' decays, by one wave.
 template <class P, bool OUT> struct Decays {
-    static constexpr int C = P::C, NI = C / 16;
+    static constexpr int C = P::C;
     const LaChain& a;
     const Place& at;
     int lane;
@@ -189,26 +184,10 @@ template <class P, bool OUT> struct Decays {
     // Factors of chunk n.  Running sums are in 64 bits: behind a reset, the differences
     // of sums far larger than themselves decide the factors.
     template <class S> __device__ __forceinline__ void scan(S& s, int64_t n) {
-        const int buf = (int)(n & 1), g = lane >> 4, m = lane & 15;
+        const int buf = (int)(n & 1);
         const double l = wave_scan64(base2(next)), end = lane64(l, C - 1);
-        double before = 0.0, own = end;     // L before this lane's tile, at its end
-        double last = 0.0;                  // at the end of tile i - 1
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            const double e = i + 1 < NI ? lane64(l, 16 * i + 15) : end;
-            if (g == i) {
-                before = last;
-                own = e;
-            }
-            last = e;
-        }
         if (lane < C) {
             if constexpr (OUT) {
-                s.row[buf][lane] = __builtin_amdgcn_exp2f((float)(l - before));
-                s.col[buf][lane] = __builtin_amdgcn_exp2f((float)(own - l));
-                // lane 16 i + j: gap of tiles i and j < i
-                const double to = __shfl(l, 16 * m + 15, 64);
-                if (m < g) s.gap[buf][g][m] = __builtin_amdgcn_exp2f((float)(before - to));
                 s.lh[buf][lane] = (float)l;
                 s.ll[buf][lane] = (float)(l - (double)(float)l);
                 s.enter[buf][lane] = inter * __builtin_amdgcn_exp2f((float)l);
@@ -227,8 +206,6 @@ template <class P, int KD> struct State {
     typedef Tile<P, ZB, BOTH> TZ;
     static constexpr int NU = KD / 16, NJ = P::C / 32;
     f32x4 H[NU];
-    Terms<typename P::Frag, P::NS> zt[NJ];
-    float tot;
     int g, m, w, zc, zd, kd;
     int64_t hz, hk;
     typename TY::Cols cols;
@@ -292,57 +269,47 @@ template <class P, int KD> struct State {
                     p[(16 * u + r) * (int)hk] = H[u][r] * f;
             }
     }
-    // z of the chunk in `buf`, scaled to the chunk's end, as terms: read, and scaled
-    struct Taken {
-        typename P::Frag z[NJ];
-        f32x4 l[NJ][2];
-    };
-    template <class S> __device__ __forceinline__ void read(const S& s, int buf, Taken& t) {
-        tot = s.total[buf];
-        zcol.of(s.z[buf] + w / 4 * (P::C * ZB));
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            t.z[j] = zcol.get(j, 0);
-            t.l[j][0] = *reinterpret_cast<const f32x4*>(&s.leave[buf][32 * j + 8 * g]);
-            t.l[j][1] = *reinterpret_cast<const f32x4*>(&s.leave[buf][32 * j + 8 * g + 4]);
-        }
-    }
-    __device__ __forceinline__ void take(const Taken& t) {
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            f32x8 v = P::widen(t.z[j]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] *= t.l[j][i / 4][i % 4];
-            P::template split<P::NS>(v, zt[j]);
-        }
-    }
-    // through that chunk
+    // through the chunk in `buf`
     template <class S> __device__ __forceinline__ void move(const S& s, int buf) {
         cols.of(s.y[buf]);
-#pragma unroll
-        for (int u = 0; u < NU; ++u) H[u] *= tot;
+        zcol.of(s.z[buf] + w / 4 * (P::C * ZB));
         // four tiles (fp32: two) at a time, the next ones' operands on their way: more
         // would not fit the registers, and a spill waits behind L's loads
-        constexpr int W = P::is_bf16 ? 4 : 2, NG = NJ * NU / W;
-        typename P::Frag yf[2][W];
+        constexpr int W = P::is_bf16 ? 4 : 2, PER = NU / W, NG = NJ * PER;
+        typename P::Frag yf[2][W], z[NJ];
+        f32x4 l[NJ][2];
         auto fetch = [&](int i) {
 #pragma unroll
-            for (int e = 0; e < W; ++e) {
-                const int u = i % (NU / W) * W + e;
-                yf[i & 1][e] = cols.get(i / (NU / W), u);
-            }
+            for (int e = 0; e < W; ++e) yf[i & 1][e] = cols.get(i / PER, i % PER * W + e);
         };
+        const float tot = s.total[buf];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            z[j] = zcol.get(j, 0);
+            l[j][0] = *reinterpret_cast<const f32x4*>(&s.leave[buf][32 * j + 8 * g]);
+            l[j][1] = *reinterpret_cast<const f32x4*>(&s.leave[buf][32 * j + 8 * g + 4]);
+        }
         fetch(0);
 #pragma unroll
+        for (int u = 0; u < NU; ++u) H[u] *= tot;
+        Terms<typename P::Frag, P::NS> zt;
+#pragma unroll
         for (int i = 0; i < NG; ++i) {
+            if (i % PER == 0) {             // z scaled to the chunk's end, as terms
+                const int j = i / PER;
+                f32x8 v = P::widen(z[j]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] *= l[j][e / 4][e % 4];
+                P::template split<P::NS>(v, zt);
+            }
             if (i + 1 < NG) fetch(i + 1);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int q = P::NS - 1; q >= 0; --q)
 #pragma unroll
                 for (int e = 0; e < W; ++e) {
-                    const int u = i % (NU / W) * W + e;
-                    H[u] = P::mma(yf[i & 1][e], zt[i / (NU / W)].t[q], H[u]);
+                    const int u = i % PER * W + e;
+                    H[u] = P::mma(yf[i & 1][e], zt.t[q], H[u]);
                 }
         }
     }
@@ -463,12 +430,7 @@ __global__ __launch_bounds__(1024) void chain_kernel(LaChain a) {
         for (int64_t n = 0; n <= nc; ++n) {
             if (n > 0) st.move(s, (int)((n - 1) & 1));
             lds_barrier();
-            if (n < nc) {
-                typename State<P, KD>::Taken t;
-                st.read(s, (int)(n & 1), t);
-                st.show();
-                st.take(t);
-            }
+            if (n < nc) st.show();
             if (GRAD && keep && n > 0) {
                 int64_t t0;
                 int len;
@@ -663,10 +625,14 @@ __global__ __launch_bounds__(1024) void chain_kernel(LaChain a) {
             }
         }
         if (n < nc && np > 0) {
-            pw.write(s, nb, pi, pj, lane, pair);
+            f32x4 c = pw.product();
             if (np > 1) {
                 pw.read(s, nb, qi, qj);
-                pw.write(s, nb, qi, qj, lane, pair);
+                pw.write(s, nb, pi, pj, lane, pair, c);
+                c = pw.product();
+                pw.write(s, nb, qi, qj, lane, pair, c);
+            } else {
+                pw.write(s, nb, pi, pj, lane, pair, c);
             }
         }
         lds_barrier();
@@ -732,9 +698,6 @@ __global__ __launch_bounds__(256 + 256 * NZ) void states_kernel(LaChain a) {
     State<P, KD> st(jb, at.zb * NZ * ZB, threadIdx.x);
     lds_barrier();
     for (int64_t n = 0; n < nc; ++n) {
-        typename State<P, KD>::Taken t;
-        st.read(s, (int)(n & 1), t);
-        st.take(t);
         st.move(s, (int)(n & 1));
         lds_barrier();
     }
