@@ -29,6 +29,17 @@
 //
 // Wave w of U keeps channels 16 w .. 16 w + 15 of the state in registers, transposed, in
 // the layout of a product's result, which is also that of the next product's operand.
+//
+// Bound by what a SIMD can issue at the clock that the power leaves it.  bf16 B8 T4096,
+// 16 heads of 128, bf16 out: 256 workgroups, 176 us (3.1 TB/s), 4600 cycles a chunk at
+// the 1.76 GHz (of 2.4) that the chip holds under it.  A chunk has 408 products of 16
+// cycles to a compute unit (40 P, 48 and 128 out, 192 the state in three terms): 1632
+// cycles on each SIMD; its vector instructions take 2200 more, which share the SIMD's
+// issue with them.  Without loads and stores it would be 160 us.  Four waves, each with
+// all the parts, took 454.
+//
+// The backward (B4: 324 us) is bound alike: dq and dk in one launch, 246, with three
+// terms everywhere for the decay's gradient, dv in another, 95, the decay 17.
 #include "linear_chain.h"
 
 namespace gdr {
@@ -640,8 +651,9 @@ __global__ __launch_bounds__(1024) void chain_kernel(LaChain a) {
 }
 
 // The states at the segments' ends alone, and the segments' decays.  A workgroup has up
-// to 128 channels of z, so that y is read once: bound by what its compute unit has of
-// loads in flight, it took 92 us instead of XX with 64 (B1 T32768 H16, heads of 128).
+// to 128 channels of z, so that y is read once and segments can be half as long: 72 us
+// and 9 to compose them where 64 channels took 92 and 6 (B1 T32768 H16, heads of 128;
+// 250 MB of k and v).  Bound by the state's products and terms: 50 us without.
 template <class P, int KD, int NZ>
 __global__ __launch_bounds__(256 + 256 * NZ) void states_kernel(LaChain a) {
     __shared__ __attribute__((aligned(512))) StatesShared<P, KD, NZ> s;
@@ -930,7 +942,8 @@ int64_t chunk(bool bf16) { return bf16 ? Bf16<3>::C : F32::C; }
 
 // Segments: as many as fill the chip (a workgroup to each of 256 compute units), of at
 // least two chunks.  A second pass over k and v and the states' round trip cost less
-// than idle units: fp32 B3 T1025 H6 72 x 40 82 us with 4 segments, 49 with 14.
+// than idle units: bf16 B1 T32768 H16, heads of 128, 386 us with 4 segments, 253 with 8;
+// fp32 B3 T1025 H6 72 x 40 64 with 4, 33 with 11.
 // `grain`: a segment's tokens are a multiple of it, or fewer.
 Plan plan(int64_t T, int64_t units, bool bf16, int64_t grain) {
     const int64_t C = chunk(bf16), most = T / (2 * C);
@@ -950,7 +963,9 @@ Plan fwd_plan(int64_t B, int64_t T, int64_t H, int64_t Dv, bool bf16) {
 }
 
 // The backward's chains.  dq, dk and dv side by side, in segments p; or dq and dk first,
-// and dv in segments pv that start where dk's chain has left states anyway.
+// and dv in segments pv that start where dk's chain has left states anyway.  With 64
+// sequences and heads of 128 the first makes 384 workgroups, two rounds of the chip, the
+// second 256 and then 256 of half the length: bf16 B4 T4096 H16 396 us and 324.
 struct BwdPlan {
     Plan p, pv;
     bool apart;

