@@ -419,7 +419,8 @@ extern "C" gdr_status_t gdr_rms_norm_fwd(int64_t R, int64_t C, gdr_dtype_t in_dt
     RmsArgs a{};
     st = rms_fill(a, R, C, in_dt, x, x_stride, res_dt, res, res_stride, w, eps, h);
     if (st != GDR_OK) return st;
-    if (!elem_ok(y, elem(out_dt)) || !apart({y, h}, {w}) || !apart({y}, {res})) return GDR_ERR_INVALID;
+    if (!elem_ok(y, elem(out_dt)) || !apart({y, h}, {w}) || !apart({y}, {res}))
+        return GDR_ERR_INVALID;
     if (y == x && (in_dt != out_dt || (x_stride != C && R > 1))) return GDR_ERR_INVALID;
     a.out_bf16 = out_dt == GDR_BF16;
     a.y = y;

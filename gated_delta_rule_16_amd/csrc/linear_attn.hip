@@ -1152,7 +1152,7 @@ int64_t la_bwd_workgroups(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t D
     const BwdPlan p = bwd_plan(B, T, H, Dk, Dv, bf16);
     const int64_t segs = p.p.nseg + p.p.marks + p.pv.nseg;
     const int64_t chain = 4 * ((B * H * segs + 7) / 8 * 8 * (2 * blocks(Dk) + blocks(Dv)));
-    const int64_t states = cdiv(B * H * Dk * Dv, 256);
+    const int64_t states = 2 * cdiv(B * H * Dk * Dv, 256);
     const int64_t sums = B * H * p.nblk;
     const int64_t most = chain > states ? chain : states;
     return most > sums ? most : sums;

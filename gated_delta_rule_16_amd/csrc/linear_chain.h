@@ -56,7 +56,8 @@ template <int NO_> struct Bf16 {
             }
         }
     }
-    template <int N> static __device__ __forceinline__ void split(const f32x8& x, Terms<Frag, N>& o) {
+    template <int N>
+    static __device__ __forceinline__ void split(const f32x8& x, Terms<Frag, N>& o) {
         uint32_t w[4][N];
 #pragma unroll
         for (int i = 0; i < 4; ++i) split_pair<N>(x[2 * i], x[2 * i + 1], w[i]);
@@ -93,7 +94,8 @@ struct F32 {
     static constexpr int EP = 4;
     static constexpr int NO = 1, NS = 1;
     typedef f32x8 Frag;
-    template <int N> static __device__ __forceinline__ void split(const f32x8& x, Terms<Frag, N>& o) {
+    template <int N>
+    static __device__ __forceinline__ void split(const f32x8& x, Terms<Frag, N>& o) {
         o.t[0] = x;
     }
     static __device__ __forceinline__ f32x8 widen(const Frag& f) { return f; }

@@ -31,8 +31,9 @@ struct LaJob {
     bool out_bf16;
     // states: start [B, H, ..] of the chain (NULL: zeros), and of its segments behind
     // the first [slot, B, H, ..], h_step slots a segment, the last of each the state
-    // between it and the next (backwards: the one before); end [B, H, ..] (for the states alone: the own ones of all
-    // segments but the last [.., B, H, ..], as from zeros, their decays in seg_decay)
+    // between it and the next (backwards: the one before); end [B, H, ..] (for the
+    // states alone: the own ones of all segments but the last [.., B, H, ..], as from
+    // zeros, their decays in seg_decay)
     const float *h_in, *h_seg;
     int64_t h_step;
     float* h_out;

@@ -91,13 +91,11 @@ int64_t la_step_workgroups(int64_t N, int64_t H, int64_t Dk, int64_t Dv) {
 hipError_t launch_la_step(const LaStepArgs& a) {
     const int nb = (int)((a.Dv + ROWS - 1) / ROWS);
     const dim3 grid((unsigned)la_step_workgroups(a.N, a.H, a.Dk, a.Dv));
-    if (a.Dk <= 64) {
-        if (a.bf16) hipLaunchKernelGGL((la_step_kernel<16, true>), grid, dim3(256), 0, a.stream, a, nb);
-        else hipLaunchKernelGGL((la_step_kernel<16, false>), grid, dim3(256), 0, a.stream, a, nb);
-    } else {
-        if (a.bf16) hipLaunchKernelGGL((la_step_kernel<32, true>), grid, dim3(256), 0, a.stream, a, nb);
-        else hipLaunchKernelGGL((la_step_kernel<32, false>), grid, dim3(256), 0, a.stream, a, nb);
-    }
+    auto go = [&](void (*kernel)(LaStepArgs, int)) {
+        hipLaunchKernelGGL(kernel, grid, dim3(256), 0, a.stream, a, nb);
+    };
+    if (a.Dk <= 64) go(a.bf16 ? la_step_kernel<16, true> : la_step_kernel<16, false>);
+    else go(a.bf16 ? la_step_kernel<32, true> : la_step_kernel<32, false>);
     return hipGetLastError();
 }
 

@@ -25,7 +25,9 @@ typedef uint32_t u32x2_e1 __attribute__((ext_vector_type(2), aligned(1)));
 // What an 8-bit output stores: the largest magnitude, and a value's byte.
 constexpr float kE4m3Max = 448.f, kInt8Max = 127.f;
 
-template <int Q8> __device__ __forceinline__ float largest() { return Q8 == 1 ? kE4m3Max : kInt8Max; }
+template <int Q8> __device__ __forceinline__ float largest() {
+    return Q8 == 1 ? kE4m3Max : kInt8Max;
+}
 
 // Eight values as bytes (e4m3: v_cvt_pk_fp8_f32, round to nearest even, NaN kept).
 template <int Q8> __device__ __forceinline__ u32x2_e1 pack8(const float (&f)[E]) {

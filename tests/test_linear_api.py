@@ -142,8 +142,8 @@ def test_rotary(gdr, kw, code):
 
 NORM_BAD = [
     (dict(x=None), 1), (dict(y=None), 1), (dict(x=ODD), 1), (dict(w=A[2] + 2), 1),
-    (dict(r=A[5]), 1), (dict(h=A[6]), 1), (dict(r=ODD, h=A[6]), 1), (dict(r=A[5], h=ODD), 1), (dict(R=-1), 1),
-    (dict(C=-1), 1), (dict(C=(1 << 20) + 32), 2), (dict(dt=5), 2), (dict(rdt=5), 2),
+    (dict(r=A[5]), 1), (dict(h=A[6]), 1), (dict(r=ODD, h=A[6]), 1), (dict(r=A[5], h=ODD), 1),
+    (dict(R=-1), 1), (dict(C=-1), 1), (dict(C=(1 << 20) + 32), 2), (dict(dt=5), 2), (dict(rdt=5), 2),
     (dict(eps=-1.0), 1), (dict(eps=float("nan")), 1), (dict(eps=float("inf")), 1),
     (dict(xs=-1), 1), (dict(rs=-1), 1), (dict(R=1 << 25), 1), (dict(R=HUGE), 1), (dict(y=A[2]), 1),
     (dict(r=A[5], h=A[0]), 1), (dict(r=A[5], h=A[2]), 1), (dict(r=A[5], h=A[6], y=A[5]), 1),
