@@ -764,16 +764,16 @@ struct Share {
     int64_t n, share, D;
 };
 
-__global__ __launch_bounds__(256) void share_kernel(Share a) {
-    const float* part = a.part[blockIdx.y];
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < a.n;
-         i += (int64_t)gridDim.x * 256) {
+// Workgroup `id` of `count`, of dq (side 0) or dk.
+__device__ __forceinline__ void share_heads(const Share& a, int side, int64_t id, int64_t count) {
+    const float* part = a.part[side];
+    for (int64_t i = id * 256 + threadIdx.x; i < a.n; i += count * 256) {
         const int64_t row = i / (a.D / 4), c = i % (a.D / 4) * 4;
         f32x4 x = {0.f, 0.f, 0.f, 0.f};
         for (int64_t k = 0; k < a.share; ++k)
             x += *reinterpret_cast<const f32x4*>(part + (row * a.share + k) * a.D + c);
         const float v[4] = {x[0], x[1], x[2], x[3]};
-        row_store<4, false>(a.out[blockIdx.y], row * a.D + c, a.bf16, v, 4);
+        row_store<4, false>(a.out[side], row * a.D + c, a.bf16, v, 4);
     }
 }
 
@@ -791,9 +791,8 @@ struct DecayGrad {
 
 // dg of one block of tokens of a (sequence, head): what all pairs across its end say,
 // <G, S> there, and the running sum of q . dq - k . dk from the end, in 64 bits.
-__global__ __launch_bounds__(256) void decay_grad_kernel(DecayGrad a) {
+__device__ __forceinline__ void decay_grad(const DecayGrad& a, int64_t id) {
     __shared__ double red[4], part[2][4];
-    const int64_t id = blockIdx.x;
     const int64_t h = id % a.H, b = id / a.H % a.B, p = id / a.H / a.B;
     const int64_t bh = b * a.H + h;
     const int tid = threadIdx.x;
@@ -868,6 +867,19 @@ __global__ __launch_bounds__(256) void decay_grad_kernel(DecayGrad a) {
         __syncthreads();
         if (tid == 0) a.part[(b * a.nblk + p) * a.H + h] = (red[0] + red[1]) + (red[2] + red[3]);
     }
+}
+
+// What is left behind the chains: the decay's gradient by the first `decays` workgroups,
+// the sums over shared heads by the others, side by side (a launch of its own for
+// either cost 4 us more).
+__global__ __launch_bounds__(256) void finish_kernel(DecayGrad d, Share m, uint32_t decays,
+                                                     uint32_t shares) {
+    if (blockIdx.x < decays) {
+        decay_grad(d, blockIdx.x);
+        return;
+    }
+    const uint32_t id = blockIdx.x - decays;
+    share_heads(m, id < shares ? 0 : 1, id < shares ? id : id - shares, shares);
 }
 
 __global__ __launch_bounds__(64) void head_sum_kernel(const double* part, float* dg, int64_t n,
@@ -1153,7 +1165,7 @@ int64_t la_bwd_workgroups(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t D
     const int64_t segs = p.p.nseg + p.p.marks + p.pv.nseg;
     const int64_t chain = 4 * ((B * H * segs + 7) / 8 * 8 * (2 * blocks(Dk) + blocks(Dv)));
     const int64_t states = 2 * cdiv(B * H * Dk * Dv, 256);
-    const int64_t sums = B * H * p.nblk;
+    const int64_t sums = B * H * p.nblk + 2 * 16384;        // the most of stride_blocks
     const int64_t most = chain > states ? chain : states;
     return most > sums ? most : sums;
 }
@@ -1237,8 +1249,10 @@ hipError_t launch_la_bwd(const LaArgs& a) {
         c.job[0] = jv;
         if ((e = launch_chain(c)) != hipSuccess) return e;
     }
+    Share m{};
+    DecayGrad d{};
+    uint32_t shares = 0, decays = 0;
     if (!own) {
-        Share m{};
         m.part[0] = f32(w.dq);
         m.part[1] = f32(w.dk);
         m.out[0] = a.dq;
@@ -1247,11 +1261,9 @@ hipError_t launch_la_bwd(const LaArgs& a) {
         m.n = a.B * a.T * a.Hk * (a.Dk / 4);
         m.share = a.H / a.Hk;
         m.D = a.Dk;
-        hipLaunchKernelGGL(share_kernel, dim3(stride_blocks(m.n), 2), dim3(256), 0, a.stream, m);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
+        shares = (uint32_t)stride_blocks(m.n);
     }
     if (a.dg) {
-        DecayGrad d{};
         d.B = a.B;
         d.T = a.T;
         d.H = a.H;
@@ -1268,16 +1280,16 @@ hipError_t launch_la_bwd(const LaArgs& a) {
         d.g_head = a.g_head;
         d.dg = a.g_head ? nullptr : a.dg;
         d.part = a.g_head ? reinterpret_cast<double*>(ws + w.part) : nullptr;
-        hipLaunchKernelGGL(decay_grad_kernel, dim3((unsigned)(a.B * a.H * d.nblk)), dim3(256), 0,
-                           a.stream, d);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-        if (a.g_head) {
-            hipLaunchKernelGGL(head_sum_kernel, dim3((unsigned)a.H), dim3(64), 0, a.stream, d.part,
-                               a.dg, a.B * d.nblk, a.H);
-            if ((e = hipGetLastError()) != hipSuccess) return e;
-        }
+        decays = (uint32_t)(a.B * a.H * d.nblk);
     }
-    return hipSuccess;
+    if (decays + shares == 0) return hipSuccess;
+    hipLaunchKernelGGL(finish_kernel, dim3(decays + 2 * shares), dim3(256), 0, a.stream, d, m,
+                       decays, shares);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (a.dg && a.g_head)
+        hipLaunchKernelGGL(head_sum_kernel, dim3((unsigned)a.H), dim3(64), 0, a.stream, d.part,
+                           a.dg, a.B * d.nblk, a.H);
+    return hipGetLastError();
 }
 
 }  // namespace gdr
