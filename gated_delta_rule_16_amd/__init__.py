@@ -200,7 +200,7 @@ lib.gdr_linear_attn_fwd.argtypes = ([_I64] * 6 + [_E] + [_P] * 6 + [_F, _U, _E] 
 lib.gdr_linear_attn_fwd.restype = ctypes.c_int
 lib.gdr_linear_attn_step.argtypes = [_I64] * 5 + [_E] + [_P] * 6 + [_F, _U, _E, _P, _P]
 lib.gdr_linear_attn_step.restype = ctypes.c_int
-lib.gdr_linear_attn_bwd_workspace_size.argtypes = [_I64] * 6 + [_E]
+lib.gdr_linear_attn_bwd_workspace_size.argtypes = [_I64] * 6 + [_E, _U]
 lib.gdr_linear_attn_bwd_workspace_size.restype = ctypes.c_size_t
 lib.gdr_linear_attn_bwd.argtypes = ([_I64] * 6 + [_E] + [_P] * 8 + [_F, _U, _E] + [_P] * 6 +
                                     [_Z, _P])
@@ -1303,9 +1303,11 @@ def gdr_linear_attn_step(q, k, v, log_decay, state, *, scale=1.0, out_dtype=None
     return o
 
 
-def gdr_linear_attn_bwd_workspace_size(B, T, H, Hk, Dk, Dv, dtype) -> int:
-    """Bytes of device workspace gdr_linear_attn_bwd needs."""
-    return int(lib.gdr_linear_attn_bwd_workspace_size(B, T, H, Hk, Dk, Dv, _DT[dtype]))
+def gdr_linear_attn_bwd_workspace_size(B, T, H, Hk, Dk, Dv, dtype, *, head_decay=False) -> int:
+    """Bytes of device workspace gdr_linear_attn_bwd needs (``head_decay``: with a
+    log_decay [H])."""
+    return int(lib.gdr_linear_attn_bwd_workspace_size(
+        B, T, H, Hk, Dk, Dv, _DT[dtype], GDR_LA_HEAD_DECAY if head_decay else 0))
 
 
 @_on_own_device
@@ -1331,7 +1333,7 @@ def gdr_linear_attn_bwd(q, k, v, log_decay, s0, dout, ds_final=None, *, scale=1.
     dg = torch.empty_like(log_decay) if want_ddecay and log_decay is not None else None
     ds0 = _new(ds_final, torch.float32, (B, H, Dv, Dk), dev) if want_ds0 else None
     workspace = _scratch(workspace, _need("gdr_linear_attn_bwd_workspace_size", B, T, H, Hk, Dk,
-                                          Dv, _DT[q.dtype]), dev)
+                                          Dv, _DT[q.dtype], flags), dev)
     _run("gdr_linear_attn_bwd", lib.gdr_linear_attn_bwd(
         B, T, H, Hk, Dk, Dv, _DT[q.dtype], _p(q), _p(k), _p(v), _i64s(*st, *dst), _p(log_decay),
         _p(s0), _p(dout), _p(ds_final), float(scale), flags, code, _p(dq), _p(dk), _p(dv), _p(dg),

@@ -214,11 +214,13 @@ extern "C" gdr_status_t gdr_linear_attn_step(int64_t N, int64_t H, int64_t Hk, i
 }
 
 extern "C" size_t gdr_linear_attn_bwd_workspace_size(int64_t B, int64_t T, int64_t H, int64_t Hk,
-                                                     int64_t Dk, int64_t Dv, gdr_dtype_t in_dt) {
-    if (la_check(B, T, H, Hk, Dk, Dv, in_dt, in_dt, 0) != GDR_OK || la_nothing(B, H) || T == 0 ||
-        !workgroups_ok((double)la_bwd_workgroups(B, T, H, Dk, Dv, in_dt == GDR_BF16)))
+                                                     int64_t Dk, int64_t Dv, gdr_dtype_t in_dt,
+                                                     uint32_t flags) {
+    const bool bf = in_dt == GDR_BF16, head = flags & GDR_LA_HEAD_DECAY;
+    if (la_check(B, T, H, Hk, Dk, Dv, in_dt, in_dt, flags) != GDR_OK || la_nothing(B, H) ||
+        T == 0 || !workgroups_ok((double)la_bwd_workgroups(B, T, H, Dk, Dv, bf, head)))
         return 0;
-    return la_bwd_workspace_bytes(B, T, H, Hk, Dk, Dv, in_dt == GDR_BF16);
+    return la_bwd_workspace_bytes(B, T, H, Hk, Dk, Dv, bf, head);
 }
 
 extern "C" gdr_status_t gdr_linear_attn_bwd(int64_t B, int64_t T, int64_t H, int64_t Hk, int64_t Dk,
@@ -252,8 +254,10 @@ extern "C" gdr_status_t gdr_linear_attn_bwd(int64_t B, int64_t T, int64_t H, int
     if (!apart({dq, dk, dv, dlog_decay, ds0, workspace}, {q, k, v, log_decay, s0, dout, ds_final}))
         return GDR_ERR_INVALID;
     const bool bf = in_dt == GDR_BF16;
-    if (!workgroups_ok((double)la_bwd_workgroups(B, T, H, Dk, Dv, bf))) return GDR_ERR_INVALID;
-    if (!ptrs_ok({workspace}) || workspace_bytes < la_bwd_workspace_bytes(B, T, H, Hk, Dk, Dv, bf))
+    if (!workgroups_ok((double)la_bwd_workgroups(B, T, H, Dk, Dv, bf, head)))
+        return GDR_ERR_INVALID;
+    if (!ptrs_ok({workspace}) ||
+        workspace_bytes < la_bwd_workspace_bytes(B, T, H, Hk, Dk, Dv, bf, head))
         return GDR_ERR_INVALID;
     LaArgs a{};
     a.B = B;

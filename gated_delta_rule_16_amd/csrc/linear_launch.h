@@ -156,9 +156,10 @@ hipError_t launch_rms_bwd(const RmsBwdArgs& a);
 int64_t la_fwd_workgroups(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, bool bf16);
 size_t la_fwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, bool bf16);
 hipError_t launch_la_fwd(const LaArgs& a);
-int64_t la_bwd_workgroups(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, bool bf16);
+int64_t la_bwd_workgroups(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, bool bf16,
+                          bool g_head);
 size_t la_bwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Hk, int64_t Dk, int64_t Dv,
-                              bool bf16);
+                              bool bf16, bool g_head);
 hipError_t launch_la_bwd(const LaArgs& a);
 hipError_t launch_la_step(const LaStepArgs& a);
 int64_t la_step_workgroups(int64_t N, int64_t H, int64_t Dk, int64_t Dv);

@@ -143,7 +143,8 @@ def test_rotary(gdr, kw, code):
 NORM_BAD = [
     (dict(x=None), 1), (dict(y=None), 1), (dict(x=ODD), 1), (dict(w=A[2] + 2), 1),
     (dict(r=A[5]), 1), (dict(h=A[6]), 1), (dict(r=ODD, h=A[6]), 1), (dict(r=A[5], h=ODD), 1),
-    (dict(R=-1), 1), (dict(C=-1), 1), (dict(C=(1 << 20) + 32), 2), (dict(dt=5), 2), (dict(rdt=5), 2),
+    (dict(R=-1), 1), (dict(C=-1), 1), (dict(C=(1 << 20) + 32), 2), (dict(dt=5), 2),
+    (dict(rdt=5), 2),
     (dict(eps=-1.0), 1), (dict(eps=float("nan")), 1), (dict(eps=float("inf")), 1),
     (dict(xs=-1), 1), (dict(rs=-1), 1), (dict(R=1 << 25), 1), (dict(R=HUGE), 1), (dict(y=A[2]), 1),
     (dict(r=A[5], h=A[0]), 1), (dict(r=A[5], h=A[2]), 1), (dict(r=A[5], h=A[6], y=A[5]), 1),
@@ -199,7 +200,11 @@ def test_empty_calls_launch_nothing(gdr):
 
 def test_workspace_sizes(gdr):
     L = gdr.lib
-    size, back = L.gdr_linear_attn_fwd_workspace_size, L.gdr_linear_attn_bwd_workspace_size
+    size = L.gdr_linear_attn_fwd_workspace_size
+
+    def back(*a, flags=0):
+        return L.gdr_linear_attn_bwd_workspace_size(*a, flags)
+
     assert size(1, 64, 4, 64, 64, BF16) == 0            # one segment
     assert size(1, 32768, 4, 64, 64, BF16) >= 4 * 4 * 64 * 64
     for a in ((-1, 64, 4, 64, 64, 1), (1, 32768, 4, 60, 64, 1), (1, 32768, 4, 64, 136, 1),
@@ -211,6 +216,10 @@ def test_workspace_sizes(gdr):
     assert back(2, 100, 4, 4, 64, 32, BF16) >= 4 * 2 * 4 * 64 * 32 + 8 * 2 * 100 * 4 * 4
     assert back(2, 100, 4, 2, 64, 32, BF16) >= \
         back(2, 100, 4, 4, 64, 32, BF16) + 8 * 2 * 100 * 4 * 64
+    # a decay per head: four times the kept states
+    assert back(64, 4096, 4, 4, 64, 32, BF16, flags=1) >= \
+        back(64, 4096, 4, 4, 64, 32, BF16) + 2 * 11 * 4 * 256 * 64 * 32
+    assert back(2, 100, 4, 4, 64, 32, BF16, flags=2) == 0
     for a in ((2, 100, 4, 3, 64, 32, 1), (2, 100, 4, 0, 64, 32, 1), (2, 100, 4, 4, 64, 30, 1),
               (2, -5, 4, 4, 64, 32, 1), (2, 100, 4, 4, 64, 32, 2), (0, 100, 4, 4, 64, 32, 1),
               (2, 0, 4, 4, 64, 32, 1), (HUGE, HUGE, 4, 4, 64, 32, 1), (2, 100, 0, 0, 64, 32, 1)):
