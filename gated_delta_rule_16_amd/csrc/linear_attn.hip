@@ -31,15 +31,15 @@
 // the layout of a product's result, which is also that of the next product's operand.
 //
 // Bound by what a SIMD can issue at the clock that the power leaves it.  bf16 B8 T4096,
-// 16 heads of 128, bf16 out: 256 workgroups, 176 us (3.1 TB/s), 4600 cycles a chunk at
+// 16 heads of 128, bf16 out: 256 workgroups, 174 us (3.1 TB/s), 4600 cycles a chunk at
 // the 1.76 GHz (of 2.4) that the chip holds under it.  A chunk has 408 products of 16
 // cycles to a compute unit (40 P, 48 and 128 out, 192 the state in three terms): 1632
 // cycles on each SIMD; its vector instructions take 2200 more, which share the SIMD's
 // issue with them.  Without loads and stores it would be 160 us.  Four waves, each with
 // all the parts, took 454.
 //
-// The backward (B4: 324 us) is bound alike: dq and dk in one launch, 246, with three
-// terms everywhere for the decay's gradient, dv in another, 95, the decay 17.
+// The backward (B4: 318 us) is bound alike: dq and dk in one launch, 213, with three
+// terms everywhere for the decay's gradient, dv in another, 82, the decay 17.
 #include "linear_chain.h"
 
 namespace gdr {
