@@ -1222,34 +1222,33 @@ def gdr_layer_norm_bwd(x, w, dy, eps=1e-5, *, dres=None, grad_dtype=torch.float3
 # ---- linear attention, rotary positions, RMS norm ----------------------------------
 
 
-def _heads(name, t, dtype, shape, device, lead):
-    """Strides of the ``lead`` leading dimensions and the head's of [.., heads, d]."""
-    _like(name, t, dtype, shape, device)
+def _channels(name, t):
+    """A token tensor's strides: all of them free but the channels'."""
     st = t.stride()
-    if shape[-1] > 1 and st[-1] != 1 and t.numel():
+    if st[-1] != 1 and t.shape[-1] > 1 and t.numel():
         raise ValueError(f"{name} must have contiguous channels")
-    return st[:lead + 1]
+    return st[:-1]
 
 
 def _la_inputs(q, k, v, log_decay, lead):
     """Checks shared by linear attention's calls; returns (device, sizes, strides,
     flags)."""
     dev = _first("q", q, lead + 2)
-    _first("k", k, lead + 2)
     _first("v", v, lead + 2)
-    Hk, Dk = q.shape[lead:]
-    H, Dv = v.shape[lead:]
-    qs = _heads("q", q, q.dtype, q.shape, dev, lead)
-    ks = _heads("k", k, q.dtype, q.shape, dev, lead)
-    vs = _heads("v", v, q.dtype, (*q.shape[:lead], H, Dv), dev, lead)
+    qs, vs, dt = q.shape, v.shape, q.dtype
+    H, Dv = vs[lead], vs[lead + 1]
+    tokens = (qs[0], qs[1]) if lead == 2 else (qs[0],)
+    _like("k", k, dt, qs, dev)
+    _like("v", v, dt, (*tokens, H, Dv), dev)
+    st = _channels("q", q) + _channels("k", k) + _channels("v", v)
     flags = 0
     if log_decay is not None:
         if isinstance(log_decay, torch.Tensor) and log_decay.dim() == 1:
             flags = GDR_LA_HEAD_DECAY
             _whole("log_decay", log_decay, torch.float32, (H,), dev)
         else:
-            _whole("log_decay", log_decay, torch.float32, (*q.shape[:lead], H), dev)
-    return dev, (*q.shape[:lead], H, Hk, Dk, Dv), (*qs, *ks, *vs), flags
+            _whole("log_decay", log_decay, torch.float32, (*tokens, H), dev)
+    return dev, (*tokens, H, qs[lead], qs[lead + 1], Dv), st, flags
 
 
 def gdr_linear_attn_fwd_workspace_size(B, T, H, Dk, Dv, dtype) -> int:
@@ -1322,8 +1321,8 @@ def gdr_linear_attn_bwd(q, k, v, log_decay, s0, dout, ds_final=None, *, scale=1.
     dev, (B, T, H, Hk, Dk, Dv), st, flags = _la_inputs(q, k, v, log_decay, 2)
     if s0 is not None:
         _whole("s0", s0, torch.float32, (B, H, Dv, Dk), dev)
-    _first("dout", dout, 4)
-    dst = _heads("dout", dout, q.dtype, (B, T, H, Dv), dev, 2)
+    _like("dout", dout, q.dtype, (B, T, H, Dv), dev)
+    dst = _channels("dout", dout)
     if ds_final is not None:
         _whole("ds_final", ds_final, torch.float32, (B, H, Dv, Dk), dev)
     code = _dt_of("grad_dtype", grad_dtype)
@@ -1391,9 +1390,10 @@ def gdr_rotary(q, k, positions, freqs, *, interleaved=False, scale=1.0, inverse=
     ks, Hk = (0,) * 6, 0
     if k is not None:
         _first("k", k, lead + 2)
-        Hk = k.shape[lead]
-        _like("k", k, q.dtype, shape[:lead] + (Hk, D), dev)
-        ks, k_out = _rotary_side("k", k, k_out, k.shape, lead, T)
+        kshape = k.shape
+        Hk = kshape[lead]
+        _like("k", k, q.dtype, (B, T, Hk, D) if lead == 2 else (B, Hk, D), dev)
+        ks, k_out = _rotary_side("k", k, k_out, kshape, lead, T)
     elif k_out is not None:
         raise ValueError("k_out needs k")
     pos, ps, start = None, 0, 0
@@ -1422,19 +1422,15 @@ _ROTARY_STRIDES = ctypes.c_int64 * 12
 def _rotary_side(name, t, out, shape, lead, T):
     """Strides per sequence, token and head of q or k and of its output, and that."""
     H, D = shape[lead], shape[lead + 1]
-    st = t.stride()
-    if D > 1 and st[-1] != 1 and t.numel():
-        raise ValueError(f"{name} must have contiguous channels")
+    st = _channels(name, t)
     if out is None:
         out = torch.empty(shape, dtype=t.dtype, device=t.device)
         so = (T * H * D, H * D, D)
-        return (st[:3] if lead == 2 else (st[0], 0, st[1])) + so, out
+        return (st if lead == 2 else (st[0], 0, st[1])) + so, out
     _like(name + "_out", out, t.dtype, shape, t.device)
-    so = out.stride()
-    if D > 1 and so[-1] != 1 and out.numel():
-        raise ValueError(f"{name}_out must have contiguous channels")
+    so = _channels(name + "_out", out)
     if lead == 2:
-        return st[:3] + so[:3], out
+        return st + so, out
     return (st[0], 0, st[1], so[0], 0, so[1]), out
 
 
