@@ -303,3 +303,42 @@ def test_large_values_in_masked_pairs(gdr_lib):
     part = [x[:, :40].contiguous() if x is not None else None for x in a]
     (ow, _), (mo, _), (dm, _) = R.la_fwd(*[n64(x) for x in part], 1.0)
     close("o", o[:, :40], ow, R.la_bound(ow, mo, dm, 64, 64, 64))
+
+
+# ---- many heads, many sequences, a decay per head over several blocks ---------------------
+
+
+@pytest.mark.parametrize("B,T,H,Hk,Dk,Dv", [(1, 5, 2048, 1, 8, 8), (3000, 2, 1, 1, 8, 16),
+                                            (2, 70, 96, 3, 16, 8)])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_many_heads_or_sequences(gdr_lib, B, T, H, Hk, Dk, Dv, dt):
+    a, do, ds = make(41, B, T, H, Hk, Dk, Dv, dt)
+    check_fwd(gdr_lib, a)
+    check_bwd(gdr_lib, a, do, ds)
+
+
+@pytest.mark.parametrize("B,T,Dk,Dv", [(130, 700, 8, 8), (2, 1500, 16, 72), (1, 515, 64, 64)])
+@pytest.mark.parametrize("state", ["none", "start", "both"])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_decay_per_head_over_blocks(gdr_lib, B, T, Dk, Dv, state, dt):
+    """The sums over blocks of tokens, with and without states at either end."""
+    a, do, ds = make(42, B, T, 1, 1, Dk, Dv, dt, "head", state=state != "none")
+    check_bwd(gdr_lib, a, do, ds if state == "both" else None)
+
+
+def test_sum_per_head_is_as_exact_as_its_tokens(gdr_lib):
+    """A decay per head is the same call with the decay of every token; its gradient is
+    the sum of theirs.  Both err by at most the bound of one of them."""
+    a, do, _ = make(43, 2, 1300, 2, 2, 64, 64, "f32", "head", state=False)
+    b = list(a)
+    b[3] = a[3].expand(2, 1300, 2).contiguous()
+    one = gdr_lib.gdr_linear_attn_bwd(*a, do, scale=0.3)
+    all_ = gdr_lib.gdr_linear_attn_bwd(*b, do, scale=0.3)
+    torch.cuda.synchronize()
+    r = R.la_bwd(*[n64(x) for x in b], n64(do), None, 0.3)
+    bound = R.la_dg_bound(r, 1300, 64, 64).sum((0, 1))
+    close("dg", one[3], r[0]["dg"].sum((0, 1)), bound)
+    close("sum", all_[3].double().sum((0, 1)), r[0]["dg"].sum((0, 1)), bound)
+    for x, y, n in zip(one[:3], all_[:3], ("dq", "dk", "dv")):
+        close(n, x, r[0][n], R.la_bound(r[0][n], r[1][n], r[2][n], 1300, 64, 64))
+        close(n, y, r[0][n], R.la_bound(r[0][n], r[1][n], r[2][n], 1300, 64, 64))
