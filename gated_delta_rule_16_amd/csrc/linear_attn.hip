@@ -38,8 +38,8 @@
 // issue with them.  Without loads and stores it would be 160 us.  Four waves, each with
 // all the parts, took 454.
 //
-// The backward (B4: 318 us) is bound alike: dq and dk in one launch, 213, with three
-// terms everywhere for the decay's gradient, dv in another, 82, the decay 17.
+// The backward (B4: 343 us) is bound alike: dq and dk in one launch, 213, with three
+// terms everywhere for the decay's gradient, dv in another, 82, the decay 25.
 #include "linear_chain.h"
 
 namespace gdr {
@@ -777,6 +777,8 @@ __device__ __forceinline__ void share_heads(const Share& a, int side, int64_t id
     }
 }
 
+constexpr int kMostKept = 512, kTurns = kMostKept / 256;   // tokens between kept states
+
 struct DecayGrad {
     int64_t B, T, H, every, nblk, state;
     int nq;                         // slots of either sum
@@ -792,13 +794,15 @@ struct DecayGrad {
 // dg of one block of tokens of a (sequence, head): what all pairs across its end say,
 // <G, S> there, and the running sum of q . dq - k . dk from the end, in 64 bits.  Its
 // terms carry the roundings of dq and dk, so its error grows with the distance from the
-// end.  A sum over all tokens (a decay per head) adds them up; there the same at the
-// block's start, from the block before, takes the error out in proportion to the
-// distance, which leaves half of it, and blocks are shorter.  Head sums of B2 T4109 H4
-// 64 x 64, six draws: 1.6e-6 off on average at 1024 tokens without, 0.5e-6 at 256 with
-// (a plain form in fp32: 0.4e-6); B4 T4096 H16 of 128 takes 350 us in place of 320.
+// end.  At the block's start the pairs across the end of the block before say the same:
+// the difference is taken out in proportion to the distance.  That and the blocks'
+// length keep dg about as exact as a form in fp32 that goes token by token: bf16 B50
+// T2737 H1 32 x 128 2.0e-6 off at 1024 tokens from the end alone, 1.6e-6 from both ends,
+// 1.0e-6 at 512 (fp32 0.6e-6).  A sum per head, which adds all of them up, has blocks of
+// 256: B2 T4109 H4 64 x 64, six draws, 1.6e-6 at first and 0.5e-6 on average (0.4e-6).
+// At B4 T4096 H16 of 128 (328 us with 1024) 512 cost 14 us, 256 30.
 __device__ __forceinline__ void decay_grad(const DecayGrad& a, int64_t id) {
-    __shared__ double red[4], part[2][4];
+    __shared__ double red[4], part[kTurns][4];
     const int64_t h = id % a.H, b = id / a.H % a.B, p = id / a.H / a.B;
     const int64_t bh = b * a.H + h;
     const int tid = threadIdx.x;
@@ -833,14 +837,14 @@ __device__ __forceinline__ void decay_grad(const DecayGrad& a, int64_t id) {
         const int64_t t = (o + 1) * a.every;
         return o + 1 < a.nblk ? sum * (double)__builtin_amdgcn_exp2f(rate(t) * kLog2e) : sum;
     };
-    const double tail = across(p);
-    double carry = tail, sum = 0.0;
+    // thread 0: the last token of 256 each
     const int wv = tid >> 6;
     const int64_t n = a.B * a.H * a.T, row = bh * a.T;
-    int turn = 0;
-    for (int64_t hi = t1; hi > t0; hi -= 256, turn ^= 1) {
-        const int64_t t = hi - 1 - tid;             // thread 0: the last token
-        double e = 0.0;
+    double e[kTurns];
+#pragma unroll
+    for (int k = 0; k < kTurns; ++k) {
+        const int64_t t = t1 - 1 - 256 * k - tid;
+        e[k] = 0.0;
         if (t >= t0) {
             // all loads at once, without branches between them
             float x[16];
@@ -852,38 +856,45 @@ __device__ __forceinline__ void decay_grad(const DecayGrad& a, int64_t id) {
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                e += i < a.nq ? (double)x[2 * i] - (double)x[2 * i + 1] : 0.0;
+                e[k] += i < a.nq ? (double)x[2 * i] - (double)x[2 * i + 1] : 0.0;
         }
-        e = wave_scan64(e);
-        if ((tid & 63) == 63) part[turn][wv] = e;
-        __syncthreads();
+        e[k] = wave_scan64(e[k]);
+        if ((tid & 63) == 63) part[k][wv] = e[k];
+    }
+    const double tail = across(p);                      // part is there behind its barriers
+    const double head = p > 0 ? across(p - 1) : 0.0;
+    double carry = tail, sum = 0.0;
+#pragma unroll
+    for (int k = 0; k < kTurns; ++k) {
         double before = 0.0, all = 0.0;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-            before += w < wv ? part[turn][w] : 0.0;
-            all += part[turn][w];
+            before += w < wv ? part[k][w] : 0.0;
+            all += part[k][w];
         }
-        if (t >= t0) {
-            // a decay of 0 has no gradient
-            const double d = rate(t) < -104.f ? 0.0 : carry + before + e;
-            sum += d;
-            if (a.dg) a.dg[(b * a.T + t) * a.H + h] = (float)d;
-        }
+        e[k] += carry + before;
         carry += all;
     }
+    // the start state's own gradient is not kept: then the end alone counts, as where
+    // either is no number
+    double off = p > 0 || !a.s0 ? carry - head : 0.0;
+    if (off - off != 0.0) off = 0.0;
+#pragma unroll
+    for (int k = 0; k < kTurns; ++k) {
+        const int64_t t = t1 - 1 - 256 * k - tid;
+        if (t < t0) continue;
+        // a decay of 0 has no gradient
+        const double share = (double)(t1 - t) / (double)(t1 - t0);
+        const double d = rate(t) < -104.f ? 0.0 : e[k] - off * share;
+        sum += d;
+        if (a.dg) a.dg[(b * a.T + t) * a.H + h] = (float)d;
+    }
     if (a.part) {
-        // at the start: pairs across the block before, or no state before the first token
-        const bool known = p > 0 || !a.s0;
-        const double off = known ? carry - (p > 0 ? across(p - 1) : 0.0) : 0.0;
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d, 64);
         if ((tid & 63) == 0) red[tid >> 6] = sum;
         __syncthreads();
-        if (tid == 0) {
-            const double all = (red[0] + red[1]) + (red[2] + red[3]);
-            const double less = rate(t0) < -104.f ? 0.0 : 0.5 * (double)(t1 - t0 + 1) * off;
-            a.part[(b * a.nblk + p) * a.H + h] = all - less;
-        }
+        if (tid == 0) a.part[(b * a.nblk + p) * a.H + h] = (red[0] + red[1]) + (red[2] + red[3]);
     }
 }
 
@@ -1009,7 +1020,7 @@ double chain_cost(int64_t workgroups, int64_t L, bool bf16) {
 
 BwdPlan bwd_plan(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, bool bf16,
                  bool g_head) {
-    const int64_t most = g_head ? 256 : 1024;       // tokens between kept states (decay_grad)
+    const int64_t most = g_head ? 256 : kMostKept;  // tokens between kept states (decay_grad)
     const int64_t BH = B * H, nk = BH * 2 * blocks(Dk), nv = BH * blocks(Dv);
     // a pass over the states alone takes half the time
     auto states = [&](const Plan& p) {
