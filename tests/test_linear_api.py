@@ -216,9 +216,9 @@ def test_workspace_sizes(gdr):
     assert back(2, 100, 4, 4, 64, 32, BF16) >= 4 * 2 * 4 * 64 * 32 + 8 * 2 * 100 * 4 * 4
     assert back(2, 100, 4, 2, 64, 32, BF16) >= \
         back(2, 100, 4, 4, 64, 32, BF16) + 8 * 2 * 100 * 4 * 64
-    # a decay per head: four times the kept states
+    # a decay per head: states at every 256 tokens in place of 512
     assert back(64, 4096, 4, 4, 64, 32, BF16, flags=1) >= \
-        back(64, 4096, 4, 4, 64, 32, BF16) + 2 * 11 * 4 * 256 * 64 * 32
+        back(64, 4096, 4, 4, 64, 32, BF16) + 2 * 8 * 4 * 256 * 64 * 32
     assert back(2, 100, 4, 4, 64, 32, BF16, flags=2) == 0
     for a in ((2, 100, 4, 3, 64, 32, 1), (2, 100, 4, 0, 64, 32, 1), (2, 100, 4, 4, 64, 30, 1),
               (2, -5, 4, 4, 64, 32, 1), (2, 100, 4, 4, 64, 32, 2), (0, 100, 4, 4, 64, 32, 1),
