@@ -38,8 +38,8 @@
 // issue with them.  Without loads and stores it would be 160 us.  Four waves, each with
 // all the parts, took 454.
 //
-// The backward (B4: 343 us) is bound alike: dq and dk in one launch, 213, with three
-// terms everywhere for the decay's gradient, dv in another, 82, the decay 25.
+// The backward (B4: 343 us) is bound alike: dq and dk in one launch, 228, with three
+// terms everywhere for the decay's gradient, dv in another, 87, the decay 28.
 #include "linear_chain.h"
 
 namespace gdr {
