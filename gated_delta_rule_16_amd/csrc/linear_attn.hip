@@ -717,11 +717,13 @@ __global__ __launch_bounds__(256 + 256 * NZ) void states_kernel(LaChain a) {
 }
 
 // States at the marks between segments, in place, from the segments' own (as from a
-// start of zeros): at(next) = decay at(this) + own.  Up to two chains at once.
+// start of zeros): at(next) = decay at(this) + own.  Up to two chains at once.  `copy`
+// (or NULL) receives the state that they start from.
 struct Compose {
     int64_t BH, state, marks;
     float* buf[2];
     const float *decay[2], *h0[2];
+    float* copy[2];
     bool back[2];
 };
 
@@ -733,6 +735,7 @@ __global__ __launch_bounds__(256) void compose_kernel(Compose a) {
     float* buf = a.buf[k] + i;
     const float* decay = a.decay[k] + i / a.state;
     float h = a.h0[k] ? a.h0[k][i] : 0.f;
+    if (a.copy[k]) a.copy[k][i] = h;
     const bool back = a.back[k];
     // batches of loads: a store would hold back the next segment's
     for (int64_t c = 0; c < a.marks; c += N) {
@@ -1078,9 +1081,10 @@ LaChain chain(const LaArgs& a, const Plan& p) {
 }
 
 // Start states of the segments behind the first, of one or two jobs (h_in, hz and hk as
-// for the whole chain), into buf, and the jobs set to start from them.
+// for the whole chain), into buf, and the jobs set to start from them.  The first job
+// starts from `copy`, where that is given.
 hipError_t segment_states(LaChain c, const Plan& p, LaJob* const* jobs, int n, float* const* buf,
-                          float* const* decay) {
+                          float* const* decay, float* copy) {
     Compose m{};
     m.BH = c.B * c.H;
     m.state = c.state;
@@ -1104,6 +1108,10 @@ hipError_t segment_states(LaChain c, const Plan& p, LaJob* const* jobs, int n, f
         const hipError_t e = launch_states(c);
         if (e != hipSuccess) return e;
     }
+    if (copy) {
+        m.copy[0] = copy;
+        jobs[0]->h_in = copy;
+    }
     hipLaunchKernelGGL(compose_kernel, dim3((unsigned)cdiv(m.BH * m.state, 256), n), dim3(256), 0,
                        c.stream, m);
     return hipGetLastError();
@@ -1124,8 +1132,9 @@ int64_t la_fwd_workgroups(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t D
 
 size_t la_fwd_workspace_bytes(int64_t B, int64_t T, int64_t H, int64_t Dk, int64_t Dv, bool bf16) {
     const Plan p = fwd_plan(B, T, H, Dv, bf16);
-    const size_t n = 4 * (size_t)(p.marks * B * H);
-    return up16(n * (size_t)(Dk * Dv)) + up16(n);
+    if (p.nseg == 1) return 0;
+    const size_t n = 4 * (size_t)(B * H), marks = (size_t)p.marks;
+    return up16((marks + 1) * n * (size_t)(Dk * Dv)) + up16(marks * n);
 }
 
 hipError_t launch_la_fwd(const LaArgs& a) {
@@ -1142,10 +1151,14 @@ hipError_t launch_la_fwd(const LaArgs& a) {
     j.hz = a.Dk;
     j.hk = 1;
     if (p.nseg > 1) {
+        // in place, the last segment writes s0's memory while the first one may still have
+        // to read it (nothing orders them in a launch): that starts from a copy
         float* buf = static_cast<float*>(a.workspace);
-        float* decay = buf + up16(4 * (size_t)(p.marks * a.B * a.H) * (size_t)c.state) / 4;
+        float* const copy = buf + (size_t)(p.marks * a.B * a.H) * (size_t)c.state;
+        float* decay = buf + up16(4 * (size_t)((p.marks + 1) * a.B * a.H) * (size_t)c.state) / 4;
         LaJob* const jobs[1] = {&j};
-        const hipError_t e = segment_states(c, p, jobs, 1, &buf, &decay);
+        const hipError_t e = segment_states(c, p, jobs, 1, &buf, &decay,
+                                            a.s0 && a.s_final == a.s0 ? copy : nullptr);
         if (e != hipSuccess) return e;
     }
     j.h_out = a.s_final;
@@ -1238,7 +1251,7 @@ hipError_t launch_la_bwd(const LaArgs& a) {
         LaJob* const jobs[2] = {&jq, &jv};
         float* const buf[2] = {f32(w.s), f32(w.g)};
         float* const decay[2] = {f32(w.sdec), f32(w.gdec)};
-        if ((e = segment_states(c, p.p, jobs, 2, buf, decay)) != hipSuccess) return e;
+        if ((e = segment_states(c, p.p, jobs, 2, buf, decay, nullptr)) != hipSuccess) return e;
         jk.h_seg = jv.h_seg;
         jk.h_step = jv.h_step;
     }

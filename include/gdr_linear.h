@@ -51,7 +51,8 @@ extern "C" {
  *   o         [B, T, H, Dv] out_dt
  *   s_final   [B, H, Dv, Dk] fp32 or NULL; may be s0 itself
  *   workspace states of a sequence's segments, where few long sequences run as
- *             segments side by side; may be NULL when its size is 0
+ *             segments side by side, and room for a copy of s0 (which s_final's store
+ *             would meet there); may be NULL when its size is 0
  *
  * fp32 inputs are computed in fp32.  bf16 inputs run on the bf16 matrix cores with
  * fp32 accumulation; every computed operand enters as three bf16 terms, so products

@@ -1,0 +1,75 @@
+"""Calls of linear attention, rotary positions and RMS norm at the edges of what they
+allow: in place across segments."""
+import pytest
+import torch
+
+import linear_reference as R
+from test_linear_attn import DT, F32, close, make, n64
+
+
+@pytest.fixture(scope="module")
+def gdr():
+    import gated_delta_rule_16_amd as g
+    return g
+
+
+# ---- the state in place where a sequence runs as segments ----------------------------
+
+# sequences of two segments and more: segments are at least two chunks (of 64 tokens, in
+# fp32 32), their states are kept at every chunk or every second one
+SEGMENTED = [(1, 256, 1, 64, 64, "bf16"), (3, 700, 1, 40, 128, "bf16"), (1, 2000, 3, 128, 128, "bf16"),
+             (1, 128, 1, 64, 64, "f32"), (5, 1030, 1, 72, 40, "f32")]
+
+
+@pytest.mark.parametrize("T,dt,marks", [(256, "bf16", 3), (128, "f32", 3), (128, "bf16", 0)])
+def test_workspace_has_room_for_the_start(gdr, T, dt, marks):
+    """Beside the states at every chunk but the last there is s0's own copy: the last
+    segment may store s_final over s0 while the first one has yet to read it."""
+    need = gdr.gdr_linear_attn_fwd_workspace_size(1, T, 3, 64, 32, DT[dt])
+    assert need >= (marks + 1) * 4 * 3 * 64 * 32 if marks else need == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,T,H,Dk,Dv,dt", SEGMENTED)
+def test_state_in_place_starts_from_a_copy(gdr_lib, B, T, H, Dk, Dv, dt):
+    """In place the first segment reads no memory that the launch writes: the state
+    that it starts from lies in the workspace, and the results are those of a call with
+    a buffer of its own, also beside work that keeps parts of the chip busy."""
+    a, _, _ = make(51, B, T, H, H, Dk, Dv, dt)
+    n = gdr_lib.gdr_linear_attn_fwd_workspace_size(B, T, H, Dk, Dv, DT[dt])
+    o, s = gdr_lib.gdr_linear_attn_fwd(*a)
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    busy, x = torch.cuda.Stream(), torch.randn(2048, 2048, device="cuda")
+    torch.cuda.synchronize()
+    for i in range(4):
+        st = a[4].clone()
+        if i:
+            busy.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(busy):
+                for _ in range(i):
+                    x @ x
+        o2, _ = gdr_lib.gdr_linear_attn_fwd(*a[:4], st, s_final=st, workspace=ws)
+        torch.cuda.synchronize()
+        assert torch.equal(o, o2) and torch.equal(s, st)
+        slots = ws.view(F32)[:n // 4 // a[4].numel() * a[4].numel()].view(-1, a[4].numel())
+        assert (slots == a[4].view(1, -1)).all(1).any()
+    (ow, sw), (mo, ms), (dm, ds) = R.la_fwd(*[n64(t) for t in a], 1.0)
+    close("s", st, sw, R.la_bound(sw, ms, ds, T, Dk, Dv))
+
+
+@pytest.mark.gpu
+def test_state_in_place_captured(gdr_lib):
+    """A prompt continued in place by a graph: every replay goes on from the state that
+    the one before left."""
+    a, _, _ = make(52, 1, 600, 3, 3, 64, 64, "bf16")
+    st = a[4].clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o, _ = gdr_lib.gdr_linear_attn_fwd(*a[:4], st, s_final=st)
+    st.copy_(a[4])
+    want = a[4].clone()
+    for _ in range(4):
+        ow, want = gdr_lib.gdr_linear_attn_fwd(*a[:4], want)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, ow) and torch.equal(st, want)
