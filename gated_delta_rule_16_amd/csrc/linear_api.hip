@@ -79,6 +79,19 @@ gdr_status_t copy_or_zero(const float* s, float* d, int64_t n, hipStream_t st) {
     return from_hip(hipGetLastError());
 }
 
+__global__ __launch_bounds__(256) void zero_kernel(uint16_t* __restrict__ d, int64_t n) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256)
+        d[i] = 0;
+}
+
+// n elements at any element's alignment.
+gdr_status_t zero_elements(void* d, gdr_dtype_t dt, int64_t n, hipStream_t st) {
+    const int64_t words = n * (int64_t)(elem(dt) / 2);
+    hipLaunchKernelGGL(zero_kernel, dim3(stride_blocks(words)), dim3(256), 0, st,
+                       static_cast<uint16_t*>(d), words);
+    return from_hip(hipGetLastError());
+}
+
 // Tensor i of [B, T, heads, d] with the caller's strides or contiguous.
 LaTensor tensor(const void* p, const int64_t* s, int i, int64_t T, int64_t heads, int64_t d,
                 int64_t share) {
@@ -235,7 +248,15 @@ extern "C" gdr_status_t gdr_linear_attn_bwd(int64_t B, int64_t T, int64_t H, int
     const gdr_status_t st = la_check(B, T, H, Hk, Dk, Dv, in_dt, grad_dt, flags);
     if (st != GDR_OK) return st;
     if (!strides_ok(strides, 12) || !token_strides_ok(strides, 4)) return GDR_ERR_INVALID;
-    if (H == 0) return GDR_OK;
+    if (H == 0) {
+        // heads of q and k that no head of v reads: the sums over none
+        if (B == 0 || T == 0 || Hk == 0) return GDR_OK;
+        if (!product_ok({B, T, Hk, Dk}) || !elem_ok(dq, elem(grad_dt)) ||
+            !elem_ok(dk, elem(grad_dt)) || !apart({dq, dk}, {q, k}))
+            return GDR_ERR_INVALID;
+        const gdr_status_t e = zero_elements(dq, grad_dt, B * T * Hk * Dk, stream);
+        return e == GDR_OK ? zero_elements(dk, grad_dt, B * T * Hk * Dk, stream) : e;
+    }
     if (!opt_elem(s0, 4) || !opt_elem(ds_final, 4) || !opt_elem(ds0, 4) ||
         !opt_elem(dlog_decay, 4) || !opt_elem(log_decay, 4) || (dlog_decay && T && B && !log_decay))
         return GDR_ERR_INVALID;

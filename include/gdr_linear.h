@@ -86,8 +86,8 @@ gdr_status_t gdr_linear_attn_step(int64_t N, int64_t H, int64_t Hk, int64_t Dk, 
 /*
  * Reverse mode of gdr_linear_attn_fwd: dout [B, T, H, Dv] in_dt is the gradient of
  * o, ds_final [B, H, Dv, Dk] fp32 or NULL that of s_final; strides {q, k, v, dout}.
- * Writes dq, dk [B, T, Hk, Dk] (sums over the heads that share one) and
- * dv [B, T, H, Dv] in grad_dt, and in fp32 dlog_decay (shaped as log_decay; NULL:
+ * Writes dq, dk [B, T, Hk, Dk] (sums over the heads that share one: zeros where H is
+ * 0) and dv [B, T, H, Dv] in grad_dt, and in fp32 dlog_decay (shaped as log_decay; NULL:
  * not wanted, as without log_decay; 0 where the decay itself is 0) and
  * ds0 [B, H, Dv, Dk] (or NULL).  The workspace holds states at every 512 tokens
  * (with GDR_LA_HEAD_DECAY 256) or fewer (at most twice 4 B H Dv Dk bytes each; twice

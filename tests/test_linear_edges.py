@@ -1,9 +1,10 @@
 """Calls of linear attention, rotary positions and RMS norm at the edges of what they
-allow: in place across segments."""
+allow: in place across segments, without heads of v."""
 import pytest
 import torch
 
 import linear_reference as R
+from test_linear_api import A, bwd
 from test_linear_attn import DT, F32, close, make, n64
 
 
@@ -73,3 +74,39 @@ def test_state_in_place_captured(gdr_lib):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(o, ow) and torch.equal(st, want)
+
+
+# ---- no heads of v ---------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dq=None), 1), (dict(dk=None), 1), (dict(dq=A[7] + 1), 1), (dict(dk=A[8] + 2, gdt=0), 1),
+    (dict(dq=A[0]), 1), (dict(dk=A[1]), 1), (dict(dk=A[7]), 1), (dict(Hk=1 << 62), 1),
+    (dict(B=0, dq=None, dk=None), 0), (dict(T=0, dq=None, dk=None), 0),
+    (dict(Hk=0, dq=None, dk=None), 0)])
+def test_no_heads_of_v_refused(gdr, kw, code):
+    assert bwd(gdr, **{**dict(H=0, Hk=2, gdt=1, v=None, do=None, dv=None, ws=None), **kw}) == code
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("grad", ["f32", "bf16"])
+@pytest.mark.parametrize("off", [0, 1])
+def test_no_heads_of_v(gdr_lib, dt, grad, off):
+    """dq and dk are sums over the heads that share q and k: over none of them, zeros."""
+    B, T, Hk, d = 2, 37, 3, 40
+    q, k = (torch.randn(B, T, Hk, d, device="cuda").to(DT[dt]) for _ in range(2))
+    v = torch.empty(B, T, 0, 64, dtype=DT[dt], device="cuda")
+    n = B * T * Hk * d
+    out = [torch.full((n + 10,), 7.0, dtype=DT[grad], device="cuda") for _ in range(2)]
+    st = gdr_lib.lib.gdr_linear_attn_bwd(
+        B, T, 0, Hk, d, 64, gdr_lib._DT[DT[dt]], q.data_ptr(), k.data_ptr(), None, None, None, None,
+        None, None, 1.0, 0, gdr_lib._DT[DT[grad]], *(x[off:].data_ptr() for x in out), None, None,
+        None, None, 0, torch.cuda.current_stream().cuda_stream)
+    got = gdr_lib.gdr_linear_attn_bwd(q, k, v, None, None, v, grad_dtype=DT[grad])
+    torch.cuda.synchronize()
+    assert st == 0
+    for x in out:
+        assert not x[off:off + n].any() and (x[off + n:] == 7).all() and (x[:off] == 7).all()
+    assert not got[0].any() and not got[1].any() and got[0].shape == got[1].shape == q.shape
+    assert got[2].shape == v.shape and got[3] is None and got[4].numel() == 0
