@@ -40,6 +40,8 @@
 //
 // The backward (B4: 343 us) is bound alike: dq and dk in one launch, 228, with three
 // terms everywhere for the decay's gradient, dv in another, 87, the decay 28.
+#include <type_traits>
+
 #include "linear_chain.h"
 
 namespace gdr {
@@ -794,18 +796,50 @@ struct DecayGrad {
     double* part;                   // [B nblk][H]
 };
 
+// wave_scan64 in runs: sums from a lane's run's first lane on (`from`; -1: it began in a
+// wave before).  Steps from before it are left out, whatever they hold.
+template <class V> __device__ __forceinline__ V run_scan(V x, int lane, int from) {
+    auto move = [](V v, auto ctrl, auto rows) -> V {
+        if constexpr (sizeof(V) == 8) return dpp_mov64<ctrl.value, rows.value>(v);
+        else return dpp_mov<ctrl.value, rows.value>(v);
+    };
+    auto step = [&](auto ctrl, auto rows, bool within) {
+        const V y = move(x, ctrl, rows);
+        x += within ? y : V(0);
+    };
+    typedef std::integral_constant<int, 0xF> all;
+    step(std::integral_constant<int, 0x111>(), all(), lane - 1 >= from);
+    step(std::integral_constant<int, 0x112>(), all(), lane - 2 >= from);
+    step(std::integral_constant<int, 0x114>(), all(), lane - 4 >= from);
+    step(std::integral_constant<int, 0x118>(), all(), lane - 8 >= from);
+    step(std::integral_constant<int, 0x142>(), std::integral_constant<int, 0xA>(),
+         from < (lane & 48));
+    step(std::integral_constant<int, 0x143>(), std::integral_constant<int, 0xC>(), from < 32);
+    return x;
+}
+
 // dg of one block of tokens of a (sequence, head): what all pairs across its end say,
-// <G, S> there, and the running sum of q . dq - k . dk from the end, in 64 bits.  Its
-// terms carry the roundings of dq and dk, so its error grows with the distance from the
-// end.  At the block's start the pairs across the end of the block before say the same:
-// the difference is taken out in proportion to the distance.  That and the blocks'
-// length keep dg about as exact as a form in fp32 that goes token by token: bf16 B50
-// T2737 H1 32 x 128 2.0e-6 off at 1024 tokens from the end alone, 1.6e-6 from both ends,
-// 1.0e-6 at 512 (fp32 0.6e-6).  A sum per head, which adds all of them up, has blocks of
-// 256: B2 T4109 H4 64 x 64, six draws, 1.6e-6 at first and 0.5e-6 on average (0.4e-6).
-// At B4 T4096 H16 of 128 (328 us with 1024) 512 cost 14 us, 256 30.
+// <G, S> there, and the running sum of q . dq - k . dk from the end, in 64 bits.  No pair
+// lies across a decay of 0: such tokens cut a block into runs, each with a sum of its own,
+// so that nothing of one packed sequence reaches another.
+//
+// The terms carry the roundings of dq and dk, so the sum's error grows with the distance
+// from the end.  At a run's start the pairs across say what the whole run should sum up
+// to: 0 at such a token, <G, S> at the block's start.  The difference is taken out in
+// proportion to the sum of |q . dq| + |k . dk| from the end on, which is what the
+// roundings in it are in proportion to: a token loses no more than its own terms may be
+// off, however large others of the run are.  (In proportion to the distance, tokens 100
+// times as large as those behind them left these with nothing but error.)
+//
+// That and the blocks' length keep dg about as exact as a form in fp32: bf16 B50 T2737 H1
+// 32 x 128 0.45e-6 off (fp32 0.36e-6), where blocks of 1024 tokens from the end alone were
+// 2.0e-6.  A sum per head, which adds all of them up, has blocks of 256: B2 T4109 H4
+// 64 x 64 0.28e-6 off (0.10e-6; three draws).  At B4 T4096 H16 of 128 (328 us with 1024)
+// 512 cost 14 us, 256 30.
 __device__ __forceinline__ void decay_grad(const DecayGrad& a, int64_t id) {
     __shared__ double red[4], part[kTurns][4];
+    __shared__ float weight[kTurns][4], rate_off[kMostKept];
+    __shared__ uint64_t first[kTurns][4];
     const int64_t h = id % a.H, b = id / a.H % a.B, p = id / a.H / a.B;
     const int64_t bh = b * a.H + h;
     const int tid = threadIdx.x;
@@ -814,9 +848,12 @@ __device__ __forceinline__ void decay_grad(const DecayGrad& a, int64_t id) {
         const float g = a.g_head ? a.g[h] : a.g[(b * a.T + t) * a.H + h];
         return g < kLeast ? kLeast : g;
     };
+    auto cuts = [&](int64_t t) { return rate(t) < -104.f; };        // e^g is 0
     // the pairs across the end of block o
     auto across = [&](int64_t o) {
-        const float* G = o + 1 < a.nblk ? a.gkeep + (o * a.B * a.H + bh) * a.state
+        const bool last = o + 1 == a.nblk;
+        const int64_t t = (o + 1) * a.every;
+        const float* G = !last ? (cuts(t) ? nullptr : a.gkeep + (o * a.B * a.H + bh) * a.state)
                          : a.ds_final ? a.ds_final + bh * a.state : nullptr;
         double sum = 0.0;
         if (G) {
@@ -837,17 +874,22 @@ __device__ __forceinline__ void decay_grad(const DecayGrad& a, int64_t id) {
         __syncthreads();
         sum = (red[0] + red[1]) + (red[2] + red[3]);
         __syncthreads();
-        const int64_t t = (o + 1) * a.every;
-        return o + 1 < a.nblk ? sum * (double)__builtin_amdgcn_exp2f(rate(t) * kLog2e) : sum;
+        return last || !G ? sum : sum * (double)__builtin_amdgcn_exp2f(rate(t) * kLog2e);
     };
     // thread 0: the last token of 256 each
-    const int wv = tid >> 6;
+    const int wv = tid >> 6, lane = tid & 63;
     const int64_t n = a.B * a.H * a.T, row = bh * a.T;
     double e[kTurns];
+    float w[kTurns];
+    bool ends[kTurns];              // the run ends here: the token before has another sum
+    int from[kTurns], run[kTurns];
 #pragma unroll
     for (int k = 0; k < kTurns; ++k) {
         const int64_t t = t1 - 1 - 256 * k - tid;
         e[k] = 0.0;
+        w[k] = 0.f;
+        ends[k] = false;
+        bool begins = false;
         if (t >= t0) {
             // all loads at once, without branches between them
             float x[16];
@@ -857,38 +899,67 @@ __device__ __forceinline__ void decay_grad(const DecayGrad& a, int64_t id) {
                 x[2 * i] = a.q[o];
                 x[2 * i + 1] = a.k[o];
             }
+            ends[k] = cuts(t);
+            begins = t + 1 < t1 && cuts(t + 1);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < 8; ++i) {
                 e[k] += i < a.nq ? (double)x[2 * i] - (double)x[2 * i + 1] : 0.0;
+                w[k] += i < a.nq ? fabsf(x[2 * i]) + fabsf(x[2 * i + 1]) : 0.f;
+            }
         }
-        e[k] = wave_scan64(e[k]);
-        if ((tid & 63) == 63) part[k][wv] = e[k];
+        const uint64_t heads = __ballot(begins), upto = heads & (~0ull >> (63 - lane));
+        from[k] = 63 - __clzll((long long)upto);
+        run[k] = __popcll(upto);
+        e[k] = run_scan(e[k], lane, from[k]);
+        w[k] = run_scan(w[k], lane, from[k]);
+        if (lane == 63) {
+            part[k][wv] = e[k];
+            weight[k][wv] = w[k];
+            first[k][wv] = heads;
+        }
     }
     const double tail = across(p);                      // part is there behind its barriers
     const double head = p > 0 ? across(p - 1) : 0.0;
     double carry = tail, sum = 0.0;
+    float carried = 0.f;
+    int runs = 0;
 #pragma unroll
     for (int k = 0; k < kTurns; ++k) {
-        double before = 0.0, all = 0.0;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            before += w < wv ? part[k][w] : 0.0;
-            all += part[k][w];
+        for (int v = 0; v < 4; ++v) {
+            if (v == wv) {
+                if (from[k] < 0) {
+                    e[k] += carry;
+                    w[k] += carried;
+                }
+                run[k] += runs;
+            }
+            const uint64_t heads = first[k][v];
+            carry = heads ? part[k][v] : carry + part[k][v];
+            carried = heads ? weight[k][v] : carried + weight[k][v];
+            runs += __popcll(heads);
         }
-        e[k] += carry + before;
-        carry += all;
     }
-    // the start state's own gradient is not kept: then the end alone counts, as where
-    // either is no number
-    double off = p > 0 || !a.s0 ? carry - head : 0.0;
-    if (off - off != 0.0) off = 0.0;
+    // what a run's sum is off, for its weight.  The start state's own gradient is not
+    // kept: then the end alone counts, as where something is no number
+#pragma unroll
+    for (int k = 0; k < kTurns; ++k) {
+        const int64_t t = t1 - 1 - 256 * k - tid;
+        if (t < t0 || !(ends[k] || t == t0)) continue;
+        double off = 0.0;
+        if (ends[k]) off = e[k];
+        else if (p > 0 || !a.s0) off = e[k] - head;
+        const float r = (float)(off / (double)w[k]);
+        rate_off[run[k]] = r - r == 0.f ? r : 0.f;
+    }
+    __syncthreads();
 #pragma unroll
     for (int k = 0; k < kTurns; ++k) {
         const int64_t t = t1 - 1 - 256 * k - tid;
         if (t < t0) continue;
         // a decay of 0 has no gradient
-        const double share = (double)(t1 - t) / (double)(t1 - t0);
-        const double d = rate(t) < -104.f ? 0.0 : e[k] - off * share;
+        const float r = rate_off[run[k]];
+        const double d = ends[k] ? 0.0 : r != 0.f ? e[k] - (double)r * (double)w[k] : e[k];
         sum += d;
         if (a.dg) a.dg[(b * a.T + t) * a.H + h] = (float)d;
     }

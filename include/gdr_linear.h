@@ -88,8 +88,8 @@ gdr_status_t gdr_linear_attn_step(int64_t N, int64_t H, int64_t Hk, int64_t Dk, 
  * o, ds_final [B, H, Dv, Dk] fp32 or NULL that of s_final; strides {q, k, v, dout}.
  * Writes dq, dk [B, T, Hk, Dk] (sums over the heads that share one: zeros where H is
  * 0) and dv [B, T, H, Dv] in grad_dt, and in fp32 dlog_decay (shaped as log_decay; NULL:
- * not wanted, as without log_decay; 0 where the decay itself is 0) and
- * ds0 [B, H, Dv, Dk] (or NULL).  The workspace holds states at every 512 tokens
+ * not wanted, as without log_decay; 0 where the decay itself is 0, which also keeps
+ * packed sequences' gradients apart) and ds0 [B, H, Dv, Dk] (or NULL).  The workspace holds states at every 512 tokens
  * (with GDR_LA_HEAD_DECAY 256) or fewer (at most twice 4 B H Dv Dk bytes each; twice
  * that where a sequence runs as segments), 8 B T H ceil(Dk / 16) bytes for the decay's
  * gradient and, where Hk < H, 8 B T H Dk bytes for dq and dk of each head.

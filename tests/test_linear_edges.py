@@ -1,5 +1,6 @@
 """Calls of linear attention, rotary positions and RMS norm at the edges of what they
-allow: in place across segments, without heads of v."""
+allow: in place across segments, without heads of v, sequences of other sizes of values
+packed into one."""
 import pytest
 import torch
 
@@ -110,3 +111,71 @@ def test_no_heads_of_v(gdr_lib, dt, grad, off):
         assert not x[off:off + n].any() and (x[off + n:] == 7).all() and (x[:off] == 7).all()
     assert not got[0].any() and not got[1].any() and got[0].shape == got[1].shape == q.shape
     assert got[2].shape == v.shape and got[3] is None and got[4].numel() == 0
+
+
+# ---- the decay's gradient among tokens of other sizes ------------------------------------
+
+
+def scaled(seed, T, cuts, scales, dt, reset, Dk=64, Dv=64):
+    """Inputs whose tokens are `scales` times as large between the cuts, which are resets
+    or not."""
+    a, do, _ = make(seed, 1, T, 2, 2, Dk, Dv, dt, state=False)
+    x = torch.ones(T, device="cuda")
+    for lo, hi, c in zip(cuts, cuts[1:], scales):
+        x[lo:hi] = c
+    x = x[None, :, None, None]
+    a[:3] = [(t.float() * x).to(DT[dt]) for t in a[:3]]
+    if reset:
+        a[3][:, cuts[1:-1]] = float("-inf")
+    return a, (do.float() * x).to(DT[dt])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,cuts,scales", [
+    (400, [0, 200, 400], [100, 1]), (400, [0, 200, 400], [1, 100]), (400, [0, 200, 400], [30, 1]),
+    (700, [0, 100, 101, 300, 512, 600, 700], [1, 50, 30, 1, 100, 0.1]),
+    (1400, [0, 3, 255, 256, 257, 700, 1100, 1400], [100, 1, 10, 100, 0.1, 100, 1])])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_decay_gradient_of_packed_sequences(gdr_lib, T, cuts, scales, dt):
+    """dlog_decay of each packed sequence within the bound of that sequence alone,
+    however large the values of the others are: no pair lies across a reset."""
+    a, do = scaled(61, T, cuts, scales, dt, True)
+    g = gdr_lib.gdr_linear_attn_bwd(*a, do)[3]
+    torch.cuda.synchronize()
+    for lo, hi in zip(cuts, cuts[1:]):
+        r = R.la_bwd(*[n64(x[:, lo:hi]) for x in a[:4]], None, n64(do[:, lo:hi]), None, 1.0)
+        want = r[0]["dg"]
+        if lo:
+            want[:, 0] = 0
+        close(f"dg {lo}..{hi}", g[:, lo:hi], want, R.la_dg_bound(r, hi - lo, 64, 64))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scales", [[100, 1], [1, 100], [1e4, 1]])
+@pytest.mark.parametrize("T", [400, 512, 1500])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_decay_gradient_behind_large_tokens(gdr_lib, scales, T, dt):
+    """The same without a reset: a token's bound holds the terms from it on, so what is
+    taken out of the sum for large tokens before it must not reach it."""
+    a, do = scaled(62, T, [0, T // 2, T], scales, dt, False)
+    g = gdr_lib.gdr_linear_attn_bwd(*a, do)[3]
+    torch.cuda.synchronize()
+    r = R.la_bwd(*[n64(x) for x in a], n64(do), None, 1.0)
+    close("dg", g, r[0]["dg"], R.la_dg_bound(r, T, 64, 64))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,cut", [(300, 120), (300, 256), (700, 513), (1300, 512)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_decay_gradient_before_a_bad_packed_sequence(gdr_lib, T, cut, bad):
+    """A v that is no number in a later packed sequence is in no gradient of the ones
+    before it: the same bits as without it."""
+    a, do = scaled(63, T, [0, cut, T], [1, 1], "bf16", True)
+    want = gdr_lib.gdr_linear_attn_bwd(*a, do)
+    a[2] = a[2].clone()
+    a[2][0, cut + 7, 0, 3] = bad
+    got = gdr_lib.gdr_linear_attn_bwd(*a, do)
+    torch.cuda.synchronize()
+    for x, y in zip(got[:4], want[:4]):
+        assert torch.equal(x[:, :cut], y[:, :cut]) and torch.equal(x[:, :, 1], y[:, :, 1])
+    assert not torch.isfinite(got[3][0, cut + 8, 0])
