@@ -17,11 +17,19 @@ namespace {
 constexpr int E = 8;
 constexpr int TB = 4;       // tokens with their loads in flight at once
 
-// sin and cos of t quarter turns.  The reduction is in 64 bits; the rest is at most
-// half a quarter turn, where the Taylor series to x^9 and x^10 err by 2e-9.
-__device__ __forceinline__ void sincos_quarters(double t, float& s, float& c) {
+// sin and cos of pos f.  The angle in quarter turns is a sum of two doubles, with what
+// the products pos f and (pos f) (2 / pi) round off and 2 / pi in two terms, so the
+// reduction loses nothing at far positions either (three rounded products would be off
+// by 2^-12 at position 2^40 and rate 1).  The rest is at most about half a quarter turn,
+// where the Taylor series to x^9 and x^10 err by 2e-9.
+__device__ __forceinline__ void sincos_at(double pos, double f, float& s, float& c) {
+#pragma clang fp contract(off)          // t is what fma(angle, kHi, -t) says it is
+    constexpr double kHi = 0x1.45f306dc9c883p-1, kLo = -0x1.6b01ec5417056p-55;     // 2 / pi
+    const double angle = pos * f, t = angle * kHi;
+    const double more = __builtin_fma(angle, kHi, -t) +
+                        __builtin_fma(angle, kLo, __builtin_fma(pos, f, -angle) * kHi);
     const double n = __builtin_rint(t);
-    const float x = (float)((t - n) * 1.5707963267948966);
+    const float x = (float)(((t - n) + more) * 1.5707963267948966);
     const int k = (int)(n - 4.0 * __builtin_rint(n * 0.25)) & 3;
     const float z = x * x;
     float p = 2.7557319224e-6f;
@@ -62,15 +70,13 @@ __global__ __launch_bounds__(256) void rotary_kernel(RotaryArgs a) {
         k.qo = b * a.q.ob + t * a.q.ot;
         k.ki = b * a.k.ib + t * a.k.it;
         k.ko = b * a.k.ob + t * a.k.ot;
-        // in quarter turns per unit of rate
-        k.pos = (double)(a.positions ? a.positions[b * a.pos_stride + t] : a.start + t) *
-                0.6366197723675814;
+        k.pos = (double)(a.positions ? a.positions[b * a.pos_stride + t] : a.start + t);
         tokens[tid] = k;
     }
     __syncthreads();
     for (int i = tid; i < nt * half; i += 256) {
         float s, c;
-        sincos_quarters(tokens[i / half].pos * a.freqs[i % half], s, c);
+        sincos_at(tokens[i / half].pos, a.freqs[i % half], s, c);
         turn[i] = float2{c * a.scale, s * (a.inverse ? -a.scale : a.scale)};
     }
     __syncthreads();

@@ -126,7 +126,9 @@ gdr_status_t gdr_linear_attn_bwd(int64_t B, int64_t T, int64_t H, int64_t Hk, in
  *             passes what the smaller ones span); may be q and k themselves with
  *             equal strides
  *
- * Angles are formed and reduced in 64 bits, sine and cosine are within 2^-22.
+ * Sine and cosine are within 2^-22 at every position (whole numbers up to 2^53, beyond
+ * as the nearest double) while |position freqs[i]| is at most 2^48: the angle is formed
+ * and reduced in two doubles.
  */
 #define GDR_ROTARY_INTERLEAVED 1u
 #define GDR_ROTARY_INVERSE 2u

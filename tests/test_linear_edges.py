@@ -1,6 +1,10 @@
 """Calls of linear attention, rotary positions and RMS norm at the edges of what they
 allow: in place across segments, without heads of v, sequences of other sizes of values
-packed into one."""
+packed into one, positions far away."""
+import math
+from fractions import Fraction
+
+import numpy as np
 import pytest
 import torch
 
@@ -179,3 +183,39 @@ def test_decay_gradient_before_a_bad_packed_sequence(gdr_lib, T, cut, bad):
     for x, y in zip(got[:4], want[:4]):
         assert torch.equal(x[:, :cut], y[:, :cut]) and torch.equal(x[:, :, 1], y[:, :, 1])
     assert not torch.isfinite(got[3][0, cut + 8, 0])
+
+
+# ---- rotary positions far away -------------------------------------------------------------
+
+PI = Fraction(314159265358979323846264338327950288419716939937510582097494459, 10 ** 62)
+
+
+def turned(pos, f):
+    """cos and sin of pos f: the product and its rest modulo 2 pi as fractions, pi to 62
+    digits, then 64 bits."""
+    rest = Fraction(pos) * Fraction(f) % (2 * PI)
+    return math.cos(rest), math.sin(rest)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("start", [0, 12345, (1 << 31) + 7, (1 << 40) + 3, -(1 << 44) + 1, (1 << 48) - 2,
+                                   (1 << 53) - 9])
+@pytest.mark.parametrize("inter", [False, True])
+def test_rotary_at_far_positions(gdr_lib, start, inter):
+    """(1, 0) turned by every angle: cosine and sine within 2^-22 of the exact ones (the
+    rates up to 2^48 / position), and half a step of fp32."""
+    T, n = 9, 32
+    f = gdr_lib.gdr_rotary_frequencies(2 * n, base=5e5)
+    if abs(start) > 1 << 48:
+        f = f / 64
+    x = torch.zeros(1, T, 1, 2 * n, device="cuda")
+    x[..., slice(0, None, 2) if inter else slice(0, n)] = 1
+    y = n64(gdr_lib.gdr_rotary(x, None, start, f, interleaved=inter)[0])[0, :, 0]
+    pos = torch.arange(start, start + T, device="cuda")
+    z = n64(gdr_lib.gdr_rotary(x, None, pos, f, interleaved=inter)[0])[0, :, 0]
+    torch.cuda.synchronize()
+    assert (y == z).all()
+    c, s = (y[:, 0::2], y[:, 1::2]) if inter else (y[:, :n], y[:, n:])
+    want = np.array([[turned(start + t, w) for w in f.tolist()] for t in range(T)])
+    for name, got, ref in (("cos", c, want[..., 0]), ("sin", s, want[..., 1])):
+        assert np.abs(got - ref).max() <= 2.0 ** -22 + 2.0 ** -24, (name, np.abs(got - ref).max())
