@@ -10,7 +10,7 @@
 // Bound by HBM: one pass over each tensor, a row in registers between its
 // reductions: one wave per row up to 2048 channels (1024 backward), four up to 8192,
 // eight up to 16384; longer rows are walked once per reduction (from L2).  32768 x 2048
-// bf16 with a residual: e4m3 in groups of 128 94 us (5.0 TB/s), backward 107 (5.0 TB/s);
+// bf16 with a residual: e4m3 in groups of 128 97 us (4.9 TB/s), backward 107 (5.0 TB/s);
 // forward 8192 x 2048 25 (5.4 TB/s).
 #include "block_launch.h"
 #include "linear_launch.h"
@@ -92,13 +92,18 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t x) {
     return x;
 }
 
-// Scale of a group whose largest magnitude is m, and what its values are
-// multiplied by.
-template <int Q8> __device__ __forceinline__ float scale_of(uint32_t m, float& inv) {
-    float s = __uint_as_float(m) / largest<Q8>();
-    if (s < 1.17549435e-38f) s = 0.f;
-    inv = s == 0.f ? 0.f : 1.f / s;
-    return s;
+// Scale of a group whose largest magnitude is m.
+template <int Q8> __device__ __forceinline__ float scale_of(uint32_t m) {
+    const float s = __uint_as_float(m) / largest<Q8>();
+    return s < 1.17549435e-38f ? 0.f : s;
+}
+
+// Values over their scale: quotients, since products with a rounded reciprocal fall on
+// the other side of a code's border where the quotient lies on it (32768 x 2048: 97 us,
+// 94 with products).
+__device__ __forceinline__ void unscale(float (&f)[E], float s) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) f[e] = s == 0.f ? 0.f : f[e] / s;
 }
 
 // 1 / sqrt(mean square + eps).  An infinite sum of squares gives 0.
@@ -162,7 +167,7 @@ __global__ __launch_bounds__(threads(WR)) void rms_fwd_kernel(RmsArgs a) {
         }
     }
     if constexpr (Q8 != 0) {
-        float scale, inv;
+        float scale;
         const bool whole = a.group == a.C;
         if (whole) {
             most = wave_max(most);
@@ -172,18 +177,17 @@ __global__ __launch_bounds__(threads(WR)) void rms_fwd_kernel(RmsArgs a) {
 #pragma unroll
                 for (int i = 0; i < WR; ++i) most = umax(most, redm[i]);
             }
-            scale = scale_of<Q8>(most, inv);
+            scale = scale_of<Q8>(most);
             if (id == 0) a.scales[row] = scale;
         }
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             if (!whole) {
-                scale = scale_of<Q8>(group_max(gmost[k], a.group), inv);
+                scale = scale_of<Q8>(group_max(gmost[k], a.group));
                 if (v[k] > 0 && at[k] % a.group == 0)
                     a.scales[row * (a.C / a.group) + at[k] / a.group] = scale;
             }
-#pragma unroll
-            for (int e = 0; e < E; ++e) h[k][e] *= inv;
+            unscale(h[k], scale);
             if (v[k] > 0) store8<Q8>(a.y, row * a.C + at[k], h[k], E);
         }
     }
@@ -233,7 +237,7 @@ __global__ __launch_bounds__(256) void rms_fwd_long_kernel(RmsArgs a) {
         }
     } else {
         const bool whole = a.group == a.C;
-        float scale, inv = 0.f;
+        float scale = 0.f;
         if (whole) {
             uint32_t most = 0;
             for (int64_t c = (int64_t)threadIdx.x * E; c < a.C; c += step) {
@@ -247,7 +251,7 @@ __global__ __launch_bounds__(256) void rms_fwd_long_kernel(RmsArgs a) {
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < 4; ++i) most = umax(most, redm[i]);
-            scale = scale_of<Q8>(most, inv);
+            scale = scale_of<Q8>(most);
             if (threadIdx.x == 0) a.scales[row] = scale;
         }
         for (int64_t c = (int64_t)threadIdx.x * E; c < a.C; c += step) {
@@ -257,11 +261,10 @@ __global__ __launch_bounds__(256) void rms_fwd_long_kernel(RmsArgs a) {
                 uint32_t m = 0;
 #pragma unroll
                 for (int e = 0; e < E; ++e) m = umax(m, magnitude(h[e]));
-                scale = scale_of<Q8>(group_max(m, a.group), inv);
+                scale = scale_of<Q8>(group_max(m, a.group));
                 if (c % a.group == 0) a.scales[row * (a.C / a.group) + c / a.group] = scale;
             }
-#pragma unroll
-            for (int e = 0; e < E; ++e) h[e] *= inv;
+            unscale(h, scale);
             store8<Q8>(a.y, row * a.C + c, h, v);
         }
     }

@@ -184,8 +184,8 @@ gdr_status_t gdr_rms_norm_fwd(int64_t R, int64_t C, gdr_dtype_t in_dt, const voi
 /*
  * The same with y in 8 bits: per row (group 0) or group of 32, 64 or 128 channels
  * (which divides C), scale = max |y| / 448 (GDR_Q_E4M3, the finite-only 8-bit float
- * with 3 bits of mantissa) or / 127 (GDR_Q_INT8), q = y / scale rounded to nearest
- * even.  scales [R, C / group] ([R, 1]) fp32; y [R, C] bytes.  A scale below fp32's
+ * with 3 bits of mantissa) or / 127 (GDR_Q_INT8), q = y / scale (both in fp32, and
+ * their quotient) rounded to nearest even.  scales [R, C / group] ([R, 1]) fp32; y [R, C] bytes.  A scale below fp32's
  * normal numbers is written as 0 with zeros.  A row with a value that is no number,
  * or infinite, has scales that are no numbers.
  */

@@ -1,6 +1,6 @@
 """Calls of linear attention, rotary positions and RMS norm at the edges of what they
 allow: in place across segments, without heads of v, sequences of other sizes of values
-packed into one, positions far away."""
+packed into one, positions far away, values on the border of two codes."""
 import math
 from fractions import Fraction
 
@@ -219,3 +219,43 @@ def test_rotary_at_far_positions(gdr_lib, start, inter):
     want = np.array([[turned(start + t, w) for w in f.tolist()] for t in range(T)])
     for name, got, ref in (("cos", c, want[..., 0]), ("sin", s, want[..., 1])):
         assert np.abs(got - ref).max() <= 2.0 ** -22 + 2.0 ** -24, (name, np.abs(got - ref).max())
+
+
+# ---- codes of 8 bits ---------------------------------------------------------------------------
+
+E4M3, I8 = torch.float8_e4m3fn, torch.int8
+
+
+def codes(y, kind):
+    """Quotients in fp32, rounded to nearest even (CPU)."""
+    s = y.abs().amax(-1, keepdim=True) / (448.0 if kind == E4M3 else 127.0)
+    q = y / s
+    return (q if kind == E4M3 else torch.round(q).clamp(-127, 127)).to(kind), s
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("C", [64, 512, 1024, 2048, 4096, 8192, 16384, 32768])
+@pytest.mark.parametrize("group", [None, 32, 128])
+@pytest.mark.parametrize("kind", [E4M3, I8])
+def test_codes_are_quotients(gdr_lib, C, group, kind):
+    """Rows of ones have the weights themselves as their norms, so every code is known:
+    for weights on the border of two codes, and at random over many scales."""
+    if C % (group or 1):
+        return
+    g = torch.Generator().manual_seed(C)
+    x = torch.ones(3, C)
+    x[1] = 1 - 2 * (torch.rand(C, generator=g) < 0.5).float()
+    n = group or C
+    half = torch.arange(n) % 253 - 126.5                     # borders of int8's codes
+    near = torch.arange(-24, 24) * 2.0 + 1                   # of e4m3's between 16 and 32
+    w0 = torch.where(torch.arange(n) % 2 == 0, half, near.repeat(-(-n // 48))[:n])
+    w0[5] = 448.0 if kind == E4M3 else 127.0
+    w0 = w0.clamp(-w0[5], w0[5])
+    for w in [c * w0.repeat(C // n) for c in (1.0, 41.0, 7.0 / 3.0, 2.0 ** -90, 3e30)] + \
+            [torch.randn(C, generator=g) * torch.exp(10 * torch.randn(C, generator=g)),
+             torch.randn(C, generator=g)]:
+        q, s = gdr_lib.gdr_rms_norm_quant(x.cuda(), w.cuda(), 0.0, group=group, out_dtype=kind)
+        torch.cuda.synchronize()
+        want, sw = codes((x * w).view(3, C // n, n), kind)
+        assert torch.equal(s.cpu(), sw.squeeze(-1))
+        assert torch.equal(q.cpu().float(), want.view(3, C).float())
