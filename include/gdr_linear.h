@@ -171,6 +171,12 @@ gdr_status_t gdr_rotary_frequencies(int64_t rot, double base, gdr_rotary_scaling
  *   h = x + res (rounded to res_dt, written out and normalised as written), or x;
  *   y = h / sqrt(mean h^2 + eps) w.
  *
+ * The squares are summed in fp32: a row whose sum is infinite there (with an infinite
+ * value, or values above 2^64 / sqrt(C)) is divided by infinity, to zeros and, for
+ * infinite values, to what is no number.  A row with a value that is no number has no
+ * others in y.
+ *
+ *   R         fewer than 2^24, with C between 8193 and 16384 than 2^23
  *   x, res, h, w, eps, y   as for gdr_layer_norm_fwd (gdr_block.h): y may be x, h
  *                          may be res
  */
@@ -186,8 +192,9 @@ gdr_status_t gdr_rms_norm_fwd(int64_t R, int64_t C, gdr_dtype_t in_dt, const voi
  * (which divides C), scale = max |y| / 448 (GDR_Q_E4M3, the finite-only 8-bit float
  * with 3 bits of mantissa) or / 127 (GDR_Q_INT8), q = y / scale (both in fp32, and
  * their quotient) rounded to nearest even.  scales [R, C / group] ([R, 1]) fp32; y [R, C] bytes.  A scale below fp32's
- * normal numbers is written as 0 with zeros.  A row with a value that is no number,
- * or infinite, has scales that are no numbers.
+ * normal numbers is written as 0 with zeros.  Where y has a value that is no number
+ * (see above), its group's or row's scale is none either; the other groups of a row with
+ * an infinite value have scales of 0 and zeros.
  */
 typedef enum { GDR_Q_E4M3 = 0, GDR_Q_INT8 = 1 } gdr_q8_t;
 

@@ -1,6 +1,7 @@
 """Calls of linear attention, rotary positions and RMS norm at the edges of what they
 allow: in place across segments, without heads of v, sequences of other sizes of values
-packed into one, positions far away, values on the border of two codes."""
+packed into one, positions far away, values on the border of two codes,
+rows with values that are no numbers."""
 import math
 from fractions import Fraction
 
@@ -9,7 +10,7 @@ import pytest
 import torch
 
 import linear_reference as R
-from test_linear_api import A, bwd
+from test_linear_api import A, bwd, norm, norm_bwd, quant
 from test_linear_attn import DT, F32, close, make, n64
 
 
@@ -259,3 +260,34 @@ def test_codes_are_quotients(gdr_lib, C, group, kind):
         want, sw = codes((x * w).view(3, C // n, n), kind)
         assert torch.equal(s.cpu(), sw.squeeze(-1))
         assert torch.equal(q.cpu().float(), want.view(3, C).float())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("C", [64, 2048, 4096, 16384, 20480])
+@pytest.mark.parametrize("kind", [E4M3, I8])
+def test_scales_of_rows_with_bad_values(gdr_lib, C, kind):
+    """A value that is no number makes all of its row's scales none; an infinite one
+    that of its own group, and zeros of the others, as do squares whose sum overflows."""
+    x = torch.randn(5, C, device="cuda")
+    want = [gdr_lib.gdr_rms_norm_quant(x, group=g, out_dtype=kind) for g in (None, 32)]
+    x[1, 7], x[2, 7], x[3] = float("nan"), float("-inf"), 1e20
+    q, s = gdr_lib.gdr_rms_norm_quant(x, group=32, out_dtype=kind)
+    q1, s1 = gdr_lib.gdr_rms_norm_quant(x, out_dtype=kind)
+    y = gdr_lib.gdr_rms_norm_fwd(x)
+    torch.cuda.synchronize()
+    for a, b in ((q, want[1][0]), (s, want[1][1]), (q1, want[0][0]), (s1, want[0][1])):
+        assert torch.equal(a[[0, 4]].float(), b[[0, 4]].float())
+    assert s[1].isnan().all() and s1[1].isnan().all() and y[1].isnan().all()
+    assert s[2, 0].isnan() and s1[2].isnan().all() and y[2, 7].isnan()
+    assert not s[2, 1:].any() and not q[2, 32:].float().any() and not y[2, 8:].any()
+    assert not s[3].any() and not s1[3].any() and not q[3].float().any() and not y[3].any()
+
+
+@pytest.mark.parametrize("C,most", [(64, 24), (2048, 24), (2049, 24), (8192, 24), (8193, 23), (16384, 23),
+                                    (16385, 24)])
+def test_rms_norm_rows_refused(gdr, C, most):
+    for call in (norm, quant, norm_bwd):
+        kw = dict(group=0) if call is quant else {}
+        assert call(gdr, R=1 << most, C=C, xs=C, **kw) == 1
+    size = gdr.lib.gdr_rms_norm_bwd_workspace_size
+    assert size(1 << most, C) == 0 and size((1 << most) - 1, C) > 0
