@@ -57,8 +57,9 @@ extern "C" {
  * fp32 inputs are computed in fp32.  bf16 inputs run on the bf16 matrix cores with
  * fp32 accumulation; every computed operand enters as three bf16 terms, so products
  * carry the 24 bits of fp32 (two terms, 2^-17 of the operand, in products that only a
- * bf16 o, dq, dk or dv takes).  Decays come from sums in 64 bits.  A value of v that
- * is infinite or no number reaches no token before it.
+ * bf16 o, dq, dk or dv takes).  Decays come from sums in 64 bits.  A value that
+ * is infinite or no number reaches no token before it; the state that it enters has no
+ * numbers from then on, behind a decay of 0 too (0 times it).
  */
 #define GDR_LA_HEAD_DECAY 1u
 #define GDR_LA_MAX_D 128
@@ -93,6 +94,9 @@ gdr_status_t gdr_linear_attn_step(int64_t N, int64_t H, int64_t Hk, int64_t Dk, 
  * (with GDR_LA_HEAD_DECAY 256) or fewer (at most twice 4 B H Dv Dk bytes each; twice
  * that where a sequence runs as segments), 8 B T H ceil(Dk / 16) bytes for the decay's
  * gradient and, where Hk < H, 8 B T H Dk bytes for dq and dk of each head.
+ * A value that is infinite or no number is in the gradients that have it in their sums
+ * and in no others, with one exception: one of k or v is also in dlog_decay of the tokens
+ * before it, back to a decay of 0 or at most as far as the kept states are apart.
  * Workspace sizes are 0 for arguments the calls reject.
  */
 size_t gdr_linear_attn_bwd_workspace_size(int64_t B, int64_t T, int64_t H, int64_t Hk, int64_t Dk,

@@ -1,7 +1,7 @@
 """Calls of linear attention, rotary positions and RMS norm at the edges of what they
 allow: in place across segments, without heads of v, sequences of other sizes of values
 packed into one, positions far away, values on the border of two codes,
-rows with values that are no numbers."""
+rows with values that are no numbers, and gradients of them."""
 import math
 from fractions import Fraction
 
@@ -291,3 +291,69 @@ def test_rms_norm_rows_refused(gdr, C, most):
         assert call(gdr, R=1 << most, C=C, xs=C, **kw) == 1
     size = gdr.lib.gdr_rms_norm_bwd_workspace_size
     assert size(1 << most, C) == 0 and size((1 << most) - 1, C) > 0
+
+
+# ---- values that are no numbers in the backward ------------------------------------------------
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("T,at", [(150, 77), (1100, 600), (1100, 511)])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_bad_values_in_the_backward(gdr_lib, bad, T, at, dt):
+    """One value that is no number reaches the gradients that have it in their sums, and
+    none beside: dq of the tokens from it on for k and v, dk and dv of those up to it for
+    q and dout, its own token's dk (for v) or dv (for k) or dq (for dout).  The decay's
+    gradient is none from it on (k, v) or up to it (q, dout), in its block of 512 also
+    before (k, v)."""
+    B, H, d = 2, 2, 64
+    a, do, ds = make(71, B, T, H, H, d, d, dt)
+    ref = R.la_bwd(*[n64(x) for x in a], n64(do), n64(ds), 0.3)
+    bound = {n: R.la_bound(*(r[n] for r in ref), T, d, d) for n in ("dq", "dk", "dv", "ds0")}
+    bound["dg"] = R.la_dg_bound(ref, T, d, d)
+    clean = gdr_lib.gdr_linear_attn_bwd(*a, do, ds, scale=0.3)
+    names = ("dq", "dk", "dv", "dg", "ds0")
+    t = np.arange(T)
+    none, own = np.zeros(T, bool), t == at
+    upto, since = t <= at, t >= at
+    block = (at // 512 * 512, (at // 512 + 1) * 512)
+    hit = dict(q=(none, upto, upto, upto, True), k=(since, none, own, t >= block[0], False),
+               v=(since, own, none, t >= block[0], False), dout=(own, upto, upto, upto, True))
+    for i, name in enumerate(("q", "k", "v", "dout")):
+        b = [*a[:3], do]
+        b[i] = b[i].clone()
+        b[i][1, at, 0, 5] = bad
+        got = gdr_lib.gdr_linear_attn_bwd(*b[:3], *a[3:], b[3], ds, scale=0.3)
+        torch.cuda.synchronize()
+        for n, x, y, rows in zip(names, got, clean, hit[name]):
+            if n == "ds0":
+                assert torch.equal(x[0], y[0]) and torch.equal(x[1, 1], y[1, 1]), (name, n)
+                assert rows != bool(torch.isfinite(x[1, 0]).all()), (name, n)
+                continue
+            assert torch.equal(x[0], y[0]) and torch.equal(x[1, :, 1], y[1, :, 1]), (name, n)
+            g, w, e = n64(x)[1, ~rows, 0], ref[0][n][1, ~rows, 0], bound[n][1, ~rows, 0]
+            close(f"{n} of a bad {name}", torch.from_numpy(g), w, e)
+            if rows.any() and n != "dg":
+                assert not np.isfinite(n64(x)[1, at, 0]).all(), (name, n)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("i", range(3))
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_bad_values_in_segments(gdr_lib, i, dt):
+    """The forward in segments: the tokens before a value that is no number, the other
+    heads and the other sequences are what they were; its own state is none."""
+    B, T, H, d, at = 2, 1100, 2, 64, 600
+    a, _, _ = make(72, B, T, H, H, d, d, dt)
+    assert gdr_lib.gdr_linear_attn_fwd_workspace_size(B, T, H, d, d, DT[dt]) > 0
+    want, sw = gdr_lib.gdr_linear_attn_fwd(*a, out_dtype=F32)
+    (ow, _), (mo, _), (dm, _) = R.la_fwd(*[n64(x) for x in a], 1.0)
+    lim = R.la_bound(ow, mo, dm, T, d, d)
+    a[i] = a[i].clone()
+    a[i][1, at, 0, 5] = float("nan")
+    o, s = gdr_lib.gdr_linear_attn_fwd(*a, out_dtype=F32)
+    torch.cuda.synchronize()
+    assert torch.equal(o[0], want[0]) and torch.equal(o[1, :, 1], want[1, :, 1])
+    assert torch.equal(s[0], sw[0]) and torch.equal(s[1, 1], sw[1, 1])
+    close("o", o[1, :at, 0], ow[1, :at, 0], lim[1, :at, 0])
+    assert torch.isnan(o[1, at, 0]).any() and torch.isnan(s[1, 0]).any() == (i > 0)
