@@ -1408,6 +1408,9 @@ def gdr_rotary(q, k, positions, freqs, *, interleaved=False, scale=1.0, inverse=
                 raise ValueError("positions must have contiguous tokens")
     else:
         start = int(positions)
+        # ctypes would cut it to 64 bits
+        if start != positions or not -1 << 63 <= start < 1 << 63:
+            raise ValueError(f"positions must be a 64-bit int, got {positions!r}")
     flags = (GDR_ROTARY_INTERLEAVED if interleaved else 0) | (GDR_ROTARY_INVERSE if inverse else 0)
     _run("gdr_rotary", lib.gdr_rotary(
         B, T, Hq, Hk, D, 2 * freqs.shape[0], _DT[q.dtype], q.data_ptr(), _p(k),

@@ -323,6 +323,8 @@ extern "C" gdr_status_t gdr_rotary(int64_t B, int64_t T, int64_t Hq, int64_t Hk,
         !strides_ok(&pos_stride, 1) || !product_ok({B, T, Hq + Hk, D}))
         return GDR_ERR_INVALID;
     if (B == 0 || T == 0 || Hq + Hk == 0) return GDR_OK;
+    // the last position is a 64-bit number too
+    if (!positions && start > INT64_MAX - (T - 1)) return GDR_ERR_INVALID;
     const size_t e = elem(dt);
     if ((Hq && (!elem_ok(q, e) || !elem_ok(q_out, e))) ||
         (Hk && (!elem_ok(k, e) || !elem_ok(k_out, e))) || !opt_elem(positions, 8) ||

@@ -10,7 +10,7 @@ import pytest
 import torch
 
 import linear_reference as R
-from test_linear_api import A, bwd, norm, norm_bwd, quant
+from test_linear_api import A, bwd, norm, norm_bwd, quant, rot
 from test_linear_attn import DT, F32, close, make, n64
 
 
@@ -220,6 +220,25 @@ def test_rotary_at_far_positions(gdr_lib, start, inter):
     want = np.array([[turned(start + t, w) for w in f.tolist()] for t in range(T)])
     for name, got, ref in (("cos", c, want[..., 0]), ("sin", s, want[..., 1])):
         assert np.abs(got - ref).max() <= 2.0 ** -22 + 2.0 ** -24, (name, np.abs(got - ref).max())
+
+
+@pytest.mark.parametrize("start,T", [((1 << 63) - 8, 9), ((1 << 63) - 1, 2), ((1 << 63) - 1, 1 << 20)])
+def test_rotary_start_refused(gdr, start, T):
+    """Positions from start on that do not all fit 64 bits."""
+    assert rot(gdr, T=T, pos=None, start=start) == 1
+
+
+@pytest.mark.gpu
+def test_rotary_start_through_the_binding(gdr_lib):
+    q, f = torch.randn(1, 4, 2, 8, device="cuda"), gdr_lib.gdr_rotary_frequencies(8)
+    for start in (1 << 63, (1 << 64) + 5, -(1 << 63) - 1, 5.5, float(1 << 63)):
+        with pytest.raises(ValueError):
+            gdr_lib.gdr_rotary(q, None, start, f)
+    want = gdr_lib.gdr_rotary(q, None, 5, f)[0]
+    for start in (5.0, np.int64(5), np.int32(5)):
+        assert torch.equal(gdr_lib.gdr_rotary(q, None, start, f)[0], want)
+    gdr_lib.gdr_rotary(q, None, -(1 << 63), f)
+    torch.cuda.synchronize()
 
 
 # ---- codes of 8 bits ---------------------------------------------------------------------------
