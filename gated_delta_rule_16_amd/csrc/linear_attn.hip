@@ -30,16 +30,18 @@
 // Wave w of U keeps channels 16 w .. 16 w + 15 of the state in registers, transposed, in
 // the layout of a product's result, which is also that of the next product's operand.
 //
-// Bound by what a SIMD can issue at the clock that the power leaves it.  bf16 B8 T4096,
-// 16 heads of 128, bf16 out: 256 workgroups, 174 us (3.1 TB/s), 4600 cycles a chunk at
-// the 1.76 GHz (of 2.4) that the chip holds under it.  A chunk has 408 products of 16
-// cycles to a compute unit (40 P, 48 and 128 out, 192 the state in three terms): 1632
-// cycles on each SIMD; its vector instructions take 2200 more, which share the SIMD's
-// issue with them.  Without loads and stores it would be 160 us.  Four waves, each with
-// all the parts, took 454.
+// Bound by the two stages' chains of dependent steps between the barriers; no unit is
+// full.  bf16 B8 T4096, 16 heads of 128, bf16 out: 256 workgroups, 175 us (3.1 TB/s), 5300
+// cycles a chunk at the 1.95 GHz (of 2.4) that the chip holds under many such calls (155
+// us at 2.4, calls apart).  A chunk has 408 products of 16 cycles to a compute unit (40 P,
+// 48 and 128 out, 192 the state in three terms): 1632 cycles on each SIMD, 31 %; its
+// vector instructions take 2250 (42 %), LDS 2950 (56 %, 500 of them bank conflicts).
+// Without loads and stores it would be 160 us.  Four waves, each with all the parts, took
+// 454.
 //
-// The backward (B4: 343 us) is bound alike: dq and dk in one launch, 228, with three
-// terms everywhere for the decay's gradient, dv in another, 87, the decay 28.
+// The backward (B4: 341 us) alike: dq and dk in one launch, 224, with three terms
+// everywhere for the decay's gradient (7300 cycles a chunk, matrix 27 %, vector 42 %, LDS
+// 51 %), dv in another, 86 (5500 cycles, matrix 30 %), the decay 28.
 #include <type_traits>
 
 #include "linear_chain.h"

@@ -10,7 +10,7 @@
 // Bound by HBM: one pass over each tensor, a row in registers between its
 // reductions: one wave per row up to 2048 channels (1024 backward), four up to 8192,
 // eight up to 16384; longer rows are walked once per reduction (from L2).  32768 x 2048
-// bf16 with a residual: e4m3 in groups of 128 97 us (4.9 TB/s), backward 107 (5.0 TB/s);
+// bf16 with a residual: e4m3 in groups of 128 97 us (4.8 TB/s; int8 101), backward 107 (5.0 TB/s);
 // forward 8192 x 2048 25 (5.4 TB/s).
 #include "block_launch.h"
 #include "linear_launch.h"

@@ -88,12 +88,13 @@ gdr_status_t gdr_linear_attn_step(int64_t N, int64_t H, int64_t Hk, int64_t Dk, 
  * Reverse mode of gdr_linear_attn_fwd: dout [B, T, H, Dv] in_dt is the gradient of
  * o, ds_final [B, H, Dv, Dk] fp32 or NULL that of s_final; strides {q, k, v, dout}.
  * Writes dq, dk [B, T, Hk, Dk] (sums over the heads that share one: zeros where H is
- * 0) and dv [B, T, H, Dv] in grad_dt, and in fp32 dlog_decay (shaped as log_decay; NULL:
- * not wanted, as without log_decay; 0 where the decay itself is 0, which also keeps
- * packed sequences' gradients apart) and ds0 [B, H, Dv, Dk] (or NULL).  The workspace holds states at every 512 tokens
- * (with GDR_LA_HEAD_DECAY 256) or fewer (at most twice 4 B H Dv Dk bytes each; twice
- * that where a sequence runs as segments), 8 B T H ceil(Dk / 16) bytes for the decay's
- * gradient and, where Hk < H, 8 B T H Dk bytes for dq and dk of each head.
+ * 0) and dv [B, T, H, Dv] in grad_dt, and in fp32 dlog_decay (shaped as log_decay;
+ * NULL: not wanted, as without log_decay; 0 where the decay itself is 0, which also
+ * keeps packed sequences' gradients apart) and ds0 [B, H, Dv, Dk] (or NULL).  The
+ * workspace holds states at every 512 tokens (with GDR_LA_HEAD_DECAY 256) or fewer (at
+ * most twice 4 B H Dv Dk bytes each; twice that where a sequence runs as segments),
+ * 8 B T H ceil(Dk / 16) bytes for the decay's gradient and, where Hk < H, 8 B T H Dk
+ * bytes for dq and dk of each head.
  * A value that is infinite or no number is in the gradients that have it in their sums
  * and in no others, with one exception: one of k or v is also in dlog_decay of the tokens
  * before it, back to a decay of 0 or at most as far as the kept states are apart.
@@ -195,10 +196,10 @@ gdr_status_t gdr_rms_norm_fwd(int64_t R, int64_t C, gdr_dtype_t in_dt, const voi
  * The same with y in 8 bits: per row (group 0) or group of 32, 64 or 128 channels
  * (which divides C), scale = max |y| / 448 (GDR_Q_E4M3, the finite-only 8-bit float
  * with 3 bits of mantissa) or / 127 (GDR_Q_INT8), q = y / scale (both in fp32, and
- * their quotient) rounded to nearest even.  scales [R, C / group] ([R, 1]) fp32; y [R, C] bytes.  A scale below fp32's
- * normal numbers is written as 0 with zeros.  Where y has a value that is no number
- * (see above), its group's or row's scale is none either; the other groups of a row with
- * an infinite value have scales of 0 and zeros.
+ * their quotient) rounded to nearest even.  scales [R, C / group] ([R, 1]) fp32; y [R, C]
+ * bytes.  A scale below fp32's normal numbers is written as 0 with zeros.  Where y has a
+ * value that is no number (see above), its group's or row's scale is none either; the
+ * other groups of a row with an infinite value have scales of 0 and zeros.
  */
 typedef enum { GDR_Q_E4M3 = 0, GDR_Q_INT8 = 1 } gdr_q8_t;
 
