@@ -39,7 +39,7 @@
 // Without loads and stores it would be 160 us.  Four waves, each with all the parts, took
 // 454.
 //
-// The backward (B4: 341 us) alike: dq and dk in one launch, 224, with three terms
+// The backward (B4: 344 us) alike: dq and dk in one launch, 224, with three terms
 // everywhere for the decay's gradient (7300 cycles a chunk, matrix 27 %, vector 42 %, LDS
 // 51 %), dv in another, 86 (5500 cycles, matrix 30 %), the decay 28.
 #include <type_traits>
@@ -614,14 +614,18 @@ __global__ __launch_bounds__(1024) void chain_kernel(LaChain a) {
 #pragma unroll
                     for (int t = 0; t < NT; ++t) {
                         const int row = 16 * tile(t) + m;
-                        float rv[4], d = 0.f;
+                        // in 64 bits, rounded once: what cancels between channels, and
+                        // then between q . dq and k . dk, is not lost (3 us of 344)
+                        float rv[4];
+                        double d = 0.0;
                         rr[t].unpack(rv);
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) d = __builtin_fmaf(rv[r], O[t][r], d);
+                        for (int r = 0; r < 4; ++r)
+                            d = __builtin_fma((double)rv[r], (double)O[t][r], d);
                         d += __shfl_xor(d, 16, 64);
                         d += __shfl_xor(d, 32, 64);
                         if (g == 0 && row < len && zc < zd)
-                            db[t0 + (back ? len - 1 - row : row)] = d;
+                            db[t0 + (back ? len - 1 - row : row)] = (float)d;
                     }
                 }
             }
@@ -833,11 +837,13 @@ template <class V> __device__ __forceinline__ V run_scan(V x, int lane, int from
 // off, however large others of the run are.  (In proportion to the distance, tokens 100
 // times as large as those behind them left these with nothing but error.)
 //
-// That and the blocks' length keep dg about as exact as a form in fp32: bf16 B50 T2737 H1
-// 32 x 128 0.45e-6 off (fp32 0.36e-6), where blocks of 1024 tokens from the end alone were
-// 2.0e-6.  A sum per head, which adds all of them up, has blocks of 256: B2 T4109 H4
-// 64 x 64 0.28e-6 off (0.10e-6; three draws).  At B4 T4096 H16 of 128 (328 us with 1024)
-// 512 cost 14 us, 256 30.
+// That, the blocks' length and dots in 64 bits (chain_kernel) keep dg as exact as a form in
+// fp32: bf16 B50 T2737 H1 32 x 128, ten draws, 0.38e-6 off on average and 0.9e-6 at most
+// (fp32 0.38e-6 and 0.7e-6; with dots in fp32 0.51e-6 and 1.4e-6; one draw that was 2.0e-6
+// with blocks of 1024 tokens from the end alone was 1.0e-6 from both ends of 512).  A sum
+// per head, which adds all of them up, has blocks of 256: B2 T4109 H4 64 x 64 0.43e-6 and
+// 1.3e-6 (0.28e-6 and 0.6e-6).  At B4 T4096 H16 of 128 (328 us with 1024) 512 cost 14 us,
+// 256 30.
 __device__ __forceinline__ void decay_grad(const DecayGrad& a, int64_t id) {
     __shared__ double red[4], part[kTurns][4];
     __shared__ float weight[kTurns][4], rate_off[kMostKept];

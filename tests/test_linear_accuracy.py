@@ -122,3 +122,32 @@ def test_backward(gdr_lib, T, D, state, dt):
         # a norm, so six times as much) is taken out, and leaves the roundings of the
         # share that is taken
         assert (np.abs(n64(got[3])[:, 0]) <= 4 * U * 6 * one * np.sqrt(var[:, 0])).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [2, 31, 48, 64])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_dots_lose_nothing_to_cancellation(gdr_lib, T, dt):
+    """Whole numbers, no decay: q . dq and k . dk of 16 channels are below 2^24, but sums
+    of products past it that cancel, channel by channel in pairs.  dlog_decay is exact."""
+    g = torch.Generator().manual_seed(T)
+
+    def ints(lo, hi, *shape):
+        return torch.randint(lo, hi + 1, shape, generator=g).double()
+
+    B, H, D, Dv = 2, 2, 32, 16
+    k = ints(-250, 250, B, T, H, D // 2).repeat_interleave(2, -1)
+    q = ints(150, 250, B, T, H, D // 2).repeat_interleave(2, -1)
+    q[..., 1::2] = ints(-1, 1, B, T, H, D // 2) - q[..., 1::2]
+    v, do = ints(-10, 10, B, T, H, Dv), ints(-10, 10, B, T, H, Dv)
+    one = R.la_bwd(*(x.numpy() for x in (q, k, v)), np.zeros((B, T, H)), None, do.numpy(), None, 1.0)[0]
+    for x, dx in ((q, one["dq"]), (k, one["dk"])):
+        p = x.numpy() * dx
+        assert np.abs(p.reshape(B, T, H, 2, 16).sum(-1)).max() < 2 ** 24 and np.abs(dx).max() < 2 ** 24
+        assert T < 31 or np.abs(p).max() > 2 ** 25
+    assert np.abs(one["dg"]).max() < 2 ** 24
+    a = [x.to(DT[dt]).cuda() for x in (q, k, v)]
+    dg = gdr_lib.gdr_linear_attn_bwd(*a, torch.zeros(B, T, H, device="cuda"), None,
+                                     do.to(DT[dt]).cuda())[3]
+    torch.cuda.synchronize()
+    assert (n64(dg) == one["dg"]).all(), np.abs(n64(dg) - one["dg"]).max()
