@@ -39,9 +39,9 @@
 // Without loads and stores it would be 160 us.  Four waves, each with all the parts, took
 // 454.
 //
-// The backward (B4: 344 us) alike: dq and dk in one launch, 224, with three terms
-// everywhere for the decay's gradient (7300 cycles a chunk, matrix 27 %, vector 42 %, LDS
-// 51 %), dv in another, 86 (5500 cycles, matrix 30 %), the decay 28.
+// The backward (B4: 344 us) alike: dq and dk in one launch, 217 to 227, with three terms
+// everywhere for the decay's gradient (7300 cycles a chunk, matrix 27 %, vector 44 %, LDS
+// 53 %), dv in another, 83 to 87 (5500 cycles, matrix 30 %), the decay 28.
 #include <type_traits>
 
 #include "linear_chain.h"
